@@ -106,6 +106,38 @@ class ChainVerifyArgs(ctypes.Structure):
                 ("is_greedy", _p), ("output_tokens", _p), ("num_accepted", _p), ("dev_status", _p),
                 ("step_counter", _p)]
 
+
+MOE_SOFTMAX, MOE_SIGMOID = 0, 1
+
+
+class MoeRouteArgs(ctypes.Structure):
+    _fields_ = [("rows", _i32), ("n_experts", _i32), ("top_k", _i32), ("scoring", _i32), ("renormalize", _i32),
+                ("scale", _f32), ("ld_logits", _i64), ("logits", _p), ("num_rows", _p), ("topk_ids", _p),
+                ("topk_weights", _p), ("expert_offsets", _p), ("sorted_rows", _p), ("slots", _p), ("dev_status", _p)]
+
+
+class GroupedLinearArgs(ctypes.Structure):
+    _fields_ = [("n_groups", _i32), ("m", _i32), ("n", _i32), ("k", _i32), ("n_src", _i32), ("epilogue", _i32),
+                ("ld_x", _i64), ("ld_w", _i64), ("ld_out", _i64), ("x", _p), ("w", _p), ("w2", _p), ("out", _p),
+                ("offsets", _p), ("row_ids", _p), ("dev_status", _p)]
+
+
+class MoeCombineArgs(ctypes.Structure):
+    _fields_ = [("rows", _i32), ("n_slots", _i32), ("top_k", _i32), ("dim", _i32), ("ld_y", _i64), ("ld_res", _i64),
+                ("ld_out", _i64), ("y", _p), ("slots", _p), ("weights", _p), ("residual", _p), ("out", _p),
+                ("dev_status", _p)]
+
+
+class QuantizeFp8Args(ctypes.Structure):
+    _fields_ = [("rows", _i32), ("k", _i32), ("ld_x", _i64), ("ld_q", _i64), ("x", _p), ("q", _p), ("scale", _p)]
+
+
+class LinearFp8Args(ctypes.Structure):
+    _fields_ = [("m", _i32), ("n", _i32), ("k", _i32), ("epilogue", _i32), ("ld_x", _i64), ("ld_w", _i64),
+                ("ld_out", _i64), ("ld_res", _i64), ("x", _p), ("x_scale", _p), ("w", _p), ("w_scale", _p),
+                ("w2", _p), ("w2_scale", _p), ("out", _p), ("residual", _p), ("dev_status", _p)]
+
+
 DRAFT_WEIGHT_NAMES = ("w_fc", "embed", "input_norm", "hidden_norm", "w_qkv", "w_o", "post_norm", "w_gate",
                       "w_up", "w_down", "final_norm", "lm_head")
 
@@ -184,6 +216,18 @@ def _declare(L):
     L.eagle3_draft_tree.argtypes = [P(DraftWeights), P(DraftTreeArgs), _p, ctypes.c_size_t, _p]
     L.eagle3_rmsnorm.restype = ctypes.c_int
     L.eagle3_rmsnorm.argtypes = [P(RmsnormArgs), _p]
+    L.eagle3_moe_route_workspace_size.restype = ctypes.c_size_t
+    L.eagle3_moe_route_workspace_size.argtypes = [P(MoeRouteArgs)]
+    L.eagle3_moe_route.restype = ctypes.c_int
+    L.eagle3_moe_route.argtypes = [P(MoeRouteArgs), _p, ctypes.c_size_t, _p]
+    L.eagle3_grouped_linear.restype = ctypes.c_int
+    L.eagle3_grouped_linear.argtypes = [P(GroupedLinearArgs), _p]
+    L.eagle3_moe_combine.restype = ctypes.c_int
+    L.eagle3_moe_combine.argtypes = [P(MoeCombineArgs), _p]
+    L.eagle3_quantize_fp8.restype = ctypes.c_int
+    L.eagle3_quantize_fp8.argtypes = [P(QuantizeFp8Args), _p]
+    L.eagle3_linear_fp8.restype = ctypes.c_int
+    L.eagle3_linear_fp8.argtypes = [P(LinearFp8Args), _p]
     L.eagle3_f32_linear.restype = ctypes.c_int
     L.eagle3_f32_linear.argtypes = [P(F32LinearArgs), _p]
     L.eagle3_f32_rmsnorm.restype = ctypes.c_int
@@ -621,6 +665,187 @@ def eagle3_verify_attn_noalloc(q, tree_k, tree_v, k_cache, v_cache, parents, pre
                          max_prefix_len=max_prefix_len, lse=lse, rope_theta=rope_theta, sm_scale=sm_scale,
                          num_splits=num_splits, dev_status=dev_status, qk_rotated=qk_rotated)
     _check(lib().eagle3_verify_attn_noalloc(ctypes.byref(a), _stream(stream)), "eagle3_verify_attn_noalloc")
+
+
+# ----------------------------------------------------------------------------- mixture of experts, 8 bits
+def _on(device, stream):
+    """Raw handle of the launch stream: `stream`, or the current stream of the tensors' device, which
+    has to be the current device (the library launches there)."""
+    if device.type != "cuda":
+        raise ValueError("the tensors must be on a CUDA device")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {device}, which is not the current device")
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+
+
+def _arg(t, dtype, shape, device, name):
+    """Data pointer of a dense tensor of this type, shape and device."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows_arg(t, dtype, shape, device, name):
+    """(data pointer, row pitch) of a 2-D view whose rows are contiguous and do not overlap."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    pitch, inner = t.stride()
+    if inner != 1 and shape[1] > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if shape[0] <= 1:
+        return t.data_ptr(), shape[1]   # a single row's pitch means nothing
+    if pitch < shape[1]:
+        raise ValueError(f"{name} has overlapping rows")
+    return t.data_ptr(), pitch
+
+
+def _scratch(need, workspace, device, stream):
+    """(pointer, bytes) of the caller's workspace, or of one allocated here (kept until the launch
+    stream is done with it)."""
+    if workspace is not None:
+        if workspace.device != device or not workspace.is_contiguous():
+            raise ValueError(f"the workspace must be a contiguous tensor on {device}")
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if need == 0:
+        return None, 0
+    own = torch.empty(need, dtype=torch.uint8, device=device)
+    if stream is not None:
+        own.record_stream(stream)
+    return own.data_ptr(), need
+
+
+def _status_arg(t, device):
+    return None if t is None else _arg(t, torch.int32, t.shape, device, "dev_status")
+
+
+def moe_route_args(logits, topk_ids, topk_weights, expert_offsets, sorted_rows, slots, *, scoring=MOE_SOFTMAX,
+                   renormalize=True, scale=1.0, num_rows=None, dev_status=None):
+    T, E = logits.shape
+    k = topk_ids.shape[1]
+    dev, i32 = logits.device, torch.int32
+    lp, ld = _rows_arg(logits, torch.float32, (T, E), dev, "logits")
+    return MoeRouteArgs(T, E, k, int(scoring), 1 if renormalize else 0, float(scale), ld, lp,
+                        None if num_rows is None else _arg(num_rows, i32, (1,), dev, "num_rows"),
+                        _arg(topk_ids, i32, (T, k), dev, "topk_ids"),
+                        _arg(topk_weights, torch.float32, (T, k), dev, "topk_weights"),
+                        _arg(expert_offsets, i32, (E + 1,), dev, "expert_offsets"),
+                        _arg(sorted_rows, i32, (T * k,), dev, "sorted_rows"), _arg(slots, i32, (T, k), dev, "slots"),
+                        _status_arg(dev_status, dev))
+
+
+def eagle3_moe_route(logits, topk_ids, topk_weights, expert_offsets, sorted_rows, slots, *, scoring=MOE_SOFTMAX,
+                     renormalize=True, scale=1.0, num_rows=None, dev_status=None, workspace=None, stream=None):
+    """Top-k experts of every row and the rows in expert order.  logits [T, E] fp32 (rows may be
+    pitched); outputs topk_ids / slots [T, k] int32, topk_weights [T, k] fp32, expert_offsets [E + 1],
+    sorted_rows [T * k] int32.  num_rows: optional [1] int32 device word, rows at or past it take no
+    expert."""
+    a = moe_route_args(logits, topk_ids, topk_weights, expert_offsets, sorted_rows, slots, scoring=scoring,
+                       renormalize=renormalize, scale=scale, num_rows=num_rows, dev_status=dev_status)
+    st = _on(logits.device, stream)
+    L, ref = lib(), ctypes.byref(a)
+    ws, nbytes = _scratch(L.eagle3_moe_route_workspace_size(ref), workspace, logits.device, stream)
+    _check(L.eagle3_moe_route(ref, ws, nbytes, st), "eagle3_moe_route")
+
+
+def grouped_linear_args(x, w, offsets, out, *, epilogue=EPI_BF16, w2=None, row_ids=None, dev_status=None):
+    E, n, k = w.shape
+    m = out.shape[0]
+    dev, bf, i32 = out.device, torch.bfloat16, torch.int32
+    n_src = x.shape[0]
+    xp, ld_x = _rows_arg(x, bf, (n_src if row_ids is not None else m, k), dev, "x")
+    op, ld_out = _rows_arg(out, bf, (m, n), dev, "out")
+    return GroupedLinearArgs(E, m, n, k, n_src, int(epilogue), ld_x, 0, ld_out, xp, _arg(w, bf, (E, n, k), dev, "w"),
+                             None if w2 is None else _arg(w2, bf, (E, n, k), dev, "w2"), op,
+                             _arg(offsets, i32, (E + 1,), dev, "offsets"),
+                             None if row_ids is None else _arg(row_ids, i32, (m,), dev, "row_ids"),
+                             _status_arg(dev_status, dev))
+
+
+def eagle3_grouped_linear(x, w, offsets, out, *, epilogue=EPI_BF16, w2=None, row_ids=None, dev_status=None,
+                          stream=None):
+    """out[s] = epilogue(x[row_ids[s]] W[e]^T) for the slots s in [offsets[e], offsets[e + 1]) of every
+    group e.  w (and w2 for EPI_SWIGLU) [E, n, k] bf16, offsets [E + 1] int32, out [m, n] bf16; x is
+    [m, k] bf16, or with row_ids ([m] int32) any number of rows to gather from.  Rows of x and out may be
+    pitched.  Rows of out at or past offsets[E] are left as they were."""
+    a = grouped_linear_args(x, w, offsets, out, epilogue=epilogue, w2=w2, row_ids=row_ids, dev_status=dev_status)
+    _check(lib().eagle3_grouped_linear(ctypes.byref(a), _on(out.device, stream)), "eagle3_grouped_linear")
+
+
+def moe_combine_args(y, slots, weights, out, *, residual=None, dev_status=None):
+    T, k = slots.shape
+    n_slots, d = y.shape
+    dev, bf = out.device, torch.bfloat16
+    yp, ld_y = _rows_arg(y, bf, (n_slots, d), dev, "y")
+    op, ld_out = _rows_arg(out, bf, (T, d), dev, "out")
+    rp, ld_res = (None, 0) if residual is None else _rows_arg(residual, bf, (T, d), dev, "residual")
+    return MoeCombineArgs(T, n_slots, k, d, ld_y, ld_res, ld_out, yp, _arg(slots, torch.int32, (T, k), dev, "slots"),
+                          _arg(weights, torch.float32, (T, k), dev, "weights"), rp, op, _status_arg(dev_status, dev))
+
+
+def eagle3_moe_combine(y, slots, weights, out, *, residual=None, dev_status=None, stream=None):
+    """out[t] = residual[t] + sum over j of weights[t, j] * y[slots[t, j]] (slots below 0 left out).
+    y [n_slots, d] bf16, slots [T, k] int32, weights [T, k] fp32, out / residual [T, d] bf16; rows of y,
+    out and residual may be pitched, out may be residual itself."""
+    a = moe_combine_args(y, slots, weights, out, residual=residual, dev_status=dev_status)
+    _check(lib().eagle3_moe_combine(ctypes.byref(a), _on(out.device, stream)), "eagle3_moe_combine")
+
+
+def quantize_fp8_args(x, q, scale):
+    m, k = x.shape
+    dev = x.device
+    xp, ld_x = _rows_arg(x, torch.bfloat16, (m, k), dev, "x")
+    qp, ld_q = _rows_arg(q, torch.float8_e4m3fn, (m, k), dev, "q")
+    return QuantizeFp8Args(m, k, ld_x, ld_q, xp, qp, _arg(scale, torch.float32, (-(-k // 128), m), dev, "scale"))
+
+
+def eagle3_quantize_fp8(x, q, scale, *, stream=None):
+    """Rows of bf16 to e4m3 with one scale for each row and 128 columns: x [m, k] bf16, q [m, k]
+    float8_e4m3fn (rows of both may be pitched), scale [ceil(k / 128), m] fp32; k a multiple of 16."""
+    a = quantize_fp8_args(x, q, scale)
+    _check(lib().eagle3_quantize_fp8(ctypes.byref(a), _on(x.device, stream)), "eagle3_quantize_fp8")
+
+
+def linear_fp8_args(x, x_scale, w, w_scale, out, *, epilogue=EPI_BF16, w2=None, w2_scale=None, residual=None,
+                    dev_status=None):
+    m, k = x.shape
+    n = w.shape[0]
+    kb, nb = -(-k // 128), -(-n // 128)
+    dev, f8, f32, bf = x.device, torch.float8_e4m3fn, torch.float32, torch.bfloat16
+    xp, ld_x = _rows_arg(x, f8, (m, k), dev, "x")
+    wp, ld_w = _rows_arg(w, f8, (n, k), dev, "w")
+    op, ld_out = _rows_arg(out, f32 if epilogue == EPI_F32 else bf, (m, n), dev, "out")
+    rp, ld_res = (None, 0) if residual is None else _rows_arg(residual, bf, (m, n), dev, "residual")
+    w2p = None
+    if w2 is not None:
+        w2p, ld_w2 = _rows_arg(w2, f8, (n, k), dev, "w2")
+        if ld_w2 != ld_w:
+            raise ValueError("w and w2 must share a row pitch")
+    return LinearFp8Args(m, n, k, int(epilogue), ld_x, ld_w, ld_out, ld_res, xp,
+                         _arg(x_scale, f32, (kb, m), dev, "x_scale"), wp, _arg(w_scale, f32, (nb, kb), dev, "w_scale"),
+                         w2p, None if w2_scale is None else _arg(w2_scale, f32, (nb, kb), dev, "w2_scale"), op, rp,
+                         _status_arg(dev_status, dev))
+
+
+def eagle3_linear_fp8(x, x_scale, w, w_scale, out, *, epilogue=EPI_BF16, w2=None, w2_scale=None, residual=None,
+                      dev_status=None, stream=None):
+    """out = epilogue(x W^T) with e4m3 values and block scales: x [m, k] float8_e4m3fn with x_scale
+    [ceil(k / 128), m] fp32 (eagle3_quantize_fp8's outputs), w (and w2 for EPI_SWIGLU) [n, k]
+    float8_e4m3fn with w_scale (w2_scale) [ceil(n / 128), ceil(k / 128)] fp32; out [m, n] bf16, fp32 for
+    EPI_F32; residual [m, n] bf16 for EPI_BF16_RESIDUAL.  Rows of x, w, out and residual may be pitched;
+    k a multiple of 16."""
+    a = linear_fp8_args(x, x_scale, w, w_scale, out, epilogue=epilogue, w2=w2, w2_scale=w2_scale, residual=residual,
+                        dev_status=dev_status)
+    _check(lib().eagle3_linear_fp8(ctypes.byref(a), _on(x.device, stream)), "eagle3_linear_fp8")
 
 
 # ----------------------------------------------------------------------------- fp32 small-model blocks

@@ -210,6 +210,9 @@ E3_DEV uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_sha
 E3_DEV void pdl_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 E3_DEV void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 
+// Largest size (rows, columns, lengths) of the calls that round sizes up to whole tiles in 32 bits
+constexpr int MAX_DIM = 0x7fffffff - (1 << 16);
+
 // Host-side value computed once per device (for the device current at the call) and kept:
 // kernel attributes and device attribute queries.  Safe for concurrent callers.
 template <typename T>

@@ -1,0 +1,827 @@
+// eagle3_quantize_fp8 and eagle3_linear_fp8: 8-bit projections, y = x W^T with e4m3 values, a scale
+// for each row and 128 columns of x and one for each 128 x 128 block of W (the projections of
+// "EAGLE-3: Engineering Implementation of LLM Inference Acceleration", section VIII and appendix C,
+// for a target held in 8 bits).
+//
+// The scales change every 128 columns of k, so the tensor cores can only sum over one such block:
+// each k-block's product goes to a TMEM buffer of its own, and the epilogue warps add it, times its
+// two scales, to fp32 accumulators in registers while the next block's MMAs run.  (This also keeps
+// the long sum out of the tensor cores' accumulation.)
+//
+// Two kernels, both warp-specialised: warp 0 loads by TMA into a ring, lane 0 of warp 1 issues
+// tcgen05.mma (kind::f8f6f4, K = 32) and the other warps run the epilogue.
+//   wide     128 rows x 256 weight rows a tile, persistent.  Rows are the M side, so a thread owns one
+//            row and its scale is one number a k-block.
+//   narrow   128 weight rows (M side) x up to 128 rows (N side, any multiple of 16): few rows, bound by
+//            the weights' bytes.  The k-blocks of a tile are cut over a thread-block cluster so that
+//            the weights stream through all SMs; the ranks' sums meet in distributed shared memory and
+//            are added in rank order.
+//
+// Every mbarrier wait is bounded; on a timeout the kernel records EAGLE3_DEV_TIMEOUT, stops issuing
+// work, drains its own TMA loads and frees its TMEM.
+#include <algorithm>
+
+#include <cuda_fp8.h>
+
+#include "../../include/eagle3_fp8.h"
+#include "tc.cuh"
+#include "tmap.cuh"
+
+namespace e3 {
+namespace {
+
+constexpr int BK = 128;                 // k values of a block and of a tile (128 bytes)
+constexpr int BM = 128;
+constexpr float E4M3_MAX = 448.0f;
+
+E3_DEV float silu(float x) { return x / (1.0f + __expf(-x)); }
+
+struct Fp8Params {
+    int m, n, k, epi, kb_total, n_blocks;   // n_blocks: row blocks of w_scale
+    int64_t ld_out, ld_res;
+    const float *x_scale, *w_scale, *w2_scale;
+    const __nv_bfloat16 *residual;
+    void *out;
+    int32_t *dev_status;
+    int tiles_m, tiles_n;   // wide: row tiles, column tiles
+    int tma_out;            // wide: outputs leave through shared memory and TMA stores
+    int n16, stages;        // narrow: rows of a tile (multiple of 16), ring depth
+};
+
+// ---- quantisation -------------------------------------------------------------------------------
+constexpr int QUANT_THREADS = 128;
+
+struct QuantParams {
+    int m, k;
+    int64_t ld_x, ld_q;
+    const __nv_bfloat16 *x;
+    uint8_t *q;
+    float *scale;
+};
+
+// A half warp holds a block of 128 columns of one row, 8 values a lane; a warp takes two neighbouring
+// blocks of R consecutive rows, all loads first, and writes the R scales of a block side by side.
+template <int R>
+__global__ void __launch_bounds__(QUANT_THREADS) quantize_kernel(const QuantParams p) {
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, pairs = (p.k + 2 * BK - 1) / (2 * BK);
+    const long long task = (long long)blockIdx.x * (QUANT_THREADS / 32) + (threadIdx.x >> 5);
+    const int row0 = (int)(task / pairs) * R, col = (int)(task % pairs) * 2 * BK + lane * 8;
+    if (row0 >= p.m) return;
+    const bool in = col < p.k;   // k is a multiple of 16: 8 values are in or out together
+    uint4 raw[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        raw[r] = make_uint4(0u, 0u, 0u, 0u);
+        if (in && row0 + r < p.m) raw[r] = __ldcs(reinterpret_cast<const uint4 *>(p.x + (size_t)(row0 + r) * p.ld_x + col));
+    }
+    float s[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        // |bf16| as integers: the largest of numbers, above them infinity, above that NaN
+        const uint32_t w[4] = {raw[r].x, raw[r].y, raw[r].z, raw[r].w};
+        uint32_t top = 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
+        top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+        for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));   // within 16 lanes
+        s[r] = top >= 0x7f80u ? __int_as_float(0x7fffffff)
+               : top == 0u    ? 1.0f
+                              : __fdiv_rn(__uint_as_float(top << 16), E4M3_MAX);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        if (!in || row0 + r >= p.m) continue;
+        const uint32_t w[4] = {raw[r].x, raw[r].y, raw[r].z, raw[r].w};
+        uint32_t q[2] = {0u, 0u};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 v = make_float2(__fdiv_rn(__uint_as_float(w[i] << 16), s[r]),
+                                         __fdiv_rn(__uint_as_float(w[i] & 0xffff0000u), s[r]));
+            q[i >> 1] |= (uint32_t)__nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3) << (16 * (i & 1));
+        }
+        *reinterpret_cast<uint2 *>(p.q + (size_t)(row0 + r) * p.ld_q + col) = make_uint2(q[0], q[1]);
+    }
+    // lane r of the half warp writes row r's scale
+    const int hl = lane & 15;
+    if ((col & ~(BK - 1)) < p.k && hl < R && row0 + hl < p.m) {
+        float v = s[0];
+#pragma unroll
+        for (int r = 1; r < R; ++r) v = hl == r ? s[r] : v;
+        p.scale[(size_t)(col / BK) * p.m + row0 + hl] = v;
+    }
+}
+
+// ---- output -------------------------------------------------------------------------------------
+// 8 consecutive outputs of a row from column col: residual, rounding, store (columns below n).
+E3_DEV void load_res8(const Fp8Params &p, int row, int col, float *v) {
+    const __nv_bfloat16 *src = p.residual + (size_t)row * p.ld_res + col;
+    if (col + 8 <= p.n && ((uintptr_t)src & 15) == 0) {
+        const uint4 r = __ldcg(reinterpret_cast<const uint4 *>(src));
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] += __uint_as_float(w[i] << 16);
+            v[2 * i + 1] += __uint_as_float(w[i] & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (col + i < p.n) v[i] += __bfloat162float(src[i]);
+    }
+}
+E3_DEV uint4 pack8(const float *v) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+E3_DEV void store8(const Fp8Params &p, int row, int col, const float *v) {
+    if (p.epi == EAGLE3_EPI_F32) {
+        float *o = (float *)p.out + (size_t)row * p.ld_out + col;
+        for (int i = 0; i < 8; ++i)
+            if (col + i < p.n) o[i] = v[i];
+    } else {
+        __nv_bfloat16 *o = (__nv_bfloat16 *)p.out + (size_t)row * p.ld_out + col;
+        for (int i = 0; i < 8; ++i)
+            if (col + i < p.n) o[i] = __float2bfloat16_rn(v[i]);
+    }
+}
+
+// ---- wide ---------------------------------------------------------------------------------------
+constexpr int WIDE_BN = 256, WIDE_STAGES = 4, WIDE_EPI_WARPS = 8, WIDE_THREADS = 64 + 32 * WIDE_EPI_WARPS;
+constexpr int WIDE_A = BM * BK, WIDE_B = WIDE_BN * BK, WIDE_STAGE = WIDE_A + WIDE_B;
+constexpr int WIDE_BOX = 32 * 128;   // output staging: 32 rows x 128 bytes a warp
+struct WideShared {
+    uint64_t full[WIDE_STAGES], empty[WIDE_STAGES], tfull[2], tempty[2], mma_done;
+    uint32_t tmem_base;
+    int abort;
+};
+constexpr int WIDE_SMEM = 1024 + WIDE_STAGES * WIDE_STAGE + WIDE_EPI_WARPS * WIDE_BOX + (int)sizeof(WideShared);
+static_assert(WIDE_SMEM <= 232448, "shared memory budget");
+
+template <bool SWIGLU>
+__global__ void __launch_bounds__(WIDE_THREADS, 1)
+    fp8_wide_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+                    const __grid_constant__ CUtensorMap tm_w2, const __grid_constant__ CUtensorMap tm_out,
+                    const Fp8Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *ring = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t *boxes = ring + WIDE_STAGES * WIDE_STAGE;
+    WideShared &sh = *reinterpret_cast<WideShared *>(boxes + WIDE_EPI_WARPS * WIDE_BOX);
+    volatile int *abort = &sh.abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < WIDE_STAGES; ++s) {
+            tc::mbar_init(&sh.full[s], 1);
+            tc::mbar_init(&sh.empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            tc::mbar_init(&sh.tfull[b], 1);
+            tc::mbar_init(&sh.tempty[b], WIDE_EPI_WARPS);
+        }
+        tc::mbar_init(&sh.mma_done, 1);
+        sh.abort = 0;
+        tc::fence_barrier_init();
+        tc::prefetch_tmap(&tm_x);
+        tc::prefetch_tmap(&tm_w);
+        if (SWIGLU) tc::prefetch_tmap(&tm_w2);
+    }
+    if (warp == 1) tc::tmem_alloc(&sh.tmem_base, 2 * WIDE_BN);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = sh.tmem_base;
+    pdl_wait();
+    pdl_trigger();
+    const int units = p.tiles_m * p.tiles_n;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0, last_parity = 0, issued = 0;
+            bool ok = true;
+            for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+                const int mb = u % p.tiles_m, nb = u / p.tiles_m;
+                for (int kb = 0; kb < p.kb_total; ++kb) {
+                    if (!tc::mbar_wait(&sh.empty[stage], phase ^ 1u, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *sx = ring + stage * WIDE_STAGE, *sw = sx + WIDE_A;
+                    tc::mbar_expect_tx(&sh.full[stage], WIDE_STAGE);
+                    tc::tma_load_2d(sx, &tm_x, kb * BK, mb * BM, &sh.full[stage]);
+                    if (SWIGLU) {
+                        tc::tma_load_2d(sw, &tm_w, kb * BK, nb * (WIDE_BN / 2), &sh.full[stage]);
+                        tc::tma_load_2d(sw + WIDE_B / 2, &tm_w2, kb * BK, nb * (WIDE_BN / 2), &sh.full[stage]);
+                    } else {
+                        tc::tma_load_2d(sw, &tm_w, kb * BK, nb * WIDE_BN, &sh.full[stage]);
+                    }
+                    issued |= 1u << stage;
+                    last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
+                    if (++stage == WIDE_STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (!ok) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
+            // no TMA write may still be in flight when the CTA exits (bounded waits)
+            for (int st = 0; st < WIDE_STAGES; ++st) {
+                if (!((issued >> st) & 1u)) continue;
+                const uint32_t par = (last_parity >> st) & 1u;
+                const long long t0 = clock64();
+                while (!tc::mbar_try(&sh.full[st], par) && clock64() - t0 < WAIT_LIMIT_CYCLES) {
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t IDESC = tc::idesc_e4m3(BM, WIDE_BN);
+            int stage = 0, buf = 0;
+            uint32_t phase = 0, buf_phase = 0;
+            bool ok = true;
+            for (int u = blockIdx.x; ok && u < units; u += gridDim.x)
+                for (int kb = 0; kb < p.kb_total; ++kb) {
+                    if (!tc::mbar_wait(&sh.tempty[buf], buf_phase ^ 1u, abort) ||
+                        !tc::mbar_wait(&sh.full[stage], phase, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after();
+                    const uint32_t a = smem_u32(ring + stage * WIDE_STAGE), b = a + WIDE_A;
+#pragma unroll
+                    for (int k = 0; k < BK / 32; ++k)
+                        tc::mma_e4m3_ss(tmem + buf * WIDE_BN, tc::desc_sw128(a + k * 32), tc::desc_sw128(b + k * 32),
+                                        IDESC, k > 0 ? 1u : 0u);
+                    tc::mma_commit(&sh.empty[stage]);
+                    tc::mma_commit(&sh.tfull[buf]);
+                    if (++stage == WIDE_STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                    buf_phase ^= (uint32_t)buf;
+                    buf ^= 1;
+                }
+            if (!ok) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
+            // every MMA this thread issued must retire before TMEM is freed (bounded wait)
+            tc::mma_commit(&sh.mma_done);
+            const long long t0 = clock64();
+            while (!tc::mbar_try(&sh.mma_done, 0) && clock64() - t0 < WAIT_LIMIT_CYCLES) {
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------------ epilogue (warps 2..9)
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        uint8_t *box = boxes + (warp - 2) * WIDE_BOX;
+        // this thread's two runs of 64 accumulator columns: neighbours, or gate and up of one run
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        const uint32_t run_a = lanes + (SWIGLU ? 64 * half : 128 * half), run_b = run_a + (SWIGLU ? 128 : 64);
+        int buf = 0;
+        uint32_t buf_phase = 0;
+        bool ok = true;
+        for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+            const int mb = u % p.tiles_m, nb = u / p.tiles_m;
+            const int row = mb * BM + quarter * 32 + lane;
+            const float *xs = p.x_scale + (row < p.m ? row : 0);
+            const int block = min(SWIGLU ? nb : 2 * nb + half, p.n_blocks - 1);
+            const float *wa = p.w_scale + (size_t)block * p.kb_total;
+            const float *wb = SWIGLU ? p.w2_scale + (size_t)block * p.kb_total : wa;
+            float acc[128];
+#pragma unroll
+            for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
+            float sx = __ldg(xs), sa = __ldg(wa), sb = SWIGLU ? __ldg(wb) : sa;
+            for (int kb = 0; kb < p.kb_total; ++kb) {
+                const float fa = sx * sa, fb = SWIGLU ? sx * sb : fa;
+                if (kb + 1 < p.kb_total) {   // the next block's scales, while this one's MMAs run
+                    sx = __ldg(xs + (size_t)(kb + 1) * p.m);
+                    sa = __ldg(wa + kb + 1);
+                    if (SWIGLU) sb = __ldg(wb + kb + 1);
+                }
+                int fine = 0;
+                if (lane == 0) fine = tc::mbar_wait(&sh.tfull[buf], buf_phase, abort) ? 1 : 0;
+                fine = __shfl_sync(0xffffffffu, fine, 0);
+                if (!fine) {
+                    if (lane == 0) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
+                    ok = false;
+                    break;
+                }
+                tc::fence_after();
+                const uint32_t t = tmem + (uint32_t)(buf * WIDE_BN);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float v[32];
+                    tc::tmem_ld32(t + (c < 2 ? run_a : run_b) + (c & 1) * 32, v);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) acc[c * 32 + i] = fmaf(v[i], c < 2 ? fa : fb, acc[c * 32 + i]);
+                }
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&sh.tempty[buf]);
+                buf_phase ^= (uint32_t)buf;
+                buf ^= 1;
+            }
+            if (!ok) break;
+            if (SWIGLU) {
+#pragma unroll
+                for (int i = 0; i < 64; ++i) acc[i] = silu(acc[i]) * acc[64 + i];
+            }
+            const int col0 = SWIGLU ? nb * (WIDE_BN / 2) + 64 * half : nb * WIDE_BN + 128 * half;
+            const int cols = SWIGLU ? 64 : 128, y = mb * BM + quarter * 32;
+            const bool f32 = p.epi == EAGLE3_EPI_F32;
+            if (p.epi == EAGLE3_EPI_BF16_RESIDUAL && row < p.m) {
+#pragma unroll
+                for (int i = 0; i < 128; i += 8)
+                    if (col0 + i < p.n) load_res8(p, row, col0 + i, acc + i);
+            }
+            if (p.tma_out) {
+                // pieces of 128 bytes: 64 bf16 or 32 fp32 columns of the warp's 32 rows
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (c * (f32 ? 32 : 64) >= cols) break;
+                    if (lane == 0) tc::bulk_wait_read<0>();   // the box's last store has read it
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        uint4 o;
+                        if (f32) {
+                            const float *v = acc + c * 32 + 4 * j;
+                            o = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                           __float_as_uint(v[3]));
+                        } else {
+                            o = pack8(acc + (c & 1) * 64 + 8 * j);
+                        }
+                        *reinterpret_cast<uint4 *>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) = o;
+                    }
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    const int x = col0 + c * (f32 ? 32 : 64);
+                    if (lane == 0 && x < p.n && y < p.m) {
+                        tc::tma_store_2d(&tm_out, x, y, box);
+                        tc::bulk_commit();
+                    }
+                }
+            } else if (row < p.m) {
+#pragma unroll
+                for (int i = 0; i < 128; i += 8)
+                    if (i < cols && col0 + i < p.n) store8(p, row, col0 + i, acc + i);
+            }
+        }
+        if (lane == 0) tc::bulk_wait<0>();
+        __syncwarp();
+    }
+
+    tc::fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc::fence_after();
+        tc::tmem_dealloc(tmem, 2 * WIDE_BN);
+    }
+}
+
+// ---- narrow -------------------------------------------------------------------------------------
+constexpr int NARROW_THREADS = 192, NARROW_MAX = 128, NARROW_STAGES = 8, NARROW_TMEM = 256, NARROW_CLUSTER = 8;
+constexpr int NARROW_RING = 106 * 1024;   // two CTAs a SM
+constexpr int NARROW_W = BM * BK;
+struct NarrowShared {
+    uint64_t full[NARROW_STAGES], empty[NARROW_STAGES], tfull[8], tempty[8], mma_done;
+    uint32_t tmem_base;
+    int abort;
+    float scales[4][2][NARROW_MAX];   // per epilogue warp: the rows' scales of a k-block, double-buffered
+};
+constexpr int NARROW_SMEM = 1024 + NARROW_RING + (int)sizeof(NarrowShared);
+static_assert(2 * (NARROW_SMEM + 1024) <= 228 * 1024, "two CTAs a SM");
+static_assert(NARROW_RING >= NARROW_MAX * BM * 4, "the ranks' sums fit the ring");
+
+E3_DEV void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;\n" ::: "memory");
+}
+// this CTA's shared-memory address in CTA `rank` of the cluster, and a load from there
+E3_DEV uint32_t cluster_addr(uint32_t addr, int rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+E3_DEV float cluster_ld(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// NT: row capacity of a tile (TMEM buffers of NT columns, NT accumulators a thread).
+// Grid: (cluster ranks = k ranges, weight tiles, row tiles).
+template <int NT, bool SWIGLU>
+__global__ void __launch_bounds__(NARROW_THREADS, NT <= 64 ? 2 : 1)
+    fp8_narrow_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+                      const __grid_constant__ CUtensorMap tm_w2, const Fp8Params p) {
+    constexpr int BUFS = NARROW_TMEM / NT;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *ring = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    NarrowShared &sh = *reinterpret_cast<NarrowShared *>(ring + NARROW_RING);
+    volatile int *abort = &sh.abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int ranks = gridDim.x, rank = blockIdx.x, mt = blockIdx.y, row0 = blockIdx.z * p.n16;
+    const int rows = min(p.n16, p.m - row0);
+    const int kb0 = (int)((long long)p.kb_total * rank / ranks), kb1 = (int)((long long)p.kb_total * (rank + 1) / ranks);
+    const int stage_bytes = NARROW_W + p.n16 * BK, stages = p.stages;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NARROW_STAGES; ++s) {
+            tc::mbar_init(&sh.full[s], 1);
+            tc::mbar_init(&sh.empty[s], 1);
+        }
+        for (int b = 0; b < BUFS; ++b) {
+            tc::mbar_init(&sh.tfull[b], 1);
+            tc::mbar_init(&sh.tempty[b], 4);
+        }
+        tc::mbar_init(&sh.mma_done, 1);
+        sh.abort = 0;
+        tc::fence_barrier_init();
+        tc::prefetch_tmap(&tm_x);
+        tc::prefetch_tmap(&tm_w);
+        if (SWIGLU) tc::prefetch_tmap(&tm_w2);
+    }
+    if (warp == 1) tc::tmem_alloc(&sh.tmem_base, NARROW_TMEM);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = sh.tmem_base;
+    pdl_wait();
+    pdl_trigger();
+
+    if (warp == 0) {
+        // ------------------------------------------------------------------ TMA producer
+        int stage = 0;
+        uint32_t phase = 0, last_parity = 0, issued = 0;   // lane 0
+        bool ok = true;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            int fine = 1;
+            if (lane == 0) {
+                fine = tc::mbar_wait(&sh.empty[stage], phase ^ 1u, abort) ? 1 : 0;
+                if (fine) {
+                    tc::mbar_expect_tx(&sh.full[stage], stage_bytes);
+                    issued |= 1u << stage;
+                    last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
+                }
+            }
+            fine = __shfl_sync(0xffffffffu, fine, 0);
+            if (!fine) {
+                ok = false;
+                break;
+            }
+            uint8_t *sw = ring + stage * stage_bytes, *sx = sw + NARROW_W;
+            if (SWIGLU) {
+                if (lane < 8) {   // 16 gate and 16 up rows for the lanes of each quarter
+                    const int q = lane >> 1, up = lane & 1;
+                    tc::tma_load_2d(sw + lane * 16 * BK, up ? &tm_w2 : &tm_w, kb * BK, mt * 64 + q * 16, &sh.full[stage]);
+                }
+            } else if (lane == 0) {
+                tc::tma_load_2d(sw, &tm_w, kb * BK, mt * BM, &sh.full[stage]);
+            }
+            if (16 * lane < p.n16) tc::tma_load_2d(sx + lane * 16 * BK, &tm_x, kb * BK, row0 + lane * 16, &sh.full[stage]);
+            if (++stage == stages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+        if (lane == 0) {
+            if (!ok) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
+            for (int st = 0; st < stages; ++st) {   // loads in flight (bounded waits)
+                if (!((issued >> st) & 1u)) continue;
+                const uint32_t par = (last_parity >> st) & 1u;
+                const long long t0 = clock64();
+                while (!tc::mbar_try(&sh.full[st], par) && clock64() - t0 < WAIT_LIMIT_CYCLES) {
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            const uint32_t idesc = tc::idesc_e4m3(BM, p.n16);
+            int stage = 0, buf = 0;
+            uint32_t phase = 0, buf_phase = 0;
+            bool ok = true;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!tc::mbar_wait(&sh.tempty[buf], buf_phase ^ 1u, abort) ||
+                    !tc::mbar_wait(&sh.full[stage], phase, abort)) {
+                    ok = false;
+                    break;
+                }
+                tc::fence_after();
+                const uint32_t a = smem_u32(ring + stage * stage_bytes), b = a + NARROW_W;
+#pragma unroll
+                for (int k = 0; k < BK / 32; ++k)
+                    tc::mma_e4m3_ss(tmem + buf * NT, tc::desc_sw128(a + k * 32), tc::desc_sw128(b + k * 32), idesc,
+                                    k > 0 ? 1u : 0u);
+                tc::mma_commit(&sh.empty[stage]);
+                tc::mma_commit(&sh.tfull[buf]);
+                if (++stage == stages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+                if (++buf == BUFS) {
+                    buf = 0;
+                    buf_phase ^= 1u;
+                }
+            }
+            if (!ok) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
+            tc::mma_commit(&sh.mma_done);
+            const long long t0 = clock64();
+            while (!tc::mbar_try(&sh.mma_done, 0) && clock64() - t0 < WAIT_LIMIT_CYCLES) {
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------------ epilogue (warps 2..5)
+        const int quarter = warp & 3;
+        const uint32_t t_col = tmem + ((uint32_t)(quarter * 32) << 16);
+        const int block = SWIGLU ? mt / 2 : mt;
+        const float *ws = (SWIGLU && lane >= 16 ? p.w2_scale : p.w_scale) + (size_t)block * p.kb_total;
+        float acc[NT];
+#pragma unroll
+        for (int i = 0; i < NT; ++i) acc[i] = 0.0f;
+        float sx[NT / 32], sw = 0.0f;
+        auto fetch = [&](int kb) {   // the k-block's scales: this lane's rows, and its weight row's
+#pragma unroll
+            for (int i = 0; i < NT / 32; ++i) {
+                const int r = lane + 32 * i;
+                sx[i] = r < rows ? __ldg(p.x_scale + (size_t)kb * p.m + row0 + r) : 0.0f;
+            }
+            sw = __ldg(ws + kb);
+        };
+        fetch(kb0);
+        int buf = 0;
+        uint32_t buf_phase = 0;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            float *strip = sh.scales[warp - 2][kb & 1];
+#pragma unroll
+            for (int i = 0; i < NT / 32; ++i) strip[lane + 32 * i] = sx[i];
+            const float fw = sw;
+            if (kb + 1 < kb1) fetch(kb + 1);
+            int fine = 0;
+            if (lane == 0) fine = tc::mbar_wait(&sh.tfull[buf], buf_phase, abort) ? 1 : 0;
+            fine = __shfl_sync(0xffffffffu, fine, 0);   // (also orders the strip's writes)
+            __syncwarp();
+            if (!fine) {
+                if (lane == 0) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
+                break;
+            }
+            tc::fence_after();
+#pragma unroll
+            for (int c = 0; c < NT; c += 32) {
+                if (c < p.n16) {
+                    float v[32];
+                    tc::tmem_ld32(t_col + buf * NT + c, v);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(strip + c + i);
+                        acc[c + i] = fmaf(v[i] * f.x, fw, acc[c + i]);
+                        acc[c + i + 1] = fmaf(v[i + 1] * f.y, fw, acc[c + i + 1]);
+                        acc[c + i + 2] = fmaf(v[i + 2] * f.z, fw, acc[c + i + 2]);
+                        acc[c + i + 3] = fmaf(v[i + 3] * f.w, fw, acc[c + i + 3]);
+                    }
+                }
+            }
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sh.tempty[buf]);
+            if (++buf == BUFS) {
+                buf = 0;
+                buf_phase ^= 1u;
+            }
+        }
+        // this rank's sums, [row][weight row], over the ring: its last loads and MMAs have completed
+        // (after a timeout another warp's may not have; the outputs are void then)
+        float *sums = reinterpret_cast<float *>(ring);
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+            if (i < rows) sums[i * BM + quarter * 32 + lane] = acc[i];
+    }
+
+    tc::fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc::fence_after();
+        tc::tmem_dealloc(tmem, NARROW_TMEM);
+    }
+    if (ranks > 1) {
+        __syncwarp();
+        cluster_sync();
+    }
+    // rows rank, rank + ranks, ...: the ranks' sums in rank order, the epilogue, the output
+    const uint32_t base = smem_u32(ring);
+    constexpr int OUT = SWIGLU ? 64 : BM;   // output columns of the tile
+    const int mine = rows > rank ? (rows - rank + ranks - 1) / ranks : 0;
+    for (int i = threadIdx.x; i < mine * OUT; i += NARROW_THREADS) {
+        const int r = rank + (i / OUT) * ranks, j = i % OUT;
+        const int at = SWIGLU ? (j >> 4) * 32 + (j & 15) : j;   // the column's (gate) lane
+        const uint32_t addr = base + (uint32_t)(r * BM + at) * 4u;
+        float y = 0.0f, y2 = 0.0f;
+        for (int s = 0; s < ranks; ++s) {
+            const uint32_t from = ranks > 1 ? cluster_addr(addr, s) : addr;
+            y += cluster_ld(from);
+            if (SWIGLU) y2 += cluster_ld(from + 64u);
+        }
+        const int col = mt * OUT + j;
+        if (col >= p.n) continue;
+        if (SWIGLU) y = silu(y) * y2;
+        const size_t row = row0 + r;
+        if (p.epi == EAGLE3_EPI_F32) {
+            ((float *)p.out)[row * p.ld_out + col] = y;
+        } else {
+            if (p.epi == EAGLE3_EPI_BF16_RESIDUAL) y += __bfloat162float(p.residual[row * p.ld_res + col]);
+            ((__nv_bfloat16 *)p.out)[row * p.ld_out + col] = __float2bfloat16_rn(y);
+        }
+    }
+    if (ranks > 1) {
+        __syncwarp();
+        cluster_sync();   // no rank leaves while another reads its sums
+    }
+}
+
+// ---- host side ----------------------------------------------------------------------------------
+eagle3_status_t validate(const eagle3_quantize_fp8_args_t *a) {
+    if (!a) return EAGLE3_ERR_INVALID_ARGUMENT;
+    if (a->rows < 0 || a->k < 1) return EAGLE3_ERR_INVALID_ARGUMENT;
+    if (a->k % 16 || a->k > MAX_DIM || a->rows > MAX_DIM) return EAGLE3_ERR_UNSUPPORTED;
+    const int64_t ld_x = a->ld_x ? a->ld_x : a->k, ld_q = a->ld_q ? a->ld_q : a->k;
+    if (ld_x < a->k || ld_q < a->k || ld_x % 8 || ld_q % 16) return EAGLE3_ERR_INVALID_ARGUMENT;
+    if (a->rows == 0) return EAGLE3_OK;
+    if (!a->x || !a->q || !a->scale) return EAGLE3_ERR_INVALID_ARGUMENT;
+    if (((uintptr_t)a->x | (uintptr_t)a->q) & 15 || (uintptr_t)a->scale & 3) return EAGLE3_ERR_INVALID_ARGUMENT;
+    return EAGLE3_OK;
+}
+
+eagle3_status_t validate(const eagle3_linear_fp8_args_t *a) {
+    if (!a) return EAGLE3_ERR_INVALID_ARGUMENT;
+    if (a->m < 0 || a->n < 1 || a->k < 1) return EAGLE3_ERR_INVALID_ARGUMENT;
+    if (a->epilogue < EAGLE3_EPI_BF16 || a->epilogue > EAGLE3_EPI_BF16_ROPE) return EAGLE3_ERR_INVALID_ARGUMENT;
+    if (a->epilogue == EAGLE3_EPI_BF16_ROPE || a->k % 16) return EAGLE3_ERR_UNSUPPORTED;
+    if (a->m > MAX_DIM || a->n > MAX_DIM || a->k > MAX_DIM) return EAGLE3_ERR_UNSUPPORTED;
+    const int64_t ld_x = a->ld_x ? a->ld_x : a->k, ld_w = a->ld_w ? a->ld_w : a->k;
+    if (ld_x < a->k || ld_w < a->k || ld_x % 16 || ld_w % 16) return EAGLE3_ERR_INVALID_ARGUMENT;
+    for (const int64_t ld : {a->ld_out, a->ld_res})
+        if (ld && ld < a->n) return EAGLE3_ERR_INVALID_ARGUMENT;
+    if (a->m == 0) return EAGLE3_OK;
+    if (!a->x || !a->x_scale || !a->w || !a->w_scale || !a->out) return EAGLE3_ERR_INVALID_ARGUMENT;
+    if (a->epilogue == EAGLE3_EPI_SWIGLU && (!a->w2 || !a->w2_scale)) return EAGLE3_ERR_INVALID_ARGUMENT;
+    if (a->epilogue == EAGLE3_EPI_BF16_RESIDUAL && !a->residual) return EAGLE3_ERR_INVALID_ARGUMENT;
+    if (((uintptr_t)a->x | (uintptr_t)a->w | (uintptr_t)a->w2) & 15) return EAGLE3_ERR_INVALID_ARGUMENT;
+    if (((uintptr_t)a->x_scale | (uintptr_t)a->w_scale | (uintptr_t)a->w2_scale | (uintptr_t)a->dev_status) & 3)
+        return EAGLE3_ERR_INVALID_ARGUMENT;
+    if (((uintptr_t)a->out & (a->epilogue == EAGLE3_EPI_F32 ? 3 : 1)) || ((uintptr_t)a->residual & 1))
+        return EAGLE3_ERR_INVALID_ARGUMENT;
+    return EAGLE3_OK;
+}
+
+// 32-row boxes of 128 bytes of the output, for TMA stores; false where its address or pitch rules them out
+bool out_map(CUtensorMap *m, const eagle3_linear_fp8_args_t *a, int64_t ld) {
+    const bool f32 = a->epilogue == EAGLE3_EPI_F32;
+    const int es = f32 ? 4 : 2;
+    if (((uintptr_t)a->out & 15) || (ld * es) % 16) return false;
+    return tmap_rows(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, es, a->out, a->m, a->n,
+                     ld, 32);
+}
+
+template <int NT, bool SWIGLU>
+cudaError_t launch_narrow(dim3 grid, cudaStream_t st, const CUtensorMap &tx, const CUtensorMap &tw,
+                          const CUtensorMap &tw2, const Fp8Params &p) {
+    static PerDevice<cudaError_t> attr;
+    const cudaError_t e = attr.get([] {
+        return cudaFuncSetAttribute(fp8_narrow_kernel<NT, SWIGLU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    NARROW_SMEM);
+    });
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(NARROW_THREADS);
+    cfg.dynamicSmemBytes = NARROW_SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = grid.x;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, fp8_narrow_kernel<NT, SWIGLU>, tx, tw, tw2, p);
+}
+
+template <bool SWIGLU>
+cudaError_t launch_wide(int grid, cudaStream_t st, const CUtensorMap &tx, const CUtensorMap &tw, const CUtensorMap &tw2,
+                        const CUtensorMap &to, const Fp8Params &p) {
+    static PerDevice<cudaError_t> attr;
+    const cudaError_t e = attr.get([] {
+        return cudaFuncSetAttribute(fp8_wide_kernel<SWIGLU>, cudaFuncAttributeMaxDynamicSharedMemorySize, WIDE_SMEM);
+    });
+    if (e != cudaSuccess) return e;
+    return launch_pdl(fp8_wide_kernel<SWIGLU>, dim3(grid), dim3(WIDE_THREADS), WIDE_SMEM, st, tx, tw, tw2, to, p);
+}
+
+}  // namespace
+}  // namespace e3
+
+using namespace e3;
+
+extern "C" eagle3_status_t eagle3_quantize_fp8(const eagle3_quantize_fp8_args_t *a, eagle3_stream_t stream) {
+    const eagle3_status_t st = validate(a);
+    if (st != EAGLE3_OK || a->rows == 0) return st;
+    QuantParams p;
+    p.m = a->rows;
+    p.k = a->k;
+    p.ld_x = a->ld_x ? a->ld_x : a->k;
+    p.ld_q = a->ld_q ? a->ld_q : a->k;
+    p.x = (const __nv_bfloat16 *)a->x;
+    p.q = a->q;
+    p.scale = a->scale;
+    const int64_t pairs = (a->k + 2 * BK - 1) / (2 * BK);
+    const int sms = device_sm_count(), per_block = QUANT_THREADS / 32;
+    auto blocks = [&](int r) { return (pairs * ((a->rows + r - 1) / r) + per_block - 1) / per_block; };
+    const cudaStream_t s = (cudaStream_t)stream;
+    const int r = blocks(8) >= 4 * (int64_t)sms ? 8 : blocks(2) >= 2 * (int64_t)sms ? 2 : 1;
+    const int64_t grid = blocks(r);
+    if (grid > INT32_MAX) return EAGLE3_ERR_UNSUPPORTED;
+    const cudaError_t e =
+        r == 8   ? launch_pdl(quantize_kernel<8>, dim3((unsigned)grid), dim3(QUANT_THREADS), 0, s, p)
+        : r == 2 ? launch_pdl(quantize_kernel<2>, dim3((unsigned)grid), dim3(QUANT_THREADS), 0, s, p)
+                 : launch_pdl(quantize_kernel<1>, dim3((unsigned)grid), dim3(QUANT_THREADS), 0, s, p);
+    return e == cudaSuccess ? EAGLE3_OK : EAGLE3_ERR_CUDA;
+}
+
+extern "C" eagle3_status_t eagle3_linear_fp8(const eagle3_linear_fp8_args_t *a, eagle3_stream_t stream) {
+    const eagle3_status_t st = validate(a);
+    if (st != EAGLE3_OK || a->m == 0) return st;
+    const bool swiglu = a->epilogue == EAGLE3_EPI_SWIGLU;
+    const int64_t ld_x = a->ld_x ? a->ld_x : a->k, ld_w = a->ld_w ? a->ld_w : a->k;
+    Fp8Params p;
+    p.m = a->m;
+    p.n = a->n;
+    p.k = a->k;
+    p.epi = a->epilogue;
+    p.kb_total = (a->k + BK - 1) / BK;
+    p.n_blocks = (a->n + BK - 1) / BK;
+    p.ld_out = a->ld_out ? a->ld_out : a->n;
+    p.ld_res = a->ld_res ? a->ld_res : a->n;
+    p.x_scale = a->x_scale;
+    p.w_scale = a->w_scale;
+    p.w2_scale = a->w2_scale;
+    p.residual = (const __nv_bfloat16 *)a->residual;
+    p.out = a->out;
+    p.dev_status = a->dev_status;
+    const int sms = std::max(1, device_sm_count());
+    const cudaStream_t s = (cudaStream_t)stream;
+    const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    const int tiles_w = (a->n + (swiglu ? 63 : BM - 1)) / (swiglu ? 64 : BM);
+    const bool narrow = a->m <= NARROW_MAX && tiles_w <= 65535;
+    CUtensorMap tx, tw, tw2, to;
+    const int w_box = narrow ? (swiglu ? 16 : BM) : (swiglu ? WIDE_BN / 2 : WIDE_BN);
+    if (!tmap_rows(&tx, u8, 1, a->x, a->m, a->k, ld_x, narrow ? 16 : BM) ||
+        !tmap_rows(&tw, u8, 1, a->w, a->n, a->k, ld_w, w_box))
+        return EAGLE3_ERR_CUDA;
+    tw2 = tw;
+    if (swiglu && !tmap_rows(&tw2, u8, 1, a->w2, a->n, a->k, ld_w, w_box)) return EAGLE3_ERR_CUDA;
+    p.tiles_m = p.tiles_n = p.tma_out = p.n16 = p.stages = 0;
+    cudaError_t e;
+    if (narrow) {
+        const int tiles_r = (a->m + NARROW_MAX - 1) / NARROW_MAX;
+        p.n16 = ((a->m + tiles_r - 1) / tiles_r + 15) / 16 * 16;
+        p.stages = std::min(NARROW_STAGES, NARROW_RING / (NARROW_W + p.n16 * BK));
+        int ranks = 1;
+        while (ranks < NARROW_CLUSTER && (int64_t)tiles_w * tiles_r * (ranks + 1) <= sms &&
+               p.kb_total >= 2 * (ranks + 1))
+            ++ranks;
+        const dim3 grid(ranks, tiles_w, tiles_r);
+        if (p.n16 <= 32)
+            e = swiglu ? launch_narrow<32, true>(grid, s, tx, tw, tw2, p) : launch_narrow<32, false>(grid, s, tx, tw, tw2, p);
+        else if (p.n16 <= 64)
+            e = swiglu ? launch_narrow<64, true>(grid, s, tx, tw, tw2, p) : launch_narrow<64, false>(grid, s, tx, tw, tw2, p);
+        else
+            e = swiglu ? launch_narrow<128, true>(grid, s, tx, tw, tw2, p)
+                       : launch_narrow<128, false>(grid, s, tx, tw, tw2, p);
+    } else {
+        p.tiles_m = (a->m + BM - 1) / BM;
+        p.tiles_n = (a->n + (swiglu ? WIDE_BN / 2 : WIDE_BN) - 1) / (swiglu ? WIDE_BN / 2 : WIDE_BN);
+        const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+        if (tiles > INT32_MAX - sms) return EAGLE3_ERR_UNSUPPORTED;   // tiles are counted in 32 bits
+        p.tma_out = out_map(&to, a, p.ld_out) ? 1 : 0;
+        if (!p.tma_out) to = tx;   // unused
+        const int grid = (int)std::min<int64_t>(sms, tiles);
+        e = swiglu ? launch_wide<true>(grid, s, tx, tw, tw2, to, p) : launch_wide<false>(grid, s, tx, tw, tw2, to, p);
+    }
+    return e == cudaSuccess ? EAGLE3_OK : EAGLE3_ERR_CUDA;
+}

@@ -1,0 +1,447 @@
+// eagle3_grouped_linear: matrix products grouped by expert with ragged row counts, on tcgen05 / TMEM
+// (bf16 in, fp32 accumulate): the expert projections of a mixture-of-experts target's feed-forward
+// layer, y_s = W_e x_s for the rows s that expert e received, with the SwiGLU of "EAGLE-3:
+// Engineering Implementation of LLM Inference Acceleration", appendix C, as an epilogue.
+//
+// The operands are swapped: 128 weight rows (output columns) are the M side of the MMA and the rows
+// of a group are the N side, because N may be any multiple of 16 up to 256 while M is fixed.  A group
+// of any size then wastes at most 15 columns of its last tile, and a group of one row costs its
+// weights' traffic and little else.
+//
+// Persistent, warp-specialised, one CTA per SM; every CTA reads the offsets, and derives the tiles by
+// a prefix sum over the groups:
+//   warp 0      TMA producer: weight tile by one box (SwiGLU: eight boxes of 16 rows, gate and up
+//               alternating, so that a lane and its neighbour 16 lanes on hold a gate / up pair); rows
+//               by boxes of 16, or by gathers of 4 rows that its lanes issue side by side
+//   warp 1      TMEM owner; lane 0 issues tcgen05.mma (M = 128, N = rows of the tile, K = 16)
+//   warps 2..5  epilogue: tcgen05.ld, SwiGLU across lanes, stores of two columns a lane
+// The accumulator is double-buffered in TMEM (2 x 256 columns).  The ring's stage holds a weight tile
+// and as many rows as the largest tile of this call has, so the ring is deep (up to 12 stages) where
+// groups are small and the call is bound by its weights' bytes.  Units run group by group, row tile
+// fastest, so that the CTAs that share a weight tile run together.
+//
+// Every mbarrier wait is bounded; on a timeout the kernel records EAGLE3_DEV_TIMEOUT, stops issuing
+// work, drains its own TMA loads and frees its TMEM.
+#include <algorithm>
+
+#include "../../include/eagle3_chain.h"
+#include "../../include/eagle3_moe.h"
+#include "tc.cuh"
+#include "tmap.cuh"
+
+namespace e3 {
+namespace {
+
+constexpr int BM = 128, BK = 64;          // weight rows and k values of a tile
+constexpr int MAX_ROWS = 256;             // rows of a tile (the MMA's N), a multiple of 16
+constexpr int NTHREADS = 192;
+constexpr int W_BYTES = BM * BK * 2;
+constexpr int ROW_BYTES = BK * 2;
+constexpr int MAX_STAGES = 12;
+constexpr int RING_BYTES = 221 * 1024;
+constexpr int MAX_E = EAGLE3_MOE_MAX_EXPERTS;
+constexpr int TMEM_COLS = 2 * MAX_ROWS;
+
+struct Shared {
+    uint64_t full[MAX_STAGES], empty[MAX_STAGES], tfull[2], tempty[2], mma_done;
+    uint32_t tmem_base;
+    int abort, max_rows;
+    int offsets[MAX_E + 1];
+    int tiles[MAX_E + 1];   // exclusive prefix sums of the groups' row tiles
+};
+constexpr int SMEM = 1024 /* align */ + RING_BYTES + (int)sizeof(Shared);
+static_assert(SMEM <= 232448, "shared memory budget");
+
+struct GroupedParams {
+    int E, m, n, k, n_src, kb_total, tiles_w;
+    int64_t ld_out;
+    __nv_bfloat16 *out;
+    const int32_t *offsets, *row_ids;
+    int32_t *dev_status;
+    int paired;   // rows of out start on 4 bytes: two columns a store
+};
+
+// Row tiles of a group of cnt rows, and the rows of each but the last: even shares (in multiples of
+// 16) of up to 8 tiles, whole tiles of 256 for larger groups.  (t <= 8 shares leave rows for the last:
+// they pass cnt / t by less than 16 each, 16 (t - 1) in all, and cnt / t > 256 (t - 1) / t >= 32 (t - 1).)
+E3_DEV int row_tiles(int cnt) { return (cnt + MAX_ROWS - 1) / MAX_ROWS; }
+E3_DEV int tile_rows(int cnt, int tiles) {
+    return tiles > 8 ? MAX_ROWS : ((cnt + tiles - 1) / tiles + 15) / 16 * 16;
+}
+
+struct Unit {
+    int e, mt, row0, rows, n16;
+};
+
+E3_DEV Unit unit_at(const Shared &sh, const GroupedParams &p, int u) {
+    const int q = u / p.tiles_w;
+    int lo = 0, hi = p.E;   // tiles[lo] <= q < tiles[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (sh.tiles[mid] <= q)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    Unit w;
+    w.e = lo;
+    const int tiles = sh.tiles[lo + 1] - sh.tiles[lo], local = u - sh.tiles[lo] * p.tiles_w;
+    const int cnt = sh.offsets[lo + 1] - sh.offsets[lo], per = tile_rows(cnt, tiles);
+    const int rt = local % tiles;
+    w.mt = local / tiles;
+    w.row0 = sh.offsets[lo] + rt * per;
+    w.rows = min(per, cnt - rt * per);
+    w.n16 = (w.rows + 15) / 16 * 16;
+    return w;
+}
+
+E3_DEV float silu(float x) { return x / (1.0f + __expf(-x)); }
+
+// Two neighbouring columns of a row, col even; the second may lie past n.
+E3_DEV void store_pair(const GroupedParams &p, int row, int col, float a, float b) {
+    __nv_bfloat16 *o = p.out + (size_t)row * p.ld_out + col;
+    if (p.paired && col + 1 < p.n) {
+        *reinterpret_cast<__nv_bfloat162 *>(o) = __floats2bfloat162_rn(a, b);
+    } else {
+        if (col < p.n) o[0] = __float2bfloat16_rn(a);
+        if (col + 1 < p.n) o[1] = __float2bfloat16_rn(b);
+    }
+}
+
+template <bool SWIGLU>
+__global__ void __launch_bounds__(NTHREADS, 1)
+    grouped_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+                   const __grid_constant__ CUtensorMap tm_w2, const GroupedParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *ring = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    Shared &sh = *reinterpret_cast<Shared *>(ring + RING_BYTES);
+    volatile int *abort = &sh.abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < MAX_STAGES; ++s) {
+            tc::mbar_init(&sh.full[s], 1);
+            tc::mbar_init(&sh.empty[s], 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            tc::mbar_init(&sh.tfull[a], 1);
+            tc::mbar_init(&sh.tempty[a], 4);
+        }
+        tc::mbar_init(&sh.mma_done, 1);
+        sh.abort = 0;
+        sh.max_rows = 16;
+        tc::fence_barrier_init();
+        tc::prefetch_tmap(&tm_x);
+        tc::prefetch_tmap(&tm_w);
+        if (SWIGLU) tc::prefetch_tmap(&tm_w2);
+    }
+    if (warp == 1) tc::tmem_alloc(&sh.tmem_base, TMEM_COLS);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = sh.tmem_base;
+    pdl_wait();   // the previous kernel's outputs: offsets, row ids, rows
+    pdl_trigger();
+
+    // the groups' row tiles
+    bool bad = false;
+    for (int e = threadIdx.x; e < p.E; e += NTHREADS) {
+        const int a = p.offsets[e], b = p.offsets[e + 1];
+        bad |= a < 0 || b < a || b > p.m || (e == 0 && a != 0);
+        sh.offsets[e] = a;
+        if (e == p.E - 1) sh.offsets[p.E] = b;
+        if (b > a) {
+            const int tiles = row_tiles(b - a);
+            sh.tiles[e] = tiles;
+            atomicMax(&sh.max_rows, tile_rows(b - a, tiles));
+        } else {
+            sh.tiles[e] = 0;
+        }
+    }
+    bad = __syncthreads_or(bad);
+    if (warp == 0) {   // exclusive prefix sums, 32 groups at a time
+        int run = 0;
+        for (int e0 = 0; e0 < p.E; e0 += 32) {
+            const int v = e0 + lane < p.E ? sh.tiles[e0 + lane] : 0;
+            int inc = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += up;
+            }
+            if (e0 + lane < p.E) sh.tiles[e0 + lane] = run + inc - v;
+            run += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        if (lane == 0) sh.tiles[p.E] = run;
+    }
+    __syncthreads();
+    const int units = bad ? 0 : sh.tiles[p.E] * p.tiles_w;
+    if (bad && blockIdx.x == 0 && threadIdx.x == 0) flag(p.dev_status, EAGLE3_DEV_BAD_COUNTS);
+    const int stage_bytes = W_BYTES + sh.max_rows * ROW_BYTES;   // a multiple of 2048
+    // whole 1024-byte blocks keep the swizzle's phase; the deepest ring that fits
+    const int stages = min(MAX_STAGES, RING_BYTES / stage_bytes);
+
+    if (warp == 0) {
+        // ------------------------------------------------------------------ TMA producer
+        int stage = 0;
+        uint32_t phase = 0, last_parity = 0, issued = 0;   // lane 0: parity of the last load per stage
+        bool ok = true;
+        for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+            const Unit w = unit_at(sh, p, u);
+            int id[2][4];
+            if (p.row_ids) {
+                // gathers lane and lane + 32, four rows each; the rows that fill up the tile repeat its last
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int r = 4 * (lane + 32 * i) + j;
+                        int v = 0;
+                        if (r < w.n16) v = __ldg(p.row_ids + w.row0 + min(r, w.rows - 1));
+                        if (v < 0 || v >= p.n_src) {
+                            flag(p.dev_status, EAGLE3_DEV_BAD_COUNTS);
+                            v = 0;
+                        }
+                        id[i][j] = v;
+                    }
+            }
+            for (int kb = 0; kb < p.kb_total; ++kb) {
+                int fine = 1;
+                if (lane == 0) {
+                    fine = tc::mbar_wait(&sh.empty[stage], phase ^ 1u, abort) ? 1 : 0;
+                    if (fine) {
+                        tc::mbar_expect_tx(&sh.full[stage], W_BYTES + w.n16 * ROW_BYTES);
+                        issued |= 1u << stage;
+                        last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
+                    }
+                }
+                fine = __shfl_sync(0xffffffffu, fine, 0);
+                if (!fine) {
+                    ok = false;
+                    break;
+                }
+                uint8_t *sw = ring + stage * stage_bytes, *sx = sw + W_BYTES;
+                const int x = kb * BK;
+                if (SWIGLU) {
+                    if (lane < 8) {
+                        const int q = lane >> 1, up = lane & 1;   // 16 rows for the lanes of quarter q
+                        tc::tma_load_3d(sw + lane * 16 * ROW_BYTES, up ? &tm_w2 : &tm_w, x, w.mt * 64 + q * 16, w.e,
+                                        &sh.full[stage]);
+                    }
+                } else if (lane == 0) {
+                    tc::tma_load_3d(sw, &tm_w, x, w.mt * BM, w.e, &sh.full[stage]);
+                }
+                if (p.row_ids) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int o = lane + 32 * i;
+                        if (4 * o < w.n16)
+                            tc::tma_gather4(sx + o * 4 * ROW_BYTES, &tm_x, x, id[i][0], id[i][1], id[i][2], id[i][3],
+                                            &sh.full[stage]);
+                    }
+                } else if (16 * lane < w.n16) {
+                    tc::tma_load_2d(sx + lane * 16 * ROW_BYTES, &tm_x, x, w.row0 + lane * 16, &sh.full[stage]);
+                }
+                if (++stage == stages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        if (lane == 0) {
+            if (!ok) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
+            // no TMA write may still be in flight when the CTA exits: wait (bounded) for the last load
+            // issued to every stage; these return at once when the loads were consumed
+            for (int st = 0; st < stages; ++st) {
+                if (!((issued >> st) & 1u)) continue;
+                const uint32_t par = (last_parity >> st) & 1u;
+                const long long t0 = clock64();
+                while (!tc::mbar_try(&sh.full[st], par) && clock64() - t0 < WAIT_LIMIT_CYCLES) {
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            int stage = 0, acc = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            bool ok = true;
+            for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+                const Unit w = unit_at(sh, p, u);
+                const uint32_t idesc = tc::idesc_bf16(BM, w.n16);
+                if (!tc::mbar_wait(&sh.tempty[acc], acc_phase ^ 1u, abort)) {
+                    ok = false;
+                    break;
+                }
+                tc::fence_after();
+                const uint32_t d = tmem + (uint32_t)(acc * MAX_ROWS);
+                for (int kb = 0; kb < p.kb_total; ++kb) {
+                    if (!tc::mbar_wait(&sh.full[stage], phase, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after();
+                    const uint32_t a_addr = smem_u32(ring + stage * stage_bytes), b_addr = a_addr + W_BYTES;
+#pragma unroll
+                    for (int k = 0; k < BK / 16; ++k)
+                        tc::mma_bf16_ss(d, tc::desc_sw128(a_addr + k * 32), tc::desc_sw128(b_addr + k * 32), idesc,
+                                        (kb > 0 || k > 0) ? 1u : 0u);
+                    tc::mma_commit(&sh.empty[stage]);
+                    if (++stage == stages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                tc::mma_commit(&sh.tfull[acc]);
+                acc_phase ^= (uint32_t)acc;
+                acc ^= 1;
+            }
+            if (!ok) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
+            // every MMA this thread issued must retire before TMEM is freed (bounded wait)
+            tc::mma_commit(&sh.mma_done);
+            const long long t0 = clock64();
+            while (!tc::mbar_try(&sh.mma_done, 0) && clock64() - t0 < WAIT_LIMIT_CYCLES) {
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------------ epilogue (warps 2..5)
+        const int quarter = warp & 3;   // TMEM lanes 32 * quarter .. + 31
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        for (int u = blockIdx.x; u < units; u += gridDim.x) {
+            const Unit w = unit_at(sh, p, u);
+            // warp-uniform wait: lane 0 polls, the outcome is broadcast
+            int ok = 0;
+            if (lane == 0) ok = tc::mbar_wait(&sh.tfull[acc], acc_phase, abort) ? 1 : 0;
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) {
+                if (lane == 0) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
+                break;
+            }
+            tc::fence_after();
+            const uint32_t t_col = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * MAX_ROWS);
+            for (int c = 0; c < w.n16; c += 32) {   // this lane's output column of 32 rows
+                float v[32];
+                tc::tmem_ld32(t_col + c, v);
+                if (SWIGLU) {
+                    const bool up = lane >= 16;
+                    const int col = (w.mt * 64 + quarter * 16 + (lane & 15)) & ~1;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        // a gate lane keeps rows i, i + 2 and its up lane i + 1, i + 3
+                        float h[2];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const float a = v[i + 2 * j], b = v[i + 2 * j + 1];
+                            const float other = __shfl_xor_sync(0xffffffffu, up ? a : b, 16);
+                            h[j] = up ? silu(other) * b : silu(a) * other;
+                        }
+                        // then an even lane takes both columns of row i (+ 1), an odd lane of i + 2 (+ 1)
+                        const bool odd = lane & 1;
+                        const float other = __shfl_xor_sync(0xffffffffu, odd ? h[0] : h[1], 1);
+                        const int r = c + i + (odd ? 2 : 0) + (up ? 1 : 0);
+                        if (r < w.rows) store_pair(p, w.row0 + r, col, odd ? other : h[0], odd ? h[1] : other);
+                    }
+                } else {
+                    const bool odd = lane & 1;
+                    const int col = w.mt * BM + quarter * 32 + (lane & ~1);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        // an even lane takes both columns of row i, an odd lane of row i + 1
+                        const float other = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
+                        const int r = c + i + (odd ? 1 : 0);
+                        if (r < w.rows) store_pair(p, w.row0 + r, col, odd ? other : v[i], odd ? v[i + 1] : other);
+                    }
+                }
+            }
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sh.tempty[acc]);
+            acc_phase ^= (uint32_t)acc;
+            acc ^= 1;
+        }
+        __syncwarp();
+    }
+
+    tc::fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc::fence_after();
+        tc::tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
+
+// ---- host side ----------------------------------------------------------------------------------
+eagle3_status_t validate(const eagle3_grouped_linear_args_t *a) {
+    if (!a) return EAGLE3_ERR_INVALID_ARGUMENT;
+    if (a->n_groups < 1 || a->m < 0 || a->n < 1 || a->k < 1) return EAGLE3_ERR_INVALID_ARGUMENT;
+    if (a->epilogue < EAGLE3_EPI_BF16 || a->epilogue > EAGLE3_EPI_BF16_ROPE) return EAGLE3_ERR_INVALID_ARGUMENT;
+    if (a->epilogue != EAGLE3_EPI_BF16 && a->epilogue != EAGLE3_EPI_SWIGLU) return EAGLE3_ERR_UNSUPPORTED;
+    if (a->n_groups > MAX_E || a->k % 8) return EAGLE3_ERR_UNSUPPORTED;
+    if (a->m > MAX_DIM || a->n > MAX_DIM || a->k > MAX_DIM) return EAGLE3_ERR_UNSUPPORTED;
+    const int64_t ld_x = a->ld_x ? a->ld_x : a->k, ld_w = a->ld_w ? a->ld_w : a->k, ld_o = a->ld_out ? a->ld_out : a->n;
+    if (ld_x < a->k || ld_w < a->k || ld_o < a->n || ld_x % 8 || ld_w % 8) return EAGLE3_ERR_INVALID_ARGUMENT;
+    if (a->m == 0) return EAGLE3_OK;
+    if (!a->x || !a->w || !a->out || !a->offsets) return EAGLE3_ERR_INVALID_ARGUMENT;
+    if (a->epilogue == EAGLE3_EPI_SWIGLU && !a->w2) return EAGLE3_ERR_INVALID_ARGUMENT;
+    if (a->row_ids && a->n_src < 1) return EAGLE3_ERR_INVALID_ARGUMENT;
+    if (((uintptr_t)a->x | (uintptr_t)a->w | (uintptr_t)a->w2) & 15) return EAGLE3_ERR_INVALID_ARGUMENT;
+    if (((uintptr_t)a->offsets | (uintptr_t)a->row_ids | (uintptr_t)a->dev_status) & 3 || (uintptr_t)a->out & 1)
+        return EAGLE3_ERR_INVALID_ARGUMENT;
+    // units are counted in 32 bits
+    if ((int64_t)((a->n + 63) / 64) * (a->m / MAX_ROWS + a->n_groups) > INT32_MAX) return EAGLE3_ERR_UNSUPPORTED;
+    return EAGLE3_OK;
+}
+
+}  // namespace
+}  // namespace e3
+
+using namespace e3;
+
+extern "C" eagle3_status_t eagle3_grouped_linear(const eagle3_grouped_linear_args_t *a, eagle3_stream_t stream) {
+    const eagle3_status_t st = validate(a);
+    if (st != EAGLE3_OK || a->m == 0) return st;
+    const bool swiglu = a->epilogue == EAGLE3_EPI_SWIGLU;
+    const int64_t ld_x = a->ld_x ? a->ld_x : a->k, ld_w = a->ld_w ? a->ld_w : a->k;
+    const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    CUtensorMap tx, tw, tw2;
+    if (!tmap_rows(&tx, bf, 2, a->x, a->row_ids ? a->n_src : a->m, a->k, ld_x, a->row_ids ? 1 : 16) ||
+        !tmap_rows(&tw, bf, 2, a->w, a->n, a->k, ld_w, swiglu ? 16 : BM, a->n_groups, a->n * ld_w))
+        return EAGLE3_ERR_CUDA;
+    tw2 = tw;
+    if (swiglu && !tmap_rows(&tw2, bf, 2, a->w2, a->n, a->k, ld_w, 16, a->n_groups, a->n * ld_w)) return EAGLE3_ERR_CUDA;
+    GroupedParams p;
+    p.E = a->n_groups;
+    p.m = a->m;
+    p.n = a->n;
+    p.k = a->k;
+    p.n_src = a->n_src;
+    p.kb_total = (a->k + BK - 1) / BK;
+    p.tiles_w = (a->n + (swiglu ? 63 : BM - 1)) / (swiglu ? 64 : BM);
+    p.ld_out = a->ld_out ? a->ld_out : a->n;
+    p.out = (__nv_bfloat16 *)a->out;
+    p.offsets = a->offsets;
+    p.row_ids = a->row_ids;
+    p.dev_status = a->dev_status;
+    p.paired = p.ld_out % 2 == 0 && ((uintptr_t)a->out & 3) == 0;
+    static PerDevice<cudaError_t> attr;
+    if (attr.get([] {
+            cudaError_t e = cudaFuncSetAttribute(grouped_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(grouped_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+            return e;
+        }) != cudaSuccess)
+        return EAGLE3_ERR_CUDA;
+    const int sms = device_sm_count();
+    const int64_t most = (int64_t)p.tiles_w * (a->m / MAX_ROWS + std::min(a->m, a->n_groups));
+    const int grid = (int)std::min<int64_t>(sms > 0 ? sms : 1, most);
+    const cudaStream_t s = (cudaStream_t)stream;
+    const cudaError_t e =
+        swiglu ? launch_pdl(grouped_kernel<true>, dim3(grid), dim3(NTHREADS), SMEM, s, tx, tw, tw2, p)
+               : launch_pdl(grouped_kernel<false>, dim3(grid), dim3(NTHREADS), SMEM, s, tx, tw, tw2, p);
+    return e == cudaSuccess ? EAGLE3_OK : EAGLE3_ERR_CUDA;
+}

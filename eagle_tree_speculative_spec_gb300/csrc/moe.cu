@@ -1,0 +1,453 @@
+// eagle3_moe_route and eagle3_moe_combine: the row bookkeeping around the products by expert of a
+// mixture-of-experts target's feed-forward layer (the layer's place: "EAGLE-3: Engineering
+// Implementation of LLM Inference Acceleration", appendix C, where it is a dense SwiGLU).
+//
+// Routing.  One warp per row keeps the row's E logits in registers (E / 32 a lane) as unsigned order
+// keys and takes the largest top_k times by a warp reduction of the key and then of the index (the
+// lowest index of the lanes that hold the maximum, so ties are exact); E is at most 512, so a row is
+// read once and its scores need no second pass.  32 rows make a chunk; a row takes an expert at most
+// once, so a chunk's choice of an expert is a 32-bit mask of rows, and a place's rank within the
+// chunk is the population count of the mask below its row: a stable counting sort without any atomic
+// whose order matters.  Up to 32 rows are one launch.  More rows are two: the first also writes the
+// places per (block, expert), the second adds the counts of the blocks before its own (at most 152
+// blocks, so at most 152 x 512 words read from L2 per block), scans the experts and places the rows.
+//
+// Combining.  A thread owns 8 columns of a row and adds the row's top_k vectors in order in fp32; the
+// loads of a row's places do not depend on one another.  Memory bound: every slot is read once.
+#include <algorithm>
+#include <cmath>
+
+#include "../../include/eagle3_chain.h"
+#include "../../include/eagle3_moe.h"
+#include "common.cuh"
+
+namespace e3 {
+namespace {
+
+constexpr int CHUNK = 32;             // rows of a mask
+constexpr int ROUTE_THREADS = 1024;   // a warp per row of a chunk
+constexpr int ROUTE_MAX_BLOCKS = 152;
+constexpr int MAX_E = EAGLE3_MOE_MAX_EXPERTS;
+
+struct RouteParams {
+    int rows, E, k, sigmoid, renorm;
+    float scale;
+    int64_t ld;
+    const float *logits;
+    const int32_t *num_rows;
+    int32_t *ids;
+    float *weights;
+    int32_t *offsets, *sorted, *slots, *dev_status;
+    int32_t *counts;      // [blocks][E] places per block (more than one block)
+    int chunks_per_block; // rows of block b: [b, b + 1) * chunks_per_block * CHUNK
+};
+
+E3_DEV int route_limit(const RouteParams &p) {
+    if (!p.num_rows) return p.rows;
+    const int n = *p.num_rows;
+    if (n < 0 || n > p.rows) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) flag(p.dev_status, EAGLE3_DEV_CAPACITY);
+        return n < 0 ? 0 : p.rows;
+    }
+    return n;
+}
+
+// The experts and weights of one row (all lanes of a warp); lane j < k returns place j's expert or -1.
+template <int PER>
+E3_DEV int route_row(const RouteParams &p, int row, bool live) {
+    const int lane = threadIdx.x & 31;
+    uint32_t key[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int e = i * 32 + lane;
+        key[i] = 0u;   // below the key of every finite number: not available
+        if (live && e < p.E) {
+            const float z = p.logits[(size_t)row * p.ld + e];
+            // -0 + 0 = +0: equal numbers get equal keys
+            if (isfinite(z)) key[i] = order_key(z + 0.0f);
+        }
+    }
+    uint32_t place_key = 0u, high = 0u;
+    int place_id = -1;
+    uint32_t taken = 0u;   // this lane's values that are taken (PER <= 16)
+    for (int j = 0; j < p.k; ++j) {
+        uint32_t best = 0u;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) best = max(best, (taken >> i) & 1u ? 0u : key[i]);
+        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+        if (top == 0u) break;   // uniform: no finite logit is left
+        uint32_t at = 0xffffffffu;
+#pragma unroll
+        for (int i = PER - 1; i >= 0; --i)
+            if (key[i] == top && !((taken >> i) & 1u)) at = (uint32_t)(i * 32 + lane);
+        at = __reduce_min_sync(0xffffffffu, at);
+        if ((int)(at & 31u) == lane) taken |= 1u << (at >> 5);
+        if (j == 0) high = top;
+        if (lane == j) {
+            place_key = top;
+            place_id = (int)at;
+        }
+    }
+    // scores of the places; the largest logit is place 0's
+    const float m = high ? key_to_float(high) : 0.0f;
+    float score = 0.0f, total = 1.0f;
+    if (place_id >= 0) {
+        const float z = key_to_float(place_key);
+        score = p.sigmoid ? 1.0f / (1.0f + expf(-z)) : expf(z - m);
+    }
+    if (p.renorm || !p.sigmoid) {
+        float part = score;
+        if (!p.renorm) {   // softmax over all finite logits
+            part = 0.0f;
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (key[i]) part += expf(key_to_float(key[i]) - m);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+        total = part;
+    }
+    if (lane < p.k) {
+        p.ids[(size_t)row * p.k + lane] = place_id;
+        p.weights[(size_t)row * p.k + lane] = total > 0.0f ? score / total * p.scale : 0.0f;
+    }
+    return place_id;
+}
+
+// Exclusive scan over the experts of total[0 .. E) (shared memory, ROUTE_THREADS threads): returns
+// this thread's (thread = expert) start, and the sum of all in *sum.
+E3_DEV int scan_experts(int v, int *warp_sums, int *sum) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += up;
+    }
+    if (lane == 31) warp_sums[warp] = inc;
+    __syncthreads();
+    int w = warp_sums[lane];   // ROUTE_THREADS / 32 = 32 warps
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += up;
+    }
+    *sum = __shfl_sync(0xffffffffu, w, 31);
+    const int before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
+    return inc - v + (warp > 0 ? before : 0);
+}
+
+// Slots of the chunk's places.  masks: the chunk's rows per expert; base: each expert's next slot.
+E3_DEV void place_chunk(const RouteParams &p, int row0, const uint32_t *masks, const int *base) {
+    for (int i = threadIdx.x; i < CHUNK * p.k; i += ROUTE_THREADS) {
+        const int r = i / p.k, row = row0 + r;
+        if (row >= p.rows) continue;
+        const size_t at = (size_t)row * p.k + (i - r * p.k);
+        const int e = p.ids[at];
+        int slot = -1;
+        if (e >= 0) {
+            slot = base[e] + __popc(masks[e] & ((1u << r) - 1u));
+            p.sorted[slot] = row;
+        }
+        p.slots[at] = slot;
+    }
+}
+
+// Experts and weights of every row; with one block also the offsets and slots, otherwise the places
+// per expert of this block's rows.
+template <int PER>
+__global__ void __launch_bounds__(ROUTE_THREADS) moe_route_kernel(const RouteParams p) {
+    __shared__ uint32_t masks[MAX_E];
+    __shared__ int base[MAX_E], warp_sums[32];
+    pdl_wait();
+    pdl_trigger();
+    const int limit = route_limit(p);
+    const int warp = threadIdx.x >> 5;
+    int mine = 0;   // thread e: places of expert e in this block
+    for (int c = 0; c < p.chunks_per_block; ++c) {
+        const int row0 = (blockIdx.x * p.chunks_per_block + c) * CHUNK, row = row0 + warp;
+        if (threadIdx.x < MAX_E) masks[threadIdx.x] = 0u;
+        __syncthreads();
+        if (row < p.rows) {
+            const int id = route_row<PER>(p, row, row < limit);
+            if (id >= 0) atomicOr(&masks[id], 1u << warp);
+        }
+        __syncthreads();
+        if (threadIdx.x < MAX_E) mine += __popc(masks[threadIdx.x]);
+        if (gridDim.x > 1) __syncthreads();
+    }
+    if (gridDim.x > 1) {
+        if (threadIdx.x < p.E) p.counts[(size_t)blockIdx.x * p.E + threadIdx.x] = mine;
+        return;
+    }
+    // a single block holds a single chunk
+    int total;
+    const int start = scan_experts(mine, warp_sums, &total);
+    if (threadIdx.x < MAX_E) base[threadIdx.x] = start;
+    if (threadIdx.x < p.E) p.offsets[threadIdx.x] = start;
+    if (threadIdx.x == 0) p.offsets[p.E] = total;
+    __syncthreads();
+    place_chunk(p, 0, masks, base);
+    for (int s = total + threadIdx.x; s < p.rows * p.k; s += ROUTE_THREADS) p.sorted[s] = -1;
+}
+
+__global__ void __launch_bounds__(ROUTE_THREADS) moe_place_kernel(const RouteParams p) {
+    __shared__ uint32_t masks[MAX_E];
+    __shared__ int base[MAX_E], before[ROUTE_THREADS], all[ROUTE_THREADS], warp_sums[32];
+    pdl_wait();
+    pdl_trigger();
+    // thread (g, e): blocks g, g + G, ... of expert e
+    const int width = p.E <= 128 ? 128 : p.E <= 256 ? 256 : 512, G = ROUTE_THREADS / width;
+    const int e = threadIdx.x % width, g = threadIdx.x / width;
+    int sum = 0, ahead = 0;
+    if (e < p.E) {
+#pragma unroll 8
+        for (int b = g; b < (int)gridDim.x; b += G) {
+            const int v = __ldg(p.counts + (size_t)b * p.E + e);
+            sum += v;
+            ahead += b < (int)blockIdx.x ? v : 0;
+        }
+    }
+    all[threadIdx.x] = sum;
+    before[threadIdx.x] = ahead;
+    __syncthreads();
+    int mine = 0, first = 0, total;
+    if (threadIdx.x < width)
+        for (int i = 0; i < G; ++i) {
+            mine += all[i * width + threadIdx.x];
+            first += before[i * width + threadIdx.x];
+        }
+    const int start = scan_experts(mine, warp_sums, &total);
+    if (threadIdx.x < MAX_E) base[threadIdx.x] = start + first;
+    if (blockIdx.x == 0) {
+        if (threadIdx.x < p.E) p.offsets[threadIdx.x] = start;
+        if (threadIdx.x == 0) p.offsets[p.E] = total;
+    }
+    for (int c = 0; c < p.chunks_per_block; ++c) {
+        const int row0 = (blockIdx.x * p.chunks_per_block + c) * CHUNK;
+        if (threadIdx.x < MAX_E) masks[threadIdx.x] = 0u;
+        __syncthreads();
+        for (int i = threadIdx.x; i < CHUNK * p.k; i += ROUTE_THREADS) {
+            const int r = i / p.k, row = row0 + r;
+            const int id = row < p.rows ? p.ids[(size_t)row * p.k + (i - r * p.k)] : -1;
+            if (id >= 0) atomicOr(&masks[id], 1u << r);
+        }
+        __syncthreads();
+        place_chunk(p, row0, masks, base);
+        __syncthreads();
+        if (threadIdx.x < MAX_E) base[threadIdx.x] += __popc(masks[threadIdx.x]);
+    }
+    const long long end = (long long)p.rows * p.k;
+    for (long long s = total + (long long)blockIdx.x * ROUTE_THREADS + threadIdx.x; s < end;
+         s += (long long)gridDim.x * ROUTE_THREADS)
+        p.sorted[s] = -1;
+}
+
+// ---- combine ------------------------------------------------------------------------------------
+constexpr int COMBINE_THREADS = 128;
+
+struct CombineParams {
+    int rows, n_slots, k, d;
+    int64_t ld_y, ld_res, ld_out;
+    const __nv_bfloat16 *y, *res;
+    const int32_t *slots;
+    const float *weights;
+    __nv_bfloat16 *out;
+    int32_t *dev_status;
+};
+
+template <int VEC>
+struct Pack;
+template <>
+struct Pack<8> {
+    using T = uint4;
+};
+template <>
+struct Pack<2> {
+    using T = uint32_t;
+};
+template <>
+struct Pack<1> {
+    using T = uint16_t;
+};
+
+template <int VEC>
+E3_DEV void unpack(const typename Pack<VEC>::T &r, float (&v)[VEC]) {
+    const __nv_bfloat16 *h = reinterpret_cast<const __nv_bfloat16 *>(&r);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = __bfloat162float(h[i]);
+}
+
+// VEC columns a thread: 8 where every row starts on 16 bytes, 2 on 4, else 1.
+template <int VEC>
+__global__ void __launch_bounds__(COMBINE_THREADS) moe_combine_kernel(const CombineParams p) {
+    using T = typename Pack<VEC>::T;
+    pdl_wait();
+    pdl_trigger();
+    const int row = blockIdx.x;
+    const int col = (blockIdx.y * COMBINE_THREADS + threadIdx.x) * VEC;
+    if (col >= p.d) return;   // VEC divides d
+    float acc[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
+    T res;
+    if (p.res) res = *reinterpret_cast<const T *>(p.res + (size_t)row * p.ld_res + col);
+    const int32_t *slots = p.slots + (size_t)row * p.k;
+    const float *weights = p.weights + (size_t)row * p.k;
+#pragma unroll 8
+    for (int j = 0; j < p.k; ++j) {
+        const int s = __ldg(slots + j);
+        if (s < 0) continue;
+        if (s >= p.n_slots) {
+            flag(p.dev_status, EAGLE3_DEV_BAD_COUNTS);
+            continue;
+        }
+        const float w = __ldg(weights + j);
+        const T raw = __ldg(reinterpret_cast<const T *>(p.y + (size_t)s * p.ld_y + col));
+        float v[VEC];
+        unpack<VEC>(raw, v);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) acc[i] = fmaf(w, v[i], acc[i]);
+    }
+    if (p.res) {
+        float v[VEC];
+        unpack<VEC>(res, v);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) acc[i] += v[i];
+    }
+    T o;
+    __nv_bfloat16 *h = reinterpret_cast<__nv_bfloat16 *>(&o);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) h[i] = __float2bfloat16_rn(acc[i]);
+    *reinterpret_cast<T *>(p.out + (size_t)row * p.ld_out + col) = o;
+}
+
+// ---- host side ----------------------------------------------------------------------------------
+struct RoutePlan {
+    int blocks, chunks_per_block;
+    size_t ws_bytes;
+};
+
+RoutePlan route_plan(const eagle3_moe_route_args_t *a) {
+    const int chunks = (a->rows + CHUNK - 1) / CHUNK;
+    RoutePlan pl;
+    pl.chunks_per_block = std::max(1, (chunks + ROUTE_MAX_BLOCKS - 1) / ROUTE_MAX_BLOCKS);
+    pl.blocks = std::max(1, (chunks + pl.chunks_per_block - 1) / pl.chunks_per_block);
+    pl.ws_bytes = pl.blocks > 1 ? (size_t)pl.blocks * a->n_experts * sizeof(int32_t) : 0;
+    return pl;
+}
+
+eagle3_status_t validate(const eagle3_moe_route_args_t *a) {
+    if (!a) return EAGLE3_ERR_INVALID_ARGUMENT;
+    if (a->rows < 0 || a->n_experts < 1 || a->top_k < 1 || a->top_k > a->n_experts) return EAGLE3_ERR_INVALID_ARGUMENT;
+    if (a->scoring != EAGLE3_MOE_SOFTMAX && a->scoring != EAGLE3_MOE_SIGMOID) return EAGLE3_ERR_INVALID_ARGUMENT;
+    if ((a->renormalize != 0 && a->renormalize != 1) || !std::isfinite(a->scale)) return EAGLE3_ERR_INVALID_ARGUMENT;
+    if (a->ld_logits && a->ld_logits < a->n_experts) return EAGLE3_ERR_INVALID_ARGUMENT;
+    if (a->n_experts > EAGLE3_MOE_MAX_EXPERTS || a->top_k > EAGLE3_MOE_MAX_TOP_K) return EAGLE3_ERR_UNSUPPORTED;
+    if ((int64_t)a->rows * a->top_k > MAX_DIM) return EAGLE3_ERR_UNSUPPORTED;   // slots are 32-bit
+    if (!a->expert_offsets) return EAGLE3_ERR_INVALID_ARGUMENT;
+    if (a->rows && (!a->logits || !a->topk_ids || !a->topk_weights || !a->sorted_rows || !a->slots))
+        return EAGLE3_ERR_INVALID_ARGUMENT;
+    const uintptr_t all = (uintptr_t)a->logits | (uintptr_t)a->num_rows | (uintptr_t)a->topk_ids |
+                          (uintptr_t)a->topk_weights | (uintptr_t)a->expert_offsets | (uintptr_t)a->sorted_rows |
+                          (uintptr_t)a->slots | (uintptr_t)a->dev_status;
+    return all & 3 ? EAGLE3_ERR_INVALID_ARGUMENT : EAGLE3_OK;
+}
+
+eagle3_status_t validate(const eagle3_moe_combine_args_t *a) {
+    if (!a) return EAGLE3_ERR_INVALID_ARGUMENT;
+    if (a->rows < 0 || a->n_slots < 0 || a->top_k < 1 || a->dim < 1) return EAGLE3_ERR_INVALID_ARGUMENT;
+    if (a->top_k > EAGLE3_MOE_MAX_TOP_K || a->rows > MAX_DIM) return EAGLE3_ERR_UNSUPPORTED;
+    if (a->dim > 65535 * COMBINE_THREADS) return EAGLE3_ERR_UNSUPPORTED;   // column blocks of the grid
+    for (const int64_t ld : {a->ld_y, a->ld_res, a->ld_out})
+        if (ld && ld < a->dim) return EAGLE3_ERR_INVALID_ARGUMENT;
+    if (a->rows == 0) return EAGLE3_OK;
+    if ((a->n_slots && !a->y) || !a->slots || !a->weights || !a->out) return EAGLE3_ERR_INVALID_ARGUMENT;
+    if (((uintptr_t)a->y | (uintptr_t)a->residual | (uintptr_t)a->out) & 1) return EAGLE3_ERR_INVALID_ARGUMENT;
+    if (((uintptr_t)a->slots | (uintptr_t)a->weights | (uintptr_t)a->dev_status) & 3) return EAGLE3_ERR_INVALID_ARGUMENT;
+    return EAGLE3_OK;
+}
+
+template <int PER>
+cudaError_t launch_route(int blocks, cudaStream_t st, const RouteParams &p) {
+    return launch_pdl(moe_route_kernel<PER>, dim3(blocks), dim3(ROUTE_THREADS), 0, st, p);
+}
+
+template <int VEC>
+cudaError_t launch_combine(cudaStream_t st, const CombineParams &p) {
+    const int per_block = COMBINE_THREADS * VEC;
+    return launch_pdl(moe_combine_kernel<VEC>, dim3(p.rows, (p.d + per_block - 1) / per_block), dim3(COMBINE_THREADS),
+                      0, st, p);
+}
+
+}  // namespace
+}  // namespace e3
+
+using namespace e3;
+
+extern "C" size_t eagle3_moe_route_workspace_size(const eagle3_moe_route_args_t *a) {
+    return validate(a) == EAGLE3_OK ? route_plan(a).ws_bytes : 0;
+}
+
+extern "C" eagle3_status_t eagle3_moe_route(const eagle3_moe_route_args_t *a, void *workspace, size_t ws_bytes,
+                                            eagle3_stream_t stream) {
+    const eagle3_status_t st = validate(a);
+    if (st != EAGLE3_OK) return st;
+    const RoutePlan pl = route_plan(a);
+    if (pl.ws_bytes && (!workspace || ws_bytes < pl.ws_bytes || ((uintptr_t)workspace & 15))) return EAGLE3_ERR_WORKSPACE;
+    RouteParams p;
+    p.rows = a->rows;
+    p.E = a->n_experts;
+    p.k = a->top_k;
+    p.sigmoid = a->scoring == EAGLE3_MOE_SIGMOID;
+    p.renorm = a->renormalize;
+    p.scale = a->scale;
+    p.ld = a->ld_logits ? a->ld_logits : a->n_experts;
+    p.logits = a->logits;
+    p.num_rows = a->num_rows;
+    p.ids = a->topk_ids;
+    p.weights = a->topk_weights;
+    p.offsets = a->expert_offsets;
+    p.sorted = a->sorted_rows;
+    p.slots = a->slots;
+    p.dev_status = a->dev_status;
+    p.counts = (int32_t *)workspace;
+    p.chunks_per_block = pl.chunks_per_block;
+    const cudaStream_t s = (cudaStream_t)stream;
+    const int per = (a->n_experts + 31) / 32;
+    const cudaError_t e = per <= 2   ? launch_route<2>(pl.blocks, s, p)
+                          : per <= 4 ? launch_route<4>(pl.blocks, s, p)
+                          : per <= 8 ? launch_route<8>(pl.blocks, s, p)
+                                     : launch_route<16>(pl.blocks, s, p);
+    if (e != cudaSuccess) return EAGLE3_ERR_CUDA;
+    if (pl.blocks > 1 && launch_pdl(moe_place_kernel, dim3(pl.blocks), dim3(ROUTE_THREADS), 0, s, p) != cudaSuccess)
+        return EAGLE3_ERR_CUDA;
+    return EAGLE3_OK;
+}
+
+extern "C" eagle3_status_t eagle3_moe_combine(const eagle3_moe_combine_args_t *a, eagle3_stream_t stream) {
+    const eagle3_status_t st = validate(a);
+    if (st != EAGLE3_OK || a->rows == 0) return st;
+    CombineParams p;
+    p.rows = a->rows;
+    p.n_slots = a->n_slots;
+    p.k = a->top_k;
+    p.d = a->dim;
+    p.ld_y = a->ld_y ? a->ld_y : a->dim;
+    p.ld_res = a->ld_res ? a->ld_res : a->dim;
+    p.ld_out = a->ld_out ? a->ld_out : a->dim;
+    p.y = (const __nv_bfloat16 *)a->y;
+    p.res = (const __nv_bfloat16 *)a->residual;
+    p.slots = a->slots;
+    p.weights = a->weights;
+    p.out = (__nv_bfloat16 *)a->out;
+    p.dev_status = a->dev_status;
+    // the widest vector that every row starts on
+    int64_t step = p.d | p.ld_y | p.ld_out | (p.res ? p.ld_res : 0);
+    const uintptr_t base = (uintptr_t)p.y | (uintptr_t)p.out | (uintptr_t)p.res;
+    const cudaStream_t s = (cudaStream_t)stream;
+    const cudaError_t e = step % 8 == 0 && base % 16 == 0  ? launch_combine<8>(s, p)
+                          : step % 2 == 0 && base % 4 == 0 ? launch_combine<2>(s, p)
+                                                           : launch_combine<1>(s, p);
+    return e == cudaSuccess ? EAGLE3_OK : EAGLE3_ERR_CUDA;
+}

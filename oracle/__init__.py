@@ -20,6 +20,8 @@ compact     Copy of the accepted path's K/V (and aux rows) into cache slots.
 attention   RoPE and tree-masked verify attention.
 llama       Tiny Llama target, EAGLE-3 draft head, vanilla and speculative decoding.
 draft_tree  Dynamic top-k draft tree (expand, frontier select, final rerank).
+moe         Expert routing, products by expert, weighted sum.
+fp8         e4m3 values with block scales: quantisation and the scaled product.
 
 Parity status per function is stated in each module header; every function
 without an independent pin says "parity unpinned".
