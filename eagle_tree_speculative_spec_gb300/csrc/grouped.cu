@@ -10,11 +10,16 @@
 //
 // Persistent, warp-specialised, one CTA per SM; every CTA reads the offsets, and derives the tiles by
 // a prefix sum over the groups:
-//   warp 0      TMA producer: weight tile by one box (SwiGLU: eight boxes of 16 rows, gate and up
-//               alternating, so that a lane and its neighbour 16 lanes on hold a gate / up pair); rows
-//               by boxes of 16, or by gathers of 4 rows that its lanes issue side by side
+//   warp 0      TMA producer: the weight tile (SwiGLU: 64 gate and 64 up rows), and the rows unless they
+//               are gathered, by at most three boxes (a box costs about 70 cycles whatever its size:
+//               boxes of 16 rows held a 3840-row product to 835 TFLOP/s)
 //   warp 1      TMEM owner; lane 0 issues tcgen05.mma (M = 128, N = rows of the tile, K = 16)
-//   warps 2..5  epilogue: tcgen05.ld, SwiGLU across lanes, stores of two columns a lane
+//   warps 2..5  epilogue: tcgen05.ld, SwiGLU, stores of two columns a lane.  TMEM lanes 0..63 hold gate
+//               columns and 64..127 their up columns: two warps that share columns swap them through
+//               shared memory, and each finishes half of the rows
+//   warps 6..9  with row_ids only: gather the rows by 16-byte asynchronous copies into the swizzled
+//               tile (TMA's four-row gathers cost as much as a box each: 2288 us for 3840 rows x 8 of
+//               64 experts, k = 4096, 2 x 1024 columns)
 // The accumulator is double-buffered in TMEM (2 x 256 columns).  The ring's stage holds a weight tile
 // and as many rows as the largest tile of this call has, so the ring is deep (up to 12 stages) where
 // groups are small and the call is bound by its weights' bytes.  Units run group by group, row tile
@@ -34,15 +39,16 @@ namespace {
 
 constexpr int BM = 128, BK = 64;          // weight rows and k values of a tile
 constexpr int MAX_ROWS = 256;             // rows of a tile (the MMA's N), a multiple of 16
-constexpr int NTHREADS = 192;
+constexpr int NTHREADS = 192, GATHER_WARPS = 4;
 constexpr int W_BYTES = BM * BK * 2;
 constexpr int ROW_BYTES = BK * 2;
 constexpr int MAX_STAGES = 12;
-constexpr int RING_BYTES = 221 * 1024;
+constexpr int RING_BYTES = 205 * 1024;
 constexpr int MAX_E = EAGLE3_MOE_MAX_EXPERTS;
 constexpr int TMEM_COLS = 2 * MAX_ROWS;
 
 struct Shared {
+    float swap[2][2][32 * 32];   // SwiGLU: per pair of warps, what each hands to the other
     uint64_t full[MAX_STAGES], empty[MAX_STAGES], tfull[2], tempty[2], mma_done;
     uint32_t tmem_base;
     int abort, max_rows;
@@ -52,9 +58,20 @@ struct Shared {
 constexpr int SMEM = 1024 /* align */ + RING_BYTES + (int)sizeof(Shared);
 static_assert(SMEM <= 232448, "shared memory budget");
 
+// Rows that a tile's boxes load: one box of 256, or up to three of 64 and one of 16 (at most the
+// next multiple of 64; rows past the tile's are loaded and not used).
+E3_DEV int box_rows(int n16) {
+    const int rest = n16 & 63;
+    return n16 > 192 ? 256 : (n16 & ~63) + (rest > 16 ? 64 : rest);
+}
+struct RowMaps {
+    CUtensorMap b16, b64, b256;
+};
+
 struct GroupedParams {
     int E, m, n, k, n_src, kb_total, tiles_w;
-    int64_t ld_out;
+    int64_t ld_out, ld_x;
+    const __nv_bfloat16 *x;   // gathered rows
     __nv_bfloat16 *out;
     const int32_t *offsets, *row_ids;
     int32_t *dev_status;
@@ -97,6 +114,26 @@ E3_DEV Unit unit_at(const Shared &sh, const GroupedParams &p, int u) {
 
 E3_DEV float silu(float x) { return x / (1.0f + __expf(-x)); }
 
+// 16 bytes to shared memory, or 16 zero bytes (src is not read then)
+E3_DEV void copy16(uint32_t dst, const void *src, bool zero) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(zero ? 0 : 16) : "memory");
+}
+// arrive on bar once this thread's copies so far have landed
+E3_DEV void copies_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(smem_u32(bar)) : "memory");
+}
+// Barrier `id` over two warps; the variant with a flag tells whether it was set for all threads.
+E3_DEV void pair_sync(int id) { asm volatile("bar.sync %0, 64;\n" ::"r"(id) : "memory"); }
+E3_DEV bool pair_all(int id, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n bar.red.and.pred q, %1, 64, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(r)
+        : "r"(id), "r"(v ? 1u : 0u)
+        : "memory");
+    return r != 0;
+}
+
 // Two neighbouring columns of a row, col even; the second may lie past n.
 E3_DEV void store_pair(const GroupedParams &p, int row, int col, float a, float b) {
     __nv_bfloat16 *o = p.out + (size_t)row * p.ld_out + col;
@@ -108,9 +145,9 @@ E3_DEV void store_pair(const GroupedParams &p, int row, int col, float a, float 
     }
 }
 
-template <bool SWIGLU>
-__global__ void __launch_bounds__(NTHREADS, 1)
-    grouped_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+template <bool SWIGLU, bool GATHER>
+__global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1)
+    grouped_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ CUtensorMap tm_w,
                    const __grid_constant__ CUtensorMap tm_w2, const GroupedParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -120,7 +157,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < MAX_STAGES; ++s) {
-            tc::mbar_init(&sh.full[s], 1);
+            tc::mbar_init(&sh.full[s], GATHER ? 1 + 32 * GATHER_WARPS : 1);
             tc::mbar_init(&sh.empty[s], 1);
         }
         for (int a = 0; a < 2; ++a) {
@@ -131,7 +168,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         sh.abort = 0;
         sh.max_rows = 16;
         tc::fence_barrier_init();
-        tc::prefetch_tmap(&tm_x);
+        if (!GATHER) {
+            tc::prefetch_tmap(&tm_x.b16);
+            tc::prefetch_tmap(&tm_x.b64);
+            tc::prefetch_tmap(&tm_x.b256);
+        }
         tc::prefetch_tmap(&tm_w);
         if (SWIGLU) tc::prefetch_tmap(&tm_w2);
     }
@@ -145,7 +186,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 
     // the groups' row tiles
     bool bad = false;
-    for (int e = threadIdx.x; e < p.E; e += NTHREADS) {
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
         const int a = p.offsets[e], b = p.offsets[e + 1];
         bad |= a < 0 || b < a || b > p.m || (e == 0 && a != 0);
         sh.offsets[e] = a;
@@ -153,7 +194,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         if (b > a) {
             const int tiles = row_tiles(b - a);
             sh.tiles[e] = tiles;
-            atomicMax(&sh.max_rows, tile_rows(b - a, tiles));
+            const int n16 = tile_rows(b - a, tiles);   // box_rows never decreases: the last tile needs no more
+            atomicMax(&sh.max_rows, GATHER ? n16 : box_rows(n16));
         } else {
             sh.tiles[e] = 0;
         }
@@ -183,72 +225,46 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------------------ TMA producer
-        int stage = 0;
-        uint32_t phase = 0, last_parity = 0, issued = 0;   // lane 0: parity of the last load per stage
-        bool ok = true;
-        for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-            const Unit w = unit_at(sh, p, u);
-            int id[2][4];
-            if (p.row_ids) {
-                // gathers lane and lane + 32, four rows each; the rows that fill up the tile repeat its last
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int r = 4 * (lane + 32 * i) + j;
-                        int v = 0;
-                        if (r < w.n16) v = __ldg(p.row_ids + w.row0 + min(r, w.rows - 1));
-                        if (v < 0 || v >= p.n_src) {
-                            flag(p.dev_status, EAGLE3_DEV_BAD_COUNTS);
-                            v = 0;
-                        }
-                        id[i][j] = v;
-                    }
-            }
-            for (int kb = 0; kb < p.kb_total; ++kb) {
-                int fine = 1;
-                if (lane == 0) {
-                    fine = tc::mbar_wait(&sh.empty[stage], phase ^ 1u, abort) ? 1 : 0;
-                    if (fine) {
-                        tc::mbar_expect_tx(&sh.full[stage], W_BYTES + w.n16 * ROW_BYTES);
-                        issued |= 1u << stage;
-                        last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
-                    }
-                }
-                fine = __shfl_sync(0xffffffffu, fine, 0);
-                if (!fine) {
-                    ok = false;
-                    break;
-                }
-                uint8_t *sw = ring + stage * stage_bytes, *sx = sw + W_BYTES;
-                const int x = kb * BK;
-                if (SWIGLU) {
-                    if (lane < 8) {
-                        const int q = lane >> 1, up = lane & 1;   // 16 rows for the lanes of quarter q
-                        tc::tma_load_3d(sw + lane * 16 * ROW_BYTES, up ? &tm_w2 : &tm_w, x, w.mt * 64 + q * 16, w.e,
-                                        &sh.full[stage]);
-                    }
-                } else if (lane == 0) {
-                    tc::tma_load_3d(sw, &tm_w, x, w.mt * BM, w.e, &sh.full[stage]);
-                }
-                if (p.row_ids) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int o = lane + 32 * i;
-                        if (4 * o < w.n16)
-                            tc::tma_gather4(sx + o * 4 * ROW_BYTES, &tm_x, x, id[i][0], id[i][1], id[i][2], id[i][3],
-                                            &sh.full[stage]);
-                    }
-                } else if (16 * lane < w.n16) {
-                    tc::tma_load_2d(sx + lane * 16 * ROW_BYTES, &tm_x, x, w.row0 + lane * 16, &sh.full[stage]);
-                }
-                if (++stage == stages) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
-            }
-        }
         if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0, last_parity = 0, issued = 0;   // parity of the last load per stage
+            bool ok = true;
+            for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+                const Unit w = unit_at(sh, p, u);
+                const int boxes = box_rows(w.n16);
+                for (int kb = 0; kb < p.kb_total; ++kb) {
+                    uint64_t *full = &sh.full[stage];
+                    if (!tc::mbar_wait(&sh.empty[stage], phase ^ 1u, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::mbar_expect_tx(full, W_BYTES + (GATHER ? 0 : boxes * ROW_BYTES));
+                    issued |= 1u << stage;
+                    last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
+                    uint8_t *sw = ring + stage * stage_bytes, *sx = sw + W_BYTES;
+                    const int x = kb * BK;
+                    if (SWIGLU) {
+                        tc::tma_load_3d(sw, &tm_w, x, w.mt * (BM / 2), w.e, full);
+                        tc::tma_load_3d(sw + W_BYTES / 2, &tm_w2, x, w.mt * (BM / 2), w.e, full);
+                    } else {
+                        tc::tma_load_3d(sw, &tm_w, x, w.mt * BM, w.e, full);
+                    }
+                    if (!GATHER) {
+                        if (boxes == 256) {
+                            tc::tma_load_2d(sx, &tm_x.b256, x, w.row0, full);
+                        } else {
+                            int r = 0;
+                            for (; r + 64 <= boxes; r += 64)
+                                tc::tma_load_2d(sx + r * ROW_BYTES, &tm_x.b64, x, w.row0 + r, full);
+                            if (r < boxes) tc::tma_load_2d(sx + r * ROW_BYTES, &tm_x.b16, x, w.row0 + r, full);
+                        }
+                    }
+                    if (++stage == stages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
             if (!ok) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
             // no TMA write may still be in flight when the CTA exits: wait (bounded) for the last load
             // issued to every stage; these return at once when the loads were consumed
@@ -281,6 +297,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
                         ok = false;
                         break;
                     }
+                    if (GATHER) tc::fence_proxy_async_smem();   // the copies were made outside the async proxy
                     tc::fence_after();
                     const uint32_t a_addr = smem_u32(ring + stage * stage_bytes), b_addr = a_addr + W_BYTES;
 #pragma unroll
@@ -306,6 +323,52 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             }
         }
         __syncwarp();
+    } else if (GATHER && warp >= 6) {
+        // ------------------------------------------------------------------ row gather (warps 6..9)
+        // Thread t copies 16-byte piece t % 8 of rows t / 8 + 16 i; its arrival on the stage's barrier
+        // follows its copies by itself.
+        const int t = threadIdx.x - NTHREADS, piece = t & 7, first = t >> 3;
+        const uint32_t dst0 = smem_u32(ring) + W_BYTES + first * ROW_BYTES + ((piece ^ (first & 7)) << 4);
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+            const Unit w = unit_at(sh, p, u);
+            const __nv_bfloat16 *src[MAX_ROWS / 16];
+#pragma unroll
+            for (int i = 0; i < MAX_ROWS / 16; ++i) {
+                if (16 * i >= w.n16) continue;
+                // rows past the tile's last repeat it
+                int v = __ldg(p.row_ids + w.row0 + min(first + 16 * i, w.rows - 1));
+                if (v < 0 || v >= p.n_src) {
+                    flag(p.dev_status, EAGLE3_DEV_BAD_COUNTS);
+                    v = 0;
+                }
+                src[i] = p.x + (size_t)v * p.ld_x + piece * 8;
+            }
+            for (int kb = 0; kb < p.kb_total; ++kb) {
+                int fine = 0;
+                if (lane == 0) fine = tc::mbar_wait(&sh.empty[stage], phase ^ 1u, abort) ? 1 : 0;
+                fine = __shfl_sync(0xffffffffu, fine, 0);
+                if (!fine) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t dst = dst0 + stage * stage_bytes;
+                const bool past = kb * BK + piece * 8 >= p.k;   // k is a multiple of 8
+                const int at = past ? 0 : kb * BK;
+#pragma unroll
+                for (int i = 0; i < MAX_ROWS / 16; ++i)
+                    if (16 * i < w.n16) copy16(dst + i * 16 * ROW_BYTES, src[i] + at, past);
+                copies_arrive(&sh.full[stage]);
+                if (++stage == stages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        asm volatile("cp.async.wait_all;\n" ::: "memory");
+        if (!ok && lane == 0) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
     } else {
         // ------------------------------------------------------------------ epilogue (warps 2..5)
         const int quarter = warp & 3;   // TMEM lanes 32 * quarter .. + 31
@@ -317,44 +380,52 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             int ok = 0;
             if (lane == 0) ok = tc::mbar_wait(&sh.tfull[acc], acc_phase, abort) ? 1 : 0;
             ok = __shfl_sync(0xffffffffu, ok, 0);
+            // (the two warps of a pair go on or leave together: they meet at barriers below)
+            if (SWIGLU) ok = pair_all(1 + (quarter & 1), ok);
             if (!ok) {
                 if (lane == 0) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
                 break;
             }
             tc::fence_after();
             const uint32_t t_col = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * MAX_ROWS);
-            for (int c = 0; c < w.n16; c += 32) {   // this lane's output column of 32 rows
-                float v[32];
-                tc::tmem_ld32(t_col + c, v);
-                if (SWIGLU) {
-                    const bool up = lane >= 16;
-                    const int col = (w.mt * 64 + quarter * 16 + (lane & 15)) & ~1;
+            const bool odd = lane & 1;
+            // rows r, r + 1, ... of this lane's column: an even lane stores both columns of row r, its
+            // odd neighbour those of row r + 1
+            auto store32 = [&](const float (&v)[32], int r0, int col) {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        // a gate lane keeps rows i, i + 2 and its up lane i + 1, i + 3
-                        float h[2];
+                for (int i = 0; i < 32; i += 2) {
+                    const float other = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
+                    const int r = r0 + i + (odd ? 1 : 0);
+                    if (r < w.rows) store_pair(p, w.row0 + r, col, odd ? other : v[i], odd ? v[i + 1] : other);
+                }
+            };
+            if (SWIGLU) {
+                const int pair = quarter & 1, up = quarter >> 1;
+                const int col = w.mt * (BM / 2) + pair * 32 + (lane & ~1);
+                for (int c = 0; c < w.n16; c += 64) {   // the gate warp takes rows c.., the up warp c + 32..
+                    const int mine = c + 32 * up, theirs = c + 32 * (up ^ 1);
+                    float v[32];
+                    if (theirs < w.n16) {
+                        tc::tmem_ld32(t_col + theirs, v);
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const float a = v[i + 2 * j], b = v[i + 2 * j + 1];
-                            const float other = __shfl_xor_sync(0xffffffffu, up ? a : b, 16);
-                            h[j] = up ? silu(other) * b : silu(a) * other;
-                        }
-                        // then an even lane takes both columns of row i (+ 1), an odd lane of i + 2 (+ 1)
-                        const bool odd = lane & 1;
-                        const float other = __shfl_xor_sync(0xffffffffu, odd ? h[0] : h[1], 1);
-                        const int r = c + i + (odd ? 2 : 0) + (up ? 1 : 0);
-                        if (r < w.rows) store_pair(p, w.row0 + r, col, odd ? other : h[0], odd ? h[1] : other);
+                        for (int i = 0; i < 32; ++i) sh.swap[pair][up][i * 32 + lane] = v[i];
                     }
-                } else {
-                    const bool odd = lane & 1;
-                    const int col = w.mt * BM + quarter * 32 + (lane & ~1);
+                    pair_sync(1 + pair);
+                    if (mine < w.n16) {
+                        tc::tmem_ld32(t_col + mine, v);
+                        const float *o = sh.swap[pair][up ^ 1] + lane;
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        // an even lane takes both columns of row i, an odd lane of row i + 1
-                        const float other = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
-                        const int r = c + i + (odd ? 1 : 0);
-                        if (r < w.rows) store_pair(p, w.row0 + r, col, odd ? other : v[i], odd ? v[i + 1] : other);
+                        for (int i = 0; i < 32; ++i) v[i] = up ? silu(o[i * 32]) * v[i] : silu(v[i]) * o[i * 32];
+                        store32(v, mine, col);
                     }
+                    pair_sync(1 + pair);   // both have read before the next rows overwrite
+                }
+            } else {
+                const int col = w.mt * BM + quarter * 32 + (lane & ~1);
+                for (int c = 0; c < w.n16; c += 32) {
+                    float v[32];
+                    tc::tmem_ld32(t_col + c, v);
+                    store32(v, c, col);
                 }
             }
             tc::fence_before();
@@ -397,6 +468,18 @@ eagle3_status_t validate(const eagle3_grouped_linear_args_t *a) {
     return EAGLE3_OK;
 }
 
+template <bool SWIGLU, bool GATHER>
+cudaError_t launch_grouped(int grid, cudaStream_t st, const RowMaps &tx, const CUtensorMap &tw,
+                           const CUtensorMap &tw2, const GroupedParams &p) {
+    static PerDevice<cudaError_t> attr;
+    const cudaError_t e = attr.get([] {
+        return cudaFuncSetAttribute(grouped_kernel<SWIGLU, GATHER>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    });
+    if (e != cudaSuccess) return e;
+    return launch_pdl(grouped_kernel<SWIGLU, GATHER>, dim3(grid), dim3(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0)), SMEM,
+                      st, tx, tw, tw2, p);
+}
+
 }  // namespace
 }  // namespace e3
 
@@ -408,12 +491,17 @@ extern "C" eagle3_status_t eagle3_grouped_linear(const eagle3_grouped_linear_arg
     const bool swiglu = a->epilogue == EAGLE3_EPI_SWIGLU;
     const int64_t ld_x = a->ld_x ? a->ld_x : a->k, ld_w = a->ld_w ? a->ld_w : a->k;
     const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    CUtensorMap tx, tw, tw2;
-    if (!tmap_rows(&tx, bf, 2, a->x, a->row_ids ? a->n_src : a->m, a->k, ld_x, a->row_ids ? 1 : 16) ||
-        !tmap_rows(&tw, bf, 2, a->w, a->n, a->k, ld_w, swiglu ? 16 : BM, a->n_groups, a->n * ld_w))
+    CUtensorMap tw, tw2;
+    RowMaps tx;
+    if (!tmap_rows(&tw, bf, 2, a->w, a->n, a->k, ld_w, swiglu ? BM / 2 : BM, a->n_groups, a->n * ld_w))
         return EAGLE3_ERR_CUDA;
-    tw2 = tw;
-    if (swiglu && !tmap_rows(&tw2, bf, 2, a->w2, a->n, a->k, ld_w, 16, a->n_groups, a->n * ld_w)) return EAGLE3_ERR_CUDA;
+    tw2 = tx.b16 = tx.b64 = tx.b256 = tw;   // where unused
+    if (swiglu && !tmap_rows(&tw2, bf, 2, a->w2, a->n, a->k, ld_w, BM / 2, a->n_groups, a->n * ld_w))
+        return EAGLE3_ERR_CUDA;
+    if (!a->row_ids && (!tmap_rows(&tx.b16, bf, 2, a->x, a->m, a->k, ld_x, 16) ||
+                        !tmap_rows(&tx.b64, bf, 2, a->x, a->m, a->k, ld_x, 64) ||
+                        !tmap_rows(&tx.b256, bf, 2, a->x, a->m, a->k, ld_x, 256)))
+        return EAGLE3_ERR_CUDA;
     GroupedParams p;
     p.E = a->n_groups;
     p.m = a->m;
@@ -423,25 +511,21 @@ extern "C" eagle3_status_t eagle3_grouped_linear(const eagle3_grouped_linear_arg
     p.kb_total = (a->k + BK - 1) / BK;
     p.tiles_w = (a->n + (swiglu ? 63 : BM - 1)) / (swiglu ? 64 : BM);
     p.ld_out = a->ld_out ? a->ld_out : a->n;
+    p.ld_x = ld_x;
+    p.x = (const __nv_bfloat16 *)a->x;
     p.out = (__nv_bfloat16 *)a->out;
     p.offsets = a->offsets;
     p.row_ids = a->row_ids;
     p.dev_status = a->dev_status;
     p.paired = p.ld_out % 2 == 0 && ((uintptr_t)a->out & 3) == 0;
-    static PerDevice<cudaError_t> attr;
-    if (attr.get([] {
-            cudaError_t e = cudaFuncSetAttribute(grouped_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-            if (e == cudaSuccess)
-                e = cudaFuncSetAttribute(grouped_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-            return e;
-        }) != cudaSuccess)
-        return EAGLE3_ERR_CUDA;
     const int sms = device_sm_count();
     const int64_t most = (int64_t)p.tiles_w * (a->m / MAX_ROWS + std::min(a->m, a->n_groups));
     const int grid = (int)std::min<int64_t>(sms > 0 ? sms : 1, most);
     const cudaStream_t s = (cudaStream_t)stream;
-    const cudaError_t e =
-        swiglu ? launch_pdl(grouped_kernel<true>, dim3(grid), dim3(NTHREADS), SMEM, s, tx, tw, tw2, p)
-               : launch_pdl(grouped_kernel<false>, dim3(grid), dim3(NTHREADS), SMEM, s, tx, tw, tw2, p);
+    const bool gather = a->row_ids != nullptr;
+    const cudaError_t e = swiglu ? (gather ? launch_grouped<true, true>(grid, s, tx, tw, tw2, p)
+                                           : launch_grouped<true, false>(grid, s, tx, tw, tw2, p))
+                                 : (gather ? launch_grouped<false, true>(grid, s, tx, tw, tw2, p)
+                                           : launch_grouped<false, false>(grid, s, tx, tw, tw2, p));
     return e == cudaSuccess ? EAGLE3_OK : EAGLE3_ERR_CUDA;
 }

@@ -95,15 +95,6 @@ E3_DEV void tma_load_2d(void *smem_dst, const CUtensorMap *map, int x, int y, ui
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
         : "memory");
 }
-// Four rows of a 2-D map whose box is one row high, at column x: consecutive 128-byte rows of the
-// destination (the swizzle goes by the shared-memory address, as for a box of four rows).
-E3_DEV void tma_gather4(void *smem_dst, const CUtensorMap *map, int x, int r0, int r1, int r2, int r3, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], "
-        "[%1, {%2, %3, %4, %5, %6}], [%7];\n" ::"r"(smem_u32(smem_dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(smem_u32(bar))
-        : "memory");
-}
 E3_DEV void prefetch_tmap(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
