@@ -34,7 +34,8 @@ constexpr int BK = 128;                 // k values of a block and of a tile (12
 constexpr int BM = 128;
 constexpr float E4M3_MAX = 448.0f;
 
-E3_DEV float silu(float x) { return x / (1.0f + __expf(-x)); }
+// (the special function unit's division: 2 steps of fp32 off at the most, 0 where exp(-x) > 2^126)
+E3_DEV float silu(float x) { return __fdividef(x, 1.0f + __expf(-x)); }
 
 struct Fp8Params {
     int m, n, k, epi, kb_total, n_blocks;   // n_blocks: row blocks of w_scale
