@@ -668,71 +668,74 @@ def eagle3_verify_attn_noalloc(q, tree_k, tree_v, k_cache, v_cache, parents, pre
 
 
 # ----------------------------------------------------------------------------- mixture of experts, 8 bits
-def _on(device, stream):
-    """Raw handle of the launch stream: `stream`, or the current stream of the tensors' device, which
-    has to be the current device (the library launches there)."""
-    if device.type != "cuda":
+# These calls are also made eagerly for single tokens, where a kernel takes 2 to 8 us: the checks of an
+# argument are one expression of attribute reads, and only a refused one is looked at more closely.
+def _on(index, stream):
+    """Raw handle of the launch stream: `stream`, or the current stream of the tensors' device `index`,
+    which has to be the current device (the library launches there)."""
+    if index < 0:
         raise ValueError("the tensors must be on a CUDA device")
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {device}, which is not the current device")
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    if index != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on cuda:{index}, which is not the current device")
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
-def _arg(t, dtype, shape, device, name):
-    """Data pointer of a dense tensor of this type, shape and device."""
+def _refuse(t, dtype, shape, index, name):
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, not on the other tensors' device")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _rows_arg(t, dtype, shape, device, name):
+def _arg(t, dtype, shape, index, name):
+    """Data pointer of a dense tensor of this type and shape on device `index`."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, dtype, shape, index, name)
+
+
+def _rows_arg(t, dtype, shape, index, name):
     """(data pointer, row pitch) of a 2-D view whose rows are contiguous and do not overlap."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index:
+        _refuse(t, dtype, shape, index, name)
     pitch, inner = t.stride()
-    if inner != 1 and shape[1] > 1:
+    rows, cols = shape
+    if inner != 1 and cols > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    if shape[0] <= 1:
-        return t.data_ptr(), shape[1]   # a single row's pitch means nothing
-    if pitch < shape[1]:
+    if rows <= 1:
+        return t.data_ptr(), cols   # a single row's pitch means nothing
+    if pitch < cols:
         raise ValueError(f"{name} has overlapping rows")
     return t.data_ptr(), pitch
 
 
-def _scratch(need, workspace, device, stream):
+def _scratch(need, workspace, like, stream):
     """(pointer, bytes) of the caller's workspace, or of one allocated here (kept until the launch
     stream is done with it)."""
     if workspace is not None:
-        if workspace.device != device or not workspace.is_contiguous():
-            raise ValueError(f"the workspace must be a contiguous tensor on {device}")
+        if workspace.get_device() != like.get_device() or not workspace.is_contiguous():
+            raise ValueError("the workspace must be a contiguous tensor on the other tensors' device")
         return workspace.data_ptr(), workspace.numel() * workspace.element_size()
     if need == 0:
         return None, 0
-    own = torch.empty(need, dtype=torch.uint8, device=device)
+    own = torch.empty(need, dtype=torch.uint8, device=like.device)
     if stream is not None:
         own.record_stream(stream)
     return own.data_ptr(), need
 
 
-def _status_arg(t, device):
-    return None if t is None else _arg(t, torch.int32, t.shape, device, "dev_status")
+def _status_arg(t, index):
+    return None if t is None else _arg(t, torch.int32, t.shape, index, "dev_status")
 
 
 def moe_route_args(logits, topk_ids, topk_weights, expert_offsets, sorted_rows, slots, *, scoring=MOE_SOFTMAX,
                    renormalize=True, scale=1.0, num_rows=None, dev_status=None):
     T, E = logits.shape
     k = topk_ids.shape[1]
-    dev, i32 = logits.device, torch.int32
+    dev, i32 = logits.get_device(), torch.int32
     lp, ld = _rows_arg(logits, torch.float32, (T, E), dev, "logits")
     return MoeRouteArgs(T, E, k, int(scoring), 1 if renormalize else 0, float(scale), ld, lp,
                         None if num_rows is None else _arg(num_rows, i32, (1,), dev, "num_rows"),
@@ -751,16 +754,16 @@ def eagle3_moe_route(logits, topk_ids, topk_weights, expert_offsets, sorted_rows
     expert."""
     a = moe_route_args(logits, topk_ids, topk_weights, expert_offsets, sorted_rows, slots, scoring=scoring,
                        renormalize=renormalize, scale=scale, num_rows=num_rows, dev_status=dev_status)
-    st = _on(logits.device, stream)
+    st = _on(logits.get_device(), stream)
     L, ref = lib(), ctypes.byref(a)
-    ws, nbytes = _scratch(L.eagle3_moe_route_workspace_size(ref), workspace, logits.device, stream)
+    ws, nbytes = _scratch(L.eagle3_moe_route_workspace_size(ref), workspace, logits, stream)
     _check(L.eagle3_moe_route(ref, ws, nbytes, st), "eagle3_moe_route")
 
 
 def grouped_linear_args(x, w, offsets, out, *, epilogue=EPI_BF16, w2=None, row_ids=None, dev_status=None):
     E, n, k = w.shape
     m = out.shape[0]
-    dev, bf, i32 = out.device, torch.bfloat16, torch.int32
+    dev, bf, i32 = out.get_device(), torch.bfloat16, torch.int32
     n_src = x.shape[0]
     xp, ld_x = _rows_arg(x, bf, (n_src if row_ids is not None else m, k), dev, "x")
     op, ld_out = _rows_arg(out, bf, (m, n), dev, "out")
@@ -778,13 +781,13 @@ def eagle3_grouped_linear(x, w, offsets, out, *, epilogue=EPI_BF16, w2=None, row
     [m, k] bf16, or with row_ids ([m] int32) any number of rows to gather from.  Rows of x and out may be
     pitched.  Rows of out at or past offsets[E] are left as they were."""
     a = grouped_linear_args(x, w, offsets, out, epilogue=epilogue, w2=w2, row_ids=row_ids, dev_status=dev_status)
-    _check(lib().eagle3_grouped_linear(ctypes.byref(a), _on(out.device, stream)), "eagle3_grouped_linear")
+    _check(lib().eagle3_grouped_linear(ctypes.byref(a), _on(out.get_device(), stream)), "eagle3_grouped_linear")
 
 
 def moe_combine_args(y, slots, weights, out, *, residual=None, dev_status=None):
     T, k = slots.shape
     n_slots, d = y.shape
-    dev, bf = out.device, torch.bfloat16
+    dev, bf = out.get_device(), torch.bfloat16
     yp, ld_y = _rows_arg(y, bf, (n_slots, d), dev, "y")
     op, ld_out = _rows_arg(out, bf, (T, d), dev, "out")
     rp, ld_res = (None, 0) if residual is None else _rows_arg(residual, bf, (T, d), dev, "residual")
@@ -797,12 +800,12 @@ def eagle3_moe_combine(y, slots, weights, out, *, residual=None, dev_status=None
     y [n_slots, d] bf16, slots [T, k] int32, weights [T, k] fp32, out / residual [T, d] bf16; rows of y,
     out and residual may be pitched, out may be residual itself."""
     a = moe_combine_args(y, slots, weights, out, residual=residual, dev_status=dev_status)
-    _check(lib().eagle3_moe_combine(ctypes.byref(a), _on(out.device, stream)), "eagle3_moe_combine")
+    _check(lib().eagle3_moe_combine(ctypes.byref(a), _on(out.get_device(), stream)), "eagle3_moe_combine")
 
 
 def quantize_fp8_args(x, q, scale):
     m, k = x.shape
-    dev = x.device
+    dev = x.get_device()
     xp, ld_x = _rows_arg(x, torch.bfloat16, (m, k), dev, "x")
     qp, ld_q = _rows_arg(q, torch.float8_e4m3fn, (m, k), dev, "q")
     return QuantizeFp8Args(m, k, ld_x, ld_q, xp, qp, _arg(scale, torch.float32, (-(-k // 128), m), dev, "scale"))
@@ -812,7 +815,7 @@ def eagle3_quantize_fp8(x, q, scale, *, stream=None):
     """Rows of bf16 to e4m3 with one scale for each row and 128 columns: x [m, k] bf16, q [m, k]
     float8_e4m3fn (rows of both may be pitched), scale [ceil(k / 128), m] fp32; k a multiple of 16."""
     a = quantize_fp8_args(x, q, scale)
-    _check(lib().eagle3_quantize_fp8(ctypes.byref(a), _on(x.device, stream)), "eagle3_quantize_fp8")
+    _check(lib().eagle3_quantize_fp8(ctypes.byref(a), _on(x.get_device(), stream)), "eagle3_quantize_fp8")
 
 
 def linear_fp8_args(x, x_scale, w, w_scale, out, *, epilogue=EPI_BF16, w2=None, w2_scale=None, residual=None,
@@ -820,7 +823,7 @@ def linear_fp8_args(x, x_scale, w, w_scale, out, *, epilogue=EPI_BF16, w2=None, 
     m, k = x.shape
     n = w.shape[0]
     kb, nb = -(-k // 128), -(-n // 128)
-    dev, f8, f32, bf = x.device, torch.float8_e4m3fn, torch.float32, torch.bfloat16
+    dev, f8, f32, bf = x.get_device(), torch.float8_e4m3fn, torch.float32, torch.bfloat16
     xp, ld_x = _rows_arg(x, f8, (m, k), dev, "x")
     wp, ld_w = _rows_arg(w, f8, (n, k), dev, "w")
     op, ld_out = _rows_arg(out, f32 if epilogue == EPI_F32 else bf, (m, n), dev, "out")
@@ -845,7 +848,7 @@ def eagle3_linear_fp8(x, x_scale, w, w_scale, out, *, epilogue=EPI_BF16, w2=None
     k a multiple of 16."""
     a = linear_fp8_args(x, x_scale, w, w_scale, out, epilogue=epilogue, w2=w2, w2_scale=w2_scale, residual=residual,
                         dev_status=dev_status)
-    _check(lib().eagle3_linear_fp8(ctypes.byref(a), _on(x.device, stream)), "eagle3_linear_fp8")
+    _check(lib().eagle3_linear_fp8(ctypes.byref(a), _on(x.get_device(), stream)), "eagle3_linear_fp8")
 
 
 # ----------------------------------------------------------------------------- fp32 small-model blocks

@@ -60,6 +60,47 @@ struct QuantParams {
     float *scale;
 };
 
+// The codes of a lane's 8 values by IEEE division.
+__device__ __noinline__ uint2 codes_exact(uint4 raw, float s) {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    uint32_t q[2] = {0u, 0u};
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = make_float2(__fdiv_rn(__uint_as_float(w[i] << 16), s),
+                                     __fdiv_rn(__uint_as_float(w[i] & 0xffff0000u), s));
+        const uint32_t c = (uint32_t)__nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+        if (i < 2)
+            q[0] |= c << (16 * i);
+        else
+            q[1] |= c << (16 * (i - 2));
+    }
+    return make_uint2(q[0], q[1]);
+}
+
+// e4m3(x / s) for 8 values.  x times (1 / s) (1 -+ 2^-21) encloses the correctly rounded quotient (1 / s
+// and the two products are off by 2^-24 each), and the conversion is monotone: where both ends have the
+// same code it is the quotient's; otherwise (a border between two codes in between: about one value in
+// 2^17) the lane divides.  Divisions for every value made the kernel issue-bound: 42 us for 3840 x 14336
+// against 25 us of bytes.
+E3_DEV uint2 codes(uint4 raw, float s) {
+    const float inv = __fdiv_rn(1.0f, s);
+    const float2 lo = make_float2(inv * (1.0f - 0x1p-21f), inv * (1.0f - 0x1p-21f));
+    const float2 hi = make_float2(inv * (1.0f + 0x1p-21f), inv * (1.0f + 0x1p-21f));
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    uint32_t a[4], b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 x = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+        a[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(__fmul2_rn(x, lo), __NV_SATFINITE, __NV_E4M3);
+        b[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(__fmul2_rn(x, hi), __NV_SATFINITE, __NV_E4M3);
+    }
+    const uint2 qa = make_uint2(a[0] | (a[1] << 16), a[2] | (a[3] << 16));
+    const uint2 qb = make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
+    // (below 2^-120 the reciprocal may overflow; a NaN scale is not above it either)
+    if (qa.x != qb.x || qa.y != qb.y || !(s >= 0x1p-120f)) return codes_exact(raw, s);
+    return qa;
+}
+
 // A half warp holds a block of 128 columns of one row, 8 values a lane; a warp takes two neighbouring
 // blocks of R consecutive rows, all loads first, and writes the R scales of a block side by side.
 template <int R>
@@ -95,15 +136,7 @@ __global__ void __launch_bounds__(QUANT_THREADS) quantize_kernel(const QuantPara
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         if (!in || row0 + r >= p.m) continue;
-        const uint32_t w[4] = {raw[r].x, raw[r].y, raw[r].z, raw[r].w};
-        uint32_t q[2] = {0u, 0u};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 v = make_float2(__fdiv_rn(__uint_as_float(w[i] << 16), s[r]),
-                                         __fdiv_rn(__uint_as_float(w[i] & 0xffff0000u), s[r]));
-            q[i >> 1] |= (uint32_t)__nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3) << (16 * (i & 1));
-        }
-        *reinterpret_cast<uint2 *>(p.q + (size_t)(row0 + r) * p.ld_q + col) = make_uint2(q[0], q[1]);
+        *reinterpret_cast<uint2 *>(p.q + (size_t)(row0 + r) * p.ld_q + col) = codes(raw[r], s[r]);
     }
     // lane r of the half warp writes row r's scale
     const int hl = lane & 15;
@@ -155,7 +188,11 @@ E3_DEV void store8(const Fp8Params &p, int row, int col, const float *v) {
 }
 
 // ---- wide ---------------------------------------------------------------------------------------
-constexpr int WIDE_BN = 256, WIDE_STAGES = 4, WIDE_EPI_WARPS = 8, WIDE_THREADS = 64 + 32 * WIDE_EPI_WARPS;
+// Three warpgroups: loads and MMAs (warps 0 and 1; 2 and 3 idle), and two of the epilogue.  The block
+// is launched with 168 registers a thread (384 x 168 = 64512); the first group keeps 56 and the
+// epilogue takes 224 (128 x 56 + 256 x 224 = 64512): 128 accumulators and two loads in flight.
+constexpr int WIDE_BN = 256, WIDE_STAGES = 4, WIDE_EPI_WARPS = 8, WIDE_THREADS = 128 + 32 * WIDE_EPI_WARPS;
+constexpr int WIDE_EPI0 = 4;   // first epilogue warp
 constexpr int WIDE_A = BM * BK, WIDE_B = WIDE_BN * BK, WIDE_STAGE = WIDE_A + WIDE_B;
 constexpr int WIDE_BOX = 32 * 128;   // output staging: 32 rows x 128 bytes a warp
 struct WideShared {
@@ -165,6 +202,15 @@ struct WideShared {
 };
 constexpr int WIDE_SMEM = 1024 + WIDE_STAGES * WIDE_STAGE + WIDE_EPI_WARPS * WIDE_BOX + (int)sizeof(WideShared);
 static_assert(WIDE_SMEM <= 232448, "shared memory budget");
+
+template <int N>
+E3_DEV void registers_give() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N>
+E3_DEV void registers_take() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
 
 template <bool SWIGLU>
 __global__ void __launch_bounds__(WIDE_THREADS, 1)
@@ -203,88 +249,92 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
     pdl_trigger();
     const int units = p.tiles_m * p.tiles_n;
 
-    if (warp == 0) {
-        // ------------------------------------------------------------------ TMA producer
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0, last_parity = 0, issued = 0;
-            bool ok = true;
-            for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-                const int mb = u % p.tiles_m, nb = u / p.tiles_m;
-                for (int kb = 0; kb < p.kb_total; ++kb) {
-                    if (!tc::mbar_wait(&sh.empty[stage], phase ^ 1u, abort)) {
-                        ok = false;
-                        break;
+    if (warp < WIDE_EPI0) {
+        registers_give<56>();
+        if (warp == 0) {
+            // ------------------------------------------------------------------ TMA producer
+            if (lane == 0) {
+                int stage = 0;
+                uint32_t phase = 0, last_parity = 0, issued = 0;
+                bool ok = true;
+                for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+                    const int mb = u % p.tiles_m, nb = u / p.tiles_m;
+                    for (int kb = 0; kb < p.kb_total; ++kb) {
+                        if (!tc::mbar_wait(&sh.empty[stage], phase ^ 1u, abort)) {
+                            ok = false;
+                            break;
+                        }
+                        uint8_t *sx = ring + stage * WIDE_STAGE, *sw = sx + WIDE_A;
+                        tc::mbar_expect_tx(&sh.full[stage], WIDE_STAGE);
+                        tc::tma_load_2d(sx, &tm_x, kb * BK, mb * BM, &sh.full[stage]);
+                        if (SWIGLU) {
+                            tc::tma_load_2d(sw, &tm_w, kb * BK, nb * (WIDE_BN / 2), &sh.full[stage]);
+                            tc::tma_load_2d(sw + WIDE_B / 2, &tm_w2, kb * BK, nb * (WIDE_BN / 2), &sh.full[stage]);
+                        } else {
+                            tc::tma_load_2d(sw, &tm_w, kb * BK, nb * WIDE_BN, &sh.full[stage]);
+                        }
+                        issued |= 1u << stage;
+                        last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
+                        if (++stage == WIDE_STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
                     }
-                    uint8_t *sx = ring + stage * WIDE_STAGE, *sw = sx + WIDE_A;
-                    tc::mbar_expect_tx(&sh.full[stage], WIDE_STAGE);
-                    tc::tma_load_2d(sx, &tm_x, kb * BK, mb * BM, &sh.full[stage]);
-                    if (SWIGLU) {
-                        tc::tma_load_2d(sw, &tm_w, kb * BK, nb * (WIDE_BN / 2), &sh.full[stage]);
-                        tc::tma_load_2d(sw + WIDE_B / 2, &tm_w2, kb * BK, nb * (WIDE_BN / 2), &sh.full[stage]);
-                    } else {
-                        tc::tma_load_2d(sw, &tm_w, kb * BK, nb * WIDE_BN, &sh.full[stage]);
-                    }
-                    issued |= 1u << stage;
-                    last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
-                    if (++stage == WIDE_STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
+                }
+                if (!ok) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
+                // no TMA write may still be in flight when the CTA exits (bounded waits)
+                for (int st = 0; st < WIDE_STAGES; ++st) {
+                    if (!((issued >> st) & 1u)) continue;
+                    const uint32_t par = (last_parity >> st) & 1u;
+                    const long long t0 = clock64();
+                    while (!tc::mbar_try(&sh.full[st], par) && clock64() - t0 < WAIT_LIMIT_CYCLES) {
                     }
                 }
             }
-            if (!ok) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
-            // no TMA write may still be in flight when the CTA exits (bounded waits)
-            for (int st = 0; st < WIDE_STAGES; ++st) {
-                if (!((issued >> st) & 1u)) continue;
-                const uint32_t par = (last_parity >> st) & 1u;
-                const long long t0 = clock64();
-                while (!tc::mbar_try(&sh.full[st], par) && clock64() - t0 < WAIT_LIMIT_CYCLES) {
-                }
-            }
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        // ------------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            constexpr uint32_t IDESC = tc::idesc_e4m3(BM, WIDE_BN);
-            int stage = 0, buf = 0;
-            uint32_t phase = 0, buf_phase = 0;
-            bool ok = true;
-            for (int u = blockIdx.x; ok && u < units; u += gridDim.x)
-                for (int kb = 0; kb < p.kb_total; ++kb) {
-                    if (!tc::mbar_wait(&sh.tempty[buf], buf_phase ^ 1u, abort) ||
-                        !tc::mbar_wait(&sh.full[stage], phase, abort)) {
-                        ok = false;
-                        break;
-                    }
-                    tc::fence_after();
-                    const uint32_t a = smem_u32(ring + stage * WIDE_STAGE), b = a + WIDE_A;
+            __syncwarp();
+        } else if (warp == 1) {
+            // ------------------------------------------------------------------ MMA issuer
+            if (lane == 0) {
+                constexpr uint32_t IDESC = tc::idesc_e4m3(BM, WIDE_BN);
+                int stage = 0, buf = 0;
+                uint32_t phase = 0, buf_phase = 0;
+                bool ok = true;
+                for (int u = blockIdx.x; ok && u < units; u += gridDim.x)
+                    for (int kb = 0; kb < p.kb_total; ++kb) {
+                        if (!tc::mbar_wait(&sh.tempty[buf], buf_phase ^ 1u, abort) ||
+                            !tc::mbar_wait(&sh.full[stage], phase, abort)) {
+                            ok = false;
+                            break;
+                        }
+                        tc::fence_after();
+                        const uint32_t a = smem_u32(ring + stage * WIDE_STAGE), b = a + WIDE_A;
 #pragma unroll
-                    for (int k = 0; k < BK / 32; ++k)
-                        tc::mma_e4m3_ss(tmem + buf * WIDE_BN, tc::desc_sw128(a + k * 32), tc::desc_sw128(b + k * 32),
-                                        IDESC, k > 0 ? 1u : 0u);
-                    tc::mma_commit(&sh.empty[stage]);
-                    tc::mma_commit(&sh.tfull[buf]);
-                    if (++stage == WIDE_STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
+                        for (int k = 0; k < BK / 32; ++k)
+                            tc::mma_e4m3_ss(tmem + buf * WIDE_BN, tc::desc_sw128(a + k * 32), tc::desc_sw128(b + k * 32),
+                                            IDESC, k > 0 ? 1u : 0u);
+                        tc::mma_commit(&sh.empty[stage]);
+                        tc::mma_commit(&sh.tfull[buf]);
+                        if (++stage == WIDE_STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                        buf_phase ^= (uint32_t)buf;
+                        buf ^= 1;
                     }
-                    buf_phase ^= (uint32_t)buf;
-                    buf ^= 1;
+                if (!ok) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
+                // every MMA this thread issued must retire before TMEM is freed (bounded wait)
+                tc::mma_commit(&sh.mma_done);
+                const long long t0 = clock64();
+                while (!tc::mbar_try(&sh.mma_done, 0) && clock64() - t0 < WAIT_LIMIT_CYCLES) {
                 }
-            if (!ok) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
-            // every MMA this thread issued must retire before TMEM is freed (bounded wait)
-            tc::mma_commit(&sh.mma_done);
-            const long long t0 = clock64();
-            while (!tc::mbar_try(&sh.mma_done, 0) && clock64() - t0 < WAIT_LIMIT_CYCLES) {
             }
+            __syncwarp();
         }
-        __syncwarp();
     } else {
-        // ------------------------------------------------------------------ epilogue (warps 2..9)
-        const int quarter = warp & 3, half = (warp - 2) >> 2;
-        uint8_t *box = boxes + (warp - 2) * WIDE_BOX;
+        registers_take<224>();
+        // ------------------------------------------------------------------ epilogue (warps 4..11)
+        const int quarter = warp & 3, half = (warp - WIDE_EPI0) >> 2;
+        uint8_t *box = boxes + (warp - WIDE_EPI0) * WIDE_BOX;
         // this thread's two runs of 64 accumulator columns: neighbours, or gate and up of one run
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         const uint32_t run_a = lanes + (SWIGLU ? 64 * half : 128 * half), run_b = run_a + (SWIGLU ? 128 : 64);
@@ -319,16 +369,28 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                 }
                 tc::fence_after();
                 const uint32_t t = tmem + (uint32_t)(buf * WIDE_BN);
+                // 32 columns a load, the next one in flight while the last is added
+                float v[2][32];
+                tc::tmem_ld32_start(t + run_a, v[0]);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    float v[32];
-                    tc::tmem_ld32(t + (c < 2 ? run_a : run_b) + (c & 1) * 32, v);
+                    tc::tmem_ld_wait(v[c & 1]);
+                    if (c < 3) {
+                        tc::tmem_ld32_start(t + (c < 1 ? run_a + 32 : run_b + (c - 1) * 32), v[(c + 1) & 1]);
+                    } else {   // the buffer is read: the MMAs may have it
+                        tc::fence_before();
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(&sh.tempty[buf]);
+                    }
+                    const float2 f = make_float2(c < 2 ? fa : fb, c < 2 ? fa : fb);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) acc[c * 32 + i] = fmaf(v[i], c < 2 ? fa : fb, acc[c * 32 + i]);
+                    for (int i = 0; i < 32; i += 2) {
+                        const float2 r = __ffma2_rn(make_float2(v[c & 1][i], v[c & 1][i + 1]), f,
+                                                    make_float2(acc[c * 32 + i], acc[c * 32 + i + 1]));
+                        acc[c * 32 + i] = r.x;
+                        acc[c * 32 + i + 1] = r.y;
+                    }
                 }
-                tc::fence_before();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&sh.tempty[buf]);
                 buf_phase ^= (uint32_t)buf;
                 buf ^= 1;
             }

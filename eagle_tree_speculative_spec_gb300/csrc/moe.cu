@@ -67,21 +67,34 @@ E3_DEV int route_row(const RouteParams &p, int row, bool live) {
             if (isfinite(z)) key[i] = order_key(z + 0.0f);
         }
     }
+    // this lane's largest logit left, and the lowest index that has it
+    uint32_t best = 0u;
+    int best_i = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        if (key[i] > best) {
+            best = key[i];
+            best_i = i;
+        }
     uint32_t place_key = 0u, high = 0u;
     int place_id = -1;
     uint32_t taken = 0u;   // this lane's values that are taken (PER <= 16)
     for (int j = 0; j < p.k; ++j) {
-        uint32_t best = 0u;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) best = max(best, (taken >> i) & 1u ? 0u : key[i]);
         const uint32_t top = __reduce_max_sync(0xffffffffu, best);
         if (top == 0u) break;   // uniform: no finite logit is left
-        uint32_t at = 0xffffffffu;
+        const uint32_t at = __reduce_min_sync(0xffffffffu, best == top ? (uint32_t)(best_i * 32 + lane) : 0xffffffffu);
+        if ((int)(at & 31u) == lane) {
+            taken |= 1u << best_i;
+            best = 0u;
 #pragma unroll
-        for (int i = PER - 1; i >= 0; --i)
-            if (key[i] == top && !((taken >> i) & 1u)) at = (uint32_t)(i * 32 + lane);
-        at = __reduce_min_sync(0xffffffffu, at);
-        if ((int)(at & 31u) == lane) taken |= 1u << (at >> 5);
+            for (int i = 0; i < PER; ++i) {
+                const uint32_t left = (taken >> i) & 1u ? 0u : key[i];
+                if (left > best) {
+                    best = left;
+                    best_i = i;
+                }
+            }
+        }
         if (j == 0) high = top;
         if (lane == j) {
             place_key = top;
@@ -137,20 +150,21 @@ E3_DEV int scan_experts(int v, int *warp_sums, int *sum) {
     return inc - v + (warp > 0 ? before : 0);
 }
 
-// Slots of the chunk's places.  masks: the chunk's rows per expert; base: each expert's next slot.
-E3_DEV void place_chunk(const RouteParams &p, int row0, const uint32_t *masks, const int *base) {
-    for (int i = threadIdx.x; i < CHUNK * p.k; i += ROUTE_THREADS) {
-        const int r = i / p.k, row = row0 + r;
-        if (row >= p.rows) continue;
-        const size_t at = (size_t)row * p.k + (i - r * p.k);
-        const int e = p.ids[at];
-        int slot = -1;
-        if (e >= 0) {
-            slot = base[e] + __popc(masks[e] & ((1u << r) - 1u));
-            p.sorted[slot] = row;
-        }
-        p.slots[at] = slot;
+// Place (tid / k, tid % k) of the chunk at row0: its expert, or -1.  A chunk has at most 32 * 16 places.
+E3_DEV int chunk_place(const RouteParams &p, int row0, int r) {
+    const int row = row0 + r;
+    return r < CHUNK && row < p.rows ? p.ids[(size_t)row0 * p.k + threadIdx.x] : -1;
+}
+// Its slot.  masks: the chunk's rows per expert; base: each expert's next slot.
+E3_DEV void place(const RouteParams &p, int row0, int r, int id, const uint32_t *masks, const int *base) {
+    const int row = row0 + r;
+    if (r >= CHUNK || row >= p.rows) return;
+    int slot = -1;
+    if (id >= 0) {
+        slot = base[id] + __popc(masks[id] & ((1u << r) - 1u));
+        p.sorted[slot] = row;
     }
+    p.slots[(size_t)row0 * p.k + threadIdx.x] = slot;
 }
 
 // Experts and weights of every row; with one block also the offsets and slots, otherwise the places
@@ -187,7 +201,8 @@ __global__ void __launch_bounds__(ROUTE_THREADS) moe_route_kernel(const RoutePar
     if (threadIdx.x < p.E) p.offsets[threadIdx.x] = start;
     if (threadIdx.x == 0) p.offsets[p.E] = total;
     __syncthreads();
-    place_chunk(p, 0, masks, base);
+    const int r = threadIdx.x / p.k;
+    place(p, 0, r, chunk_place(p, 0, r), masks, base);
     for (int s = total + threadIdx.x; s < p.rows * p.k; s += ROUTE_THREADS) p.sorted[s] = -1;
 }
 
@@ -196,16 +211,23 @@ __global__ void __launch_bounds__(ROUTE_THREADS) moe_place_kernel(const RoutePar
     __shared__ int base[MAX_E], before[ROUTE_THREADS], all[ROUTE_THREADS], warp_sums[32];
     pdl_wait();
     pdl_trigger();
-    // thread (g, e): blocks g, g + G, ... of expert e
+    const int r = threadIdx.x / p.k, first_row = blockIdx.x * p.chunks_per_block * CHUNK;
+    int id = chunk_place(p, first_row, r);   // in flight with the counts
+    // thread (g, e): blocks g, g + G, ... of expert e, 16 loads at a time
     const int width = p.E <= 128 ? 128 : p.E <= 256 ? 256 : 512, G = ROUTE_THREADS / width;
     const int e = threadIdx.x % width, g = threadIdx.x / width;
     int sum = 0, ahead = 0;
     if (e < p.E) {
-#pragma unroll 8
-        for (int b = g; b < (int)gridDim.x; b += G) {
-            const int v = __ldg(p.counts + (size_t)b * p.E + e);
-            sum += v;
-            ahead += b < (int)blockIdx.x ? v : 0;
+        for (int b0 = g; b0 < (int)gridDim.x; b0 += 16 * G) {
+            int v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                v[i] = b0 + i * G < (int)gridDim.x ? __ldg(p.counts + (size_t)(b0 + i * G) * p.E + e) : 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                sum += v[i];
+                ahead += b0 + i * G < (int)blockIdx.x ? v[i] : 0;
+            }
         }
     }
     all[threadIdx.x] = sum;
@@ -224,16 +246,13 @@ __global__ void __launch_bounds__(ROUTE_THREADS) moe_place_kernel(const RoutePar
         if (threadIdx.x == 0) p.offsets[p.E] = total;
     }
     for (int c = 0; c < p.chunks_per_block; ++c) {
-        const int row0 = (blockIdx.x * p.chunks_per_block + c) * CHUNK;
+        const int row0 = first_row + c * CHUNK;
+        if (c > 0) id = chunk_place(p, row0, r);
         if (threadIdx.x < MAX_E) masks[threadIdx.x] = 0u;
         __syncthreads();
-        for (int i = threadIdx.x; i < CHUNK * p.k; i += ROUTE_THREADS) {
-            const int r = i / p.k, row = row0 + r;
-            const int id = row < p.rows ? p.ids[(size_t)row * p.k + (i - r * p.k)] : -1;
-            if (id >= 0) atomicOr(&masks[id], 1u << r);
-        }
+        if (id >= 0) atomicOr(&masks[id], 1u << r);
         __syncthreads();
-        place_chunk(p, row0, masks, base);
+        place(p, row0, r, id, masks, base);
         __syncthreads();
         if (threadIdx.x < MAX_E) base[threadIdx.x] += __popc(masks[threadIdx.x]);
     }
@@ -294,20 +313,31 @@ __global__ void __launch_bounds__(COMBINE_THREADS) moe_combine_kernel(const Comb
     if (p.res) res = *reinterpret_cast<const T *>(p.res + (size_t)row * p.ld_res + col);
     const int32_t *slots = p.slots + (size_t)row * p.k;
     const float *weights = p.weights + (size_t)row * p.k;
-#pragma unroll 8
-    for (int j = 0; j < p.k; ++j) {
-        const int s = __ldg(slots + j);
-        if (s < 0) continue;
-        if (s >= p.n_slots) {
-            flag(p.dev_status, EAGLE3_DEV_BAD_COUNTS);
-            continue;
-        }
-        const float w = __ldg(weights + j);
-        const T raw = __ldg(reinterpret_cast<const T *>(p.y + (size_t)s * p.ld_y + col));
-        float v[VEC];
-        unpack<VEC>(raw, v);
+    for (int j0 = 0; j0 < p.k; j0 += 8) {   // the loads of 8 places together
+        int at[8];
+        float w[8];
+        T raw[8];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) acc[i] = fmaf(w, v[i], acc[i]);
+        for (int i = 0; i < 8; ++i) {
+            at[i] = j0 + i < p.k ? __ldg(slots + j0 + i) : -1;
+            w[i] = j0 + i < p.k ? __ldg(weights + j0 + i) : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (at[i] >= p.n_slots) {
+                flag(p.dev_status, EAGLE3_DEV_BAD_COUNTS);
+                at[i] = -1;
+            }
+            if (at[i] >= 0) raw[i] = __ldg(reinterpret_cast<const T *>(p.y + (size_t)at[i] * p.ld_y + col));
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (at[i] < 0) continue;
+            float v[VEC];
+            unpack<VEC>(raw[i], v);
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) acc[c] = fmaf(w[i], v[c], acc[c]);
+        }
     }
     if (p.res) {
         float v[VEC];
