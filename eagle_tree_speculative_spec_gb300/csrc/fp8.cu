@@ -8,7 +8,7 @@
 // two scales, to fp32 accumulators in registers while the next block's MMAs run.  (This also keeps
 // the long sum out of the tensor cores' accumulation.)
 //
-// Two kernels, both warp-specialised: warp 0 loads by TMA into a ring, lane 0 of warp 1 issues
+// Two kernels, both warp-specialised: warp 0 loads by TMA into a ring, a lane of warp 1 issues
 // tcgen05.mma (kind::f8f6f4, K = 32) and the other warps run the epilogue.
 //   wide     128 rows x 256 weight rows a tile, persistent.  Rows are the M side, so a thread owns one
 //            row and its scale is one number a k-block.
@@ -190,13 +190,17 @@ E3_DEV void store8(const Fp8Params &p, int row, int col, const float *v) {
 // ---- wide ---------------------------------------------------------------------------------------
 // Three warpgroups: loads and MMAs (warps 0 and 1; 2 and 3 idle), and two of the epilogue.  The block
 // is launched with 168 registers a thread (384 x 168 = 64512); the first group keeps 56 and the
-// epilogue takes 224 (128 x 56 + 256 x 224 = 64512): 128 accumulators and two loads in flight.
+// epilogue takes 224 (128 x 56 + 256 x 224 = 64512): 128 accumulators, two loads of 16, scales.
 constexpr int WIDE_BN = 256, WIDE_STAGES = 4, WIDE_EPI_WARPS = 8, WIDE_THREADS = 128 + 32 * WIDE_EPI_WARPS;
 constexpr int WIDE_EPI0 = 4;   // first epilogue warp
 constexpr int WIDE_A = BM * BK, WIDE_B = WIDE_BN * BK, WIDE_STAGE = WIDE_A + WIDE_B;
 constexpr int WIDE_BOX = 32 * 128;   // output staging: 32 rows x 128 bytes a warp
+// One barrier before and one after the MMAs of a k-block, both counted by its ring stage: full completes
+// when the loads have landed and the epilogue warps have read the TMEM buffer (that of two k-blocks
+// before), done when the MMAs have run, which both frees the stage and fills the buffer.  (With barriers
+// of their own for the buffers the issuing thread spent 640 cycles a k-block on waits and commits.)
 struct WideShared {
-    uint64_t full[WIDE_STAGES], empty[WIDE_STAGES], tfull[2], tempty[2], mma_done;
+    uint64_t full[WIDE_STAGES], done[WIDE_STAGES], mma_done;
     uint32_t tmem_base;
     int abort;
 };
@@ -226,12 +230,8 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < WIDE_STAGES; ++s) {
-            tc::mbar_init(&sh.full[s], 1);
-            tc::mbar_init(&sh.empty[s], 1);
-        }
-        for (int b = 0; b < 2; ++b) {
-            tc::mbar_init(&sh.tfull[b], 1);
-            tc::mbar_init(&sh.tempty[b], WIDE_EPI_WARPS);
+            tc::mbar_init(&sh.full[s], 1 + WIDE_EPI_WARPS);
+            tc::mbar_init(&sh.done[s], 1);
         }
         tc::mbar_init(&sh.mma_done, 1);
         sh.abort = 0;
@@ -253,14 +253,14 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
         registers_give<56>();
         if (warp == 0) {
             // ------------------------------------------------------------------ TMA producer
-            if (lane == 0) {
+            if (tc::elect_one()) {
                 int stage = 0;
                 uint32_t phase = 0, last_parity = 0, issued = 0;
                 bool ok = true;
                 for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
                     const int mb = u % p.tiles_m, nb = u / p.tiles_m;
                     for (int kb = 0; kb < p.kb_total; ++kb) {
-                        if (!tc::mbar_wait(&sh.empty[stage], phase ^ 1u, abort)) {
+                        if (!tc::mbar_wait(&sh.done[stage], phase ^ 1u, abort)) {
                             ok = false;
                             break;
                         }
@@ -294,31 +294,29 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
             __syncwarp();
         } else if (warp == 1) {
             // ------------------------------------------------------------------ MMA issuer
-            if (lane == 0) {
+            if (tc::elect_one()) {
                 constexpr uint32_t IDESC = tc::idesc_e4m3(BM, WIDE_BN);
+                const uint64_t desc0 = tc::desc_sw128(smem_u32(ring));
                 int stage = 0, buf = 0;
-                uint32_t phase = 0, buf_phase = 0;
+                uint32_t phase = 0;
                 bool ok = true;
                 for (int u = blockIdx.x; ok && u < units; u += gridDim.x)
                     for (int kb = 0; kb < p.kb_total; ++kb) {
-                        if (!tc::mbar_wait(&sh.tempty[buf], buf_phase ^ 1u, abort) ||
-                            !tc::mbar_wait(&sh.full[stage], phase, abort)) {
+                        if (!tc::mbar_wait(&sh.full[stage], phase, abort)) {
                             ok = false;
                             break;
                         }
                         tc::fence_after();
-                        const uint32_t a = smem_u32(ring + stage * WIDE_STAGE), b = a + WIDE_A;
+                        // (descriptors count 16 bytes)
+                        const uint64_t a = desc0 + (uint32_t)(stage * (WIDE_STAGE >> 4)), b = a + (WIDE_A >> 4);
 #pragma unroll
                         for (int k = 0; k < BK / 32; ++k)
-                            tc::mma_e4m3_ss(tmem + buf * WIDE_BN, tc::desc_sw128(a + k * 32), tc::desc_sw128(b + k * 32),
-                                            IDESC, k > 0 ? 1u : 0u);
-                        tc::mma_commit(&sh.empty[stage]);
-                        tc::mma_commit(&sh.tfull[buf]);
+                            tc::mma_e4m3_ss(tmem + buf * WIDE_BN, a + k * 2, b + k * 2, IDESC, k > 0 ? 1u : 0u);
+                        tc::mma_commit(&sh.done[stage]);
                         if (++stage == WIDE_STAGES) {
                             stage = 0;
                             phase ^= 1u;
                         }
-                        buf_phase ^= (uint32_t)buf;
                         buf ^= 1;
                     }
                 if (!ok) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
@@ -338,9 +336,13 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
         // this thread's two runs of 64 accumulator columns: neighbours, or gate and up of one run
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         const uint32_t run_a = lanes + (SWIGLU ? 64 * half : 128 * half), run_b = run_a + (SWIGLU ? 128 : 64);
-        int buf = 0;
-        uint32_t buf_phase = 0;
+        int stage = 0, buf = 0;
+        uint32_t phase = 0;
         bool ok = true;
+        if (lane == 0) {   // both buffers are free
+            tc::mbar_arrive(&sh.full[0]);
+            tc::mbar_arrive(&sh.full[1]);
+        }
         for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
             const int mb = u % p.tiles_m, nb = u / p.tiles_m;
             const int row = mb * BM + quarter * 32 + lane;
@@ -351,16 +353,41 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
             float acc[128];
 #pragma unroll
             for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
-            float sx = __ldg(xs), sa = __ldg(wa), sb = SWIGLU ? __ldg(wb) : sa;
-            for (int kb = 0; kb < p.kb_total; ++kb) {
-                const float fa = sx * sa, fb = SWIGLU ? sx * sb : fa;
-                if (kb + 1 < p.kb_total) {   // the next block's scales, while this one's MMAs run
-                    sx = __ldg(xs + (size_t)(kb + 1) * p.m);
-                    sa = __ldg(wa + kb + 1);
-                    if (SWIGLU) sb = __ldg(wb + kb + 1);
+            // scales, far enough ahead of their use for a loaded L2: the row's of 4 k-blocks at a time, the
+            // weights' of 32, one a lane
+            float sx[4], sx_next[4], sa = 0.0f, sb = 0.0f, sa_next = 0.0f, sb_next = 0.0f;
+            auto fetch_x = [&](int kb, float (&s)[4]) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[i] = kb + i < p.kb_total ? __ldg(xs + (size_t)(kb + i) * p.m) : 0.0f;
+            };
+            auto fetch_w = [&](int kb, float &s, float &s2) {
+                if (kb + lane < p.kb_total) {
+                    s = __ldg(wa + kb + lane);
+                    if (SWIGLU) s2 = __ldg(wb + kb + lane);
                 }
+            };
+            fetch_x(0, sx);
+            fetch_w(0, sa, sb);
+            for (int kb = 0; kb < p.kb_total; ++kb) {
+                if (kb % 4 == 0) {
+                    if (kb > 0) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) sx[i] = sx_next[i];
+                    }
+                    fetch_x(kb + 4, sx_next);
+                }
+                if (kb % 32 == 0) {
+                    if (kb > 0) {
+                        sa = sa_next;
+                        sb = sb_next;
+                    }
+                    fetch_w(kb + 32, sa_next, sb_next);
+                }
+                const float row_scale = kb & 2 ? (kb & 1 ? sx[3] : sx[2]) : (kb & 1 ? sx[1] : sx[0]);
+                const float fa = row_scale * __shfl_sync(0xffffffffu, sa, kb & 31);
+                const float fb = SWIGLU ? row_scale * __shfl_sync(0xffffffffu, sb, kb & 31) : fa;
                 int fine = 0;
-                if (lane == 0) fine = tc::mbar_wait(&sh.tfull[buf], buf_phase, abort) ? 1 : 0;
+                if (lane == 0) fine = tc::mbar_wait(&sh.done[stage], phase, abort) ? 1 : 0;
                 fine = __shfl_sync(0xffffffffu, fine, 0);
                 if (!fine) {
                     if (lane == 0) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
@@ -369,29 +396,32 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                 }
                 tc::fence_after();
                 const uint32_t t = tmem + (uint32_t)(buf * WIDE_BN);
-                // 32 columns a load, the next one in flight while the last is added
-                float v[2][32];
-                tc::tmem_ld32_start(t + run_a, v[0]);
+                // 16 columns a load, the next one in flight while the last is added (32 spilled)
+                float v[2][16];
+                tc::tmem_ld16_start(t + run_a, v[0]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < 8; ++c) {
                     tc::tmem_ld_wait(v[c & 1]);
-                    if (c < 3) {
-                        tc::tmem_ld32_start(t + (c < 1 ? run_a + 32 : run_b + (c - 1) * 32), v[(c + 1) & 1]);
-                    } else {   // the buffer is read: the MMAs may have it
+                    if (c < 7) {
+                        tc::tmem_ld16_start(t + (c < 3 ? run_a + (c + 1) * 16 : run_b + (c - 3) * 16), v[(c + 1) & 1]);
+                    } else {   // the buffer is read: it may take the k-block after the next
                         tc::fence_before();
                         __syncwarp();
-                        if (lane == 0) tc::mbar_arrive(&sh.tempty[buf]);
+                        if (lane == 0) tc::mbar_arrive(&sh.full[(stage + 2) % WIDE_STAGES]);
                     }
-                    const float2 f = make_float2(c < 2 ? fa : fb, c < 2 ? fa : fb);
+                    const float2 f = make_float2(c < 4 ? fa : fb, c < 4 ? fa : fb);
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
+                    for (int i = 0; i < 16; i += 2) {
                         const float2 r = __ffma2_rn(make_float2(v[c & 1][i], v[c & 1][i + 1]), f,
-                                                    make_float2(acc[c * 32 + i], acc[c * 32 + i + 1]));
-                        acc[c * 32 + i] = r.x;
-                        acc[c * 32 + i + 1] = r.y;
+                                                    make_float2(acc[c * 16 + i], acc[c * 16 + i + 1]));
+                        acc[c * 16 + i] = r.x;
+                        acc[c * 16 + i + 1] = r.y;
                     }
                 }
-                buf_phase ^= (uint32_t)buf;
+                if (++stage == WIDE_STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
                 buf ^= 1;
             }
             if (!ok) break;
@@ -571,7 +601,8 @@ __global__ void __launch_bounds__(NARROW_THREADS, NT <= 64 ? 2 : 1)
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
+        if (tc::elect_one()) {
+            const uint64_t desc0 = tc::desc_sw128(smem_u32(ring));
             const uint32_t idesc = tc::idesc_e4m3(BM, p.n16);
             int stage = 0, buf = 0;
             uint32_t phase = 0, buf_phase = 0;
@@ -583,11 +614,10 @@ __global__ void __launch_bounds__(NARROW_THREADS, NT <= 64 ? 2 : 1)
                     break;
                 }
                 tc::fence_after();
-                const uint32_t a = smem_u32(ring + stage * stage_bytes), b = a + NARROW_W;
+                const uint64_t a = desc0 + (uint32_t)(stage * stage_bytes >> 4), b = a + (NARROW_W >> 4);
 #pragma unroll
                 for (int k = 0; k < BK / 32; ++k)
-                    tc::mma_e4m3_ss(tmem + buf * NT, tc::desc_sw128(a + k * 32), tc::desc_sw128(b + k * 32), idesc,
-                                    k > 0 ? 1u : 0u);
+                    tc::mma_e4m3_ss(tmem + buf * NT, a + k * 2, b + k * 2, idesc, k > 0 ? 1u : 0u);
                 tc::mma_commit(&sh.empty[stage]);
                 tc::mma_commit(&sh.tfull[buf]);
                 if (++stage == stages) {

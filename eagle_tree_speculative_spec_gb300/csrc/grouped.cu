@@ -13,7 +13,7 @@
 //   warp 0      TMA producer: the weight tile (SwiGLU: 64 gate and 64 up rows), and the rows unless they
 //               are gathered, by at most three boxes (a box costs about 70 cycles whatever its size:
 //               boxes of 16 rows held a 3840-row product to 835 TFLOP/s)
-//   warp 1      TMEM owner; lane 0 issues tcgen05.mma (M = 128, N = rows of the tile, K = 16)
+//   warp 1      TMEM owner; one lane issues tcgen05.mma (M = 128, N = rows of the tile, K = 16)
 //   warps 2..5  epilogue: tcgen05.ld, SwiGLU, stores of two columns a lane.  TMEM lanes 0..63 hold gate
 //               columns and 64..127 their up columns: two warps that share columns swap them through
 //               shared memory, and each finishes half of the rows
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
 
     if (warp == 0) {
         // ------------------------------------------------------------------ TMA producer
-        if (lane == 0) {
+        if (tc::elect_one()) {
             int stage = 0;
             uint32_t phase = 0, last_parity = 0, issued = 0;   // parity of the last load per stage
             bool ok = true;
@@ -283,7 +283,8 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
+        if (tc::elect_one()) {
+            const uint64_t desc0 = tc::desc_sw128(smem_u32(ring));
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true;
@@ -303,11 +304,11 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
                     }
                     if (GATHER) tc::fence_proxy_async_smem();   // the copies were made outside the async proxy
                     tc::fence_after();
-                    const uint32_t a_addr = smem_u32(ring + stage * stage_bytes), b_addr = a_addr + W_BYTES;
+                    // (descriptors count 16 bytes)
+                    const uint64_t a = desc0 + (uint32_t)(stage * stage_bytes >> 4), b = a + (W_BYTES >> 4);
 #pragma unroll
                     for (int k = 0; k < BK / 16; ++k)
-                        tc::mma_bf16_ss(d, tc::desc_sw128(a_addr + k * 32), tc::desc_sw128(b_addr + k * 32), idesc,
-                                        (kb > 0 || k > 0) ? 1u : 0u);
+                        tc::mma_bf16_ss(d, a + k * 2, b + k * 2, idesc, (kb > 0 || k > 0) ? 1u : 0u);
                     tc::mma_commit(&sh.empty[stage]);
                     if (++stage == stages) {
                         stage = 0;

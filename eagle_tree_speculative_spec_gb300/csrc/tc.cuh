@@ -99,6 +99,16 @@ E3_DEV void prefetch_tmap(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
+// True for one lane of the (converged) warp, the same one each time.  A loop of single-thread
+// instructions runs inside `if (elect_one())`: the compiler then keeps descriptors and barrier addresses
+// in uniform registers.  (Inside `if (lane == 0)` a group of one barrier wait, four tcgen05.mma and a
+// commit takes about 470 cycles to issue, here 271; the four MMAs run for 512 at N = 256.)
+E3_DEV bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(p));
+    return p != 0;
+}
+
 // ---- tcgen05 ---------------------------------------------------------------------------------------
 // Shared-memory matrix descriptor for a K-major tile written by TMA with 128-byte swizzle: rows of
 // 64 bf16 (128 B), 8-row groups 1024 B apart (stride byte offset), version 1, layout SWIZZLE_128B.
@@ -197,26 +207,21 @@ E3_DEV void tmem_ld32(uint32_t taddr, float (&v)[32]) {
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// The same load without the wait, and the wait for all loads of the thread so far (it names the
-// registers of one load, so that no use of them is scheduled before it).
-E3_DEV void tmem_ld32_start(uint32_t taddr, float (&v)[32]) {
+// 16 columns without the wait, and the wait for all loads of the thread so far (it names the registers
+// of one load, so that no use of them is scheduled before it).
+E3_DEV void tmem_ld16_start(uint32_t taddr, float (&v)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
         : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
-          "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
-          "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
-          "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+          "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
         : "r"(taddr)
         : "memory");
 }
-E3_DEV void tmem_ld_wait(float (&v)[32]) {
+E3_DEV void tmem_ld_wait(float (&v)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;\n"
                  : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
                    "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]),
-                   "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]),
-                   "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]),
-                   "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+                   "+f"(v[15])
                  :
                  : "memory");
 }
