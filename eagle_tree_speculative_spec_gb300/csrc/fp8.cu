@@ -190,11 +190,16 @@ E3_DEV void store8(const Fp8Params &p, int row, int col, const float *v) {
 // ---- wide ---------------------------------------------------------------------------------------
 // Three warpgroups: loads and MMAs (warps 0 and 1; 2 and 3 idle), and two of the epilogue.  The block
 // is launched with 168 registers a thread (384 x 168 = 64512); the first group keeps 56 and the
-// epilogue takes 224 (128 x 56 + 256 x 224 = 64512): 128 accumulators, two loads of 16, scales.
+// epilogue takes 224 (128 x 56 + 256 x 224 = 64512): 128 accumulators, two loads of 16, scales.  The
+// epilogue is short of issue slots: the instructions around the 128 additions of a k-block (waits that
+// poll, addresses made anew) weigh as much as they do, so barriers go by precomputed shared-memory
+// addresses and a poll is a handful of instructions: 3840 x 2 * 14336 x 4096 412 -> 350 us.  (Four
+// groups of 64 accumulators and 104 registers: 358 us.)
 constexpr int WIDE_BN = 256, WIDE_STAGES = 4, WIDE_EPI_WARPS = 8, WIDE_THREADS = 128 + 32 * WIDE_EPI_WARPS;
 constexpr int WIDE_EPI0 = 4;   // first epilogue warp
+constexpr int WIDE_RUN = 512 / WIDE_EPI_WARPS;   // accumulator columns of a thread: two runs of this many
 constexpr int WIDE_A = BM * BK, WIDE_B = WIDE_BN * BK, WIDE_STAGE = WIDE_A + WIDE_B;
-constexpr int WIDE_BOX = 32 * 128;   // output staging: 32 rows x 128 bytes a warp
+constexpr int WIDE_BOX = 32 * 64;   // output staging: 32 rows x 64 bytes a warp
 // One barrier before and one after the MMAs of a k-block, both counted by its ring stage: full completes
 // when the loads have landed and the epilogue warps have read the TMEM buffer (that of two k-blocks
 // before), done when the MMAs have run, which both frees the stage and fills the buffer.  (With barriers
@@ -225,7 +230,6 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
     uint8_t *ring = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *boxes = ring + WIDE_STAGES * WIDE_STAGE;
     WideShared &sh = *reinterpret_cast<WideShared *>(boxes + WIDE_EPI_WARPS * WIDE_BOX);
-    volatile int *abort = &sh.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -248,6 +252,8 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
     pdl_wait();
     pdl_trigger();
     const int units = p.tiles_m * p.tiles_n;
+    const uint32_t ring0 = smem_u32(ring), full0 = smem_u32(sh.full), done0 = smem_u32(sh.done);
+    const uint32_t abort0 = smem_u32(&sh.abort);
 
     if (warp < WIDE_EPI0) {
         registers_give<56>();
@@ -260,18 +266,18 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                 for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
                     const int mb = u % p.tiles_m, nb = u / p.tiles_m;
                     for (int kb = 0; kb < p.kb_total; ++kb) {
-                        if (!tc::mbar_wait(&sh.done[stage], phase ^ 1u, abort)) {
+                        if (!tc::mbar_wait(done0 + stage * 8, phase ^ 1u, abort0)) {
                             ok = false;
                             break;
                         }
-                        uint8_t *sx = ring + stage * WIDE_STAGE, *sw = sx + WIDE_A;
-                        tc::mbar_expect_tx(&sh.full[stage], WIDE_STAGE);
-                        tc::tma_load_2d(sx, &tm_x, kb * BK, mb * BM, &sh.full[stage]);
+                        const uint32_t full = full0 + stage * 8, sx = ring0 + stage * WIDE_STAGE, sw = sx + WIDE_A;
+                        tc::mbar_expect_tx(full, WIDE_STAGE);
+                        tc::tma_load_2d(sx, &tm_x, kb * BK, mb * BM, full);
                         if (SWIGLU) {
-                            tc::tma_load_2d(sw, &tm_w, kb * BK, nb * (WIDE_BN / 2), &sh.full[stage]);
-                            tc::tma_load_2d(sw + WIDE_B / 2, &tm_w2, kb * BK, nb * (WIDE_BN / 2), &sh.full[stage]);
+                            tc::tma_load_2d(sw, &tm_w, kb * BK, nb * (WIDE_BN / 2), full);
+                            tc::tma_load_2d(sw + WIDE_B / 2, &tm_w2, kb * BK, nb * (WIDE_BN / 2), full);
                         } else {
-                            tc::tma_load_2d(sw, &tm_w, kb * BK, nb * WIDE_BN, &sh.full[stage]);
+                            tc::tma_load_2d(sw, &tm_w, kb * BK, nb * WIDE_BN, full);
                         }
                         issued |= 1u << stage;
                         last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
@@ -283,26 +289,21 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                 }
                 if (!ok) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
                 // no TMA write may still be in flight when the CTA exits (bounded waits)
-                for (int st = 0; st < WIDE_STAGES; ++st) {
-                    if (!((issued >> st) & 1u)) continue;
-                    const uint32_t par = (last_parity >> st) & 1u;
-                    const long long t0 = clock64();
-                    while (!tc::mbar_try(&sh.full[st], par) && clock64() - t0 < WAIT_LIMIT_CYCLES) {
-                    }
-                }
+                for (int st = 0; st < WIDE_STAGES; ++st)
+                    if ((issued >> st) & 1u) tc::mbar_drain(full0 + st * 8, (last_parity >> st) & 1u);
             }
             __syncwarp();
         } else if (warp == 1) {
             // ------------------------------------------------------------------ MMA issuer
             if (tc::elect_one()) {
                 constexpr uint32_t IDESC = tc::idesc_e4m3(BM, WIDE_BN);
-                const uint64_t desc0 = tc::desc_sw128(smem_u32(ring));
+                const uint64_t desc0 = tc::desc_sw128(ring0);
                 int stage = 0, buf = 0;
                 uint32_t phase = 0;
                 bool ok = true;
                 for (int u = blockIdx.x; ok && u < units; u += gridDim.x)
                     for (int kb = 0; kb < p.kb_total; ++kb) {
-                        if (!tc::mbar_wait(&sh.full[stage], phase, abort)) {
+                        if (!tc::mbar_wait(full0 + stage * 8, phase, abort0)) {
                             ok = false;
                             break;
                         }
@@ -312,7 +313,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
 #pragma unroll
                         for (int k = 0; k < BK / 32; ++k)
                             tc::mma_e4m3_ss(tmem + buf * WIDE_BN, a + k * 2, b + k * 2, IDESC, k > 0 ? 1u : 0u);
-                        tc::mma_commit(&sh.done[stage]);
+                        tc::mma_commit(done0 + stage * 8);
                         if (++stage == WIDE_STAGES) {
                             stage = 0;
                             phase ^= 1u;
@@ -321,21 +322,20 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                     }
                 if (!ok) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
                 // every MMA this thread issued must retire before TMEM is freed (bounded wait)
-                tc::mma_commit(&sh.mma_done);
-                const long long t0 = clock64();
-                while (!tc::mbar_try(&sh.mma_done, 0) && clock64() - t0 < WAIT_LIMIT_CYCLES) {
-                }
+                tc::mma_commit(smem_u32(&sh.mma_done));
+                tc::mbar_drain(smem_u32(&sh.mma_done), 0);
             }
             __syncwarp();
         }
     } else {
         registers_take<224>();
         // ------------------------------------------------------------------ epilogue (warps 4..11)
-        const int quarter = warp & 3, half = (warp - WIDE_EPI0) >> 2;
+        const int quarter = warp & 3, part = (warp - WIDE_EPI0) >> 2;
         uint8_t *box = boxes + (warp - WIDE_EPI0) * WIDE_BOX;
-        // this thread's two runs of 64 accumulator columns: neighbours, or gate and up of one run
+        // this thread's two runs of accumulator columns: neighbours, or gate and up of one run
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        const uint32_t run_a = lanes + (SWIGLU ? 64 * half : 128 * half), run_b = run_a + (SWIGLU ? 128 : 64);
+        const uint32_t run_a = lanes + (SWIGLU ? WIDE_RUN : 2 * WIDE_RUN) * part, run_b = run_a + (SWIGLU ? 128 : WIDE_RUN);
+        const int kb_total = p.kb_total;
         int stage = 0, buf = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -347,69 +347,50 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
             const int mb = u % p.tiles_m, nb = u / p.tiles_m;
             const int row = mb * BM + quarter * 32 + lane;
             const float *xs = p.x_scale + (row < p.m ? row : 0);
-            const int block = min(SWIGLU ? nb : 2 * nb + half, p.n_blocks - 1);
+            const int block = min(SWIGLU ? nb : 2 * nb + part * 2 * WIDE_RUN / BK, p.n_blocks - 1);
             const float *wa = p.w_scale + (size_t)block * p.kb_total;
             const float *wb = SWIGLU ? p.w2_scale + (size_t)block * p.kb_total : wa;
-            float acc[128];
+            float acc[2 * WIDE_RUN];
 #pragma unroll
-            for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
-            // scales, far enough ahead of their use for a loaded L2: the row's of 4 k-blocks at a time, the
-            // weights' of 32, one a lane
-            float sx[4], sx_next[4], sa = 0.0f, sb = 0.0f, sa_next = 0.0f, sb_next = 0.0f;
-            auto fetch_x = [&](int kb, float (&s)[4]) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) s[i] = kb + i < p.kb_total ? __ldg(xs + (size_t)(kb + i) * p.m) : 0.0f;
-            };
-            auto fetch_w = [&](int kb, float &s, float &s2) {
-                if (kb + lane < p.kb_total) {
-                    s = __ldg(wa + kb + lane);
-                    if (SWIGLU) s2 = __ldg(wb + kb + lane);
+            for (int i = 0; i < 2 * WIDE_RUN; ++i) acc[i] = 0.0f;
+            // scales, far enough ahead of their use for a loaded L2: the row's two k-blocks ahead, the
+            // weights' of 32 k-blocks, one a lane
+            const float *at = xs;
+            float sx = __ldg(at), sx1 = kb_total > 1 ? __ldg(at + p.m) : 0.0f, sa = 0.0f, sb = 0.0f;
+            at += 2 * (size_t)p.m;
+#pragma unroll 1
+            for (int kb = 0; kb < kb_total; ++kb) {
+                const float sx2 = kb + 2 < kb_total ? __ldg(at) : 0.0f;
+                at += p.m;
+                if ((kb & 31) == 0) {
+                    const int i = min(kb + lane, kb_total - 1);
+                    sa = __ldg(wa + i);
+                    if (SWIGLU) sb = __ldg(wb + i);
                 }
-            };
-            fetch_x(0, sx);
-            fetch_w(0, sa, sb);
-            for (int kb = 0; kb < p.kb_total; ++kb) {
-                if (kb % 4 == 0) {
-                    if (kb > 0) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) sx[i] = sx_next[i];
-                    }
-                    fetch_x(kb + 4, sx_next);
-                }
-                if (kb % 32 == 0) {
-                    if (kb > 0) {
-                        sa = sa_next;
-                        sb = sb_next;
-                    }
-                    fetch_w(kb + 32, sa_next, sb_next);
-                }
-                const float row_scale = kb & 2 ? (kb & 1 ? sx[3] : sx[2]) : (kb & 1 ? sx[1] : sx[0]);
-                const float fa = row_scale * __shfl_sync(0xffffffffu, sa, kb & 31);
-                const float fb = SWIGLU ? row_scale * __shfl_sync(0xffffffffu, sb, kb & 31) : fa;
-                int fine = 0;
-                if (lane == 0) fine = tc::mbar_wait(&sh.done[stage], phase, abort) ? 1 : 0;
-                fine = __shfl_sync(0xffffffffu, fine, 0);
-                if (!fine) {
-                    if (lane == 0) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
+                const float fa = sx * __shfl_sync(0xffffffffu, sa, kb & 31);
+                const float fb = SWIGLU ? sx * __shfl_sync(0xffffffffu, sb, kb & 31) : fa;
+                if (!tc::mbar_wait_warp(done0 + stage * 8, phase, abort0)) {
                     ok = false;
                     break;
                 }
                 tc::fence_after();
                 const uint32_t t = tmem + (uint32_t)(buf * WIDE_BN);
-                // 16 columns a load, the next one in flight while the last is added (32 spilled)
+                // 16 columns a load, the next one in flight while the last is added
                 float v[2][16];
                 tc::tmem_ld16_start(t + run_a, v[0]);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
+                for (int c = 0; c < WIDE_RUN / 8; ++c) {
                     tc::tmem_ld_wait(v[c & 1]);
-                    if (c < 7) {
-                        tc::tmem_ld16_start(t + (c < 3 ? run_a + (c + 1) * 16 : run_b + (c - 3) * 16), v[(c + 1) & 1]);
+                    if (c + 1 < WIDE_RUN / 8) {
+                        tc::tmem_ld16_start(t + (c + 1 < WIDE_RUN / 16 ? run_a + (c + 1) * 16
+                                                                       : run_b + (c + 1 - WIDE_RUN / 16) * 16),
+                                            v[(c + 1) & 1]);
                     } else {   // the buffer is read: it may take the k-block after the next
                         tc::fence_before();
                         __syncwarp();
-                        if (lane == 0) tc::mbar_arrive(&sh.full[(stage + 2) % WIDE_STAGES]);
+                        if (lane == 0) tc::mbar_arrive(full0 + ((stage + 2) % WIDE_STAGES) * 8);
                     }
-                    const float2 f = make_float2(c < 4 ? fa : fb, c < 4 ? fa : fb);
+                    const float2 f = make_float2(c < WIDE_RUN / 16 ? fa : fb, c < WIDE_RUN / 16 ? fa : fb);
 #pragma unroll
                     for (int i = 0; i < 16; i += 2) {
                         const float2 r = __ffma2_rn(make_float2(v[c & 1][i], v[c & 1][i + 1]), f,
@@ -418,47 +399,52 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                         acc[c * 16 + i + 1] = r.y;
                     }
                 }
+                sx = sx1;
+                sx1 = sx2;
                 if (++stage == WIDE_STAGES) {
                     stage = 0;
                     phase ^= 1u;
                 }
                 buf ^= 1;
             }
-            if (!ok) break;
+            if (!ok) {
+                if (lane == 0) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
+                break;
+            }
             if (SWIGLU) {
 #pragma unroll
-                for (int i = 0; i < 64; ++i) acc[i] = silu(acc[i]) * acc[64 + i];
+                for (int i = 0; i < WIDE_RUN; ++i) acc[i] = silu(acc[i]) * acc[WIDE_RUN + i];
             }
-            const int col0 = SWIGLU ? nb * (WIDE_BN / 2) + 64 * half : nb * WIDE_BN + 128 * half;
-            const int cols = SWIGLU ? 64 : 128, y = mb * BM + quarter * 32;
+            const int cols = SWIGLU ? WIDE_RUN : 2 * WIDE_RUN, y = mb * BM + quarter * 32;
+            const int col0 = nb * (SWIGLU ? WIDE_BN / 2 : WIDE_BN) + cols * part;
             const bool f32 = p.epi == EAGLE3_EPI_F32;
             if (p.epi == EAGLE3_EPI_BF16_RESIDUAL && row < p.m) {
 #pragma unroll
-                for (int i = 0; i < 128; i += 8)
+                for (int i = 0; i < 2 * WIDE_RUN; i += 8)
                     if (col0 + i < p.n) load_res8(p, row, col0 + i, acc + i);
             }
             if (p.tma_out) {
-                // pieces of 128 bytes: 64 bf16 or 32 fp32 columns of the warp's 32 rows
+                // pieces of 64 bytes: 32 bf16 or 16 fp32 columns of the warp's 32 rows, in the 64-byte swizzle
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if (c * (f32 ? 32 : 64) >= cols) break;
+                for (int c = 0; c < WIDE_RUN / 8; ++c) {
+                    if (c * (f32 ? 16 : 32) >= cols) break;
                     if (lane == 0) tc::bulk_wait_read<0>();   // the box's last store has read it
                     __syncwarp();
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
+                    for (int j = 0; j < 4; ++j) {
                         uint4 o;
                         if (f32) {
-                            const float *v = acc + c * 32 + 4 * j;
+                            const float *v = acc + c * 16 + 4 * j;
                             o = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
                                            __float_as_uint(v[3]));
                         } else {
-                            o = pack8(acc + (c & 1) * 64 + 8 * j);
+                            o = pack8(acc + c % (WIDE_RUN / 16) * 32 + 8 * j);
                         }
-                        *reinterpret_cast<uint4 *>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) = o;
+                        *reinterpret_cast<uint4 *>(box + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = o;
                     }
                     tc::fence_proxy_async_smem();
                     __syncwarp();
-                    const int x = col0 + c * (f32 ? 32 : 64);
+                    const int x = col0 + c * (f32 ? 16 : 32);
                     if (lane == 0 && x < p.n && y < p.m) {
                         tc::tma_store_2d(&tm_out, x, y, box);
                         tc::bulk_commit();
@@ -466,7 +452,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                 }
             } else if (row < p.m) {
 #pragma unroll
-                for (int i = 0; i < 128; i += 8)
+                for (int i = 0; i < 2 * WIDE_RUN; i += 8)
                     if (i < cols && col0 + i < p.n) store8(p, row, col0 + i, acc + i);
             }
         }
@@ -663,11 +649,8 @@ __global__ void __launch_bounds__(NARROW_THREADS, NT <= 64 ? 2 : 1)
             for (int i = 0; i < NT / 32; ++i) strip[lane + 32 * i] = sx[i];
             const float fw = sw;
             if (kb + 1 < kb1) fetch(kb + 1);
-            int fine = 0;
-            if (lane == 0) fine = tc::mbar_wait(&sh.tfull[buf], buf_phase, abort) ? 1 : 0;
-            fine = __shfl_sync(0xffffffffu, fine, 0);   // (also orders the strip's writes)
-            __syncwarp();
-            if (!fine) {
+            // (the vote also orders the strip's writes)
+            if (!tc::mbar_wait_warp(smem_u32(&sh.tfull[buf]), buf_phase, smem_u32(&sh.abort))) {
                 if (lane == 0) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
                 break;
             }
@@ -780,13 +763,13 @@ eagle3_status_t validate(const eagle3_linear_fp8_args_t *a) {
     return EAGLE3_OK;
 }
 
-// 32-row boxes of 128 bytes of the output, for TMA stores; false where its address or pitch rules them out
+// 32-row boxes of 64 bytes of the output, for TMA stores; false where its address or pitch rules them out
 bool out_map(CUtensorMap *m, const eagle3_linear_fp8_args_t *a, int64_t ld) {
     const bool f32 = a->epilogue == EAGLE3_EPI_F32;
     const int es = f32 ? 4 : 2;
     if (((uintptr_t)a->out & 15) || (ld * es) % 16) return false;
     return tmap_rows(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, es, a->out, a->m, a->n,
-                     ld, 32);
+                     ld, 32, 0, 0, 64);
 }
 
 template <int NT, bool SWIGLU>

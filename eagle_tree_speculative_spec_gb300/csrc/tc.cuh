@@ -44,7 +44,74 @@ E3_DEV bool mbar_wait(uint64_t *bar, uint32_t parity, volatile int *abort, long 
     }
 }
 
+// The same by shared-memory address (computed once) and by whole warps, for loops that are short of issue
+// slots and registers: a poll is a handful of instructions, every lane gets the same answer, and the bound
+// is a number of polls (at least 20 cycles each: MAX_POLLS are seconds, as WAIT_LIMIT_CYCLES).
+constexpr uint32_t MAX_POLLS = 1u << 27;
+E3_DEV bool mbar_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+E3_DEV bool mbar_wait_warp(uint32_t bar, uint32_t parity, uint32_t abort_addr) {
+    for (uint32_t n = 1; !__all_sync(0xffffffffu, mbar_try(bar, parity)); ++n) {
+        if ((n & 1023u) == 0u) {
+            uint32_t gone;
+            asm volatile("ld.volatile.shared.u32 %0, [%1];\n" : "=r"(gone) : "r"(abort_addr) : "memory");
+            if (__any_sync(0xffffffffu, gone != 0u || n >= MAX_POLLS)) {
+                asm volatile("st.volatile.shared.u32 [%0], %1;\n" ::"r"(abort_addr), "r"(1) : "memory");
+                return false;
+            }
+        }
+    }
+    return true;
+}
+// the same by one thread
+E3_DEV bool mbar_wait(uint32_t bar, uint32_t parity, uint32_t abort_addr) {
+    for (uint32_t n = 1; !mbar_try(bar, parity); ++n) {
+        if ((n & 1023u) == 0u) {
+            uint32_t gone;
+            asm volatile("ld.volatile.shared.u32 %0, [%1];\n" : "=r"(gone) : "r"(abort_addr) : "memory");
+            if (gone != 0u || n >= MAX_POLLS) {
+                asm volatile("st.volatile.shared.u32 [%0], %1;\n" ::"r"(abort_addr), "r"(1) : "memory");
+                return false;
+            }
+        }
+    }
+    return true;
+}
+// after the last use: wait for a phase without regard to the abort flag
+E3_DEV void mbar_drain(uint32_t bar, uint32_t parity) {
+    for (uint32_t n = 0; n < MAX_POLLS && !mbar_try(bar, parity); ++n) {
+    }
+}
+E3_DEV void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
+}
+E3_DEV void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(bytes) : "memory");
+}
+
 // ---- TMA -----------------------------------------------------------------------------------------
+// (by shared-memory address)
+E3_DEV void tma_load_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+E3_DEV void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
 E3_DEV void tma_load_3d(void *smem_dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(
@@ -171,6 +238,9 @@ E3_DEV void mma_e4m3_ss(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_
 E3_DEV void mma_commit(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(smem_u32(bar))
                  : "memory");
+}
+E3_DEV void mma_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
 }
 E3_DEV void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
 E3_DEV void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
