@@ -77,28 +77,29 @@ __device__ __noinline__ uint2 codes_exact(uint4 raw, float s) {
     return make_uint2(q[0], q[1]);
 }
 
-// e4m3(x / s) for 8 values.  x times (1 / s) (1 -+ 2^-21) encloses the correctly rounded quotient (1 / s
-// and the two products are off by 2^-24 each), and the conversion is monotone: where both ends have the
-// same code it is the quotient's; otherwise (a border between two codes in between: about one value in
-// 2^17) the lane divides.  Divisions for every value made the kernel issue-bound: 42 us for 3840 x 14336
-// against 25 us of bytes.
+// e4m3(x / s) for 8 values.  With y = 1 / s rounded to nearest, q0 = x y and q = q0 + (x - q0 s) y (each
+// operation rounded once) is the correctly rounded quotient: Markstein's correction step ("Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990).  His theorem wants q0 within a step
+// of the quotient, which x y need not be, but s is a bf16 number over 448 and x a bf16 number, so that
+// there are 128 x 128 pairs of significands: all of them were checked, and powers of two change nothing as
+// long as nothing under- or overflows (s >= 2^-90, and x / s at most 448).  -0 keeps its sign.  IEEE
+// divisions for every value made the kernel issue-bound: 42 us for 3840 x 14336 against 25 us of bytes.
 E3_DEV uint2 codes(uint4 raw, float s) {
-    const float inv = __fdiv_rn(1.0f, s);
-    const float2 lo = make_float2(inv * (1.0f - 0x1p-21f), inv * (1.0f - 0x1p-21f));
-    const float2 hi = make_float2(inv * (1.0f + 0x1p-21f), inv * (1.0f + 0x1p-21f));
+    if (!(s >= 0x1p-90f)) return codes_exact(raw, s);   // or NaN
+    const float y = __fdiv_rn(1.0f, s);
+    const float2 y2 = make_float2(y, y), s2 = make_float2(-s, -s);
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-    uint32_t a[4], b[4];
+    uint32_t c[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 x = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
-        a[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(__fmul2_rn(x, lo), __NV_SATFINITE, __NV_E4M3);
-        b[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(__fmul2_rn(x, hi), __NV_SATFINITE, __NV_E4M3);
+        const float2 q0 = __fmul2_rn(x, y2);
+        const float2 q = __ffma2_rn(__ffma2_rn(q0, s2, x), y2, q0);
+        c[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
     }
-    const uint2 qa = make_uint2(a[0] | (a[1] << 16), a[2] | (a[3] << 16));
-    const uint2 qb = make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
-    // (below 2^-120 the reciprocal may overflow; a NaN scale is not above it either)
-    if (qa.x != qb.x || qa.y != qb.y || !(s >= 0x1p-120f)) return codes_exact(raw, s);
-    return qa;
+    // (the signs of 4 values: the high bytes of two words)
+    return make_uint2(c[0] | (c[1] << 16) | (__byte_perm(w[0], w[1], 0x7531) & 0x80808080u),
+                      c[2] | (c[3] << 16) | (__byte_perm(w[2], w[3], 0x7531) & 0x80808080u));
 }
 
 // A half warp holds a block of 128 columns of one row, 8 values a lane; a warp takes two neighbouring
@@ -470,14 +471,15 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
 }
 
 // ---- narrow -------------------------------------------------------------------------------------
-constexpr int NARROW_THREADS = 192, NARROW_MAX = 128, NARROW_STAGES = 8, NARROW_TMEM = 256, NARROW_CLUSTER = 8;
+constexpr int NARROW_EPI_WARPS = 8, NARROW_THREADS = 64 + 32 * NARROW_EPI_WARPS, NARROW_MAX = 128;
+constexpr int NARROW_STAGES = 8, NARROW_TMEM = 256, NARROW_CLUSTER = 8;
 constexpr int NARROW_RING = 106 * 1024;   // two CTAs a SM
 constexpr int NARROW_W = BM * BK;
 struct NarrowShared {
     uint64_t full[NARROW_STAGES], empty[NARROW_STAGES], tfull[8], tempty[8], mma_done;
     uint32_t tmem_base;
     int abort;
-    float scales[4][2][NARROW_MAX];   // per epilogue warp: the rows' scales of a k-block, double-buffered
+    float scales[NARROW_EPI_WARPS][2][NARROW_MAX / 2];   // per epilogue warp: its rows' scales, double-buffered
 };
 constexpr int NARROW_SMEM = 1024 + NARROW_RING + (int)sizeof(NarrowShared);
 static_assert(2 * (NARROW_SMEM + 1024) <= 228 * 1024, "two CTAs a SM");
@@ -498,10 +500,10 @@ E3_DEV float cluster_ld(uint32_t addr) {
     return v;
 }
 
-// NT: row capacity of a tile (TMEM buffers of NT columns, NT accumulators a thread).
+// NT: row capacity of a tile (TMEM buffers of NT columns, NT / 2 accumulators a thread).
 // Grid: (cluster ranks = k ranges, weight tiles, row tiles).
 template <int NT, bool SWIGLU>
-__global__ void __launch_bounds__(NARROW_THREADS, NT <= 64 ? 2 : 1)
+__global__ void __launch_bounds__(NARROW_THREADS, 2)
     fp8_narrow_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                       const __grid_constant__ CUtensorMap tm_w2, const Fp8Params p) {
     constexpr int BUFS = NARROW_TMEM / NT;
@@ -522,7 +524,7 @@ __global__ void __launch_bounds__(NARROW_THREADS, NT <= 64 ? 2 : 1)
         }
         for (int b = 0; b < BUFS; ++b) {
             tc::mbar_init(&sh.tfull[b], 1);
-            tc::mbar_init(&sh.tempty[b], 4);
+            tc::mbar_init(&sh.tempty[b], NARROW_EPI_WARPS);
         }
         tc::mbar_init(&sh.mma_done, 1);
         sh.abort = 0;
@@ -536,6 +538,12 @@ __global__ void __launch_bounds__(NARROW_THREADS, NT <= 64 ? 2 : 1)
     __syncthreads();
     tc::fence_after();
     const uint32_t tmem = sh.tmem_base;
+    // The weights' first k-blocks into L2 while the previous kernel ends (L2 is coherent: should that kernel
+    // write them, the loads below still see what it wrote)
+    if (warp == 0 && lane < 8 && kb0 + lane < kb1) {
+        tc::tma_prefetch_2d(&tm_w, (kb0 + lane) * BK, SWIGLU ? mt * 64 : mt * BM);
+        if (SWIGLU) tc::tma_prefetch_2d(&tm_w2, (kb0 + lane) * BK, mt * 64);
+    }
     pdl_wait();
     pdl_trigger();
 
@@ -623,20 +631,23 @@ __global__ void __launch_bounds__(NARROW_THREADS, NT <= 64 ? 2 : 1)
         }
         __syncwarp();
     } else {
-        // ------------------------------------------------------------------ epilogue (warps 2..5)
-        const int quarter = warp & 3;
-        const uint32_t t_col = tmem + ((uint32_t)(quarter * 32) << 16);
+        // ------------------------------------------------------------------ epilogue (warps 2..9)
+        constexpr int HALF = NT / 2;   // rows of a warp: two warps share a quarter of the TMEM lanes
+        const int quarter = warp & 3, r0 = (warp - 2) / 4 * HALF;
+        const uint32_t t_col = tmem + ((uint32_t)(quarter * 32) << 16) + r0;
         const int block = SWIGLU ? mt / 2 : mt;
         const float *ws = (SWIGLU && lane >= 16 ? p.w2_scale : p.w_scale) + (size_t)block * p.kb_total;
-        float acc[NT];
+        const uint32_t tfull0 = smem_u32(sh.tfull), tempty0 = smem_u32(sh.tempty), abort0 = smem_u32(&sh.abort);
+        float acc[HALF];
 #pragma unroll
-        for (int i = 0; i < NT; ++i) acc[i] = 0.0f;
-        float sx[NT / 32], sw = 0.0f;
+        for (int i = 0; i < HALF; ++i) acc[i] = 0.0f;
+        constexpr int PER = (HALF + 31) / 32;
+        float sx[PER], sw = 0.0f;
         auto fetch = [&](int kb) {   // the k-block's scales: this lane's rows, and its weight row's
 #pragma unroll
-            for (int i = 0; i < NT / 32; ++i) {
+            for (int i = 0; i < PER; ++i) {
                 const int r = lane + 32 * i;
-                sx[i] = r < rows ? __ldg(p.x_scale + (size_t)kb * p.m + row0 + r) : 0.0f;
+                sx[i] = r < HALF && r0 + r < rows ? __ldg(p.x_scale + (size_t)kb * p.m + row0 + r0 + r) : 0.0f;
             }
             sw = __ldg(ws + kb);
         };
@@ -646,22 +657,25 @@ __global__ void __launch_bounds__(NARROW_THREADS, NT <= 64 ? 2 : 1)
         for (int kb = kb0; kb < kb1; ++kb) {
             float *strip = sh.scales[warp - 2][kb & 1];
 #pragma unroll
-            for (int i = 0; i < NT / 32; ++i) strip[lane + 32 * i] = sx[i];
+            for (int i = 0; i < PER; ++i)
+                if (lane + 32 * i < HALF) strip[lane + 32 * i] = sx[i];
             const float fw = sw;
             if (kb + 1 < kb1) fetch(kb + 1);
             // (the vote also orders the strip's writes)
-            if (!tc::mbar_wait_warp(smem_u32(&sh.tfull[buf]), buf_phase, smem_u32(&sh.abort))) {
+            if (!tc::mbar_wait_warp(tfull0 + buf * 8, buf_phase, abort0)) {
                 if (lane == 0) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
                 break;
             }
+            __syncwarp();
             tc::fence_after();
 #pragma unroll
-            for (int c = 0; c < NT; c += 32) {
-                if (c < p.n16) {
-                    float v[32];
-                    tc::tmem_ld32(t_col + buf * NT + c, v);
+            for (int c = 0; c < HALF; c += 16) {
+                if (r0 + c < p.n16) {
+                    float v[16];
+                    tc::tmem_ld16_start(t_col + buf * NT + c, v);
+                    tc::tmem_ld_wait(v);
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
+                    for (int i = 0; i < 16; i += 4) {
                         const float4 f = *reinterpret_cast<const float4 *>(strip + c + i);
                         acc[c + i] = fmaf(v[i] * f.x, fw, acc[c + i]);
                         acc[c + i + 1] = fmaf(v[i + 1] * f.y, fw, acc[c + i + 1]);
@@ -672,7 +686,7 @@ __global__ void __launch_bounds__(NARROW_THREADS, NT <= 64 ? 2 : 1)
             }
             tc::fence_before();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&sh.tempty[buf]);
+            if (lane == 0) tc::mbar_arrive(tempty0 + buf * 8);
             if (++buf == BUFS) {
                 buf = 0;
                 buf_phase ^= 1u;
@@ -680,10 +694,10 @@ __global__ void __launch_bounds__(NARROW_THREADS, NT <= 64 ? 2 : 1)
         }
         // this rank's sums, [row][weight row], over the ring: its last loads and MMAs have completed
         // (after a timeout another warp's may not have; the outputs are void then)
-        float *sums = reinterpret_cast<float *>(ring);
+        float *sums = reinterpret_cast<float *>(ring) + r0 * BM + quarter * 32 + lane;
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
-            if (i < rows) sums[i * BM + quarter * 32 + lane] = acc[i];
+        for (int i = 0; i < HALF; ++i)
+            if (r0 + i < rows) sums[i * BM] = acc[i];
     }
 
     tc::fence_before();
