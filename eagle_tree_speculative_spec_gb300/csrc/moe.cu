@@ -2,15 +2,17 @@
 // mixture-of-experts target's feed-forward layer (the layer's place: "EAGLE-3: Engineering
 // Implementation of LLM Inference Acceleration", appendix C, where it is a dense SwiGLU).
 //
-// Routing.  One warp per row keeps the row's E logits in registers (E / 32 a lane) as unsigned order
-// keys and takes the largest top_k times by a warp reduction of the key and then of the index (the
-// lowest index of the lanes that hold the maximum, so ties are exact); E is at most 512, so a row is
-// read once and its scores need no second pass.  32 rows make a chunk; a row takes an expert at most
-// once, so a chunk's choice of an expert is a 32-bit mask of rows, and a place's rank within the
-// chunk is the population count of the mask below its row: a stable counting sort without any atomic
-// whose order matters.  Up to 32 rows are one launch.  More rows are two: the first also writes the
-// places per (block, expert), the second adds the counts of the blocks before its own (at most 152
-// blocks, so at most 152 x 512 words read from L2 per block), scans the experts and places the rows.
+// Routing.  One warp per row: a lane takes E / 32 logits as unsigned order keys, ranks them among
+// themselves and lays them down in that order in shared memory, so that the largest top_k of the row are
+// a merge of 32 sorted lists: a warp reduction of the heads' keys, one of the indices of those that have
+// the maximum (the lowest, so ties are exact), and the winner's next key.  (Finding a lane's next key by
+// a search among its registers took 850 instructions a row of 256 logits and 8 places, twice as many.)  32
+// rows make a chunk; a row takes an expert at most once, so a chunk's choice of an expert is a 32-bit mask
+// of rows, and a place's rank within the chunk is the population count of the mask below its row: a stable
+// counting sort without any atomic whose order matters.  Up to 32 rows are one launch.  More rows are two:
+// the first also writes the places per (block, expert), the second adds the counts of the blocks before
+// its own (at most 152 blocks, so at most 152 x 512 words read from L2 per block), scans the experts and
+// places the rows.
 //
 // Combining.  A thread owns 8 columns of a row and adds the row's top_k vectors in order in fp32; the
 // loads of a row's places do not depend on one another.  Memory bound: every slot is read once.
@@ -38,7 +40,7 @@ struct RouteParams {
     int32_t *ids;
     float *weights;
     int32_t *offsets, *sorted, *slots, *dev_status;
-    int32_t *counts;      // [blocks][E] places per block (more than one block)
+    int32_t *counts;      // [blocks][E rounded up to 4] places per block (more than one block)
     int chunks_per_block; // rows of block b: [b, b + 1) * chunks_per_block * CHUNK
 };
 
@@ -53,8 +55,9 @@ E3_DEV int route_limit(const RouteParams &p) {
 }
 
 // The experts and weights of one row (all lanes of a warp); lane j < k returns place j's expert or -1.
+// sorted: the warp's (PER + 1) x 32 words.
 template <int PER>
-E3_DEV int route_row(const RouteParams &p, int row, bool live) {
+E3_DEV int route_row(const RouteParams &p, int row, bool live, uint32_t *sorted) {
     const int lane = threadIdx.x & 31;
     uint32_t key[PER];
 #pragma unroll
@@ -67,33 +70,37 @@ E3_DEV int route_row(const RouteParams &p, int row, bool live) {
             if (isfinite(z)) key[i] = order_key(z + 0.0f);
         }
     }
-    // this lane's largest logit left, and the lowest index that has it
-    uint32_t best = 0u;
-    int best_i = 0;
+    // ranks among the lane's own keys (equal ones by index), and the keys in that order, with a 0 behind
+    int rank[PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-        if (key[i] > best) {
-            best = key[i];
-            best_i = i;
+    for (int i = 0; i < PER; ++i) rank[i] = 0;
+#pragma unroll
+    for (int i = 1; i < PER; ++i)
+#pragma unroll
+        for (int j = 0; j < i; ++j) {
+            const bool first = key[j] >= key[i];
+            rank[i] += first ? 1 : 0;
+            rank[j] += first ? 0 : 1;
         }
-    uint32_t place_key = 0u, high = 0u;
-    int place_id = -1;
-    uint32_t taken = 0u;   // this lane's values that are taken (PER <= 16)
-    for (int j = 0; j < p.k; ++j) {
-        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-        if (top == 0u) break;   // uniform: no finite logit is left
-        const uint32_t at = __reduce_min_sync(0xffffffffu, best == top ? (uint32_t)(best_i * 32 + lane) : 0xffffffffu);
-        if ((int)(at & 31u) == lane) {
-            taken |= 1u << best_i;
-            best = 0u;
+    uint64_t order = 0;   // 4 bits an index, the first's lowest
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const uint32_t left = (taken >> i) & 1u ? 0u : key[i];
-                if (left > best) {
-                    best = left;
-                    best_i = i;
-                }
-            }
+    for (int i = 0; i < PER; ++i) {
+        sorted[rank[i] * 32 + lane] = key[i];
+        order |= (uint64_t)i << (4 * rank[i]);
+    }
+    sorted[PER * 32 + lane] = 0u;
+    uint32_t place_key = 0u, high = 0u, next = lane;   // next: this lane's head in `sorted`
+    int place_id = -1;
+    uint32_t head = sorted[next], head_id = (uint32_t)(order & 15u) * 32u + lane;
+    for (int j = 0; j < p.k; ++j) {
+        const uint32_t top = __reduce_max_sync(0xffffffffu, head);
+        if (top == 0u) break;   // uniform: no finite logit is left
+        const uint32_t at = __reduce_min_sync(0xffffffffu, head == top ? head_id : 0xffffffffu);
+        if (head == top && head_id == at) {
+            order >>= 4;
+            next += 32;
+            head = sorted[next];
+            head_id = (uint32_t)(order & 15u) * 32u + lane;
         }
         if (j == 0) high = top;
         if (lane == j) {
@@ -171,6 +178,7 @@ E3_DEV void place(const RouteParams &p, int row0, int r, int id, const uint32_t 
 // per expert of this block's rows.
 template <int PER>
 __global__ void __launch_bounds__(ROUTE_THREADS) moe_route_kernel(const RouteParams p) {
+    extern __shared__ uint32_t lists[];
     __shared__ uint32_t masks[MAX_E];
     __shared__ int base[MAX_E], warp_sums[32];
     pdl_wait();
@@ -183,7 +191,7 @@ __global__ void __launch_bounds__(ROUTE_THREADS) moe_route_kernel(const RoutePar
         if (threadIdx.x < MAX_E) masks[threadIdx.x] = 0u;
         __syncthreads();
         if (row < p.rows) {
-            const int id = route_row<PER>(p, row, row < limit);
+            const int id = route_row<PER>(p, row, row < limit, lists + warp * (PER + 1) * 32);
             if (id >= 0) atomicOr(&masks[id], 1u << warp);
         }
         __syncthreads();
@@ -191,7 +199,7 @@ __global__ void __launch_bounds__(ROUTE_THREADS) moe_route_kernel(const RoutePar
         if (gridDim.x > 1) __syncthreads();
     }
     if (gridDim.x > 1) {
-        if (threadIdx.x < p.E) p.counts[(size_t)blockIdx.x * p.E + threadIdx.x] = mine;
+        if (threadIdx.x < p.E) p.counts[(size_t)blockIdx.x * ((p.E + 3) & ~3) + threadIdx.x] = mine;
         return;
     }
     // a single block holds a single chunk
@@ -208,25 +216,28 @@ __global__ void __launch_bounds__(ROUTE_THREADS) moe_route_kernel(const RoutePar
 
 __global__ void __launch_bounds__(ROUTE_THREADS) moe_place_kernel(const RouteParams p) {
     __shared__ uint32_t masks[MAX_E];
-    __shared__ int base[MAX_E], before[ROUTE_THREADS], all[ROUTE_THREADS], warp_sums[32];
+    __shared__ int base[MAX_E], warp_sums[32];
+    __shared__ int4 before[ROUTE_THREADS], all[ROUTE_THREADS];   // [group][4 experts]
     pdl_wait();
     pdl_trigger();
     const int r = threadIdx.x / p.k, first_row = blockIdx.x * p.chunks_per_block * CHUNK;
     int id = chunk_place(p, first_row, r);   // in flight with the counts
-    // thread (g, e): blocks g, g + G, ... of expert e, 16 loads at a time
-    const int width = p.E <= 128 ? 128 : p.E <= 256 ? 256 : 512, G = ROUTE_THREADS / width;
-    const int e = threadIdx.x % width, g = threadIdx.x / width;
-    int sum = 0, ahead = 0;
-    if (e < p.E) {
-        for (int b0 = g; b0 < (int)gridDim.x; b0 += 16 * G) {
-            int v[16];
+    // thread (g, q): experts 4 q .. 4 q + 3 of blocks g, g + G, ..., 8 loads at a time
+    const int quads = (p.E + 3) >> 2, bits = quads <= 32 ? 5 : quads <= 64 ? 6 : 7;
+    const int q = threadIdx.x & ((1 << bits) - 1), g = threadIdx.x >> bits, G = ROUTE_THREADS >> bits;
+    int4 sum = make_int4(0, 0, 0, 0), ahead = sum;
+    if (q < quads) {
+        const int4 *at = reinterpret_cast<const int4 *>(p.counts) + (size_t)g * quads + q;
+        const int step = G * quads;
+        int left = ((int)gridDim.x - g + G - 1) / G, left_ahead = ((int)blockIdx.x - g + G - 1) / G;
+        for (; left > 0; left -= 8, left_ahead -= 8, at += 8 * step) {
+            int4 v[8];
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                v[i] = b0 + i * G < (int)gridDim.x ? __ldg(p.counts + (size_t)(b0 + i * G) * p.E + e) : 0;
+            for (int i = 0; i < 8; ++i) v[i] = i < left ? __ldg(at + i * step) : make_int4(0, 0, 0, 0);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                sum += v[i];
-                ahead += b0 + i * G < (int)blockIdx.x ? v[i] : 0;
+            for (int i = 0; i < 8; ++i) {
+                sum.x += v[i].x, sum.y += v[i].y, sum.z += v[i].z, sum.w += v[i].w;
+                if (i < left_ahead) ahead.x += v[i].x, ahead.y += v[i].y, ahead.z += v[i].z, ahead.w += v[i].w;
             }
         }
     }
@@ -234,11 +245,14 @@ __global__ void __launch_bounds__(ROUTE_THREADS) moe_place_kernel(const RoutePar
     before[threadIdx.x] = ahead;
     __syncthreads();
     int mine = 0, first = 0, total;
-    if (threadIdx.x < width)
+    if (threadIdx.x < p.E) {
+        const int *sums = reinterpret_cast<const int *>(all) + threadIdx.x;
+        const int *firsts = reinterpret_cast<const int *>(before) + threadIdx.x;
         for (int i = 0; i < G; ++i) {
-            mine += all[i * width + threadIdx.x];
-            first += before[i * width + threadIdx.x];
+            mine += sums[i << (bits + 2)];
+            first += firsts[i << (bits + 2)];
         }
+    }
     const int start = scan_experts(mine, warp_sums, &total);
     if (threadIdx.x < MAX_E) base[threadIdx.x] = start + first;
     if (blockIdx.x == 0) {
@@ -363,7 +377,7 @@ RoutePlan route_plan(const eagle3_moe_route_args_t *a) {
     RoutePlan pl;
     pl.chunks_per_block = std::max(1, (chunks + ROUTE_MAX_BLOCKS - 1) / ROUTE_MAX_BLOCKS);
     pl.blocks = std::max(1, (chunks + pl.chunks_per_block - 1) / pl.chunks_per_block);
-    pl.ws_bytes = pl.blocks > 1 ? (size_t)pl.blocks * a->n_experts * sizeof(int32_t) : 0;
+    pl.ws_bytes = pl.blocks > 1 ? (size_t)pl.blocks * ((a->n_experts + 3) & ~3) * sizeof(int32_t) : 0;
     return pl;
 }
 
@@ -400,7 +414,13 @@ eagle3_status_t validate(const eagle3_moe_combine_args_t *a) {
 
 template <int PER>
 cudaError_t launch_route(int blocks, cudaStream_t st, const RouteParams &p) {
-    return launch_pdl(moe_route_kernel<PER>, dim3(blocks), dim3(ROUTE_THREADS), 0, st, p);
+    constexpr int LISTS = CHUNK * (PER + 1) * 32 * 4;
+    static PerDevice<cudaError_t> attr;
+    const cudaError_t e = attr.get([] {
+        return cudaFuncSetAttribute(moe_route_kernel<PER>, cudaFuncAttributeMaxDynamicSharedMemorySize, LISTS);
+    });
+    if (e != cudaSuccess) return e;
+    return launch_pdl(moe_route_kernel<PER>, dim3(blocks), dim3(ROUTE_THREADS), LISTS, st, p);
 }
 
 template <int VEC>
