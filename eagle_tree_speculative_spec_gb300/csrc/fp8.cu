@@ -77,16 +77,27 @@ __device__ __noinline__ uint2 codes_exact(uint4 raw, float s) {
     return make_uint2(q[0], q[1]);
 }
 
-// e4m3(x / s) for 8 values.  With y = 1 / s rounded to nearest, q0 = x y and q = q0 + (x - q0 s) y (each
-// operation rounded once) is the correctly rounded quotient: Markstein's correction step ("Computation of
-// elementary functions on the IBM RISC System/6000 processor", 1990).  His theorem wants q0 within a step
-// of the quotient, which x y need not be, but s is a bf16 number over 448 and x a bf16 number, so that
-// there are 128 x 128 pairs of significands: all of them were checked, and powers of two change nothing as
-// long as nothing under- or overflows (s >= 2^-90, and x / s at most 448).  -0 keeps its sign.  IEEE
-// divisions for every value made the kernel issue-bound: 42 us for 3840 x 14336 against 25 us of bytes.
-E3_DEV uint2 codes(uint4 raw, float s) {
-    if (!(s >= 0x1p-90f)) return codes_exact(raw, s);   // or NaN
-    const float y = __fdiv_rn(1.0f, s);
+// Quotients without a division (IEEE divisions made the kernel issue-bound: 42 us for 3840 x 14336 against
+// 25 us of bytes).  With y the correctly rounded 1 / b and q0 = a y, q = q0 + (a - q0 b) y (each operation
+// rounded once) is a / b correctly rounded: Markstein's correction step ("Computation of elementary
+// functions on the IBM RISC System/6000 processor", 1990); y itself is one Newton step from an
+// approximation.  His theorem wants q0 within a step of the quotient, which a y need not be; but a block's
+// maximum and its values are bf16 numbers and the scale is such a number over 448, so that there are 128
+// significands of scales and 128 x 128 of quotients: all were checked (for y0 up to 3 steps off), and
+// powers of two change nothing as long as nothing under- or overflows (maxima from 2^-80 on).
+constexpr uint32_t QUANT_LEAST = 0x1780u;   // bf16 bits of 2^-80
+E3_DEV float scale_of(uint32_t top) {       // top: bf16 bits of the block's maximum, QUANT_LEAST or more
+    constexpr float Y = 0x1.24924ap-9f;     // 1 / 448 rounded to nearest
+    const float a = __uint_as_float(top << 16), q0 = a * Y;
+    return fmaf(fmaf(-q0, E4M3_MAX, a), Y, q0);
+}
+E3_DEV float reciprocal_of(float s) {
+    float y0;
+    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(y0) : "f"(s));
+    return fmaf(y0, fmaf(-s, y0, 1.0f), y0);
+}
+// e4m3(x / s) for 8 values, y = 1 / s.  -0 keeps its sign.
+E3_DEV uint2 codes(uint4 raw, float s, float y) {
     const float2 y2 = make_float2(y, y), s2 = make_float2(-s, -s);
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
     uint32_t c[4];
@@ -104,49 +115,57 @@ E3_DEV uint2 codes(uint4 raw, float s) {
 
 // A half warp holds a block of 128 columns of one row, 8 values a lane; a warp takes two neighbouring
 // blocks of R consecutive rows, all loads first, and writes the R scales of a block side by side.
+template <int R, bool WHOLE>
+E3_DEV void quantize_rows(const QuantParams &p, int row0, int col) {
+    const int lane = threadIdx.x & 31;
+    const bool in = col < p.k;   // k is a multiple of 16: 8 values are in or out together
+    uint4 raw[R];
+    const __nv_bfloat16 *x = p.x + (size_t)row0 * p.ld_x + col;
+#pragma unroll
+    for (int r = 0; r < R; ++r, x += p.ld_x) {
+        raw[r] = make_uint4(0u, 0u, 0u, 0u);
+        if (in && (WHOLE || row0 + r < p.m)) raw[r] = __ldcs(reinterpret_cast<const uint4 *>(x));
+    }
+    float scale = 0.0f;   // lane r of the half warp keeps row r's
+    uint8_t *q = p.q + (size_t)row0 * p.ld_q + col;
+#pragma unroll
+    for (int r = 0; r < R; ++r, q += p.ld_q) {
+        // |bf16| as integers: the largest of numbers, above them infinity, above that NaN
+        uint32_t top = __vmaxu2(__vmaxu2(raw[r].x & 0x7fff7fffu, raw[r].y & 0x7fff7fffu),
+                                __vmaxu2(raw[r].z & 0x7fff7fffu, raw[r].w & 0x7fff7fffu));
+        top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+        for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));   // within 16 lanes
+        float s;
+        uint2 c;
+        if (top >= QUANT_LEAST && top < 0x7f80u) {
+            s = scale_of(top);
+            c = codes(raw[r], s, reciprocal_of(s));
+        } else {
+            s = top >= 0x7f80u ? __int_as_float(0x7fffffff)
+                : top == 0u    ? 1.0f
+                               : __fdiv_rn(__uint_as_float(top << 16), E4M3_MAX);
+            c = codes_exact(raw[r], s);
+        }
+        if (in && (WHOLE || row0 + r < p.m)) *reinterpret_cast<uint2 *>(q) = c;
+        scale = (lane & 15) == r ? s : scale;
+    }
+    const int hl = lane & 15;
+    if ((col & ~(BK - 1)) < p.k && hl < R && row0 + hl < p.m) p.scale[(size_t)(col / BK) * p.m + row0 + hl] = scale;
+}
+
 template <int R>
 __global__ void __launch_bounds__(QUANT_THREADS) quantize_kernel(const QuantParams p) {
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31, pairs = (p.k + 2 * BK - 1) / (2 * BK);
+    const int pairs = (p.k + 2 * BK - 1) / (2 * BK);
     const long long task = (long long)blockIdx.x * (QUANT_THREADS / 32) + (threadIdx.x >> 5);
-    const int row0 = (int)(task / pairs) * R, col = (int)(task % pairs) * 2 * BK + lane * 8;
-    if (row0 >= p.m) return;
-    const bool in = col < p.k;   // k is a multiple of 16: 8 values are in or out together
-    uint4 raw[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        raw[r] = make_uint4(0u, 0u, 0u, 0u);
-        if (in && row0 + r < p.m) raw[r] = __ldcs(reinterpret_cast<const uint4 *>(p.x + (size_t)(row0 + r) * p.ld_x + col));
-    }
-    float s[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        // |bf16| as integers: the largest of numbers, above them infinity, above that NaN
-        const uint32_t w[4] = {raw[r].x, raw[r].y, raw[r].z, raw[r].w};
-        uint32_t top = 0u;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
-        top = max(top & 0xffffu, top >> 16);
-#pragma unroll
-        for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));   // within 16 lanes
-        s[r] = top >= 0x7f80u ? __int_as_float(0x7fffffff)
-               : top == 0u    ? 1.0f
-                              : __fdiv_rn(__uint_as_float(top << 16), E4M3_MAX);
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        if (!in || row0 + r >= p.m) continue;
-        *reinterpret_cast<uint2 *>(p.q + (size_t)(row0 + r) * p.ld_q + col) = codes(raw[r], s[r]);
-    }
-    // lane r of the half warp writes row r's scale
-    const int hl = lane & 15;
-    if ((col & ~(BK - 1)) < p.k && hl < R && row0 + hl < p.m) {
-        float v = s[0];
-#pragma unroll
-        for (int r = 1; r < R; ++r) v = hl == r ? s[r] : v;
-        p.scale[(size_t)(col / BK) * p.m + row0 + hl] = v;
-    }
+    const int row0 = (int)(task / pairs) * R, col = (int)(task % pairs) * 2 * BK + (threadIdx.x & 31) * 8;
+    if (row0 >= p.m) return;   // whole warps
+    if (row0 + R <= p.m)
+        quantize_rows<R, true>(p, row0, col);
+    else
+        quantize_rows<R, false>(p, row0, col);
 }
 
 // ---- output -------------------------------------------------------------------------------------
