@@ -250,7 +250,8 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
     uint8_t *ring = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *boxes = ring + WIDE_STAGES * WIDE_STAGE;
     WideShared &sh = *reinterpret_cast<WideShared *>(boxes + WIDE_EPI_WARPS * WIDE_BOX);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t tid = tc::thread_index();
+    const int warp = (int)(tid >> 5), lane = (int)(tid & 31u);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < WIDE_STAGES; ++s) {
@@ -406,9 +407,9 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                                                                        : run_b + (c + 1 - WIDE_RUN / 16) * 16),
                                             v[(c + 1) & 1]);
                     } else {   // the buffer is read: it may take the k-block after the next
+                        // (the wait for the last load was the whole warp's)
                         tc::fence_before();
-                        __syncwarp();
-                        if (lane == 0) tc::mbar_arrive(full0 + ((stage + 2) % WIDE_STAGES) * 8);
+                        tc::mbar_arrive_if(full0 + ((stage + 2) % WIDE_STAGES) * 8, lane == 0);
                     }
                     const float2 f = make_float2(c < WIDE_RUN / 16 ? fa : fb, c < WIDE_RUN / 16 ? fa : fb);
 #pragma unroll

@@ -92,6 +92,12 @@ E3_DEV void mbar_drain(uint32_t bar, uint32_t parity) {
 E3_DEV void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
+// by the lanes for which `one` holds, without a branch
+E3_DEV void mbar_arrive_if(uint32_t bar, bool one) {
+    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n @p mbarrier.arrive.shared::cta.b64 _, [%0];\n}\n" ::"r"(bar),
+                 "r"(one ? 1u : 0u)
+                 : "memory");
+}
 E3_DEV void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(bytes) : "memory");
 }
@@ -180,6 +186,14 @@ E3_DEV bool elect_one() {
     uint32_t p;
     asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(p));
     return p != 0;
+}
+
+// threadIdx.x in a register for good: the compiler otherwise reads the special register again (some 20
+// cycles) wherever registers are short, several times in an inner loop.
+E3_DEV uint32_t thread_index() {
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%tid.x;\n" : "=r"(t));
+    return t;
 }
 
 // ---- tcgen05 ---------------------------------------------------------------------------------------
