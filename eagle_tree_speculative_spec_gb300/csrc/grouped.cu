@@ -123,8 +123,8 @@ E3_DEV void copy16(uint32_t dst, const void *src, bool zero) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(zero ? 0 : 16) : "memory");
 }
 // arrive on bar once this thread's copies so far have landed
-E3_DEV void copies_arrive(uint64_t *bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(smem_u32(bar)) : "memory");
+E3_DEV void copies_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
 }
 // Barrier `id` over two warps; the variant with a flag tells whether it was set for all threads.
 E3_DEV void pair_sync(int id) { asm volatile("bar.sync %0, 64;\n" ::"r"(id) : "memory"); }
@@ -156,8 +156,8 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     Shared &sh = *reinterpret_cast<Shared *>(ring + RING_BYTES);
-    volatile int *abort = &sh.abort;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t tid = tc::thread_index();
+    const int warp = (int)(tid >> 5), lane = (int)(tid & 31u);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < MAX_STAGES; ++s) {
@@ -227,6 +227,9 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
     // whole 1024-byte blocks keep the swizzle's phase; the deepest ring that fits
     const int stages = min(MAX_STAGES, RING_BYTES / stage_bytes);
 
+    const uint32_t ring0 = smem_u32(ring), full0 = smem_u32(sh.full), empty0 = smem_u32(sh.empty);
+    const uint32_t tfull0 = smem_u32(sh.tfull), tempty0 = smem_u32(sh.tempty), abort0 = smem_u32(&sh.abort);
+
     if (warp == 0) {
         // ------------------------------------------------------------------ TMA producer
         if (tc::elect_one()) {
@@ -237,15 +240,15 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
                 const Unit w = unit_at(sh, p, u);
                 const int boxes = box_rows(w.n16);
                 for (int kb = 0; kb < p.kb_total; ++kb) {
-                    uint64_t *full = &sh.full[stage];
-                    if (!tc::mbar_wait(&sh.empty[stage], phase ^ 1u, abort)) {
+                    const uint32_t full = full0 + stage * 8;
+                    if (!tc::mbar_wait(empty0 + stage * 8, phase ^ 1u, abort0)) {
                         ok = false;
                         break;
                     }
                     tc::mbar_expect_tx(full, W_BYTES + (GATHER ? 0 : boxes * ROW_BYTES));
                     issued |= 1u << stage;
                     last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
-                    uint8_t *sw = ring + stage * stage_bytes, *sx = sw + W_BYTES;
+                    const uint32_t sw = ring0 + stage * stage_bytes, sx = sw + W_BYTES;
                     const int x = kb * BK;
                     if (SWIGLU) {
                         tc::tma_load_3d(sw, &tm_w, x, w.mt * (BM / 2), w.e, full);
@@ -272,33 +275,28 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
             if (!ok) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
             // no TMA write may still be in flight when the CTA exits: wait (bounded) for the last load
             // issued to every stage; these return at once when the loads were consumed
-            for (int st = 0; st < stages; ++st) {
-                if (!((issued >> st) & 1u)) continue;
-                const uint32_t par = (last_parity >> st) & 1u;
-                const long long t0 = clock64();
-                while (!tc::mbar_try(&sh.full[st], par) && clock64() - t0 < WAIT_LIMIT_CYCLES) {
-                }
-            }
+            for (int st = 0; st < stages; ++st)
+                if ((issued >> st) & 1u) tc::mbar_drain(full0 + st * 8, (last_parity >> st) & 1u);
         }
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------------ MMA issuer
         if (tc::elect_one()) {
-            const uint64_t desc0 = tc::desc_sw128(smem_u32(ring));
+            const uint64_t desc0 = tc::desc_sw128(ring0);
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true;
             for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
                 const Unit w = unit_at(sh, p, u);
                 const uint32_t idesc = tc::idesc_bf16(BM, w.n16);
-                if (!tc::mbar_wait(&sh.tempty[acc], acc_phase ^ 1u, abort)) {
+                if (!tc::mbar_wait(tempty0 + acc * 8, acc_phase ^ 1u, abort0)) {
                     ok = false;
                     break;
                 }
                 tc::fence_after();
                 const uint32_t d = tmem + (uint32_t)(acc * MAX_ROWS);
                 for (int kb = 0; kb < p.kb_total; ++kb) {
-                    if (!tc::mbar_wait(&sh.full[stage], phase, abort)) {
+                    if (!tc::mbar_wait(full0 + stage * 8, phase, abort0)) {
                         ok = false;
                         break;
                     }
@@ -309,31 +307,29 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
 #pragma unroll
                     for (int k = 0; k < BK / 16; ++k)
                         tc::mma_bf16_ss(d, a + k * 2, b + k * 2, idesc, (kb > 0 || k > 0) ? 1u : 0u);
-                    tc::mma_commit(&sh.empty[stage]);
+                    tc::mma_commit(empty0 + stage * 8);
                     if (++stage == stages) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
                 if (!ok) break;
-                tc::mma_commit(&sh.tfull[acc]);
+                tc::mma_commit(tfull0 + acc * 8);
                 acc_phase ^= (uint32_t)acc;
                 acc ^= 1;
             }
             if (!ok) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
             // every MMA this thread issued must retire before TMEM is freed (bounded wait)
-            tc::mma_commit(&sh.mma_done);
-            const long long t0 = clock64();
-            while (!tc::mbar_try(&sh.mma_done, 0) && clock64() - t0 < WAIT_LIMIT_CYCLES) {
-            }
+            tc::mma_commit(smem_u32(&sh.mma_done));
+            tc::mbar_drain(smem_u32(&sh.mma_done), 0);
         }
         __syncwarp();
     } else if (GATHER && warp >= 6) {
         // ------------------------------------------------------------------ row gather (warps 6..9)
         // Thread t copies 16-byte piece t % 8 of rows t / 8 + 16 i; its arrival on the stage's barrier
         // follows its copies by itself.
-        const int t = threadIdx.x - NTHREADS, piece = t & 7, first = t >> 3;
-        const uint32_t dst0 = smem_u32(ring) + W_BYTES + first * ROW_BYTES + ((piece ^ (first & 7)) << 4);
+        const int t = (int)tid - NTHREADS, piece = t & 7, first = t >> 3;
+        const uint32_t dst0 = ring0 + W_BYTES + first * ROW_BYTES + ((piece ^ (first & 7)) << 4);
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -352,10 +348,7 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
                 src[i] = p.x + (size_t)v * p.ld_x + piece * 8;
             }
             for (int kb = 0; kb < p.kb_total; ++kb) {
-                int fine = 0;
-                if (lane == 0) fine = tc::mbar_wait(&sh.empty[stage], phase ^ 1u, abort) ? 1 : 0;
-                fine = __shfl_sync(0xffffffffu, fine, 0);
-                if (!fine) {
+                if (!tc::mbar_wait_warp(empty0 + stage * 8, phase ^ 1u, abort0)) {
                     ok = false;
                     break;
                 }
@@ -365,7 +358,7 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
 #pragma unroll
                 for (int i = 0; i < MAX_ROWS / 16; ++i)
                     if (16 * i < w.n16) copy16(dst + i * 16 * ROW_BYTES, src[i] + at, past);
-                copies_arrive(&sh.full[stage]);
+                copies_arrive(full0 + stage * 8);
                 if (++stage == stages) {
                     stage = 0;
                     phase ^= 1u;
@@ -381,10 +374,7 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
         uint32_t acc_phase = 0;
         for (int u = blockIdx.x; u < units; u += gridDim.x) {
             const Unit w = unit_at(sh, p, u);
-            // warp-uniform wait: lane 0 polls, the outcome is broadcast
-            int ok = 0;
-            if (lane == 0) ok = tc::mbar_wait(&sh.tfull[acc], acc_phase, abort) ? 1 : 0;
-            ok = __shfl_sync(0xffffffffu, ok, 0);
+            bool ok = tc::mbar_wait_warp(tfull0 + acc * 8, acc_phase, abort0);
             // (the two warps of a pair go on or leave together: they meet at barriers below)
             if (SWIGLU) ok = pair_all(1 + (quarter & 1), ok);
             if (!ok) {
@@ -450,7 +440,7 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
             }
             tc::fence_before();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&sh.tempty[acc]);
+            tc::mbar_arrive_if(tempty0 + acc * 8, lane == 0);
             acc_phase ^= (uint32_t)acc;
             acc ^= 1;
         }
