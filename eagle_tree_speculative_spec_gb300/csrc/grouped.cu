@@ -17,7 +17,7 @@
 //   warps 2..5  epilogue: tcgen05.ld, SwiGLU, stores of two columns a lane.  TMEM lanes 0..63 hold gate
 //               columns and 64..127 their up columns: two warps that share columns swap them through
 //               shared memory, and each finishes half of the rows
-//   warps 6..9  with row_ids only: gather the rows by 16-byte asynchronous copies into the swizzled
+//   warps 6..13 with row_ids only: gather the rows by 16-byte asynchronous copies into the swizzled
 //               tile (TMA's four-row gathers cost as much as a box each: 2288 us for 3840 rows x 8 of
 //               64 experts, k = 4096, 2 x 1024 columns)
 // The accumulator is double-buffered in TMEM (2 x 256 columns).  The ring's stage holds a weight tile
@@ -39,7 +39,8 @@ namespace {
 
 constexpr int BM = 128, BK = 64;          // weight rows and k values of a tile
 constexpr int MAX_ROWS = 256;             // rows of a tile (the MMA's N), a multiple of 16
-constexpr int NTHREADS = 192, GATHER_WARPS = 4;
+constexpr int NTHREADS = 192, GATHER_WARPS = 8;
+constexpr int GATHER_ROWS = 4 * GATHER_WARPS;   // rows of a pass: 8 threads a row
 constexpr int W_BYTES = BM * BK * 2;
 constexpr int ROW_BYTES = BK * 2;
 constexpr int MAX_STAGES = 12;
@@ -325,8 +326,8 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
         }
         __syncwarp();
     } else if (GATHER && warp >= 6) {
-        // ------------------------------------------------------------------ row gather (warps 6..9)
-        // Thread t copies 16-byte piece t % 8 of rows t / 8 + 16 i; its arrival on the stage's barrier
+        // ------------------------------------------------------------------ row gather (warps 6..13)
+        // Thread t copies 16-byte piece t % 8 of rows t / 8 + 32 i; its arrival on the stage's barrier
         // follows its copies by itself.
         const int t = (int)tid - NTHREADS, piece = t & 7, first = t >> 3;
         const uint32_t dst0 = ring0 + W_BYTES + first * ROW_BYTES + ((piece ^ (first & 7)) << 4);
@@ -335,12 +336,12 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
         bool ok = true;
         for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
             const Unit w = unit_at(sh, p, u);
-            const __nv_bfloat16 *src[MAX_ROWS / 16];
+            const __nv_bfloat16 *src[MAX_ROWS / GATHER_ROWS];
 #pragma unroll
-            for (int i = 0; i < MAX_ROWS / 16; ++i) {
-                if (16 * i >= w.n16) continue;
+            for (int i = 0; i < MAX_ROWS / GATHER_ROWS; ++i) {
+                if (GATHER_ROWS * i >= w.n16) continue;
                 // rows past the tile's last repeat it
-                int v = __ldg(p.row_ids + w.row0 + min(first + 16 * i, w.rows - 1));
+                int v = __ldg(p.row_ids + w.row0 + min(first + GATHER_ROWS * i, w.rows - 1));
                 if (v < 0 || v >= p.n_src) {
                     flag(p.dev_status, EAGLE3_DEV_BAD_COUNTS);
                     v = 0;
@@ -356,8 +357,8 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
                 const bool past = kb * BK + piece * 8 >= p.k;   // k is a multiple of 8
                 const int at = past ? 0 : kb * BK;
 #pragma unroll
-                for (int i = 0; i < MAX_ROWS / 16; ++i)
-                    if (16 * i < w.n16) copy16(dst + i * 16 * ROW_BYTES, src[i] + at, past);
+                for (int i = 0; i < MAX_ROWS / GATHER_ROWS; ++i)
+                    if (first + GATHER_ROWS * i < w.n16) copy16(dst + i * GATHER_ROWS * ROW_BYTES, src[i] + at, past);
                 copies_arrive(full0 + stage * 8);
                 if (++stage == stages) {
                     stage = 0;
