@@ -17,6 +17,9 @@ A step, every part of it a libeagle3 call on the caller's stream:
       eagle3_linear     fused QKV projection; q and k leave it rotated at prefix_len + depth
       eagle3_verify_attn tree-masked attention over the layer's cache and the tree
       eagle3_linear     O projection + residual, post-norm, SwiGLU gate/up, down + residual
+                        (a mixture-of-experts layer instead: router logits, eagle3_moe_route, the
+                        experts' SwiGLU gate/up and down by eagle3_grouped_linear,
+                        eagle3_moe_combine + residual)
                         (fold_norms: the RMSNorms before QKV, gate/up and the LM head are folded
                         into those projections: the O and down projections emit each row's sum of
                         squares, the next projection reads the raw residual stream with the norm
@@ -52,12 +55,19 @@ class SpeculativeStep:
     the sampled-children mode does not apply), temperature, seed, rope_theta, eps.
     target: dict with embed [V, d], lm_head [V, d], final_norm [d] and per-layer lists of
     wqkv [(Hq + 2 Hkv) D, d], wo [d, Hq D], wg / wu [F, d], wd [d, F], norm1 / norm2 [d] (bf16).
+    A layer whose wg, wu [E, Fe, d] and wd [E, d, Fe] are 3-D is a mixture of experts with the router
+    weights router[layer] [E, d] (bf16); cfg then has experts_per_token, and optionally moe_scoring
+    (MOE_SOFTMAX), moe_renormalize (True) and moe_scale (1.0).  E and Fe are the same in all such
+    layers.  fold_norms keeps the norm kernels in front of a mixture-of-experts layer's router and
+    behind its combination.
     draft: dict of the eagle3_draft_tree weights (bf16; see _lib.DRAFT_WEIGHT_NAMES).
     s_max: cache capacity; max_prefix: host bound on every prefix length over the run (the kernels
     read the exact lengths from device memory, so one set of prepared calls serves every step).
 
     The caller fills the caches and the per-sequence state (prefix_len, draft_len, aux_in,
     next_tok, tc) before the first step; the buffers are attributes of this object."""
+
+    moe_layers = {}   # (E, Fe) of the mixture-of-experts layers, by layer; set by prepare()
 
     def __init__(self, cfg, target, draft, s_max, max_prefix, dev, fused_rope=True, d2t=None, fold_norms=False):
         c = self.cfg = dict(cfg)
@@ -134,7 +144,8 @@ class SpeculativeStep:
     # ------------------------------------------------------------------------------ preparation
     def prepare(self, ws_linear_bytes=512 << 20, ws_attn_bytes=256 << 20, lazy_head=False):
         """Build every argument struct of the step once.  Ops are (kind, call) pairs; kind names
-        the calls a profiler may want to time ("gemm", "gemm_gateup", "verify_attn") or is None.
+        the calls a profiler may want to time ("gemm", "gemm_gateup", "verify_attn", and "grouped",
+        "grouped_gateup" of mixture-of-experts layers) or is None.
         lazy_head: the acceptance computes the target LM head's logits itself, one level of the walk
         at a time and only for the nodes it visits (same decisions as the full head; the logits
         buffer is then not written)."""
@@ -199,6 +210,10 @@ class SpeculativeStep:
 
         T = self.target
         taps = {t: i for i, t in enumerate(c["taps"])}
+        moe = [T["wg"][l].dim() == 3 for l in range(c["layers"])]
+        self.moe_layers = {l: tuple(T["wg"][l].shape[:2]) for l, m in enumerate(moe) if m}
+        if self.moe_layers:
+            self._alloc_moe()
         fold = self.fold_norms
         if fold and self._folded is None:
             self._folded = self._fold_weights()
@@ -210,7 +225,7 @@ class SpeculativeStep:
         for l in range(c["layers"]):
             # the attention norm: a kernel on layer 0 (embedding gather) and on tapped layers (the tap
             # copies the stream entering the layer); otherwise folded into the QKV projection
-            fold1 = fold and l > 0 and l not in taps
+            fold1 = fold and l > 0 and l not in taps and not moe[l - 1]
             if l > 0 and not fold1:
                 tap = self.aux_tree[:, taps[l] * d:(taps[l] + 1) * d] if l in taps else None
                 norm(self.x, T["norm1"][l], self.h, tap=tap)
@@ -230,7 +245,11 @@ class SpeculativeStep:
             keep.append(va)
             ops.append(("verify_attn", lambda a=va: L.eagle3_verify_attn(ctypes.byref(a), ap, ab, st)))
             lin(self.attn, T["wo"][l], self.x, epi=e3.EPI_BF16_RESIDUAL, res=self.x,
-                ssq_out=self.ssq_mid if fold else None)
+                ssq_out=self.ssq_mid if fold and not moe[l] else None)
+            if moe[l]:
+                norm(self.x, T["norm2"][l], self.h)
+                self._moe_layer(l, lin, ops, dev_st, st)
+                continue
             if fold:   # the post-attention norm folded into the gate / up projection
                 lin(self.x, Fw["wg"][l], self.act, epi=e3.EPI_SWIGLU, w2=Fw["wu"][l], kind="gemm_gateup",
                     ssq_in=self.ssq_mid)
@@ -239,7 +258,7 @@ class SpeculativeStep:
                 lin(self.h, T["wg"][l], self.act, epi=e3.EPI_SWIGLU, w2=T["wu"][l], kind="gemm_gateup")
             lin(self.act, T["wd"][l], self.x, epi=e3.EPI_BF16_RESIDUAL, res=self.x,
                 ssq_out=self.ssq_next if fold else None)
-        fold_f = fold and not self.lazy_head   # the lazy head gathers normalised rows
+        fold_f = fold and not self.lazy_head and not moe[-1]   # the lazy head gathers normalised rows
         if not fold_f:
             norm(self.x, T["final_norm"], self.h)
         # ---- acceptance over the tree (the emitted row is the next step's catch-up tokens)
@@ -287,6 +306,53 @@ class SpeculativeStep:
         self.ops = self.draft_ops + self.verify_ops
         return self
 
+    def _alloc_moe(self):
+        """Buffers of the mixture-of-experts layers (shared by all of them)."""
+        T, c = self.target, self.cfg
+        (E, Fe), d = next(iter(self.moe_layers.values())), c["d"]
+        for l in self.moe_layers:
+            for name, shape in (("wg", (E, Fe, d)), ("wu", (E, Fe, d)), ("wd", (E, d, Fe)), ("router", (E, d))):
+                if tuple(T[name][l].shape) != shape:
+                    raise ValueError(f"{name}[{l}] has shape {tuple(T[name][l].shape)}, expected {shape}")
+        k, R, dev = int(c["experts_per_token"]), c["B"] * c["N"], self.dev
+        bf, i32, f32 = torch.bfloat16, torch.int32, torch.float32
+        self.moe_logits = torch.empty(R, E, dtype=f32, device=dev)
+        self.moe_ids = torch.empty(R, k, dtype=i32, device=dev)
+        self.moe_weights = torch.empty(R, k, dtype=f32, device=dev)
+        self.moe_offsets = torch.empty(E + 1, dtype=i32, device=dev)
+        self.moe_rows = torch.empty(R * k, dtype=i32, device=dev)
+        self.moe_slots = torch.empty(R, k, dtype=i32, device=dev)
+        self.moe_act = torch.empty(R * k, Fe, dtype=bf, device=dev)
+        self.moe_out = torch.empty(R * k, d, dtype=bf, device=dev)
+        a = self._moe_route_args()
+        need = _lib.lib().eagle3_moe_route_workspace_size(ctypes.byref(a))
+        self.ws_moe = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+
+    def _moe_route_args(self):
+        c = self.cfg
+        return _lib.moe_route_args(self.moe_logits, self.moe_ids, self.moe_weights, self.moe_offsets, self.moe_rows,
+                                   self.moe_slots, scoring=c.get("moe_scoring", _lib.MOE_SOFTMAX),
+                                   renormalize=c.get("moe_renormalize", True), scale=c.get("moe_scale", 1.0),
+                                   dev_status=self.dev_status)
+
+    def _moe_layer(self, l, lin, ops, dev_st, st):
+        """The calls of layer l's mixture-of-experts feed-forward: self.h (normalised) -> self.x += ..."""
+        e3, T, L = _lib, self.target, _lib.lib()
+        lin(self.h, T["router"][l], self.moe_logits, epi=e3.EPI_F32)
+        ra = self._moe_route_args()
+        up = e3.grouped_linear_args(self.h, T["wg"][l], self.moe_offsets, self.moe_act, epilogue=e3.EPI_SWIGLU,
+                                    w2=T["wu"][l], row_ids=self.moe_rows, dev_status=self.dev_status)
+        down = e3.grouped_linear_args(self.moe_act, T["wd"][l], self.moe_offsets, self.moe_out,
+                                      dev_status=self.dev_status)
+        ca = e3.moe_combine_args(self.moe_out, self.moe_slots, self.moe_weights, self.x, residual=self.x,
+                                 dev_status=self.dev_status)
+        self._keep += [ra, up, down, ca]
+        wp, wb = ctypes.c_void_p(self.ws_moe.data_ptr()), ctypes.c_size_t(self.ws_moe.numel())
+        ops.append((None, lambda a=ra: L.eagle3_moe_route(ctypes.byref(a), wp, wb, st)))
+        ops.append(("grouped_gateup", lambda a=up: L.eagle3_grouped_linear(ctypes.byref(a), st)))
+        ops.append(("grouped", lambda a=down: L.eagle3_grouped_linear(ctypes.byref(a), st)))
+        ops.append((None, lambda a=ca: L.eagle3_moe_combine(ctypes.byref(a), st)))
+
     def _fold_weights(self):
         """Weights with the RMSNorm weight folded in, W' = W diag(g), made once (bf16 of the fp32
         product); a norm weight of all ones leaves W itself."""
@@ -296,9 +362,10 @@ class SpeculativeStep:
             if bool(torch.all(g == 1)):
                 return w
             return (w.float() * g.float()[None, :]).to(torch.bfloat16).contiguous()
+        dense = lambda name: [None if T[name][l].dim() == 3 else fold(T[name][l], T["norm2"][l])
+                              for l in range(c["layers"])]
         return {"wqkv": [fold(T["wqkv"][l], T["norm1"][l]) for l in range(c["layers"])],
-                "wg": [fold(T["wg"][l], T["norm2"][l]) for l in range(c["layers"])],
-                "wu": [fold(T["wu"][l], T["norm2"][l]) for l in range(c["layers"])],
+                "wg": dense("wg"), "wu": dense("wu"),
                 "lm_head": fold(T["lm_head"], T["final_norm"])}
 
     # ------------------------------------------------------------------------------ issue
@@ -331,7 +398,10 @@ class SpeculativeStep:
         Vd = V if self.d2t is None else int(self.d2t.numel())
         R = c["B"] * c["N"]
         per_layer = 2 * R * (d * qw + Hq * D * d + 2 * d * F + F * d)
-        target = c["layers"] * per_layer + 2 * (R if head_rows is None else head_rows) * d * V
+        target = c["layers"] * per_layer
+        for E, Fe in self.moe_layers.values():   # the router and experts_per_token of the experts instead
+            target += 2 * R * (d * E + int(c["experts_per_token"]) * 3 * d * Fe - 3 * d * F)
+        target += 2 * (R if head_rows is None else head_rows) * d * V
         rows_d = c["B"] * c["top_k"]
         draft_layer = lambda m: 2 * m * (2 * d * qw + Hq * D * d + 2 * d * F + F * d)
         tc_rows = c["B"] if catchup_rows is None else catchup_rows

@@ -33,6 +33,7 @@ import math
 
 import numpy as np
 
+from . import moe
 from .accept import accept_greedy, argmax
 from .attention import ROPE_THETA, rope_apply
 from .tree import anc_bits, depths
@@ -110,6 +111,7 @@ class Llama:
                  aux_layers=()):
         self.w, self.L, self.H, self.KVH, self.D = w, n_layers, n_heads, n_kv_heads, head_dim
         self.eps, self.theta, self.aux_layers = eps, theta, tuple(aux_layers)
+        self.moe = {}   # oracle.moe.route's arguments (k, ...) for layers with a router
 
     def new_cache(self):
         return KV(self.L)
@@ -136,9 +138,18 @@ class Llama:
             o = _attend_rows(q, k, v, cache.k[l], cache.v[l], visible, self.KVH, scale)
             x = x + _rows(w[p + "wo"], o.reshape(T, -1))
             h = rmsnorm(x, w[p + "mlp_norm"], self.eps)
-            x = x + _rows(w[p + "w_down"], silu(_rows(w[p + "w_gate"], h)) * _rows(w[p + "w_up"], h))
+            x = x + self.mlp(p, h)
         logits = _rows(w["lm_head"], rmsnorm(x, w["final_norm"], self.eps))
         return logits, (np.concatenate(aux, -1) if aux else None), new_k, new_v
+
+    def mlp(self, p, h):
+        """SwiGLU; with a router among the layer's weights, a mixture of experts (oracle.moe)."""
+        w = self.w
+        if p + "router" not in w:
+            return _rows(w[p + "w_down"], silu(_rows(w[p + "w_gate"], h)) * _rows(w[p + "w_up"], h))
+        ids, weights, offsets, rows, slots = moe.route(_rows(w[p + "router"], h), **self.moe)
+        act = moe.grouped_linear(h, w[p + "w_gate"], offsets, rows, w[p + "w_up"])[0]
+        return moe.combine(moe.grouped_linear(act, w[p + "w_down"], offsets)[0], slots, weights)[0]
 
     def commit(self, cache, new_k, new_v, rows):
         for l in range(self.L):
