@@ -505,21 +505,6 @@ constexpr int NARROW_SMEM = 1024 + NARROW_RING + (int)sizeof(NarrowShared);
 static_assert(2 * (NARROW_SMEM + 1024) <= 228 * 1024, "two CTAs a SM");
 static_assert(NARROW_RING >= NARROW_MAX * BM * 4, "the ranks' sums fit the ring");
 
-E3_DEV void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;\n" ::: "memory");
-}
-// this CTA's shared-memory address in CTA `rank` of the cluster, and a load from there
-E3_DEV uint32_t cluster_addr(uint32_t addr, int rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
-    return r;
-}
-E3_DEV float cluster_ld(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v) : "r"(addr) : "memory");
-    return v;
-}
-
 // NT: row capacity of a tile (TMEM buffers of NT columns, NT / 2 accumulators a thread).
 // Grid: (cluster ranks = k ranges, weight tiles, row tiles).
 template <int NT, bool SWIGLU>
@@ -729,7 +714,7 @@ __global__ void __launch_bounds__(NARROW_THREADS, 2)
     }
     if (ranks > 1) {
         __syncwarp();
-        cluster_sync();
+        tc::cluster_sync();
     }
     // rows rank, rank + ranks, ...: the ranks' sums in rank order, the epilogue, the output
     const uint32_t base = smem_u32(ring);
@@ -741,9 +726,9 @@ __global__ void __launch_bounds__(NARROW_THREADS, 2)
         const uint32_t addr = base + (uint32_t)(r * BM + at) * 4u;
         float y = 0.0f, y2 = 0.0f;
         for (int s = 0; s < ranks; ++s) {
-            const uint32_t from = ranks > 1 ? cluster_addr(addr, s) : addr;
-            y += cluster_ld(from);
-            if (SWIGLU) y2 += cluster_ld(from + 64u);
+            const uint32_t from = ranks > 1 ? tc::cluster_addr(addr, s) : addr;
+            y += tc::cluster_ld(from);
+            if (SWIGLU) y2 += tc::cluster_ld(from + 64u);
         }
         const int col = mt * OUT + j;
         if (col >= p.n) continue;
@@ -758,7 +743,7 @@ __global__ void __launch_bounds__(NARROW_THREADS, 2)
     }
     if (ranks > 1) {
         __syncwarp();
-        cluster_sync();   // no rank leaves while another reads its sums
+        tc::cluster_sync();   // no rank leaves while another reads its sums
     }
 }
 

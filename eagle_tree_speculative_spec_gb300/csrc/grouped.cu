@@ -8,12 +8,13 @@
 // of any size then wastes at most 15 columns of its last tile, and a group of one row costs its
 // weights' traffic and little else.
 //
-// Persistent, warp-specialised, one CTA per SM; every CTA reads the offsets, and derives the tiles by
-// a prefix sum over the groups:
+// Persistent, warp-specialised, one CTA per SM, two CTAs on one tile (PAIR, below) but for few weight rows;
+// every CTA reads the offsets, and derives the tiles by a prefix sum over the groups:
 //   warp 0      TMA producer: the weight tile (SwiGLU: 64 gate and 64 up rows), and the rows unless they
 //               are gathered, by at most three boxes (a box costs about 70 cycles whatever its size:
-//               boxes of 16 rows held a 3840-row product to 835 TFLOP/s)
-//   warp 1      TMEM owner; one lane issues tcgen05.mma (M = 128, N = rows of the tile, K = 16)
+//               boxes of 16 rows held a 3840 x 8192 x 4096 product to 835 TFLOP/s; it runs at 1860)
+//   warp 1      TMEM owner; one lane issues tcgen05.mma (M = 128, or 256 for the pair, N = rows of the
+//               tile, K = 16)
 //   warps 2..5  epilogue: tcgen05.ld, SwiGLU, stores of two columns a lane.  TMEM lanes 0..63 hold gate
 //               columns and 64..127 their up columns: two warps that share columns swap them through
 //               shared memory, and each finishes half of the rows
@@ -80,17 +81,25 @@ struct GroupedParams {
 };
 
 // Row tiles of a group of cnt rows, and the rows of each but the last: even shares (in multiples of
-// 16) of up to 8 tiles, whole tiles of 256 for larger groups.  (t <= 8 shares leave rows for the last:
-// they pass cnt / t by less than 16 each, 16 (t - 1) in all, and cnt / t > 256 (t - 1) / t >= 32 (t - 1).)
+// STEP: 16, or 32 for a pair of CTAs, which takes half each) of up to 8 tiles, whole tiles of 256 for
+// larger groups.  (t <= 8 shares leave rows for the last: they pass cnt / t by less than 32 each,
+// 31 (t - 1) in all, and cnt / t > 256 (t - 1) / t >= 32 (t - 1).)
 E3_DEV int row_tiles(int cnt) { return (cnt + MAX_ROWS - 1) / MAX_ROWS; }
+template <int STEP>
+E3_DEV int round_rows(int rows) {
+    return (rows + STEP - 1) / STEP * STEP;
+}
+template <int STEP>
 E3_DEV int tile_rows(int cnt, int tiles) {
-    return tiles > 8 ? MAX_ROWS : ((cnt + tiles - 1) / tiles + 15) / 16 * 16;
+    return tiles > 8 ? MAX_ROWS : round_rows<STEP>((cnt + tiles - 1) / tiles);
 }
 
+// Weight tile mt (of both CTAs of a pair) of group e by rows [row0, row0 + rows), the MMA's N = n16.
 struct Unit {
     int e, mt, row0, rows, n16;
 };
 
+template <int STEP>
 E3_DEV Unit unit_at(const Shared &sh, const GroupedParams &p, int u) {
     const int q = u / p.tiles_w;
     int lo = 0, hi = p.E;   // tiles[lo] <= q < tiles[hi]
@@ -104,12 +113,12 @@ E3_DEV Unit unit_at(const Shared &sh, const GroupedParams &p, int u) {
     Unit w;
     w.e = lo;
     const int tiles = sh.tiles[lo + 1] - sh.tiles[lo], local = u - sh.tiles[lo] * p.tiles_w;
-    const int cnt = sh.offsets[lo + 1] - sh.offsets[lo], per = tile_rows(cnt, tiles);
+    const int cnt = sh.offsets[lo + 1] - sh.offsets[lo], per = tile_rows<STEP>(cnt, tiles);
     const int rt = local % tiles;
     w.mt = local / tiles;
     w.row0 = sh.offsets[lo] + rt * per;
     w.rows = min(per, cnt - rt * per);
-    w.n16 = (w.rows + 15) / 16 * 16;
+    w.n16 = round_rows<STEP>(w.rows);
     return w;
 }
 
@@ -150,7 +159,13 @@ E3_DEV void store_pair(const GroupedParams &p, int row, int col, float a, float 
     }
 }
 
-template <bool SWIGLU, bool GATHER>
+// PAIR: two CTAs of a cluster work on one unit, 256 weight rows (128 each) by up to 256 rows (half loaded by
+// each), with MMAs that the even CTA issues for both.  Each SM's shared memory then takes 32 KB of loads and
+// 32 KB of operand reads a k-block in place of 48 and 48, which at 128 bytes a cycle are 512 cycles, the MMAs'
+// own time, in place of 750 (3840 rows x 8 of 64 experts, k = 4096, 2 x 1024 columns: 377 -> 325 us, 1586
+// TFLOP/s; k = 1024, 4096 columns: 206 -> 179 us).  The odd CTA's stages are announced to the even one by a
+// thread that waits for them and arrives on its barrier; commits go to the barriers of both.
+template <bool SWIGLU, bool GATHER, bool PAIR>
 __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1)
     grouped_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ CUtensorMap tm_w,
                    const __grid_constant__ CUtensorMap tm_w2, const GroupedParams p) {
@@ -159,15 +174,19 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
     Shared &sh = *reinterpret_cast<Shared *>(ring + RING_BYTES);
     const uint32_t tid = tc::thread_index();
     const int warp = (int)(tid >> 5), lane = (int)(tid & 31u);
+    constexpr int STEP = PAIR ? 32 : 16;
+    const int rank = PAIR ? (int)(blockIdx.x & 1u) : 0;   // in the pair (a cluster of two)
+    const int unit0 = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x, unit_step = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < MAX_STAGES; ++s) {
-            tc::mbar_init(&sh.full[s], GATHER ? 1 + 32 * GATHER_WARPS : 1);
+            // the load's arrival, the gathering threads', and in the even CTA of a pair the odd one's
+            tc::mbar_init(&sh.full[s], 1 + (GATHER ? 32 * GATHER_WARPS : 0) + (PAIR && rank == 0 ? 1 : 0));
             tc::mbar_init(&sh.empty[s], 1);
         }
         for (int a = 0; a < 2; ++a) {
             tc::mbar_init(&sh.tfull[a], 1);
-            tc::mbar_init(&sh.tempty[a], 4);
+            tc::mbar_init(&sh.tempty[a], PAIR ? 8 : 4);
         }
         tc::mbar_init(&sh.mma_done, 1);
         sh.abort = 0;
@@ -181,9 +200,19 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
         tc::prefetch_tmap(&tm_w);
         if (SWIGLU) tc::prefetch_tmap(&tm_w2);
     }
-    if (warp == 1) tc::tmem_alloc(&sh.tmem_base, TMEM_COLS);
+    if (warp == 1) {
+        if (PAIR)
+            tc::tmem2_alloc(&sh.tmem_base, TMEM_COLS);
+        else
+            tc::tmem_alloc(&sh.tmem_base, TMEM_COLS);
+    }
     tc::fence_before();
-    __syncthreads();
+    if (PAIR) {
+        __syncwarp();
+        tc::cluster_sync();
+    } else {
+        __syncthreads();
+    }
     tc::fence_after();
     const uint32_t tmem = sh.tmem_base;
     pdl_wait();   // the previous kernel's outputs: offsets, row ids, rows
@@ -199,8 +228,8 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
         if (b > a) {
             const int tiles = row_tiles(b - a);
             sh.tiles[e] = tiles;
-            const int n16 = tile_rows(b - a, tiles);   // box_rows never decreases: the last tile needs no more
-            atomicMax(&sh.max_rows, GATHER ? n16 : box_rows(n16));
+            const int rows = tile_rows<STEP>(b - a, tiles) / (PAIR ? 2 : 1);   // of this CTA
+            atomicMax(&sh.max_rows, GATHER ? rows : box_rows(rows));   // box_rows never decreases: the last tile needs no more
         } else {
             sh.tiles[e] = 0;
         }
@@ -237,9 +266,10 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
             int stage = 0;
             uint32_t phase = 0, last_parity = 0, issued = 0;   // parity of the last load per stage
             bool ok = true;
-            for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-                const Unit w = unit_at(sh, p, u);
-                const int boxes = box_rows(w.n16);
+            for (int u = unit0; ok && u < units; u += unit_step) {
+                const Unit w = unit_at<STEP>(sh, p, u);
+                const int mine = w.n16 / (PAIR ? 2 : 1), boxes = box_rows(mine);   // rows that this CTA loads
+                const int row0 = w.row0 + rank * mine, mt = PAIR ? 2 * w.mt + rank : w.mt;
                 for (int kb = 0; kb < p.kb_total; ++kb) {
                     const uint32_t full = full0 + stage * 8;
                     if (!tc::mbar_wait(empty0 + stage * 8, phase ^ 1u, abort0)) {
@@ -252,19 +282,19 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
                     const uint32_t sw = ring0 + stage * stage_bytes, sx = sw + W_BYTES;
                     const int x = kb * BK;
                     if (SWIGLU) {
-                        tc::tma_load_3d(sw, &tm_w, x, w.mt * (BM / 2), w.e, full);
-                        tc::tma_load_3d(sw + W_BYTES / 2, &tm_w2, x, w.mt * (BM / 2), w.e, full);
+                        tc::tma_load_3d(sw, &tm_w, x, mt * (BM / 2), w.e, full);
+                        tc::tma_load_3d(sw + W_BYTES / 2, &tm_w2, x, mt * (BM / 2), w.e, full);
                     } else {
-                        tc::tma_load_3d(sw, &tm_w, x, w.mt * BM, w.e, full);
+                        tc::tma_load_3d(sw, &tm_w, x, mt * BM, w.e, full);
                     }
                     if (!GATHER) {
                         if (boxes == 256) {
-                            tc::tma_load_2d(sx, &tm_x.b256, x, w.row0, full);
+                            tc::tma_load_2d(sx, &tm_x.b256, x, row0, full);
                         } else {
                             int r = 0;
                             for (; r + 64 <= boxes; r += 64)
-                                tc::tma_load_2d(sx + r * ROW_BYTES, &tm_x.b64, x, w.row0 + r, full);
-                            if (r < boxes) tc::tma_load_2d(sx + r * ROW_BYTES, &tm_x.b16, x, w.row0 + r, full);
+                                tc::tma_load_2d(sx + r * ROW_BYTES, &tm_x.b64, x, row0 + r, full);
+                            if (r < boxes) tc::tma_load_2d(sx + r * ROW_BYTES, &tm_x.b16, x, row0 + r, full);
                         }
                     }
                     if (++stage == stages) {
@@ -282,14 +312,36 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------------ MMA issuer
-        if (tc::elect_one()) {
+        if (PAIR && rank == 1) {
+            // the odd CTA: its stages to the even one's barriers
+            if (tc::elect_one()) {
+                const uint32_t even = tc::cluster_addr(full0, 0);
+                int stage = 0;
+                uint32_t phase = 0;
+                bool ok = true;
+                for (int u = unit0; ok && u < units; u += unit_step)
+                    for (int kb = 0; kb < p.kb_total; ++kb) {
+                        if (!tc::mbar_wait(full0 + stage * 8, phase, abort0)) {
+                            ok = false;
+                            break;
+                        }
+                        if (GATHER) tc::fence_proxy_async_smem();   // the copies were made outside the async proxy
+                        tc::mbar_arrive_cluster_if(even + stage * 8, true);
+                        if (++stage == stages) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                if (!ok) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
+            }
+        } else if (tc::elect_one()) {
             const uint64_t desc0 = tc::desc_sw128(ring0);
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true;
-            for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-                const Unit w = unit_at(sh, p, u);
-                const uint32_t idesc = tc::idesc_bf16(BM, w.n16);
+            for (int u = unit0; ok && u < units; u += unit_step) {
+                const Unit w = unit_at<STEP>(sh, p, u);
+                const uint32_t idesc = tc::idesc_bf16(PAIR ? 2 * BM : BM, w.n16);
                 if (!tc::mbar_wait(tempty0 + acc * 8, acc_phase ^ 1u, abort0)) {
                     ok = false;
                     break;
@@ -306,22 +358,36 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
                     // (descriptors count 16 bytes)
                     const uint64_t a = desc0 + (uint32_t)(stage * stage_bytes >> 4), b = a + (W_BYTES >> 4);
 #pragma unroll
-                    for (int k = 0; k < BK / 16; ++k)
-                        tc::mma_bf16_ss(d, a + k * 2, b + k * 2, idesc, (kb > 0 || k > 0) ? 1u : 0u);
-                    tc::mma_commit(empty0 + stage * 8);
+                    for (int k = 0; k < BK / 16; ++k) {
+                        const uint32_t add = kb > 0 || k > 0 ? 1u : 0u;
+                        if (PAIR)
+                            tc::mma2_bf16_ss(d, a + k * 2, b + k * 2, idesc, add);
+                        else
+                            tc::mma_bf16_ss(d, a + k * 2, b + k * 2, idesc, add);
+                    }
+                    if (PAIR)
+                        tc::mma2_commit(empty0 + stage * 8, 3);
+                    else
+                        tc::mma_commit(empty0 + stage * 8);
                     if (++stage == stages) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
                 if (!ok) break;
-                tc::mma_commit(tfull0 + acc * 8);
+                if (PAIR)
+                    tc::mma2_commit(tfull0 + acc * 8, 3);
+                else
+                    tc::mma_commit(tfull0 + acc * 8);
                 acc_phase ^= (uint32_t)acc;
                 acc ^= 1;
             }
             if (!ok) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
             // every MMA this thread issued must retire before TMEM is freed (bounded wait)
-            tc::mma_commit(smem_u32(&sh.mma_done));
+            if (PAIR)
+                tc::mma2_commit(smem_u32(&sh.mma_done), 1);
+            else
+                tc::mma_commit(smem_u32(&sh.mma_done));
             tc::mbar_drain(smem_u32(&sh.mma_done), 0);
         }
         __syncwarp();
@@ -334,14 +400,16 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-            const Unit w = unit_at(sh, p, u);
-            const __nv_bfloat16 *src[MAX_ROWS / GATHER_ROWS];
+        for (int u = unit0; ok && u < units; u += unit_step) {
+            const Unit w = unit_at<STEP>(sh, p, u);
+            constexpr int PASSES = MAX_ROWS / (PAIR ? 2 : 1) / GATHER_ROWS;
+            const int mine = w.n16 / (PAIR ? 2 : 1), from = rank * mine + first;   // rows that this CTA copies
+            const __nv_bfloat16 *src[PASSES];
 #pragma unroll
-            for (int i = 0; i < MAX_ROWS / GATHER_ROWS; ++i) {
-                if (GATHER_ROWS * i >= w.n16) continue;
+            for (int i = 0; i < PASSES; ++i) {
+                if (GATHER_ROWS * i >= mine) continue;
                 // rows past the tile's last repeat it
-                int v = __ldg(p.row_ids + w.row0 + min(first + GATHER_ROWS * i, w.rows - 1));
+                int v = __ldg(p.row_ids + w.row0 + min(from + GATHER_ROWS * i, w.rows - 1));
                 if (v < 0 || v >= p.n_src) {
                     flag(p.dev_status, EAGLE3_DEV_BAD_COUNTS);
                     v = 0;
@@ -357,8 +425,8 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
                 const bool past = kb * BK + piece * 8 >= p.k;   // k is a multiple of 8
                 const int at = past ? 0 : kb * BK;
 #pragma unroll
-                for (int i = 0; i < MAX_ROWS / GATHER_ROWS; ++i)
-                    if (first + GATHER_ROWS * i < w.n16) copy16(dst + i * GATHER_ROWS * ROW_BYTES, src[i] + at, past);
+                for (int i = 0; i < PASSES; ++i)
+                    if (first + GATHER_ROWS * i < mine) copy16(dst + i * GATHER_ROWS * ROW_BYTES, src[i] + at, past);
                 copies_arrive(full0 + stage * 8);
                 if (++stage == stages) {
                     stage = 0;
@@ -371,10 +439,11 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
     } else {
         // ------------------------------------------------------------------ epilogue (warps 2..5)
         const int quarter = warp & 3;   // TMEM lanes 32 * quarter .. + 31
+        const uint32_t tempty_even = PAIR ? tc::cluster_addr(tempty0, 0) : tempty0;
         int acc = 0;
         uint32_t acc_phase = 0;
-        for (int u = blockIdx.x; u < units; u += gridDim.x) {
-            const Unit w = unit_at(sh, p, u);
+        for (int u = unit0; u < units; u += unit_step) {
+            const Unit w = unit_at<STEP>(sh, p, u);
             bool ok = tc::mbar_wait_warp(tfull0 + acc * 8, acc_phase, abort0);
             // (the two warps of a pair go on or leave together: they meet at barriers below)
             if (SWIGLU) ok = pair_all(1 + (quarter & 1), ok);
@@ -385,6 +454,7 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
             tc::fence_after();
             const uint32_t t_col = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * MAX_ROWS);
             const bool odd = lane & 1;
+            const int mt = PAIR ? 2 * w.mt + rank : w.mt;
             // rows r, r + 1, ... of this lane's column: an even lane stores both columns of row r, its
             // odd neighbour those of row r + 1
             auto store32 = [&](float (&v)[32], int r0, int col) {
@@ -409,7 +479,7 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
             };
             if (SWIGLU) {
                 const int pair = quarter & 1, up = quarter >> 1;
-                const int col = w.mt * (BM / 2) + pair * 32 + (lane & ~1);
+                const int col = mt * (BM / 2) + pair * 32 + (lane & ~1);
                 for (int c = 0; c < w.n16; c += 64) {   // the gate warp takes rows c.., the up warp c + 32..
                     const int mine = c + 32 * up, theirs = c + 32 * (up ^ 1);
                     float v[32];
@@ -432,7 +502,7 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
                     pair_sync(1 + pair);   // both have read before the next rows overwrite
                 }
             } else {
-                const int col = w.mt * BM + quarter * 32 + (lane & ~1);
+                const int col = mt * BM + quarter * 32 + (lane & ~1);
                 for (int c = 0; c < w.n16; c += 32) {
                     float v[32];
                     tc::tmem_ld32(t_col + c, v);
@@ -441,7 +511,10 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
             }
             tc::fence_before();
             __syncwarp();
-            tc::mbar_arrive_if(tempty0 + acc * 8, lane == 0);
+            if (PAIR)
+                tc::mbar_arrive_cluster_if(tempty_even + acc * 8, lane == 0);
+            else
+                tc::mbar_arrive_if(tempty0 + acc * 8, lane == 0);
             acc_phase ^= (uint32_t)acc;
             acc ^= 1;
         }
@@ -449,11 +522,19 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
     }
 
     tc::fence_before();
-    __syncthreads();
+    if (PAIR) {   // no CTA leaves while the other may arrive on its barriers or multiply into its TMEM
+        __syncwarp();
+        tc::cluster_sync();
+    } else {
+        __syncthreads();
+    }
     if (warp == 1) {
         __syncwarp();
         tc::fence_after();
-        tc::tmem_dealloc(tmem, TMEM_COLS);
+        if (PAIR)
+            tc::tmem2_dealloc(tmem, TMEM_COLS);
+        else
+            tc::tmem_dealloc(tmem, TMEM_COLS);
     }
 }
 
@@ -479,16 +560,58 @@ eagle3_status_t validate(const eagle3_grouped_linear_args_t *a) {
     return EAGLE3_OK;
 }
 
-template <bool SWIGLU, bool GATHER>
-cudaError_t launch_grouped(int grid, cudaStream_t st, const RowMaps &tx, const CUtensorMap &tw,
+// CTAs, or pairs of them, that the device holds at once: a GPC with an odd number of SMs leaves one without a
+// partner.
+template <bool SWIGLU, bool GATHER, bool PAIR>
+int resident() {
+    if (cudaFuncSetAttribute(grouped_kernel<SWIGLU, GATHER, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) !=
+        cudaSuccess)
+        return 0;
+    if (!PAIR) return device_sm_count();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * device_sm_count());
+    cfg.blockDim = dim3(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0));
+    cfg.dynamicSmemBytes = SMEM;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = 2;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    return cudaOccupancyMaxActiveClusters(&n, grouped_kernel<SWIGLU, GATHER, PAIR>, &cfg) == cudaSuccess ? n : 0;
+}
+
+// units: an upper bound on the call's units
+template <bool SWIGLU, bool GATHER, bool PAIR>
+cudaError_t launch_grouped(int64_t units, cudaStream_t st, const RowMaps &tx, const CUtensorMap &tw,
                            const CUtensorMap &tw2, const GroupedParams &p) {
-    static PerDevice<cudaError_t> attr;
-    const cudaError_t e = attr.get([] {
-        return cudaFuncSetAttribute(grouped_kernel<SWIGLU, GATHER>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-    });
-    if (e != cudaSuccess) return e;
-    return launch_pdl(grouped_kernel<SWIGLU, GATHER>, dim3(grid), dim3(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0)), SMEM,
-                      st, tx, tw, tw2, p);
+    static PerDevice<int> cache;
+    const int most = cache.get(resident<SWIGLU, GATHER, PAIR>);
+    if (most < 1) return cudaErrorUnknown;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>(most, units) * (PAIR ? 2 : 1));
+    cfg.blockDim = dim3(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0));
+    cfg.dynamicSmemBytes = SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = 2;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = PAIR ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, grouped_kernel<SWIGLU, GATHER, PAIR>, tx, tw, tw2, p);
+}
+
+template <bool PAIR>
+cudaError_t launch_grouped(bool swiglu, bool gather, int64_t units, cudaStream_t st, const RowMaps &tx,
+                           const CUtensorMap &tw, const CUtensorMap &tw2, const GroupedParams &p) {
+    return swiglu ? (gather ? launch_grouped<true, true, PAIR>(units, st, tx, tw, tw2, p)
+                            : launch_grouped<true, false, PAIR>(units, st, tx, tw, tw2, p))
+                  : (gather ? launch_grouped<false, true, PAIR>(units, st, tx, tw, tw2, p)
+                            : launch_grouped<false, false, PAIR>(units, st, tx, tw, tw2, p));
 }
 
 }  // namespace
@@ -529,14 +652,16 @@ extern "C" eagle3_status_t eagle3_grouped_linear(const eagle3_grouped_linear_arg
     p.row_ids = a->row_ids;
     p.dev_status = a->dev_status;
     p.paired = p.ld_out % 2 == 0 && ((uintptr_t)a->out & 3) == 0;
-    const int sms = device_sm_count();
-    const int64_t most = (int64_t)p.tiles_w * (a->m / MAX_ROWS + std::min(a->m, a->n_groups));
-    const int grid = (int)std::min<int64_t>(sms > 0 ? sms : 1, most);
+    // Pairs of CTAs, unless the last pair's odd CTA would be without weight rows and that is more than a
+    // sixth of the work: one tile of weight rows (2048 rows x 8 of 64 experts, k = 4096, 128 columns) takes
+    // 33 us by single CTAs and 53 us by pairs, three tiles 68 and 74 us, 16 tiles (3840 rows, 2 x 1024
+    // columns) 377 and 325 us.  With few rows, where the weights' bytes bound the call, both are alike.
+    const bool pair = p.tiles_w % 2 == 0 || p.tiles_w >= 5;
+    if (pair) p.tiles_w = (p.tiles_w + 1) / 2;
+    const int64_t units = (int64_t)p.tiles_w * (a->m / MAX_ROWS + std::min(a->m, a->n_groups));
     const cudaStream_t s = (cudaStream_t)stream;
     const bool gather = a->row_ids != nullptr;
-    const cudaError_t e = swiglu ? (gather ? launch_grouped<true, true>(grid, s, tx, tw, tw2, p)
-                                           : launch_grouped<true, false>(grid, s, tx, tw, tw2, p))
-                                 : (gather ? launch_grouped<false, true>(grid, s, tx, tw, tw2, p)
-                                           : launch_grouped<false, false>(grid, s, tx, tw, tw2, p));
+    const cudaError_t e = pair ? launch_grouped<true>(swiglu, gather, units, s, tx, tw, tw2, p)
+                               : launch_grouped<false>(swiglu, gather, units, s, tx, tw, tw2, p);
     return e == cudaSuccess ? EAGLE3_OK : EAGLE3_ERR_CUDA;
 }

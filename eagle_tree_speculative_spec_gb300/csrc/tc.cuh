@@ -47,7 +47,7 @@ E3_DEV bool mbar_wait(uint64_t *bar, uint32_t parity, volatile int *abort, long 
 // The same by shared-memory address (computed once) and by whole warps, for loops that are short of issue
 // slots and registers: a poll is a handful of instructions, every lane gets the same answer, and the bound
 // is a number of polls (at least 20 cycles each: MAX_POLLS are seconds, as WAIT_LIMIT_CYCLES).
-constexpr uint32_t MAX_POLLS = 1u << 27;
+constexpr uint32_t MAX_POLLS = 1u << 25;
 E3_DEV bool mbar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -100,6 +100,32 @@ E3_DEV void mbar_arrive_if(uint32_t bar, bool one) {
 }
 E3_DEV void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+// ---- clusters: barriers and addresses of the other CTAs ---------------------------------------------
+E3_DEV void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;\n" ::: "memory");
+}
+// this CTA's shared-memory address in CTA `rank` of the cluster, and a load from there
+E3_DEV uint32_t cluster_addr(uint32_t addr, int rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+E3_DEV float cluster_ld(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+// Arrive on a barrier anywhere in the cluster (cluster_addr) by the lanes for which `one` holds.  The
+// default order is enough for what it announces here: loads that another barrier has shown to have landed
+// (or copies behind a proxy fence) and TMEM reads that have been waited for; there are no plain writes to
+// publish.  (.release.cluster flushes them all the same: a product of two-CTA tiles took 2.9 times as long.)
+E3_DEV void mbar_arrive_cluster_if(uint32_t bar, bool one) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n @p mbarrier.arrive.shared::cluster.b64 _, [%0];\n}\n" ::"r"(bar),
+        "r"(one ? 1u : 0u)
+        : "memory");
 }
 
 // ---- TMA -----------------------------------------------------------------------------------------
@@ -261,6 +287,31 @@ E3_DEV void mma_commit(uint64_t *bar) {
 }
 E3_DEV void mma_commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
+}
+// Two CTAs of a cluster on one tile (cta_group::2): issued by one thread of the even CTA, M = 256 (128 rows
+// of A and of the accumulator in each CTA), B's rows half in each; the same offsets in both.  The commit
+// arrives on the barrier at this offset in every CTA of the mask.
+E3_DEV void mma2_bf16_ss(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+E3_DEV void mma2_commit(uint32_t bar, uint16_t cta_mask) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(bar),
+        "h"(cta_mask)
+        : "memory");
+}
+// by one warp of each CTA of the pair
+E3_DEV void tmem2_alloc(uint32_t *dst_smem, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(dst_smem)), "r"(ncols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n" ::: "memory");
+}
+E3_DEV void tmem2_dealloc(uint32_t base, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(base), "r"(ncols) : "memory");
 }
 E3_DEV void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
 E3_DEV void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
