@@ -355,7 +355,8 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
         uint8_t *box = boxes + (warp - WIDE_EPI0) * WIDE_BOX;
         // this thread's two runs of accumulator columns: neighbours, or gate and up of one run
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        const uint32_t run_a = lanes + (SWIGLU ? WIDE_RUN : 2 * WIDE_RUN) * part, run_b = run_a + (SWIGLU ? 128 : WIDE_RUN);
+        const uint32_t run_a = lanes + (SWIGLU ? WIDE_RUN : 2 * WIDE_RUN) * part;
+        const uint32_t run_b = run_a + (SWIGLU ? 128 : WIDE_RUN);
         const int kb_total = p.kb_total;
         int stage = 0, buf = 0;
         uint32_t phase = 0;
@@ -519,7 +520,8 @@ __global__ void __launch_bounds__(NARROW_THREADS, 2)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int ranks = gridDim.x, rank = blockIdx.x, mt = blockIdx.y, row0 = blockIdx.z * p.n16;
     const int rows = min(p.n16, p.m - row0);
-    const int kb0 = (int)((long long)p.kb_total * rank / ranks), kb1 = (int)((long long)p.kb_total * (rank + 1) / ranks);
+    const int kb0 = (int)((long long)p.kb_total * rank / ranks);
+    const int kb1 = (int)((long long)p.kb_total * (rank + 1) / ranks);
     const int stage_bytes = NARROW_W + p.n16 * BK, stages = p.stages;
 
     if (threadIdx.x == 0) {
@@ -576,12 +578,14 @@ __global__ void __launch_bounds__(NARROW_THREADS, 2)
             if (SWIGLU) {
                 if (lane < 8) {   // 16 gate and 16 up rows for the lanes of each quarter
                     const int q = lane >> 1, up = lane & 1;
-                    tc::tma_load_2d(sw + lane * 16 * BK, up ? &tm_w2 : &tm_w, kb * BK, mt * 64 + q * 16, &sh.full[stage]);
+                    tc::tma_load_2d(sw + lane * 16 * BK, up ? &tm_w2 : &tm_w, kb * BK, mt * 64 + q * 16,
+                                    &sh.full[stage]);
                 }
             } else if (lane == 0) {
                 tc::tma_load_2d(sw, &tm_w, kb * BK, mt * BM, &sh.full[stage]);
             }
-            if (16 * lane < p.n16) tc::tma_load_2d(sx + lane * 16 * BK, &tm_x, kb * BK, row0 + lane * 16, &sh.full[stage]);
+            if (16 * lane < p.n16)
+                tc::tma_load_2d(sx + lane * 16 * BK, &tm_x, kb * BK, row0 + lane * 16, &sh.full[stage]);
             if (++stage == stages) {
                 stage = 0;
                 phase ^= 1u;
@@ -787,8 +791,8 @@ bool out_map(CUtensorMap *m, const eagle3_linear_fp8_args_t *a, int64_t ld) {
     const bool f32 = a->epilogue == EAGLE3_EPI_F32;
     const int es = f32 ? 4 : 2;
     if (((uintptr_t)a->out & 15) || (ld * es) % 16) return false;
-    return tmap_rows(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, es, a->out, a->m, a->n,
-                     ld, 32, 0, 0, 64);
+    const CUtensorMapDataType type = f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    return tmap_rows(m, type, es, a->out, a->m, a->n, ld, 32, 0, 0, 64);
 }
 
 template <int NT, bool SWIGLU>
@@ -902,9 +906,11 @@ extern "C" eagle3_status_t eagle3_linear_fp8(const eagle3_linear_fp8_args_t *a, 
             ++ranks;
         const dim3 grid(ranks, tiles_w, tiles_r);
         if (p.n16 <= 32)
-            e = swiglu ? launch_narrow<32, true>(grid, s, tx, tw, tw2, p) : launch_narrow<32, false>(grid, s, tx, tw, tw2, p);
+            e = swiglu ? launch_narrow<32, true>(grid, s, tx, tw, tw2, p)
+                       : launch_narrow<32, false>(grid, s, tx, tw, tw2, p);
         else if (p.n16 <= 64)
-            e = swiglu ? launch_narrow<64, true>(grid, s, tx, tw, tw2, p) : launch_narrow<64, false>(grid, s, tx, tw, tw2, p);
+            e = swiglu ? launch_narrow<64, true>(grid, s, tx, tw, tw2, p)
+                       : launch_narrow<64, false>(grid, s, tx, tw, tw2, p);
         else
             e = swiglu ? launch_narrow<128, true>(grid, s, tx, tw, tw2, p)
                        : launch_narrow<128, false>(grid, s, tx, tw, tw2, p);

@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
     const int warp = (int)(tid >> 5), lane = (int)(tid & 31u);
     constexpr int STEP = PAIR ? 32 : 16;
     const int rank = PAIR ? (int)(blockIdx.x & 1u) : 0;   // in the pair (a cluster of two)
-    const int unit0 = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x, unit_step = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
+    const int unit0 = (int)blockIdx.x >> (PAIR ? 1 : 0), unit_step = (int)gridDim.x >> (PAIR ? 1 : 0);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < MAX_STAGES; ++s) {
@@ -229,7 +229,8 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
             const int tiles = row_tiles(b - a);
             sh.tiles[e] = tiles;
             const int rows = tile_rows<STEP>(b - a, tiles) / (PAIR ? 2 : 1);   // of this CTA
-            atomicMax(&sh.max_rows, GATHER ? rows : box_rows(rows));   // box_rows never decreases: the last tile needs no more
+            // (box_rows never decreases: a group's last tile needs no more)
+            atomicMax(&sh.max_rows, GATHER ? rows : box_rows(rows));
         } else {
             sh.tiles[e] = 0;
         }

@@ -408,7 +408,8 @@ eagle3_status_t validate(const eagle3_moe_combine_args_t *a) {
     if (a->rows == 0) return EAGLE3_OK;
     if ((a->n_slots && !a->y) || !a->slots || !a->weights || !a->out) return EAGLE3_ERR_INVALID_ARGUMENT;
     if (((uintptr_t)a->y | (uintptr_t)a->residual | (uintptr_t)a->out) & 1) return EAGLE3_ERR_INVALID_ARGUMENT;
-    if (((uintptr_t)a->slots | (uintptr_t)a->weights | (uintptr_t)a->dev_status) & 3) return EAGLE3_ERR_INVALID_ARGUMENT;
+    if (((uintptr_t)a->slots | (uintptr_t)a->weights | (uintptr_t)a->dev_status) & 3)
+        return EAGLE3_ERR_INVALID_ARGUMENT;
     return EAGLE3_OK;
 }
 
@@ -444,7 +445,8 @@ extern "C" eagle3_status_t eagle3_moe_route(const eagle3_moe_route_args_t *a, vo
     const eagle3_status_t st = validate(a);
     if (st != EAGLE3_OK) return st;
     const RoutePlan pl = route_plan(a);
-    if (pl.ws_bytes && (!workspace || ws_bytes < pl.ws_bytes || ((uintptr_t)workspace & 15))) return EAGLE3_ERR_WORKSPACE;
+    if (pl.ws_bytes && (!workspace || ws_bytes < pl.ws_bytes || ((uintptr_t)workspace & 15)))
+        return EAGLE3_ERR_WORKSPACE;
     RouteParams p;
     p.rows = a->rows;
     p.E = a->n_experts;

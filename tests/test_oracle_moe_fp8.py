@@ -1,4 +1,6 @@
 """Pins of the oracle's mixture-of-experts and 8-bit functions (CPU only)."""
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -76,3 +78,38 @@ def test_layer_with_equal_experts_is_the_dense_layer():
         h = moe.grouped_linear(x, rep(wg), off, rows, rep(wu))[0]
         y = moe.grouped_linear(h, rep(wd), off)[0]
         np.testing.assert_allclose(moe.combine(y, slots, w, x)[0], dense, rtol=1e-12, atol=1e-12)
+
+
+# ----------------------------------------------------------------------------- quotients by correction
+def _rn(f):
+    """A Fraction to the nearest number of 24 significant bits, ties to even."""
+    if f == 0:
+        return f
+    sign, f = (-1 if f < 0 else 1), abs(f)
+    e = f.numerator.bit_length() - f.denominator.bit_length()
+    e -= Fraction(2) ** e > f
+    u = Fraction(2) ** (e - 23)
+    n, rest = divmod(f / u, 1)
+    n = int(n) + (rest > Fraction(1, 2) or (rest == Fraction(1, 2) and int(n) % 2 == 1))
+    return sign * n * u
+
+
+def test_corrected_quotients_are_correctly_rounded():
+    """What the quantisation kernel relies on: for every significand of a block's maximum and of a value,
+    scale, reciprocal and quotient by one correction step are the correctly rounded ones."""
+    y448 = _rn(Fraction(1, 448))
+    assert float(y448).hex() == "0x1.24924a0000000p-9"
+    for top in range(128, 256):
+        a = Fraction(top)
+        q0 = _rn(a * y448)
+        s = _rn(a / 448)
+        assert _rn(q0 + _rn(a - q0 * 448) * y448) == s
+        y = _rn(1 / s)
+        e = y.numerator.bit_length() - y.denominator.bit_length()
+        step = Fraction(2) ** (e - (Fraction(2) ** e > y) - 23)
+        for d in range(-3, 4):
+            y0 = y + d * step
+            assert _rn(y0 + y0 * _rn(1 - s * y0)) == y
+        for x in range(128, 256):
+            q0 = _rn(x * y)
+            assert _rn(q0 + _rn(x - q0 * s) * y) == _rn(x / s)
