@@ -12,10 +12,10 @@
 // tcgen05.mma (kind::f8f6f4, K = 32) and the other warps run the epilogue.
 //   wide     128 rows x 256 weight rows a tile, persistent.  Rows are the M side, so a thread owns one
 //            row and its scale is one number a k-block.
-//   narrow   128 weight rows (M side) x up to 128 rows (N side, any multiple of 16): few rows, bound by
-//            the weights' bytes.  The k-blocks of a tile are cut over a thread-block cluster so that
-//            the weights stream through all SMs; the ranks' sums meet in distributed shared memory and
-//            are added in rank order.
+//   narrow   128 weight rows (M side) x up to 64 rows (N side, any multiple of 16): few rows, bound by
+//            the weights' bytes.
+// Where the tiles do not fill the GPU, the k-blocks of a tile are cut over the CTAs of a thread-block
+// cluster; the ranks' sums meet in distributed shared memory and are added in rank order.
 //
 // Every mbarrier wait is bounded; on a timeout the kernel records EAGLE3_DEV_TIMEOUT, stops issuing
 // work, drains its own TMA loads and frees its TMEM.
@@ -45,6 +45,7 @@ struct Fp8Params {
     void *out;
     int32_t *dev_status;
     int tiles_m, tiles_n;   // wide: row tiles, column tiles
+    int ranks;              // wide: CTAs of a cluster, each a range of a tile's k-blocks (then one tile a cluster)
     int tma_out;            // wide: outputs leave through shared memory and TMA stores
     int n16, stages;        // narrow: rows of a tile (multiple of 16), ring depth
 };
@@ -196,14 +197,26 @@ E3_DEV uint4 pack8(const float *v) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 E3_DEV void store8(const Fp8Params &p, int row, int col, const float *v) {
+    const bool whole = col + 8 <= p.n;
     if (p.epi == EAGLE3_EPI_F32) {
         float *o = (float *)p.out + (size_t)row * p.ld_out + col;
-        for (int i = 0; i < 8; ++i)
-            if (col + i < p.n) o[i] = v[i];
+        if (whole && ((uintptr_t)o & 15) == 0) {
+            *reinterpret_cast<float4 *>(o) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4 *>(o + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (col + i < p.n) o[i] = v[i];
+        }
     } else {
         __nv_bfloat16 *o = (__nv_bfloat16 *)p.out + (size_t)row * p.ld_out + col;
-        for (int i = 0; i < 8; ++i)
-            if (col + i < p.n) o[i] = __float2bfloat16_rn(v[i]);
+        if (whole && ((uintptr_t)o & 15) == 0) {
+            *reinterpret_cast<uint4 *>(o) = pack8(v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (col + i < p.n) o[i] = __float2bfloat16_rn(v[i]);
+        }
     }
 }
 
@@ -217,6 +230,7 @@ E3_DEV void store8(const Fp8Params &p, int row, int col, const float *v) {
 // groups of 64 accumulators and 104 registers: 358 us.)
 constexpr int WIDE_BN = 256, WIDE_STAGES = 4, WIDE_EPI_WARPS = 8, WIDE_THREADS = 128 + 32 * WIDE_EPI_WARPS;
 constexpr int WIDE_EPI0 = 4;   // first epilogue warp
+constexpr int WIDE_RANKS = 8;  // largest cluster
 constexpr int WIDE_RUN = 512 / WIDE_EPI_WARPS;   // accumulator columns of a thread: two runs of this many
 constexpr int WIDE_A = BM * BK, WIDE_B = WIDE_BN * BK, WIDE_STAGE = WIDE_A + WIDE_B;
 constexpr int WIDE_BOX = 32 * 64;   // output staging: 32 rows x 64 bytes a warp
@@ -232,6 +246,15 @@ struct WideShared {
 constexpr int WIDE_SMEM = 1024 + WIDE_STAGES * WIDE_STAGE + WIDE_EPI_WARPS * WIDE_BOX + (int)sizeof(WideShared);
 static_assert(WIDE_SMEM <= 232448, "shared memory budget");
 
+
+// SPLIT: where rank src's sums of piece j (8 columns of each run, 128 rows) of an epilogue half lie in the ring
+// of the rank that the piece belongs to, j % ranks; byte offset of a row's first value.
+__host__ __device__ constexpr int split_pieces(int ranks) { return (WIDE_RUN / 8 + ranks - 1) / ranks; }
+__host__ __device__ constexpr int split_bytes(int ranks) { return ranks * 2 * split_pieces(ranks) * 16 * BM * 4; }
+E3_DEV uint32_t split_offset(int ranks, int src, int part, int j, int row) {
+    return (uint32_t)((((src * 2 + part) * split_pieces(ranks) + j / ranks) * 16 * BM + row) * 4);
+}
+
 template <int N>
 E3_DEV void registers_give() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
@@ -241,7 +264,10 @@ E3_DEV void registers_take() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
 }
 
-template <bool SWIGLU>
+// SPLIT: a cluster of p.ranks CTAs works on one tile, each on a range of the k-blocks.  Pieces of 8 columns of
+// both runs belong to the ranks in turn: each rank sends the others their pieces of its sums by remote stores
+// (reading them took three times as long), and adds up and finishes its own.
+template <bool SWIGLU, bool SPLIT>
 __global__ void __launch_bounds__(WIDE_THREADS, 1)
     fp8_wide_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                     const __grid_constant__ CUtensorMap tm_w2, const __grid_constant__ CUtensorMap tm_out,
@@ -275,6 +301,10 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
     const int units = p.tiles_m * p.tiles_n;
     const uint32_t ring0 = smem_u32(ring), full0 = smem_u32(sh.full), done0 = smem_u32(sh.done);
     const uint32_t abort0 = smem_u32(&sh.abort);
+    const int ranks = SPLIT ? p.ranks : 1, rank = SPLIT ? (int)blockIdx.x % ranks : 0;
+    const int unit0 = SPLIT ? (int)blockIdx.x / ranks : (int)blockIdx.x, unit_step = SPLIT ? units : (int)gridDim.x;
+    const int kb0 = SPLIT ? (int)((long long)p.kb_total * rank / ranks) : 0;
+    const int kb1 = SPLIT ? (int)((long long)p.kb_total * (rank + 1) / ranks) : p.kb_total;
 
     if (warp < WIDE_EPI0) {
         registers_give<56>();
@@ -284,9 +314,9 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                 int stage = 0;
                 uint32_t phase = 0, last_parity = 0, issued = 0;
                 bool ok = true;
-                for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+                for (int u = unit0; ok && u < units; u += unit_step) {
                     const int mb = u % p.tiles_m, nb = u / p.tiles_m;
-                    for (int kb = 0; kb < p.kb_total; ++kb) {
+                    for (int kb = kb0; kb < kb1; ++kb) {
                         if (!tc::mbar_wait(done0 + stage * 8, phase ^ 1u, abort0)) {
                             ok = false;
                             break;
@@ -322,8 +352,8 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                 int stage = 0, buf = 0;
                 uint32_t phase = 0;
                 bool ok = true;
-                for (int u = blockIdx.x; ok && u < units; u += gridDim.x)
-                    for (int kb = 0; kb < p.kb_total; ++kb) {
+                for (int u = unit0; ok && u < units; u += unit_step)
+                    for (int kb = kb0; kb < kb1; ++kb) {
                         if (!tc::mbar_wait(full0 + stage * 8, phase, abort0)) {
                             ok = false;
                             break;
@@ -348,6 +378,10 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
             }
             __syncwarp();
         }
+        if (SPLIT) {   // (the epilogue's two)
+            tc::cluster_sync();
+            tc::cluster_sync();
+        }
     } else {
         registers_take<224>();
         // ------------------------------------------------------------------ epilogue (warps 4..11)
@@ -357,7 +391,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         const uint32_t run_a = lanes + (SWIGLU ? WIDE_RUN : 2 * WIDE_RUN) * part;
         const uint32_t run_b = run_a + (SWIGLU ? 128 : WIDE_RUN);
-        const int kb_total = p.kb_total;
+        const int kb_total = kb1 - kb0;
         int stage = 0, buf = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -365,13 +399,13 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
             tc::mbar_arrive(&sh.full[0]);
             tc::mbar_arrive(&sh.full[1]);
         }
-        for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+        for (int u = unit0; ok && u < units; u += unit_step) {
             const int mb = u % p.tiles_m, nb = u / p.tiles_m;
             const int row = mb * BM + quarter * 32 + lane;
-            const float *xs = p.x_scale + (row < p.m ? row : 0);
+            const float *xs = p.x_scale + (size_t)kb0 * p.m + (row < p.m ? row : 0);
             const int block = min(SWIGLU ? nb : 2 * nb + part * 2 * WIDE_RUN / BK, p.n_blocks - 1);
-            const float *wa = p.w_scale + (size_t)block * p.kb_total;
-            const float *wb = SWIGLU ? p.w2_scale + (size_t)block * p.kb_total : wa;
+            const float *wa = p.w_scale + (size_t)block * p.kb_total + kb0;
+            const float *wb = SWIGLU ? p.w2_scale + (size_t)block * p.kb_total + kb0 : wa;
             float acc[2 * WIDE_RUN];
 #pragma unroll
             for (int i = 0; i < 2 * WIDE_RUN; ++i) acc[i] = 0.0f;
@@ -433,6 +467,20 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                 if (lane == 0) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
                 break;
             }
+            if (SPLIT) {
+                // over the rings, when all ranks' loads and MMAs have completed
+                tc::cluster_sync();
+#pragma unroll
+                for (int j = 0; j < WIDE_RUN / 8; ++j) {
+                    const uint32_t to = tc::cluster_addr(ring0, j % ranks) + split_offset(ranks, rank, part, j, quarter * 32 + lane);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        tc::cluster_st(to + i * BM * 4, acc[j * 8 + i]);
+                        tc::cluster_st(to + (8 + i) * BM * 4, acc[WIDE_RUN + j * 8 + i]);
+                    }
+                }
+                break;   // one tile a cluster
+            }
             if (SWIGLU) {
 #pragma unroll
                 for (int i = 0; i < WIDE_RUN; ++i) acc[i] = silu(acc[i]) * acc[WIDE_RUN + i];
@@ -480,6 +528,45 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
         }
         if (lane == 0) tc::bulk_wait<0>();
         __syncwarp();
+        if (SPLIT) {
+            if (!ok) tc::cluster_sync();   // (after a timeout; its sums are void)
+            __syncwarp();
+            tc::cluster_sync();
+            const int mb = unit0 % p.tiles_m, nb = unit0 / p.tiles_m, row = mb * BM + quarter * 32 + lane;
+            const int col0 = nb * (SWIGLU ? WIDE_BN / 2 : WIDE_BN) + (SWIGLU ? WIDE_RUN : 2 * WIDE_RUN) * part;
+            for (int piece = rank; piece < WIDE_RUN / 8; piece += ranks) {
+                const int j = piece * 8;
+                float a[8], b[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) a[i] = b[i] = 0.0f;
+                for (int s = 0; s < ranks; ++s) {   // in rank order
+                    const float *from = reinterpret_cast<const float *>(
+                        ring + split_offset(ranks, s, part, piece, quarter * 32 + lane));
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        a[i] += from[i * BM];
+                        b[i] += from[(8 + i) * BM];
+                    }
+                }
+                if (row >= p.m) continue;
+                if (SWIGLU) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) a[i] = silu(a[i]) * b[i];
+                    if (col0 + j < p.n) store8(p, row, col0 + j, a);
+                } else {
+                    const bool res = p.epi == EAGLE3_EPI_BF16_RESIDUAL;
+                    if (col0 + j < p.n) {
+                        if (res) load_res8(p, row, col0 + j, a);
+                        store8(p, row, col0 + j, a);
+                    }
+                    if (col0 + WIDE_RUN + j < p.n) {
+                        if (res) load_res8(p, row, col0 + WIDE_RUN + j, b);
+                        store8(p, row, col0 + WIDE_RUN + j, b);
+                    }
+                }
+            }
+            __syncwarp();
+        }
     }
 
     tc::fence_before();
@@ -492,7 +579,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
 }
 
 // ---- narrow -------------------------------------------------------------------------------------
-constexpr int NARROW_EPI_WARPS = 8, NARROW_THREADS = 64 + 32 * NARROW_EPI_WARPS, NARROW_MAX = 128;
+constexpr int NARROW_EPI_WARPS = 8, NARROW_THREADS = 64 + 32 * NARROW_EPI_WARPS, NARROW_MAX = 64;
 constexpr int NARROW_STAGES = 8, NARROW_TMEM = 256, NARROW_CLUSTER = 8;
 constexpr int NARROW_RING = 106 * 1024;   // two CTAs a SM
 constexpr int NARROW_W = BM * BK;
@@ -507,7 +594,7 @@ static_assert(2 * (NARROW_SMEM + 1024) <= 228 * 1024, "two CTAs a SM");
 static_assert(NARROW_RING >= NARROW_MAX * BM * 4, "the ranks' sums fit the ring");
 
 // NT: row capacity of a tile (TMEM buffers of NT columns, NT / 2 accumulators a thread).
-// Grid: (cluster ranks = k ranges, weight tiles, row tiles).
+// Grid: (cluster ranks = k ranges, weight tiles).
 template <int NT, bool SWIGLU>
 __global__ void __launch_bounds__(NARROW_THREADS, 2)
     fp8_narrow_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
@@ -518,8 +605,7 @@ __global__ void __launch_bounds__(NARROW_THREADS, 2)
     NarrowShared &sh = *reinterpret_cast<NarrowShared *>(ring + NARROW_RING);
     volatile int *abort = &sh.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int ranks = gridDim.x, rank = blockIdx.x, mt = blockIdx.y, row0 = blockIdx.z * p.n16;
-    const int rows = min(p.n16, p.m - row0);
+    const int ranks = gridDim.x, rank = blockIdx.x, mt = blockIdx.y, rows = p.m;
     const int kb0 = (int)((long long)p.kb_total * rank / ranks);
     const int kb1 = (int)((long long)p.kb_total * (rank + 1) / ranks);
     const int stage_bytes = NARROW_W + p.n16 * BK, stages = p.stages;
@@ -585,7 +671,7 @@ __global__ void __launch_bounds__(NARROW_THREADS, 2)
                 tc::tma_load_2d(sw, &tm_w, kb * BK, mt * BM, &sh.full[stage]);
             }
             if (16 * lane < p.n16)
-                tc::tma_load_2d(sx + lane * 16 * BK, &tm_x, kb * BK, row0 + lane * 16, &sh.full[stage]);
+                tc::tma_load_2d(sx + lane * 16 * BK, &tm_x, kb * BK, lane * 16, &sh.full[stage]);
             if (++stage == stages) {
                 stage = 0;
                 phase ^= 1u;
@@ -656,7 +742,7 @@ __global__ void __launch_bounds__(NARROW_THREADS, 2)
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
                 const int r = lane + 32 * i;
-                sx[i] = r < HALF && r0 + r < rows ? __ldg(p.x_scale + (size_t)kb * p.m + row0 + r0 + r) : 0.0f;
+                sx[i] = r < HALF && r0 + r < rows ? __ldg(p.x_scale + (size_t)kb * p.m + r0 + r) : 0.0f;
             }
             sw = __ldg(ws + kb);
         };
@@ -737,7 +823,7 @@ __global__ void __launch_bounds__(NARROW_THREADS, 2)
         const int col = mt * OUT + j;
         if (col >= p.n) continue;
         if (SWIGLU) y = silu(y) * y2;
-        const size_t row = row0 + r;
+        const size_t row = r;
         if (p.epi == EAGLE3_EPI_F32) {
             ((float *)p.out)[row * p.ld_out + col] = y;
         } else {
@@ -821,15 +907,65 @@ cudaError_t launch_narrow(dim3 grid, cudaStream_t st, const CUtensorMap &tx, con
     return cudaLaunchKernelEx(&cfg, fp8_narrow_kernel<NT, SWIGLU>, tx, tw, tw2, p);
 }
 
+// Clusters of `ranks` CTAs of the wide kernel that the device holds at once (0 on an error).
+template <bool SWIGLU, bool SPLIT>
+int wide_clusters(int ranks) {
+    if (cudaFuncSetAttribute(fp8_wide_kernel<SWIGLU, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, WIDE_SMEM) !=
+        cudaSuccess)
+        return 0;
+    if (!SPLIT) return device_sm_count();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ranks * device_sm_count());
+    cfg.blockDim = dim3(WIDE_THREADS);
+    cfg.dynamicSmemBytes = WIDE_SMEM;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = ranks;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    return cudaOccupancyMaxActiveClusters(&n, fp8_wide_kernel<SWIGLU, SPLIT>, &cfg) == cudaSuccess ? n : 0;
+}
+
+struct ClusterCounts {
+    int n[WIDE_RANKS + 1];
+};
+
 template <bool SWIGLU>
-cudaError_t launch_wide(int grid, cudaStream_t st, const CUtensorMap &tx, const CUtensorMap &tw, const CUtensorMap &tw2,
-                        const CUtensorMap &to, const Fp8Params &p) {
-    static PerDevice<cudaError_t> attr;
-    const cudaError_t e = attr.get([] {
-        return cudaFuncSetAttribute(fp8_wide_kernel<SWIGLU>, cudaFuncAttributeMaxDynamicSharedMemorySize, WIDE_SMEM);
+cudaError_t launch_wide(cudaStream_t st, const CUtensorMap &tx, const CUtensorMap &tw, const CUtensorMap &tw2,
+                        const CUtensorMap &to, Fp8Params &p) {
+    static PerDevice<ClusterCounts> cache;
+    const ClusterCounts most = cache.get([] {
+        ClusterCounts c = {};
+        c.n[1] = wide_clusters<SWIGLU, false>(1);
+        for (int r = 2; r <= WIDE_RANKS; ++r)
+            if (split_bytes(r) <= WIDE_STAGES * WIDE_STAGE) c.n[r] = wide_clusters<SWIGLU, true>(r);
+        return c;
     });
-    if (e != cudaSuccess) return e;
-    return launch_pdl(fp8_wide_kernel<SWIGLU>, dim3(grid), dim3(WIDE_THREADS), WIDE_SMEM, st, tx, tw, tw2, to, p);
+    if (most.n[1] < 1) return cudaErrorUnknown;
+    // As many ranks as leave every tile a resident cluster, if that saves each CTA 18 k-blocks: a k-block takes
+    // 0.35 us, and meeting and adding up about 6 us (256 x 4096 x 14336, 112 k-blocks: 44 us by single CTAs, 30
+    // by two, 21 by four; 256 x 1024 x 2048, 16 k-blocks: 9.4 and 11.8 us).
+    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+    p.ranks = 1;
+    for (int r = 2; r <= WIDE_RANKS; ++r)
+        if (tiles <= most.n[r] && p.kb_total - p.kb_total / r >= 18) p.ranks = r;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>(most.n[p.ranks], tiles) * p.ranks);
+    cfg.blockDim = dim3(WIDE_THREADS);
+    cfg.dynamicSmemBytes = WIDE_SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = p.ranks;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = p.ranks > 1 ? 2 : 1;
+    return p.ranks > 1 ? cudaLaunchKernelEx(&cfg, fp8_wide_kernel<SWIGLU, true>, tx, tw, tw2, to, p)
+                       : cudaLaunchKernelEx(&cfg, fp8_wide_kernel<SWIGLU, false>, tx, tw, tw2, to, p);
 }
 
 }  // namespace
@@ -886,7 +1022,12 @@ extern "C" eagle3_status_t eagle3_linear_fp8(const eagle3_linear_fp8_args_t *a, 
     const cudaStream_t s = (cudaStream_t)stream;
     const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     const int tiles_w = (a->n + (swiglu ? 63 : BM - 1)) / (swiglu ? 64 : BM);
-    const bool narrow = a->m <= NARROW_MAX && tiles_w <= 65535;
+    p.tiles_m = (a->m + BM - 1) / BM;
+    p.tiles_n = (a->n + (swiglu ? WIDE_BN / 2 : WIDE_BN) - 1) / (swiglu ? WIDE_BN / 2 : WIDE_BN);
+    // Few rows by the narrow kernel, from 33 rows on unless the wide one's tiles cover half of the SMs.
+    // 8 x 6144 x 4096: 8.0 us narrow, 14.7 wide; 64 x 6144 x 4096 (24 wide tiles): 13.3 and 13.3; 64 rows x
+    // 2 * 14336 x 4096 (112): 31 and 25; 96 x 4096 x 14336: 34 (with tiles of 128 rows) and 20.
+    const bool narrow = tiles_w <= 65535 && (a->m <= NARROW_MAX / 2 || (a->m <= NARROW_MAX && 2 * p.tiles_n < sms));
     CUtensorMap tx, tw, tw2, to;
     const int w_box = narrow ? (swiglu ? 16 : BM) : (swiglu ? WIDE_BN / 2 : WIDE_BN);
     if (!tmap_rows(&tx, u8, 1, a->x, a->m, a->k, ld_x, narrow ? 16 : BM) ||
@@ -894,35 +1035,27 @@ extern "C" eagle3_status_t eagle3_linear_fp8(const eagle3_linear_fp8_args_t *a, 
         return EAGLE3_ERR_CUDA;
     tw2 = tw;
     if (swiglu && !tmap_rows(&tw2, u8, 1, a->w2, a->n, a->k, ld_w, w_box)) return EAGLE3_ERR_CUDA;
-    p.tiles_m = p.tiles_n = p.tma_out = p.n16 = p.stages = 0;
+    p.tma_out = p.n16 = p.stages = 0;
+    p.ranks = 1;
     cudaError_t e;
     if (narrow) {
-        const int tiles_r = (a->m + NARROW_MAX - 1) / NARROW_MAX;
-        p.n16 = ((a->m + tiles_r - 1) / tiles_r + 15) / 16 * 16;
+        p.n16 = (a->m + 15) / 16 * 16;
         p.stages = std::min(NARROW_STAGES, NARROW_RING / (NARROW_W + p.n16 * BK));
         int ranks = 1;
-        while (ranks < NARROW_CLUSTER && (int64_t)tiles_w * tiles_r * (ranks + 1) <= sms &&
-               p.kb_total >= 2 * (ranks + 1))
-            ++ranks;
-        const dim3 grid(ranks, tiles_w, tiles_r);
+        while (ranks < NARROW_CLUSTER && (int64_t)tiles_w * (ranks + 1) <= sms && p.kb_total >= 2 * (ranks + 1)) ++ranks;
+        const dim3 grid(ranks, tiles_w);
         if (p.n16 <= 32)
             e = swiglu ? launch_narrow<32, true>(grid, s, tx, tw, tw2, p)
                        : launch_narrow<32, false>(grid, s, tx, tw, tw2, p);
-        else if (p.n16 <= 64)
+        else
             e = swiglu ? launch_narrow<64, true>(grid, s, tx, tw, tw2, p)
                        : launch_narrow<64, false>(grid, s, tx, tw, tw2, p);
-        else
-            e = swiglu ? launch_narrow<128, true>(grid, s, tx, tw, tw2, p)
-                       : launch_narrow<128, false>(grid, s, tx, tw, tw2, p);
     } else {
-        p.tiles_m = (a->m + BM - 1) / BM;
-        p.tiles_n = (a->n + (swiglu ? WIDE_BN / 2 : WIDE_BN) - 1) / (swiglu ? WIDE_BN / 2 : WIDE_BN);
         const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
         if (tiles > INT32_MAX - sms) return EAGLE3_ERR_UNSUPPORTED;   // tiles are counted in 32 bits
         p.tma_out = out_map(&to, a, p.ld_out) ? 1 : 0;
         if (!p.tma_out) to = tx;   // unused
-        const int grid = (int)std::min<int64_t>(sms, tiles);
-        e = swiglu ? launch_wide<true>(grid, s, tx, tw, tw2, to, p) : launch_wide<false>(grid, s, tx, tw, tw2, to, p);
+        e = swiglu ? launch_wide<true>(s, tx, tw, tw2, to, p) : launch_wide<false>(s, tx, tw, tw2, to, p);
     }
     return e == cudaSuccess ? EAGLE3_OK : EAGLE3_ERR_CUDA;
 }

@@ -117,6 +117,9 @@ E3_DEV float cluster_ld(uint32_t addr) {
     asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v) : "r"(addr) : "memory");
     return v;
 }
+E3_DEV void cluster_st(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(addr), "f"(v) : "memory");
+}
 // Arrive on a barrier anywhere in the cluster (cluster_addr) by the lanes for which `one` holds.  The
 // default order is enough for what it announces here: loads that another barrier has shown to have landed
 // (or copies behind a proxy fence) and TMEM reads that have been waited for; there are no plain writes to

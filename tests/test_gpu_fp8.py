@@ -138,6 +138,14 @@ def test_fp8_many_rows(m, n, k, epi):
     _check(m, n, k, epi)
 
 
+@pytest.mark.parametrize("epi", EPIS)
+@pytest.mark.parametrize("m,n,k", [(70, 130, 4112), (129, 1, 2560), (200, 521, 8192), (100, 2600, 3088)])
+def test_fp8_k_ranges(m, n, k, epi):
+    """Few tiles and a long k: the k-blocks are cut over a cluster, with odd ranges and odd columns."""
+    _check(m, n, k, epi)
+    _check(m, n, k, epi, seed=1, out_pitch=3)
+
+
 @pytest.mark.parametrize("m", [5, 300])
 @pytest.mark.parametrize("epi", EPIS)
 def test_fp8_pitched_views(m, epi):
