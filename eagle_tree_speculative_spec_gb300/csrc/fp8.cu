@@ -220,14 +220,45 @@ E3_DEV void store8(const Fp8Params &p, int row, int col, const float *v) {
     }
 }
 
+// 16 columns of up to 32 rows from a warp's box (64-byte rows in the 64-byte swizzle): this lane's column c of
+// rows r0, r0 + 2, ... below most.
+template <bool SWIGLU>
+E3_DEV void store_rows16(const Fp8Params &p, const uint8_t *box, int y, int col, int r0, int c, int most) {
+    const bool res = !SWIGLU && p.epi == EAGLE3_EPI_BF16_RESIDUAL, f32 = !SWIGLU && p.epi == EAGLE3_EPI_F32;
+    const __nv_bfloat16 *src = res ? p.residual + (size_t)(y + r0) * p.ld_res + col : nullptr;
+    const size_t at = (size_t)(y + r0) * p.ld_out + col;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {   // 8 rows at a time, their residuals first
+        float add[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = 16 * h + 2 * i;
+            add[i] = res && r + r0 < most ? __bfloat162float(src[(size_t)r * p.ld_res]) : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = 16 * h + 2 * i;
+            if (r + r0 >= most) continue;
+            float v = *reinterpret_cast<const float *>(box + (r + r0) * 64 + (((c >> 2) ^ (((r + r0) >> 1) & 3)) << 4) +
+                                                       (c & 3) * 4);
+            if (res) v += add[i];
+            if (f32)
+                ((float *)p.out)[at + (size_t)r * p.ld_out] = v;
+            else
+                ((__nv_bfloat16 *)p.out)[at + (size_t)r * p.ld_out] = __float2bfloat16_rn(v);
+        }
+    }
+}
+
 // ---- wide ---------------------------------------------------------------------------------------
 // Three warpgroups: loads and MMAs (warps 0 and 1; 2 and 3 idle), and two of the epilogue.  The block
-// is launched with 168 registers a thread (384 x 168 = 64512); the first group keeps 56 and the
-// epilogue takes 224 (128 x 56 + 256 x 224 = 64512): 128 accumulators, two loads of 16, scales.  The
+// is launched with 168 registers a thread (384 x 168 = 64512); the first group keeps 40 and the
+// epilogue takes 232 (128 x 40 + 256 x 232 = 64512): 128 accumulators, two loads of 16, scales.  The
 // epilogue is short of issue slots: the instructions around the 128 additions of a k-block (waits that
 // poll, addresses made anew) weigh as much as they do, so barriers go by precomputed shared-memory
-// addresses and a poll is a handful of instructions: 3840 x 2 * 14336 x 4096 412 -> 350 us.  (Four
-// groups of 64 accumulators and 104 registers: 358 us.)
+// addresses, a poll is a handful of instructions and the thread index stays in a register: 3840 x 2 * 14336 x
+// 4096 412 -> 337 us, 2680 TFLOP/s; 3840 x 6144 x 4096 74 us.  (Four groups of 64 accumulators and 104
+// registers: 358 us.)  What is left is still the epilogue: without its additions the kernel takes 265 us.
 constexpr int WIDE_BN = 256, WIDE_STAGES = 4, WIDE_EPI_WARPS = 8, WIDE_THREADS = 128 + 32 * WIDE_EPI_WARPS;
 constexpr int WIDE_EPI0 = 4;   // first epilogue warp
 constexpr int WIDE_RANKS = 8;  // largest cluster
@@ -267,7 +298,11 @@ E3_DEV void registers_take() {
 // SPLIT: a cluster of p.ranks CTAs works on one tile, each on a range of the k-blocks.  Pieces of 8 columns of
 // both runs belong to the ranks in turn: each rank sends the others their pieces of its sums by remote stores
 // (reading them took three times as long), and adds up and finishes its own.
-template <bool SWIGLU, bool SPLIT>
+// OUT: how outputs leave.  The variants are kernels of their own: what stands behind the main loop decides
+// whether its 128 accumulators and scales stay in registers (both ways in one kernel: 3840 x 2 * 14336 x 4096 346
+// -> 444 us).
+enum { OUT_TMA, OUT_STAGED, OUT_SPLIT };
+template <bool SWIGLU, int OUT>
 __global__ void __launch_bounds__(WIDE_THREADS, 1)
     fp8_wide_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                     const __grid_constant__ CUtensorMap tm_w2, const __grid_constant__ CUtensorMap tm_out,
@@ -276,6 +311,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
     uint8_t *ring = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint8_t *boxes = ring + WIDE_STAGES * WIDE_STAGE;
     WideShared &sh = *reinterpret_cast<WideShared *>(boxes + WIDE_EPI_WARPS * WIDE_BOX);
+    constexpr bool SPLIT = OUT == OUT_SPLIT;
     const uint32_t tid = tc::thread_index();
     const int warp = (int)(tid >> 5), lane = (int)(tid & 31u);
 
@@ -307,7 +343,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
     const int kb1 = SPLIT ? (int)((long long)p.kb_total * (rank + 1) / ranks) : p.kb_total;
 
     if (warp < WIDE_EPI0) {
-        registers_give<56>();
+        registers_give<40>();
         if (warp == 0) {
             // ------------------------------------------------------------------ TMA producer
             if (tc::elect_one()) {
@@ -383,7 +419,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
             tc::cluster_sync();
         }
     } else {
-        registers_take<224>();
+        registers_take<232>();
         // ------------------------------------------------------------------ epilogue (warps 4..11)
         const int quarter = warp & 3, part = (warp - WIDE_EPI0) >> 2;
         uint8_t *box = boxes + (warp - WIDE_EPI0) * WIDE_BOX;
@@ -487,13 +523,13 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
             }
             const int cols = SWIGLU ? WIDE_RUN : 2 * WIDE_RUN, y = mb * BM + quarter * 32;
             const int col0 = nb * (SWIGLU ? WIDE_BN / 2 : WIDE_BN) + cols * part;
-            const bool f32 = p.epi == EAGLE3_EPI_F32;
-            if (p.epi == EAGLE3_EPI_BF16_RESIDUAL && row < p.m) {
+            const bool f32 = !SWIGLU && p.epi == EAGLE3_EPI_F32;
+            if (OUT == OUT_TMA && !SWIGLU && p.epi == EAGLE3_EPI_BF16_RESIDUAL && row < p.m) {
 #pragma unroll
                 for (int i = 0; i < 2 * WIDE_RUN; i += 8)
                     if (col0 + i < p.n) load_res8(p, row, col0 + i, acc + i);
             }
-            if (p.tma_out) {
+            if (OUT == OUT_TMA) {
                 // pieces of 64 bytes: 32 bf16 or 16 fp32 columns of the warp's 32 rows, in the 64-byte swizzle
 #pragma unroll
                 for (int c = 0; c < WIDE_RUN / 8; ++c) {
@@ -520,10 +556,22 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                         tc::bulk_commit();
                     }
                 }
-            } else if (row < p.m) {
+            } else if (OUT == OUT_STAGED) {
+                // 16 columns of the warp's 32 rows at a time through the box, back by half warps that hold the 16
+                // columns of a row.  (Stores of a row a lane: 2000 x 6146 x 4096 139 us, 47 at 6144.)
+                const int c = lane & 15, r0 = lane >> 4;
 #pragma unroll
-                for (int i = 0; i < 2 * WIDE_RUN; i += 8)
-                    if (i < cols && col0 + i < p.n) store8(p, row, col0 + i, acc + i);
+                for (int i = 0; i < 2 * WIDE_RUN; i += 16) {
+                    if (i >= cols || col0 + i >= p.n) break;
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        *reinterpret_cast<float4 *>(box + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
+                            make_float4(acc[i + 4 * j], acc[i + 4 * j + 1], acc[i + 4 * j + 2], acc[i + 4 * j + 3]);
+                    __syncwarp();
+                    const int col = col0 + i + c;
+                    store_rows16<SWIGLU>(p, box, y, col, r0, c, col < p.n ? min(32, p.m - y) : 0);
+                }
             }
         }
         if (lane == 0) tc::bulk_wait<0>();
@@ -908,12 +956,12 @@ cudaError_t launch_narrow(dim3 grid, cudaStream_t st, const CUtensorMap &tx, con
 }
 
 // Clusters of `ranks` CTAs of the wide kernel that the device holds at once (0 on an error).
-template <bool SWIGLU, bool SPLIT>
+template <bool SWIGLU, int OUT>
 int wide_clusters(int ranks) {
-    if (cudaFuncSetAttribute(fp8_wide_kernel<SWIGLU, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, WIDE_SMEM) !=
+    if (cudaFuncSetAttribute(fp8_wide_kernel<SWIGLU, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, WIDE_SMEM) !=
         cudaSuccess)
         return 0;
-    if (!SPLIT) return device_sm_count();
+    if (OUT != OUT_SPLIT) return device_sm_count();
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ranks * device_sm_count());
     cfg.blockDim = dim3(WIDE_THREADS);
@@ -925,7 +973,7 @@ int wide_clusters(int ranks) {
     cfg.attrs = &at;
     cfg.numAttrs = 1;
     int n = 0;
-    return cudaOccupancyMaxActiveClusters(&n, fp8_wide_kernel<SWIGLU, SPLIT>, &cfg) == cudaSuccess ? n : 0;
+    return cudaOccupancyMaxActiveClusters(&n, fp8_wide_kernel<SWIGLU, OUT>, &cfg) == cudaSuccess ? n : 0;
 }
 
 struct ClusterCounts {
@@ -938,9 +986,9 @@ cudaError_t launch_wide(cudaStream_t st, const CUtensorMap &tx, const CUtensorMa
     static PerDevice<ClusterCounts> cache;
     const ClusterCounts most = cache.get([] {
         ClusterCounts c = {};
-        c.n[1] = wide_clusters<SWIGLU, false>(1);
+        c.n[1] = std::min(wide_clusters<SWIGLU, OUT_TMA>(1), wide_clusters<SWIGLU, OUT_STAGED>(1));
         for (int r = 2; r <= WIDE_RANKS; ++r)
-            if (split_bytes(r) <= WIDE_STAGES * WIDE_STAGE) c.n[r] = wide_clusters<SWIGLU, true>(r);
+            if (split_bytes(r) <= WIDE_STAGES * WIDE_STAGE) c.n[r] = wide_clusters<SWIGLU, OUT_SPLIT>(r);
         return c;
     });
     if (most.n[1] < 1) return cudaErrorUnknown;
@@ -964,8 +1012,9 @@ cudaError_t launch_wide(cudaStream_t st, const CUtensorMap &tx, const CUtensorMa
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = p.ranks > 1 ? 2 : 1;
-    return p.ranks > 1 ? cudaLaunchKernelEx(&cfg, fp8_wide_kernel<SWIGLU, true>, tx, tw, tw2, to, p)
-                       : cudaLaunchKernelEx(&cfg, fp8_wide_kernel<SWIGLU, false>, tx, tw, tw2, to, p);
+    return p.ranks > 1 ? cudaLaunchKernelEx(&cfg, fp8_wide_kernel<SWIGLU, OUT_SPLIT>, tx, tw, tw2, to, p)
+           : p.tma_out ? cudaLaunchKernelEx(&cfg, fp8_wide_kernel<SWIGLU, OUT_TMA>, tx, tw, tw2, to, p)
+                       : cudaLaunchKernelEx(&cfg, fp8_wide_kernel<SWIGLU, OUT_STAGED>, tx, tw, tw2, to, p);
 }
 
 }  // namespace
@@ -1052,8 +1101,11 @@ extern "C" eagle3_status_t eagle3_linear_fp8(const eagle3_linear_fp8_args_t *a, 
                        : launch_narrow<64, false>(grid, s, tx, tw, tw2, p);
     } else {
         const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
-        if (tiles > INT32_MAX - sms) return EAGLE3_ERR_UNSUPPORTED;   // tiles are counted in 32 bits
-        p.tma_out = out_map(&to, a, p.ld_out) ? 1 : 0;
+        if (tiles > MAX_DIM) return EAGLE3_ERR_UNSUPPORTED;   // tiles are counted in 32 bits
+        // (a residual is added to rows a lane holds: by 16-byte loads or not at all)
+        const bool res8 = a->epilogue != EAGLE3_EPI_BF16_RESIDUAL ||
+                          (((uintptr_t)a->residual & 15) == 0 && p.ld_res % 8 == 0);
+        p.tma_out = res8 && out_map(&to, a, p.ld_out) ? 1 : 0;
         if (!p.tma_out) to = tx;   // unused
         e = swiglu ? launch_wide<true>(s, tx, tw, tw2, to, p) : launch_wide<false>(s, tx, tw, tw2, to, p);
     }

@@ -557,7 +557,7 @@ eagle3_status_t validate(const eagle3_grouped_linear_args_t *a) {
     if (((uintptr_t)a->offsets | (uintptr_t)a->row_ids | (uintptr_t)a->dev_status) & 3 || (uintptr_t)a->out & 1)
         return EAGLE3_ERR_INVALID_ARGUMENT;
     // units are counted in 32 bits
-    if ((int64_t)((a->n + 63) / 64) * (a->m / MAX_ROWS + a->n_groups) > INT32_MAX) return EAGLE3_ERR_UNSUPPORTED;
+    if ((int64_t)((a->n + 63) / 64) * (a->m / MAX_ROWS + a->n_groups) > MAX_DIM) return EAGLE3_ERR_UNSUPPORTED;
     return EAGLE3_OK;
 }
 

@@ -311,26 +311,33 @@ E3_DEV void unpack(const typename Pack<VEC>::T &r, float (&v)[VEC]) {
     for (int i = 0; i < VEC; ++i) v[i] = __bfloat162float(h[i]);
 }
 
-// VEC columns a thread: 8 where every row starts on 16 bytes, 2 on 4, else 1.
-template <int VEC>
+// VEC columns a vector: 8 where every row starts on 16 bytes, 2 on 4, else 1.  A thread takes VECS vectors,
+// COMBINE_THREADS apart, so that narrow ones keep as many bytes in flight (3840 x 8 rows of 4094 and 4095
+// columns with one vector a thread: 79 and 126 us, 50 at 4096).
+template <int VEC, int VECS>
 __global__ void __launch_bounds__(COMBINE_THREADS) moe_combine_kernel(const CombineParams p) {
     using T = typename Pack<VEC>::T;
     pdl_wait();
     pdl_trigger();
     const int row = blockIdx.x;
-    const int col = (blockIdx.y * COMBINE_THREADS + threadIdx.x) * VEC;
+    const int col = (blockIdx.y * VECS * COMBINE_THREADS + threadIdx.x) * VEC;
+    constexpr int APART = COMBINE_THREADS * VEC;
     if (col >= p.d) return;   // VEC divides d
-    float acc[VEC];
+    float acc[VECS][VEC];
+    T res[VECS];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
-    T res;
-    if (p.res) res = *reinterpret_cast<const T *>(p.res + (size_t)row * p.ld_res + col);
+    for (int u = 0; u < VECS; ++u) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) acc[u][i] = 0.0f;
+        if (p.res && col + u * APART < p.d)
+            res[u] = *reinterpret_cast<const T *>(p.res + (size_t)row * p.ld_res + col + u * APART);
+    }
     const int32_t *slots = p.slots + (size_t)row * p.k;
     const float *weights = p.weights + (size_t)row * p.k;
     for (int j0 = 0; j0 < p.k; j0 += 8) {   // the loads of 8 places together
         int at[8];
         float w[8];
-        T raw[8];
+        T raw[8][VECS];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             at[i] = j0 + i < p.k ? __ldg(slots + j0 + i) : -1;
@@ -342,28 +349,39 @@ __global__ void __launch_bounds__(COMBINE_THREADS) moe_combine_kernel(const Comb
                 flag(p.dev_status, EAGLE3_DEV_BAD_COUNTS);
                 at[i] = -1;
             }
-            if (at[i] >= 0) raw[i] = __ldg(reinterpret_cast<const T *>(p.y + (size_t)at[i] * p.ld_y + col));
+            if (at[i] < 0) continue;
+            const __nv_bfloat16 *y = p.y + (size_t)at[i] * p.ld_y + col;
+#pragma unroll
+            for (int u = 0; u < VECS; ++u)
+                if (VECS == 1 || col + u * APART < p.d) raw[i][u] = __ldg(reinterpret_cast<const T *>(y + u * APART));
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             if (at[i] < 0) continue;
-            float v[VEC];
-            unpack<VEC>(raw[i], v);
 #pragma unroll
-            for (int c = 0; c < VEC; ++c) acc[c] = fmaf(w[i], v[c], acc[c]);
+            for (int u = 0; u < VECS; ++u) {
+                float v[VEC];
+                unpack<VEC>(raw[i][u], v);
+#pragma unroll
+                for (int c = 0; c < VEC; ++c) acc[u][c] = fmaf(w[i], v[c], acc[u][c]);
+            }
         }
     }
-    if (p.res) {
-        float v[VEC];
-        unpack<VEC>(res, v);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) acc[i] += v[i];
+    for (int u = 0; u < VECS; ++u) {
+        if (col + u * APART >= p.d) break;
+        if (p.res) {
+            float v[VEC];
+            unpack<VEC>(res[u], v);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) acc[u][i] += v[i];
+        }
+        T o;
+        __nv_bfloat16 *h = reinterpret_cast<__nv_bfloat16 *>(&o);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) h[i] = __float2bfloat16_rn(acc[u][i]);
+        *reinterpret_cast<T *>(p.out + (size_t)row * p.ld_out + col + u * APART) = o;
     }
-    T o;
-    __nv_bfloat16 *h = reinterpret_cast<__nv_bfloat16 *>(&o);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) h[i] = __float2bfloat16_rn(acc[i]);
-    *reinterpret_cast<T *>(p.out + (size_t)row * p.ld_out + col) = o;
 }
 
 // ---- host side ----------------------------------------------------------------------------------
@@ -424,11 +442,11 @@ cudaError_t launch_route(int blocks, cudaStream_t st, const RouteParams &p) {
     return launch_pdl(moe_route_kernel<PER>, dim3(blocks), dim3(ROUTE_THREADS), LISTS, st, p);
 }
 
-template <int VEC>
+template <int VEC, int VECS>
 cudaError_t launch_combine(cudaStream_t st, const CombineParams &p) {
-    const int per_block = COMBINE_THREADS * VEC;
-    return launch_pdl(moe_combine_kernel<VEC>, dim3(p.rows, (p.d + per_block - 1) / per_block), dim3(COMBINE_THREADS),
-                      0, st, p);
+    const int per_block = COMBINE_THREADS * VEC * VECS;
+    return launch_pdl(moe_combine_kernel<VEC, VECS>, dim3(p.rows, (p.d + per_block - 1) / per_block),
+                      dim3(COMBINE_THREADS), 0, st, p);
 }
 
 }  // namespace
@@ -498,8 +516,8 @@ extern "C" eagle3_status_t eagle3_moe_combine(const eagle3_moe_combine_args_t *a
     int64_t step = p.d | p.ld_y | p.ld_out | (p.res ? p.ld_res : 0);
     const uintptr_t base = (uintptr_t)p.y | (uintptr_t)p.out | (uintptr_t)p.res;
     const cudaStream_t s = (cudaStream_t)stream;
-    const cudaError_t e = step % 8 == 0 && base % 16 == 0  ? launch_combine<8>(s, p)
-                          : step % 2 == 0 && base % 4 == 0 ? launch_combine<2>(s, p)
-                                                           : launch_combine<1>(s, p);
+    const cudaError_t e = step % 8 == 0 && base % 16 == 0  ? launch_combine<8, 1>(s, p)
+                          : step % 2 == 0 && base % 4 == 0 ? launch_combine<2, 4>(s, p)
+                                                           : launch_combine<1, 4>(s, p);
     return e == cudaSuccess ? EAGLE3_OK : EAGLE3_ERR_CUDA;
 }
