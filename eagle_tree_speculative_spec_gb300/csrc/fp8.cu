@@ -8,7 +8,7 @@
 // two scales, to fp32 accumulators in registers while the next block's MMAs run.  (This also keeps
 // the long sum out of the tensor cores' accumulation.)
 //
-// Two kernels, both warp-specialised: warp 0 loads by TMA into a ring, a lane of warp 1 issues
+// Two kernels (the rule between them stands at the launch), both warp-specialised: warp 0 loads by TMA into a ring, a lane of warp 1 issues
 // tcgen05.mma (kind::f8f6f4, K = 32) and the other warps run the epilogue.
 //   wide     128 rows x 256 weight rows a tile, persistent.  Rows are the M side, so a thread owns one
 //            row and its scale is one number a k-block.
@@ -34,7 +34,8 @@ constexpr int BK = 128;                 // k values of a block and of a tile (12
 constexpr int BM = 128;
 constexpr float E4M3_MAX = 448.0f;
 
-// (the special function unit's division: 2 steps of fp32 off at the most, 0 where exp(-x) > 2^126)
+// (By the special function unit: the exponential is 2 + 1.2 |x| steps of fp32 off at the most and the division
+// 2, against a bf16 result's 2^15; 0 where exp(-x) passes 2^126, x below -87.3, where silu is above -2^-119.)
 E3_DEV float silu(float x) { return __fdividef(x, 1.0f + __expf(-x)); }
 
 struct Fp8Params {
@@ -170,6 +171,10 @@ __global__ void __launch_bounds__(QUANT_THREADS) quantize_kernel(const QuantPara
 }
 
 // ---- output -------------------------------------------------------------------------------------
+// Residuals are read past L1: out may be the same buffer, and a line's other columns another CTA's.
+E3_DEV float res1(const __nv_bfloat16 *src) {
+    return __uint_as_float((uint32_t)__ldcg(reinterpret_cast<const unsigned short *>(src)) << 16);
+}
 // 8 consecutive outputs of a row from column col: residual, rounding, store (columns below n).
 E3_DEV void load_res8(const Fp8Params &p, int row, int col, float *v) {
     const __nv_bfloat16 *src = p.residual + (size_t)row * p.ld_res + col;
@@ -184,7 +189,7 @@ E3_DEV void load_res8(const Fp8Params &p, int row, int col, float *v) {
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (col + i < p.n) v[i] += __bfloat162float(src[i]);
+            if (col + i < p.n) v[i] += res1(src + i);
     }
 }
 E3_DEV uint4 pack8(const float *v) {
@@ -233,7 +238,7 @@ E3_DEV void store_rows16(const Fp8Params &p, const uint8_t *box, int y, int col,
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int r = 16 * h + 2 * i;
-            add[i] = res && r + r0 < most ? __bfloat162float(src[(size_t)r * p.ld_res]) : 0.0f;
+            add[i] = res && r + r0 < most ? res1(src + (size_t)r * p.ld_res) : 0.0f;
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -276,7 +281,6 @@ struct WideShared {
 };
 constexpr int WIDE_SMEM = 1024 + WIDE_STAGES * WIDE_STAGE + WIDE_EPI_WARPS * WIDE_BOX + (int)sizeof(WideShared);
 static_assert(WIDE_SMEM <= 232448, "shared memory budget");
-
 
 // SPLIT: where rank src's sums of piece j (8 columns of each run, 128 rows) of an epilogue half lie in the ring
 // of the rank that the piece belongs to, j % ranks; byte offset of a row's first value.
@@ -875,7 +879,7 @@ __global__ void __launch_bounds__(NARROW_THREADS, 2)
         if (p.epi == EAGLE3_EPI_F32) {
             ((float *)p.out)[row * p.ld_out + col] = y;
         } else {
-            if (p.epi == EAGLE3_EPI_BF16_RESIDUAL) y += __bfloat162float(p.residual[row * p.ld_res + col]);
+            if (p.epi == EAGLE3_EPI_BF16_RESIDUAL) y += res1(p.residual + row * p.ld_res + col);
             ((__nv_bfloat16 *)p.out)[row * p.ld_out + col] = __float2bfloat16_rn(y);
         }
     }

@@ -124,8 +124,9 @@ E3_DEV Unit unit_at(const Shared &sh, const GroupedParams &p, int u) {
 
 // The division by the special function unit: straight-line code, so that a warp, which has its
 // scheduler almost to itself here, works on many columns at once.  (An IEEE division is a branch per
-// value; with it the SwiGLU epilogue took twice the main loop's time at k = 4096.)  2 steps of fp32 off
-// at the most, and 0 where exp(-x) > 2^126.
+// value; with it the SwiGLU epilogue took twice the main loop's time at k = 4096.)  The exponential is 2 +
+// 1.2 |x| steps of fp32 off at the most and the division 2, against a bf16 result's 2^15; 0 where exp(-x)
+// passes 2^126 (x below -87.3, where silu is above -2^-119).
 E3_DEV float silu(float x) { return __fdividef(x, 1.0f + __expf(-x)); }
 
 // 16 bytes to shared memory, or 16 zero bytes (src is not read then)

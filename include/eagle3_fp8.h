@@ -48,10 +48,13 @@ eagle3_status_t eagle3_quantize_fp8(const eagle3_quantize_fp8_args_t *args, eagl
  * The inner sums run on the tcgen05 tensor cores (products exact, fp32 accumulation over one block
  * of 128), the outer one in fp32 registers.  Epilogues as in eagle3_linear.h: EAGLE3_EPI_BF16,
  * EAGLE3_EPI_F32, EAGLE3_EPI_BF16_RESIDUAL (out may be the residual buffer itself) and
- * EAGLE3_EPI_SWIGLU (silu(y) * y2 with y2 from w2, w2_scale).  Scales may have any fp32 value; a
- * NaN among the values or the scales makes the outputs that read it NaN.  With few rows the sum
- * over b is cut into ranges that a thread-block cluster adds in order; the cut comes from the shape
- * and the device's SM count, so results are reproducible on a given GPU model.
+ * EAGLE3_EPI_SWIGLU (silu(y) * y2 with y2 from w2, w2_scale; silu of less than -87.3 is 0).  A NaN
+ * among the values or the scales makes the outputs that read it NaN.  Scales may be 0, subnormal or
+ * negative; x_scale * w_scale, and x_scale times an inner sum (at most 448 * 448 * 128), have to stay
+ * below fp32's largest number, and lose bits where they fall below its smallest normal one.  Where the
+ * output has few tiles the sum over b is cut into ranges that a thread-block cluster adds in order;
+ * the cut comes from the shape and from how many CTAs the device holds, so results are reproducible on
+ * a given GPU model.
  * ---------------------------------------------------------------------------------------------- */
 typedef struct {
     int32_t m, n, k;          /* rows of x, rows of W (= output columns), contraction (k % 16 == 0) */

@@ -77,7 +77,8 @@ eagle3_status_t eagle3_moe_route(const eagle3_moe_route_args_t *args, void *work
  *
  * Slots [offsets[e], offsets[e + 1]) use the weights of group e; r(s) = row_ids[s], or s itself
  * without row_ids.  Epilogues: EAGLE3_EPI_BF16 (out bf16), EAGLE3_EPI_SWIGLU
- * (out bf16 = silu(x W^T) * (x W2^T)).  bf16 in, fp32 accumulation on the tcgen05 tensor cores.
+ * (out bf16 = silu(x W^T) * (x W2^T); silu of less than -87.3 is 0).  bf16 in, fp32 accumulation on the
+ * tcgen05 tensor cores.
  * Groups may be empty.  Rows of out at or past offsets[n_groups] are left as they were.
  *
  * EAGLE3_DEV_BAD_COUNTS (eagle3_chain.h) is raised when offsets do not start at 0, decrease or pass

@@ -223,3 +223,77 @@ def test_quantize_then_product_in_a_graph():
             graph.replay()
             torch.cuda.synchronize()
             assert torch.equal(out, eager)
+
+
+@pytest.mark.parametrize("m,k,out_pitch", [(17, 128, 0), (200, 128, 0), (200, 128, 1), (100, 4096, 0)])
+def test_fp8_extreme_gates(m, k, out_pitch):
+    """Gates from -1e18 to 1e18 in every kernel: x[r] = (1, 1, 0, ...) with the scale a, unit weights: both sums
+    are a.  Tolerance as in the bf16 tests."""
+    dev = require_gpu()
+    n, kb = 64, k // 128
+    values = [0.0, -0.0, 1.0, -1.0, -20.0, -60.0, -80.0, -87.0, -87.5, -88.0, -89.0, -100.0, 88.0, 100.0, 1e18, -1e18]
+    a = np.array([values[i % len(values)] for i in range(m)], np.float32)
+    x = np.zeros((m, k), np.uint8)
+    wg, wu = np.zeros((n, k), np.uint8), np.zeros((n, k), np.uint8)
+    one = fp8.encode(np.ones((1, 1)))[0, 0]
+    x[:, k - 2:] = one
+    wg[:, k - 2] = wu[:, k - 1] = one
+    t = lambda v: torch.from_numpy(v).to(dev)
+    xs, ws = np.repeat(a[None], kb, 0), np.ones((1, kb), np.float32)
+    out = torch.empty(m, n + out_pitch, dtype=bf, device=dev)[:, :n]
+    e3.eagle3_linear_fp8(_f8(x, dev), t(xs), _f8(wg, dev), t(ws), out, epilogue=e3.EPI_SWIGLU, w2=_f8(wu, dev),
+                         w2_scale=t(ws))
+    a = a.astype(np.float64)
+    want = moe.silu(a) * a
+    tol = (BF16 + 2 * U * (8 + 1.2 * np.abs(np.clip(a, -100, 100)))) * np.abs(want)
+    tol = tol + np.where(a < -87, 2.0 ** -119, 0) * np.abs(a) + 2.0 ** -133
+    assert (np.abs(_np(out) - want[:, None]) <= tol[:, None]).all()
+
+
+@pytest.mark.parametrize("m,n,k", [(20, 200, 256), (200, 200, 256), (200, 200, 4096)])
+def test_fp8_offsets_past_32_bits(m, n, k):
+    """Rows so far apart that the last ones start past 2^31 elements from the first."""
+    dev = require_gpu()
+    pitch = (2 ** 31 // (m - 1) // 16 + 2) * 16
+    x, xs, ws, wss = _data(m, n, k, 12)
+    t = lambda v: torch.from_numpy(v).to(dev)
+    xd = torch.empty(m, pitch, dtype=torch.uint8, device=dev)[:, :k]
+    xd.copy_(t(x))
+    out = torch.empty(m, pitch, dtype=bf, device=dev)[:, :n]
+    e3.eagle3_linear_fp8(xd.view(f8), t(xs), _f8(ws[0], dev), t(wss[0]), out)
+    y, S = fp8.linear(x, xs, ws[0], wss[0])
+    tol = (256 + 3 + xs.shape[0]) * U * S
+    assert (np.abs(_np(out) - y) <= tol + BF16 * (np.abs(y) + tol) + 1e-37).all()
+    b = torch.empty(m, pitch, dtype=bf, device=dev)[:, :k]
+    b.copy_(torch.randn(m, k, generator=torch.Generator().manual_seed(13)))
+    scale = torch.empty(-(-k // 128), m, device=dev)
+    e3.eagle3_quantize_fp8(b, xd.view(f8), scale)
+    codes, want = fp8.quantize(b.float().cpu().numpy())
+    np.testing.assert_array_equal(scale.cpu().numpy(), want)
+    np.testing.assert_array_equal(xd.cpu().numpy(), codes)
+
+
+def test_fp8_on_two_streams_at_once():
+    """The kernels with and without clusters, side by side."""
+    dev = require_gpu()
+    t = lambda v: torch.from_numpy(v).to(dev)
+    sets = []
+    for m, n, k in ((20, 300, 1024), (200, 600, 4096), (700, 1300, 512), (64, 256, 4096)):
+        x, xs, ws, wss = _data(m, n, k, 14)
+        sets.append([_f8(x, dev), t(xs), _f8(ws[0], dev), t(wss[0]), torch.empty(m, n, dtype=bf, device=dev)])
+    run = lambda order: [e3.eagle3_linear_fp8(*sets[i]) for i in order]
+    run(range(4))
+    torch.cuda.synchronize()
+    want = [s[4].clone() for s in sets]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        for s in sets:
+            s[4].zero_()
+        torch.cuda.synchronize()
+        for order, stream in zip(((0, 1), (2, 3)), streams):
+            with torch.cuda.stream(stream):
+                for _ in range(4):
+                    run(order)
+        torch.cuda.synchronize()
+        for s, w in zip(sets, want):
+            assert torch.equal(s[4], w)

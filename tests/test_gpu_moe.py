@@ -391,3 +391,60 @@ def test_calls_on_two_streams_at_once():
         torch.cuda.synchronize()
         for L, w in zip(layers, want):
             assert int(L["st"]) == 0 and torch.equal(L["out"], w)
+
+
+# ----------------------------------------------------------------------------- borders
+def _silu_tol(a, up):
+    """silu(a) * up: the exponential is 2 + 1.2 |a| fp32 steps (2 u) off, division and product 3 more, the
+    result is rounded to bf16; below -87.3 it is 0, an error of less than 2^-119 times up."""
+    want = moe.silu(a) * up
+    tol = (BF16 + 2 * U * (8 + 1.2 * np.abs(np.clip(a, -100, 100)))) * np.abs(want)
+    return want, tol + np.where(a < -87, 2.0 ** -119, 0) * np.abs(up) + TINY
+
+
+@pytest.mark.parametrize("n", [64, 256])   # single CTAs and pairs
+def test_grouped_extreme_gates(n):
+    """Gates from the lowest number to infinity: x[s] = (gate, up, 0, ...) and unit weights."""
+    dev = require_gpu()
+    gates = [0.0, -0.0, 1.0, -1.0, -20.0, -60.0, -80.0, -87.0, -87.5, -88.0, -89.0, -100.0, 88.0, 100.0, -1e30, -3e38]
+    ups = [1.0, -2.0, 1e30, 0.0]
+    pairs = [(a, u) for a in gates for u in ups] + [(3e38, 1.0), (3e38, 0.5)]
+    x = torch.zeros(len(pairs), 64, dtype=bf)
+    x[:, :2] = torch.tensor(pairs).to(bf)
+    wg, wu = torch.zeros(1, n, 64, dtype=bf), torch.zeros(1, n, 64, dtype=bf)
+    wg[:, :, 0] = 1
+    wu[:, :, 1] = 1
+    out = torch.empty(len(pairs), n, dtype=bf, device=dev)
+    off = _offsets([len(pairs)], dev)
+    e3.eagle3_grouped_linear(x.to(dev), wg.to(dev), off, out, epilogue=e3.EPI_SWIGLU, w2=wu.to(dev))
+    want, tol = _silu_tol(_np(x[:, 0]), _np(x[:, 1]))
+    assert (np.abs(_np(out) - want[:, None]) <= tol[:, None]).all()
+    wg[:, :, 0] = 2   # the sum passes fp32's range: +inf
+    e3.eagle3_grouped_linear(x.to(dev), wg.to(dev), off, out, epilogue=e3.EPI_SWIGLU, w2=wu.to(dev))
+    assert (out[-2:] == float("inf")).all()
+
+
+def test_offsets_past_32_bits():
+    """Rows, weights and slots further than 2^31 elements from their first."""
+    dev = require_gpu()
+    g = torch.Generator().manual_seed(11)
+    k, n, far = 4096, 1100, 600000
+    x = torch.empty(far, k, dtype=bf, device=dev)
+    ids = torch.tensor([far - 1, 0, far - 3], dtype=i32, device=dev)
+    x[ids.long()] = torch.randn(3, k, generator=g).to(bf).to(dev)
+    w = torch.empty(512, n, k, dtype=bf, device=dev)
+    used = [0, 511]
+    w[used] = (torch.randn(2, n, k, generator=g) * k ** -0.5).to(bf).to(dev)
+    off = torch.ones(513, dtype=i32, device=dev)   # row 0 by group 0, rows 1 and 2 by group 511
+    off[0], off[512] = 0, 3
+    out = torch.empty(3, n, dtype=bf, device=dev)
+    e3.eagle3_grouped_linear(x, w, off, out, row_ids=ids)
+    want, S, _, _ = moe.grouped_linear(_np(x[ids.long()]), _np(w[used]), np.array([0, 1, 3]))
+    tol = 2 * U * k * S
+    assert (np.abs(_np(out) - want) <= tol + BF16 * (np.abs(want) + tol) + TINY).all()
+    slots = torch.tensor([[far - 1, 0], [-1, far - 3]], dtype=i32, device=dev)
+    res = torch.empty(2, k, dtype=bf, device=dev)
+    e3.eagle3_moe_combine(x, slots, torch.ones(2, 2, device=dev), res)
+    want = _np(x[ids.long()])
+    want = np.stack([want[0] + want[1], want[2]])
+    assert (np.abs(_np(res) - want) <= (BF16 + 4 * U) * (np.abs(want) + 1)).all()
