@@ -9,10 +9,13 @@
 // a search among its registers took 850 instructions a row of 256 logits and 8 places, twice as many.)  32
 // rows make a chunk; a row takes an expert at most once, so a chunk's choice of an expert is a 32-bit mask
 // of rows, and a place's rank within the chunk is the population count of the mask below its row: a stable
-// counting sort without any atomic whose order matters.  Up to 32 rows are one launch.  More rows are two:
-// the first also writes the places per (block, expert), the second adds the counts of the blocks before
-// its own (at most 152 blocks, so at most 152 x 512 words read from L2 per block), scans the experts and
-// places the rows.
+// counting sort without any atomic whose order matters.  Up to 256 rows are one launch of a thread-block
+// cluster, a chunk a block, whose places per expert the blocks read from one another's shared memory (64 rows
+// of 256 experts: 7.5 us by two launches and 15 with their host time, 7.1 and 7.6 by one; with more chunks a
+// block the rows are too few at a time: 512 rows 8.2 us by two launches, 12.6 by one).  More rows are two
+// launches: the first also writes the places per (block, expert), the second adds the counts of the blocks
+// before its own (at most 152 blocks, so at most 152 x 512 words read from L2 per block), scans the experts
+// and places the rows.
 //
 // Combining.  A thread owns 8 columns of a row (or four vectors of 2 or 1, by alignment) and adds the row's
 // top_k vectors in order in fp32; the loads of a row's places do not depend on one another.  Memory bound:
@@ -22,7 +25,7 @@
 
 #include "../../include/eagle3_chain.h"
 #include "../../include/eagle3_moe.h"
-#include "common.cuh"
+#include "tc.cuh"
 
 namespace e3 {
 namespace {
@@ -30,6 +33,7 @@ namespace {
 constexpr int CHUNK = 32;             // rows of a mask
 constexpr int ROUTE_THREADS = 1024;   // a warp per row of a chunk
 constexpr int ROUTE_MAX_BLOCKS = 152;
+constexpr int ROUTE_RANKS = 8;        // largest cluster (one launch)
 constexpr int MAX_E = EAGLE3_MOE_MAX_EXPERTS;
 
 struct RouteParams {
@@ -41,8 +45,9 @@ struct RouteParams {
     int32_t *ids;
     float *weights;
     int32_t *offsets, *sorted, *slots, *dev_status;
-    int32_t *counts;      // [blocks][E rounded up to 4] places per block (more than one block)
+    int32_t *counts;      // [blocks][E rounded up to 4] places per block (two launches)
     int chunks_per_block; // rows of block b: [b, b + 1) * chunks_per_block * CHUNK
+    int ranks;            // one launch: blocks, a cluster; 0: two launches
 };
 
 E3_DEV int route_limit(const RouteParams &p) {
@@ -175,20 +180,20 @@ E3_DEV void place(const RouteParams &p, int row0, int r, int id, const uint32_t 
     p.slots[(size_t)row0 * p.k + threadIdx.x] = slot;
 }
 
-// Experts and weights of every row; with one block also the offsets and slots, otherwise the places
-// per expert of this block's rows.
+// Experts and weights of every row; and in one launch the offsets and slots, in two the places per expert of
+// this block's rows.
 template <int PER>
 __global__ void __launch_bounds__(ROUTE_THREADS) moe_route_kernel(const RouteParams p) {
     extern __shared__ uint32_t lists[];
     __shared__ uint32_t masks[MAX_E];
-    __shared__ int base[MAX_E], warp_sums[32];
+    __shared__ int base[MAX_E], counts[MAX_E], warp_sums[32];
     pdl_wait();
     pdl_trigger();
     const int limit = route_limit(p);
-    const int warp = threadIdx.x >> 5;
+    const int warp = threadIdx.x >> 5, first_row = blockIdx.x * p.chunks_per_block * CHUNK;
     int mine = 0;   // thread e: places of expert e in this block
     for (int c = 0; c < p.chunks_per_block; ++c) {
-        const int row0 = (blockIdx.x * p.chunks_per_block + c) * CHUNK, row = row0 + warp;
+        const int row = first_row + c * CHUNK + warp;
         if (threadIdx.x < MAX_E) masks[threadIdx.x] = 0u;
         __syncthreads();
         if (row < p.rows) {
@@ -197,22 +202,39 @@ __global__ void __launch_bounds__(ROUTE_THREADS) moe_route_kernel(const RoutePar
         }
         __syncthreads();
         if (threadIdx.x < MAX_E) mine += __popc(masks[threadIdx.x]);
-        if (gridDim.x > 1) __syncthreads();
+        if (!p.ranks) __syncthreads();
     }
-    if (gridDim.x > 1) {
+    if (!p.ranks) {
         if (threadIdx.x < p.E) p.counts[(size_t)blockIdx.x * ((p.E + 3) & ~3) + threadIdx.x] = mine;
         return;
     }
-    // a single block holds a single chunk
-    int total;
-    const int start = scan_experts(mine, warp_sums, &total);
-    if (threadIdx.x < MAX_E) base[threadIdx.x] = start;
-    if (threadIdx.x < p.E) p.offsets[threadIdx.x] = start;
-    if (threadIdx.x == 0) p.offsets[p.E] = total;
+    // one launch: every block holds a single chunk
+    int all = mine, before = 0, total;   // of all ranks, of the ranks before this one
+    if (p.ranks > 1) {
+        if (threadIdx.x < MAX_E) counts[threadIdx.x] = mine;
+        tc::cluster_sync();
+        if (threadIdx.x < MAX_E) {
+            all = 0;
+            const uint32_t at = smem_u32(counts + threadIdx.x);
+            for (int s = 0; s < p.ranks; ++s) {
+                const int n = (int)__float_as_uint(tc::cluster_ld(tc::cluster_addr(at, s)));
+                all += n;
+                before += s < (int)blockIdx.x ? n : 0;
+            }
+        }
+    }
+    const int start = scan_experts(all, warp_sums, &total);
+    if (threadIdx.x < MAX_E) base[threadIdx.x] = start + before;
+    if (blockIdx.x == 0) {
+        if (threadIdx.x < p.E) p.offsets[threadIdx.x] = start;
+        if (threadIdx.x == 0) p.offsets[p.E] = total;
+    }
     __syncthreads();
     const int r = threadIdx.x / p.k;
-    place(p, 0, r, chunk_place(p, 0, r), masks, base);
-    for (int s = total + threadIdx.x; s < p.rows * p.k; s += ROUTE_THREADS) p.sorted[s] = -1;
+    place(p, first_row, r, chunk_place(p, first_row, r), masks, base);
+    for (int s = total + blockIdx.x * ROUTE_THREADS + threadIdx.x; s < p.rows * p.k; s += p.ranks * ROUTE_THREADS)
+        p.sorted[s] = -1;
+    if (p.ranks > 1) tc::cluster_sync();   // no rank leaves while another reads its counts
 }
 
 __global__ void __launch_bounds__(ROUTE_THREADS) moe_place_kernel(const RouteParams p) {
@@ -388,16 +410,18 @@ __global__ void __launch_bounds__(COMBINE_THREADS) moe_combine_kernel(const Comb
 
 // ---- host side ----------------------------------------------------------------------------------
 struct RoutePlan {
-    int blocks, chunks_per_block;
+    int blocks, chunks_per_block, ranks;
     size_t ws_bytes;
 };
 
 RoutePlan route_plan(const eagle3_moe_route_args_t *a) {
     const int chunks = (a->rows + CHUNK - 1) / CHUNK;
     RoutePlan pl;
+    const bool one = chunks <= ROUTE_RANKS;
     pl.chunks_per_block = std::max(1, (chunks + ROUTE_MAX_BLOCKS - 1) / ROUTE_MAX_BLOCKS);
     pl.blocks = std::max(1, (chunks + pl.chunks_per_block - 1) / pl.chunks_per_block);
-    pl.ws_bytes = pl.blocks > 1 ? (size_t)pl.blocks * ((a->n_experts + 3) & ~3) * sizeof(int32_t) : 0;
+    pl.ranks = one ? pl.blocks : 0;
+    pl.ws_bytes = !one ? (size_t)pl.blocks * ((a->n_experts + 3) & ~3) * sizeof(int32_t) : 0;
     return pl;
 }
 
@@ -408,7 +432,8 @@ eagle3_status_t validate(const eagle3_moe_route_args_t *a) {
     if ((a->renormalize != 0 && a->renormalize != 1) || !std::isfinite(a->scale)) return EAGLE3_ERR_INVALID_ARGUMENT;
     if (a->ld_logits && a->ld_logits < a->n_experts) return EAGLE3_ERR_INVALID_ARGUMENT;
     if (a->n_experts > EAGLE3_MOE_MAX_EXPERTS || a->top_k > EAGLE3_MOE_MAX_TOP_K) return EAGLE3_ERR_UNSUPPORTED;
-    if ((int64_t)a->rows * a->top_k > MAX_DIM) return EAGLE3_ERR_UNSUPPORTED;   // slots are 32-bit
+    // slots are 32-bit, and rows rounded up to whole blocks (at most a 152nd of them)
+    if ((int64_t)a->rows * a->top_k > MAX_DIM - (1 << 24)) return EAGLE3_ERR_UNSUPPORTED;
     if (!a->expert_offsets) return EAGLE3_ERR_INVALID_ARGUMENT;
     if (a->rows && (!a->logits || !a->topk_ids || !a->topk_weights || !a->sorted_rows || !a->slots))
         return EAGLE3_ERR_INVALID_ARGUMENT;
@@ -441,7 +466,20 @@ cudaError_t launch_route(int blocks, cudaStream_t st, const RouteParams &p) {
         return cudaFuncSetAttribute(moe_route_kernel<PER>, cudaFuncAttributeMaxDynamicSharedMemorySize, LISTS);
     });
     if (e != cudaSuccess) return e;
-    return launch_pdl(moe_route_kernel<PER>, dim3(blocks), dim3(ROUTE_THREADS), LISTS, st, p);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(ROUTE_THREADS);
+    cfg.dynamicSmemBytes = LISTS;
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = std::max(1, p.ranks);
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = p.ranks > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, moe_route_kernel<PER>, p);
 }
 
 template <int VEC, int VECS>
@@ -485,6 +523,7 @@ extern "C" eagle3_status_t eagle3_moe_route(const eagle3_moe_route_args_t *a, vo
     p.dev_status = a->dev_status;
     p.counts = (int32_t *)workspace;
     p.chunks_per_block = pl.chunks_per_block;
+    p.ranks = pl.ranks;
     const cudaStream_t s = (cudaStream_t)stream;
     const int per = (a->n_experts + 31) / 32;
     const cudaError_t e = per <= 2   ? launch_route<2>(pl.blocks, s, p)
@@ -492,7 +531,7 @@ extern "C" eagle3_status_t eagle3_moe_route(const eagle3_moe_route_args_t *a, vo
                           : per <= 8 ? launch_route<8>(pl.blocks, s, p)
                                      : launch_route<16>(pl.blocks, s, p);
     if (e != cudaSuccess) return EAGLE3_ERR_CUDA;
-    if (pl.blocks > 1 && launch_pdl(moe_place_kernel, dim3(pl.blocks), dim3(ROUTE_THREADS), 0, s, p) != cudaSuccess)
+    if (!pl.ranks && launch_pdl(moe_place_kernel, dim3(pl.blocks), dim3(ROUTE_THREADS), 0, s, p) != cudaSuccess)
         return EAGLE3_ERR_CUDA;
     return EAGLE3_OK;
 }

@@ -65,7 +65,7 @@ def _check_route(z, k, status=0, **kw):
 
 
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 64, 8), (5, 33, 16), (31, 8, 2), (32, 512, 8), (33, 512, 16), (60, 20, 3),
-                                   (64, 64, 6), (65, 128, 8), (1000, 256, 8), (3840, 100, 4), (6000, 7, 7)])
+                                   (64, 64, 6), (65, 128, 8), (200, 512, 16), (256, 30, 5), (257, 64, 8), (1000, 256, 8), (3840, 100, 4), (6000, 7, 7)])
 @pytest.mark.parametrize("sigmoid,renorm", [(False, True), (True, False)])
 def test_route(T, E, k, sigmoid, renorm):
     dev = require_gpu()
@@ -75,7 +75,7 @@ def test_route(T, E, k, sigmoid, renorm):
 
 @pytest.mark.parametrize("sigmoid", [False, True])
 @pytest.mark.parametrize("renorm", [False, True])
-@pytest.mark.parametrize("T", [20, 75])
+@pytest.mark.parametrize("T", [20, 75, 300])
 def test_route_unavailable_and_tied(sigmoid, renorm, T):
     """Ties (among them -0 and +0), rows with fewer than k finite logits, with none, the lowest value."""
     dev = require_gpu()
@@ -92,7 +92,7 @@ def test_route_unavailable_and_tied(sigmoid, renorm, T):
     _check_route(z.to(dev), 6, sigmoid=sigmoid, renorm=renorm)
 
 
-@pytest.mark.parametrize("T,num_rows", [(20, 0), (20, 7), (20, 20), (300, 0), (300, 33), (300, 299), (5000, 4001)])
+@pytest.mark.parametrize("T,num_rows", [(20, 0), (20, 7), (20, 20), (200, 0), (200, 111), (300, 0), (300, 33), (300, 299), (5000, 4001)])
 def test_route_num_rows(T, num_rows):
     dev = require_gpu()
     z = torch.randn(T, 48, generator=torch.Generator().manual_seed(4)).to(dev)
@@ -375,7 +375,7 @@ def test_layer_eager_graph_and_side_stream():
 
 def test_calls_on_two_streams_at_once():
     dev = require_gpu()
-    layers = [_layer(dev, 300, 256, 256, 16, 4, seed=s) for s in (1, 2)]
+    layers = [_layer(dev, T, 256, 256, 16, 4, seed=T) for T in (300, 90)]
     for L in layers:
         _run_layer(L)
     torch.cuda.synchronize()

@@ -33,11 +33,12 @@ def _route(**kw):
     (dict(scale=float("inf")), 1),
     (dict(ld_logits=15), 1),
     (dict(rows=2 ** 30), 2),                 # more slots than 32 bits count
+    (dict(rows=2 ** 31 - 70000, top_k=1), 2),   # rows of whole blocks pass 32 bits
     (dict(logits=None), 1),
     (dict(slots=None), 1),
     (dict(rows=0, expert_offsets=None), 1),  # the offsets are written for no rows too
     (dict(topk_ids=18), 1),
-    (dict(), 6),                             # 40 rows need the workspace
+    (dict(rows=257), 6),                     # from 257 rows on with a workspace
 ])
 def test_route_refusals(kw, want):
     a = _route(**kw)
@@ -47,8 +48,8 @@ def test_route_refusals(kw, want):
 def test_route_workspace_size():
     L = built_lib()
     size = lambda **kw: L.eagle3_moe_route_workspace_size(ctypes.byref(_route(**kw)))
-    assert size(rows=0) == 0 and size(rows=32) == 0
-    assert size(rows=33) == 2 * 16 * 4
+    assert size(rows=0) == 0 and size(rows=32) == 0 and size(rows=256) == 0
+    assert size(rows=257) == 9 * 16 * 4
     assert size(rows=200000) <= 152 * 16 * 4
     assert size(rows=-1) == 0
     assert L.eagle3_moe_route_workspace_size(None) == 0
