@@ -192,6 +192,14 @@ E3_DEV void load_res8(const Fp8Params &p, int row, int col, float *v) {
             if (col + i < p.n) v[i] += res1(src + i);
     }
 }
+E3_DEV void add_quad(float *v, uint4 q) {   // 8 bf16
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] += __uint_as_float(w[i] << 16);
+        v[2 * i + 1] += __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
 E3_DEV uint4 pack8(const float *v) {
     uint32_t w[4];
 #pragma unroll
@@ -225,33 +233,69 @@ E3_DEV void store8(const Fp8Params &p, int row, int col, const float *v) {
     }
 }
 
-// 16 columns of up to 32 rows from a warp's box (64-byte rows in the 64-byte swizzle): this lane's column c of
-// rows r0, r0 + 2, ... below most.
-template <bool SWIGLU>
-E3_DEV void store_rows16(const Fp8Params &p, const uint8_t *box, int y, int col, int r0, int c, int most) {
-    const bool res = !SWIGLU && p.epi == EAGLE3_EPI_BF16_RESIDUAL, f32 = !SWIGLU && p.epi == EAGLE3_EPI_F32;
-    const __nv_bfloat16 *src = res ? p.residual + (size_t)(y + r0) * p.ld_res + col : nullptr;
-    const size_t at = (size_t)(y + r0) * p.ld_out + col;
+// A warp's staging box, 32 rows of 64 bytes in the 64-byte swizzle: 16-byte piece j, 4-byte word c and 2-byte half
+// c of row r.
+E3_DEV uint4 *box_quad(uint8_t *box, int r, int j) {
+    return reinterpret_cast<uint4 *>(box + r * 64 + ((j ^ ((r >> 1) & 3)) << 4));
+}
+E3_DEV uint32_t *box_word(uint8_t *box, int r, int c) {
+    return reinterpret_cast<uint32_t *>(box + r * 64 + (((c >> 2) ^ ((r >> 1) & 3)) << 4) + (c & 3) * 4);
+}
+E3_DEV unsigned short *box_half(uint8_t *box, int r, int c) {
+    return reinterpret_cast<unsigned short *>(box + r * 64 + (((c >> 3) ^ ((r >> 1) & 3)) << 4) + (c & 7) * 2);
+}
+// Rows of any alignment leave a box by half warps, two rows a store.  These loops are short code without branches,
+// 8 stores in flight: unrolled over a tile's rows and columns they were thousands of instructions, fetched anew
+// for every tile.
+E3_DEV void store_rows(uint8_t *box, float *o, int64_t ld, int rows, int most, int lane) {
+    const int c = lane & 15, h = lane >> 4;
+    o += h * ld + c;
+#pragma unroll 1
+    for (int r0 = h; r0 < rows + h; r0 += 16) {
+        uint32_t w[8];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {   // 8 rows at a time, their residuals first
-        float add[8];
+        for (int r = 0; r < 8; ++r) w[r] = *box_word(box, r0 + 2 * r, c);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = 16 * h + 2 * i;
-            add[i] = res && r + r0 < most ? res1(src + (size_t)r * p.ld_res) : 0.0f;
+        for (int r = 0; r < 8; ++r, o += 2 * ld)
+            if (r0 + 2 * r < rows && c < most) *o = __uint_as_float(w[r]);
+    }
+}
+// 32 bf16 columns, the first `most`.  Words leave on 4-byte boundaries: of a row that starts between two, lane c
+// takes columns 2 c - 1 and 2 c (none, for c = 0).  The columns that are left, a row's first or last, follow, a
+// row a lane.
+E3_DEV void store_rows(uint8_t *box, __nv_bfloat16 *out, int64_t ld, int rows, int most, int lane) {
+    unsigned short *base = reinterpret_cast<unsigned short *>(out);
+    const int c = lane & 15, h = lane >> 4, odd0 = (int)((uintptr_t)out >> 1) & 1, turn = (int)ld & 1;
+    const int odd = odd0 ^ (turn & h);   // rows h, h + 2, ... start between words
+    const bool in = 2 * c + 1 - odd < most && (c > 0 || !odd);
+    unsigned short *o = base + h * ld + 2 * c - odd;
+#pragma unroll 1
+    for (int r0 = h; r0 < rows + h; r0 += 16) {
+        uint32_t w[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) w[r] = *box_word(box, r0 + 2 * r, c);
+#pragma unroll
+        for (int r = 0; r < 8; ++r, o += 2 * ld) {
+            const uint32_t before = __shfl_up_sync(0xffffffffu, w[r], 1);
+            const uint32_t v = odd ? __byte_perm(before, w[r], 0x5432) : w[r];
+            if (in && r0 + 2 * r < rows) *reinterpret_cast<uint32_t *>(o) = v;
         }
+    }
+    const int mine = odd0 ^ (turn & lane);
+    unsigned short *row = base + (size_t)lane * ld;
+    if (lane < rows && mine) row[0] = *box_half(box, lane, 0);
+    if (lane < rows && ((most + mine) & 1)) row[most - 1] = *box_half(box, lane, most - 1);
+}
+// 32 columns, the first `most`, of `rows` rows from src to the box, 16 rows in flight
+E3_DEV void load_rows(uint8_t *box, const __nv_bfloat16 *src, int64_t ld, int rows, int most, int lane) {
+    const unsigned short *at = reinterpret_cast<const unsigned short *>(src) + lane;
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += 16) {
+        unsigned short a[16];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = 16 * h + 2 * i;
-            if (r + r0 >= most) continue;
-            float v = *reinterpret_cast<const float *>(box + (r + r0) * 64 + (((c >> 2) ^ (((r + r0) >> 1) & 3)) << 4) +
-                                                       (c & 3) * 4);
-            if (res) v += add[i];
-            if (f32)
-                ((float *)p.out)[at + (size_t)r * p.ld_out] = v;
-            else
-                ((__nv_bfloat16 *)p.out)[at + (size_t)r * p.ld_out] = __float2bfloat16_rn(v);
-        }
+        for (int r = 0; r < 16; ++r, at += ld) a[r] = r0 + r < rows && lane < most ? __ldcg(at) : (unsigned short)0;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) *box_half(box, r0 + r, lane) = a[r];
     }
 }
 
@@ -261,9 +305,10 @@ E3_DEV void store_rows16(const Fp8Params &p, const uint8_t *box, int y, int col,
 // epilogue takes 232 (128 x 40 + 256 x 232 = 64512): 128 accumulators, two loads of 16, scales.  The
 // epilogue is short of issue slots: the instructions around the 128 additions of a k-block (waits that
 // poll, addresses made anew) weigh as much as they do, so barriers go by precomputed shared-memory
-// addresses, a poll is a handful of instructions and the thread index stays in a register: 3840 x 2 * 14336 x
-// 4096 412 -> 337 us, 2680 TFLOP/s; 3840 x 6144 x 4096 74 us.  (Four groups of 64 accumulators and 104
-// registers: 358 us.)  What is left is still the epilogue: without its additions the kernel takes 265 us.
+// addresses, a poll is a handful of instructions, the thread index stays in a register, and the shared memory's
+// base is an offset to its symbol, not an integer made a pointer, whose accesses would be generic (337 -> 309 us):
+// 3840 x 2 * 14336 x 4096 412 -> 309 us, 2910 TFLOP/s; 3840 x 6144 x 4096 69 us.  (Four groups of 64 accumulators
+// and 104 registers: 358 us.)  What is left is still the epilogue: without its additions the kernel takes 265 us.
 constexpr int WIDE_BN = 256, WIDE_STAGES = 4, WIDE_EPI_WARPS = 8, WIDE_THREADS = 128 + 32 * WIDE_EPI_WARPS;
 constexpr int WIDE_EPI0 = 4;   // first epilogue warp
 constexpr int WIDE_RANKS = 8;  // largest cluster
@@ -275,11 +320,11 @@ constexpr int WIDE_BOX = 32 * 64;   // output staging: 32 rows x 64 bytes a warp
 // before), done when the MMAs have run, which both frees the stage and fills the buffer.  (With barriers
 // of their own for the buffers the issuing thread spent 640 cycles a k-block on waits and commits.)
 struct WideShared {
-    uint64_t full[WIDE_STAGES], done[WIDE_STAGES], mma_done;
+    uint64_t full[WIDE_STAGES], done[WIDE_STAGES], mma_done, res[WIDE_EPI_WARPS];
     uint32_t tmem_base;
     int abort;
 };
-constexpr int WIDE_SMEM = 1024 + WIDE_STAGES * WIDE_STAGE + WIDE_EPI_WARPS * WIDE_BOX + (int)sizeof(WideShared);
+constexpr int WIDE_SMEM = 1024 + WIDE_STAGES * WIDE_STAGE + 2 * WIDE_EPI_WARPS * WIDE_BOX + (int)sizeof(WideShared);
 static_assert(WIDE_SMEM <= 232448, "shared memory budget");
 
 // SPLIT: where rank src's sums of piece j (8 columns of each run, 128 rows) of an epilogue half lie in the ring
@@ -302,20 +347,20 @@ E3_DEV void registers_take() {
 // SPLIT: a cluster of p.ranks CTAs works on one tile, each on a range of the k-blocks.  Pieces of 8 columns of
 // both runs belong to the ranks in turn: each rank sends the others their pieces of its sums by remote stores
 // (reading them took three times as long), and adds up and finishes its own.
-// OUT: how outputs leave.  The variants are kernels of their own: what stands behind the main loop decides
-// whether its 128 accumulators and scales stay in registers (both ways in one kernel: 3840 x 2 * 14336 x 4096 346
-// -> 444 us).
+// OUT: how outputs leave; RES: with residuals.  The variants are kernels of their own: what stands behind the main
+// loop decides whether its 128 accumulators and scales stay in registers (stores by TMA and by the warps in one
+// kernel: 3840 x 2 * 14336 x 4096 346 -> 444 us).
 enum { OUT_TMA, OUT_STAGED, OUT_SPLIT };
-template <bool SWIGLU, int OUT>
+template <bool SWIGLU, int OUT, bool RES>
 __global__ void __launch_bounds__(WIDE_THREADS, 1)
     fp8_wide_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                     const __grid_constant__ CUtensorMap tm_w2, const __grid_constant__ CUtensorMap tm_out,
-                    const Fp8Params p) {
+                    const __grid_constant__ CUtensorMap tm_res, const Fp8Params p) {
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *ring = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t *ring = smem_raw + (-smem_u32(smem_raw) & 1023u);   // (the compiler knows it as shared memory)
     uint8_t *boxes = ring + WIDE_STAGES * WIDE_STAGE;
-    WideShared &sh = *reinterpret_cast<WideShared *>(boxes + WIDE_EPI_WARPS * WIDE_BOX);
-    constexpr bool SPLIT = OUT == OUT_SPLIT;
+    WideShared &sh = *reinterpret_cast<WideShared *>(boxes + 2 * WIDE_EPI_WARPS * WIDE_BOX);
+    constexpr bool SPLIT = OUT == OUT_SPLIT, RES_TMA = OUT == OUT_TMA && RES;
     const uint32_t tid = tc::thread_index();
     const int warp = (int)(tid >> 5), lane = (int)(tid & 31u);
 
@@ -325,6 +370,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
             tc::mbar_init(&sh.done[s], 1);
         }
         tc::mbar_init(&sh.mma_done, 1);
+        for (int w = 0; w < WIDE_EPI_WARPS; ++w) tc::mbar_init(&sh.res[w], 1);
         sh.abort = 0;
         tc::fence_barrier_init();
         tc::prefetch_tmap(&tm_x);
@@ -426,7 +472,9 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
         registers_take<232>();
         // ------------------------------------------------------------------ epilogue (warps 4..11)
         const int quarter = warp & 3, part = (warp - WIDE_EPI0) >> 2;
-        uint8_t *box = boxes + (warp - WIDE_EPI0) * WIDE_BOX;
+        uint8_t *box = boxes + (warp - WIDE_EPI0) * WIDE_BOX, *res_box = box + WIDE_EPI_WARPS * WIDE_BOX;
+        const uint32_t res_bar = smem_u32(&sh.res[warp - WIDE_EPI0]);
+        uint32_t res_phase = 0;
         // this thread's two runs of accumulator columns: neighbours, or gate and up of one run
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         const uint32_t run_a = lanes + (SWIGLU ? WIDE_RUN : 2 * WIDE_RUN) * part;
@@ -521,61 +569,77 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                 }
                 break;   // one tile a cluster
             }
-            if (SWIGLU) {
-#pragma unroll
-                for (int i = 0; i < WIDE_RUN; ++i) acc[i] = silu(acc[i]) * acc[WIDE_RUN + i];
-            }
             const int cols = SWIGLU ? WIDE_RUN : 2 * WIDE_RUN, y = mb * BM + quarter * 32;
             const int col0 = nb * (SWIGLU ? WIDE_BN / 2 : WIDE_BN) + cols * part;
-            const bool f32 = !SWIGLU && p.epi == EAGLE3_EPI_F32;
-            if (OUT == OUT_TMA && !SWIGLU && p.epi == EAGLE3_EPI_BF16_RESIDUAL && row < p.m) {
-#pragma unroll
-                for (int i = 0; i < 2 * WIDE_RUN; i += 8)
-                    if (col0 + i < p.n) load_res8(p, row, col0 + i, acc + i);
+            const bool f32 = !SWIGLU && !RES && p.epi == EAGLE3_EPI_F32;
+            const int rows = min(32, p.m - y), ln = lane;
+            // Residuals by TMA too, 32 columns at a time to a box of their own, the next while these are added and
+            // stored.  (Loads of a row a lane: 2000 x 6144 x 4096 66 us, 54 so; with the first box before the main
+            // loop 52, but 3840 x 4096 x 14336 in place 246 us in place of 218.)
+            if (RES_TMA && lane == 0 && col0 < p.n) {
+                tc::mbar_expect_tx(res_bar, WIDE_BOX);
+                tc::tma_load_2d(smem_u32(res_box), &tm_res, col0, y, res_bar);
             }
-            if (OUT == OUT_TMA) {
-                // pieces of 64 bytes: 32 bf16 or 16 fp32 columns of the warp's 32 rows, in the 64-byte swizzle
+            // pieces of 64 bytes: 32 bf16 or 16 fp32 columns of the warp's 32 rows, in the 64-byte swizzle
 #pragma unroll
-                for (int c = 0; c < WIDE_RUN / 8; ++c) {
-                    if (c * (f32 ? 16 : 32) >= cols) break;
-                    if (lane == 0) tc::bulk_wait_read<0>();   // the box's last store has read it
+            for (int c = 0; c < WIDE_RUN / 8; ++c) {
+                if (c * (f32 ? 16 : 32) >= cols) break;
+                const int x = col0 + c * (f32 ? 16 : 32);
+                if (OUT == OUT_TMA && lane == 0) tc::bulk_wait_read<0>();   // the box's last store has read it
+                __syncwarp();
+                if (SWIGLU) {
+#pragma unroll
+                    for (int i = 32 * c; i < 32 * c + 32; ++i) acc[i] = silu(acc[i]) * acc[WIDE_RUN + i];
+                }
+                if (RES_TMA && ok && x < p.n) {
+                    ok = tc::mbar_wait_warp(res_bar, res_phase, abort0);
+                    res_phase ^= 1u;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        add_quad(acc + c % (WIDE_RUN / 16) * 32 + 8 * j, *box_quad(res_box, lane, j));
+                    __syncwarp();
+                    if (ok && lane == 0 && c + 1 < 2 * WIDE_RUN / 32 && x + 32 < p.n) {
+                        tc::mbar_expect_tx(res_bar, WIDE_BOX);
+                        tc::tma_load_2d(smem_u32(res_box), &tm_res, x + 32, y, res_bar);
+                    }
+                } else if (OUT == OUT_STAGED && RES && x < p.n) {
+                    load_rows(box, p.residual + (size_t)y * p.ld_res + x, p.ld_res, rows, min(32, p.n - x), lane);
                     __syncwarp();
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint4 o;
-                        if (f32) {
-                            const float *v = acc + c * 16 + 4 * j;
-                            o = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                                           __float_as_uint(v[3]));
-                        } else {
-                            o = pack8(acc + c % (WIDE_RUN / 16) * 32 + 8 * j);
-                        }
-                        *reinterpret_cast<uint4 *>(box + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = o;
+                    for (int j = 0; j < 4; ++j) add_quad(acc + c % (WIDE_RUN / 16) * 32 + 8 * j, *box_quad(box, lane, j));
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint4 o;
+                    if (f32) {
+                        const float *v = acc + c * 16 + 4 * j;
+                        o = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                       __float_as_uint(v[3]));
+                    } else {
+                        o = pack8(acc + c % (WIDE_RUN / 16) * 32 + 8 * j);
                     }
+                    *box_quad(box, lane, j) = o;
+                }
+                if (OUT == OUT_TMA) {
                     tc::fence_proxy_async_smem();
                     __syncwarp();
-                    const int x = col0 + c * (f32 ? 16 : 32);
                     if (lane == 0 && x < p.n && y < p.m) {
                         tc::tma_store_2d(&tm_out, x, y, box);
                         tc::bulk_commit();
                     }
-                }
-            } else if (OUT == OUT_STAGED) {
-                // 16 columns of the warp's 32 rows at a time through the box, back by half warps that hold the 16
-                // columns of a row.  (Stores of a row a lane: 2000 x 6146 x 4096 139 us, 47 at 6144.)
-                const int c = lane & 15, r0 = lane >> 4;
-#pragma unroll
-                for (int i = 0; i < 2 * WIDE_RUN; i += 16) {
-                    if (i >= cols || col0 + i >= p.n) break;
+                } else {
                     __syncwarp();
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        *reinterpret_cast<float4 *>(box + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
-                            make_float4(acc[i + 4 * j], acc[i + 4 * j + 1], acc[i + 4 * j + 2], acc[i + 4 * j + 3]);
-                    __syncwarp();
-                    const int col = col0 + i + c;
-                    store_rows16<SWIGLU>(p, box, y, col, r0, c, col < p.n ? min(32, p.m - y) : 0);
+                    if (x >= p.n) continue;
+                    const size_t at = (size_t)y * p.ld_out + x;
+                    if (f32)
+                        store_rows(box, (float *)p.out + at, p.ld_out, rows, p.n - x, lane);
+                    else
+                        store_rows(box, (__nv_bfloat16 *)p.out + at, p.ld_out, rows, min(32, p.n - x), lane);
                 }
+            }
+            if (RES_TMA && !ok && lane == 0) {
+                flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
+                tc::mbar_drain(res_bar, res_phase ^ 1u);
             }
         }
         if (lane == 0) tc::bulk_wait<0>();
@@ -606,7 +670,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                     for (int i = 0; i < 8; ++i) a[i] = silu(a[i]) * b[i];
                     if (col0 + j < p.n) store8(p, row, col0 + j, a);
                 } else {
-                    const bool res = p.epi == EAGLE3_EPI_BF16_RESIDUAL;
+                    constexpr bool res = RES;
                     if (col0 + j < p.n) {
                         if (res) load_res8(p, row, col0 + j, a);
                         store8(p, row, col0 + j, a);
@@ -653,7 +717,7 @@ __global__ void __launch_bounds__(NARROW_THREADS, 2)
                       const __grid_constant__ CUtensorMap tm_w2, const Fp8Params p) {
     constexpr int BUFS = NARROW_TMEM / NT;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *ring = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t *ring = smem_raw + (-smem_u32(smem_raw) & 1023u);
     NarrowShared &sh = *reinterpret_cast<NarrowShared *>(ring + NARROW_RING);
     volatile int *abort = &sh.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -924,13 +988,13 @@ eagle3_status_t validate(const eagle3_linear_fp8_args_t *a) {
     return EAGLE3_OK;
 }
 
-// 32-row boxes of 64 bytes of the output, for TMA stores; false where its address or pitch rules them out
-bool out_map(CUtensorMap *m, const eagle3_linear_fp8_args_t *a, int64_t ld) {
-    const bool f32 = a->epilogue == EAGLE3_EPI_F32;
+// 32-row boxes of 64 bytes of an [m, n] matrix (the output, the residual), by TMA; false where its address or pitch
+// rules that out
+bool box_map(CUtensorMap *m, const eagle3_linear_fp8_args_t *a, const void *base, int64_t ld, bool f32) {
     const int es = f32 ? 4 : 2;
-    if (((uintptr_t)a->out & 15) || (ld * es) % 16) return false;
+    if (((uintptr_t)base & 15) || (ld * es) % 16) return false;
     const CUtensorMapDataType type = f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    return tmap_rows(m, type, es, a->out, a->m, a->n, ld, 32, 0, 0, 64);
+    return tmap_rows(m, type, es, base, a->m, a->n, ld, 32, 0, 0, 64);
 }
 
 template <int NT, bool SWIGLU>
@@ -960,9 +1024,9 @@ cudaError_t launch_narrow(dim3 grid, cudaStream_t st, const CUtensorMap &tx, con
 }
 
 // Clusters of `ranks` CTAs of the wide kernel that the device holds at once (0 on an error).
-template <bool SWIGLU, int OUT>
+template <bool SWIGLU, int OUT, bool RES>
 int wide_clusters(int ranks) {
-    if (cudaFuncSetAttribute(fp8_wide_kernel<SWIGLU, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, WIDE_SMEM) !=
+    if (cudaFuncSetAttribute(fp8_wide_kernel<SWIGLU, OUT, RES>, cudaFuncAttributeMaxDynamicSharedMemorySize, WIDE_SMEM) !=
         cudaSuccess)
         return 0;
     if (OUT != OUT_SPLIT) return device_sm_count();
@@ -977,22 +1041,22 @@ int wide_clusters(int ranks) {
     cfg.attrs = &at;
     cfg.numAttrs = 1;
     int n = 0;
-    return cudaOccupancyMaxActiveClusters(&n, fp8_wide_kernel<SWIGLU, OUT>, &cfg) == cudaSuccess ? n : 0;
+    return cudaOccupancyMaxActiveClusters(&n, fp8_wide_kernel<SWIGLU, OUT, RES>, &cfg) == cudaSuccess ? n : 0;
 }
 
 struct ClusterCounts {
     int n[WIDE_RANKS + 1];
 };
 
-template <bool SWIGLU>
+template <bool SWIGLU, bool RES>
 cudaError_t launch_wide(cudaStream_t st, const CUtensorMap &tx, const CUtensorMap &tw, const CUtensorMap &tw2,
-                        const CUtensorMap &to, Fp8Params &p) {
+                        const CUtensorMap &to, const CUtensorMap &tr, Fp8Params &p) {
     static PerDevice<ClusterCounts> cache;
     const ClusterCounts most = cache.get([] {
         ClusterCounts c = {};
-        c.n[1] = std::min(wide_clusters<SWIGLU, OUT_TMA>(1), wide_clusters<SWIGLU, OUT_STAGED>(1));
+        c.n[1] = std::min(wide_clusters<SWIGLU, OUT_TMA, RES>(1), wide_clusters<SWIGLU, OUT_STAGED, RES>(1));
         for (int r = 2; r <= WIDE_RANKS; ++r)
-            if (split_bytes(r) <= WIDE_STAGES * WIDE_STAGE) c.n[r] = wide_clusters<SWIGLU, OUT_SPLIT>(r);
+            if (split_bytes(r) <= WIDE_STAGES * WIDE_STAGE) c.n[r] = wide_clusters<SWIGLU, OUT_SPLIT, RES>(r);
         return c;
     });
     if (most.n[1] < 1) return cudaErrorUnknown;
@@ -1016,9 +1080,9 @@ cudaError_t launch_wide(cudaStream_t st, const CUtensorMap &tx, const CUtensorMa
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = p.ranks > 1 ? 2 : 1;
-    return p.ranks > 1 ? cudaLaunchKernelEx(&cfg, fp8_wide_kernel<SWIGLU, OUT_SPLIT>, tx, tw, tw2, to, p)
-           : p.tma_out ? cudaLaunchKernelEx(&cfg, fp8_wide_kernel<SWIGLU, OUT_TMA>, tx, tw, tw2, to, p)
-                       : cudaLaunchKernelEx(&cfg, fp8_wide_kernel<SWIGLU, OUT_STAGED>, tx, tw, tw2, to, p);
+    return p.ranks > 1 ? cudaLaunchKernelEx(&cfg, fp8_wide_kernel<SWIGLU, OUT_SPLIT, RES>, tx, tw, tw2, to, tr, p)
+           : p.tma_out ? cudaLaunchKernelEx(&cfg, fp8_wide_kernel<SWIGLU, OUT_TMA, RES>, tx, tw, tw2, to, tr, p)
+                       : cudaLaunchKernelEx(&cfg, fp8_wide_kernel<SWIGLU, OUT_STAGED, RES>, tx, tw, tw2, to, tr, p);
 }
 
 }  // namespace
@@ -1081,7 +1145,7 @@ extern "C" eagle3_status_t eagle3_linear_fp8(const eagle3_linear_fp8_args_t *a, 
     // 8 x 6144 x 4096: 8.0 us narrow, 14.7 wide; 64 x 6144 x 4096 (24 wide tiles): 13.3 and 13.3; 64 rows x
     // 2 * 14336 x 4096 (112): 31 and 25; 96 x 4096 x 14336: 34 (with tiles of 128 rows) and 20.
     const bool narrow = tiles_w <= 65535 && (a->m <= NARROW_MAX / 2 || (a->m <= NARROW_MAX && 2 * p.tiles_n < sms));
-    CUtensorMap tx, tw, tw2, to;
+    CUtensorMap tx, tw, tw2, to, tr;
     const int w_box = narrow ? (swiglu ? 16 : BM) : (swiglu ? WIDE_BN / 2 : WIDE_BN);
     if (!tmap_rows(&tx, u8, 1, a->x, a->m, a->k, ld_x, narrow ? 16 : BM) ||
         !tmap_rows(&tw, u8, 1, a->w, a->n, a->k, ld_w, w_box))
@@ -1106,12 +1170,14 @@ extern "C" eagle3_status_t eagle3_linear_fp8(const eagle3_linear_fp8_args_t *a, 
     } else {
         const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
         if (tiles > MAX_DIM) return EAGLE3_ERR_UNSUPPORTED;   // tiles are counted in 32 bits
-        // (a residual is added to rows a lane holds: by 16-byte loads or not at all)
-        const bool res8 = a->epilogue != EAGLE3_EPI_BF16_RESIDUAL ||
-                          (((uintptr_t)a->residual & 15) == 0 && p.ld_res % 8 == 0);
-        p.tma_out = res8 && out_map(&to, a, p.ld_out) ? 1 : 0;
+        const bool res = a->epilogue == EAGLE3_EPI_BF16_RESIDUAL;
+        p.tma_out = box_map(&to, a, a->out, p.ld_out, a->epilogue == EAGLE3_EPI_F32) &&
+                    (!res || box_map(&tr, a, a->residual, p.ld_res, false));
         if (!p.tma_out) to = tx;   // unused
-        e = swiglu ? launch_wide<true>(s, tx, tw, tw2, to, p) : launch_wide<false>(s, tx, tw, tw2, to, p);
+        if (!p.tma_out || !res) tr = tx;
+        e = swiglu                                      ? launch_wide<true, false>(s, tx, tw, tw2, to, tr, p)
+            : a->epilogue == EAGLE3_EPI_BF16_RESIDUAL ? launch_wide<false, true>(s, tx, tw, tw2, to, tr, p)
+                                                      : launch_wide<false, false>(s, tx, tw, tw2, to, tr, p);
     }
     return e == cudaSuccess ? EAGLE3_OK : EAGLE3_ERR_CUDA;
 }

@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
     grouped_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ CUtensorMap tm_w,
                    const __grid_constant__ CUtensorMap tm_w2, const GroupedParams p) {
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *ring = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint8_t *ring = smem_raw + (-smem_u32(smem_raw) & 1023u);   // (the compiler knows it as shared memory)
     Shared &sh = *reinterpret_cast<Shared *>(ring + RING_BYTES);
     const uint32_t tid = tc::thread_index();
     const int warp = (int)(tid >> 5), lane = (int)(tid & 31u);
