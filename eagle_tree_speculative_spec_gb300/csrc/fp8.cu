@@ -33,6 +33,7 @@ namespace {
 constexpr int BK = 128;                 // k values of a block and of a tile (128 bytes)
 constexpr int BM = 128;
 constexpr float E4M3_MAX = 448.0f;
+constexpr int MAX_RANKS = 8;            // largest cluster
 
 // (By the special function unit: the exponential is 2 + 1.2 |x| steps of fp32 off at the most and the division
 // 2, against a bf16 result's 2^15; 0 where exp(-x) passes 2^126, x below -87.3, where silu is above -2^-119.)
@@ -311,7 +312,6 @@ E3_DEV void load_rows(uint8_t *box, const __nv_bfloat16 *src, int64_t ld, int ro
 // and 104 registers: 358 us.)  What is left is still the epilogue: without its additions the kernel takes 265 us.
 constexpr int WIDE_BN = 256, WIDE_STAGES = 4, WIDE_EPI_WARPS = 8, WIDE_THREADS = 128 + 32 * WIDE_EPI_WARPS;
 constexpr int WIDE_EPI0 = 4;   // first epilogue warp
-constexpr int WIDE_RANKS = 8;  // largest cluster
 constexpr int WIDE_RUN = 512 / WIDE_EPI_WARPS;   // accumulator columns of a thread: two runs of this many
 constexpr int WIDE_A = BM * BK, WIDE_B = WIDE_BN * BK, WIDE_STAGE = WIDE_A + WIDE_B;
 constexpr int WIDE_BOX = 32 * 64;   // output staging: 32 rows x 64 bytes a warp
@@ -696,7 +696,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
 
 // ---- narrow -------------------------------------------------------------------------------------
 constexpr int NARROW_EPI_WARPS = 8, NARROW_THREADS = 64 + 32 * NARROW_EPI_WARPS, NARROW_MAX = 64;
-constexpr int NARROW_STAGES = 8, NARROW_TMEM = 256, NARROW_CLUSTER = 8;
+constexpr int NARROW_STAGES = 8, NARROW_TMEM = 256;
 constexpr int NARROW_RING = 106 * 1024;   // two CTAs a SM
 constexpr int NARROW_W = BM * BK;
 struct NarrowShared {
@@ -997,15 +997,47 @@ bool box_map(CUtensorMap *m, const eagle3_linear_fp8_args_t *a, const void *base
     return tmap_rows(m, type, es, base, a->m, a->n, ld, 32, 0, 0, 64);
 }
 
+// Clusters of `ranks` CTAs of a kernel that the device holds at once (0 on an error).
+template <class Kernel>
+int resident_clusters(Kernel *kernel, int ranks, int threads, int smem) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ranks * device_sm_count());
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = ranks;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : 0;
+}
+struct ClusterCounts {
+    int n[MAX_RANKS + 1];
+};
+
 template <int NT, bool SWIGLU>
-cudaError_t launch_narrow(dim3 grid, cudaStream_t st, const CUtensorMap &tx, const CUtensorMap &tw,
+cudaError_t launch_narrow(int tiles, cudaStream_t st, const CUtensorMap &tx, const CUtensorMap &tw,
                           const CUtensorMap &tw2, const Fp8Params &p) {
-    static PerDevice<cudaError_t> attr;
-    const cudaError_t e = attr.get([] {
-        return cudaFuncSetAttribute(fp8_narrow_kernel<NT, SWIGLU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    NARROW_SMEM);
+    static PerDevice<ClusterCounts> cache;
+    const ClusterCounts most = cache.get([] {
+        ClusterCounts c = {};
+        if (cudaFuncSetAttribute(fp8_narrow_kernel<NT, SWIGLU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 NARROW_SMEM) == cudaSuccess)
+            for (int r = 1; r <= MAX_RANKS; ++r)
+                c.n[r] = resident_clusters(fp8_narrow_kernel<NT, SWIGLU>, r, NARROW_THREADS, NARROW_SMEM);
+        return c;
     });
-    if (e != cudaSuccess) return e;
+    if (most.n[1] < 1) return cudaErrorUnknown;
+    // As many ranks as leave every tile a resident cluster, two k-blocks each at least.  The query counts one CTA a
+    // SM; shared memory, registers and TMEM hold two, and two keep more loads in flight (8 rows, 99 tiles of 2 *
+    // 6306 x 11040: 45 us by single CTAs, 28 by clusters of two, 41 by three, of which 92 are resident; 48 tiles of
+    // 6144 x 4096: 8.2 us by three ranks, 7.1 by four, 11.8 by six, of which 46 are).
+    int ranks = 1;
+    for (int r = 2; r <= MAX_RANKS; ++r)
+        if (tiles <= 2 * most.n[r] && p.kb_total >= 2 * r) ranks = r;
+    const dim3 grid(ranks, tiles);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(NARROW_THREADS);
@@ -1023,30 +1055,14 @@ cudaError_t launch_narrow(dim3 grid, cudaStream_t st, const CUtensorMap &tx, con
     return cudaLaunchKernelEx(&cfg, fp8_narrow_kernel<NT, SWIGLU>, tx, tw, tw2, p);
 }
 
-// Clusters of `ranks` CTAs of the wide kernel that the device holds at once (0 on an error).
 template <bool SWIGLU, int OUT, bool RES>
 int wide_clusters(int ranks) {
     if (cudaFuncSetAttribute(fp8_wide_kernel<SWIGLU, OUT, RES>, cudaFuncAttributeMaxDynamicSharedMemorySize, WIDE_SMEM) !=
         cudaSuccess)
         return 0;
     if (OUT != OUT_SPLIT) return device_sm_count();
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ranks * device_sm_count());
-    cfg.blockDim = dim3(WIDE_THREADS);
-    cfg.dynamicSmemBytes = WIDE_SMEM;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = ranks;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    int n = 0;
-    return cudaOccupancyMaxActiveClusters(&n, fp8_wide_kernel<SWIGLU, OUT, RES>, &cfg) == cudaSuccess ? n : 0;
+    return resident_clusters(fp8_wide_kernel<SWIGLU, OUT, RES>, ranks, WIDE_THREADS, WIDE_SMEM);
 }
-
-struct ClusterCounts {
-    int n[WIDE_RANKS + 1];
-};
 
 template <bool SWIGLU, bool RES>
 cudaError_t launch_wide(cudaStream_t st, const CUtensorMap &tx, const CUtensorMap &tw, const CUtensorMap &tw2,
@@ -1055,7 +1071,7 @@ cudaError_t launch_wide(cudaStream_t st, const CUtensorMap &tx, const CUtensorMa
     const ClusterCounts most = cache.get([] {
         ClusterCounts c = {};
         c.n[1] = std::min(wide_clusters<SWIGLU, OUT_TMA, RES>(1), wide_clusters<SWIGLU, OUT_STAGED, RES>(1));
-        for (int r = 2; r <= WIDE_RANKS; ++r)
+        for (int r = 2; r <= MAX_RANKS; ++r)
             if (split_bytes(r) <= WIDE_STAGES * WIDE_STAGE) c.n[r] = wide_clusters<SWIGLU, OUT_SPLIT, RES>(r);
         return c;
     });
@@ -1065,7 +1081,7 @@ cudaError_t launch_wide(cudaStream_t st, const CUtensorMap &tx, const CUtensorMa
     // by two, 21 by four; 256 x 1024 x 2048, 16 k-blocks: 9.4 and 11.8 us).
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
     p.ranks = 1;
-    for (int r = 2; r <= WIDE_RANKS; ++r)
+    for (int r = 2; r <= MAX_RANKS; ++r)
         if (tiles <= most.n[r] && p.kb_total - p.kb_total / r >= 18) p.ranks = r;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)std::min<int64_t>(most.n[p.ranks], tiles) * p.ranks);
@@ -1158,15 +1174,12 @@ extern "C" eagle3_status_t eagle3_linear_fp8(const eagle3_linear_fp8_args_t *a, 
     if (narrow) {
         p.n16 = (a->m + 15) / 16 * 16;
         p.stages = std::min(NARROW_STAGES, NARROW_RING / (NARROW_W + p.n16 * BK));
-        int ranks = 1;
-        while (ranks < NARROW_CLUSTER && (int64_t)tiles_w * (ranks + 1) <= sms && p.kb_total >= 2 * (ranks + 1)) ++ranks;
-        const dim3 grid(ranks, tiles_w);
         if (p.n16 <= 32)
-            e = swiglu ? launch_narrow<32, true>(grid, s, tx, tw, tw2, p)
-                       : launch_narrow<32, false>(grid, s, tx, tw, tw2, p);
+            e = swiglu ? launch_narrow<32, true>(tiles_w, s, tx, tw, tw2, p)
+                       : launch_narrow<32, false>(tiles_w, s, tx, tw, tw2, p);
         else
-            e = swiglu ? launch_narrow<64, true>(grid, s, tx, tw, tw2, p)
-                       : launch_narrow<64, false>(grid, s, tx, tw, tw2, p);
+            e = swiglu ? launch_narrow<64, true>(tiles_w, s, tx, tw, tw2, p)
+                       : launch_narrow<64, false>(tiles_w, s, tx, tw, tw2, p);
     } else {
         const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
         if (tiles > MAX_DIM) return EAGLE3_ERR_UNSUPPORTED;   // tiles are counted in 32 bits
