@@ -448,3 +448,27 @@ def test_offsets_past_32_bits():
     want = _np(x[ids.long()])
     want = np.stack([want[0] + want[1], want[2]])
     assert (np.abs(_np(res) - want) <= (BF16 + 4 * U) * (np.abs(want) + 1)).all()
+
+
+def test_readme_example():
+    """The documentation's mixture-of-experts and 8-bit example, run as written."""
+    dev = require_gpu()
+    import os
+    import re
+
+    from oracle import fp8
+    from tests._util import ROOT
+    text = open(os.path.join(ROOT, "README.md")).read()
+    code = [b for b in re.findall(r"```python\n(.*?)```", text, flags=re.S) if "eagle3_moe_route" in b]
+    assert len(code) == 1
+    v = {}
+    exec(code[0], v)
+    torch.cuda.synchronize()
+    L = dict(z=v["logits"], ids=v["ids"], x=v["x"], wg=v["wg"], wu=v["wu"], wd=v["wd"], res=v["res"])
+    want = _layer_ref(L, v["T"])
+    # as in the layer test above: two roundings of intermediates and one of the output
+    assert (np.abs(_np(v["out"]) - want) <= 8 * BF16 * (1 + np.abs(want))).all()
+    codes, scale = fp8.quantize(v["out"].float().cpu().numpy())
+    y, S = fp8.linear(codes, scale, v["w8"].view(torch.uint8).cpu().numpy(), v["w_scale"].cpu().numpy())
+    tol = (256 + 3 + scale.shape[0]) * U * S
+    assert (np.abs(_np(v["proj"]) - y) <= tol + BF16 * (np.abs(y) + tol) + TINY).all()
