@@ -26,6 +26,8 @@
 // groups are small and the call is bound by its weights' bytes.  Units run group by group, row tile
 // fastest, so that the CTAs that share a weight tile run together.
 //
+// Where the units leave SMs idle, a cluster shares each one's k-blocks (SPLIT, below).
+//
 // Every mbarrier wait is bounded; on a timeout the kernel records EAGLE3_DEV_TIMEOUT, stops issuing
 // work, drains its own TMA loads and frees its TMEM.
 #include <algorithm>
@@ -78,6 +80,7 @@ struct GroupedParams {
     const int32_t *offsets, *row_ids;
     int32_t *dev_status;
     int paired;   // rows of out start on 4 bytes: two columns a store
+    int ranks;    // SPLIT: CTAs of a cluster
 };
 
 // Row tiles of a group of cnt rows, and the rows of each but the last: even shares (in multiples of
@@ -166,7 +169,21 @@ E3_DEV void store_pair(const GroupedParams &p, int row, int col, float a, float 
 // own time, in place of 750 (3840 rows x 8 of 64 experts, k = 4096, 2 x 1024 columns: 377 -> 325 us, 1586
 // TFLOP/s; k = 1024, 4096 columns: 206 -> 179 us).  The odd CTA's stages are announced to the even one by a
 // thread that waits for them and arrives on its barrier; commits go to the barriers of both.
-template <bool SWIGLU, bool GATHER, bool PAIR>
+
+// SPLIT: a cluster of p.ranks CTAs works on one unit, each on a range of the k-blocks, where the units leave SMs
+// idle.  Chunks of 8 rows of the tile belong to the ranks in turn: each sends the others their chunks of its sums
+// by remote stores over their rings, adds up its own in rank order and finishes them.
+enum { SINGLE, PAIRED, SPLIT_K };
+constexpr int SPLIT_ROWS = 8;   // rows of a chunk
+__host__ __device__ constexpr int split_bytes(int ranks) {
+    return ranks * ((MAX_ROWS / SPLIT_ROWS + ranks - 1) / ranks) * SPLIT_ROWS * BM * 4;
+}
+static_assert(split_bytes(2) <= RING_BYTES && split_bytes(3) <= RING_BYTES && split_bytes(4) <= RING_BYTES &&
+                  split_bytes(5) <= RING_BYTES && split_bytes(6) <= RING_BYTES && split_bytes(7) <= RING_BYTES &&
+                  split_bytes(8) <= RING_BYTES,
+              "the ranks' sums fit the ring");
+
+template <bool SWIGLU, bool GATHER, int MODE>
 __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1)
     grouped_kernel(const __grid_constant__ RowMaps tm_x, const __grid_constant__ CUtensorMap tm_w,
                    const __grid_constant__ CUtensorMap tm_w2, const GroupedParams p) {
@@ -175,9 +192,14 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
     Shared &sh = *reinterpret_cast<Shared *>(ring + RING_BYTES);
     const uint32_t tid = tc::thread_index();
     const int warp = (int)(tid >> 5), lane = (int)(tid & 31u);
+    constexpr bool PAIR = MODE == PAIRED, SPLIT = MODE == SPLIT_K;
     constexpr int STEP = PAIR ? 32 : 16;
     const int rank = PAIR ? (int)(blockIdx.x & 1u) : 0;   // in the pair (a cluster of two)
-    const int unit0 = (int)blockIdx.x >> (PAIR ? 1 : 0), unit_step = (int)gridDim.x >> (PAIR ? 1 : 0);
+    const int unit0 = SPLIT ? (int)blockIdx.x / p.ranks : (int)blockIdx.x >> (PAIR ? 1 : 0);
+    const int unit_step = SPLIT ? (int)gridDim.x : (int)gridDim.x >> (PAIR ? 1 : 0);   // (SPLIT: one unit)
+    const int part = SPLIT ? (int)blockIdx.x % p.ranks : 0;                            // range of the k-blocks
+    const int kb0 = SPLIT ? (int)((long long)p.kb_total * part / p.ranks) : 0;
+    const int kb1 = SPLIT ? (int)((long long)p.kb_total * (part + 1) / p.ranks) : p.kb_total;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < MAX_STAGES; ++s) {
@@ -272,7 +294,7 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
                 const Unit w = unit_at<STEP>(sh, p, u);
                 const int mine = w.n16 / (PAIR ? 2 : 1), boxes = box_rows(mine);   // rows that this CTA loads
                 const int row0 = w.row0 + rank * mine, mt = PAIR ? 2 * w.mt + rank : w.mt;
-                for (int kb = 0; kb < p.kb_total; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     const uint32_t full = full0 + stage * 8;
                     if (!tc::mbar_wait(empty0 + stage * 8, phase ^ 1u, abort0)) {
                         ok = false;
@@ -322,7 +344,7 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
                 uint32_t phase = 0;
                 bool ok = true;
                 for (int u = unit0; ok && u < units; u += unit_step)
-                    for (int kb = 0; kb < p.kb_total; ++kb) {
+                    for (int kb = kb0; kb < kb1; ++kb) {
                         if (!tc::mbar_wait(full0 + stage * 8, phase, abort0)) {
                             ok = false;
                             break;
@@ -350,7 +372,7 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
                 }
                 tc::fence_after();
                 const uint32_t d = tmem + (uint32_t)(acc * MAX_ROWS);
-                for (int kb = 0; kb < p.kb_total; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     if (!tc::mbar_wait(full0 + stage * 8, phase, abort0)) {
                         ok = false;
                         break;
@@ -361,7 +383,7 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
                     const uint64_t a = desc0 + (uint32_t)(stage * stage_bytes >> 4), b = a + (W_BYTES >> 4);
 #pragma unroll
                     for (int k = 0; k < BK / 16; ++k) {
-                        const uint32_t add = kb > 0 || k > 0 ? 1u : 0u;
+                        const uint32_t add = kb > kb0 || k > 0 ? 1u : 0u;
                         if (PAIR)
                             tc::mma2_bf16_ss(d, a + k * 2, b + k * 2, idesc, add);
                         else
@@ -418,7 +440,7 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
                 }
                 src[i] = p.x + (size_t)v * p.ld_x + piece * 8;
             }
-            for (int kb = 0; kb < p.kb_total; ++kb) {
+            for (int kb = kb0; kb < kb1; ++kb) {
                 if (!tc::mbar_wait_warp(empty0 + stage * 8, phase ^ 1u, abort0)) {
                     ok = false;
                     break;
@@ -444,6 +466,7 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
         const uint32_t tempty_even = PAIR ? tc::cluster_addr(tempty0, 0) : tempty0;
         int acc = 0;
         uint32_t acc_phase = 0;
+        Unit unit = {};   // SPLIT: the cluster's
         for (int u = unit0; u < units; u += unit_step) {
             const Unit w = unit_at<STEP>(sh, p, u);
             bool ok = tc::mbar_wait_warp(tfull0 + acc * 8, acc_phase, abort0);
@@ -455,6 +478,25 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
             }
             tc::fence_after();
             const uint32_t t_col = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * MAX_ROWS);
+            if (SPLIT) {
+                unit = w;
+                tc::cluster_sync();   // all ranks' loads and MMAs have completed
+                const int chunks = w.n16 / SPLIT_ROWS, each = (chunks + p.ranks - 1) / p.ranks;
+                for (int c = 0; c < w.n16; c += 32) {
+                    float v[32];
+                    tc::tmem_ld32(t_col + c, v);
+#pragma unroll
+                    for (int i = 0; i < 32; i += SPLIT_ROWS) {
+                        const int j = (c + i) / SPLIT_ROWS, to = j % p.ranks;
+                        if (j >= chunks) continue;
+                        const uint32_t at = tc::cluster_addr(ring0, to) +
+                                            (uint32_t)(((part * each + j / p.ranks) * SPLIT_ROWS * BM + quarter * 32 + lane) * 4);
+#pragma unroll
+                        for (int r = 0; r < SPLIT_ROWS; ++r) tc::cluster_st(at + r * BM * 4, v[i + r]);
+                    }
+                }
+                break;
+            }
             const bool odd = lane & 1;
             const int mt = PAIR ? 2 * w.mt + rank : w.mt;
             // rows r, r + 1, ... of this lane's column: an even lane stores both columns of row r, its
@@ -521,6 +563,42 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
             acc ^= 1;
         }
         __syncwarp();
+        if (SPLIT) {
+            if (unit.rows == 0) tc::cluster_sync();   // (no unit, or a timeout: its sums are void)
+            __syncwarp();
+            tc::cluster_sync();
+            // this rank's chunks: 128 threads take a column each, or with SwiGLU a pair's column and half of the rows
+            const int t = (int)tid - 64, chunks = unit.n16 / SPLIT_ROWS, each = (chunks + p.ranks - 1) / p.ranks;
+            const int c = SWIGLU ? t & 63 : t, col = unit.mt * (SWIGLU ? BM / 2 : BM) + c;
+            constexpr int ROWS = SWIGLU ? SPLIT_ROWS / 2 : SPLIT_ROWS;
+            for (int j = part; j < chunks; j += p.ranks) {
+                const int first = SWIGLU ? (t >> 6) * ROWS : 0;
+                const float *from = reinterpret_cast<const float *>(ring) + (j / p.ranks * SPLIT_ROWS + first) * BM + c;
+                float a[ROWS], b[ROWS];
+#pragma unroll
+                for (int r = 0; r < ROWS; ++r) a[r] = b[r] = 0.0f;
+                for (int s = 0; s < p.ranks; ++s, from += each * SPLIT_ROWS * BM) {   // in rank order
+#pragma unroll
+                    for (int r = 0; r < ROWS; ++r) {
+                        a[r] += from[r * BM];
+                        if (SWIGLU) b[r] += from[r * BM + BM / 2];
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < ROWS; ++r) {
+                    const int row = j * SPLIT_ROWS + first + r;
+                    if (row < unit.rows && col < p.n)
+                        p.out[(size_t)(unit.row0 + row) * p.ld_out + col] =
+                            __float2bfloat16_rn(SWIGLU ? silu(a[r]) * b[r] : a[r]);
+                }
+            }
+            __syncwarp();
+        }
+    }
+    if (SPLIT && (warp < 2 || warp >= 6)) {   // (the epilogue's two)
+        __syncwarp();
+        tc::cluster_sync();
+        tc::cluster_sync();
     }
 
     tc::fence_before();
@@ -562,37 +640,38 @@ eagle3_status_t validate(const eagle3_grouped_linear_args_t *a) {
     return EAGLE3_OK;
 }
 
-// CTAs, or pairs of them, that the device holds at once: a GPC with an odd number of SMs leaves one without a
-// partner.
-template <bool SWIGLU, bool GATHER, bool PAIR>
-int resident() {
-    if (cudaFuncSetAttribute(grouped_kernel<SWIGLU, GATHER, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) !=
+constexpr int MAX_RANKS = 8;
+struct ClusterCounts {
+    int n[MAX_RANKS + 1];   // by cluster size
+};
+
+// CTAs, or clusters of `ranks`, that the device holds at once (a GPC with an odd number of SMs leaves one without
+// a partner); 0 on an error.
+template <bool SWIGLU, bool GATHER, int MODE>
+int resident(int ranks) {
+    if (cudaFuncSetAttribute(grouped_kernel<SWIGLU, GATHER, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) !=
         cudaSuccess)
         return 0;
-    if (!PAIR) return device_sm_count();
+    if (ranks == 1) return device_sm_count();
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * device_sm_count());
+    cfg.gridDim = dim3(ranks * device_sm_count());
     cfg.blockDim = dim3(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0));
     cfg.dynamicSmemBytes = SMEM;
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = 2;
+    at.val.clusterDim.x = ranks;
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
     int n = 0;
-    return cudaOccupancyMaxActiveClusters(&n, grouped_kernel<SWIGLU, GATHER, PAIR>, &cfg) == cudaSuccess ? n : 0;
+    return cudaOccupancyMaxActiveClusters(&n, grouped_kernel<SWIGLU, GATHER, MODE>, &cfg) == cudaSuccess ? n : 0;
 }
 
-// units: an upper bound on the call's units
-template <bool SWIGLU, bool GATHER, bool PAIR>
-cudaError_t launch_grouped(int64_t units, cudaStream_t st, const RowMaps &tx, const CUtensorMap &tw,
-                           const CUtensorMap &tw2, const GroupedParams &p) {
-    static PerDevice<int> cache;
-    const int most = cache.get(resident<SWIGLU, GATHER, PAIR>);
-    if (most < 1) return cudaErrorUnknown;
+template <bool SWIGLU, bool GATHER, int MODE>
+cudaError_t launch_mode(int clusters, int ranks, cudaStream_t st, const RowMaps &tx, const CUtensorMap &tw,
+                        const CUtensorMap &tw2, const GroupedParams &p) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)std::min<int64_t>(most, units) * (PAIR ? 2 : 1));
+    cfg.gridDim = dim3((unsigned)clusters * ranks);
     cfg.blockDim = dim3(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0));
     cfg.dynamicSmemBytes = SMEM;
     cfg.stream = st;
@@ -600,20 +679,48 @@ cudaError_t launch_grouped(int64_t units, cudaStream_t st, const RowMaps &tx, co
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = 2;
+    at[1].val.clusterDim.x = ranks;
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = PAIR ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, grouped_kernel<SWIGLU, GATHER, PAIR>, tx, tw, tw2, p);
+    cfg.numAttrs = ranks > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, grouped_kernel<SWIGLU, GATHER, MODE>, tx, tw, tw2, p);
 }
 
-template <bool PAIR>
-cudaError_t launch_grouped(bool swiglu, bool gather, int64_t units, cudaStream_t st, const RowMaps &tx,
-                           const CUtensorMap &tw, const CUtensorMap &tw2, const GroupedParams &p) {
-    return swiglu ? (gather ? launch_grouped<true, true, PAIR>(units, st, tx, tw, tw2, p)
-                            : launch_grouped<true, false, PAIR>(units, st, tx, tw, tw2, p))
-                  : (gather ? launch_grouped<false, true, PAIR>(units, st, tx, tw, tw2, p)
-                            : launch_grouped<false, false, PAIR>(units, st, tx, tw, tw2, p));
+// row_tiles: an upper bound on the call's row tiles
+template <bool SWIGLU, bool GATHER>
+cudaError_t launch_grouped(int64_t row_tiles, cudaStream_t st, const RowMaps &tx, const CUtensorMap &tw,
+                           const CUtensorMap &tw2, GroupedParams &p) {
+    static PerDevice<ClusterCounts> singles, pairs, splits;
+    const ClusterCounts split = splits.get([] {
+        ClusterCounts c = {};
+        for (int r = 2; r <= MAX_RANKS; ++r) c.n[r] = resident<SWIGLU, GATHER, SPLIT_K>(r);
+        return c;
+    });
+    // Few units: as many ranks as leave every unit a resident cluster, if that saves each CTA 6 k-blocks, and one
+    // more for each 16 rows of a tile: a k-block takes 0.2 us, and sending, meeting and adding up 1 us for a few
+    // rows, 5 us for 256.  (2 rows, 2 groups, 1024 columns: k = 14336 45 us by single CTAs, 15 by eight ranks, k =
+    // 1024 7.3 and 6.0, k = 512 5.7 and 5.8; 500 rows, 2 groups, 512 columns: k = 4096 20 and 13, k = 1024 9.2 and 11.)
+    p.ranks = 1;
+    for (int r = 2; r <= MAX_RANKS; ++r)
+        if (row_tiles * p.tiles_w <= split.n[r] && p.kb_total - p.kb_total / r >= 6 + std::min(p.m, MAX_ROWS) / 16)
+            p.ranks = r;
+    if (p.ranks > 1)
+        return launch_mode<SWIGLU, GATHER, SPLIT_K>((int)(row_tiles * p.tiles_w), p.ranks, st, tx, tw, tw2, p);
+    // Pairs of CTAs, unless the last pair's odd CTA would be without weight rows and that is more than a
+    // sixth of the work: one tile of weight rows (2048 rows x 8 of 64 experts, k = 4096, 128 columns) takes
+    // 33 us by single CTAs and 53 us by pairs, three tiles 68 and 74 us, 16 tiles (3840 rows, 2 x 1024
+    // columns) 377 and 325 us.  With few rows, where the weights' bytes bound the call, both are alike.
+    if (p.tiles_w % 2 == 0 || p.tiles_w >= 5) {
+        p.tiles_w = (p.tiles_w + 1) / 2;
+        const ClusterCounts most = pairs.get([] { return ClusterCounts{{0, resident<SWIGLU, GATHER, PAIRED>(2)}}; });
+        if (most.n[1] < 1) return cudaErrorUnknown;
+        return launch_mode<SWIGLU, GATHER, PAIRED>((int)std::min<int64_t>(most.n[1], row_tiles * p.tiles_w), 2, st, tx, tw,
+                                                   tw2, p);
+    }
+    const ClusterCounts most = singles.get([] { return ClusterCounts{{0, resident<SWIGLU, GATHER, SINGLE>(1)}}; });
+    if (most.n[1] < 1) return cudaErrorUnknown;
+    return launch_mode<SWIGLU, GATHER, SINGLE>((int)std::min<int64_t>(most.n[1], row_tiles * p.tiles_w), 1, st, tx, tw, tw2,
+                                               p);
 }
 
 }  // namespace
@@ -654,16 +761,11 @@ extern "C" eagle3_status_t eagle3_grouped_linear(const eagle3_grouped_linear_arg
     p.row_ids = a->row_ids;
     p.dev_status = a->dev_status;
     p.paired = p.ld_out % 2 == 0 && ((uintptr_t)a->out & 3) == 0;
-    // Pairs of CTAs, unless the last pair's odd CTA would be without weight rows and that is more than a
-    // sixth of the work: one tile of weight rows (2048 rows x 8 of 64 experts, k = 4096, 128 columns) takes
-    // 33 us by single CTAs and 53 us by pairs, three tiles 68 and 74 us, 16 tiles (3840 rows, 2 x 1024
-    // columns) 377 and 325 us.  With few rows, where the weights' bytes bound the call, both are alike.
-    const bool pair = p.tiles_w % 2 == 0 || p.tiles_w >= 5;
-    if (pair) p.tiles_w = (p.tiles_w + 1) / 2;
-    const int64_t units = (int64_t)p.tiles_w * (a->m / MAX_ROWS + std::min(a->m, a->n_groups));
+    const int64_t row_tiles = a->m / MAX_ROWS + std::min(a->m, a->n_groups);
     const cudaStream_t s = (cudaStream_t)stream;
-    const bool gather = a->row_ids != nullptr;
-    const cudaError_t e = pair ? launch_grouped<true>(swiglu, gather, units, s, tx, tw, tw2, p)
-                               : launch_grouped<false>(swiglu, gather, units, s, tx, tw, tw2, p);
+    const cudaError_t e = swiglu ? (a->row_ids ? launch_grouped<true, true>(row_tiles, s, tx, tw, tw2, p)
+                                               : launch_grouped<true, false>(row_tiles, s, tx, tw, tw2, p))
+                                 : (a->row_ids ? launch_grouped<false, true>(row_tiles, s, tx, tw, tw2, p)
+                                               : launch_grouped<false, false>(row_tiles, s, tx, tw, tw2, p));
     return e == cudaSuccess ? EAGLE3_OK : EAGLE3_ERR_CUDA;
 }

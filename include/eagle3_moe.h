@@ -79,7 +79,10 @@ eagle3_status_t eagle3_moe_route(const eagle3_moe_route_args_t *args, void *work
  * without row_ids.  Epilogues: EAGLE3_EPI_BF16 (out bf16), EAGLE3_EPI_SWIGLU
  * (out bf16 = silu(x W^T) * (x W2^T); silu of less than -87.3 is 0).  bf16 in, fp32 accumulation on the
  * tcgen05 tensor cores.
- * Groups may be empty.  Rows of out at or past offsets[n_groups] are left as they were.
+ * Groups may be empty.  Rows of out at or past offsets[n_groups] are left as they were.  With few rows
+ * and columns the sum over k is cut into ranges that a thread-block cluster adds in order; the cut comes
+ * from the shape and from how many CTAs the device holds, never from the offsets, so results are
+ * reproducible on a given GPU model.
  *
  * EAGLE3_DEV_BAD_COUNTS (eagle3_chain.h) is raised when offsets do not start at 0, decrease or pass
  * m (out is then not written at all), and when a row id of a used slot is outside [0, n_src) (that

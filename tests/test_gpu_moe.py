@@ -186,6 +186,16 @@ def test_grouped(counts, n, k, swiglu, gather):
     _grouped(counts, n, k, swiglu, gather, seed=sum(counts) + n)
 
 
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("counts,n,k", [
+    ([1], 128, 1024), ([0, 1, 0, 2], 200, 2056), ([3, 17], 77, 1000), ([256], 64, 4096), ([250, 0, 40], 130, 1544),
+    ([0, 0], 64, 2048), ([9, 8, 7, 6, 5], 500, 640), ([600], 40, 3000)])
+def test_grouped_k_ranges(counts, n, k, swiglu, gather):
+    """Few units and a long k: the k-blocks are cut over a cluster."""
+    _grouped(counts, n, k, swiglu, gather, seed=n + k, spare=3, pitch=8 if gather else 0)
+
+
 def test_grouped_spare_rows_and_pitches():
     _grouped([3, 40, 0, 9], 96, 128, False, True, spare=21, pitch=8)
     _grouped([3, 40, 0, 9], 96, 128, True, False, spare=21, pitch=8)
