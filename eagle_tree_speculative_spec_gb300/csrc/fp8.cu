@@ -1157,10 +1157,10 @@ extern "C" eagle3_status_t eagle3_linear_fp8(const eagle3_linear_fp8_args_t *a, 
     const int tiles_w = (a->n + (swiglu ? 63 : BM - 1)) / (swiglu ? 64 : BM);
     p.tiles_m = (a->m + BM - 1) / BM;
     p.tiles_n = (a->n + (swiglu ? WIDE_BN / 2 : WIDE_BN) - 1) / (swiglu ? WIDE_BN / 2 : WIDE_BN);
-    // Few rows by the narrow kernel, from 33 rows on unless the wide one's tiles cover half of the SMs.
-    // 8 x 6144 x 4096: 8.0 us narrow, 14.7 wide; 64 x 6144 x 4096 (24 wide tiles): 13.3 and 13.3; 64 rows x
-    // 2 * 14336 x 4096 (112): 31 and 25; 96 x 4096 x 14336: 34 (with tiles of 128 rows) and 20.
-    const bool narrow = tiles_w <= 65535 && (a->m <= NARROW_MAX / 2 || (a->m <= NARROW_MAX && 2 * p.tiles_n < sms));
+    // Few rows by the narrow kernel, from 25 rows on unless the wide one's tiles cover half of the SMs.
+    // 8 x 6144 x 4096 (24 wide tiles): 7.4 us narrow, 14.5 wide; 64 rows 10.9 and 13.2.  24 x 24576 x 4096 (96): 22 and
+    // 27; 32 rows 24.6 and 21.0, 64 rows 27 and 21.  96 x 4096 x 14336: 34 (with tiles of 128 rows) and 20.
+    const bool narrow = tiles_w <= 65535 && (a->m <= 24 || (a->m <= NARROW_MAX && 2 * p.tiles_n < sms));
     CUtensorMap tx, tw, tw2, to, tr;
     const int w_box = narrow ? (swiglu ? 16 : BM) : (swiglu ? WIDE_BN / 2 : WIDE_BN);
     if (!tmap_rows(&tx, u8, 1, a->x, a->m, a->k, ld_x, narrow ? 16 : BM) ||

@@ -125,7 +125,7 @@ EPIS = ["bf16", "f32", "residual", "swiglu"]
 @pytest.mark.parametrize("epi", EPIS)
 @pytest.mark.parametrize("m,n,k", [
     (1, 64, 128), (1, 1, 16), (3, 130, 144), (16, 256, 512), (17, 1000, 1024), (33, 96, 2064), (64, 640, 4096),
-    (65, 100, 256), (100, 300, 400), (128, 512, 768), (8, 6144, 4096)])
+    (65, 100, 256), (100, 300, 400), (128, 512, 768), (8, 6144, 4096), (24, 19601, 256), (28, 19601, 256)])
 def test_fp8_few_rows(m, n, k, epi):
     _check(m, n, k, epi)
 
