@@ -153,9 +153,11 @@ def test_fp8_pitched_views(m, epi):
     _check(m, 200, 272, epi, out_pitch=3)      # rows that no 16-byte store fits
 
 
-@pytest.mark.parametrize("m", [5, 300])
-def test_fp8_residual_in_place(m):
-    _check(m, 264, 256, "residual", in_place=True)
+@pytest.mark.parametrize("m,n,k", [(5, 264, 256), (300, 264, 256), (200, 264, 4096), (300, 263, 256), (2500, 5000, 128),
+                                   (2500, 5001, 128)])
+def test_fp8_residual_in_place(m, n, k):
+    """Every kernel, and several tiles a CTA."""
+    _check(m, n, k, "residual", in_place=True)
 
 
 @pytest.mark.parametrize("m", [4, 200])
