@@ -8,8 +8,8 @@
 // two scales, to fp32 accumulators in registers while the next block's MMAs run.  (This also keeps
 // the long sum out of the tensor cores' accumulation.)
 //
-// Two kernels (the rule between them stands at the launch), both warp-specialised: warp 0 loads by TMA into a ring, a lane of warp 1 issues
-// tcgen05.mma (kind::f8f6f4, K = 32) and the other warps run the epilogue.
+// Two kernels (the rule between them stands at the launch), both warp-specialised: warp 0 loads by TMA into a
+// ring, a lane of warp 1 issues tcgen05.mma (kind::f8f6f4, K = 32) and the other warps run the epilogue.
 //   wide     128 rows x 256 weight rows a tile, persistent.  Rows are the M side, so a thread owns one
 //            row and its scale is one number a k-block.
 //   narrow   128 weight rows (M side) x up to 64 rows (N side, any multiple of 16): few rows, bound by
@@ -560,7 +560,8 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                 tc::cluster_sync();
 #pragma unroll
                 for (int j = 0; j < WIDE_RUN / 8; ++j) {
-                    const uint32_t to = tc::cluster_addr(ring0, j % ranks) + split_offset(ranks, rank, part, j, quarter * 32 + lane);
+                    const uint32_t to =
+                        tc::cluster_addr(ring0, j % ranks) + split_offset(ranks, rank, part, j, quarter * 32 + lane);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         tc::cluster_st(to + i * BM * 4, acc[j * 8 + i]);
@@ -572,7 +573,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
             const int cols = SWIGLU ? WIDE_RUN : 2 * WIDE_RUN, y = mb * BM + quarter * 32;
             const int col0 = nb * (SWIGLU ? WIDE_BN / 2 : WIDE_BN) + cols * part;
             const bool f32 = !SWIGLU && !RES && p.epi == EAGLE3_EPI_F32;
-            const int rows = min(32, p.m - y), ln = lane;
+            const int rows = min(32, p.m - y);
             // Residuals by TMA too, 32 columns at a time to a box of their own, the next while these are added and
             // stored.  (Loads of a row a lane: 2000 x 6144 x 4096 66 us, 54 so; with the first box before the main
             // loop 52, but 3840 x 4096 x 14336 in place 246 us in place of 218.)

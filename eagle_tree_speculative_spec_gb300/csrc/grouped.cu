@@ -489,8 +489,8 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
                     for (int i = 0; i < 32; i += SPLIT_ROWS) {
                         const int j = (c + i) / SPLIT_ROWS, to = j % p.ranks;
                         if (j >= chunks) continue;
-                        const uint32_t at = tc::cluster_addr(ring0, to) +
-                                            (uint32_t)(((part * each + j / p.ranks) * SPLIT_ROWS * BM + quarter * 32 + lane) * 4);
+                        const int word = (part * each + j / p.ranks) * SPLIT_ROWS * BM + quarter * 32 + lane;
+                        const uint32_t at = tc::cluster_addr(ring0, to) + (uint32_t)(word * 4);
 #pragma unroll
                         for (int r = 0; r < SPLIT_ROWS; ++r) tc::cluster_st(at + r * BM * 4, v[i + r]);
                     }
@@ -714,13 +714,13 @@ cudaError_t launch_grouped(int64_t row_tiles, cudaStream_t st, const RowMaps &tx
         p.tiles_w = (p.tiles_w + 1) / 2;
         const ClusterCounts most = pairs.get([] { return ClusterCounts{{0, resident<SWIGLU, GATHER, PAIRED>(2)}}; });
         if (most.n[1] < 1) return cudaErrorUnknown;
-        return launch_mode<SWIGLU, GATHER, PAIRED>((int)std::min<int64_t>(most.n[1], row_tiles * p.tiles_w), 2, st, tx, tw,
-                                                   tw2, p);
+        const int pairs_used = (int)std::min<int64_t>(most.n[1], row_tiles * p.tiles_w);
+        return launch_mode<SWIGLU, GATHER, PAIRED>(pairs_used, 2, st, tx, tw, tw2, p);
     }
     const ClusterCounts most = singles.get([] { return ClusterCounts{{0, resident<SWIGLU, GATHER, SINGLE>(1)}}; });
     if (most.n[1] < 1) return cudaErrorUnknown;
-    return launch_mode<SWIGLU, GATHER, SINGLE>((int)std::min<int64_t>(most.n[1], row_tiles * p.tiles_w), 1, st, tx, tw, tw2,
-                                               p);
+    const int ctas = (int)std::min<int64_t>(most.n[1], row_tiles * p.tiles_w);
+    return launch_mode<SWIGLU, GATHER, SINGLE>(ctas, 1, st, tx, tw, tw2, p);
 }
 
 }  // namespace

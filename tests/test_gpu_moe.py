@@ -64,8 +64,9 @@ def _check_route(z, k, status=0, **kw):
     assert (err <= tol * np.abs(w) + 1e-37).all(), (err.max(), tol)
 
 
-@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 64, 8), (5, 33, 16), (31, 8, 2), (32, 512, 8), (33, 512, 16), (60, 20, 3),
-                                   (64, 64, 6), (65, 128, 8), (200, 512, 16), (256, 30, 5), (257, 64, 8), (1000, 256, 8), (3840, 100, 4), (6000, 7, 7)])
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 64, 8), (5, 33, 16), (31, 8, 2), (32, 512, 8), (33, 512, 16),
+                                   (60, 20, 3), (64, 64, 6), (65, 128, 8), (200, 512, 16), (256, 30, 5), (257, 64, 8),
+                                   (1000, 256, 8), (3840, 100, 4), (6000, 7, 7)])
 @pytest.mark.parametrize("sigmoid,renorm", [(False, True), (True, False)])
 def test_route(T, E, k, sigmoid, renorm):
     dev = require_gpu()
