@@ -115,6 +115,34 @@ def test_route_no_rows_and_pitched_logits():
     _check_route(wide[:, 10:50], 5)
 
 
+def test_route_own_workspace():
+    """Without a workspace: eager calls on two streams in turn, captured and replayed between them."""
+    dev = require_gpu()
+    z = [torch.randn(T, 48, generator=torch.Generator().manual_seed(T)).to(dev) for T in (300, 700)]
+    want = [_route(x, 4)[0] for x in z]
+    outs = [{k: torch.empty_like(v) for k, v in w.items()} for w in want]
+    call = lambda i, **kw: e3.eagle3_moe_route(z[i], *(outs[i][k] for k in ("ids", "w", "off", "rows", "slots")), **kw)
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side), torch.cuda.graph(graph, stream=side):
+        call(0)
+        call(1)
+    for _ in range(20):
+        for o in outs:
+            for v in o.values():
+                v.fill_(-7)
+        torch.cuda.synchronize()
+        call(0, stream=side)
+        junk = torch.full((1 << 14,), 3, dtype=i32, device=dev)   # the current stream's, beside the side stream's calls
+        call(1, stream=side)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert (junk == 3).all()
+        for o, w in zip(outs, want):
+            for k in w:
+                assert torch.equal(o[k], w[k]), k
+
+
 def test_route_many_rows():
     """More rows than a block per 32: several chunks a block."""
     dev = require_gpu()
