@@ -47,7 +47,7 @@ struct Fp8Params {
     void *out;
     int32_t *dev_status;
     int tiles_m, tiles_n;   // wide: row tiles, column tiles
-    int ranks;              // wide: CTAs of a cluster, each a range of a tile's k-blocks (then one tile a cluster)
+    int ranks;              // OUT_SPLIT: CTAs of a cluster, each a range of a tile's k-blocks (one tile a cluster)
     int tma_out;            // wide: outputs leave through shared memory and TMA stores
     int n16, stages;        // narrow: rows of a tile (multiple of 16), ring depth
 };
@@ -176,23 +176,6 @@ __global__ void __launch_bounds__(QUANT_THREADS) quantize_kernel(const QuantPara
 E3_DEV float res1(const __nv_bfloat16 *src) {
     return __uint_as_float((uint32_t)__ldcg(reinterpret_cast<const unsigned short *>(src)) << 16);
 }
-// 8 consecutive outputs of a row from column col: residual, rounding, store (columns below n).
-E3_DEV void load_res8(const Fp8Params &p, int row, int col, float *v) {
-    const __nv_bfloat16 *src = p.residual + (size_t)row * p.ld_res + col;
-    if (col + 8 <= p.n && ((uintptr_t)src & 15) == 0) {
-        const uint4 r = __ldcg(reinterpret_cast<const uint4 *>(src));
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] += __uint_as_float(w[i] << 16);
-            v[2 * i + 1] += __uint_as_float(w[i] & 0xffff0000u);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (col + i < p.n) v[i] += res1(src + i);
-    }
-}
 E3_DEV void add_quad(float *v, uint4 q) {   // 8 bf16
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -210,27 +193,43 @@ E3_DEV uint4 pack8(const float *v) {
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
-E3_DEV void store8(const Fp8Params &p, int row, int col, const float *v) {
-    const bool whole = col + 8 <= p.n;
-    if (p.epi == EAGLE3_EPI_F32) {
+// 4 consecutive outputs of a row from column col: residual, rounding, store (columns below n).
+template <bool RES>
+E3_DEV void store4(const Fp8Params &p, int row, int col, float4 v4) {
+    float v[4] = {v4.x, v4.y, v4.z, v4.w};
+    const bool whole = col + 4 <= p.n;
+    if (!RES && p.epi == EAGLE3_EPI_F32) {
         float *o = (float *)p.out + (size_t)row * p.ld_out + col;
         if (whole && ((uintptr_t)o & 15) == 0) {
-            *reinterpret_cast<float4 *>(o) = make_float4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<float4 *>(o + 4) = make_float4(v[4], v[5], v[6], v[7]);
+            *reinterpret_cast<float4 *>(o) = v4;
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < 4; ++i)
                 if (col + i < p.n) o[i] = v[i];
         }
-    } else {
-        __nv_bfloat16 *o = (__nv_bfloat16 *)p.out + (size_t)row * p.ld_out + col;
-        if (whole && ((uintptr_t)o & 15) == 0) {
-            *reinterpret_cast<uint4 *>(o) = pack8(v);
+        return;
+    }
+    if (RES) {
+        const __nv_bfloat16 *src = p.residual + (size_t)row * p.ld_res + col;
+        if (whole && ((uintptr_t)src & 7) == 0) {
+            const uint2 r = __ldcg(reinterpret_cast<const uint2 *>(src));
+            v[0] += __uint_as_float(r.x << 16), v[1] += __uint_as_float(r.x & 0xffff0000u);
+            v[2] += __uint_as_float(r.y << 16), v[3] += __uint_as_float(r.y & 0xffff0000u);
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (col + i < p.n) o[i] = __float2bfloat16_rn(v[i]);
+            for (int i = 0; i < 4; ++i)
+                if (col + i < p.n) v[i] += res1(src + i);
         }
+    }
+    __nv_bfloat16 *o = (__nv_bfloat16 *)p.out + (size_t)row * p.ld_out + col;
+    if (whole && ((uintptr_t)o & 7) == 0) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+        *reinterpret_cast<uint2 *>(o) =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (col + i < p.n) o[i] = __float2bfloat16_rn(v[i]);
     }
 }
 
@@ -312,27 +311,37 @@ E3_DEV void load_rows(uint8_t *box, const __nv_bfloat16 *src, int64_t ld, int ro
 // and 104 registers: 358 us.)  What is left is still the epilogue: without its additions the kernel takes 265 us.
 constexpr int WIDE_BN = 256, WIDE_STAGES = 4, WIDE_EPI_WARPS = 8, WIDE_THREADS = 128 + 32 * WIDE_EPI_WARPS;
 constexpr int WIDE_EPI0 = 4;   // first epilogue warp
-constexpr int WIDE_RUN = 512 / WIDE_EPI_WARPS;   // accumulator columns of a thread: two runs of this many
-constexpr int WIDE_A = BM * BK, WIDE_B = WIDE_BN * BK, WIDE_STAGE = WIDE_A + WIDE_B;
+constexpr int SPLIT_BN = 128, SPLIT_STAGES = 6;   // OUT_SPLIT's narrower tiles
+constexpr int WIDE_A = BM * BK, WIDE_RING = WIDE_STAGES * (WIDE_A + WIDE_BN * BK);
+static_assert(SPLIT_STAGES * (WIDE_A + SPLIT_BN * BK) <= WIDE_RING, "the ring of narrower tiles");
 constexpr int WIDE_BOX = 32 * 64;   // output staging: 32 rows x 64 bytes a warp
 // One barrier before and one after the MMAs of a k-block, both counted by its ring stage: full completes
-// when the loads have landed and the epilogue warps have read the TMEM buffer (that of two k-blocks
+// when the loads have landed and the epilogue warps have read the TMEM buffer (that of BUFS k-blocks
 // before), done when the MMAs have run, which both frees the stage and fills the buffer.  (With barriers
 // of their own for the buffers the issuing thread spent 640 cycles a k-block on waits and commits.)
 struct WideShared {
-    uint64_t full[WIDE_STAGES], done[WIDE_STAGES], mma_done, res[WIDE_EPI_WARPS];
+    uint64_t full[SPLIT_STAGES], done[SPLIT_STAGES], mma_done, res[WIDE_EPI_WARPS];
     uint32_t tmem_base;
     int abort;
 };
-constexpr int WIDE_SMEM = 1024 + WIDE_STAGES * WIDE_STAGE + 2 * WIDE_EPI_WARPS * WIDE_BOX + (int)sizeof(WideShared);
+constexpr int WIDE_SMEM = 1024 + WIDE_RING + 2 * WIDE_EPI_WARPS * WIDE_BOX + (int)sizeof(WideShared);
 static_assert(WIDE_SMEM <= 232448, "shared memory budget");
 
-// SPLIT: where rank src's sums of piece j (8 columns of each run, 128 rows) of an epilogue half lie in the ring
-// of the rank that the piece belongs to, j % ranks; byte offset of a row's first value.
-__host__ __device__ constexpr int split_pieces(int ranks) { return (WIDE_RUN / 8 + ranks - 1) / ranks; }
-__host__ __device__ constexpr int split_bytes(int ranks) { return ranks * 2 * split_pieces(ranks) * 16 * BM * 4; }
+// SPLIT: where rank src's sums of piece j (4 columns of each run, 128 rows) of an epilogue half lie in the ring of
+// the rank that the piece belongs to, j / split_pieces: two quads of values, all rows of a quad side by side; byte
+// offset of a row's first quad.
+template <int BN>
+__host__ __device__ constexpr int split_pieces(int ranks) {
+    return (2 * BN / WIDE_EPI_WARPS / 4 + ranks - 1) / ranks;
+}
+template <int BN>
+__host__ __device__ constexpr int split_bytes(int ranks) {
+    return ranks * 2 * split_pieces<BN>(ranks) * 2 * BM * 16;
+}
+template <int BN>
 E3_DEV uint32_t split_offset(int ranks, int src, int part, int j, int row) {
-    return (uint32_t)((((src * 2 + part) * split_pieces(ranks) + j / ranks) * 16 * BM + row) * 4);
+    const int each = split_pieces<BN>(ranks);
+    return (uint32_t)((((src * 2 + part) * each + j % each) * 2 * BM + row) * 16);
 }
 
 template <int N>
@@ -344,29 +353,33 @@ E3_DEV void registers_take() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
 }
 
-// SPLIT: a cluster of p.ranks CTAs works on one tile, each on a range of the k-blocks.  Pieces of 8 columns of
-// both runs belong to the ranks in turn: each rank sends the others their pieces of its sums by remote stores
-// (reading them took three times as long, and stores of 16 bytes a lane, 64 apart, are 4 to 7 us slower than these of a
-// whole warp's 128 bytes), and adds up and finishes its own.
+// SPLIT: a cluster of p.ranks CTAs works on one tile (of 256 columns or 128), each on a range of the k-blocks.
+// Pieces of 4 columns of both runs belong to the ranks in shares: each rank sends the others their pieces of its sums
+// by remote stores (reading them took three times as long), and adds up and finishes its own.  The stores are bound
+// by the bytes, some 20 a cycle (128 x 256 sums: 5 us; a lane's quads side by side, 64 bytes from the next lane's: 9 to
+// 12), which narrower tiles halve.
 // OUT: how outputs leave; RES: with residuals.  The variants are kernels of their own: what stands behind the main
 // loop decides whether its 128 accumulators and scales stay in registers (stores by TMA and by the warps in one
 // kernel: 3840 x 2 * 14336 x 4096 346 -> 444 us).
 enum { OUT_TMA, OUT_STAGED, OUT_SPLIT };
-template <bool SWIGLU, int OUT, bool RES>
+template <bool SWIGLU, int OUT, bool RES, int BN = WIDE_BN>
 __global__ void __launch_bounds__(WIDE_THREADS, 1)
     fp8_wide_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                     const __grid_constant__ CUtensorMap tm_w2, const __grid_constant__ CUtensorMap tm_out,
                     const __grid_constant__ CUtensorMap tm_res, const Fp8Params p) {
+    constexpr bool SPLIT = OUT == OUT_SPLIT, RES_TMA = OUT == OUT_TMA && RES;
+    constexpr int RUN = 2 * BN / WIDE_EPI_WARPS;   // a thread's two runs of columns
+    constexpr int STAGES = BN == WIDE_BN ? WIDE_STAGES : SPLIT_STAGES, STAGE = WIDE_A + BN * BK;
+    constexpr int BUFS = 512 / BN;                 // TMEM buffers
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = smem_raw + (-smem_u32(smem_raw) & 1023u);   // (the compiler knows it as shared memory)
-    uint8_t *boxes = ring + WIDE_STAGES * WIDE_STAGE;
+    uint8_t *boxes = ring + WIDE_RING;
     WideShared &sh = *reinterpret_cast<WideShared *>(boxes + 2 * WIDE_EPI_WARPS * WIDE_BOX);
-    constexpr bool SPLIT = OUT == OUT_SPLIT, RES_TMA = OUT == OUT_TMA && RES;
     const uint32_t tid = tc::thread_index();
     const int warp = (int)(tid >> 5), lane = (int)(tid & 31u);
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < WIDE_STAGES; ++s) {
+        for (int s = 0; s < STAGES; ++s) {
             tc::mbar_init(&sh.full[s], 1 + WIDE_EPI_WARPS);
             tc::mbar_init(&sh.done[s], 1);
         }
@@ -378,7 +391,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
         tc::prefetch_tmap(&tm_w);
         if (SWIGLU) tc::prefetch_tmap(&tm_w2);
     }
-    if (warp == 1) tc::tmem_alloc(&sh.tmem_base, 2 * WIDE_BN);
+    if (warp == 1) tc::tmem_alloc(&sh.tmem_base, BUFS * BN);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -408,18 +421,18 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                             ok = false;
                             break;
                         }
-                        const uint32_t full = full0 + stage * 8, sx = ring0 + stage * WIDE_STAGE, sw = sx + WIDE_A;
-                        tc::mbar_expect_tx(full, WIDE_STAGE);
+                        const uint32_t full = full0 + stage * 8, sx = ring0 + stage * STAGE, sw = sx + WIDE_A;
+                        tc::mbar_expect_tx(full, STAGE);
                         tc::tma_load_2d(sx, &tm_x, kb * BK, mb * BM, full);
                         if (SWIGLU) {
-                            tc::tma_load_2d(sw, &tm_w, kb * BK, nb * (WIDE_BN / 2), full);
-                            tc::tma_load_2d(sw + WIDE_B / 2, &tm_w2, kb * BK, nb * (WIDE_BN / 2), full);
+                            tc::tma_load_2d(sw, &tm_w, kb * BK, nb * (BN / 2), full);
+                            tc::tma_load_2d(sw + BN * BK / 2, &tm_w2, kb * BK, nb * (BN / 2), full);
                         } else {
-                            tc::tma_load_2d(sw, &tm_w, kb * BK, nb * WIDE_BN, full);
+                            tc::tma_load_2d(sw, &tm_w, kb * BK, nb * BN, full);
                         }
                         issued |= 1u << stage;
                         last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
-                        if (++stage == WIDE_STAGES) {
+                        if (++stage == STAGES) {
                             stage = 0;
                             phase ^= 1u;
                         }
@@ -427,14 +440,14 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                 }
                 if (!ok) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
                 // no TMA write may still be in flight when the CTA exits (bounded waits)
-                for (int st = 0; st < WIDE_STAGES; ++st)
+                for (int st = 0; st < STAGES; ++st)
                     if ((issued >> st) & 1u) tc::mbar_drain(full0 + st * 8, (last_parity >> st) & 1u);
             }
             __syncwarp();
         } else if (warp == 1) {
             // ------------------------------------------------------------------ MMA issuer
             if (tc::elect_one()) {
-                constexpr uint32_t IDESC = tc::idesc_e4m3(BM, WIDE_BN);
+                constexpr uint32_t IDESC = tc::idesc_e4m3(BM, BN);
                 const uint64_t desc0 = tc::desc_sw128(ring0);
                 int stage = 0, buf = 0;
                 uint32_t phase = 0;
@@ -447,16 +460,16 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                         }
                         tc::fence_after();
                         // (descriptors count 16 bytes)
-                        const uint64_t a = desc0 + (uint32_t)(stage * (WIDE_STAGE >> 4)), b = a + (WIDE_A >> 4);
+                        const uint64_t a = desc0 + (uint32_t)(stage * (STAGE >> 4)), b = a + (WIDE_A >> 4);
 #pragma unroll
                         for (int k = 0; k < BK / 32; ++k)
-                            tc::mma_e4m3_ss(tmem + buf * WIDE_BN, a + k * 2, b + k * 2, IDESC, k > 0 ? 1u : 0u);
+                            tc::mma_e4m3_ss(tmem + buf * BN, a + k * 2, b + k * 2, IDESC, k > 0 ? 1u : 0u);
                         tc::mma_commit(done0 + stage * 8);
-                        if (++stage == WIDE_STAGES) {
+                        if (++stage == STAGES) {
                             stage = 0;
                             phase ^= 1u;
                         }
-                        buf ^= 1;
+                        buf = (buf + 1) % BUFS;
                     }
                 if (!ok) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
                 // every MMA this thread issued must retire before TMEM is freed (bounded wait)
@@ -478,26 +491,26 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
         uint32_t res_phase = 0;
         // this thread's two runs of accumulator columns: neighbours, or gate and up of one run
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        const uint32_t run_a = lanes + (SWIGLU ? WIDE_RUN : 2 * WIDE_RUN) * part;
-        const uint32_t run_b = run_a + (SWIGLU ? 128 : WIDE_RUN);
+        const uint32_t run_a = lanes + (SWIGLU ? RUN : 2 * RUN) * part;
+        const uint32_t run_b = run_a + (SWIGLU ? BN / 2 : RUN);
         const int kb_total = kb1 - kb0;
         int stage = 0, buf = 0;
         uint32_t phase = 0;
         bool ok = true;
-        if (lane == 0) {   // both buffers are free
-            tc::mbar_arrive(&sh.full[0]);
-            tc::mbar_arrive(&sh.full[1]);
+        if (lane == 0) {   // all buffers are free
+#pragma unroll
+            for (int i = 0; i < BUFS; ++i) tc::mbar_arrive(&sh.full[i]);
         }
         for (int u = unit0; ok && u < units; u += unit_step) {
             const int mb = u % p.tiles_m, nb = u / p.tiles_m;
             const int row = mb * BM + quarter * 32 + lane;
             const float *xs = p.x_scale + (size_t)kb0 * p.m + (row < p.m ? row : 0);
-            const int block = min(SWIGLU ? nb : 2 * nb + part * 2 * WIDE_RUN / BK, p.n_blocks - 1);
+            const int block = min((SWIGLU ? nb * (BN / 2) + RUN * part : nb * BN + 2 * RUN * part) / BK, p.n_blocks - 1);
             const float *wa = p.w_scale + (size_t)block * p.kb_total + kb0;
             const float *wb = SWIGLU ? p.w2_scale + (size_t)block * p.kb_total + kb0 : wa;
-            float acc[2 * WIDE_RUN];
+            float acc[2 * RUN];
 #pragma unroll
-            for (int i = 0; i < 2 * WIDE_RUN; ++i) acc[i] = 0.0f;
+            for (int i = 0; i < 2 * RUN; ++i) acc[i] = 0.0f;
             // scales, far enough ahead of their use for a loaded L2: the row's two k-blocks ahead, the
             // weights' of 32 k-blocks, one a lane
             const float *at = xs;
@@ -519,23 +532,23 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                     break;
                 }
                 tc::fence_after();
-                const uint32_t t = tmem + (uint32_t)(buf * WIDE_BN);
+                const uint32_t t = tmem + (uint32_t)(buf * BN);
                 // 16 columns a load, the next one in flight while the last is added
                 float v[2][16];
                 tc::tmem_ld16_start(t + run_a, v[0]);
 #pragma unroll
-                for (int c = 0; c < WIDE_RUN / 8; ++c) {
+                for (int c = 0; c < RUN / 8; ++c) {
                     tc::tmem_ld_wait(v[c & 1]);
-                    if (c + 1 < WIDE_RUN / 8) {
-                        tc::tmem_ld16_start(t + (c + 1 < WIDE_RUN / 16 ? run_a + (c + 1) * 16
-                                                                       : run_b + (c + 1 - WIDE_RUN / 16) * 16),
+                    if (c + 1 < RUN / 8) {
+                        tc::tmem_ld16_start(t + (c + 1 < RUN / 16 ? run_a + (c + 1) * 16
+                                                                       : run_b + (c + 1 - RUN / 16) * 16),
                                             v[(c + 1) & 1]);
                     } else {   // the buffer is read: it may take the k-block after the next
                         // (the wait for the last load was the whole warp's)
                         tc::fence_before();
-                        tc::mbar_arrive_if(full0 + ((stage + 2) % WIDE_STAGES) * 8, lane == 0);
+                        tc::mbar_arrive_if(full0 + ((stage + BUFS) % STAGES) * 8, lane == 0);
                     }
-                    const float2 f = make_float2(c < WIDE_RUN / 16 ? fa : fb, c < WIDE_RUN / 16 ? fa : fb);
+                    const float2 f = make_float2(c < RUN / 16 ? fa : fb, c < RUN / 16 ? fa : fb);
 #pragma unroll
                     for (int i = 0; i < 16; i += 2) {
                         const float2 r = __ffma2_rn(make_float2(v[c & 1][i], v[c & 1][i + 1]), f,
@@ -546,11 +559,11 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                 }
                 sx = sx1;
                 sx1 = sx2;
-                if (++stage == WIDE_STAGES) {
+                if (++stage == STAGES) {
                     stage = 0;
                     phase ^= 1u;
                 }
-                buf ^= 1;
+                buf = (buf + 1) % BUFS;
             }
             if (!ok) {
                 if (lane == 0) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
@@ -560,19 +573,17 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                 // over the rings, when all ranks' loads and MMAs have completed
                 tc::cluster_sync();
 #pragma unroll
-                for (int j = 0; j < WIDE_RUN / 8; ++j) {
-                    const uint32_t to =
-                        tc::cluster_addr(ring0, j % ranks) + split_offset(ranks, rank, part, j, quarter * 32 + lane);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        tc::cluster_st(to + i * BM * 4, acc[j * 8 + i]);
-                        tc::cluster_st(to + (8 + i) * BM * 4, acc[WIDE_RUN + j * 8 + i]);
-                    }
+                for (int j = 0; j < RUN / 4; ++j) {
+                    const uint32_t to = tc::cluster_addr(ring0, j / split_pieces<BN>(ranks)) +
+                                        split_offset<BN>(ranks, rank, part, j, quarter * 32 + lane);
+                    const float *v = acc + j * 4, *w = v + RUN;
+                    tc::cluster_st4(to, v[0], v[1], v[2], v[3]);
+                    tc::cluster_st4(to + BM * 16, w[0], w[1], w[2], w[3]);
                 }
                 break;   // one tile a cluster
             }
-            const int cols = SWIGLU ? WIDE_RUN : 2 * WIDE_RUN, y = mb * BM + quarter * 32;
-            const int col0 = nb * (SWIGLU ? WIDE_BN / 2 : WIDE_BN) + cols * part;
+            const int cols = SWIGLU ? RUN : 2 * RUN, y = mb * BM + quarter * 32;
+            const int col0 = nb * (SWIGLU ? BN / 2 : BN) + cols * part;
             const bool f32 = !SWIGLU && !RES && p.epi == EAGLE3_EPI_F32;
             const int rows = min(32, p.m - y);
             // Residuals by TMA too, 32 columns at a time to a box of their own, the next while these are added and
@@ -584,23 +595,23 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
             }
             // pieces of 64 bytes: 32 bf16 or 16 fp32 columns of the warp's 32 rows, in the 64-byte swizzle
 #pragma unroll
-            for (int c = 0; c < WIDE_RUN / 8; ++c) {
+            for (int c = 0; c < RUN / 8; ++c) {
                 if (c * (f32 ? 16 : 32) >= cols) break;
                 const int x = col0 + c * (f32 ? 16 : 32);
                 if (OUT == OUT_TMA && lane == 0) tc::bulk_wait_read<0>();   // the box's last store has read it
                 __syncwarp();
                 if (SWIGLU) {
 #pragma unroll
-                    for (int i = 32 * c; i < 32 * c + 32; ++i) acc[i] = silu(acc[i]) * acc[WIDE_RUN + i];
+                    for (int i = 32 * c; i < 32 * c + 32; ++i) acc[i] = silu(acc[i]) * acc[RUN + i];
                 }
                 if (RES_TMA && ok && x < p.n) {
                     ok = tc::mbar_wait_warp(res_bar, res_phase, abort0);
                     res_phase ^= 1u;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        add_quad(acc + c % (WIDE_RUN / 16) * 32 + 8 * j, *box_quad(res_box, lane, j));
+                        add_quad(acc + c % (RUN / 16) * 32 + 8 * j, *box_quad(res_box, lane, j));
                     __syncwarp();
-                    if (ok && lane == 0 && c + 1 < 2 * WIDE_RUN / 32 && x + 32 < p.n) {
+                    if (ok && lane == 0 && c + 1 < 2 * RUN / 32 && x + 32 < p.n) {
                         tc::mbar_expect_tx(res_bar, WIDE_BOX);
                         tc::tma_load_2d(smem_u32(res_box), &tm_res, x + 32, y, res_bar);
                     }
@@ -608,7 +619,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                     load_rows(box, p.residual + (size_t)y * p.ld_res + x, p.ld_res, rows, min(32, p.n - x), lane);
                     __syncwarp();
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) add_quad(acc + c % (WIDE_RUN / 16) * 32 + 8 * j, *box_quad(box, lane, j));
+                    for (int j = 0; j < 4; ++j) add_quad(acc + c % (RUN / 16) * 32 + 8 * j, *box_quad(box, lane, j));
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -618,7 +629,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                         o = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
                                        __float_as_uint(v[3]));
                     } else {
-                        o = pack8(acc + c % (WIDE_RUN / 16) * 32 + 8 * j);
+                        o = pack8(acc + c % (RUN / 16) * 32 + 8 * j);
                     }
                     *box_quad(box, lane, j) = o;
                 }
@@ -651,36 +662,25 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
             __syncwarp();
             tc::cluster_sync();
             const int mb = unit0 % p.tiles_m, nb = unit0 / p.tiles_m, row = mb * BM + quarter * 32 + lane;
-            const int col0 = nb * (SWIGLU ? WIDE_BN / 2 : WIDE_BN) + (SWIGLU ? WIDE_RUN : 2 * WIDE_RUN) * part;
-            for (int piece = rank; piece < WIDE_RUN / 8; piece += ranks) {
-                const int j = piece * 8;
-                float a[8], b[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) a[i] = b[i] = 0.0f;
+            const int col0 = nb * (SWIGLU ? BN / 2 : BN) + (SWIGLU ? RUN : 2 * RUN) * part;
+            const int each = split_pieces<BN>(ranks);
+            for (int piece = rank * each; piece < min((rank + 1) * each, RUN / 4); ++piece) {
+                const int j = piece * 4;
+                float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b = a;
                 for (int s = 0; s < ranks; ++s) {   // in rank order
-                    const float *from = reinterpret_cast<const float *>(
-                        ring + split_offset(ranks, s, part, piece, quarter * 32 + lane));
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        a[i] += from[i * BM];
-                        b[i] += from[(8 + i) * BM];
-                    }
+                    const float4 *from = reinterpret_cast<const float4 *>(
+                        ring + split_offset<BN>(ranks, s, part, piece, quarter * 32 + lane));
+                    const float4 v = from[0], w = from[BM];
+                    a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
+                    b.x += w.x, b.y += w.y, b.z += w.z, b.w += w.w;
                 }
                 if (row >= p.m) continue;
                 if (SWIGLU) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) a[i] = silu(a[i]) * b[i];
-                    if (col0 + j < p.n) store8(p, row, col0 + j, a);
+                    a = make_float4(silu(a.x) * b.x, silu(a.y) * b.y, silu(a.z) * b.z, silu(a.w) * b.w);
+                    store4<RES>(p, row, col0 + j, a);
                 } else {
-                    constexpr bool res = RES;
-                    if (col0 + j < p.n) {
-                        if (res) load_res8(p, row, col0 + j, a);
-                        store8(p, row, col0 + j, a);
-                    }
-                    if (col0 + WIDE_RUN + j < p.n) {
-                        if (res) load_res8(p, row, col0 + WIDE_RUN + j, b);
-                        store8(p, row, col0 + WIDE_RUN + j, b);
-                    }
+                    store4<RES>(p, row, col0 + j, a);
+                    store4<RES>(p, row, col0 + RUN + j, b);
                 }
             }
             __syncwarp();
@@ -692,7 +692,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
     if (warp == 1) {
         __syncwarp();
         tc::fence_after();
-        tc::tmem_dealloc(tmem, 2 * WIDE_BN);
+        tc::tmem_dealloc(tmem, BUFS * BN);
     }
 }
 
@@ -1057,36 +1057,59 @@ cudaError_t launch_narrow(int tiles, cudaStream_t st, const CUtensorMap &tx, con
     return cudaLaunchKernelEx(&cfg, fp8_narrow_kernel<NT, SWIGLU>, tx, tw, tw2, p);
 }
 
-template <bool SWIGLU, int OUT, bool RES>
+template <bool SWIGLU, int OUT, bool RES, int BN = WIDE_BN>
 int wide_clusters(int ranks) {
-    if (cudaFuncSetAttribute(fp8_wide_kernel<SWIGLU, OUT, RES>, cudaFuncAttributeMaxDynamicSharedMemorySize, WIDE_SMEM) !=
-        cudaSuccess)
+    if (cudaFuncSetAttribute(fp8_wide_kernel<SWIGLU, OUT, RES, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             WIDE_SMEM) != cudaSuccess)
         return 0;
     if (OUT != OUT_SPLIT) return device_sm_count();
-    return resident_clusters(fp8_wide_kernel<SWIGLU, OUT, RES>, ranks, WIDE_THREADS, WIDE_SMEM);
+    return resident_clusters(fp8_wide_kernel<SWIGLU, OUT, RES, BN>, ranks, WIDE_THREADS, WIDE_SMEM);
+}
+
+// The weights' tensor maps with boxes of `rows` rows
+bool weight_maps(CUtensorMap *tw, CUtensorMap *tw2, const eagle3_linear_fp8_args_t *a, int rows) {
+    const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    const int64_t ld_w = a->ld_w ? a->ld_w : a->k;
+    if (!tmap_rows(tw, u8, 1, a->w, a->n, a->k, ld_w, rows)) return false;
+    *tw2 = *tw;   // where unused
+    return a->epilogue != EAGLE3_EPI_SWIGLU || tmap_rows(tw2, u8, 1, a->w2, a->n, a->k, ld_w, rows);
 }
 
 template <bool SWIGLU, bool RES>
-cudaError_t launch_wide(cudaStream_t st, const CUtensorMap &tx, const CUtensorMap &tw, const CUtensorMap &tw2,
-                        const CUtensorMap &to, const CUtensorMap &tr, Fp8Params &p) {
+cudaError_t launch_wide(const eagle3_linear_fp8_args_t *a, cudaStream_t st, const CUtensorMap &tx, const CUtensorMap &to,
+                        const CUtensorMap &tr, Fp8Params &p) {
     static PerDevice<ClusterCounts> cache;
     const ClusterCounts most = cache.get([] {
         ClusterCounts c = {};
-        c.n[1] = std::min(wide_clusters<SWIGLU, OUT_TMA, RES>(1), wide_clusters<SWIGLU, OUT_STAGED, RES>(1));
+        c.n[0] = std::min(wide_clusters<SWIGLU, OUT_TMA, RES>(1), wide_clusters<SWIGLU, OUT_STAGED, RES>(1));
         for (int r = 2; r <= MAX_RANKS; ++r)
-            if (split_bytes(r) <= WIDE_STAGES * WIDE_STAGE) c.n[r] = wide_clusters<SWIGLU, OUT_SPLIT, RES>(r);
+            if (split_bytes<WIDE_BN>(r) <= WIDE_RING && split_bytes<SPLIT_BN>(r) <= WIDE_RING)
+                c.n[r] = std::min(wide_clusters<SWIGLU, OUT_SPLIT, RES>(r),
+                                  wide_clusters<SWIGLU, OUT_SPLIT, RES, SPLIT_BN>(r));
         return c;
     });
-    if (most.n[1] < 1) return cudaErrorUnknown;
-    // As many ranks as leave every tile a resident cluster, if that saves each CTA 18 k-blocks: a k-block takes
-    // 0.35 us, and meeting and adding up about 6 us (256 x 4096 x 14336, 112 k-blocks: 44 us by single CTAs, 30
-    // by two, 21 by four; 256 x 1024 x 2048, 16 k-blocks: 9.4 and 11.8 us).
-    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+    if (most.n[0] < 1) return cudaErrorUnknown;
+    // Few tiles: their k-blocks over as many ranks as leave every tile a resident cluster, with tiles of 256 or 128
+    // columns, by the k-blocks in a row: a CTA's own (0.35 us each, whatever the width: they wait for L2), and 17 or 7
+    // for sending, meeting and adding up 128 x 256 or 128 x 128 sums.  (256 x 4096 x 14336: 44 us by single CTAs, 25 by
+    // four ranks of 256 columns, 29 by two of 128; 128 x 4096 x 4096: 15, 13.6 by six, 9.2 by four of 128; 128 x 1024 x
+    // 2048: 9.0 and 7.3 by eight of 128; x 1024: 6.3 either way.)
+    const int cols = SWIGLU ? SPLIT_BN / 2 : SPLIT_BN, narrower_n = (p.n + cols - 1) / cols;
+    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, narrower = (int64_t)p.tiles_m * narrower_n;
+    int64_t least = (tiles + most.n[0] - 1) / most.n[0] * p.kb_total;
+    bool narrow = false;
     p.ranks = 1;
-    for (int r = 2; r <= MAX_RANKS; ++r)
-        if (tiles <= most.n[r] && p.kb_total - p.kb_total / r >= 18) p.ranks = r;
+    for (int r = 2; r <= std::min(MAX_RANKS, p.kb_total); ++r) {
+        const int own = (p.kb_total + r - 1) / r;
+        if (tiles <= most.n[r] && own + 17 < least) least = own + 17, p.ranks = r, narrow = false;
+        if (narrower <= most.n[r] && own + 7 < least) least = own + 7, p.ranks = r, narrow = true;
+    }
+    CUtensorMap tw, tw2;
+    if (!weight_maps(&tw, &tw2, a, (narrow ? SPLIT_BN : WIDE_BN) / (SWIGLU ? 2 : 1))) return cudaErrorInvalidValue;
+    if (narrow) p.tiles_n = narrower_n;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)std::min<int64_t>(most.n[p.ranks], tiles) * p.ranks);
+    const int64_t split = (narrow ? narrower : tiles) * p.ranks;
+    cfg.gridDim = dim3((unsigned)(p.ranks > 1 ? split : std::min<int64_t>(most.n[0], tiles)));
     cfg.blockDim = dim3(WIDE_THREADS);
     cfg.dynamicSmemBytes = WIDE_SMEM;
     cfg.stream = st;
@@ -1098,6 +1121,8 @@ cudaError_t launch_wide(cudaStream_t st, const CUtensorMap &tx, const CUtensorMa
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = p.ranks > 1 ? 2 : 1;
+    if (narrow)
+        return cudaLaunchKernelEx(&cfg, fp8_wide_kernel<SWIGLU, OUT_SPLIT, RES, SPLIT_BN>, tx, tw, tw2, to, tr, p);
     return p.ranks > 1 ? cudaLaunchKernelEx(&cfg, fp8_wide_kernel<SWIGLU, OUT_SPLIT, RES>, tx, tw, tw2, to, tr, p)
            : p.tma_out ? cudaLaunchKernelEx(&cfg, fp8_wide_kernel<SWIGLU, OUT_TMA, RES>, tx, tw, tw2, to, tr, p)
                        : cudaLaunchKernelEx(&cfg, fp8_wide_kernel<SWIGLU, OUT_STAGED, RES>, tx, tw, tw2, to, tr, p);
@@ -1137,7 +1162,7 @@ extern "C" eagle3_status_t eagle3_linear_fp8(const eagle3_linear_fp8_args_t *a, 
     const eagle3_status_t st = validate(a);
     if (st != EAGLE3_OK || a->m == 0) return st;
     const bool swiglu = a->epilogue == EAGLE3_EPI_SWIGLU;
-    const int64_t ld_x = a->ld_x ? a->ld_x : a->k, ld_w = a->ld_w ? a->ld_w : a->k;
+    const int64_t ld_x = a->ld_x ? a->ld_x : a->k;
     Fp8Params p;
     p.m = a->m;
     p.n = a->n;
@@ -1164,16 +1189,12 @@ extern "C" eagle3_status_t eagle3_linear_fp8(const eagle3_linear_fp8_args_t *a, 
     // 27; 32 rows 24.6 and 21.0, 64 rows 27 and 21.  96 x 4096 x 14336: 34 (with tiles of 128 rows) and 20.
     const bool narrow = tiles_w <= 65535 && (a->m <= 24 || (a->m <= NARROW_MAX && 2 * p.tiles_n < sms));
     CUtensorMap tx, tw, tw2, to, tr;
-    const int w_box = narrow ? (swiglu ? 16 : BM) : (swiglu ? WIDE_BN / 2 : WIDE_BN);
-    if (!tmap_rows(&tx, u8, 1, a->x, a->m, a->k, ld_x, narrow ? 16 : BM) ||
-        !tmap_rows(&tw, u8, 1, a->w, a->n, a->k, ld_w, w_box))
-        return EAGLE3_ERR_CUDA;
-    tw2 = tw;
-    if (swiglu && !tmap_rows(&tw2, u8, 1, a->w2, a->n, a->k, ld_w, w_box)) return EAGLE3_ERR_CUDA;
+    if (!tmap_rows(&tx, u8, 1, a->x, a->m, a->k, ld_x, narrow ? 16 : BM)) return EAGLE3_ERR_CUDA;
     p.tma_out = p.n16 = p.stages = 0;
     p.ranks = 1;
     cudaError_t e;
     if (narrow) {
+        if (!weight_maps(&tw, &tw2, a, swiglu ? 16 : BM)) return EAGLE3_ERR_CUDA;
         p.n16 = (a->m + 15) / 16 * 16;
         p.stages = std::min(NARROW_STAGES, NARROW_RING / (NARROW_W + p.n16 * BK));
         if (p.n16 <= 32)
@@ -1190,9 +1211,9 @@ extern "C" eagle3_status_t eagle3_linear_fp8(const eagle3_linear_fp8_args_t *a, 
                     (!res || box_map(&tr, a, a->residual, p.ld_res, false));
         if (!p.tma_out) to = tx;   // unused
         if (!p.tma_out || !res) tr = tx;
-        e = swiglu                                      ? launch_wide<true, false>(s, tx, tw, tw2, to, tr, p)
-            : a->epilogue == EAGLE3_EPI_BF16_RESIDUAL ? launch_wide<false, true>(s, tx, tw, tw2, to, tr, p)
-                                                      : launch_wide<false, false>(s, tx, tw, tw2, to, tr, p);
+        e = swiglu                                      ? launch_wide<true, false>(a, s, tx, to, tr, p)
+            : a->epilogue == EAGLE3_EPI_BF16_RESIDUAL ? launch_wide<false, true>(a, s, tx, to, tr, p)
+                                                      : launch_wide<false, false>(a, s, tx, to, tr, p);
     }
     return e == cudaSuccess ? EAGLE3_OK : EAGLE3_ERR_CUDA;
 }

@@ -120,6 +120,9 @@ E3_DEV float cluster_ld(uint32_t addr) {
 E3_DEV void cluster_st(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(addr), "f"(v) : "memory");
 }
+E3_DEV void cluster_st4(uint32_t addr, float a, float b, float c, float d) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};\n" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
+}
 // Arrive on a barrier anywhere in the cluster (cluster_addr) by the lanes for which `one` holds.  The
 // default order is enough for what it announces here: loads that another barrier has shown to have landed
 // (or copies behind a proxy fence) and TMEM reads that have been waited for; there are no plain writes to

@@ -139,9 +139,11 @@ def test_fp8_many_rows(m, n, k, epi):
 
 
 @pytest.mark.parametrize("epi", EPIS)
-@pytest.mark.parametrize("m,n,k", [(70, 130, 4112), (129, 1, 2560), (200, 521, 8192), (100, 2600, 3088)])
+@pytest.mark.parametrize("m,n,k", [(70, 130, 4112), (129, 1, 2560), (200, 521, 8192), (100, 2600, 3088),
+                                   (1100, 1001, 6160), (1100, 1161, 6160)])
 def test_fp8_k_ranges(m, n, k, epi):
-    """Few tiles and a long k: the k-blocks are cut over a cluster, with odd ranges and odd columns."""
+    """Few tiles and a long k: the k-blocks are cut over a cluster, with odd ranges and odd columns (the last two by
+    tiles of 256 columns, the others of 128)."""
     _check(m, n, k, epi)
     _check(m, n, k, epi, seed=1, out_pitch=3)
 
