@@ -700,8 +700,9 @@ cudaError_t launch_grouped(int64_t row_tiles, cudaStream_t st, const RowMaps &tx
     // more for each 16 rows of a tile: a k-block takes 0.2 us, and sending, meeting and adding up 1 us for a few
     // rows, 5 us for 256.  (2 rows, 2 groups, 1024 columns: k = 14336 45 us by single CTAs, 15 by eight ranks, k =
     // 1024 7.3 and 6.0, k = 512 5.7 and 5.8; 500 rows, 2 groups, 512 columns: k = 4096 20 and 13, k = 1024 9.2 and 11.)
+    // Every rank has a k-block: without one it would send what an earlier kernel left in tensor memory.
     p.ranks = 1;
-    for (int r = 2; r <= MAX_RANKS; ++r)
+    for (int r = 2; r <= std::min(MAX_RANKS, p.kb_total); ++r)
         if (row_tiles * p.tiles_w <= split.n[r] && p.kb_total - p.kb_total / r >= 6 + std::min(p.m, MAX_ROWS) / 16)
             p.ranks = r;
     if (p.ranks > 1)

@@ -511,3 +511,39 @@ def test_readme_example():
     y, S = fp8.linear(codes, scale, v["w8"].view(torch.uint8).cpu().numpy(), v["w_scale"].cpu().numpy())
     tol = (256 + 3 + scale.shape[0]) * U * S
     assert (np.abs(_np(v["proj"]) - y) <= tol + BF16 * (np.abs(y) + tol) + TINY).all()
+
+
+# ----------------------------------------------------------------------------- as few k-blocks as ranks
+def _leave_in_tmem(value):
+    """Accumulators full of `value` in the tensor memory of every SM."""
+    dev = require_gpu()
+    x = torch.full((1024, 64), value, dtype=bf, device=dev)
+    e3.eagle3_grouped_linear(x, torch.ones(1, 128 * 160, 64, dtype=bf, device=dev), _offsets([1024], dev),
+                             torch.empty(1024, 128 * 160, dtype=bf, device=dev))
+
+
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("k", [320, 328, 384, 392, 448, 456, 512, 576])
+@pytest.mark.parametrize("counts,n", [([1], 64), ([1], 128), ([0, 1, 0], 200), ([2, 2], 1024), ([15], 128), ([16], 64),
+                                      ([3, 28], 128)])
+def test_grouped_short_k_ranges(counts, n, k, swiglu, gather):
+    """5 to 9 k-blocks, where a cut over a cluster begins to pay: every rank has a block of its own, so that nothing
+    of what an earlier call left in tensor memory (NaN, large sums) gets into the sums, and every run gives the
+    same bits."""
+    _leave_in_tmem(float("nan"))
+    _grouped(counts, n, k, swiglu, gather, seed=n + k, spare=2)
+    dev = require_gpu()
+    g = torch.Generator().manual_seed(k)
+    m = sum(counts)
+    x, w, w2 = (torch.randn(*s, generator=g).to(bf).to(dev) for s in ((m, k), (len(counts), n, k), (len(counts), n, k)))
+    ids = torch.arange(m, dtype=i32, device=dev) if gather else None
+    outs = []
+    for value in (1.0, 3e4, float("nan")):
+        _leave_in_tmem(value)
+        out = torch.empty(m, n, dtype=bf, device=dev)
+        e3.eagle3_grouped_linear(x, w, _offsets(counts, dev), out, epilogue=e3.EPI_SWIGLU if swiglu else e3.EPI_BF16,
+                                 w2=w2 if swiglu else None, row_ids=ids)
+        outs.append(out)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
