@@ -228,6 +228,10 @@ def _declare(L):
     L.eagle3_quantize_fp8.argtypes = [P(QuantizeFp8Args), _p]
     L.eagle3_linear_fp8.restype = ctypes.c_int
     L.eagle3_linear_fp8.argtypes = [P(LinearFp8Args), _p]
+    L.eagle3_test_grouped_linear_timeout.restype = ctypes.c_int
+    L.eagle3_test_grouped_linear_timeout.argtypes = [P(GroupedLinearArgs), _i32, _i32, _i64, _p]
+    L.eagle3_test_linear_fp8_timeout.restype = ctypes.c_int
+    L.eagle3_test_linear_fp8_timeout.argtypes = [P(LinearFp8Args), _i32, _i32, _i64, _p]
     L.eagle3_f32_linear.restype = ctypes.c_int
     L.eagle3_f32_linear.argtypes = [P(F32LinearArgs), _p]
     L.eagle3_f32_rmsnorm.restype = ctypes.c_int
@@ -785,6 +789,16 @@ def eagle3_grouped_linear(x, w, offsets, out, *, epilogue=EPI_BF16, w2=None, row
     _check(lib().eagle3_grouped_linear(ctypes.byref(a), _on(out.get_device(), stream)), "eagle3_grouped_linear")
 
 
+def eagle3_test_grouped_linear_timeout(x, w, offsets, out, *, stall_block, wait_limit_cycles, stall_rank=-1, stream=None,
+                                       **kw):
+    """Test hook (include/eagle3_testing.h): eagle3_grouped_linear with a k-block that never arrives and every
+    bounded wait limited to wait_limit_cycles, so the timeout path runs."""
+    a = grouped_linear_args(x, w, offsets, out, **kw)
+    _check(lib().eagle3_test_grouped_linear_timeout(ctypes.byref(a), int(stall_block), int(stall_rank),
+                                                    int(wait_limit_cycles), _on(out.get_device(), stream)),
+           "eagle3_test_grouped_linear_timeout")
+
+
 def moe_combine_args(y, slots, weights, out, *, residual=None, dev_status=None):
     T, k = slots.shape
     n_slots, d = y.shape
@@ -850,6 +864,16 @@ def eagle3_linear_fp8(x, x_scale, w, w_scale, out, *, epilogue=EPI_BF16, w2=None
     a = linear_fp8_args(x, x_scale, w, w_scale, out, epilogue=epilogue, w2=w2, w2_scale=w2_scale, residual=residual,
                         dev_status=dev_status)
     _check(lib().eagle3_linear_fp8(ctypes.byref(a), _on(x.get_device(), stream)), "eagle3_linear_fp8")
+
+
+def eagle3_test_linear_fp8_timeout(x, x_scale, w, w_scale, out, *, stall_block, wait_limit_cycles, stall_rank=-1,
+                                   stream=None, **kw):
+    """Test hook (include/eagle3_testing.h): eagle3_linear_fp8 with a k-block that never arrives and every bounded
+    wait limited to wait_limit_cycles, so the timeout path runs."""
+    a = linear_fp8_args(x, x_scale, w, w_scale, out, **kw)
+    _check(lib().eagle3_test_linear_fp8_timeout(ctypes.byref(a), int(stall_block), int(stall_rank),
+                                                int(wait_limit_cycles), _on(x.get_device(), stream)),
+           "eagle3_test_linear_fp8_timeout")
 
 
 # ----------------------------------------------------------------------------- fp32 small-model blocks

@@ -194,6 +194,26 @@ E3_DEV void flag(int32_t *dev_status, int bits) {
 
 // ~2 s at 2 GHz: a wait that outlives this has lost its producer
 constexpr long long WAIT_LIMIT_CYCLES = 4000000000LL;
+// What a launch says about its waits (by test hooks only otherwise than here): their limit in 1024 clocks, and a load
+// stage whose barrier expects an arrival that never comes, in all CTAs or those of one rank in their cluster
+struct WaitRule {
+    uint32_t limit = (uint32_t)(WAIT_LIMIT_CYCLES >> 10);
+    int stall_stage = -1, stall_rank = -1;
+};
+E3_DEV int missing_arrivals(const WaitRule &w, int stage, int rank) {
+    return stage == w.stall_stage && (w.stall_rank < 0 || w.stall_rank == rank) ? 1 : 0;
+}
+// A test hook's rule from its arguments; false where they are out of range
+constexpr int LEAST_STAGES = 4;   // load stages that every kernel with such a rule has
+inline bool stall_rule(WaitRule *w, int stall_block, int stall_rank, long long limit_cycles) {
+    if (stall_block < 0 || stall_block >= LEAST_STAGES || stall_rank < -1 || limit_cycles < 1000 ||
+        limit_cycles > WAIT_LIMIT_CYCLES)
+        return false;
+    w->limit = (uint32_t)(limit_cycles >> 10);
+    w->stall_stage = stall_block;
+    w->stall_rank = stall_rank;
+    return true;
+}
 
 E3_DEV uint32_t smem_u32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 

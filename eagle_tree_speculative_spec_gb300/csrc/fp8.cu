@@ -24,6 +24,7 @@
 #include <cuda_fp8.h>
 
 #include "../../include/eagle3_fp8.h"
+#include "../../include/eagle3_testing.h"
 #include "tc.cuh"
 #include "tmap.cuh"
 
@@ -50,6 +51,7 @@ struct Fp8Params {
     int ranks;              // OUT_SPLIT: CTAs of a cluster, each a range of a tile's k-blocks (one tile a cluster)
     int tma_out;            // wide: outputs leave through shared memory and TMA stores
     int n16, stages;        // narrow: rows of a tile (multiple of 16), ring depth
+    WaitRule wait;
 };
 
 // ---- quantisation -------------------------------------------------------------------------------
@@ -326,6 +328,7 @@ struct WideShared {
 };
 constexpr int WIDE_SMEM = 1024 + WIDE_RING + 2 * WIDE_EPI_WARPS * WIDE_BOX + (int)sizeof(WideShared);
 static_assert(WIDE_SMEM <= 232448, "shared memory budget");
+static_assert(WIDE_STAGES >= LEAST_STAGES && SPLIT_STAGES >= LEAST_STAGES, "stages");
 
 // SPLIT: where rank src's sums of piece j (4 columns of each run, 128 rows) of an epilogue half lie in the ring of
 // the rank that the piece belongs to, j / split_pieces: two quads of values, all rows of a quad side by side; byte
@@ -380,7 +383,8 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            tc::mbar_init(&sh.full[s], 1 + WIDE_EPI_WARPS);
+            tc::mbar_init(&sh.full[s],
+                          1 + WIDE_EPI_WARPS + missing_arrivals(p.wait, s, SPLIT ? (int)blockIdx.x % p.ranks : 0));
             tc::mbar_init(&sh.done[s], 1);
         }
         tc::mbar_init(&sh.mma_done, 1);
@@ -417,7 +421,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                 for (int u = unit0; ok && u < units; u += unit_step) {
                     const int mb = u % p.tiles_m, nb = u / p.tiles_m;
                     for (int kb = kb0; kb < kb1; ++kb) {
-                        if (!tc::mbar_wait(done0 + stage * 8, phase ^ 1u, abort0)) {
+                        if (!tc::mbar_wait(done0 + stage * 8, phase ^ 1u, abort0, p.wait.limit)) {
                             ok = false;
                             break;
                         }
@@ -440,8 +444,9 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                 }
                 if (!ok) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
                 // no TMA write may still be in flight when the CTA exits (bounded waits)
+                const uint32_t t0 = tc::kiloclock();
                 for (int st = 0; st < STAGES; ++st)
-                    if ((issued >> st) & 1u) tc::mbar_drain(full0 + st * 8, (last_parity >> st) & 1u);
+                    if ((issued >> st) & 1u) tc::mbar_drain(full0 + st * 8, (last_parity >> st) & 1u, t0, p.wait.limit);
             }
             __syncwarp();
         } else if (warp == 1) {
@@ -454,7 +459,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                 bool ok = true;
                 for (int u = unit0; ok && u < units; u += unit_step)
                     for (int kb = kb0; kb < kb1; ++kb) {
-                        if (!tc::mbar_wait(full0 + stage * 8, phase, abort0)) {
+                        if (!tc::mbar_wait(full0 + stage * 8, phase, abort0, p.wait.limit)) {
                             ok = false;
                             break;
                         }
@@ -474,7 +479,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                 if (!ok) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
                 // every MMA this thread issued must retire before TMEM is freed (bounded wait)
                 tc::mma_commit(smem_u32(&sh.mma_done));
-                tc::mbar_drain(smem_u32(&sh.mma_done), 0);
+                tc::mbar_drain(smem_u32(&sh.mma_done), 0, tc::kiloclock(), p.wait.limit);
             }
             __syncwarp();
         }
@@ -527,7 +532,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                 }
                 const float fa = sx * __shfl_sync(0xffffffffu, sa, kb & 31);
                 const float fb = SWIGLU ? sx * __shfl_sync(0xffffffffu, sb, kb & 31) : fa;
-                if (!tc::mbar_wait_warp(done0 + stage * 8, phase, abort0)) {
+                if (!tc::mbar_wait_warp(done0 + stage * 8, phase, abort0, p.wait.limit)) {
                     ok = false;
                     break;
                 }
@@ -605,7 +610,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
                     for (int i = 32 * c; i < 32 * c + 32; ++i) acc[i] = silu(acc[i]) * acc[RUN + i];
                 }
                 if (RES_TMA && ok && x < p.n) {
-                    ok = tc::mbar_wait_warp(res_bar, res_phase, abort0);
+                    ok = tc::mbar_wait_warp(res_bar, res_phase, abort0, p.wait.limit);
                     res_phase ^= 1u;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
@@ -652,7 +657,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
             }
             if (RES_TMA && !ok && lane == 0) {
                 flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
-                tc::mbar_drain(res_bar, res_phase ^ 1u);
+                tc::mbar_drain(res_bar, res_phase ^ 1u, tc::kiloclock(), p.wait.limit);
             }
         }
         if (lane == 0) tc::bulk_wait<0>();
@@ -710,6 +715,7 @@ struct NarrowShared {
 constexpr int NARROW_SMEM = 1024 + NARROW_RING + (int)sizeof(NarrowShared);
 static_assert(2 * (NARROW_SMEM + 1024) <= 228 * 1024, "two CTAs a SM");
 static_assert(NARROW_RING >= NARROW_MAX * BM * 4, "the ranks' sums fit the ring");
+static_assert(NARROW_RING / (NARROW_W + NARROW_MAX * BK) >= LEAST_STAGES, "stages of the largest tiles");
 
 // NT: row capacity of a tile (TMEM buffers of NT columns, NT / 2 accumulators a thread).
 // Grid: (cluster ranks = k ranges, weight tiles).
@@ -727,10 +733,11 @@ __global__ void __launch_bounds__(NARROW_THREADS, 2)
     const int kb0 = (int)((long long)p.kb_total * rank / ranks);
     const int kb1 = (int)((long long)p.kb_total * (rank + 1) / ranks);
     const int stage_bytes = NARROW_W + p.n16 * BK, stages = p.stages;
+    const long long wait_limit = (long long)p.wait.limit << 10;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < NARROW_STAGES; ++s) {
-            tc::mbar_init(&sh.full[s], 1);
+            tc::mbar_init(&sh.full[s], 1 + missing_arrivals(p.wait, s, rank));
             tc::mbar_init(&sh.empty[s], 1);
         }
         for (int b = 0; b < BUFS; ++b) {
@@ -766,7 +773,7 @@ __global__ void __launch_bounds__(NARROW_THREADS, 2)
         for (int kb = kb0; kb < kb1; ++kb) {
             int fine = 1;
             if (lane == 0) {
-                fine = tc::mbar_wait(&sh.empty[stage], phase ^ 1u, abort) ? 1 : 0;
+                fine = tc::mbar_wait(&sh.empty[stage], phase ^ 1u, abort, wait_limit) ? 1 : 0;
                 if (fine) {
                     tc::mbar_expect_tx(&sh.full[stage], stage_bytes);
                     issued |= 1u << stage;
@@ -797,11 +804,11 @@ __global__ void __launch_bounds__(NARROW_THREADS, 2)
         }
         if (lane == 0) {
             if (!ok) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
+            const long long t0 = clock64();
             for (int st = 0; st < stages; ++st) {   // loads in flight (bounded waits)
                 if (!((issued >> st) & 1u)) continue;
                 const uint32_t par = (last_parity >> st) & 1u;
-                const long long t0 = clock64();
-                while (!tc::mbar_try(&sh.full[st], par) && clock64() - t0 < WAIT_LIMIT_CYCLES) {
+                while (!tc::mbar_try(&sh.full[st], par) && clock64() - t0 < wait_limit) {
                 }
             }
         }
@@ -815,8 +822,8 @@ __global__ void __launch_bounds__(NARROW_THREADS, 2)
             uint32_t phase = 0, buf_phase = 0;
             bool ok = true;
             for (int kb = kb0; kb < kb1; ++kb) {
-                if (!tc::mbar_wait(&sh.tempty[buf], buf_phase ^ 1u, abort) ||
-                    !tc::mbar_wait(&sh.full[stage], phase, abort)) {
+                if (!tc::mbar_wait(&sh.tempty[buf], buf_phase ^ 1u, abort, wait_limit) ||
+                    !tc::mbar_wait(&sh.full[stage], phase, abort, wait_limit)) {
                     ok = false;
                     break;
                 }
@@ -839,7 +846,7 @@ __global__ void __launch_bounds__(NARROW_THREADS, 2)
             if (!ok) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
             tc::mma_commit(&sh.mma_done);
             const long long t0 = clock64();
-            while (!tc::mbar_try(&sh.mma_done, 0) && clock64() - t0 < WAIT_LIMIT_CYCLES) {
+            while (!tc::mbar_try(&sh.mma_done, 0) && clock64() - t0 < wait_limit) {
             }
         }
         __syncwarp();
@@ -875,7 +882,7 @@ __global__ void __launch_bounds__(NARROW_THREADS, 2)
             const float fw = sw;
             if (kb + 1 < kb1) fetch(kb + 1);
             // (the vote also orders the strip's writes)
-            if (!tc::mbar_wait_warp(tfull0 + buf * 8, buf_phase, abort0)) {
+            if (!tc::mbar_wait_warp(tfull0 + buf * 8, buf_phase, abort0, p.wait.limit)) {
                 if (lane == 0) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
                 break;
             }
@@ -1158,7 +1165,7 @@ extern "C" eagle3_status_t eagle3_quantize_fp8(const eagle3_quantize_fp8_args_t 
     return e == cudaSuccess ? EAGLE3_OK : EAGLE3_ERR_CUDA;
 }
 
-extern "C" eagle3_status_t eagle3_linear_fp8(const eagle3_linear_fp8_args_t *a, eagle3_stream_t stream) {
+static eagle3_status_t linear_fp8(const eagle3_linear_fp8_args_t *a, const WaitRule &wait, eagle3_stream_t stream) {
     const eagle3_status_t st = validate(a);
     if (st != EAGLE3_OK || a->m == 0) return st;
     const bool swiglu = a->epilogue == EAGLE3_EPI_SWIGLU;
@@ -1178,6 +1185,7 @@ extern "C" eagle3_status_t eagle3_linear_fp8(const eagle3_linear_fp8_args_t *a, 
     p.residual = (const __nv_bfloat16 *)a->residual;
     p.out = a->out;
     p.dev_status = a->dev_status;
+    p.wait = wait;
     const int sms = std::max(1, device_sm_count());
     const cudaStream_t s = (cudaStream_t)stream;
     const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
@@ -1216,4 +1224,16 @@ extern "C" eagle3_status_t eagle3_linear_fp8(const eagle3_linear_fp8_args_t *a, 
                                                       : launch_wide<false, false>(a, s, tx, to, tr, p);
     }
     return e == cudaSuccess ? EAGLE3_OK : EAGLE3_ERR_CUDA;
+}
+
+extern "C" eagle3_status_t eagle3_linear_fp8(const eagle3_linear_fp8_args_t *a, eagle3_stream_t stream) {
+    return linear_fp8(a, WaitRule(), stream);
+}
+
+extern "C" eagle3_status_t eagle3_test_linear_fp8_timeout(const eagle3_linear_fp8_args_t *a, int32_t stall_block,
+                                                          int32_t stall_rank, int64_t wait_limit_cycles,
+                                                          eagle3_stream_t stream) {
+    WaitRule wait;
+    if (!stall_rule(&wait, stall_block, stall_rank, wait_limit_cycles)) return EAGLE3_ERR_INVALID_ARGUMENT;
+    return linear_fp8(a, wait, stream);
 }

@@ -34,6 +34,7 @@
 
 #include "../../include/eagle3_chain.h"
 #include "../../include/eagle3_moe.h"
+#include "../../include/eagle3_testing.h"
 #include "tc.cuh"
 #include "tmap.cuh"
 
@@ -61,6 +62,7 @@ struct Shared {
 };
 constexpr int SMEM = 1024 /* align */ + RING_BYTES + (int)sizeof(Shared);
 static_assert(SMEM <= 232448, "shared memory budget");
+static_assert(RING_BYTES / (W_BYTES + MAX_ROWS * ROW_BYTES) >= LEAST_STAGES, "stages of the largest tiles");
 
 // Rows that a tile's boxes load: one box of 256, or up to three of 64 and one of 16 (at most the
 // next multiple of 64; rows past the tile's are loaded and not used).
@@ -81,6 +83,7 @@ struct GroupedParams {
     int32_t *dev_status;
     int paired;   // rows of out start on 4 bytes: two columns a store
     int ranks;    // SPLIT: CTAs of a cluster
+    WaitRule wait;
 };
 
 // Row tiles of a group of cnt rows, and the rows of each but the last: even shares (in multiples of
@@ -204,7 +207,8 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
     if (threadIdx.x == 0) {
         for (int s = 0; s < MAX_STAGES; ++s) {
             // the load's arrival, the gathering threads', and in the even CTA of a pair the odd one's
-            tc::mbar_init(&sh.full[s], 1 + (GATHER ? 32 * GATHER_WARPS : 0) + (PAIR && rank == 0 ? 1 : 0));
+            tc::mbar_init(&sh.full[s], 1 + (GATHER ? 32 * GATHER_WARPS : 0) + (PAIR && rank == 0 ? 1 : 0) +
+                                           missing_arrivals(p.wait, s, SPLIT ? part : rank));
             tc::mbar_init(&sh.empty[s], 1);
         }
         for (int a = 0; a < 2; ++a) {
@@ -296,7 +300,7 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
                 const int row0 = w.row0 + rank * mine, mt = PAIR ? 2 * w.mt + rank : w.mt;
                 for (int kb = kb0; kb < kb1; ++kb) {
                     const uint32_t full = full0 + stage * 8;
-                    if (!tc::mbar_wait(empty0 + stage * 8, phase ^ 1u, abort0)) {
+                    if (!tc::mbar_wait(empty0 + stage * 8, phase ^ 1u, abort0, p.wait.limit)) {
                         ok = false;
                         break;
                     }
@@ -330,8 +334,9 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
             if (!ok) flag(p.dev_status, EAGLE3_DEV_TIMEOUT);
             // no TMA write may still be in flight when the CTA exits: wait (bounded) for the last load
             // issued to every stage; these return at once when the loads were consumed
+            const uint32_t t0 = tc::kiloclock();
             for (int st = 0; st < stages; ++st)
-                if ((issued >> st) & 1u) tc::mbar_drain(full0 + st * 8, (last_parity >> st) & 1u);
+                if ((issued >> st) & 1u) tc::mbar_drain(full0 + st * 8, (last_parity >> st) & 1u, t0, p.wait.limit);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -345,7 +350,7 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
                 bool ok = true;
                 for (int u = unit0; ok && u < units; u += unit_step)
                     for (int kb = kb0; kb < kb1; ++kb) {
-                        if (!tc::mbar_wait(full0 + stage * 8, phase, abort0)) {
+                        if (!tc::mbar_wait(full0 + stage * 8, phase, abort0, p.wait.limit)) {
                             ok = false;
                             break;
                         }
@@ -366,14 +371,14 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
             for (int u = unit0; ok && u < units; u += unit_step) {
                 const Unit w = unit_at<STEP>(sh, p, u);
                 const uint32_t idesc = tc::idesc_bf16(PAIR ? 2 * BM : BM, w.n16);
-                if (!tc::mbar_wait(tempty0 + acc * 8, acc_phase ^ 1u, abort0)) {
+                if (!tc::mbar_wait(tempty0 + acc * 8, acc_phase ^ 1u, abort0, p.wait.limit)) {
                     ok = false;
                     break;
                 }
                 tc::fence_after();
                 const uint32_t d = tmem + (uint32_t)(acc * MAX_ROWS);
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!tc::mbar_wait(full0 + stage * 8, phase, abort0)) {
+                    if (!tc::mbar_wait(full0 + stage * 8, phase, abort0, p.wait.limit)) {
                         ok = false;
                         break;
                     }
@@ -412,7 +417,7 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
                 tc::mma2_commit(smem_u32(&sh.mma_done), 1);
             else
                 tc::mma_commit(smem_u32(&sh.mma_done));
-            tc::mbar_drain(smem_u32(&sh.mma_done), 0);
+            tc::mbar_drain(smem_u32(&sh.mma_done), 0, tc::kiloclock(), p.wait.limit);
         }
         __syncwarp();
     } else if (GATHER && warp >= 6) {
@@ -441,7 +446,7 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
                 src[i] = p.x + (size_t)v * p.ld_x + piece * 8;
             }
             for (int kb = kb0; kb < kb1; ++kb) {
-                if (!tc::mbar_wait_warp(empty0 + stage * 8, phase ^ 1u, abort0)) {
+                if (!tc::mbar_wait_warp(empty0 + stage * 8, phase ^ 1u, abort0, p.wait.limit)) {
                     ok = false;
                     break;
                 }
@@ -469,7 +474,7 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
         Unit unit = {};   // SPLIT: the cluster's
         for (int u = unit0; u < units; u += unit_step) {
             const Unit w = unit_at<STEP>(sh, p, u);
-            bool ok = tc::mbar_wait_warp(tfull0 + acc * 8, acc_phase, abort0);
+            bool ok = tc::mbar_wait_warp(tfull0 + acc * 8, acc_phase, abort0, p.wait.limit);
             // (the two warps of a pair go on or leave together: they meet at barriers below)
             if (SWIGLU) ok = pair_all(1 + (quarter & 1), ok);
             if (!ok) {
@@ -729,7 +734,8 @@ cudaError_t launch_grouped(int64_t row_tiles, cudaStream_t st, const RowMaps &tx
 
 using namespace e3;
 
-extern "C" eagle3_status_t eagle3_grouped_linear(const eagle3_grouped_linear_args_t *a, eagle3_stream_t stream) {
+static eagle3_status_t grouped_linear(const eagle3_grouped_linear_args_t *a, const WaitRule &wait,
+                                      eagle3_stream_t stream) {
     const eagle3_status_t st = validate(a);
     if (st != EAGLE3_OK || a->m == 0) return st;
     const bool swiglu = a->epilogue == EAGLE3_EPI_SWIGLU;
@@ -761,6 +767,7 @@ extern "C" eagle3_status_t eagle3_grouped_linear(const eagle3_grouped_linear_arg
     p.offsets = a->offsets;
     p.row_ids = a->row_ids;
     p.dev_status = a->dev_status;
+    p.wait = wait;
     p.paired = p.ld_out % 2 == 0 && ((uintptr_t)a->out & 3) == 0;
     const int64_t row_tiles = a->m / MAX_ROWS + std::min(a->m, a->n_groups);
     const cudaStream_t s = (cudaStream_t)stream;
@@ -769,4 +776,16 @@ extern "C" eagle3_status_t eagle3_grouped_linear(const eagle3_grouped_linear_arg
                                  : (a->row_ids ? launch_grouped<false, true>(row_tiles, s, tx, tw, tw2, p)
                                                : launch_grouped<false, false>(row_tiles, s, tx, tw, tw2, p));
     return e == cudaSuccess ? EAGLE3_OK : EAGLE3_ERR_CUDA;
+}
+
+extern "C" eagle3_status_t eagle3_grouped_linear(const eagle3_grouped_linear_args_t *a, eagle3_stream_t stream) {
+    return grouped_linear(a, WaitRule(), stream);
+}
+
+extern "C" eagle3_status_t eagle3_test_grouped_linear_timeout(const eagle3_grouped_linear_args_t *a, int32_t stall_block,
+                                                              int32_t stall_rank, int64_t wait_limit_cycles,
+                                                              eagle3_stream_t stream) {
+    WaitRule wait;
+    if (!stall_rule(&wait, stall_block, stall_rank, wait_limit_cycles)) return EAGLE3_ERR_INVALID_ARGUMENT;
+    return grouped_linear(a, wait, stream);
 }

@@ -45,9 +45,10 @@ E3_DEV bool mbar_wait(uint64_t *bar, uint32_t parity, volatile int *abort, long 
 }
 
 // The same by shared-memory address (computed once) and by whole warps, for loops that are short of issue
-// slots and registers: a poll is a handful of instructions, every lane gets the same answer, and the bound
-// is a number of polls (at least 20 cycles each: MAX_POLLS are seconds, as WAIT_LIMIT_CYCLES).
-constexpr uint32_t MAX_POLLS = 1u << 25;
+// slots and registers: a poll is a handful of instructions, and every lane gets the same answer.  The clock and the
+// abort flag are read every 64 polls (a poll of a barrier that does not complete suspends its thread for some 7800
+// cycles, but nothing says how long it has to).  `limit` is in 1024 clocks.
+E3_DEV uint32_t kiloclock() { return (uint32_t)(clock64() >> 10); }
 E3_DEV bool mbar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -57,12 +58,14 @@ E3_DEV bool mbar_try(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
-E3_DEV bool mbar_wait_warp(uint32_t bar, uint32_t parity, uint32_t abort_addr) {
+E3_DEV bool mbar_wait_warp(uint32_t bar, uint32_t parity, uint32_t abort_addr, uint32_t limit) {
+    uint32_t t0 = 0u;
     for (uint32_t n = 1; !__all_sync(0xffffffffu, mbar_try(bar, parity)); ++n) {
-        if ((n & 1023u) == 0u) {
+        if ((n & 63u) == 0u) {
             uint32_t gone;
             asm volatile("ld.volatile.shared.u32 %0, [%1];\n" : "=r"(gone) : "r"(abort_addr) : "memory");
-            if (__any_sync(0xffffffffu, gone != 0u || n >= MAX_POLLS)) {
+            if (n == 64u) t0 = kiloclock();
+            if (__any_sync(0xffffffffu, gone != 0u || kiloclock() - t0 > limit)) {
                 asm volatile("st.volatile.shared.u32 [%0], %1;\n" ::"r"(abort_addr), "r"(1) : "memory");
                 return false;
             }
@@ -71,12 +74,14 @@ E3_DEV bool mbar_wait_warp(uint32_t bar, uint32_t parity, uint32_t abort_addr) {
     return true;
 }
 // the same by one thread
-E3_DEV bool mbar_wait(uint32_t bar, uint32_t parity, uint32_t abort_addr) {
+E3_DEV bool mbar_wait(uint32_t bar, uint32_t parity, uint32_t abort_addr, uint32_t limit) {
+    uint32_t t0 = 0u;
     for (uint32_t n = 1; !mbar_try(bar, parity); ++n) {
-        if ((n & 1023u) == 0u) {
+        if ((n & 63u) == 0u) {
             uint32_t gone;
             asm volatile("ld.volatile.shared.u32 %0, [%1];\n" : "=r"(gone) : "r"(abort_addr) : "memory");
-            if (gone != 0u || n >= MAX_POLLS) {
+            if (n == 64u) t0 = kiloclock();
+            if (gone != 0u || kiloclock() - t0 > limit) {
                 asm volatile("st.volatile.shared.u32 [%0], %1;\n" ::"r"(abort_addr), "r"(1) : "memory");
                 return false;
             }
@@ -84,9 +89,10 @@ E3_DEV bool mbar_wait(uint32_t bar, uint32_t parity, uint32_t abort_addr) {
     }
     return true;
 }
-// after the last use: wait for a phase without regard to the abort flag
-E3_DEV void mbar_drain(uint32_t bar, uint32_t parity) {
-    for (uint32_t n = 0; n < MAX_POLLS && !mbar_try(bar, parity); ++n) {
+// after the last use: wait for a phase without regard to the abort flag, until `limit` past t0 (of kiloclock(), shared
+// by the barriers of a ring)
+E3_DEV void mbar_drain(uint32_t bar, uint32_t parity, uint32_t t0, uint32_t limit) {
+    while (!mbar_try(bar, parity) && kiloclock() - t0 <= limit) {
     }
 }
 E3_DEV void mbar_arrive(uint32_t bar) {
