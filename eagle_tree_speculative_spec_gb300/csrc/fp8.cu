@@ -349,10 +349,12 @@ E3_DEV uint32_t split_offset(int ranks, int src, int part, int j, int row) {
 
 template <int N>
 E3_DEV void registers_give() {
+    __syncwarp();
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
 }
 template <int N>
 E3_DEV void registers_take() {
+    __syncwarp();
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
 }
 
@@ -664,7 +666,6 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
         __syncwarp();
         if (SPLIT) {
             if (!ok) tc::cluster_sync();   // (after a timeout; its sums are void)
-            __syncwarp();
             tc::cluster_sync();
             const int mb = unit0 % p.tiles_m, nb = unit0 / p.tiles_m, row = mb * BM + quarter * 32 + lane;
             const int col0 = nb * (SWIGLU ? BN / 2 : BN) + (SWIGLU ? RUN : 2 * RUN) * part;
@@ -928,7 +929,6 @@ __global__ void __launch_bounds__(NARROW_THREADS, 2)
         tc::tmem_dealloc(tmem, NARROW_TMEM);
     }
     if (ranks > 1) {
-        __syncwarp();
         tc::cluster_sync();
     }
     // rows rank, rank + ranks, ...: the ranks' sums in rank order, the epilogue, the output
@@ -957,7 +957,6 @@ __global__ void __launch_bounds__(NARROW_THREADS, 2)
         }
     }
     if (ranks > 1) {
-        __syncwarp();
         tc::cluster_sync();   // no rank leaves while another reads its sums
     }
 }

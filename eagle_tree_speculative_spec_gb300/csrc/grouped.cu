@@ -235,7 +235,6 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
     }
     tc::fence_before();
     if (PAIR) {
-        __syncwarp();
         tc::cluster_sync();
     } else {
         __syncthreads();
@@ -525,6 +524,7 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
                     for (int i = 0; i < 32; i += 2)
                         if (first + i < w.rows) store_pair(p, w.row0 + first + i, col, v[i], v[i + 1]);
                 }
+                __syncwarp();   // (what follows, TMEM loads or a pair's barrier, wants the whole warp)
             };
             if (SWIGLU) {
                 const int pair = quarter & 1, up = quarter >> 1;
@@ -570,7 +570,6 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
         __syncwarp();
         if (SPLIT) {
             if (unit.rows == 0) tc::cluster_sync();   // (no unit, or a timeout: its sums are void)
-            __syncwarp();
             tc::cluster_sync();
             // this rank's chunks: 128 threads take a column each, or with SwiGLU a pair's column and half of the rows
             const int t = (int)tid - 64, chunks = unit.n16 / SPLIT_ROWS, each = (chunks + p.ranks - 1) / p.ranks;
@@ -601,14 +600,12 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
         }
     }
     if (SPLIT && (warp < 2 || warp >= 6)) {   // (the epilogue's two)
-        __syncwarp();
         tc::cluster_sync();
         tc::cluster_sync();
     }
 
     tc::fence_before();
     if (PAIR) {   // no CTA leaves while the other may arrive on its barriers or multiply into its TMEM
-        __syncwarp();
         tc::cluster_sync();
     } else {
         __syncthreads();

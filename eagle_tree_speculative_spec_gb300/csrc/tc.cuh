@@ -109,7 +109,9 @@ E3_DEV void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
 }
 
 // ---- clusters: barriers and addresses of the other CTAs ---------------------------------------------
+// (the aligned forms want the whole warp, whatever branches its lanes have just come from)
 E3_DEV void cluster_sync() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;\n" ::: "memory");
 }
 // this CTA's shared-memory address in CTA `rank` of the cluster, and a load from there

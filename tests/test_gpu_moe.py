@@ -547,3 +547,18 @@ def test_grouped_short_k_ranges(counts, n, k, swiglu, gather):
         outs.append(out)
     torch.cuda.synchronize()
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+@pytest.mark.parametrize("T", [33, 61, 97, 130, 191, 225, 256])
+@pytest.mark.parametrize("k", [1, 3, 7])
+def test_route_cluster_with_uneven_ends(T, k):
+    """One launch of a cluster whose last rows, empty places and filler end in the middle of a warp, ten times over."""
+    dev = require_gpu()
+    z = torch.randn(T, 24, generator=torch.Generator().manual_seed(T + k))
+    z[::3, k // 2:] = -float("inf")   # every third row has too few
+    z = z.to(dev)
+    _check_route(z, k, num_rows=T - 5)
+    want = _route(z, k, num_rows=T - 5)[0]
+    for _ in range(10):
+        got = _route(z, k, num_rows=T - 5)[0]
+        assert all(torch.equal(got[n], want[n]) for n in want)
