@@ -248,10 +248,11 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
     bool bad = false;
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
         const int a = p.offsets[e], b = p.offsets[e + 1];
-        bad |= a < 0 || b < a || b > p.m || (e == 0 && a != 0);
+        const bool wrong = a < 0 || b < a || b > p.m || (e == 0 && a != 0);
+        bad |= wrong;
         sh.offsets[e] = a;
         if (e == p.E - 1) sh.offsets[p.E] = b;
-        if (b > a) {
+        if (!wrong && b > a) {   // (differences and tile counts of wild offsets would overflow)
             const int tiles = row_tiles(b - a);
             sh.tiles[e] = tiles;
             const int rows = tile_rows<STEP>(b - a, tiles) / (PAIR ? 2 : 1);   // of this CTA

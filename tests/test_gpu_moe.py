@@ -562,3 +562,26 @@ def test_route_cluster_with_uneven_ends(T, k):
     for _ in range(10):
         got = _route(z, k, num_rows=T - 5)[0]
         assert all(torch.equal(got[n], want[n]) for n in want)
+
+
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("n,k", [(128, 64), (640, 64), (64, 4096)])   # single CTAs, pairs, k over a cluster
+@pytest.mark.parametrize("offsets", [[0, 2 ** 31 - 1, -2 ** 31, 4], [-2 ** 31, 2 ** 31 - 1, 0, 4], [0, 2, 2 ** 31 - 1, 4],
+                                     [2 ** 31 - 1, -2 ** 31, 2 ** 31 - 1, -2 ** 31], [0, 4, 4, -1]])
+def test_grouped_wild_offsets(offsets, n, k, gather, swiglu):
+    """Offsets whose differences pass 32 bits: flagged, nothing written, and the next call is in order."""
+    dev = require_gpu()
+    x, w = torch.ones(4, k, dtype=bf, device=dev), torch.ones(3, n, k, dtype=bf, device=dev)
+    out, st = torch.full((4, n), 7.0, dtype=bf, device=dev), torch.zeros(1, dtype=i32, device=dev)
+    ids = torch.arange(4, dtype=i32, device=dev) if gather else None
+    call = lambda off: e3.eagle3_grouped_linear(x, w, torch.tensor(off, dtype=i32, device=dev), out, row_ids=ids,
+                                                epilogue=e3.EPI_SWIGLU if swiglu else e3.EPI_BF16,
+                                                w2=w if swiglu else None, dev_status=st)
+    call(offsets)
+    torch.cuda.synchronize()
+    assert int(st) == 0x20 and (out == 7).all()
+    st.zero_()
+    call([0, 1, 1, 4])
+    torch.cuda.synchronize()
+    assert int(st) == 0 and (out == (k * k if swiglu else k)).all()
