@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
                             break;
                         }
                         if (GATHER) tc::fence_proxy_async_smem();   // the copies were made outside the async proxy
-                        tc::mbar_arrive_cluster_if(even + stage * 8, true);
+                        tc::mbar_arrive_cluster_smem(even + stage * 8);
                         if (++stage == stages) {
                             stage = 0;
                             phase ^= 1u;
@@ -378,7 +378,9 @@ __global__ void __launch_bounds__(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), 1
                 tc::fence_after();
                 const uint32_t d = tmem + (uint32_t)(acc * MAX_ROWS);
                 for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!tc::mbar_wait(full0 + stage * 8, phase, abort0, p.wait.limit)) {
+                    const uint32_t full = full0 + stage * 8;
+                    if (!(PAIR ? tc::mbar_wait_cluster_smem(full, phase, abort0, p.wait.limit)
+                               : tc::mbar_wait(full, phase, abort0, p.wait.limit))) {
                         ok = false;
                         break;
                     }

@@ -74,9 +74,10 @@ E3_DEV bool mbar_wait_warp(uint32_t bar, uint32_t parity, uint32_t abort_addr, u
     return true;
 }
 // the same by one thread
-E3_DEV bool mbar_wait(uint32_t bar, uint32_t parity, uint32_t abort_addr, uint32_t limit) {
+template <typename Poll>
+E3_DEV bool mbar_wait_by(Poll poll, uint32_t abort_addr, uint32_t limit) {
     uint32_t t0 = 0u;
-    for (uint32_t n = 1; !mbar_try(bar, parity); ++n) {
+    for (uint32_t n = 1; !poll(); ++n) {
         if ((n & 63u) == 0u) {
             uint32_t gone;
             asm volatile("ld.volatile.shared.u32 %0, [%1];\n" : "=r"(gone) : "r"(abort_addr) : "memory");
@@ -88,6 +89,9 @@ E3_DEV bool mbar_wait(uint32_t bar, uint32_t parity, uint32_t abort_addr, uint32
         }
     }
     return true;
+}
+E3_DEV bool mbar_wait(uint32_t bar, uint32_t parity, uint32_t abort_addr, uint32_t limit) {
+    return mbar_wait_by([=] { return mbar_try(bar, parity); }, abort_addr, limit);
 }
 // after the last use: wait for a phase without regard to the abort flag, until `limit` past t0 (of kiloclock(), shared
 // by the barriers of a ring)
@@ -131,15 +135,36 @@ E3_DEV void cluster_st(uint32_t addr, float v) {
 E3_DEV void cluster_st4(uint32_t addr, float a, float b, float c, float d) {
     asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};\n" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
 }
-// Arrive on a barrier anywhere in the cluster (cluster_addr) by the lanes for which `one` holds.  The
-// default order is enough for what it announces here: loads that another barrier has shown to have landed
-// (or copies behind a proxy fence) and TMEM reads that have been waited for; there are no plain writes to
-// publish.  (.release.cluster flushes them all the same: a product of two-CTA tiles took 2.9 times as long.)
+// Arrive on a barrier anywhere in the cluster (cluster_addr) by the lanes for which `one` holds, to announce TMEM reads
+// that have been waited for: there are no writes to publish, and the default order is enough.
 E3_DEV void mbar_arrive_cluster_if(uint32_t bar, bool one) {
     asm volatile(
         "{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n @p mbarrier.arrive.shared::cluster.b64 _, [%0];\n}\n" ::"r"(bar),
         "r"(one ? 1u : 0u)
         : "memory");
+}
+// The same to announce what lies in this CTA's shared memory, and the wait that goes with it: a release and an acquire of
+// cluster scope, which the default scope (one CTA) would not be, restricted to shared memory.  (An unrestricted
+// .release.cluster takes some 1800 cycles: a product of two-CTA tiles took 2.9 times as long; so restricted 1.01 times.)
+E3_DEV void mbar_arrive_cluster_smem(uint32_t bar) {
+    asm volatile(
+        "fence.release.sync_restrict::shared::cta.cluster;\n"
+        "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(bar)
+        : "memory");
+}
+E3_DEV bool mbar_wait_cluster_smem(uint32_t bar, uint32_t parity, uint32_t abort_addr, uint32_t limit) {
+    const bool ok = mbar_wait_by([=] {
+        uint32_t done;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(done)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        return done != 0;
+    }, abort_addr, limit);
+    asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;\n" ::: "memory");
+    return ok;
 }
 
 // ---- TMA -----------------------------------------------------------------------------------------

@@ -21,3 +21,17 @@ def test_aligned_instructions_are_converged(instruction, uses):
             body = text[text.rindex("E3_DEV void", 0, m.start()):m.start()]
             assert "}" not in body and "__syncwarp();" in body, (os.path.basename(path), body)
     assert found == uses
+
+
+def test_other_ctas_are_told_at_cluster_scope():
+    """What one CTA of a pair announces to the other about its shared memory is released and acquired at cluster scope;
+    arrivals of the default scope announce TMEM reads only (tempty)."""
+    tc = open(os.path.join(CSRC, "tc.cuh")).read()
+    arrive = tc[tc.index("E3_DEV void mbar_arrive_cluster_smem"):tc.index("E3_DEV bool mbar_wait_cluster_smem")]
+    wait = tc[tc.index("E3_DEV bool mbar_wait_cluster_smem"):]
+    assert arrive.index("fence.release.sync_restrict::shared::cta.cluster") < arrive.index("mbarrier.arrive.relaxed.cluster")
+    assert wait.index("try_wait.parity.relaxed.cluster") < wait.index("fence.acquire.sync_restrict::shared::cluster.cluster")
+    for path in glob.glob(os.path.join(CSRC, "*.cu")):
+        for line in open(path):
+            if "mbar_arrive_cluster_if" in line:
+                assert "tempty" in line, (os.path.basename(path), line)
