@@ -233,8 +233,24 @@ E3_DEV void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;\n" :
 // Largest size (rows, columns, lengths) of the calls that round sizes up to whole tiles in 32 bits
 constexpr int MAX_DIM = 0x7fffffff - (1 << 16);
 
+// How many clusters of 2, 3, ... CTAs (index: the size; 1: single CTAs) a device holds at once, -1 where the query failed
+constexpr int MAX_CLUSTER = 8;
+struct ClusterCounts {
+    int n[MAX_CLUSTER + 1];
+};
+
+// Whether a query's answer is one to keep: an attribute set, a count that is there
+inline bool succeeded(cudaError_t e) { return e == cudaSuccess; }
+inline bool succeeded(int n) { return n > 0; }
+inline bool succeeded(const ClusterCounts &c) {
+    for (const int n : c.n)
+        if (n < 0) return false;
+    return true;
+}
+
 // Host-side value computed once per device (for the device current at the call) and kept:
-// kernel attributes and device attribute queries.  Safe for concurrent callers.
+// kernel attributes and device attribute queries.  One that failed is returned but not kept, so that the next call
+// asks again.  Safe for concurrent callers.
 template <typename T>
 struct PerDevice {
     static constexpr int MAX_DEVICES = 128;
@@ -248,7 +264,7 @@ struct PerDevice {
         std::lock_guard<std::mutex> lock(mu);
         if (!done[dev]) {
             val[dev] = f();
-            done[dev] = true;
+            done[dev] = succeeded(val[dev]);
         }
         return val[dev];
     }
@@ -264,6 +280,31 @@ inline int device_sm_count() {
             n = 0;
         return n > 0 ? n : 0;
     });
+}
+
+// Clusters of `ranks` CTAs of a kernel that the device holds at once, -1 on an error
+template <class Kernel>
+inline int resident_clusters(Kernel *kernel, int ranks, int threads, int smem) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return -1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ranks * device_sm_count());
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = ranks;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : -1;
+}
+// The same of single CTAs, where shared memory leaves room for one a SM
+template <class Kernel>
+inline int resident_ctas(Kernel *kernel, int smem) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return -1;
+    const int sms = device_sm_count();
+    return sms > 0 ? sms : -1;
 }
 
 template <typename... KArgs, typename... Args>

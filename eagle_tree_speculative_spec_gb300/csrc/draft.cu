@@ -1121,9 +1121,9 @@ extern "C" eagle3_status_t eagle3_draft_tree(const eagle3_draft_weights_t *W, co
             int n = 0;
             if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, topk_kernel<NT_TOPK>, NT_TOPK, 0) != cudaSuccess)
                 n = 0;
-            return n > 0 ? n : 1;
+            return n;
         });
-        const int wave = sms * per_sm;
+        const int wave = sms * (per_sm > 0 ? per_sm : 1);
         const TopkOut o = {(int32_t *)P(pl.o_ttok), (float *)P(pl.o_tlq), a->d2t, m.V, a->dev_status};
         // the shared-memory ring needs 16-byte rows: rows of a multiple of 4 floats, aligned logits
         const bool ring_ok = m.Vd % 4 == 0 && ((uintptr_t)logits & 15) == 0;

@@ -34,7 +34,6 @@ namespace {
 constexpr int BK = 128;                 // k values of a block and of a tile (128 bytes)
 constexpr int BM = 128;
 constexpr float E4M3_MAX = 448.0f;
-constexpr int MAX_RANKS = 8;            // largest cluster
 
 // (By the special function unit: the exponential is 2 + 1.2 |x| steps of fp32 off at the most and the division
 // 2, against a bf16 result's 2^15; 0 where exp(-x) passes 2^126, x below -87.3, where silu is above -2^-119.)
@@ -1005,45 +1004,23 @@ bool box_map(CUtensorMap *m, const eagle3_linear_fp8_args_t *a, const void *base
     return tmap_rows(m, type, es, base, a->m, a->n, ld, 32, 0, 0, 64);
 }
 
-// Clusters of `ranks` CTAs of a kernel that the device holds at once (0 on an error).
-template <class Kernel>
-int resident_clusters(Kernel *kernel, int ranks, int threads, int smem) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ranks * device_sm_count());
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = ranks;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    int n = 0;
-    return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : 0;
-}
-struct ClusterCounts {
-    int n[MAX_RANKS + 1];
-};
-
 template <int NT, bool SWIGLU>
 cudaError_t launch_narrow(int tiles, cudaStream_t st, const CUtensorMap &tx, const CUtensorMap &tw,
                           const CUtensorMap &tw2, const Fp8Params &p) {
     static PerDevice<ClusterCounts> cache;
     const ClusterCounts most = cache.get([] {
         ClusterCounts c = {};
-        if (cudaFuncSetAttribute(fp8_narrow_kernel<NT, SWIGLU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 NARROW_SMEM) == cudaSuccess)
-            for (int r = 1; r <= MAX_RANKS; ++r)
-                c.n[r] = resident_clusters(fp8_narrow_kernel<NT, SWIGLU>, r, NARROW_THREADS, NARROW_SMEM);
+        for (int r = 1; r <= MAX_CLUSTER; ++r)
+            c.n[r] = resident_clusters(fp8_narrow_kernel<NT, SWIGLU>, r, NARROW_THREADS, NARROW_SMEM);
         return c;
     });
-    if (most.n[1] < 1) return cudaErrorUnknown;
+    if (!succeeded(most) || most.n[1] < 1) return cudaErrorUnknown;
     // As many ranks as leave every tile a resident cluster, two k-blocks each at least.  The query counts one CTA a
     // SM; shared memory, registers and TMEM hold two, and two keep more loads in flight (8 rows, 99 tiles of 2 *
     // 6306 x 11040: 45 us by single CTAs, 28 by clusters of two, 41 by three, of which 92 are resident; 48 tiles of
     // 6144 x 4096: 8.2 us by three ranks, 7.1 by four, 11.8 by six, of which 46 are).
     int ranks = 1;
-    for (int r = 2; r <= MAX_RANKS; ++r)
+    for (int r = 2; r <= MAX_CLUSTER; ++r)
         if (tiles <= 2 * most.n[r] && p.kb_total >= 2 * r) ranks = r;
     const dim3 grid(ranks, tiles);
     cudaLaunchConfig_t cfg = {};
@@ -1065,11 +1042,8 @@ cudaError_t launch_narrow(int tiles, cudaStream_t st, const CUtensorMap &tx, con
 
 template <bool SWIGLU, int OUT, bool RES, int BN = WIDE_BN>
 int wide_clusters(int ranks) {
-    if (cudaFuncSetAttribute(fp8_wide_kernel<SWIGLU, OUT, RES, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             WIDE_SMEM) != cudaSuccess)
-        return 0;
-    if (OUT != OUT_SPLIT) return device_sm_count();
-    return resident_clusters(fp8_wide_kernel<SWIGLU, OUT, RES, BN>, ranks, WIDE_THREADS, WIDE_SMEM);
+    const auto kernel = fp8_wide_kernel<SWIGLU, OUT, RES, BN>;
+    return OUT == OUT_SPLIT ? resident_clusters(kernel, ranks, WIDE_THREADS, WIDE_SMEM) : resident_ctas(kernel, WIDE_SMEM);
 }
 
 // The weights' tensor maps with boxes of `rows` rows
@@ -1087,14 +1061,14 @@ cudaError_t launch_wide(const eagle3_linear_fp8_args_t *a, cudaStream_t st, cons
     static PerDevice<ClusterCounts> cache;
     const ClusterCounts most = cache.get([] {
         ClusterCounts c = {};
-        c.n[0] = std::min(wide_clusters<SWIGLU, OUT_TMA, RES>(1), wide_clusters<SWIGLU, OUT_STAGED, RES>(1));
-        for (int r = 2; r <= MAX_RANKS; ++r)
+        c.n[1] = std::min(wide_clusters<SWIGLU, OUT_TMA, RES>(1), wide_clusters<SWIGLU, OUT_STAGED, RES>(1));
+        for (int r = 2; r <= MAX_CLUSTER; ++r)
             if (split_bytes<WIDE_BN>(r) <= WIDE_RING && split_bytes<SPLIT_BN>(r) <= WIDE_RING)
                 c.n[r] = std::min(wide_clusters<SWIGLU, OUT_SPLIT, RES>(r),
                                   wide_clusters<SWIGLU, OUT_SPLIT, RES, SPLIT_BN>(r));
         return c;
     });
-    if (most.n[0] < 1) return cudaErrorUnknown;
+    if (!succeeded(most) || most.n[1] < 1) return cudaErrorUnknown;
     // Few tiles: their k-blocks over as many ranks as leave every tile a resident cluster, with tiles of 256 or 128
     // columns, by the k-blocks in a row: a CTA's own (0.35 us each, whatever the width: they wait for L2), and 17 or 7
     // for sending, meeting and adding up 128 x 256 or 128 x 128 sums.  (256 x 4096 x 14336: 44 us by single CTAs, 25 by
@@ -1102,10 +1076,10 @@ cudaError_t launch_wide(const eagle3_linear_fp8_args_t *a, cudaStream_t st, cons
     // 2048: 9.0 and 7.3 by eight of 128; x 1024: 6.3 either way.)
     const int cols = SWIGLU ? SPLIT_BN / 2 : SPLIT_BN, narrower_n = (p.n + cols - 1) / cols;
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, narrower = (int64_t)p.tiles_m * narrower_n;
-    int64_t least = (tiles + most.n[0] - 1) / most.n[0] * p.kb_total;
+    int64_t least = (tiles + most.n[1] - 1) / most.n[1] * p.kb_total;
     bool narrow = false;
     p.ranks = 1;
-    for (int r = 2; r <= std::min(MAX_RANKS, p.kb_total); ++r) {
+    for (int r = 2; r <= std::min(MAX_CLUSTER, p.kb_total); ++r) {
         const int own = (p.kb_total + r - 1) / r;
         if (tiles <= most.n[r] && own + 17 < least) least = own + 17, p.ranks = r, narrow = false;
         if (narrower <= most.n[r] && own + 7 < least) least = own + 7, p.ranks = r, narrow = true;
@@ -1115,7 +1089,7 @@ cudaError_t launch_wide(const eagle3_linear_fp8_args_t *a, cudaStream_t st, cons
     if (narrow) p.tiles_n = narrower_n;
     cudaLaunchConfig_t cfg = {};
     const int64_t split = (narrow ? narrower : tiles) * p.ranks;
-    cfg.gridDim = dim3((unsigned)(p.ranks > 1 ? split : std::min<int64_t>(most.n[0], tiles)));
+    cfg.gridDim = dim3((unsigned)(p.ranks > 1 ? split : std::min<int64_t>(most.n[1], tiles)));
     cfg.blockDim = dim3(WIDE_THREADS);
     cfg.dynamicSmemBytes = WIDE_SMEM;
     cfg.stream = st;

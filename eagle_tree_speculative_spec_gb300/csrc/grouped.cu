@@ -645,31 +645,13 @@ eagle3_status_t validate(const eagle3_grouped_linear_args_t *a) {
     return EAGLE3_OK;
 }
 
-constexpr int MAX_RANKS = 8;
-struct ClusterCounts {
-    int n[MAX_RANKS + 1];   // by cluster size
-};
-
 // CTAs, or clusters of `ranks`, that the device holds at once (a GPC with an odd number of SMs leaves one without
-// a partner); 0 on an error.
+// a partner); -1 on an error.
 template <bool SWIGLU, bool GATHER, int MODE>
 int resident(int ranks) {
-    if (cudaFuncSetAttribute(grouped_kernel<SWIGLU, GATHER, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) !=
-        cudaSuccess)
-        return 0;
-    if (ranks == 1) return device_sm_count();
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ranks * device_sm_count());
-    cfg.blockDim = dim3(NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0));
-    cfg.dynamicSmemBytes = SMEM;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = ranks;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    int n = 0;
-    return cudaOccupancyMaxActiveClusters(&n, grouped_kernel<SWIGLU, GATHER, MODE>, &cfg) == cudaSuccess ? n : 0;
+    const auto kernel = grouped_kernel<SWIGLU, GATHER, MODE>;
+    return ranks == 1 ? resident_ctas(kernel, SMEM)
+                      : resident_clusters(kernel, ranks, NTHREADS + (GATHER ? 32 * GATHER_WARPS : 0), SMEM);
 }
 
 template <bool SWIGLU, bool GATHER, int MODE>
@@ -698,16 +680,17 @@ cudaError_t launch_grouped(int64_t row_tiles, cudaStream_t st, const RowMaps &tx
     static PerDevice<ClusterCounts> singles, pairs, splits;
     const ClusterCounts split = splits.get([] {
         ClusterCounts c = {};
-        for (int r = 2; r <= MAX_RANKS; ++r) c.n[r] = resident<SWIGLU, GATHER, SPLIT_K>(r);
+        for (int r = 2; r <= MAX_CLUSTER; ++r) c.n[r] = resident<SWIGLU, GATHER, SPLIT_K>(r);
         return c;
     });
+    if (!succeeded(split)) return cudaErrorUnknown;   // (not "none are resident": the cut decides the order of sums)
     // Few units: as many ranks as leave every unit a resident cluster, if that saves each CTA 6 k-blocks, and one
     // more for each 16 rows of a tile: a k-block takes 0.2 us, and sending, meeting and adding up 1 us for a few
     // rows, 5 us for 256.  (2 rows, 2 groups, 1024 columns: k = 14336 45 us by single CTAs, 15 by eight ranks, k =
     // 1024 7.3 and 6.0, k = 512 5.7 and 5.8; 500 rows, 2 groups, 512 columns: k = 4096 20 and 13, k = 1024 9.2 and 11.)
     // Every rank has a k-block: without one it would send what an earlier kernel left in tensor memory.
     p.ranks = 1;
-    for (int r = 2; r <= std::min(MAX_RANKS, p.kb_total); ++r)
+    for (int r = 2; r <= std::min(MAX_CLUSTER, p.kb_total); ++r)
         if (row_tiles * p.tiles_w <= split.n[r] && p.kb_total - p.kb_total / r >= 6 + std::min(p.m, MAX_ROWS) / 16)
             p.ranks = r;
     if (p.ranks > 1)
