@@ -46,8 +46,8 @@ E3_DEV bool mbar_wait(uint64_t *bar, uint32_t parity, volatile int *abort, long 
 
 // The same by shared-memory address (computed once) and by whole warps, for loops that are short of issue
 // slots and registers: a poll is a handful of instructions, and every lane gets the same answer.  The clock and the
-// abort flag are read every 64 polls (a poll of a barrier that does not complete suspends its thread for some 7800
-// cycles, but nothing says how long it has to).  `limit` is in 1024 clocks.
+// abort flag are read every 64 polls (a poll of a barrier that does not complete was measured to suspend its thread
+// for 7800 cycles, which the instruction does not promise).  `limit` is in 1024 clocks.
 E3_DEV uint32_t kiloclock() { return (uint32_t)(clock64() >> 10); }
 E3_DEV bool mbar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;

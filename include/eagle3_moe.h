@@ -41,7 +41,8 @@ typedef enum {
  * logit that is not finite (-inf, +inf, NaN) marks an expert that the row does not take; a row with
  * fewer than top_k finite logits, and a row at or past *num_rows, leaves the remaining places empty
  * (id -1, weight 0, slot -1).  The weight of a place is its score, divided by the sum of the row's
- * chosen scores if renormalize is set (0 where that sum is 0), times scale.  fp32 throughout.
+ * chosen scores if renormalize is set (0 where that sum is 0), times scale.  fp32 throughout: the
+ * sigmoid of a logit below -88.7 is 0, so that a row of such logits alone has weights of 0.
  *
  * The taken places, sorted by expert and within an expert by row, are numbered from 0: these
  * numbers are the slots.  Slots [expert_offsets[e], expert_offsets[e + 1]) belong to expert e,
