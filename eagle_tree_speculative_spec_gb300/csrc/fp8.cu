@@ -301,17 +301,17 @@ E3_DEV void load_rows(uint8_t *box, const __nv_bfloat16 *src, int64_t ld, int ro
 }
 
 // ---- wide ---------------------------------------------------------------------------------------
-// Three warpgroups: loads and MMAs (warps 0 and 1; 2 and 3 idle), and two of the epilogue.  The block
-// is launched with 168 registers a thread (384 x 168 = 64512); the first group keeps 40 and the
-// epilogue takes 232 (128 x 40 + 256 x 232 = 64512): 128 accumulators, two loads of 16, scales.  The
-// instructions around the 128 additions of a k-block (waits that poll, addresses made anew) weigh as much as they do,
-// so barriers go by precomputed shared-memory addresses, a poll is a handful of instructions, the thread index stays
-// in a register, and the shared memory's base is an offset to its symbol, not an integer made a pointer, whose accesses would be generic (337 -> 309 us):
-// 3840 x 2 * 14336 x 4096 412 -> 309 us in a burst of a dozen calls, 319 to 347 (2830 to 2600 TFLOP/s) by box and
-// clock in longer runs; 3840 x 6144 x 4096 72 us.  (Four groups of 64 accumulators and 104 registers: 358 us.)
-// What bounds it: a tile moves 48 KB a k-block into shared memory and its MMAs read as much, 768 cycles at 128 bytes
-// a cycle for MMAs of 512 (707 k-blocks an SM: 262 us at 2070 MHz; without the additions the kernel takes 265); the
-// rest are the waits for one TMEM load at a time and their additions.  Issue slots (50%) are not full.
+// Three warpgroups: loads and MMAs (warps 0 and 1; 2 and 3 idle), and two of the epilogue.  The block is launched
+// with 168 registers a thread (384 x 168 = 64512); the first group keeps 40 and the epilogue takes 232 (128 x 40 +
+// 256 x 232 = 64512): 128 accumulators, two loads of 16, scales.  The instructions around the 128 additions of a
+// k-block (waits that poll, addresses made anew) weigh as much as they do, so barriers go by precomputed
+// shared-memory addresses, a poll is a handful of instructions, the thread index stays in a register, and the shared
+// memory's base is an offset to its symbol, not an integer made a pointer, whose accesses would be generic (337 ->
+// 309 us): 3840 x 2 * 14336 x 4096 412 -> 309 us in a burst of a dozen calls, 319 to 347 (2830 to 2600 TFLOP/s) by
+// box and clock in longer runs; 3840 x 6144 x 4096 72 us.  (Four groups of 64 accumulators and 104 registers: 358
+// us.) What bounds it: a tile moves 48 KB a k-block into shared memory and its MMAs read as much, 768 cycles at 128
+// bytes a cycle for MMAs of 512 (707 k-blocks an SM: 262 us at 2070 MHz; without the additions the kernel takes
+// 265); the rest are the waits for one TMEM load at a time and their additions.  Issue slots (50%) are not full.
 constexpr int WIDE_BN = 256, WIDE_STAGES = 4, WIDE_EPI_WARPS = 8, WIDE_THREADS = 128 + 32 * WIDE_EPI_WARPS;
 constexpr int WIDE_EPI0 = 4;   // first epilogue warp
 constexpr int SPLIT_BN = 128, SPLIT_STAGES = 6;   // OUT_SPLIT's narrower tiles
