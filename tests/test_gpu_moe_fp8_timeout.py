@@ -60,34 +60,32 @@ def _gives_up(call, hook, args, kw, stall_block, stall_rank, limit=LIMIT, least=
         assert int(st) == 0 and torch.equal(out, want)
 
 
+STALLS = [(0, -1), (2, -1), (1, 0), (1, 1)]   # (block, rank); rank 1 only where there are clusters
+SINGLE = [([1], 128, 256, False), ([300, 7], 128, 640, False)]   # one weight tile: single CTAs
+PAIRS = [([1], 128, 256, True), ([300, 7], 128, 640, True), ([300, 0, 90], 512, 640, False), ([300, 0, 90], 512, 640, True)]
+SPLIT = [([2, 3], 128, 4096, False), ([2, 3], 128, 4096, True)]   # k over a cluster
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("gather", [False, True])
-@pytest.mark.parametrize("swiglu", [False, True])
-@pytest.mark.parametrize("counts,n,k", [
-    ([1], 128, 256), ([300, 7], 128, 640),   # one weight tile: single CTAs (two tiles with SwiGLU: pairs)
-    ([300, 0, 90], 512, 640),                # pairs
-    ([2, 3], 128, 4096)])                    # k over a cluster
-@pytest.mark.parametrize("stall_block,stall_rank", [(0, -1), (2, -1), (1, 0), (1, 1)])
+@pytest.mark.parametrize("counts,n,k,swiglu,stall_block,stall_rank",
+                         [(*c, *s) for c in SINGLE for s in STALLS[:3]] + [(*c, *s) for c in PAIRS + SPLIT for s in STALLS])
 def test_grouped_waits_run_out(counts, n, k, swiglu, gather, stall_block, stall_rank):
-    dev = require_gpu()
-    if stall_rank == 1 and n == 128 and k < 4096 and not swiglu:
-        pytest.skip("no clusters")
-    args, kw = _grouped_call(dev, counts, n, k, swiglu, gather)
+    args, kw = _grouped_call(require_gpu(), counts, n, k, swiglu, gather)
     _gives_up(e3.eagle3_grouped_linear, _lib.eagle3_test_grouped_linear_timeout, args, kw, stall_block, stall_rank)
+
+
+ALONE = [(8, 128, 256, 0), (300, 512, 640, 0), (300, 512, 640, 1)]            # narrow; wide, outputs by TMA and by the warps
+CLUSTERS = [(60, 200, 4096, 0), (200, 512, 8192, 0), (1100, 1001, 6160, 0)]   # narrow; wide, tiles of 128 and 256 columns
 
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("epi", [e3.EPI_BF16, e3.EPI_F32, e3.EPI_BF16_RESIDUAL, e3.EPI_SWIGLU])
-@pytest.mark.parametrize("m,n,k,out_pitch,ranks", [
-    (8, 128, 256, 0, 1), (60, 200, 4096, 0, 2),        # narrow, alone and over a cluster
-    (300, 512, 640, 0, 1), (300, 512, 640, 1, 1),      # wide, outputs by TMA and by the warps
-    (200, 512, 8192, 0, 2), (1100, 1001, 6160, 0, 2)])  # over a cluster, tiles of 128 and 256 columns
-@pytest.mark.parametrize("stall_block,stall_rank", [(0, -1), (1, -1), (1, 0), (1, 1)])
-def test_fp8_waits_run_out(m, n, k, out_pitch, ranks, epi, stall_block, stall_rank):
-    dev = require_gpu()
-    if stall_rank >= ranks:
-        pytest.skip("no clusters")
-    args, kw = _fp8_call(dev, m, n, k, epi, out_pitch)
+@pytest.mark.parametrize("m,n,k,out_pitch,stall_block,stall_rank",
+                         [(*c, *s) for c in ALONE for s in ((0, -1), (1, -1), (1, 0))] +
+                         [(*c, *s) for c in CLUSTERS for s in STALLS])
+def test_fp8_waits_run_out(m, n, k, out_pitch, epi, stall_block, stall_rank):
+    args, kw = _fp8_call(require_gpu(), m, n, k, epi, out_pitch)
     _gives_up(e3.eagle3_linear_fp8, _lib.eagle3_test_linear_fp8_timeout, args, kw, stall_block, stall_rank)
 
 
