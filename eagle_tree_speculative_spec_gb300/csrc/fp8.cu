@@ -308,7 +308,7 @@ E3_DEV void load_rows(uint8_t *box, const __nv_bfloat16 *src, int64_t ld, int ro
 // shared-memory addresses, a poll is a handful of instructions, the thread index stays in a register, and the shared
 // memory's base is an offset to its symbol, not an integer made a pointer, whose accesses would be generic (337 ->
 // 309 us): 3840 x 2 * 14336 x 4096 412 -> 309 us in a burst of a dozen calls, 319 to 347 (2830 to 2600 TFLOP/s) by
-// box and clock in longer runs; 3840 x 6144 x 4096 72 us.  (Four groups of 64 accumulators and 104 registers: 358
+// GPU and clock in longer runs; 3840 x 6144 x 4096 72 us.  (Four groups of 64 accumulators and 104 registers: 358
 // us.) What bounds it: a tile moves 48 KB a k-block into shared memory and its MMAs read as much, 768 cycles at 128
 // bytes a cycle for MMAs of 512 (707 k-blocks an SM: 262 us at 2070 MHz; without the additions the kernel takes
 // 265); the rest are the waits for one TMEM load at a time and their additions.  Issue slots (50%) are not full.

@@ -170,7 +170,7 @@ E3_DEV void store_pair(const GroupedParams &p, int row, int col, float a, float 
 // each), with MMAs that the even CTA issues for both.  Each SM's shared memory then takes 32 KB of loads and
 // 32 KB of operand reads a k-block in place of 48 and 48, which at 128 bytes a cycle are 512 cycles, the MMAs'
 // own time, in place of 750 (3840 rows x 8 of 64 experts, k = 4096, 2 x 1024 columns: 377 -> 325 us in a
-// burst of a dozen calls; k = 1024, 4096 columns: 206 -> 179 us; in longer runs 339 to 374 by box and clock, 1520 to
+// burst of a dozen calls; k = 1024, 4096 columns: 206 -> 179 us; in longer runs 339 to 374 by GPU and clock, 1520 to
 // 1380 TFLOP/s, and 192 to 204).  The odd CTA's stages are announced to the even one by a thread that waits for them
 // and arrives on its barrier, at cluster scope; commits go to the barriers of both.
 
