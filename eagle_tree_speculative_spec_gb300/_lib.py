@@ -138,6 +138,42 @@ class LinearFp8Args(ctypes.Structure):
                 ("w2", _p), ("w2_scale", _p), ("out", _p), ("residual", _p), ("dev_status", _p)]
 
 
+ROPE_NONE, ROPE_LINEAR, ROPE_BASE, ROPE_BANDS, ROPE_RAMP = 0, 1, 2, 3, 4
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+KV_BF16, KV_E4M3 = 0, 1
+KV_GROUP = 64
+
+
+class RopeTableArgs(ctypes.Structure):
+    _fields_ = [("rotary_dim", _i32), ("scaling", _i32), ("original_positions", _i32), ("theta", ctypes.c_double),
+                ("factor", ctypes.c_double), ("low_turns", ctypes.c_double), ("high_turns", ctypes.c_double),
+                ("table", _p)]
+
+
+class RopeArgs(ctypes.Structure):
+    _fields_ = [("rows", _i32), ("n_heads", _i32), ("head_dim", _i32), ("rotary_dim", _i32), ("elem_bytes", _i32),
+                ("layout", _i32), ("inverse", _i32), ("amplitude", _f32), ("x_row_stride", _i64),
+                ("out_row_stride", _i64), ("x", _p), ("positions", _p), ("table", _p), ("out", _p)]
+
+
+class AppendKvArgs(ctypes.Structure):
+    _fields_ = [("batch", _i32), ("n_kv_heads", _i32), ("head_dim", _i32), ("format", _i32), ("n_rows", _i32),
+                ("max_new", _i32), ("rows_per_seq", _i32), ("max_blocks", _i32), ("block_size", _i32),
+                ("n_pages", _i32), ("rotary_dim", _i32), ("rope_layout", _i32), ("rope_amplitude", _f32),
+                ("row_stride", _i64), ("k_new", _p), ("v_new", _p), ("cache_len", _p), ("n_new", _p),
+                ("row_start", _p), ("row_ids", _p), ("block_table", _p), ("rope_table", _p), ("k_cache", _p),
+                ("v_cache", _p), ("k_scale", _p), ("v_scale", _p), ("dev_status", _p)]
+
+
+class VerifyAttnFp8Args(ctypes.Structure):
+    _fields_ = [("batch", _i32), ("n_nodes", _i32), ("n_heads", _i32), ("n_kv_heads", _i32), ("head_dim", _i32),
+                ("max_prefix_len", _i32), ("num_splits", _i32), ("max_blocks", _i32), ("block_size", _i32),
+                ("n_pages", _i32), ("sm_scale", _f32), ("q_node_stride", _i64), ("kv_node_stride", _i64), ("q", _p),
+                ("tree_k", _p), ("tree_v", _p), ("parents", _p), ("k_cache", _p), ("v_cache", _p), ("k_scale", _p),
+                ("v_scale", _p), ("block_table", _p), ("prefix_len", _p), ("out", _p), ("lse", _p),
+                ("dev_status", _p)]
+
+
 DRAFT_WEIGHT_NAMES = ("w_fc", "embed", "input_norm", "hidden_norm", "w_qkv", "w_o", "post_norm", "w_gate",
                       "w_up", "w_down", "final_norm", "lm_head")
 
@@ -228,6 +264,16 @@ def _declare(L):
     L.eagle3_quantize_fp8.argtypes = [P(QuantizeFp8Args), _p]
     L.eagle3_linear_fp8.restype = ctypes.c_int
     L.eagle3_linear_fp8.argtypes = [P(LinearFp8Args), _p]
+    L.eagle3_rope_table.restype = ctypes.c_int
+    L.eagle3_rope_table.argtypes = [P(RopeTableArgs), _p]
+    L.eagle3_rope.restype = ctypes.c_int
+    L.eagle3_rope.argtypes = [P(RopeArgs), _p]
+    L.eagle3_append_kv.restype = ctypes.c_int
+    L.eagle3_append_kv.argtypes = [P(AppendKvArgs), _p]
+    L.eagle3_verify_attn_fp8_workspace_size.restype = ctypes.c_size_t
+    L.eagle3_verify_attn_fp8_workspace_size.argtypes = [P(VerifyAttnFp8Args)]
+    L.eagle3_verify_attn_fp8.restype = ctypes.c_int
+    L.eagle3_verify_attn_fp8.argtypes = [P(VerifyAttnFp8Args), _p, ctypes.c_size_t, _p]
     L.eagle3_test_grouped_linear_timeout.restype = ctypes.c_int
     L.eagle3_test_grouped_linear_timeout.argtypes = [P(GroupedLinearArgs), _i32, _i32, _i64, _p]
     L.eagle3_test_linear_fp8_timeout.restype = ctypes.c_int
@@ -874,6 +920,192 @@ def eagle3_test_linear_fp8_timeout(x, x_scale, w, w_scale, out, *, stall_block, 
     _check(lib().eagle3_test_linear_fp8_timeout(ctypes.byref(a), int(stall_block), int(stall_rank),
                                                 int(wait_limit_cycles), _on(x.get_device(), stream)),
            "eagle3_test_linear_fp8_timeout")
+
+
+# ----------------------------------------------------------------------------- 8-bit paged KV cache
+def eagle3_rope_table(table, *, theta=500000.0, scaling=ROPE_NONE, factor=1.0, low_turns=1.0, high_turns=4.0,
+                      original_positions=8192, stream=None):
+    """Fill table [rotary_dim / 2] int64 with the turns of one position of every pair, as 64-bit fractions
+    (include/eagle3_kv.h); a program makes it once.  ROPE_RAMP usually takes high_turns=32."""
+    if table.dim() != 1:
+        raise ValueError("table must be [rotary_dim / 2]")
+    dev = table.get_device()
+    a = RopeTableArgs(2 * table.shape[0], int(scaling), int(original_positions), float(theta), float(factor),
+                      float(low_turns), float(high_turns), _arg(table, torch.int64, table.shape, dev, "table"))
+    _check(lib().eagle3_rope_table(ctypes.byref(a), _on(dev, stream)), "eagle3_rope_table")
+
+
+def _heads_arg(t, dtype, shape, index, name):
+    """(data pointer, row pitch) of a [rows, heads, dim] view whose heads are dense."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index:
+        _refuse(t, dtype, shape, index, name)
+    rows, heads, dim = shape
+    pitch, head, inner = t.stride()
+    if (inner != 1 and dim > 1) or (head != dim and heads > 1):
+        raise ValueError(f"{name} must have dense heads")
+    if rows <= 1:
+        return t.data_ptr(), heads * dim   # a single row's pitch means nothing
+    if pitch < heads * dim:
+        raise ValueError(f"{name} has overlapping rows")
+    return t.data_ptr(), pitch
+
+
+def rope_args(x, positions, table, out, *, layout=ROPE_HALF, inverse=False, amplitude=1.0):
+    T, H, D = x.shape
+    dev = x.get_device()
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"x must be bfloat16 or float32, got {x.dtype}")
+    if table.dim() != 1:
+        raise ValueError("table must be [rotary_dim / 2]")
+    xp, xs = _heads_arg(x, x.dtype, (T, H, D), dev, "x")
+    op, os_ = _heads_arg(out, x.dtype, (T, H, D), dev, "out")
+    return RopeArgs(T, H, D, 2 * table.shape[0], x.element_size(), int(layout), 1 if inverse else 0, float(amplitude),
+                    xs, os_, xp, _arg(positions, torch.int32, (T,), dev, "positions"),
+                    _arg(table, torch.int64, table.shape, dev, "table"), op)
+
+
+def eagle3_rope(x, positions, table, out, *, layout=ROPE_HALF, inverse=False, amplitude=1.0, stream=None):
+    """Rotary positions of rows of heads: x and out [T, H, D] bf16 or fp32 (heads dense, rows may be pitched,
+    out may be x), positions [T] int32, table [R / 2] int64 of eagle3_rope_table: the first R dims of
+    every head are turned, the others copied.  inverse: by the opposite angle (the backward pass)."""
+    a = rope_args(x, positions, table, out, layout=layout, inverse=inverse, amplitude=amplitude)
+    _check(lib().eagle3_rope(ctypes.byref(a), _on(x.get_device(), stream)), "eagle3_rope")
+
+
+def _scales_arg(t, shape, index, name):
+    if t is None:
+        raise ValueError(f"{name} is needed by an e4m3 cache")
+    return _arg(t, torch.uint8, shape, index, name)
+
+
+def append_kv_args(k_new, v_new, cache_len, n_new, block_table, k_cache, v_cache, *, max_new, block_size, k_scale=None,
+                   v_scale=None, row_start=None, row_ids=None, rows_per_seq=0, rope_table=None,
+                   rope_layout=ROPE_HALF, rope_amplitude=1.0, dev_status=None):
+    n_rows, Hkv, D = k_new.shape
+    dev, i32, bf = k_new.get_device(), torch.int32, torch.bfloat16
+    B, max_blocks = block_table.shape
+    bs = int(block_size)
+    e4m3 = k_cache.dtype is torch.float8_e4m3fn
+    if bs < 1 or (e4m3 and bs % KV_GROUP):
+        raise ValueError("block_size must be positive, a multiple of 64 for an e4m3 cache")
+    kp, rs = _heads_arg(k_new, bf, (n_rows, Hkv, D), dev, "k_new")
+    vp, vrs = _heads_arg(v_new, bf, (n_rows, Hkv, D), dev, "v_new")
+    if rs != vrs:
+        raise ValueError("k_new and v_new must share a row pitch")
+    if e4m3:
+        pages = k_cache.shape[0]
+        shape, dt = (pages, Hkv, bs, D), torch.float8_e4m3fn
+        sshape = (pages, Hkv, bs // KV_GROUP)
+        ks, vs = _scales_arg(k_scale, sshape, dev, "k_scale"), _scales_arg(v_scale, sshape, dev, "v_scale")
+    else:
+        pages = k_cache.shape[0] // bs
+        shape, dt = (pages * bs, Hkv, D), bf
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("a bf16 cache has no scales")
+        ks = vs = None
+    opt = lambda t, shape, name: None if t is None else _arg(t, i32, shape, dev, name)
+    return AppendKvArgs(B, Hkv, D, KV_E4M3 if e4m3 else KV_BF16, n_rows, int(max_new), int(rows_per_seq), max_blocks, bs,
+                        pages, 0 if rope_table is None else 2 * rope_table.shape[0], int(rope_layout),
+                        float(rope_amplitude), rs, kp, vp, _arg(cache_len, i32, (B,), dev, "cache_len"),
+                        opt(n_new, (B,), "n_new"), opt(row_start, (B,), "row_start"),
+                        opt(row_ids, (B, int(max_new)), "row_ids"),
+                        _arg(block_table, i32, (B, max_blocks), dev, "block_table"),
+                        None if rope_table is None else _arg(rope_table, torch.int64, rope_table.shape, dev, "rope_table"),
+                        _arg(k_cache, dt, shape, dev, "k_cache"), _arg(v_cache, dt, shape, dev, "v_cache"), ks, vs,
+                        _status_arg(dev_status, dev))
+
+
+def eagle3_append_kv(k_new, v_new, cache_len, n_new, block_table, k_cache, v_cache, *, max_new, block_size, k_scale=None,
+                     v_scale=None, row_start=None, row_ids=None, rows_per_seq=0, rope_table=None,
+                     rope_layout=ROPE_HALF, rope_amplitude=1.0, dev_status=None, stream=None):
+    """New tokens' keys and values into a paged cache, at positions cache_len[b] + j for j < n_new[b] <= max_new.
+    k_new / v_new [T, Hkv, D] bf16 (heads dense, rows pitched alike): token j of sequence b is row
+    row_start[b] + j, or b * max_new + j without row_start, or b * rows_per_seq + row_ids[b, j] (row_ids
+    [B, max_new]; n_new None: up to the first negative id).  rope_table: turn the keys to their positions.
+    k_cache / v_cache: float8_e4m3fn [pages, Hkv, block_size, D] with k_scale / v_scale uint8 [pages, Hkv,
+    block_size / 64], or bf16 [pages * block_size, Hkv, D].  cache_len is not advanced."""
+    a = append_kv_args(k_new, v_new, cache_len, n_new, block_table, k_cache, v_cache, max_new=max_new,
+                       block_size=block_size, k_scale=k_scale, v_scale=v_scale, row_start=row_start, row_ids=row_ids,
+                       rows_per_seq=rows_per_seq, rope_table=rope_table, rope_layout=rope_layout,
+                       rope_amplitude=rope_amplitude, dev_status=dev_status)
+    _check(lib().eagle3_append_kv(ctypes.byref(a), _on(k_new.get_device(), stream)), "eagle3_append_kv")
+
+
+def _nodes_arg(t, shape, index, name):
+    """(data pointer, node pitch) of a [B, N, heads, dim] bf16 view: heads dense, nodes of all sequences at one pitch."""
+    B, N, H, D = shape
+    if t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != index:
+        _refuse(t, torch.bfloat16, shape, index, name)
+    sb, sn, sh, sd = t.stride()
+    pitch = sn if N > 1 else sb if B > 1 else H * D
+    if sd != 1 or (sh != D and H > 1) or (B > 1 and N > 1 and sb != N * sn) or pitch < H * D:
+        raise ValueError(f"{name} must be node-strided with dense heads")
+    return t.data_ptr(), pitch
+
+
+def verify_attn_fp8_args(q, k_cache, v_cache, k_scale, v_scale, block_table, prefix_len, out, *, max_prefix_len,
+                         tree_k=None, tree_v=None, parents=None, lse=None, sm_scale=0.0, num_splits=0, dev_status=None):
+    B, N, Hq, D = q.shape
+    pages, Hkv, bs, _ = k_cache.shape
+    dev, i32, f8 = q.get_device(), torch.int32, torch.float8_e4m3fn
+    qp, qs = _nodes_arg(q, (B, N, Hq, D), dev, "q")
+    tkp = tvp = None
+    kvs = 0
+    if tree_k is not None or tree_v is not None or parents is not None:
+        if tree_k is None or tree_v is None or parents is None:
+            raise ValueError("a tree is tree_k, tree_v and parents")
+        tkp, kvs = _nodes_arg(tree_k, (B, N, Hkv, D), dev, "tree_k")
+        tvp, vvs = _nodes_arg(tree_v, (B, N, Hkv, D), dev, "tree_v")
+        if kvs != vvs:
+            raise ValueError("tree_k and tree_v must share a node pitch")
+    if bs < 1 or bs % KV_GROUP:
+        raise ValueError("pages must hold a multiple of 64 places")
+    sshape = (pages, Hkv, bs // KV_GROUP)
+    return VerifyAttnFp8Args(B, N, Hq, Hkv, D, int(max_prefix_len), int(num_splits), block_table.shape[1], bs, pages,
+                             float(sm_scale), qs, kvs, qp, tkp, tvp,
+                             None if parents is None else _arg(parents, i32, (B, N), dev, "parents"),
+                             _arg(k_cache, f8, (pages, Hkv, bs, D), dev, "k_cache"),
+                             _arg(v_cache, f8, (pages, Hkv, bs, D), dev, "v_cache"),
+                             _scales_arg(k_scale, sshape, dev, "k_scale"), _scales_arg(v_scale, sshape, dev, "v_scale"),
+                             _arg(block_table, i32, (B, block_table.shape[1]), dev, "block_table"),
+                             _arg(prefix_len, i32, (B,), dev, "prefix_len"),
+                             _arg(out, torch.bfloat16, (B, N, Hq, D), dev, "out"),
+                             None if lse is None else _arg(lse, torch.float32, (B, N, Hq), dev, "lse"),
+                             _status_arg(dev_status, dev))
+
+
+def eagle3_verify_attn_fp8_workspace_size(args):
+    return lib().eagle3_verify_attn_fp8_workspace_size(ctypes.byref(args))
+
+
+def eagle3_verify_attn_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, prefix_len, out, *, max_prefix_len,
+                           tree_k=None, tree_v=None, parents=None, lse=None, sm_scale=0.0, num_splits=0,
+                           dev_status=None, workspace=None, stream=None):
+    """Attention of q [B, N, Hq, 128] bf16 (rotated; node-strided with dense heads) over the first prefix_len[b]
+    positions of an e4m3 cache (float8_e4m3fn [pages, Hkv, block_size, 128], scales uint8 [pages, Hkv,
+    block_size / 64], block_table [B, max_blocks] int32) and, with tree_k / tree_v [B, N, Hkv, 128] bf16 and
+    parents [B, N] int32, over each node's ancestors and itself.  out [B, N, Hq, 128] bf16, lse [B, N, Hq] fp32."""
+    a = verify_attn_fp8_args(q, k_cache, v_cache, k_scale, v_scale, block_table, prefix_len, out,
+                             max_prefix_len=max_prefix_len, tree_k=tree_k, tree_v=tree_v, parents=parents, lse=lse,
+                             sm_scale=sm_scale, num_splits=num_splits, dev_status=dev_status)
+    index = q.get_device()
+    st = _on(index, stream)
+    L, ref = lib(), ctypes.byref(a)
+    if workspace is not None:
+        if workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError("the workspace must be a contiguous tensor on the other tensors' device")
+        _check(L.eagle3_verify_attn_fp8(ref, workspace.data_ptr(), workspace.numel() * workspace.element_size(), st),
+               "eagle3_verify_attn_fp8")
+        return
+    need = L.eagle3_verify_attn_fp8_workspace_size(ref)
+    if need == 0:
+        _check(L.eagle3_verify_attn_fp8(ref, None, 0, st), "eagle3_verify_attn_fp8")
+        return
+    own = torch._C._cuda_cudaCachingAllocator_raw_alloc(need, st)   # a block of the launch stream, as in eagle3_moe_route
+    try:
+        _check(L.eagle3_verify_attn_fp8(ref, own, need, st), "eagle3_verify_attn_fp8")
+    finally:
+        torch._C._cuda_cudaCachingAllocator_raw_delete(own)
 
 
 # ----------------------------------------------------------------------------- fp32 small-model blocks

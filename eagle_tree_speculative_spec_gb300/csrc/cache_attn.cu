@@ -1,0 +1,535 @@
+// eagle3_verify_attn_fp8: attention of single tokens and of tree nodes over an e4m3 paged cache with a power-of-two
+// scale for each 64 places and KV head (include/eagle3_kv.h).
+//
+// Sources: "Advanced speculative decoding: tree drafts and EAGLE", sections "Why trees" and "Implementation" (each
+// node sees the whole prefix plus itself and its ancestors); "EAGLE-3: Engineering Implementation of LLM Inference
+// Acceleration", appendix C (GQA, 1/sqrt(D) scaling).
+//
+// Rows kernel: 16 query rows (row = node * rep + head of the KV group) by the warps of a CTA, each with 32 keys of
+// its own at a time and running maxima and sums of its own, merged at the end in warp order.  Nothing is staged: a
+// lane reads 16 codes of a key row at once, and which dims of K (keys of V) a lane holds is laid out so that they are
+// the B fragments of mma.m16n8k16 after conversion to fp16, which is exact.  The dims of Q and the columns of O are
+// permuted to match.
+//   scores   lane (g, c) of a warp, g = lane / 4, c = lane % 4, reads key g of each 8, dims [16c, 16c + 16) and
+//            [64 + 16c, 64 + 16c + 16): word w of the first run is the fragment of k-step w, the k indices
+//            {2c, 2c + 1, 2c + 8, 2c + 9} being the dims 16c + 4w + {0, 1, 2, 3}
+//   values   keys {2c, 2c + 1, 2c + 8, 2c + 9} of each 16, dims [16g, 16g + 16): byte permutes pair up two keys' codes
+//            of a dim; column tile t of O holds the dims 16n + t, n = 0 .. 7
+// Q is scaled by a power of two for each row so that fp16 holds it (bf16's 8 bits fit, elements 2^-36 below the row's
+// largest vanish); the factor comes back with the scale of K's group in fp32.  Weights are held 2^7 up, so that fp16's
+// 11 bits reach down to 2^-21 of the largest, and V's group scale is put on them relative to the largest so far.
+#include "cache_attn.cuh"
+
+#include <cfloat>
+
+namespace e3 {
+namespace {
+
+constexpr int D = 128;
+constexpr int CHUNK = 32;           // keys of a warp's step: within one group of 64, so one scale and one page
+constexpr int NW = 4;               // warps
+constexpr int NT = NW * 32;
+constexpr int ROWS = 16;
+constexpr int O_PITCH = D + 4;
+
+E3_DEV uint32_t e4m3x2_f16(uint32_t two) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
+    return h;
+}
+
+E3_DEV void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 16 consecutive bf16 as fp16 pairs, times a power of two
+E3_DEV void bf16x16_f16(const __nv_bfloat16 *src, float factor, uint32_t (&out)[8]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(src + 8 * i);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[e]));
+            out[4 * i + e] = pack_f16(f.x * factor, f.y * factor);
+        }
+    }
+}
+
+// the largest finite magnitude of 8 bf16 (others: set in `odd`)
+E3_DEV float amax8(uint4 u, bool &odd) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    float m = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const uint32_t h = (e & 1 ? w[e >> 1] >> 16 : w[e >> 1]) & 0x7fffu;
+        if (h < 0x7f80u)
+            m = fmaxf(m, __uint_as_float(h << 16));
+        else
+            odd = true;
+    }
+    return m;
+}
+
+// The running state of a warp: rows g and g + 8 of its 16
+struct RowState {
+    float m[2], l[2];
+    int ev;               // V's scale byte that o is relative to
+    float o[16][4];
+};
+
+// The weights of a step of 32 keys, as A fragments, from its raw scores s (four tiles of 8 keys) by the rows' factors f;
+// seen: bit 2 n + i of a row for this lane's key 2c + i of tile n; ev: V's scale byte.
+E3_DEV void softmax_step(RowState &st, float (&s)[4][4], const float (&f)[2], const uint32_t (&seen)[2], int ev,
+                         uint32_t (&pf)[2][4]) {
+    float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int r = e >> 1;
+            s[n][e] = (seen[r] >> (2 * n + (e & 1))) & 1u ? s[n][e] * f[r] : -INFINITY;
+            mx[r] = fmaxf(mx[r], s[n][e]);
+        }
+    bool grown = ev > st.ev && ev != 255;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+        grown = grown || mx[r] > st.m[r] + RESCALE_LOG2;
+    }
+    if (__any_sync(0xffffffffu, grown)) {
+        const float down = ev > st.ev && ev != 255 ? exp2_int(st.ev - ev) : 1.0f;
+        if (ev != 255) st.ev = max(st.ev, ev);
+        float c[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const float m = fmaxf(st.m[r], mx[r]);
+            c[r] = st.m[r] == -INFINITY ? 0.0f : fast_exp2(st.m[r] - m);
+            st.m[r] = m;
+            st.l[r] *= c[r];
+            c[r] *= down;
+        }
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+            st.o[t][0] *= c[0];
+            st.o[t][1] *= c[0];
+            st.o[t][2] *= c[1];
+            st.o[t][3] *= c[1];
+        }
+    }
+    const float vs = ev == 255 ? __int_as_float(0x7fc00000) : exp2_int(ev - st.ev);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const float nm = st.m[r] == -INFINITY ? 0.0f : WEIGHT_LOG2 - st.m[r];
+        float sum = 0.0f;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const float p0 = fast_exp2(s[n][2 * r] + nm), p1 = fast_exp2(s[n][2 * r + 1] + nm);
+            sum += p0 + p1;
+            pf[n >> 1][(n & 1) * 2 + r] = pack_f16(p0 * vs, p1 * vs);
+        }
+        st.l[r] += sum;
+    }
+}
+
+// grid: (split, KV head and row group, sequence)
+__global__ void __launch_bounds__(NT, 2) cache_attn_rows_kernel(const CacheAttn p) {
+    __shared__ float so[NW][ROWS][O_PITCH];
+    __shared__ float sm[NW][ROWS], sl[NW][ROWS];
+    __shared__ int sev[NW];
+    pdl_wait();
+    pdl_trigger();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int split = blockIdx.x, groups = p.row_groups, h = blockIdx.y / groups, b = blockIdx.z;
+    const int row0 = blockIdx.y % groups * ROWS, nrows = min(ROWS, p.N * p.rep - row0);
+    const bool reports = split == 0 && blockIdx.y == 0 && threadIdx.x == 0;
+    int L = __ldg(p.prefix_len + b);
+    if (L < 0 || L > p.max_prefix) {
+        if (reports) flag(p.dev_status, EAGLE3_DEV_CAPACITY);
+        L = max(0, min(L, p.max_prefix));
+    }
+
+    // ---- Q: fragments of the two rows of this lane, each row scaled to [2^12, 2^13)
+    uint32_t qf[8][4];
+    float f[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const int row = g + 8 * r;
+        float top = 0.0f;
+        const __nv_bfloat16 *src = p.q;
+        if (row < nrows) {
+            const int node = (row0 + row) / p.rep, head = h * p.rep + (row0 + row) % p.rep;
+            src = p.q + ((size_t)b * p.N + node) * p.q_ns + (size_t)head * D + 16 * c;
+            bool odd = false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                top = fmaxf(top, amax8(*reinterpret_cast<const uint4 *>(src + 64 * (i >> 1) + 8 * (i & 1)), odd));
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int up = row_shift(top, 12);
+        f[r] = p.scale_log2 * exp2_int(-up);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (row < nrows) bf16x16_f16(src + 64 * i, exp2_int(up), w);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                qf[4 * i + k][r] = w[2 * k];
+                qf[4 * i + k][2 + r] = w[2 * k + 1];
+            }
+        }
+    }
+
+    RowState st;
+    st.m[0] = st.m[1] = -INFINITY;
+    st.l[0] = st.l[1] = 0.0f;
+    st.ev = 0;
+#pragma unroll
+    for (int t = 0; t < 16; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st.o[t][e] = 0.0f;
+
+    // ---- the prefix: chunks [c0, c1) of this split, one after the other by the warps
+    const int chunks = (L + CHUNK - 1) / CHUNK;
+    const int c0 = (int)((long long)chunks * split / p.splits), c1 = (int)((long long)chunks * (split + 1) / p.splits);
+    const int32_t *bt = p.block_table + (size_t)b * p.max_blocks;
+    const int sgroups = p.block_size / EAGLE3_KV_GROUP;
+    for (int ch = c0 + warp; ch < c1; ch += NW) {
+        const int key0 = ch * CHUNK;
+        const int page = __ldg(bt + key0 / p.block_size), place = key0 % p.block_size;
+        const bool there = page >= 0 && page < p.n_pages;
+        const size_t head_page = (size_t)(there ? page : 0) * p.Hkv + h;
+        const uint8_t *kp = p.kc + (head_page * p.block_size + place) * D;
+        const uint8_t *vp = p.vc + (head_page * p.block_size + place) * D;
+        const int left = L - key0;   // keys of this chunk that are there
+        const size_t sg = head_page * sgroups + place / EAGLE3_KV_GROUP;
+        const int ek = there ? __ldg(p.ks + sg) : 1, ev = there ? __ldg(p.vs + sg) : 1;
+        uint4 kw[4][2], vw[2][4];
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                kw[n][i] = there && 8 * n + g < left
+                               ? *reinterpret_cast<const uint4 *>(kp + (8 * n + g) * D + 64 * i + 16 * c) : zero;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int key = 16 * k + 2 * c + (e & 1) + (e >> 1) * 8;
+                vw[k][e] = there && key < left ? *reinterpret_cast<const uint4 *>(vp + key * D + 16 * g) : zero;
+            }
+        float s[4][4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint4 u = kw[n][k >> 2];
+                const uint32_t w = (k & 3) == 0 ? u.x : (k & 3) == 1 ? u.y : (k & 3) == 2 ? u.z : u.w;
+                mma_f16(s[n], qf[k][0], qf[k][1], qf[k][2], qf[k][3], e4m3x2_f16(w), e4m3x2_f16(w >> 16));
+            }
+        }
+        uint32_t seen[2] = {0xffu, 0xffu};
+        if (left < CHUNK) {
+            seen[0] = 0;
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) seen[0] |= (8 * n + 2 * c + i < left ? 1u : 0u) << (2 * n + i);
+            seen[1] = seen[0];
+        }
+        const float ks = scale_of(ek);
+        const float fs[2] = {f[0] * ks, f[1] * ks};
+        uint32_t pf[2][4];
+        softmax_step(st, s, fs, seen, ev, pf);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                auto word = [&](const uint4 &u) { return w == 0 ? u.x : w == 1 ? u.y : w == 2 ? u.z : u.w; };
+                const uint32_t r0 = word(vw[k][0]), r1 = word(vw[k][1]), r2 = word(vw[k][2]), r3 = word(vw[k][3]);
+                const uint32_t lo0 = __byte_perm(r0, r1, 0x5140), hi0 = __byte_perm(r0, r1, 0x7362);
+                const uint32_t lo1 = __byte_perm(r2, r3, 0x5140), hi1 = __byte_perm(r2, r3, 0x7362);
+                mma_f16(st.o[4 * w], pf[k][0], pf[k][1], pf[k][2], pf[k][3], e4m3x2_f16(lo0), e4m3x2_f16(lo1));
+                mma_f16(st.o[4 * w + 1], pf[k][0], pf[k][1], pf[k][2], pf[k][3], e4m3x2_f16(lo0 >> 16), e4m3x2_f16(lo1 >> 16));
+                mma_f16(st.o[4 * w + 2], pf[k][0], pf[k][1], pf[k][2], pf[k][3], e4m3x2_f16(hi0), e4m3x2_f16(hi1));
+                mma_f16(st.o[4 * w + 3], pf[k][0], pf[k][1], pf[k][2], pf[k][3], e4m3x2_f16(hi0 >> 16), e4m3x2_f16(hi1 >> 16));
+            }
+    }
+
+    // ---- the tree: its nodes as one or two more chunks of the last split
+    if (p.tree_k && split == p.splits - 1) {
+        const int32_t *par = p.parents + (size_t)b * p.N;
+        for (int ch = warp; ch * CHUNK < p.N; ch += NW) {
+            const int key0 = ch * CHUNK;
+            // bf16 rows as fp16, K and V each by a power of two of the chunk's largest
+            const __nv_bfloat16 *tk = p.tree_k + (size_t)b * p.N * p.kv_ns + (size_t)h * D;
+            const __nv_bfloat16 *tv = p.tree_v + (size_t)b * p.N * p.kv_ns + (size_t)h * D;
+            float km = 0.0f, vm = 0.0f;
+            bool odd_k = false, odd_v = false;   // V is not finite somewhere: see below
+            for (int i = lane; i < CHUNK * (D / 8); i += 32) {
+                const int key = key0 + i / (D / 8), d0 = i % (D / 8) * 8;
+                if (key >= p.N) break;
+                km = fmaxf(km, amax8(*reinterpret_cast<const uint4 *>(tk + key * p.kv_ns + d0), odd_k));
+                vm = fmaxf(vm, amax8(*reinterpret_cast<const uint4 *>(tv + key * p.kv_ns + d0), odd_v));
+            }
+#pragma unroll
+            for (int x = 16; x; x >>= 1) {
+                km = fmaxf(km, __shfl_xor_sync(0xffffffffu, km, x));
+                vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, x));
+            }
+            const int kup = row_shift(km, 8), vup = row_shift(vm, 8);   // to [2^8, 2^9), as the codes
+            float s[4][4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+                const int key = key0 + 8 * n + g;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                    if (key < p.N) bf16x16_f16(tk + key * p.kv_ns + 64 * i + 16 * c, exp2_int(kup), w);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_f16(s[n], qf[4 * i + k][0], qf[4 * i + k][1], qf[4 * i + k][2], qf[4 * i + k][3], w[2 * k],
+                                w[2 * k + 1]);
+                }
+            }
+            uint32_t seen[2] = {0, 0};
+            uint64_t anc[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int row = g + 8 * r;
+                bool bad = false;
+                anc[r] = row < nrows ? path_bits(par, (row0 + row) / p.rep, bad) : 0ull;
+                if (bad && h == 0) flag(p.dev_status, EAGLE3_DEV_BAD_TREE);
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        seen[r] |= (uint32_t)((anc[r] >> (key0 + 8 * n + 2 * c + i)) & 1ull) << (2 * n + i);
+            }
+            const float fs[2] = {f[0] * exp2_int(-kup), f[1] * exp2_int(-kup)};
+            uint32_t pf[2][4];
+            softmax_step(st, s, fs, seen, max(0, min(254, 127 - vup)), pf);
+            const float vf = exp2_int(vup);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t v[4][4];   // [key][8 dims as bf16 pairs]
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int key = key0 + 16 * k + 2 * c + (e & 1) + (e >> 1) * 8;
+                        const uint4 u = key < p.N ? *reinterpret_cast<const uint4 *>(tv + key * p.kv_ns + 16 * g + 8 * half)
+                                                  : make_uint4(0, 0, 0, 0);
+                        v[e][0] = u.x, v[e][1] = u.y, v[e][2] = u.z, v[e][3] = u.w;
+                    }
+#pragma unroll
+                    for (int d = 0; d < 8; ++d) {
+                        auto at = [&](int e) {
+                            const uint32_t w = v[e][d >> 1];
+                            const float x = __uint_as_float(d & 1 ? w & 0xffff0000u : w << 16);
+                            return fabsf(x) <= FLT_MAX ? x * vf : 0.0f;
+                        };
+                        mma_f16(st.o[8 * half + d], pf[k][0], pf[k][1], pf[k][2], pf[k][3], pack_f16(at(0), at(1)),
+                                pack_f16(at(2), at(3)));
+                    }
+                }
+            // infinities and NaN of V, which a weight of 0 would have spread over every row: to the rows that see them
+            if (__any_sync(0xffffffffu, odd_v)) {
+                for (int key = key0; key < min(p.N, key0 + CHUNK); ++key)
+#pragma unroll
+                    for (int t = 0; t < 16; ++t)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float x = (float)tv[key * p.kv_ns + 32 * c + 16 * (e & 1) + t];
+                            if (!(fabsf(x) <= FLT_MAX) && (anc[e >> 1] >> key & 1ull)) st.o[t][e] += x;
+                        }
+            }
+        }
+    }
+
+    // ---- the warps' results, in warp order
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        float l = st.l[r];
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
+        if (c == 0) {
+            sm[warp][g + 8 * r] = st.m[r];
+            sl[warp][g + 8 * r] = l;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int t = 0; t < 16; t += 4)
+                *reinterpret_cast<float4 *>(&so[warp][g + 8 * r][32 * c + 16 * i + t]) =
+                    make_float4(st.o[t][2 * r + i], st.o[t + 1][2 * r + i], st.o[t + 2][2 * r + i], st.o[t + 3][2 * r + i]);
+    }
+    if (lane == 0) sev[warp] = st.ev;
+    __syncthreads();
+    for (int row = warp; row < nrows; row += NW) {
+        float M = -INFINITY, l = 0.0f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) M = fmaxf(M, sm[w][row]);
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            const float m = sm[w][row];
+            // (a warp whose scores are all NaN has no maximum but a sum)
+            const float e = m == -INFINITY ? (sl[w][row] == 0.0f ? 0.0f : 1.0f) : fast_exp2(m - M);
+            l += e * sl[w][row];
+            const float vs = e * scale_of(sev[w]);
+            const float4 x = *reinterpret_cast<const float4 *>(&so[w][row][4 * lane]);
+            if (e != 0.0f) o = make_float4(o.x + vs * x.x, o.y + vs * x.y, o.z + vs * x.z, o.w + vs * x.w);
+        }
+        const int node = (row0 + row) / p.rep, head = h * p.rep + (row0 + row) % p.rep;
+        const size_t at = ((size_t)b * p.N + node) * p.Hq + head;
+        if (p.splits == 1) {
+            store_row(p, at, lane, M, l, o);
+        } else {
+            const size_t part = (size_t)split * p.B * p.N * p.Hq + at;
+            if (l != 0.0f) *reinterpret_cast<float4 *>(p.part_o + part * D + 4 * lane) = o;   // (NaN too)
+            if (lane == 0) *reinterpret_cast<float2 *>(p.part_ml + 2 * part) = make_float2(M, l);
+        }
+    }
+}
+
+// The splits' results in split order: one warp a row.
+__global__ void __launch_bounds__(128) cache_attn_merge_kernel(const CacheAttn p) {
+    pdl_wait();
+    pdl_trigger();
+    const long long rows = (long long)p.B * p.N * p.Hq;
+    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (row >= rows) return;
+    float M = -INFINITY, l = 0.0f;
+    for (int s = 0; s < p.splits; ++s) M = fmaxf(M, p.part_ml[2 * (s * rows + row)]);
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int s = 0; s < p.splits; ++s) {
+        const float2 ml = *reinterpret_cast<const float2 *>(p.part_ml + 2 * (s * rows + row));
+        if (ml.y == 0.0f) continue;
+        const float e = ml.x == -INFINITY ? 1.0f : fast_exp2(ml.x - M);
+        const float4 x = *reinterpret_cast<const float4 *>(p.part_o + (s * rows + row) * D + 4 * lane);
+        l += e * ml.y;
+        o = make_float4(o.x + e * x.x, o.y + e * x.y, o.z + e * x.z, o.w + e * x.w);
+    }
+    store_row(p, (size_t)row, lane, M, l, o);
+}
+
+// parts of the prefix: enough CTAs for the GPU, none with fewer than 8 chunks a warp
+int plan_splits(const CacheAttn &p, int requested) {
+    const int chunks = (p.max_prefix + CHUNK - 1) / CHUNK;
+    if (requested > 0) return requested < chunks ? requested : chunks > 0 ? chunks : 1;
+    const int64_t units = (int64_t)p.B * p.Hkv * p.row_groups;
+    const int64_t want = (8 * (int64_t)device_sm_count() + units - 1) / units;
+    const int64_t most = chunks / (8 * NW);
+    const int64_t s = want < most ? want : most;
+    return s < 1 ? 1 : s > 512 ? 512 : (int)s;
+}
+
+bool valid(const eagle3_verify_attn_fp8_args_t *a, eagle3_status_t *why) {
+    *why = EAGLE3_ERR_INVALID_ARGUMENT;
+    if (!a || a->batch < 0 || a->n_nodes < 1 || a->n_heads < 1 || a->n_kv_heads < 1 || a->head_dim < 1 ||
+        a->max_prefix_len < 0 || a->num_splits < 0 || a->max_blocks < 1 || a->block_size < 1 ||
+        a->block_size % EAGLE3_KV_GROUP || a->n_pages < 1 || a->q_node_stride < 0 || a->kv_node_stride < 0 ||
+        !(a->sm_scale >= 0.0f && a->sm_scale <= FLT_MAX) || a->n_heads % a->n_kv_heads)
+        return false;
+    if (!a->tree_k != !a->tree_v || !a->tree_k != !a->parents) return false;
+    if ((a->q_node_stride && (a->q_node_stride < (int64_t)a->n_heads * D || a->q_node_stride % 8)) ||
+        (a->kv_node_stride && (a->kv_node_stride < (int64_t)a->n_kv_heads * D || a->kv_node_stride % 8)))
+        return false;
+    *why = EAGLE3_ERR_UNSUPPORTED;
+    if (a->head_dim != D || a->n_nodes > 64 || a->batch > 65535 || a->n_heads > 4096 || a->max_prefix_len > MAX_DIM ||
+        (int64_t)a->n_pages * a->n_kv_heads * a->block_size > MAX_DIM ||
+        (int64_t)a->batch * a->n_nodes * a->n_heads > MAX_DIM)
+        return false;
+    *why = EAGLE3_ERR_CAPACITY;
+    if ((int64_t)a->max_blocks * a->block_size < a->max_prefix_len) return false;
+    *why = EAGLE3_OK;
+    if (a->batch == 0) return true;
+    *why = EAGLE3_ERR_INVALID_ARGUMENT;
+    const void *wide[] = {a->q, a->k_cache, a->v_cache, a->out};
+    for (const void *ptr : wide)
+        if (!ptr || ((uintptr_t)ptr & 15)) return false;
+    if (!a->k_scale || !a->v_scale || !a->block_table || !a->prefix_len ||
+        (((uintptr_t)a->tree_k | (uintptr_t)a->tree_v) & 15) ||
+        (((uintptr_t)a->block_table | (uintptr_t)a->prefix_len | (uintptr_t)a->parents | (uintptr_t)a->lse) & 3))
+        return false;
+    *why = EAGLE3_OK;
+    return true;
+}
+
+CacheAttn plan(const eagle3_verify_attn_fp8_args_t *a) {
+    CacheAttn p = {};
+    p.B = a->batch;
+    p.N = a->n_nodes;
+    p.Hq = a->n_heads;
+    p.Hkv = a->n_kv_heads;
+    p.rep = a->n_heads / a->n_kv_heads;
+    p.max_prefix = a->max_prefix_len;
+    p.max_blocks = a->max_blocks;
+    p.block_size = a->block_size;
+    p.n_pages = a->n_pages;
+    p.scale_log2 = (a->sm_scale > 0.0f ? a->sm_scale : 1.0f / sqrtf((float)D)) * 1.4426950408889634f;
+    p.q_ns = a->q_node_stride ? a->q_node_stride : (int64_t)a->n_heads * D;
+    p.kv_ns = a->kv_node_stride ? a->kv_node_stride : (int64_t)a->n_kv_heads * D;
+    p.q = (const __nv_bfloat16 *)a->q;
+    p.tree_k = (const __nv_bfloat16 *)a->tree_k;
+    p.tree_v = (const __nv_bfloat16 *)a->tree_v;
+    p.parents = a->parents;
+    p.kc = a->k_cache;
+    p.vc = a->v_cache;
+    p.ks = a->k_scale;
+    p.vs = a->v_scale;
+    p.block_table = a->block_table;
+    p.prefix_len = a->prefix_len;
+    p.out = (__nv_bfloat16 *)a->out;
+    p.lse = a->lse;
+    p.dev_status = a->dev_status;
+    p.row_groups = (p.N * p.rep + ROWS - 1) / ROWS;
+    p.splits = plan_splits(p, a->num_splits);
+    return p;
+}
+
+size_t workspace_of(const CacheAttn &p) {
+    return p.splits > 1 ? (size_t)p.splits * p.B * p.N * p.Hq * (D + 2) * sizeof(float) + 256 : 0;
+}
+
+}  // namespace
+}  // namespace e3
+
+using namespace e3;
+
+extern "C" size_t eagle3_verify_attn_fp8_workspace_size(const eagle3_verify_attn_fp8_args_t *a) {
+    eagle3_status_t why;
+    if (!valid(a, &why) || a->batch == 0) return 0;
+    return workspace_of(plan(a));
+}
+
+extern "C" eagle3_status_t eagle3_verify_attn_fp8(const eagle3_verify_attn_fp8_args_t *a, void *workspace,
+                                                  size_t workspace_bytes, eagle3_stream_t stream) {
+    eagle3_status_t why;
+    if (!valid(a, &why) || a->batch == 0) return why;
+    CacheAttn p = plan(a);
+    if (p.splits > 1) {
+        if (!workspace || workspace_bytes < workspace_of(p)) return EAGLE3_ERR_WORKSPACE;
+        p.part_o = (float *)(((uintptr_t)workspace + 255) & ~(uintptr_t)255);
+        p.part_ml = p.part_o + (size_t)p.splits * p.B * p.N * p.Hq * D;
+    }
+    const cudaStream_t st = (cudaStream_t)stream;
+    const dim3 grid((unsigned)p.splits, (unsigned)(p.Hkv * p.row_groups), (unsigned)p.B);
+    if (launch_pdl(cache_attn_rows_kernel, grid, dim3(NT), 0, st, p) != cudaSuccess) return EAGLE3_ERR_CUDA;
+    if (p.splits > 1) {
+        const long long rows = (long long)p.B * p.N * p.Hq;
+        if (launch_pdl(cache_attn_merge_kernel, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, p) != cudaSuccess)
+            return EAGLE3_ERR_CUDA;
+    }
+    return EAGLE3_OK;
+}

@@ -1,0 +1,85 @@
+// What the kernels of eagle3_verify_attn_fp8 share.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "eagle3_kv.h"
+
+namespace e3 {
+
+struct CacheAttn {
+    int B, N, Hq, Hkv, rep, max_prefix, splits, row_groups;
+    int max_blocks, block_size, n_pages;
+    float scale_log2;               // sm_scale * log2(e)
+    int64_t q_ns, kv_ns;
+    const __nv_bfloat16 *q, *tree_k, *tree_v;
+    const int32_t *parents;
+    const uint8_t *kc, *vc, *ks, *vs;
+    const int32_t *block_table, *prefix_len;
+    __nv_bfloat16 *out;
+    float *lse;
+    int32_t *dev_status;
+    // results of the splits: [split][B][N][Hq], o (unnormalised, times V's scale) where l is not 0
+    float *part_o, *part_ml;
+};
+
+constexpr float RESCALE_LOG2 = 8.0f;   // the running maximum moves once a score is this far above it
+constexpr float WEIGHT_LOG2 = 7.0f;    // weights are held times 2^7: at most 2^15 in fp16
+
+// 2^x on the special-function unit (flushes subnormal results to zero)
+E3_DEV float fast_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 2^n, 0 below 2^-126 (n at most 127)
+E3_DEV float exp2_int(int n) { return n < -126 ? 0.0f : __int_as_float((n + 127) << 23); }
+
+// what a scale byte stands for
+E3_DEV float scale_of(int byte) {
+    return __int_as_float(byte == 255 ? 0x7fc00000 : byte == 0 ? 0x400000 : byte << 23);
+}
+
+// the power of two that brings a row's largest magnitude to [2^to, 2^(to + 1)); 0 of a row that is all zero or not
+// finite, and never so far that 2^-n or 2^n is not a normal number
+E3_DEV int row_shift(float amax, int to) {
+    const int e = (int)(__float_as_uint(amax) >> 23);
+    return e == 0 || e == 255 ? 0 : max(-126, min(126, to + 127 - e));
+}
+
+E3_DEV uint32_t pack_f16(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// The nodes that node i sees: itself and its ancestors, up to the root or to a parent that is none
+E3_DEV uint64_t path_bits(const int32_t *par, int i, bool &bad) {
+    uint64_t bits = 1ull << i;
+    for (;;) {
+        const int q = __ldg(par + i);
+        if (i == 0) {
+            if (q != -1) bad = true;
+            return bits;
+        }
+        if (q < 0 || q >= i) {
+            bad = true;
+            return bits;
+        }
+        i = q;
+        bits |= 1ull << i;
+    }
+}
+
+// A finished row: dims [4 lane, 4 lane + 4) of o by each lane of a warp
+E3_DEV void store_row(const CacheAttn &p, size_t row, int lane, float m, float l, float4 o) {
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    __nv_bfloat162 w[2] = {__floats2bfloat162_rn(o.x * inv, o.y * inv), __floats2bfloat162_rn(o.z * inv, o.w * inv)};
+    *reinterpret_cast<uint2 *>(p.out + row * 128 + 4 * lane) = *reinterpret_cast<const uint2 *>(w);
+    // (the weights are 2^WEIGHT_LOG2 up)
+    if (p.lse && lane == 0)
+        p.lse[row] = l == 0.0f ? -INFINITY : (m == -INFINITY ? l : ((m - WEIGHT_LOG2) + log2f(l)) * 0.6931471805599453f);
+}
+
+}  // namespace e3
