@@ -9,6 +9,7 @@
 // in registers between the two passes over them (largest magnitude, codes), so that everything is read and written
 // once.  Prompts: a CTA of 256 threads takes the jobs of a group, one after the other, with the group's cosines and
 // sines in shared memory.  Few tokens a sequence (at most 8): a warp takes a job.
+#include "e4m3.cuh"
 #include "rope.cuh"
 
 #include <cfloat>
@@ -140,26 +141,6 @@ E3_DEV void turn8(const Params &p, const __nv_bfloat16 *row, int d0, const float
         const float o = (float)row[upper ? j : d + p.half];
         v[i] = upper ? v[i] * w.x + o * w.y : v[i] * w.x - o * w.y;
     }
-}
-
-// 2^(127 - s) of a scale byte, NaN of 255
-E3_DEV float inverse_scale(int s) { return s == 255 ? __int_as_float(0x7fc00000) : __int_as_float((254 - s) << 23); }
-
-// the least byte s >= 1 with m <= 448 * 2^(s - 127) of a finite m >= 0 (448 = 1.75 * 2^8)
-E3_DEV int scale_byte(float m) {
-    const uint32_t u = __float_as_uint(m);
-    return max(1, (int)(u >> 23) - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0));
-}
-
-E3_DEV uint32_t to_e4m3x2(float lo, float hi) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-E3_DEV float2 from_e4m3x2(uint32_t two) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
-    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
 // 8 codes of another scale: by 2^-down, rounded again

@@ -32,12 +32,6 @@ constexpr int NT = NW * 32;
 constexpr int ROWS = 16;
 constexpr int O_PITCH = D + 4;
 
-E3_DEV uint32_t e4m3x2_f16(uint32_t two) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
-    return h;
-}
-
 E3_DEV void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};\n"
@@ -57,21 +51,6 @@ E3_DEV void bf16x16_f16(const __nv_bfloat16 *src, float factor, uint32_t (&out)[
             out[4 * i + e] = pack_f16(f.x * factor, f.y * factor);
         }
     }
-}
-
-// the largest finite magnitude of 8 bf16 (others: set in `odd`)
-E3_DEV float amax8(uint4 u, bool &odd) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    float m = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const uint32_t h = (e & 1 ? w[e >> 1] >> 16 : w[e >> 1]) & 0x7fffu;
-        if (h < 0x7f80u)
-            m = fmaxf(m, __uint_as_float(h << 16));
-        else
-            odd = true;
-    }
-    return m;
 }
 
 // The running state of a warp: rows g and g + 8 of its 16
@@ -498,6 +477,8 @@ CacheAttn plan(const eagle3_verify_attn_fp8_args_t *a) {
     return p;
 }
 
+bool is_wide(const CacheAttn &p) { return p.N * p.rep > ROWS; }
+
 size_t workspace_of(const CacheAttn &p) {
     return p.splits > 1 ? (size_t)p.splits * p.B * p.N * p.Hq * (D + 2) * sizeof(float) + 256 : 0;
 }
@@ -510,7 +491,8 @@ using namespace e3;
 extern "C" size_t eagle3_verify_attn_fp8_workspace_size(const eagle3_verify_attn_fp8_args_t *a) {
     eagle3_status_t why;
     if (!valid(a, &why) || a->batch == 0) return 0;
-    return workspace_of(plan(a));
+    const CacheAttn p = plan(a);
+    return is_wide(p) ? cache_attn_wide_workspace(p, a->num_splits) : workspace_of(p);
 }
 
 extern "C" eagle3_status_t eagle3_verify_attn_fp8(const eagle3_verify_attn_fp8_args_t *a, void *workspace,
@@ -518,6 +500,7 @@ extern "C" eagle3_status_t eagle3_verify_attn_fp8(const eagle3_verify_attn_fp8_a
     eagle3_status_t why;
     if (!valid(a, &why) || a->batch == 0) return why;
     CacheAttn p = plan(a);
+    if (is_wide(p)) return cache_attn_wide(p, a->num_splits, WaitRule(), workspace, workspace_bytes, (cudaStream_t)stream);
     if (p.splits > 1) {
         if (!workspace || workspace_bytes < workspace_of(p)) return EAGLE3_ERR_WORKSPACE;
         p.part_o = (float *)(((uintptr_t)workspace + 255) & ~(uintptr_t)255);

@@ -1,9 +1,9 @@
 // What the kernels of eagle3_verify_attn_fp8 share.
 #pragma once
 
-#include <cuda_fp16.h>
+#include <cfloat>
 
-#include "common.cuh"
+#include "e4m3.cuh"
 #include "eagle3_kv.h"
 
 namespace e3 {
@@ -37,11 +37,6 @@ E3_DEV float fast_exp2(float x) {
 // 2^n, 0 below 2^-126 (n at most 127)
 E3_DEV float exp2_int(int n) { return n < -126 ? 0.0f : __int_as_float((n + 127) << 23); }
 
-// what a scale byte stands for
-E3_DEV float scale_of(int byte) {
-    return __int_as_float(byte == 255 ? 0x7fc00000 : byte == 0 ? 0x400000 : byte << 23);
-}
-
 // the power of two that brings a row's largest magnitude to [2^to, 2^(to + 1)); 0 of a row that is all zero or not
 // finite, and never so far that 2^-n or 2^n is not a normal number
 E3_DEV int row_shift(float amax, int to) {
@@ -52,6 +47,21 @@ E3_DEV int row_shift(float amax, int to) {
 E3_DEV uint32_t pack_f16(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// the largest finite magnitude of 8 bf16 (others: set in `odd`)
+E3_DEV float amax8(uint4 u, bool &odd) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    float m = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const uint32_t h = (e & 1 ? w[e >> 1] >> 16 : w[e >> 1]) & 0x7fffu;
+        if (h < 0x7f80u)
+            m = fmaxf(m, __uint_as_float(h << 16));
+        else
+            odd = true;
+    }
+    return m;
 }
 
 // The nodes that node i sees: itself and its ancestors, up to the root or to a parent that is none
@@ -72,14 +82,21 @@ E3_DEV uint64_t path_bits(const int32_t *par, int i, bool &bad) {
     }
 }
 
+E3_DEV float lse_of(float m, float l) {   // (the weights are 2^WEIGHT_LOG2 up)
+    return l == 0.0f ? -INFINITY : m == -INFINITY ? l : ((m - WEIGHT_LOG2) + log2f(l)) * 0.6931471805599453f;
+}
+
 // A finished row: dims [4 lane, 4 lane + 4) of o by each lane of a warp
 E3_DEV void store_row(const CacheAttn &p, size_t row, int lane, float m, float l, float4 o) {
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     __nv_bfloat162 w[2] = {__floats2bfloat162_rn(o.x * inv, o.y * inv), __floats2bfloat162_rn(o.z * inv, o.w * inv)};
     *reinterpret_cast<uint2 *>(p.out + row * 128 + 4 * lane) = *reinterpret_cast<const uint2 *>(w);
-    // (the weights are 2^WEIGHT_LOG2 up)
-    if (p.lse && lane == 0)
-        p.lse[row] = l == 0.0f ? -INFINITY : (m == -INFINITY ? l : ((m - WEIGHT_LOG2) + log2f(l)) * 0.6931471805599453f);
+    if (p.lse && lane == 0) p.lse[row] = lse_of(m, l);
 }
+
+// many rows (cache_attn_wide.cu); requested: parts of the prefix, 0 = its own choice
+size_t cache_attn_wide_workspace(const CacheAttn &a, int requested);
+eagle3_status_t cache_attn_wide(const CacheAttn &a, int requested, const WaitRule &wait, void *workspace, size_t bytes,
+                                cudaStream_t stream);
 
 }  // namespace e3

@@ -6,9 +6,11 @@ Rotations.  The angle is exact to 2^-33 turns and rounded to fp32 as a fraction 
 below ANGLE = 7 u for each of the two terms, and 3 roundings of the products and the sum: an element is off by at most
 amplitude (|a| + |b|) 10 u, and half a step of the type it is stored in (2^-8 of a bf16 value, 2^-4 of an e4m3 one or 2^-10 of its
 scale's unit).  Positions beyond 2^20 add the table's own 2^-53 of a turn each.
-Attention.  A score: its products are exact, but for queries in two 8-bit parts, off by 2^-18 of the row's largest; 128 additions, each off
+Attention.  A score: its products are exact, but for queries (and tree keys) in two 8-bit parts: the row is scaled so
+that its largest magnitude is above 224, and what is below 2^-2 there is rounded to steps of 2^-9, so off by at most 2^-10,
+2^-17 of the row's largest (of the tree's largest key element); 128 additions, each off
 by at most one step (2 u) of the sum of magnitudes S, and 6 roundings of scales and the maximum's subtraction: (256 + 6) u S
-in natural units, and the 2^x unit is within 2^-22: a weight is off by w = (262 u S + 2^-18 Qmax |k|_1 scale + 2^-21) of
+in natural units, and the 2^x unit is within 2^-22: a weight is off by w = (262 u S + 2^-17 (Qmax |k|_1 + Kmax |q|_1) scale + 2^-21) of
 itself, and by 2^-11 where it is rounded to fp16 for V (2^-31 of the largest weight below fp16's normal range, n 2^-31 in all).
 With M the weighted mean magnitude of V, an output is off by (2 w + 2^-11 + (n + 64) 2 u) M + n 2^-31 max|V| before
 bf16's half step; the logarithm by w + (n + 64) 2 u + 8 u |lse|.
@@ -435,7 +437,8 @@ def _expected(pool, lens, q, tk, tv, par, sm_scale=0.0):
         ks = [np.abs(k).sum(2).max() if n else 0.0, np.abs(t[0]).sum(2).max() if tk is not None else 0.0]
         vs = [np.abs(v).max() if n else 0.0, np.abs(t[1]).max() if tk is not None else 0.0]
         keys = n + (q.shape[1] if tk is not None else 0)
-        w = 262 * U * dot + 2.0 ** -18 * np.abs(qb).max(2) * max(ks) * (sm_scale or 128 ** -0.5) + 2.0 ** -21
+        parts = np.abs(qb).max(2) * max(ks) + (np.abs(t[0]).max() * np.abs(qb).sum(2) if tk is not None else 0.0)
+        w = 262 * U * dot + 2.0 ** -17 * parts * (sm_scale or 128 ** -0.5) + 2.0 ** -21
         acc = (keys + 64) * 2 * U
         tol = (2 * w + 2.0 ** -11 + acc)[..., None] * mag + keys * 2.0 ** -31 * max(vs)
         tol = tol + BF16 * (np.abs(out) + tol)
