@@ -49,20 +49,38 @@ E3_DEV uint32_t pack_f16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// the largest finite magnitude of 8 bf16 (others: set in `odd`)
-E3_DEV float amax8(uint4 u, bool &odd) {
+E3_DEV uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// the largest magnitude of 8 bf16 as its 15 bits, which are in order (BF16_INF and up: not finite), and of the finite ones
+constexpr uint32_t BF16_INF = 0x7f80u;
+E3_DEV uint32_t amax_bits(uint4 u) {
+    const uint32_t m = max_u16x2(max_u16x2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu), max_u16x2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
+    return max(m & 0xffffu, m >> 16);
+}
+E3_DEV uint32_t amax_bits_finite(uint4 u) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    float m = 0.0f;
+    uint32_t m = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const uint32_t h = (e & 1 ? w[e >> 1] >> 16 : w[e >> 1]) & 0x7fffu;
-        if (h < 0x7f80u)
-            m = fmaxf(m, __uint_as_float(h << 16));
-        else
-            odd = true;
+        m = max(m, h < BF16_INF ? h : 0u);
     }
     return m;
 }
+// the largest finite magnitude of 8 bf16 (others: set in `odd`)
+E3_DEV float amax8(uint4 u, bool &odd) {
+    uint32_t m = amax_bits(u);
+    if (m >= BF16_INF) {
+        odd = true;
+        m = amax_bits_finite(u);
+    }
+    return __uint_as_float(m << 16);
+}
+// scale_byte of a finite bf16 magnitude's bits
+E3_DEV int scale_byte_bits(uint32_t m) { return max(1, (int)(m >> 7) - 8 + ((m & 0x7fu) > 0x60u ? 1 : 0)); }
 
 // The nodes that node i sees: itself and its ancestors, up to the root or to a parent that is none
 E3_DEV uint64_t path_bits(const int32_t *par, int i, bool &bad) {

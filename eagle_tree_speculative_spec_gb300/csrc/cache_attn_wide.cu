@@ -8,16 +8,17 @@
 // S = Q K^T takes K's codes as they lie in memory: Q is held as two e4m3 parts (row scaled to at most 448; hi = e4m3(q),
 // lo = e4m3(q - hi): 4 + 4 bits are bf16's 8), so that QK runs as two e4m3 products, in the time of one of bf16, and K is
 // never converted.  P V runs in fp16: weights in 11 bits (8 bits of bf16, or two e4m3 parts whose floor is 2^-18 of the
-// largest weight, would cost long sums), V's codes converted exactly, times the power of two by which their group's scale
-// differs from the range's largest.
+// largest weight, would cost long sums) and V's codes, converted exactly; the scale of V's group is put on the weights,
+// relative to the largest so far, by adding to the exponent.
 //
 // Two streams of (S, P, O) in tensor memory keep the tensor cores busy while the other's softmax runs: with more than
 // 128 rows a stream is a row tile and both take every key tile; with up to 128 the streams take alternate key tiles of
 // the same rows and are added up at the end of the unit.
 //   warp 0        TMA: K tiles into a ring of 3, V codes into a ring of 2
 //   warp 1, 2     the MMAs of S, and of P V (one thread issues an MMA about every 110 cycles: two threads)
-//   warp 3        looks a unit ahead: largest V scale of its range, the tree's scales and ancestor bits
-//   warps 4..7    V codes to fp16; Q's parts and row scales of the next unit; the tree's K and V
+//   warp 3        looks ahead: the places and scales of the next 32 tiles, a tile a lane (two dependent loads, which
+//                 whoever needs them would wait for tile by tile)
+//   warps 4..7    V codes to fp16; Q's parts, row scales and ancestor bits of the next unit; the tree's K and V
 //   warps 8..15   softmax of stream 0 and 1, a row a thread; at the end of a unit its results
 // All waits are bounded; one that runs out sets EAGLE3_DEV_TIMEOUT and the CTA drains and exits.
 #include "cache_attn.cuh"
@@ -31,9 +32,9 @@ constexpr int D = 128;
 constexpr int BK = 128;                 // keys of a tile
 constexpr int BT = 64;                  // nodes of the tree's tile
 constexpr int KS = 3, VS = 2, VB = 2;   // stages: K codes, V codes, V in fp16
-constexpr int INFO = 8;                 // tiles whose scales are on hand
+constexpr int AHEAD = 32;               // tiles that warp 3 looks up at once, two such batches
 constexpr int NT = 512;
-constexpr int V_SHIFT = 6;              // V's fp16 values are 2^6 up: 448 -> 28672
+constexpr int LEAST_SHIFT = -60;        // of V's scale on the weights: fp16 has nothing left of them long before
 constexpr uint32_t K_TILE = BK * D, V_TILE = 2 * K_TILE;
 constexpr uint32_t Q_PART = 128 * D;    // a row tile of one part
 constexpr uint32_t OFF_Q = 0;           // [row tile][hi, lo]
@@ -42,25 +43,27 @@ constexpr uint32_t OFF_VR = OFF_K + KS * K_TILE;
 constexpr uint32_t OFF_V = OFF_VR + VS * K_TILE;
 constexpr uint32_t SMEM_DYN = OFF_V + VB * V_TILE + 1024;   // + alignment slack
 constexpr uint32_t TM_O = 0, TM_S = 256;                    // each [stream] * 128 columns
-constexpr int REGS_FEW = 64, REGS_SOFTMAX = 192;            // 2 * 128 * (64 + 192) = 65536 registers
+constexpr int REGS_FEW = 88, REGS_SOFTMAX = 168;            // 2 * 128 * (88 + 168) = 65536 registers
 constexpr int MERGE_WARPS = 8;
 
 struct Smem {
     uint64_t k_full[KS], k_empty[KS], vr_full[VS], vr_empty[VS], v_full[VB], v_empty[VB];
     uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
     uint64_t q_full, q_empty;
-    uint64_t info_full[INFO];
-    uint64_t u_full[2], u_empty[2], r_full[2];   // by unit parity
+    uint64_t ahead_full[2], ahead_empty[2];
+    uint64_t r_full[2], u_empty[2], tree_full[2];   // by unit parity
+    uint64_t c_sync;                             // warps 4..7 among themselves (a wait that ends, unlike bar.sync)
     uint64_t x_full, x_empty;                    // stream 1's statistics, one row tile only
     uint64_t mma_done[2];
     uint64_t anc[2][64];
     float qf[2][256];
-    float info_f[INFO][2];                       // score factors of the tile's two halves
-    int info_keys[INFO];                         // keys of the tile that are there, -1: the tree
-    int ev[2], tree_kb[2], odd_v[2];
+    int row[2 * AHEAD][2];                       // of the tile's two groups in the pool's map
+    uchar4 scale[2 * AHEAD];                     // K, K, V, V
+    int tree_k[2], tree_v[2], odd_v[2];          // the tree's scale bytes; whether a value is not finite
+    uint32_t top_k[4], top_v[4];
     float x_m[128], x_l[128];
-    long long warp_sum[NT / 32];
-    long long start_off, total;
+    int x_ev, x_odd;
+    long long start_off, range;
     int start_b, start_k;
     uint32_t tmem_base;
     int abort_flag;
@@ -71,6 +74,7 @@ struct Wide {
     CacheAttn a;
     int tiles2;                     // two row tiles (else one)
     int rows_per_group, row_groups, heads;   // heads = Hkv * row_groups: units of a sequence
+    uint32_t rep_magic;             // row / rep = umulhi(row, magic), 0: rep is 1
     int least;                      // tiles of a range, at least, where there are fewer than CTAs want
     WaitRule wait;
     // workspace: tiles before each sequence [B + 1], then {total tiles of all units, CTAs that have any}; where each
@@ -79,6 +83,14 @@ struct Wide {
     int4 *start;
     float *part_o, *part_ml;
 };
+
+// (exact: rows < 2^18, rep <= 2^12)
+E3_DEV int row_node(const Wide &p, int row) { return p.rep_magic ? (int)__umulhi((uint32_t)row, p.rep_magic) : row; }
+// element of query row `row` of the KV group g
+E3_DEV size_t row_at(const Wide &p, int b, int g, int row) {
+    const int node = row_node(p, row);
+    return ((size_t)b * p.a.N + node) * p.a.q_ns + (size_t)(g * p.a.rep + row - node * p.a.rep) * D;
+}
 
 E3_DEV int seq_len(const CacheAttn &a, int b) { return max(0, min(__ldg(a.prefix_len + b), a.max_prefix)); }
 E3_DEV int seq_tiles(const CacheAttn &a, int L) { return max(1, (L + BK - 1) / BK + (a.tree_k ? 1 : 0)); }
@@ -119,12 +131,7 @@ struct Walk {
     E3_DEV bool is_tree(const Wide &p, int i) const { return p.a.tree_k && i == nt - 1; }
 };
 
-E3_DEV uint32_t hmul2(uint32_t a, uint32_t b) {
-    const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
-
-// 8 fp32 as the two e4m3 parts, 8 bytes each (what is not finite: NaN)
+// 8 fp32 as the two e4m3 parts, 8 bytes each
 E3_DEV void two_parts(const float (&v)[8], uint2 &hi, uint2 &lo) {
     uint32_t h[4], l[4];
 #pragma unroll
@@ -146,6 +153,93 @@ E3_DEV void bf16x8(uint4 u, float (&v)[8]) {
     }
 }
 
+// 8 bf16 by a power of two, as chunk c of a row of two part tiles (128-byte rows, swizzled) `apart` bytes apart; what is
+// not finite (odd: some may be) as NaN
+E3_DEV void store_parts(uint4 x, float up, bool odd, uint8_t *tile, uint32_t apart, int row, int c) {
+    float v[8];
+    bf16x8(x, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= up;
+    if (odd) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = fabsf(v[e]) <= FLT_MAX ? v[e] : __int_as_float(0x7fc00000);
+    }
+    uint2 hi, lo;
+    two_parts(v, hi, lo);
+    uint8_t *at = tile + row * 128 + ((((uint32_t)c >> 1) ^ ((uint32_t)row & 7u)) << 4) + (c & 1) * 8;
+    *reinterpret_cast<uint2 *>(at) = hi;
+    *reinterpret_cast<uint2 *>(at + apart) = lo;
+}
+
+// The largest finite magnitudes of N rows, 16 lanes a row (the other 16 of a warp N more), as bits; whether the warp has
+// anything that is not finite.  Two rows a word, and all words a step at a time: the exchanges overlap.
+template <int N>
+E3_DEV bool row_maxima(const uint4 (&x)[N], uint32_t (&top)[N]) {
+    uint32_t all = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        top[j] = amax_bits(x[j]);
+        all = max(all, top[j]);
+    }
+    const bool odd = __any_sync(0xffffffffu, all >= BF16_INF);
+    if (odd) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) top[j] = amax_bits_finite(x[j]);
+    }
+    uint32_t two[N / 2], other[N / 2];
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) two[j] = top[2 * j] | top[2 * j + 1] << 16;
+#pragma unroll
+    for (int d = 8; d; d >>= 1) {
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) other[j] = __shfl_xor_sync(0xffffffffu, two[j], d);
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) two[j] = max_u16x2(two[j], other[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) {
+        top[2 * j] = two[j] & 0xffffu;
+        top[2 * j + 1] = two[j] >> 16;
+    }
+    return odd;
+}
+
+// The nodes that each node sees, by a warp: every node's set joined with that of the node it has got to, which moves
+// twice as far each time
+E3_DEV void tree_paths(const CacheAttn &a, int b, bool report, int lane, uint64_t *anc) {
+    int to[2];
+    uint64_t bits[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int i = lane + 32 * h;
+        const int q = i < a.N ? __ldg(a.parents + (size_t)b * a.N + i) : -1;
+        const bool bad = i < a.N && (i == 0 ? q != -1 : q < 0 || q >= i);
+        if (bad && report) flag(a.dev_status, EAGLE3_DEV_BAD_TREE);
+        to[h] = i == 0 || bad ? -1 : q;
+        bits[h] = 1ull << i;
+    }
+    for (int step = 0; step < 6; ++step) {
+        uint64_t more[2];
+        int next[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int from = max(0, to[h]);
+            const uint64_t b0 = __shfl_sync(0xffffffffu, bits[0], from & 31), b1 = __shfl_sync(0xffffffffu, bits[1], from & 31);
+            const int n0 = __shfl_sync(0xffffffffu, to[0], from & 31), n1 = __shfl_sync(0xffffffffu, to[1], from & 31);
+            more[h] = to[h] < 0 ? 0ull : from < 32 ? b0 : b1;
+            next[h] = to[h] < 0 ? -1 : from < 32 ? n0 : n1;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            bits[h] |= more[h];
+            to[h] = next[h];
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        if (lane + 32 * h < a.N) anc[lane + 32 * h] = bits[h];
+}
+
 E3_DEV float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -161,14 +255,15 @@ __global__ void __launch_bounds__(NT, 1)
                            const __grid_constant__ Wide p) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ Smem ss;
-    const uint32_t sm = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t *smp = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sm = smem_u32(smp);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t abort = smem_u32(&ss.abort_flag), limit = p.wait.limit;
     const CacheAttn &a = p.a;
     const bool two = p.tiles2 != 0;
     auto bar = [](uint64_t &b) { return smem_u32(&b); };
 
-    if (tid == 0) {
+    if (tid == 32) {
         for (int s = 0; s < KS; ++s) {
             tc::mbar_init(&ss.k_full[s], 1 + missing_arrivals(p.wait, s, 0));
             tc::mbar_init(&ss.k_empty[s], 1);
@@ -186,90 +281,76 @@ __global__ void __launch_bounds__(NT, 1)
             tc::mbar_init(&ss.p_full[m], 4);
             tc::mbar_init(&ss.pv_done[m], 1);
             tc::mbar_init(&ss.o_free[m], 4);
-            tc::mbar_init(&ss.u_full[m], 1);
-            tc::mbar_init(&ss.u_empty[m], 12);
+            tc::mbar_init(&ss.ahead_full[m], 1);
+            tc::mbar_init(&ss.ahead_empty[m], 9);   // the loads, eight softmax warps
             tc::mbar_init(&ss.r_full[m], 4);
+            tc::mbar_init(&ss.u_empty[m], 8);
+            tc::mbar_init(&ss.tree_full[m], 1);
             tc::mbar_init(&ss.mma_done[m], 1);
         }
-        for (int i = 0; i < INFO; ++i) tc::mbar_init(&ss.info_full[i], 1);
         tc::mbar_init(&ss.q_full, 4);
         tc::mbar_init(&ss.q_empty, 1);
+        tc::mbar_init(&ss.c_sync, 4);
         tc::mbar_init(&ss.x_full, 4);
         tc::mbar_init(&ss.x_empty, 4);
         ss.abort_flag = 0;
-        ss.start_b = 0;
         tc::fence_barrier_init();
         tc::prefetch_tmap(&tm_k);
         tc::prefetch_tmap(&tm_v);
     }
+    __syncwarp();
     if (warp == 1) tc::tmem_alloc(&ss.tmem_base, 512);
     pdl_wait();
     pdl_trigger();
 
     // ---- this CTA's range: the tiles of all sequences summed up, then the sequence that holds its first
-    long long total, range_lo, range_hi;
-    {
+    if (warp == 0) {
         auto tiles_at = [&](int b) { return b < a.B ? (long long)seq_tiles(a, seq_len(a, b)) : 0ll; };
-        // sum of the block's values before this thread's (inclusive of them in `all` for the whole block)
-        auto scan = [&](long long v, long long &all) {
-            long long x = v;
+        long long seqs = 0;
+        for (int b = lane; b < a.B; b += 32) seqs += tiles_at(b);
+#pragma unroll
+        for (int d = 16; d; d >>= 1) seqs += __shfl_xor_sync(0xffffffffu, seqs, d);
+        const long long total = seqs * p.heads;
+        // as many CTAs as leave each `least` tiles
+        const long long ctas = max(1ll, min((long long)gridDim.x, total / p.least));
+        const bool first = blockIdx.x == 0, idle = blockIdx.x >= ctas;
+        const long long lo = idle ? total : blockIdx.x * total / ctas, hi = idle ? total : (blockIdx.x + 1) * total / ctas;
+        if (lane == 0) {
+            ss.range = hi - lo;
+            if (first) {
+                p.cum[a.B] = seqs;
+                p.cum[a.B + 1] = total;
+                p.cum[a.B + 2] = ctas;
+            }
+        }
+        long long sum = 0;   // of the sequences before
+        for (int b0 = 0; b0 < a.B && (first || (sum * p.heads <= lo && !idle)); b0 += 32) {
+            const long long mine = tiles_at(b0 + lane);
+            long long x = mine;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const long long y = __shfl_up_sync(0xffffffffu, x, d);
                 if (lane >= d) x += y;
             }
-            if (lane == 31) ss.warp_sum[warp] = x;
-            __syncthreads();
-            long long before = 0;
-            all = 0;
-            for (int w = 0; w < NT / 32; ++w) {
-                if (w < warp) before += ss.warp_sum[w];
-                all += ss.warp_sum[w];
+            const long long before = sum + x - mine;
+            if (first && b0 + lane < a.B) p.cum[b0 + lane] = before;
+            if (mine > 0 && before * p.heads <= lo && lo < (before + mine) * p.heads) {
+                const long long at = lo - before * p.heads;
+                ss.start_b = b0 + lane;
+                ss.start_k = (int)(at / mine);
+                ss.start_off = at % mine;
+                p.start[blockIdx.x] = make_int4(b0 + lane, (int)(at / mine), (int)(at % mine), 0);
             }
-            __syncthreads();
-            return before + x - v;
-        };
-        long long seqs = 0;
-        for (int b0 = 0; b0 < a.B; b0 += NT) {
-            long long all;
-            const long long before = scan(tiles_at(b0 + tid), all);
-            if (blockIdx.x == 0 && p.cum && b0 + tid < a.B) p.cum[b0 + tid] = seqs + before;
-            seqs += all;
-        }
-        total = seqs * p.heads;
-        // as many CTAs as leave each `least` tiles
-        const long long ctas = max(1ll, min((long long)gridDim.x, total / p.least));
-        if (blockIdx.x == 0 && tid == 0 && p.cum) {
-            p.cum[a.B] = seqs;
-            p.cum[a.B + 1] = total;
-            p.cum[a.B + 2] = ctas;
-        }
-        const bool idle = blockIdx.x >= ctas;
-        range_lo = idle ? total : blockIdx.x * total / ctas;
-        range_hi = idle ? total : (blockIdx.x + 1) * total / ctas;
-        if (!idle) {
-            seqs = 0;
-            for (int b0 = 0; b0 < a.B; b0 += NT) {
-                long long all;
-                const long long mine = tiles_at(b0 + tid), before = seqs + scan(mine, all);
-                if (mine > 0 && before * p.heads <= range_lo && range_lo < (before + mine) * p.heads) {
-                    const long long at = range_lo - before * p.heads;
-                    ss.start_b = b0 + tid;
-                    ss.start_k = (int)(at / mine);
-                    ss.start_off = at % mine;
-                    if (p.start) p.start[blockIdx.x] = make_int4(b0 + tid, (int)(at / mine), (int)(at % mine), 0);
-                }
-                seqs += all;
-            }
+            sum += __shfl_sync(0xffffffffu, x, 31);
         }
     }
-    const long long range = range_hi - range_lo;
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
+    const long long range = ss.range;
     const uint32_t tmem = ss.tmem_base;
 
-    // (each branch gives or takes by itself: the compiler allots registers by branch)
+    // (each branch gives or takes registers by itself: the compiler allots them by branch)
     Walk w;
     if (warp == 0) {
         // ------------------------------------------------------------------ TMA
@@ -278,47 +359,31 @@ __global__ void __launch_bounds__(NT, 1)
             uint32_t t = 0, tv = 0;
             bool ok = true;
             for (bool more = w.begin(p, ss, range); more && ok; more = ok && w.next(p)) {
-                const int g = w.k / p.row_groups, sgroups = a.block_size / EAGLE3_KV_GROUP;
-                const int32_t *bt = a.block_table + (size_t)w.b * a.max_blocks;
-                for (int i = w.i0; i < w.i1; ++i, ++t) {
-                    const int s = (int)(t % KS);
+                for (int i = w.i0; i < w.i1 && ok; ++i, ++t) {
+                    if (t % AHEAD == 0 && !tc::mbar_wait(bar(ss.ahead_full[t / AHEAD & 1]), t / (2 * AHEAD) & 1u, abort, limit)) {
+                        ok = false;
+                        break;
+                    }
+                    const int s = (int)(t % KS), sv = (int)(tv % VS);
+                    const int r0 = ss.row[t % (2 * AHEAD)][0], r1 = ss.row[t % (2 * AHEAD)][1];
+                    if (t % AHEAD == AHEAD - 1) tc::mbar_arrive(bar(ss.ahead_empty[t / AHEAD & 1]));
                     if (w.is_tree(p, i)) continue;   // (warps 4..7 fill that stage)
                     if (!tc::mbar_wait(bar(ss.k_empty[s]), ((t / KS) & 1u) ^ 1u, abort, limit)) {
                         ok = false;
                         break;
                     }
-                    // two groups of 64 places; one that is not there starts above the pool and reads as zeros
-                    int row[2];
-                    float f[2];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int pos = i * BK + h * 64;
-                        row[h] = -64;
-                        f[h] = 1.0f;
-                        if (pos >= w.L) continue;
-                        const int page = __ldg(bt + pos / a.block_size), place = pos % a.block_size;
-                        if (page < 0 || page >= a.n_pages) continue;
-                        row[h] = (page * a.Hkv + g) * a.block_size + place;
-                        f[h] = scale_of(__ldg(a.ks + ((size_t)page * a.Hkv + g) * sgroups + place / EAGLE3_KV_GROUP));
-                    }
-                    ss.info_f[t % INFO][0] = f[0];
-                    ss.info_f[t % INFO][1] = f[1];
-                    ss.info_keys[t % INFO] = min(BK, w.L - i * BK);
-                    tc::mbar_arrive(bar(ss.info_full[t % INFO]));
                     tc::mbar_expect_tx(bar(ss.k_full[s]), K_TILE);
-                    const uint32_t dst = sm + OFF_K + s * K_TILE;
-                    tc::tma_load_2d(dst, &tm_k, 0, row[0], bar(ss.k_full[s]));
-                    tc::tma_load_2d(dst + K_TILE / 2, &tm_k, 0, row[1], bar(ss.k_full[s]));
-                    const int sv = (int)(tv % VS);
+                    const uint32_t dst = sm + OFF_K + s * K_TILE, dv = sm + OFF_VR + sv * K_TILE;
+                    tc::tma_load_2d(dst, &tm_k, 0, r0, bar(ss.k_full[s]));
+                    tc::tma_load_2d(dst + K_TILE / 2, &tm_k, 0, r1, bar(ss.k_full[s]));
                     if (!tc::mbar_wait(bar(ss.vr_empty[sv]), ((tv / VS) & 1u) ^ 1u, abort, limit)) {
                         ok = false;
                         ++t;
                         break;
                     }
                     tc::mbar_expect_tx(bar(ss.vr_full[sv]), K_TILE);
-                    const uint32_t dv = sm + OFF_VR + sv * K_TILE;
-                    tc::tma_load_2d(dv, &tm_v, 0, row[0], bar(ss.vr_full[sv]));
-                    tc::tma_load_2d(dv + K_TILE / 2, &tm_v, 0, row[1], bar(ss.vr_full[sv]));
+                    tc::tma_load_2d(dv, &tm_v, 0, r0, bar(ss.vr_full[sv]));
+                    tc::tma_load_2d(dv + K_TILE / 2, &tm_v, 0, r1, bar(ss.vr_full[sv]));
                     ++tv;
                 }
             }
@@ -408,10 +473,12 @@ __global__ void __launch_bounds__(NT, 1)
                         }
                         tc::fence_after();
                         const uint32_t t_p = tmem + TM_S + (uint32_t)(m * 128);
-                        for (int kk = 0; kk < ksteps; ++kk)
-                            tc::mma_bf16_ts(tmem + TM_O + (uint32_t)(m * 128), t_p + (uint32_t)(kk * 8),
-                                            tc::desc_mn_sw128(vaddr + kk * 2048, V_TILE / 2, 1024), IDESC,
-                                            !fresh || kk > 0 ? 1u : 0u);
+#pragma unroll
+                        for (int kk = 0; kk < BK / 16; ++kk)
+                            if (kk < ksteps)
+                                tc::mma_bf16_ts(tmem + TM_O + (uint32_t)(m * 128), t_p + (uint32_t)(kk * 8),
+                                                tc::desc_mn_sw128(vaddr + kk * 2048, V_TILE / 2, 1024), IDESC,
+                                                !fresh || kk > 0 ? 1u : 0u);
                         tc::mma_commit(bar(ss.pv_done[m]));
                     }
                     if (ok) tc::mma_commit(bar(ss.v_empty[s]));
@@ -423,211 +490,215 @@ __global__ void __launch_bounds__(NT, 1)
         }
         __syncwarp();
     } else if (warp == 3) {
-        // ------------------------------------------------------------------ a unit ahead
+        // ------------------------------------------------------------------ places and scales ahead
         tc::registers_give<REGS_FEW>();
         bool ok = true;
+        uint32_t t = 0;
         for (bool more = w.begin(p, ss, range); more && ok; more = ok && w.next(p)) {
-            const int u = w.n & 1;
-            if (w.n >= 2 && !tc::mbar_wait_warp(bar(ss.u_empty[u]), ((w.n - 2) >> 1) & 1u, abort, limit)) {
-                ok = false;
-                break;
-            }
             const int g = w.k / p.row_groups, sgroups = a.block_size / EAGLE3_KV_GROUP;
             const int32_t *bt = a.block_table + (size_t)w.b * a.max_blocks;
-            const bool tree = a.tree_k && w.i1 == w.nt;
-            const int g0 = w.i0 * 2, g1 = (int)(((long long)min((long long)w.L, (long long)w.i1 * BK) + 63) / 64);
-            int ev = 1;
-            for (int x = g0 + lane; x < g1; x += 32) {
-                const int pos = x * 64, page = __ldg(bt + pos / a.block_size), place = pos % a.block_size;
-                if (page < 0 || page >= a.n_pages) continue;
-                const int e = __ldg(a.vs + ((size_t)page * a.Hkv + g) * sgroups + place / EAGLE3_KV_GROUP);
-                if (e != 255) ev = max(ev, e);
-            }
-            bool odd_k = false, odd_v = false;
-            float km = 0.0f;
-            if (tree) {
-                const __nv_bfloat16 *tk = a.tree_k + (size_t)w.b * a.N * a.kv_ns + (size_t)g * D;
-                const __nv_bfloat16 *tv = a.tree_v + (size_t)w.b * a.N * a.kv_ns + (size_t)g * D;
-                float vm = 0.0f;
-                for (int x = lane; x < a.N * (D / 8); x += 32) {
-                    const int64_t at = (x >> 4) * a.kv_ns + (x & 15) * 8;
-                    km = fmaxf(km, amax8(*reinterpret_cast<const uint4 *>(tk + at), odd_k));
-                    vm = fmaxf(vm, amax8(*reinterpret_cast<const uint4 *>(tv + at), odd_v));
+            for (int i = w.i0; i < w.i1;) {
+                const uint32_t batch = t / AHEAD;
+                if (t % AHEAD == 0 && batch >= 2 &&
+                    !tc::mbar_wait_warp(bar(ss.ahead_empty[batch & 1]), ((batch - 2) >> 1) & 1u, abort, limit)) {
+                    ok = false;
+                    break;
                 }
-                ev = max(ev, scale_byte(vm));
-                for (int i = lane; i < a.N; i += 32) {
-                    bool bad = false;
-                    ss.anc[u][i] = path_bits(a.parents + (size_t)w.b * a.N, i, bad);
-                    if (bad && w.k == 0) flag(a.dev_status, EAGLE3_DEV_BAD_TREE);
-                }
-            }
+                const int n = min(AHEAD - (int)(t % AHEAD), w.i1 - i);
+                if (lane < n) {
+                    // a group that is not there starts above the pool, where the load reads zeros
+                    int row[2] = {-64, -64}, ks[2] = {127, 127}, vs[2] = {1, 1};
 #pragma unroll
-            for (int x = 16; x; x >>= 1) {
-                ev = max(ev, __shfl_xor_sync(0xffffffffu, ev, x));
-                km = fmaxf(km, __shfl_xor_sync(0xffffffffu, km, x));
+                    for (int h = 0; h < 2; ++h) {
+                        const long long pos = (long long)(i + lane) * BK + h * 64;
+                        if (pos >= w.L) continue;
+                        const int page = __ldg(bt + (int)pos / a.block_size), place = (int)pos % a.block_size;
+                        if (page < 0 || page >= a.n_pages) continue;
+                        row[h] = (page * a.Hkv + g) * a.block_size + place;
+                        const size_t at = ((size_t)page * a.Hkv + g) * sgroups + place / EAGLE3_KV_GROUP;
+                        ks[h] = __ldg(a.ks + at);
+                        vs[h] = __ldg(a.vs + at);
+                    }
+                    const int slot = (int)((t + lane) % (2 * AHEAD));
+                    ss.row[slot][0] = row[0];
+                    ss.row[slot][1] = row[1];
+                    ss.scale[slot] = make_uchar4(ks[0], ks[1], vs[0], vs[1]);
+                }
+                t += n;
+                i += n;
+                __syncwarp();
+                if (t % AHEAD == 0 && lane == 0) tc::mbar_arrive(bar(ss.ahead_full[batch & 1]));
             }
-            odd_v = __any_sync(0xffffffffu, odd_v);
-            if (lane == 0) {
-                ss.ev[u] = ev;
-                ss.tree_kb[u] = scale_byte(km);
-                ss.odd_v[u] = tree && odd_v;
-                const int L = __ldg(a.prefix_len + w.b);
-                if ((L < 0 || L > a.max_prefix) && w.k == 0 && w.i0 == 0) flag(a.dev_status, EAGLE3_DEV_CAPACITY);
-            }
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(bar(ss.u_full[u]));
         }
+        if (ok && t % AHEAD != 0 && lane == 0) tc::mbar_arrive(bar(ss.ahead_full[t / AHEAD & 1]));
         if (!ok && lane == 0) flag(a.dev_status, EAGLE3_DEV_TIMEOUT);
     } else if (warp < 8) {
         // ------------------------------------------------------------------ conversions
         tc::registers_give<REGS_FEW>();
         const int cw = warp - 4;
-        uint32_t t = 0, tv = 0;
+        uint32_t t = 0, tv = 0, syncs = 0;
         bool ok = true;
+        auto together = [&] {
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(bar(ss.c_sync));
+            return tc::mbar_wait_warp(bar(ss.c_sync), syncs++ & 1u, abort, limit);
+        };
         for (bool more = w.begin(p, ss, range); more && ok; more = ok && w.next(p)) {
             const int u = w.n & 1, g = w.k / p.row_groups, row0 = w.k % p.row_groups * p.rows_per_group;
-            if (!tc::mbar_wait_warp(bar(ss.u_full[u]), (w.n >> 1) & 1u, abort, limit) ||
+            if ((w.n >= 2 && !tc::mbar_wait_warp(bar(ss.u_empty[u]), ((w.n - 2) >> 1) & 1u, abort, limit)) ||
                 (w.n > 0 && !tc::mbar_wait_warp(bar(ss.q_empty), (w.n - 1) & 1u, abort, limit))) {
                 ok = false;
                 break;
             }
-            // ---- Q's parts: 16 lanes a row, two rows at a time
+            const bool tree = a.tree_k && w.i1 == w.nt;
+            // ---- Q's parts: 16 lanes a row, two rows at a time, eight such pairs on their way
             const int nrows = min(p.rows_per_group, a.N * a.rep - row0);
-#pragma unroll 4
-            for (int it = 0; it < p.rows_per_group / 8; ++it) {
-                const int row = it * 8 + cw * 2 + (lane >> 4), c = lane & 15;
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (row < nrows) {
-                    const int node = (row0 + row) / a.rep, head = g * a.rep + (row0 + row) % a.rep;
-                    x = *reinterpret_cast<const uint4 *>(a.q + ((size_t)w.b * a.N + node) * a.q_ns + (size_t)head * D + c * 8);
+            for (int it = 0; it < p.rows_per_group / 8; it += 8) {
+                uint4 x[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int row = (it + j) * 8 + cw * 2 + (lane >> 4);
+                    x[j] = make_uint4(0, 0, 0, 0);
+                    if (row < nrows) x[j] = *reinterpret_cast<const uint4 *>(a.q + row_at(p, w.b, g, row0 + row) + (lane & 15) * 8);
                 }
-                bool odd = false;
-                float top = amax8(x, odd);
+                uint32_t top[8];
+                const bool odd = row_maxima<8>(x, top);
 #pragma unroll
-                for (int d = 8; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                const int byte = scale_byte(top);
-                const float up = inverse_scale(byte);
-                float v[8];
-                bf16x8(x, v);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = fabsf(v[e]) <= FLT_MAX ? v[e] * up : __int_as_float(0x7fc00000);
-                uint2 hi, lo;
-                two_parts(v, hi, lo);
-                const uint32_t at = sm + OFF_Q + (row >> 7) * 2 * Q_PART + (row & 127) * 128 +
-                                    ((((uint32_t)c >> 1) ^ ((uint32_t)row & 7u)) << 4) + (c & 1) * 8;
-                asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(hi.x), "r"(hi.y) : "memory");
-                asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + Q_PART), "r"(lo.x), "r"(lo.y) : "memory");
-                if (c == 0) ss.qf[u][row] = a.scale_log2 * scale_of(byte);
+                for (int j = 0; j < 8; ++j) {
+                    const int row = (it + j) * 8 + cw * 2 + (lane >> 4), byte = scale_byte_bits(top[j]);
+                    store_parts(x[j], inverse_scale(byte), odd, smp + OFF_Q + (row >> 7) * 2 * Q_PART, Q_PART, row & 127, lane & 15);
+                    if ((lane & 15) == 0) ss.qf[u][row] = a.scale_log2 * scale_of(byte);
+                }
             }
-            const int evref = ss.ev[u];
             tc::fence_proxy_async_smem();
+            if (cw == 0) {
+                if (tree) tree_paths(a, w.b, w.k == 0, lane, ss.anc[u]);
+                const int L = __ldg(a.prefix_len + w.b);
+                if (lane == 0 && (L < 0 || L > a.max_prefix) && w.k == 0 && w.i0 == 0) flag(a.dev_status, EAGLE3_DEV_CAPACITY);
+            }
             __syncwarp();
             if (lane == 0) {
                 tc::mbar_arrive(bar(ss.q_full));
                 tc::mbar_arrive(bar(ss.r_full[u]));
             }
-            const int sgroups = a.block_size / EAGLE3_KV_GROUP;
-            const int32_t *bt = a.block_table + (size_t)w.b * a.max_blocks;
+            // the next unit's queries, and this unit's tree, into L2
+            {
+                Walk nx = w;
+                if (nx.next(p)) {
+                    const int ng = nx.k / p.row_groups, nrow0 = nx.k % p.row_groups * p.rows_per_group;
+                    const int rows_next = min(p.rows_per_group, a.N * a.rep - nrow0);
+                    for (int row = cw * 32 + lane; row < rows_next; row += 128)
+                        tc::prefetch_l2(a.q + row_at(p, nx.b, ng, nrow0 + row), 2 * D);
+                }
+                if (tree && cw < 2)
+                    for (int i = lane; i < a.N; i += 32)
+                        tc::prefetch_l2((cw ? a.tree_v : a.tree_k) + ((size_t)w.b * a.N + i) * a.kv_ns + (size_t)g * D, 2 * D);
+            }
             for (int i = w.i0; i < w.i1; ++i, ++t) {
                 const int s = (int)(t % VB);
-                const uint32_t dst = sm + OFF_V + s * V_TILE;
+                uint8_t *dst = smp + OFF_V + s * V_TILE;
                 if (w.is_tree(p, i)) {
-                    // ---- the tree: K in two parts into its stage, V in fp16
-                    if (!tc::mbar_wait_warp(bar(ss.k_empty[t % KS]), ((t / KS) & 1u) ^ 1u, abort, limit) ||
+                    // ---- the tree: V in fp16, K in two parts into its stage, each by the power of two of its largest
+                    const int c = lane & 15, r0 = cw * 2 + (lane >> 4);
+                    uint4 x[BT / 8];
+                    bool odd = false;
+                    // the rows of this warp in x, and the scale byte of them all
+                    auto load = [&](const __nv_bfloat16 *src, uint32_t *tops, int &byte) {
+                        src += (size_t)w.b * a.N * a.kv_ns + (size_t)g * D + c * 8;
+#pragma unroll
+                        for (int j = 0; j < BT / 8; ++j) {
+                            x[j] = make_uint4(0, 0, 0, 0);
+                            if (j * 8 + r0 < a.N) x[j] = *reinterpret_cast<const uint4 *>(src + (j * 8 + r0) * a.kv_ns);
+                        }
+                        uint32_t top[BT / 8], all = 0;
+                        odd = row_maxima<BT / 8>(x, top);
+#pragma unroll
+                        for (int j = 0; j < BT / 8; ++j) all = max(all, top[j]);
+                        all = max(all, __shfl_xor_sync(0xffffffffu, all, 16));
+                        if (lane == 0) tops[cw] = all;
+                        const bool got = together();
+                        byte = scale_byte_bits(max(max(tops[0], tops[1]), max(tops[2], tops[3])));
+                        return got;
+                    };
+                    int kb, vb;
+                    if (cw == 0 && lane == 0) ss.odd_v[u] = 0;
+                    if (!load(a.tree_v, ss.top_v, vb) ||
                         !tc::mbar_wait_warp(bar(ss.v_empty[s]), ((t / VB) & 1u) ^ 1u, abort, limit)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t kd = sm + OFF_K + (t % KS) * K_TILE;
-                    const int kb = ss.tree_kb[u];
-                    const float kup = inverse_scale(kb), vup = inverse_scale(evref) * (float)(1 << V_SHIFT);
-                    const size_t base = (size_t)w.b * a.N * a.kv_ns + (size_t)g * D;
-#pragma unroll 2
-                    for (int it = 0; it < BT / 8; ++it) {
-                        const int row = it * 8 + cw * 2 + (lane >> 4), c = lane & 15;
-                        uint4 xk = make_uint4(0, 0, 0, 0), xv = xk;
-                        if (row < a.N) {
-                            xk = *reinterpret_cast<const uint4 *>(a.tree_k + base + row * a.kv_ns + c * 8);
-                            xv = *reinterpret_cast<const uint4 *>(a.tree_v + base + row * a.kv_ns + c * 8);
-                        }
-                        float v[8];
-                        bf16x8(xk, v);
+                    if (lane == 0 && odd) ss.odd_v[u] = 1;
+                    const float vup = inverse_scale(vb);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] = fabsf(v[e]) <= FLT_MAX ? v[e] * kup : __int_as_float(0x7fc00000);
-                        uint2 hi, lo;
-                        two_parts(v, hi, lo);
-                        const uint32_t at = kd + row * 128 + ((((uint32_t)c >> 1) ^ ((uint32_t)row & 7u)) << 4) + (c & 1) * 8;
-                        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(hi.x), "r"(hi.y) : "memory");
-                        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + K_TILE / 2), "r"(lo.x), "r"(lo.y) : "memory");
-                        bf16x8(xv, v);
+                    for (int j = 0; j < BT / 8; ++j) {
+                        const int row = j * 8 + r0;
+                        float v[8];
+                        bf16x8(x[j], v);
+                        if (odd) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) v[e] = fabsf(v[e]) <= FLT_MAX ? v[e] : 0.0f;
+                        }
                         uint32_t h[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float x0 = v[2 * e], x1 = v[2 * e + 1];
-                            h[e] = pack_f16(fabsf(x0) <= FLT_MAX ? x0 * vup : 0.0f, fabsf(x1) <= FLT_MAX ? x1 * vup : 0.0f);
-                        }
-                        const uint32_t av = dst + (c >> 3) * (V_TILE / 2) + row * 128 +
-                                            (((uint32_t)c & 7u) ^ ((uint32_t)row & 7u)) * 16;
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(av), "r"(h[0]), "r"(h[1]), "r"(h[2]),
-                                     "r"(h[3])
-                                     : "memory");
+                        for (int e = 0; e < 4; ++e) h[e] = pack_f16(v[2 * e] * vup, v[2 * e + 1] * vup);
+                        *reinterpret_cast<uint4 *>(dst + (c >> 3) * (V_TILE / 2) + row * 128 +
+                                                   (((uint32_t)c & 7u) ^ ((uint32_t)row & 7u)) * 16) =
+                            make_uint4(h[0], h[1], h[2], h[3]);
                     }
+                    if (!load(a.tree_k, ss.top_k, kb) ||
+                        !tc::mbar_wait_warp(bar(ss.k_empty[t % KS]), ((t / KS) & 1u) ^ 1u, abort, limit)) {
+                        ok = false;
+                        break;
+                    }
+#pragma unroll
+                    for (int j = 0; j < BT / 8; ++j)
+                        store_parts(x[j], inverse_scale(kb), odd, smp + OFF_K + (t % KS) * K_TILE, K_TILE / 2, j * 8 + r0, c);
                     tc::fence_proxy_async_smem();
-                    asm volatile("bar.sync 1, 128;" ::: "memory");   // all of K is there: one arrival
+                    if (!together()) {   // all of K is there: one arrival
+                        ok = false;
+                        break;
+                    }
                     if (cw == 0 && lane == 0) {
-                        ss.info_f[t % INFO][0] = ss.info_f[t % INFO][1] = scale_of(kb);
-                        ss.info_keys[t % INFO] = -1;
-                        tc::mbar_arrive(bar(ss.info_full[t % INFO]));
+                        ss.tree_k[u] = kb;
+                        ss.tree_v[u] = vb;
+                        tc::mbar_arrive(bar(ss.tree_full[u]));
                         tc::mbar_arrive(bar(ss.k_full[t % KS]));
                     }
                     if (lane == 0) tc::mbar_arrive(bar(ss.v_full[s]));
                     continue;
                 }
-                // ---- V's codes of 32 keys a warp (all in one group): 8 lanes a key
+                // ---- V's codes of 32 keys a warp: 8 lanes a key
                 const int sv = (int)(tv % VS);
-                const int pos = i * BK + cw * 32;
-                int e = 1;
-                if (pos < w.L) {
-                    const int page = __ldg(bt + pos / a.block_size), place = pos % a.block_size;
-                    if (page >= 0 && page < a.n_pages)
-                        e = __ldg(a.vs + ((size_t)page * a.Hkv + g) * sgroups + place / EAGLE3_KV_GROUP);
-                }
-                // 2^(e - evref + V_SHIFT) in fp16: 0 where it is below its smallest
-                const float vs = e == 255 ? __int_as_float(0x7fc00000) : exp2_int(e - evref + V_SHIFT);
-                const uint32_t vs2 = pack_f16(vs, vs);
                 if (!tc::mbar_wait_warp(bar(ss.vr_full[sv]), (tv / VS) & 1u, abort, limit) ||
                     !tc::mbar_wait_warp(bar(ss.v_empty[s]), ((t / VB) & 1u) ^ 1u, abort, limit)) {
                     ok = false;
                     break;
                 }
-                const uint32_t src = sm + OFF_VR + sv * K_TILE;
+                const uint8_t *src = smp + OFF_VR + sv * K_TILE;
                 const int c = lane & 7;
 #pragma unroll
-                for (int it = 0; it < 8; ++it) {
-                    const int key = cw * 32 + it * 4 + (lane >> 3);
-                    uint32_t x[4];
-                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                                 : "r"(src + key * 128 + (((uint32_t)c ^ ((uint32_t)key & 7u)) << 4)));
-                    if (i * BK + key >= w.L) x[0] = x[1] = x[2] = x[3] = 0;   // whatever lies behind the last key
-                    uint32_t y[8];
+                for (int it = 0; it < 8; it += 4) {
+                    uint4 x[4];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        y[2 * q] = hmul2(e4m3x2_f16(x[q]), vs2);
-                        y[2 * q + 1] = hmul2(e4m3x2_f16(x[q] >> 16), vs2);
+                    for (int j = 0; j < 4; ++j) {
+                        const int key = cw * 32 + (it + j) * 4 + (lane >> 3);
+                        x[j] = *reinterpret_cast<const uint4 *>(src + key * 128 + (((uint32_t)c ^ ((uint32_t)key & 7u)) << 4));
+                        if (i * BK + key >= w.L) x[j] = make_uint4(0, 0, 0, 0);   // whatever lies behind the last key
                     }
-                    // 16 dims: two chunks of a block of 64; the upper block's lanes store theirs in the other order, so
-                    // that 8 lanes fill all banks
-                    const uint32_t blk = dst + (c >> 2) * (V_TILE / 2) + key * 128;
-                    const bool swap = c >= 4;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t ch = (uint32_t)(2 * c + (swap ? 1 - h : h)) & 7u;
-                        const uint32_t at = blk + ((ch ^ ((uint32_t)key & 7u)) << 4);
-                        const bool second = swap ? h == 0 : h == 1;
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(second ? y[4] : y[0]),
-                                     "r"(second ? y[5] : y[1]), "r"(second ? y[6] : y[2]), "r"(second ? y[7] : y[3])
-                                     : "memory");
+                    for (int j = 0; j < 4; ++j) {
+                        const int key = cw * 32 + (it + j) * 4 + (lane >> 3);
+                        const uint4 lo = make_uint4(e4m3x2_f16(x[j].x), e4m3x2_f16(x[j].x >> 16), e4m3x2_f16(x[j].y),
+                                                    e4m3x2_f16(x[j].y >> 16));
+                        const uint4 hi = make_uint4(e4m3x2_f16(x[j].z), e4m3x2_f16(x[j].z >> 16), e4m3x2_f16(x[j].w),
+                                                    e4m3x2_f16(x[j].w >> 16));
+                        // 16 dims: two chunks of a block of 64; the upper block's lanes store theirs in the other order,
+                        // so that 8 lanes fill all banks
+                        uint8_t *blk = dst + (c >> 2) * (V_TILE / 2) + key * 128;
+                        const bool swap = c >= 4;
+                        const uint32_t c0 = (uint32_t)(2 * c) & 7u, key7 = (uint32_t)key & 7u;
+                        *reinterpret_cast<uint4 *>(blk + (((c0 + (swap ? 1u : 0u)) ^ key7) << 4)) = swap ? hi : lo;
+                        *reinterpret_cast<uint4 *>(blk + (((c0 + (swap ? 0u : 1u)) ^ key7) << 4)) = swap ? lo : hi;
                     }
                 }
                 tc::fence_proxy_async_smem();
@@ -638,8 +709,7 @@ __global__ void __launch_bounds__(NT, 1)
                 }
                 ++tv;
             }
-            __syncwarp();
-            if (ok && lane == 0) tc::mbar_arrive(bar(ss.u_empty[u]));
+            if (ok && !tree && cw == 0 && lane == 0) tc::mbar_arrive(bar(ss.tree_full[u]));   // (a phase a unit)
         }
         if (!ok && lane == 0) flag(a.dev_status, EAGLE3_DEV_TIMEOUT);
     } else {
@@ -653,20 +723,36 @@ __global__ void __launch_bounds__(NT, 1)
         for (bool more = w.begin(p, ss, range); more && ok; more = ok && w.next(p)) {
             const int u = w.n & 1, g = w.k / p.row_groups, row0 = w.k % p.row_groups * p.rows_per_group;
             const int row = two ? m * 128 + r : r, nrows = min(p.rows_per_group, a.N * a.rep - row0);
-            if (!tc::mbar_wait_warp(bar(ss.u_full[u]), (w.n >> 1) & 1u, abort, limit) ||
-                !tc::mbar_wait_warp(bar(ss.r_full[u]), (w.n >> 1) & 1u, abort, limit)) {
+            if (!tc::mbar_wait_warp(bar(ss.r_full[u]), (w.n >> 1) & 1u, abort, limit)) {
                 ok = false;
                 break;
             }
             const float fr = ss.qf[u][row];
-            uint64_t anc = 0;
-            if (a.tree_k && w.i1 == w.nt && row < nrows) anc = ss.anc[u][(row0 + row) / a.rep];
             float m_run = -INFINITY, l_run = 0.0f;
-            bool fresh = true;
+            int evref = 0;                     // V's scale byte that O is relative to: the largest so far
+            bool fresh = true, odd_v = false;
             for (int i = w.i0; i < w.i1; ++i, ++t) {
+                const uint32_t batch = t / AHEAD;
+                if (t % AHEAD == 0 && !tc::mbar_wait_warp(bar(ss.ahead_full[batch & 1]), (batch >> 1) & 1u, abort, limit)) {
+                    ok = false;
+                    break;
+                }
+                uchar4 sb = ss.scale[t % (2 * AHEAD)];
+                if (t % AHEAD == AHEAD - 1) {
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(bar(ss.ahead_empty[batch & 1]));
+                }
                 if (!two && (int)(t & 1u) != m) continue;
-                if (!tc::mbar_wait_warp(bar(ss.info_full[t % INFO]), (t / INFO) & 1u, abort, limit) ||
-                    !tc::mbar_wait_warp(bar(ss.s_full[m]), stream_tiles(two, m, t) & 1u, abort, limit)) {
+                const bool tree = w.is_tree(p, i);
+                if (tree) {
+                    if (!tc::mbar_wait_warp(bar(ss.tree_full[u]), (w.n >> 1) & 1u, abort, limit)) {
+                        ok = false;
+                        break;
+                    }
+                    sb = make_uchar4(ss.tree_k[u], ss.tree_k[u], ss.tree_v[u], ss.tree_v[u]);
+                    odd_v = ss.odd_v[u] != 0;
+                }
+                if (!tc::mbar_wait_warp(bar(ss.s_full[m]), stream_tiles(two, m, t) & 1u, abort, limit)) {
                     ok = false;
                     break;
                 }
@@ -675,53 +761,57 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) tc::tmem_ld32_start(t_s + 32u * q, sc + 32 * q);
                 // (a factor that underflows would make NaN of the masked scores; a NaN stays)
-                float f0 = fr * ss.info_f[t % INFO][0], f1 = fr * ss.info_f[t % INFO][1];
+                float f0 = fr * scale_of(sb.x), f1 = fr * scale_of(sb.y);
                 f0 = f0 < FLT_MIN ? FLT_MIN : f0;
                 f1 = f1 < FLT_MIN ? FLT_MIN : f1;
-                const int keys = ss.info_keys[t % INFO];
+                const int keys = tree ? -1 : min(BK, w.L - i * BK);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) tc::tmem_ld32_wait(sc + 32 * q);
                 if (keys < BK) {
+                    uint64_t anc = 0;
+                    if (tree && row < nrows) anc = ss.anc[u][row_node(p, row0 + row)];
                     uint32_t vis[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const int n = keys - 32 * q;
-                        vis[q] = keys < 0 ? (q < 2 ? (uint32_t)(anc >> (32 * q)) : 0u)
+                        vis[q] = keys < 0 ? (q < 2 ? (uint32_t)(anc >> (32 * (q & 1))) : 0u)
                                           : n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
                     }
 #pragma unroll
                     for (int e = 0; e < 128; ++e) sc[e] = (vis[e >> 5] >> (e & 31)) & 1u ? sc[e] : -INFINITY;
                 }
-                float mq[2][2] = {{-INFINITY, -INFINITY}, {-INFINITY, -INFINITY}};
+                float mq[2][4];
 #pragma unroll
-                for (int e = 0; e < 128; e += 2) mq[e >> 6][(e >> 1) & 1] = max3(mq[e >> 6][(e >> 1) & 1], sc[e], sc[e + 1]);
-                const float mx = fmaxf(fmaxf(mq[0][0], mq[0][1]) * f0, fmaxf(mq[1][0], mq[1][1]) * f1);
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mq[h][e] = max3(sc[64 * h + 3 * e], sc[64 * h + 3 * e + 1], sc[64 * h + 3 * e + 2]);
+#pragma unroll
+                    for (int e = 12; e < 64; e += 2) mq[h][(e >> 1) & 3] = max3(mq[h][(e >> 1) & 3], sc[64 * h + e], sc[64 * h + e + 1]);
+                }
+                const float mx = fmaxf(max3(fmaxf(mq[0][0], mq[0][1]), mq[0][2], mq[0][3]) * f0,
+                                       max3(fmaxf(mq[1][0], mq[1][1]), mq[1][2], mq[1][3]) * f1);
                 const bool need = mx > m_run + RESCALE_LOG2;
-                if (__any_sync(0xffffffffu, need)) {
+                const int ev = max(sb.z == 255 ? 0 : sb.z, sb.w == 255 ? 0 : sb.w);
+                const bool moved = __any_sync(0xffffffffu, need || ev > evref);
+                float corr = 1.0f;
+                if (moved) {
                     const float m_new = need ? mx : m_run;
-                    const float corr = need ? (m_run == -INFINITY ? 0.0f : fast_exp2(m_run - m_new)) : 1.0f;
+                    corr = need ? (m_run == -INFINITY ? 0.0f : fast_exp2(m_run - m_new)) : 1.0f;
                     l_run *= corr;
                     m_run = m_new;
-                    // (the weights of the tile before have been multiplied: S waited for that)
-                    if (!fresh) {
-#pragma unroll 1
-                        for (int q = 0; q < 4; ++q) {
-                            float o[32];
-                            tc::tmem_ld32(t_o + 32u * q, o);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] *= corr;
-                            tc::tmem_st32(t_o + 32u * q, o);
-                        }
+                    if (ev > evref) {
+                        corr *= exp2_int(evref - ev);
+                        evref = ev;
                     }
                 }
-                fresh = false;
                 const float nm = m_run == -INFINITY ? 0.0f : WEIGHT_LOG2 - m_run;
-                const float2 nm2 = make_float2(nm, nm);
-                float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    const float f = q ? f1 : f0;
-                    const float2 f2 = make_float2(f, f);
+                    // the weights by V's scale: 2^down of them; their sum without it
+                    const int vb = q ? sb.w : sb.z, down = max(LEAST_SHIFT, vb - evref);
+                    const float f = q ? f1 : f0, n = vb == 255 ? __int_as_float(0x7fc00000) : nm + (float)down;
+                    const float2 f2 = make_float2(f, f), nm2 = make_float2(n, n);
+                    float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
                     uint32_t pk[32];
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
@@ -730,17 +820,30 @@ __global__ void __launch_bounds__(NT, 1)
                         sum[e & 1] = __fadd2_rn(sum[e & 1], y);
                         pk[e] = pack_f16(y.x, y.y);
                     }
-                    tc::tmem_st32u(t_s + 32u * q, pk);
+                    const float2 s2 = __fadd2_rn(sum[0], sum[1]);
+                    l_run += (s2.x + s2.y) * exp2_int(-down);
+                    tc::tmem_st32u_start(t_s + 32u * q, pk);
                 }
-                const float2 s2 = __fadd2_rn(sum[0], sum[1]);
-                l_run += s2.x + s2.y;
+                tc::tmem_st_wait();
+                // O (now that the scores' registers are free; P V of the tile before is done, since S waited for it)
+                if (moved && !fresh) {
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        float o[32];
+                        tc::tmem_ld32(t_o + 32u * q, o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] *= corr;
+                        tc::tmem_st32(t_o + 32u * q, o);
+                    }
+                }
+                fresh = false;
                 tc::fence_before();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(bar(ss.p_full[m]));
             }
             if (!ok) break;
             // ---- the unit's results
-            float e0 = 1.0f, e1 = 0.0f, M = m_run, l = l_run;
+            float e0 = scale_of(evref), e1 = 0.0f, M = m_run, l = l_run;   // factors of the streams' sums
             if (!two) {
                 if (m == 1) {
                     if (w.n > 0 && !tc::mbar_wait_warp(bar(ss.x_empty), (w.n - 1) & 1u, abort, limit)) {
@@ -749,6 +852,10 @@ __global__ void __launch_bounds__(NT, 1)
                     }
                     ss.x_m[r] = m_run;
                     ss.x_l[r] = l_run;
+                    if (r == 0) {
+                        ss.x_ev = evref;
+                        ss.x_odd = odd_v ? 1 : 0;
+                    }
                     __syncwarp();
                     if (lane == 0) {
                         tc::mbar_arrive(bar(ss.x_full));
@@ -760,13 +867,15 @@ __global__ void __launch_bounds__(NT, 1)
                     ok = false;
                     break;
                 }
-                const float m2 = ss.x_m[r], l2 = ss.x_l[r];
+                const float m2 = ss.x_m[r], l2 = ss.x_l[r], v2 = scale_of(ss.x_ev);
+                odd_v = odd_v || ss.x_odd != 0;
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(bar(ss.x_empty));
                 M = fmaxf(m_run, m2);
-                e0 = weight_of(m_run, l_run, M);
-                e1 = weight_of(m2, l2, M);
-                l = e0 * l_run + e1 * l2;
+                const float a0 = weight_of(m_run, l_run, M), a1 = weight_of(m2, l2, M);
+                l = a0 * l_run + a1 * l2;
+                e0 *= a0;
+                e1 = v2 * a1;
                 const uint32_t n1 = stream_tiles(false, 1, t);
                 if (n1 > 0 && !tc::mbar_wait_warp(bar(ss.pv_done[1]), (n1 - 1) & 1u, abort, limit)) {
                     ok = false;
@@ -781,31 +890,24 @@ __global__ void __launch_bounds__(NT, 1)
             tc::fence_after();
             const bool whole = w.i0 == 0 && w.i1 == w.nt;
             const bool mine = row < nrows;
-            const int node = (row0 + row) / a.rep, head = g * a.rep + (row0 + row) % a.rep;
+            const int node = row_node(p, row0 + row), head = g * a.rep + row0 + row - node * a.rep;
             const size_t at = ((size_t)w.b * a.N + (mine ? node : 0)) * a.Hq + (mine ? head : 0);
             const size_t part = (size_t)(2 * blockIdx.x + (w.n > 0 ? 1 : 0)) * p.rows_per_group + row;
-            const int evref = ss.ev[u];
-            const bool odd_v = ss.odd_v[u] != 0;
-            // 2^(evref - 127 - V_SHIFT), in two steps where it is no normal number
-            const float vs = scale_of(evref) * (1.0f / (1 << V_SHIFT));
+            const uint64_t anc = odd_v && mine ? ss.anc[u][node] : 0;
             const float inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+            const bool has0 = l_run != 0.0f && e0 != 0.0f, has1 = e1 != 0.0f;   // (a stream without a key has summed up nothing)
 #pragma unroll 1
             for (int q = 0; q < 4; ++q) {
                 float o[32];
                 tc::tmem_ld32(t_lane + TM_O + 32u * q + (two ? m * 128u : 0u), o);   // warp-collective
-                if (!two) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = e0 != 0.0f ? o[e] * e0 : 0.0f;
+                for (int e = 0; e < 32; ++e) o[e] = has0 ? o[e] * e0 : 0.0f;
+                if (!two) {
                     float o2[32];
                     tc::tmem_ld32(t_lane + TM_O + 128u + 32u * q, o2);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = e1 != 0.0f ? o[e] + o2[e] * e1 : o[e];
-                } else if (l == 0.0f) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = 0.0f;
+                    for (int e = 0; e < 32; ++e) o[e] = has1 ? o[e] + o2[e] * e1 : o[e];
                 }
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] *= vs;
                 // infinities and NaN of the tree's values, to the rows that see them
                 if (odd_v && mine) {
                     for (int j = 0; j < a.N; ++j) {
@@ -917,6 +1019,7 @@ Plan plan(const CacheAttn &a, int requested) {
     w.rows_per_group = w.tiles2 ? 256 : 128;
     w.row_groups = (rows + w.rows_per_group - 1) / w.rows_per_group;
     w.heads = a.Hkv * w.row_groups;
+    w.rep_magic = a.rep == 1 ? 0u : (uint32_t)(((1ull << 32) + a.rep - 1) / a.rep);
     const int64_t units = (int64_t)a.B * w.heads;
     const int64_t most = units * ((a.max_prefix + BK - 1) / BK + 1);
     const int64_t sms = device_sm_count() > 0 ? device_sm_count() : 1;
