@@ -1,25 +1,27 @@
 // eagle3_verify_attn_fp8 for many query rows (trees): the tcgen05 kernel, and the join of what its CTAs shared.
 //
-// A unit of work is a sequence, a KV head and up to 256 query rows (row = node * rep + head); its keys come in tiles of
-// 128 places, the tree's nodes as one more.  The tiles of all units, one after the other, are cut into equal ranges, one
-// for each CTA (one CTA an SM): ragged lengths, one long sequence and many short ones are all spread evenly, and a unit
-// is cut only where a range ends.  Cut units leave unnormalised partial results, which a second kernel joins in order.
+// A unit of work is a sequence and a KV head; its query rows (row = node * rep + head) are cut into groups of 128, each with
+// a CTA of its own, so that the CTAs of a unit read its keys at about the same time.  Keys come in tiles of 128 places, the
+// tree's nodes as one more.  The tiles of all units, one after the other, are cut into equal ranges, one for each CTA (of a
+// row group; one CTA an SM): ragged lengths, one long sequence and many short ones are all spread evenly, and a unit is
+// cut only where a range ends.  Cut units leave unnormalised partial results, which a second kernel joins in order.
 //
 // S = Q K^T takes K's codes as they lie in memory: Q is held as two e4m3 parts (row scaled to at most 448; hi = e4m3(q),
 // lo = e4m3(q - hi): 4 + 4 bits are bf16's 8), so that QK runs as two e4m3 products, in the time of one of bf16, and K is
-// never converted.  P V runs in fp16: weights in 11 bits (8 bits of bf16, or two e4m3 parts whose floor is 2^-18 of the
-// largest weight, would cost long sums) and V's codes, converted exactly; the scale of V's group is put on the weights,
-// relative to the largest so far, by adding to the exponent.
+// never converted.  The parts stay in tensor memory: read from shared memory for every tile, they would be half of its
+// traffic.  P V runs in fp16: weights in 11 bits (8 bits of bf16, or two e4m3 parts whose floor is 2^-18 of the largest
+// weight, would cost long sums) and V's codes, converted exactly; the scale of V's group is put on the weights, relative to
+// the largest so far, by adding to the exponent.
 //
-// Two streams of (S, P, O) in tensor memory keep the tensor cores busy while the other's softmax runs: with more than
-// 128 rows a stream is a row tile and both take every key tile; with up to 128 the streams take alternate key tiles of
-// the same rows and are added up at the end of the unit.
-//   warp 0        TMA: K tiles into a ring of 3, V codes into a ring of 2
+//   warp 0        TMA: K tiles into a ring of 4, V codes into a ring of 3
 //   warp 1, 2     the MMAs of S, and of P V (one thread issues an MMA about every 110 cycles: two threads)
 //   warp 3        looks ahead: the places and scales of the next 32 tiles, a tile a lane (two dependent loads, which
 //                 whoever needs them would wait for tile by tile)
 //   warps 4..7    V codes to fp16; Q's parts, row scales and ancestor bits of the next unit; the tree's K and V
-//   warps 8..15   softmax of stream 0 and 1, a row a thread; at the end of a unit its results
+//   warps 8..15   softmax, two warps for each quarter of the rows, a row a thread: each takes one of the tile's two groups
+//                 of 64 keys (so one scale), and they exchange the maxima; at the end of a unit its results
+// Tensor memory: O 128 columns, two tiles of S, one of P (fp16 pairs), Q's parts.  S is free for the tile after next once the
+// softmax has loaded it, so that QK runs two tiles ahead.
 // All waits are bounded; one that runs out sets EAGLE3_DEV_TIMEOUT and the CTA drains and exits.
 #include "cache_attn.cuh"
 #include "tc.cuh"
@@ -31,54 +33,52 @@ namespace {
 constexpr int D = 128;
 constexpr int BK = 128;                 // keys of a tile
 constexpr int BT = 64;                  // nodes of the tree's tile
-constexpr int KS = 3, VS = 2, VB = 2;   // stages: K codes, V codes, V in fp16
+constexpr int KS = 4, VS = 3, VB = 3;   // stages: K codes, V codes, V in fp16
 constexpr int AHEAD = 32;               // tiles that warp 3 looks up at once, two such batches
+constexpr int ROWS = 128;               // query rows of a CTA
 constexpr int NT = 512;
 constexpr int LEAST_SHIFT = -60;        // of V's scale on the weights: fp16 has nothing left of them long before
 constexpr uint32_t K_TILE = BK * D, V_TILE = 2 * K_TILE;
-constexpr uint32_t Q_PART = 128 * D;    // a row tile of one part
-constexpr uint32_t OFF_Q = 0;           // [row tile][hi, lo]
-constexpr uint32_t OFF_K = OFF_Q + 4 * Q_PART;
+constexpr uint32_t OFF_K = 0;
 constexpr uint32_t OFF_VR = OFF_K + KS * K_TILE;
 constexpr uint32_t OFF_V = OFF_VR + VS * K_TILE;
 constexpr uint32_t SMEM_DYN = OFF_V + VB * V_TILE + 1024;   // + alignment slack
-constexpr uint32_t TM_O = 0, TM_S = 256;                    // each [stream] * 128 columns
-constexpr int REGS_FEW = 88, REGS_SOFTMAX = 168;            // 2 * 128 * (88 + 168) = 65536 registers
-constexpr int MERGE_WARPS = 8;
+// tensor memory, columns: O; S of two tiles; P; Q's parts, 32 columns each
+constexpr uint32_t TM_O = 0, TM_S = 128, TM_P = 384, TM_Q = 448;
+constexpr int JOIN_WARPS = 8;
 
 struct Smem {
     uint64_t k_full[KS], k_empty[KS], vr_full[VS], vr_empty[VS], v_full[VB], v_empty[VB];
-    uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
+    uint64_t s_full[2], s_empty[2], p_full, pv_done, o_free;
     uint64_t q_full, q_empty;
     uint64_t ahead_full[2], ahead_empty[2];
     uint64_t r_full[2], u_empty[2], tree_full[2];   // by unit parity
     uint64_t c_sync;                             // warps 4..7 among themselves (a wait that ends, unlike bar.sync)
-    uint64_t x_full, x_empty;                    // stream 1's statistics, one row tile only
     uint64_t mma_done[2];
     uint64_t anc[2][64];
-    float qf[2][256];
+    float qf[2][ROWS];
+    float mx[2][2][ROWS];                        // [tile parity][half][row]
+    float l[2][ROWS];                            // [half][row]
     int row[2 * AHEAD][2];                       // of the tile's two groups in the pool's map
     uchar4 scale[2 * AHEAD];                     // K, K, V, V
     int tree_k[2], tree_v[2], odd_v[2];          // the tree's scale bytes; whether a value is not finite
     uint32_t top_k[4], top_v[4];
-    float x_m[128], x_l[128];
-    int x_ev, x_odd;
     long long start_off, range;
     int start_b, start_k;
     uint32_t tmem_base;
     int abort_flag;
 };
 static_assert(SMEM_DYN + sizeof(Smem) <= 232448, "shared memory budget");
+static_assert(KS >= LEAST_STAGES, "the timeout test stalls one of them");
 
 struct Wide {
     CacheAttn a;
-    int tiles2;                     // two row tiles (else one)
-    int rows_per_group, row_groups, heads;   // heads = Hkv * row_groups: units of a sequence
+    int row_groups;
     uint32_t rep_magic;             // row / rep = umulhi(row, magic), 0: rep is 1
     int least;                      // tiles of a range, at least, where there are fewer than CTAs want
     WaitRule wait;
-    // workspace: tiles before each sequence [B + 1], then {total tiles of all units, CTAs that have any}; where each
-    // CTA begins (tile of its first unit); partial results [2 * CTAs][rows_per_group]
+    // workspace: tiles before each sequence's first unit, as tiles of one head [B + 1], then {total tiles of all units,
+    // ranges that have any}; where each range begins (tile of its first unit); partial results [2 * CTAs][ROWS]
     long long *cum;
     int4 *start;
     float *part_o, *part_ml;
@@ -95,12 +95,9 @@ E3_DEV size_t row_at(const Wide &p, int b, int g, int row) {
 E3_DEV int seq_len(const CacheAttn &a, int b) { return max(0, min(__ldg(a.prefix_len + b), a.max_prefix)); }
 E3_DEV int seq_tiles(const CacheAttn &a, int L) { return max(1, (L + BK - 1) / BK + (a.tree_k ? 1 : 0)); }
 
-// Tiles of a stream before the CTA's tile t
-E3_DEV uint32_t stream_tiles(bool two, int m, uint32_t t) { return two ? t : (t + 1u - (uint32_t)m) >> 1; }
-
 // A role's walk over its CTA's range
 struct Walk {
-    int b, k, i0, i1, nt, L, n;     // sequence, unit of the sequence, tiles [i0, i1) of nt, units so far
+    int b, k, i0, i1, nt, L, n;     // sequence, KV head, tiles [i0, i1) of nt, units so far
     long long left;
     E3_DEV bool begin(const Wide &p, const Smem &s, long long range) {
         b = s.start_b;
@@ -118,7 +115,7 @@ struct Walk {
         left -= i1 - i0;
         if (left <= 0) return false;
         ++n;
-        if (++k == p.heads) {
+        if (++k == p.a.Hkv) {
             k = 0;
             ++b;
             L = seq_len(p.a, b);
@@ -260,7 +257,8 @@ __global__ void __launch_bounds__(NT, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t abort = smem_u32(&ss.abort_flag), limit = p.wait.limit;
     const CacheAttn &a = p.a;
-    const bool two = p.tiles2 != 0;
+    const int range_id = blockIdx.x / p.row_groups, row0 = blockIdx.x % p.row_groups * ROWS;   // this CTA's rows
+    const int nrows = min(ROWS, a.N * a.rep - row0);
     auto bar = [](uint64_t &b) { return smem_u32(&b); };
 
     if (tid == 32) {
@@ -278,9 +276,7 @@ __global__ void __launch_bounds__(NT, 1)
         }
         for (int m = 0; m < 2; ++m) {
             tc::mbar_init(&ss.s_full[m], 1);
-            tc::mbar_init(&ss.p_full[m], 4);
-            tc::mbar_init(&ss.pv_done[m], 1);
-            tc::mbar_init(&ss.o_free[m], 4);
+            tc::mbar_init(&ss.s_empty[m], 8);
             tc::mbar_init(&ss.ahead_full[m], 1);
             tc::mbar_init(&ss.ahead_empty[m], 9);   // the loads, eight softmax warps
             tc::mbar_init(&ss.r_full[m], 4);
@@ -288,11 +284,12 @@ __global__ void __launch_bounds__(NT, 1)
             tc::mbar_init(&ss.tree_full[m], 1);
             tc::mbar_init(&ss.mma_done[m], 1);
         }
+        tc::mbar_init(&ss.p_full, 8);
+        tc::mbar_init(&ss.pv_done, 1);
+        tc::mbar_init(&ss.o_free, 8);
         tc::mbar_init(&ss.q_full, 4);
         tc::mbar_init(&ss.q_empty, 1);
         tc::mbar_init(&ss.c_sync, 4);
-        tc::mbar_init(&ss.x_full, 4);
-        tc::mbar_init(&ss.x_empty, 4);
         ss.abort_flag = 0;
         tc::fence_barrier_init();
         tc::prefetch_tmap(&tm_k);
@@ -310,21 +307,21 @@ __global__ void __launch_bounds__(NT, 1)
         for (int b = lane; b < a.B; b += 32) seqs += tiles_at(b);
 #pragma unroll
         for (int d = 16; d; d >>= 1) seqs += __shfl_xor_sync(0xffffffffu, seqs, d);
-        const long long total = seqs * p.heads;
-        // as many CTAs as leave each `least` tiles
-        const long long ctas = max(1ll, min((long long)gridDim.x, total / p.least));
-        const bool first = blockIdx.x == 0, idle = blockIdx.x >= ctas;
-        const long long lo = idle ? total : blockIdx.x * total / ctas, hi = idle ? total : (blockIdx.x + 1) * total / ctas;
+        const long long total = seqs * a.Hkv;
+        // as many ranges as leave each `least` tiles
+        const long long ranges = max(1ll, min((long long)(gridDim.x / p.row_groups), total / p.least));
+        const bool first = blockIdx.x == 0, idle = range_id >= ranges;
+        const long long lo = idle ? total : range_id * total / ranges, hi = idle ? total : (range_id + 1) * total / ranges;
         if (lane == 0) {
             ss.range = hi - lo;
             if (first) {
                 p.cum[a.B] = seqs;
                 p.cum[a.B + 1] = total;
-                p.cum[a.B + 2] = ctas;
+                p.cum[a.B + 2] = ranges;
             }
         }
         long long sum = 0;   // of the sequences before
-        for (int b0 = 0; b0 < a.B && (first || (sum * p.heads <= lo && !idle)); b0 += 32) {
+        for (int b0 = 0; b0 < a.B && (first || (sum * a.Hkv <= lo && !idle)); b0 += 32) {
             const long long mine = tiles_at(b0 + lane);
             long long x = mine;
 #pragma unroll
@@ -334,12 +331,12 @@ __global__ void __launch_bounds__(NT, 1)
             }
             const long long before = sum + x - mine;
             if (first && b0 + lane < a.B) p.cum[b0 + lane] = before;
-            if (mine > 0 && before * p.heads <= lo && lo < (before + mine) * p.heads) {
-                const long long at = lo - before * p.heads;
+            if (mine > 0 && before * a.Hkv <= lo && lo < (before + mine) * a.Hkv) {
+                const long long at = lo - before * a.Hkv;
                 ss.start_b = b0 + lane;
                 ss.start_k = (int)(at / mine);
                 ss.start_off = at % mine;
-                p.start[blockIdx.x] = make_int4(b0 + lane, (int)(at / mine), (int)(at % mine), 0);
+                if (row0 == 0) p.start[range_id] = make_int4(b0 + lane, (int)(at / mine), (int)(at % mine), 0);
             }
             sum += __shfl_sync(0xffffffffu, x, 31);
         }
@@ -350,11 +347,9 @@ __global__ void __launch_bounds__(NT, 1)
     const long long range = ss.range;
     const uint32_t tmem = ss.tmem_base;
 
-    // (each branch gives or takes registers by itself: the compiler allots them by branch)
     Walk w;
     if (warp == 0) {
         // ------------------------------------------------------------------ TMA
-        tc::registers_give<REGS_FEW>();
         if (tc::elect_one()) {
             uint32_t t = 0, tv = 0;
             bool ok = true;
@@ -397,7 +392,6 @@ __global__ void __launch_bounds__(NT, 1)
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------------ S = Q K^T
-        tc::registers_give<REGS_FEW>();
         if (tc::elect_one()) {
             constexpr uint32_t IDESC = tc::idesc_e4m3(128, BK), IDESC_T = tc::idesc_e4m3(128, BT);
             uint32_t t = 0;
@@ -412,32 +406,26 @@ __global__ void __launch_bounds__(NT, 1)
                     }
                     const bool tree = w.is_tree(p, i);
                     const uint32_t kaddr = sm + OFF_K + s * K_TILE;
-                    const int m0 = two ? 0 : (int)(t & 1u), m1 = two ? 2 : m0 + 1;
-                    for (int m = m0; m < m1; ++m) {
-                        // the buffer last held the weights of the stream's tile before
-                        const uint32_t n = stream_tiles(two, m, t);
-                        if (n > 0 && !tc::mbar_wait(bar(ss.pv_done[m]), (n - 1) & 1u, abort, limit)) {
-                            ok = false;
-                            break;
-                        }
-                        tc::fence_after();
-                        const uint32_t d = tmem + TM_S + (uint32_t)(m * 128);
-                        const uint32_t q = sm + OFF_Q + (two ? m : 0) * 2 * Q_PART;
-                        if (!tree) {
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)   // hi, then lo
-                                tc::mma_e4m3_ss(d, tc::desc_sw128(q + (k >> 2) * Q_PART + (k & 3) * 32),
-                                                tc::desc_sw128(kaddr + (k & 3) * 32), IDESC, k > 0 ? 1u : 0u);
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 16; ++k)   // K in two parts too
-                                tc::mma_e4m3_ss(d, tc::desc_sw128(q + ((k >> 2) & 1) * Q_PART + (k & 3) * 32),
-                                                tc::desc_sw128(kaddr + (k >> 3) * (K_TILE / 2) + (k & 3) * 32), IDESC_T,
-                                                k > 0 ? 1u : 0u);
-                        }
-                        tc::mma_commit(bar(ss.s_full[m]));
+                    const int b = (int)(t & 1u);
+                    if (t >= 2 && !tc::mbar_wait(bar(ss.s_empty[b]), ((t - 2) >> 1) & 1u, abort, limit)) {
+                        ok = false;
+                        break;
                     }
-                    if (ok) tc::mma_commit(bar(ss.k_empty[s]));
+                    tc::fence_after();
+                    const uint32_t d = tmem + TM_S + (uint32_t)(b * BK), q = tmem + TM_Q;
+                    if (!tree) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)   // hi, then lo
+                            tc::mma_e4m3_ts(d, q + (uint32_t)(k * 8), tc::desc_sw128(kaddr + (k & 3) * 32), IDESC, k > 0 ? 1u : 0u);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)   // K in two parts too
+                            tc::mma_e4m3_ts(d, q + (uint32_t)((k & 7) * 8),
+                                            tc::desc_sw128(kaddr + (k >> 3) * (K_TILE / 2) + (k & 3) * 32), IDESC_T,
+                                            k > 0 ? 1u : 0u);
+                    }
+                    tc::mma_commit(bar(ss.s_full[b]));
+                    tc::mma_commit(bar(ss.k_empty[s]));
                 }
                 if (ok) tc::mma_commit(bar(ss.q_empty));
             }
@@ -448,7 +436,6 @@ __global__ void __launch_bounds__(NT, 1)
         __syncwarp();
     } else if (warp == 2) {
         // ------------------------------------------------------------------ O += P V
-        tc::registers_give<REGS_FEW>();
         if (tc::elect_one()) {
             constexpr uint32_t IDESC = tc::idesc_f16_bmn(128, D);
             uint32_t t = 0;
@@ -462,26 +449,22 @@ __global__ void __launch_bounds__(NT, 1)
                     }
                     const int ksteps = (w.is_tree(p, i) ? BT : BK) / 16;
                     const uint32_t vaddr = sm + OFF_V + s * V_TILE;
-                    const int m0 = two ? 0 : (int)(t & 1u), m1 = two ? 2 : m0 + 1;
-                    const bool fresh = i - w.i0 < (two ? 1 : 2);   // the stream's first of the unit
-                    for (int m = m0; m < m1; ++m) {
-                        // (a unit's first overwrites O: the one before it must have been read)
-                        if (!tc::mbar_wait(bar(ss.p_full[m]), stream_tiles(two, m, t) & 1u, abort, limit) ||
-                            (fresh && w.n > 0 && !tc::mbar_wait(bar(ss.o_free[m]), (w.n - 1) & 1u, abort, limit))) {
-                            ok = false;
-                            break;
-                        }
-                        tc::fence_after();
-                        const uint32_t t_p = tmem + TM_S + (uint32_t)(m * 128);
-#pragma unroll
-                        for (int kk = 0; kk < BK / 16; ++kk)
-                            if (kk < ksteps)
-                                tc::mma_bf16_ts(tmem + TM_O + (uint32_t)(m * 128), t_p + (uint32_t)(kk * 8),
-                                                tc::desc_mn_sw128(vaddr + kk * 2048, V_TILE / 2, 1024), IDESC,
-                                                !fresh || kk > 0 ? 1u : 0u);
-                        tc::mma_commit(bar(ss.pv_done[m]));
+                    const bool fresh = i == w.i0;
+                    // (a unit's first overwrites O: the one before it must have been read)
+                    if (!tc::mbar_wait(bar(ss.p_full), t & 1u, abort, limit) ||
+                        (fresh && w.n > 0 && !tc::mbar_wait(bar(ss.o_free), (w.n - 1) & 1u, abort, limit))) {
+                        ok = false;
+                        break;
                     }
-                    if (ok) tc::mma_commit(bar(ss.v_empty[s]));
+                    tc::fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < BK / 16; ++kk)
+                        if (kk < ksteps)
+                            tc::mma_bf16_ts(tmem + TM_O, tmem + TM_P + (uint32_t)(kk * 8),
+                                            tc::desc_mn_sw128(vaddr + kk * 2048, V_TILE / 2, 1024), IDESC,
+                                            !fresh || kk > 0 ? 1u : 0u);
+                    tc::mma_commit(bar(ss.pv_done));
+                    tc::mma_commit(bar(ss.v_empty[s]));
                 }
             }
             if (!ok) flag(a.dev_status, EAGLE3_DEV_TIMEOUT);
@@ -491,11 +474,10 @@ __global__ void __launch_bounds__(NT, 1)
         __syncwarp();
     } else if (warp == 3) {
         // ------------------------------------------------------------------ places and scales ahead
-        tc::registers_give<REGS_FEW>();
         bool ok = true;
         uint32_t t = 0;
         for (bool more = w.begin(p, ss, range); more && ok; more = ok && w.next(p)) {
-            const int g = w.k / p.row_groups, sgroups = a.block_size / EAGLE3_KV_GROUP;
+            const int g = w.k, sgroups = a.block_size / EAGLE3_KV_GROUP;
             const int32_t *bt = a.block_table + (size_t)w.b * a.max_blocks;
             for (int i = w.i0; i < w.i1;) {
                 const uint32_t batch = t / AHEAD;
@@ -534,7 +516,6 @@ __global__ void __launch_bounds__(NT, 1)
         if (!ok && lane == 0) flag(a.dev_status, EAGLE3_DEV_TIMEOUT);
     } else if (warp < 8) {
         // ------------------------------------------------------------------ conversions
-        tc::registers_give<REGS_FEW>();
         const int cw = warp - 4;
         uint32_t t = 0, tv = 0, syncs = 0;
         bool ok = true;
@@ -544,33 +525,72 @@ __global__ void __launch_bounds__(NT, 1)
             return tc::mbar_wait_warp(bar(ss.c_sync), syncs++ & 1u, abort, limit);
         };
         for (bool more = w.begin(p, ss, range); more && ok; more = ok && w.next(p)) {
-            const int u = w.n & 1, g = w.k / p.row_groups, row0 = w.k % p.row_groups * p.rows_per_group;
+            const int u = w.n & 1, g = w.k;
             if ((w.n >= 2 && !tc::mbar_wait_warp(bar(ss.u_empty[u]), ((w.n - 2) >> 1) & 1u, abort, limit)) ||
                 (w.n > 0 && !tc::mbar_wait_warp(bar(ss.q_empty), (w.n - 1) & 1u, abort, limit))) {
                 ok = false;
                 break;
             }
             const bool tree = a.tree_k && w.i1 == w.nt;
-            // ---- Q's parts: 16 lanes a row, two rows at a time, eight such pairs on their way
-            const int nrows = min(p.rows_per_group, a.N * a.rep - row0);
-            for (int it = 0; it < p.rows_per_group / 8; it += 8) {
-                uint4 x[8];
+            tc::fence_after();
+            // ---- Q's parts: a row a thread, its 128 dims in registers
+            {
+                const int r = cw * 32 + lane;
+                uint32_t x[64];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int row = (it + j) * 8 + cw * 2 + (lane >> 4);
-                    x[j] = make_uint4(0, 0, 0, 0);
-                    if (row < nrows) x[j] = *reinterpret_cast<const uint4 *>(a.q + row_at(p, w.b, g, row0 + row) + (lane & 15) * 8);
-                }
-                uint32_t top[8];
-                const bool odd = row_maxima<8>(x, top);
+                for (int j = 0; j < 64; ++j) x[j] = 0;
+                if (r < nrows) {
+                    const uint4 *src = reinterpret_cast<const uint4 *>(a.q + row_at(p, w.b, g, row0 + r));
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int row = (it + j) * 8 + cw * 2 + (lane >> 4), byte = scale_byte_bits(top[j]);
-                    store_parts(x[j], inverse_scale(byte), odd, smp + OFF_Q + (row >> 7) * 2 * Q_PART, Q_PART, row & 127, lane & 15);
-                    if ((lane & 15) == 0) ss.qf[u][row] = a.scale_log2 * scale_of(byte);
+                    for (int j = 0; j < 16; ++j) {
+                        const uint4 v = src[j];
+                        x[4 * j] = v.x, x[4 * j + 1] = v.y, x[4 * j + 2] = v.z, x[4 * j + 3] = v.w;
+                    }
                 }
+                uint32_t top4[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int j = 0; j < 64; ++j) top4[j & 3] = max_u16x2(top4[j & 3], x[j] & 0x7fff7fffu);
+                const uint32_t top2 = max_u16x2(max_u16x2(top4[0], top4[1]), max_u16x2(top4[2], top4[3]));
+                uint32_t top = max(top2 & 0xffffu, top2 >> 16);
+                const bool odd = top >= BF16_INF;   // something is not finite: the largest of the others, and NaN
+                if (odd) {
+                    top = 0;
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) {
+                        const uint32_t lo = x[j] & 0x7fffu, hi = (x[j] >> 16) & 0x7fffu;
+                        top = max(top, max(lo < BF16_INF ? lo : 0u, hi < BF16_INF ? hi : 0u));
+                    }
+                }
+                const int byte = scale_byte_bits(top);
+                const float up = inverse_scale(byte);
+                // words 4 j .. 4 j + 3 (8 dims) become two words of each part
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    float v[8];
+                    bf16x8(make_uint4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]), v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] *= up;
+                    if (odd) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] = fabsf(v[e]) <= FLT_MAX ? v[e] : __int_as_float(0x7fc00000);
+                    }
+                    uint2 hi, lo;
+                    two_parts(v, hi, lo);
+                    x[4 * j] = hi.x, x[4 * j + 1] = hi.y, x[4 * j + 2] = lo.x, x[4 * j + 3] = lo.y;
+                }
+                const uint32_t tq = tmem + ((uint32_t)(cw * 32) << 16) + TM_Q;
+                uint32_t part[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) part[j] = x[4 * (j >> 1) + (j & 1)];
+                __syncwarp();
+                tc::tmem_st32u_start(tq, part);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) part[j] = x[4 * (j >> 1) + 2 + (j & 1)];
+                tc::tmem_st32u_start(tq + 32u, part);
+                tc::tmem_st_wait();
+                ss.qf[u][r] = a.scale_log2 * scale_of(byte);
+                tc::fence_before();
             }
-            tc::fence_proxy_async_smem();
             if (cw == 0) {
                 if (tree) tree_paths(a, w.b, w.k == 0, lane, ss.anc[u]);
                 const int L = __ldg(a.prefix_len + w.b);
@@ -585,10 +605,8 @@ __global__ void __launch_bounds__(NT, 1)
             {
                 Walk nx = w;
                 if (nx.next(p)) {
-                    const int ng = nx.k / p.row_groups, nrow0 = nx.k % p.row_groups * p.rows_per_group;
-                    const int rows_next = min(p.rows_per_group, a.N * a.rep - nrow0);
-                    for (int row = cw * 32 + lane; row < rows_next; row += 128)
-                        tc::prefetch_l2(a.q + row_at(p, nx.b, ng, nrow0 + row), 2 * D);
+                    const int row = cw * 32 + lane;
+                    if (row < nrows) tc::prefetch_l2(a.q + row_at(p, nx.b, nx.k, row0 + row), 2 * D);
                 }
                 if (tree && cw < 2)
                     for (int i = lane; i < a.N; i += 32)
@@ -677,16 +695,16 @@ __global__ void __launch_bounds__(NT, 1)
                 const uint8_t *src = smp + OFF_VR + sv * K_TILE;
                 const int c = lane & 7;
 #pragma unroll
-                for (int it = 0; it < 8; it += 4) {
-                    uint4 x[4];
+                for (int it = 0; it < 8; it += 8) {
+                    uint4 x[8];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
+                    for (int j = 0; j < 8; ++j) {
                         const int key = cw * 32 + (it + j) * 4 + (lane >> 3);
                         x[j] = *reinterpret_cast<const uint4 *>(src + key * 128 + (((uint32_t)c ^ ((uint32_t)key & 7u)) << 4));
                         if (i * BK + key >= w.L) x[j] = make_uint4(0, 0, 0, 0);   // whatever lies behind the last key
                     }
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
+                    for (int j = 0; j < 8; ++j) {
                         const int key = cw * 32 + (it + j) * 4 + (lane >> 3);
                         const uint4 lo = make_uint4(e4m3x2_f16(x[j].x), e4m3x2_f16(x[j].x >> 16), e4m3x2_f16(x[j].y),
                                                     e4m3x2_f16(x[j].y >> 16));
@@ -714,82 +732,66 @@ __global__ void __launch_bounds__(NT, 1)
         if (!ok && lane == 0) flag(a.dev_status, EAGLE3_DEV_TIMEOUT);
     } else {
         // ------------------------------------------------------------------ softmax and results
-        tc::registers_take<REGS_SOFTMAX>();
-        const int m = (warp - 8) >> 2, r = (warp & 3) * 32 + lane;   // stream, TMEM lane
-        const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t t_s = t_lane + TM_S + (uint32_t)(m * 128), t_o = t_lane + TM_O + (uint32_t)(m * 128);
+        // (no way out of the loops: the two warps of a quarter meet at a barrier for every tile; after a wait that ran
+        // out they go on without waiting)
+        const int quarter = warp & 3, half = (warp - 8) >> 2, r = quarter * 32 + lane;
+        const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
+        auto pair_sync = [&] { asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory"); };
         uint32_t t = 0;
         bool ok = true;
-        for (bool more = w.begin(p, ss, range); more && ok; more = ok && w.next(p)) {
-            const int u = w.n & 1, g = w.k / p.row_groups, row0 = w.k % p.row_groups * p.rows_per_group;
-            const int row = two ? m * 128 + r : r, nrows = min(p.rows_per_group, a.N * a.rep - row0);
-            if (!tc::mbar_wait_warp(bar(ss.r_full[u]), (w.n >> 1) & 1u, abort, limit)) {
-                ok = false;
-                break;
-            }
-            const float fr = ss.qf[u][row];
+        auto wait = [&](uint64_t &b, uint32_t parity) { ok = ok && tc::mbar_wait_warp(bar(b), parity & 1u, abort, limit); };
+        for (bool more = w.begin(p, ss, range); more; more = w.next(p)) {
+            const int u = w.n & 1, g = w.k;
+            wait(ss.r_full[u], w.n >> 1);
+            const float fr = ss.qf[u][r];
             float m_run = -INFINITY, l_run = 0.0f;
             int evref = 0;                     // V's scale byte that O is relative to: the largest so far
-            bool fresh = true, odd_v = false;
+            bool odd_v = false;
             for (int i = w.i0; i < w.i1; ++i, ++t) {
                 const uint32_t batch = t / AHEAD;
-                if (t % AHEAD == 0 && !tc::mbar_wait_warp(bar(ss.ahead_full[batch & 1]), (batch >> 1) & 1u, abort, limit)) {
-                    ok = false;
-                    break;
-                }
+                if (t % AHEAD == 0) wait(ss.ahead_full[batch & 1], batch >> 1);
                 uchar4 sb = ss.scale[t % (2 * AHEAD)];
                 if (t % AHEAD == AHEAD - 1) {
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(bar(ss.ahead_empty[batch & 1]));
                 }
-                if (!two && (int)(t & 1u) != m) continue;
                 const bool tree = w.is_tree(p, i);
                 if (tree) {
-                    if (!tc::mbar_wait_warp(bar(ss.tree_full[u]), (w.n >> 1) & 1u, abort, limit)) {
-                        ok = false;
-                        break;
-                    }
+                    wait(ss.tree_full[u], w.n >> 1);
                     sb = make_uchar4(ss.tree_k[u], ss.tree_k[u], ss.tree_v[u], ss.tree_v[u]);
                     odd_v = ss.odd_v[u] != 0;
                 }
-                if (!tc::mbar_wait_warp(bar(ss.s_full[m]), stream_tiles(two, m, t) & 1u, abort, limit)) {
-                    ok = false;
-                    break;
-                }
+                wait(ss.s_full[t & 1], t >> 1);
                 tc::fence_after();
-                float sc[128];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) tc::tmem_ld32_start(t_s + 32u * q, sc + 32 * q);
+                const uint32_t t_s = t_lane + TM_S + (t & 1) * BK + half * 64;
+                float sc[64];
+                tc::tmem_ld32_start(t_s, sc);
+                tc::tmem_ld32_start(t_s + 32u, sc + 32);
                 // (a factor that underflows would make NaN of the masked scores; a NaN stays)
-                float f0 = fr * scale_of(sb.x), f1 = fr * scale_of(sb.y);
-                f0 = f0 < FLT_MIN ? FLT_MIN : f0;
-                f1 = f1 < FLT_MIN ? FLT_MIN : f1;
-                const int keys = tree ? -1 : min(BK, w.L - i * BK);
+                float f = fr * scale_of(half ? sb.y : sb.x);
+                f = f < FLT_MIN ? FLT_MIN : f;
+                const int keys = tree ? -1 : w.L - i * BK - 64 * half;   // of this half, 64 or more: all
+                tc::tmem_ld32_wait(sc);
+                tc::tmem_ld32_wait(sc + 32);
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(bar(ss.s_empty[t & 1]));
+                if (tree || keys < 64) {
+                    uint64_t vis = keys > 0 ? (1ull << keys) - 1ull : 0ull;
+                    if (tree) vis = half == 0 && r < nrows ? ss.anc[u][row_node(p, row0 + r)] : 0ull;
+                    const uint32_t v0 = (uint32_t)vis, v1 = (uint32_t)(vis >> 32);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) tc::tmem_ld32_wait(sc + 32 * q);
-                if (keys < BK) {
-                    uint64_t anc = 0;
-                    if (tree && row < nrows) anc = ss.anc[u][row_node(p, row0 + row)];
-                    uint32_t vis[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int n = keys - 32 * q;
-                        vis[q] = keys < 0 ? (q < 2 ? (uint32_t)(anc >> (32 * (q & 1))) : 0u)
-                                          : n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 128; ++e) sc[e] = (vis[e >> 5] >> (e & 31)) & 1u ? sc[e] : -INFINITY;
+                    for (int e = 0; e < 64; ++e) sc[e] = ((e < 32 ? v0 : v1) >> (e & 31)) & 1u ? sc[e] : -INFINITY;
                 }
-                float mq[2][4];
+                float mq[4];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int e = 0; e < 4; ++e) mq[e] = max3(sc[3 * e], sc[3 * e + 1], sc[3 * e + 2]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) mq[h][e] = max3(sc[64 * h + 3 * e], sc[64 * h + 3 * e + 1], sc[64 * h + 3 * e + 2]);
-#pragma unroll
-                    for (int e = 12; e < 64; e += 2) mq[h][(e >> 1) & 3] = max3(mq[h][(e >> 1) & 3], sc[64 * h + e], sc[64 * h + e + 1]);
-                }
-                const float mx = fmaxf(max3(fmaxf(mq[0][0], mq[0][1]), mq[0][2], mq[0][3]) * f0,
-                                       max3(fmaxf(mq[1][0], mq[1][1]), mq[1][2], mq[1][3]) * f1);
+                for (int e = 12; e < 64; e += 2) mq[(e >> 1) & 3] = max3(mq[(e >> 1) & 3], sc[e], sc[e + 1]);
+                float mx = max3(fmaxf(mq[0], mq[1]), mq[2], mq[3]) * f;
+                ss.mx[t & 1][half][r] = mx;
+                pair_sync();
+                mx = fmaxf(mx, ss.mx[t & 1][half ^ 1][r]);
                 const bool need = mx > m_run + RESCALE_LOG2;
                 const int ev = max(sb.z == 255 ? 0 : sb.z, sb.w == 255 ? 0 : sb.w);
                 const bool moved = __any_sync(0xffffffffu, need || ev > evref);
@@ -804,115 +806,69 @@ __global__ void __launch_bounds__(NT, 1)
                         evref = ev;
                     }
                 }
-                const float nm = m_run == -INFINITY ? 0.0f : WEIGHT_LOG2 - m_run;
+                // the weights by V's scale: 2^down of them; their sum without it
+                const int vb = half ? sb.w : sb.z, down = max(LEAST_SHIFT, vb - evref);
+                const float nm = vb == 255 ? __int_as_float(0x7fc00000)
+                                           : (m_run == -INFINITY ? 0.0f : WEIGHT_LOG2 - m_run) + (float)down;
+                const float2 f2 = make_float2(f, f), nm2 = make_float2(nm, nm);
+                float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+                uint32_t pk[32];
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    // the weights by V's scale: 2^down of them; their sum without it
-                    const int vb = q ? sb.w : sb.z, down = max(LEAST_SHIFT, vb - evref);
-                    const float f = q ? f1 : f0, n = vb == 255 ? __int_as_float(0x7fc00000) : nm + (float)down;
-                    const float2 f2 = make_float2(f, f), nm2 = make_float2(n, n);
-                    float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
-                    uint32_t pk[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const float2 x = __ffma2_rn(make_float2(sc[64 * q + 2 * e], sc[64 * q + 2 * e + 1]), f2, nm2);
-                        const float2 y = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-                        sum[e & 1] = __fadd2_rn(sum[e & 1], y);
-                        pk[e] = pack_f16(y.x, y.y);
-                    }
-                    const float2 s2 = __fadd2_rn(sum[0], sum[1]);
-                    l_run += (s2.x + s2.y) * exp2_int(-down);
-                    tc::tmem_st32u_start(t_s + 32u * q, pk);
+                for (int e = 0; e < 32; ++e) {
+                    const float2 x = __ffma2_rn(make_float2(sc[2 * e], sc[2 * e + 1]), f2, nm2);
+                    const float2 y = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                    sum[e & 1] = __fadd2_rn(sum[e & 1], y);
+                    pk[e] = pack_f16(y.x, y.y);
                 }
-                tc::tmem_st_wait();
-                // O (now that the scores' registers are free; P V of the tile before is done, since S waited for it)
-                if (moved && !fresh) {
+                const float2 s2 = __fadd2_rn(sum[0], sum[1]);
+                l_run += (s2.x + s2.y) * exp2_int(-down);
+                // P, and O: once the tile before has been multiplied
+                if (t > 0) {
+                    wait(ss.pv_done, t - 1);
+                    tc::fence_after();
+                }
+                if (!tree || half == 0) tc::tmem_st32u_start(t_lane + TM_P + half * 32u, pk);
+                if (moved && i > w.i0) {
 #pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
+                    for (int q = 0; q < 2; ++q) {
                         float o[32];
-                        tc::tmem_ld32(t_o + 32u * q, o);
+                        const uint32_t t_o = t_lane + TM_O + half * 64u + 32u * q;
+                        tc::tmem_ld32(t_o, o);
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] *= corr;
-                        tc::tmem_st32(t_o + 32u * q, o);
+                        tc::tmem_st32(t_o, o);
                     }
                 }
-                fresh = false;
+                tc::tmem_st_wait();
                 tc::fence_before();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(bar(ss.p_full[m]));
+                if (lane == 0) tc::mbar_arrive(bar(ss.p_full));
             }
-            if (!ok) break;
-            // ---- the unit's results
-            float e0 = scale_of(evref), e1 = 0.0f, M = m_run, l = l_run;   // factors of the streams' sums
-            if (!two) {
-                if (m == 1) {
-                    if (w.n > 0 && !tc::mbar_wait_warp(bar(ss.x_empty), (w.n - 1) & 1u, abort, limit)) {
-                        ok = false;
-                        break;
-                    }
-                    ss.x_m[r] = m_run;
-                    ss.x_l[r] = l_run;
-                    if (r == 0) {
-                        ss.x_ev = evref;
-                        ss.x_odd = odd_v ? 1 : 0;
-                    }
-                    __syncwarp();
-                    if (lane == 0) {
-                        tc::mbar_arrive(bar(ss.x_full));
-                        tc::mbar_arrive(bar(ss.u_empty[u]));
-                    }
-                    continue;
-                }
-                if (!tc::mbar_wait_warp(bar(ss.x_full), w.n & 1u, abort, limit)) {
-                    ok = false;
-                    break;
-                }
-                const float m2 = ss.x_m[r], l2 = ss.x_l[r], v2 = scale_of(ss.x_ev);
-                odd_v = odd_v || ss.x_odd != 0;
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(bar(ss.x_empty));
-                M = fmaxf(m_run, m2);
-                const float a0 = weight_of(m_run, l_run, M), a1 = weight_of(m2, l2, M);
-                l = a0 * l_run + a1 * l2;
-                e0 *= a0;
-                e1 = v2 * a1;
-                const uint32_t n1 = stream_tiles(false, 1, t);
-                if (n1 > 0 && !tc::mbar_wait_warp(bar(ss.pv_done[1]), (n1 - 1) & 1u, abort, limit)) {
-                    ok = false;
-                    break;
-                }
-            }
-            const uint32_t done = stream_tiles(two, m, t);
-            if (done > 0 && !tc::mbar_wait_warp(bar(ss.pv_done[m]), (done - 1) & 1u, abort, limit)) {
-                ok = false;
-                break;
-            }
+            // ---- the unit's results: this half's columns
+            ss.l[half][r] = l_run;
+            pair_sync();
+            const float l = ss.l[0][r] + ss.l[1][r];
+            wait(ss.pv_done, t - 1);
             tc::fence_after();
-            const bool whole = w.i0 == 0 && w.i1 == w.nt;
-            const bool mine = row < nrows;
-            const int node = row_node(p, row0 + row), head = g * a.rep + row0 + row - node * a.rep;
+            const bool whole = w.i0 == 0 && w.i1 == w.nt, mine = r < nrows;
+            const int node = row_node(p, row0 + r), head = g * a.rep + row0 + r - node * a.rep;
             const size_t at = ((size_t)w.b * a.N + (mine ? node : 0)) * a.Hq + (mine ? head : 0);
-            const size_t part = (size_t)(2 * blockIdx.x + (w.n > 0 ? 1 : 0)) * p.rows_per_group + row;
+            const size_t part = (size_t)(2 * blockIdx.x + (w.n > 0 ? 1 : 0)) * ROWS + r;
             const uint64_t anc = odd_v && mine ? ss.anc[u][node] : 0;
-            const float inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
-            const bool has0 = l_run != 0.0f && e0 != 0.0f, has1 = e1 != 0.0f;   // (a stream without a key has summed up nothing)
+            // (a row without a key has summed up nothing)
+            const float back = scale_of(evref), inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
 #pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 2; ++q) {
                 float o[32];
-                tc::tmem_ld32(t_lane + TM_O + 32u * q + (two ? m * 128u : 0u), o);   // warp-collective
+                const int c0 = half * 64 + 32 * q;
+                tc::tmem_ld32(t_lane + TM_O + (uint32_t)c0, o);   // warp-collective
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = has0 ? o[e] * e0 : 0.0f;
-                if (!two) {
-                    float o2[32];
-                    tc::tmem_ld32(t_lane + TM_O + 128u + 32u * q, o2);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = has1 ? o[e] + o2[e] * e1 : o[e];
-                }
+                for (int e = 0; e < 32; ++e) o[e] = l != 0.0f ? o[e] * back : 0.0f;
                 // infinities and NaN of the tree's values, to the rows that see them
                 if (odd_v && mine) {
                     for (int j = 0; j < a.N; ++j) {
                         if (!(anc >> j & 1ull)) continue;
-                        const __nv_bfloat16 *tv = a.tree_v + ((size_t)w.b * a.N + j) * a.kv_ns + (size_t)g * D + 32 * q;
+                        const __nv_bfloat16 *tv = a.tree_v + ((size_t)w.b * a.N + j) * a.kv_ns + (size_t)g * D + c0;
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
                             const float x = (float)tv[e];
@@ -922,7 +878,7 @@ __global__ void __launch_bounds__(NT, 1)
                 }
                 if (!mine) continue;
                 if (whole) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(a.out + at * D + 32 * q);
+                    uint4 *dst = reinterpret_cast<uint4 *>(a.out + at * D + c0);
 #pragma unroll
                     for (int c8 = 0; c8 < 4; ++c8) {
                         uint32_t x[4];
@@ -934,7 +890,7 @@ __global__ void __launch_bounds__(NT, 1)
                         dst[c8] = make_uint4(x[0], x[1], x[2], x[3]);
                     }
                 } else {
-                    float4 *dst = reinterpret_cast<float4 *>(p.part_o + part * D + 32 * q);
+                    float4 *dst = reinterpret_cast<float4 *>(p.part_o + part * D + c0);
 #pragma unroll
                     for (int c4 = 0; c4 < 8; ++c4) dst[c4] = make_float4(o[4 * c4], o[4 * c4 + 1], o[4 * c4 + 2], o[4 * c4 + 3]);
                 }
@@ -942,17 +898,17 @@ __global__ void __launch_bounds__(NT, 1)
             tc::fence_before();
             __syncwarp();
             if (lane == 0) {
-                tc::mbar_arrive(bar(ss.o_free[m]));
-                if (!two) tc::mbar_arrive(bar(ss.o_free[1]));
+                tc::mbar_arrive(bar(ss.o_free));
                 tc::mbar_arrive(bar(ss.u_empty[u]));
             }
-            if (mine) {
+            if (mine && half == 0) {
                 if (whole) {
-                    if (a.lse) a.lse[at] = lse_of(M, l);
+                    if (a.lse) a.lse[at] = lse_of(m_run, l);
                 } else {
-                    *reinterpret_cast<float2 *>(p.part_ml + 2 * part) = make_float2(M, l);
+                    *reinterpret_cast<float2 *>(p.part_ml + 2 * part) = make_float2(m_run, l);
                 }
             }
+            pair_sync();   // (the sums are read before the next unit's are written)
         }
         if (!ok && lane == 0) flag(a.dev_status, EAGLE3_DEV_TIMEOUT);
     }
@@ -966,28 +922,29 @@ __global__ void __launch_bounds__(NT, 1)
     }
 }
 
-// Joins the units that were cut, in the order of their CTAs: grid (CTA whose range begins inside a unit, rows).
-__global__ void __launch_bounds__(MERGE_WARPS * 32) cache_attn_join_kernel(const __grid_constant__ Wide p) {
+// Joins the units that were cut, in the order of their ranges: grid (range that begins inside a unit, row group, rows).
+__global__ void __launch_bounds__(JOIN_WARPS * 32) cache_attn_join_kernel(const __grid_constant__ Wide p) {
     pdl_wait();
     pdl_trigger();
     const CacheAttn &a = p.a;
-    const long long total = p.cum[a.B + 1], ctas = p.cum[a.B + 2];
+    const long long total = p.cum[a.B + 1], ranges = p.cum[a.B + 2];
     const long long c = blockIdx.x + 1;
-    if (c >= ctas) return;
+    if (c >= ranges) return;
     const int4 st = p.start[c];
     if (st.z == 0) return;                              // begins with a unit
     const long long before = p.cum[st.x], nt = p.cum[st.x + 1] - before;
-    const long long u0 = before * p.heads + st.y * nt;
-    auto owner = [&](long long x) { return ((x + 1) * ctas - 1) / total; };
+    const long long u0 = before * a.Hkv + st.y * nt;
+    auto owner = [&](long long x) { return ((x + 1) * ranges - 1) / total; };
     const long long first = owner(u0), last = owner(u0 + nt - 1);
     if (first != c - 1) return;                         // not the unit's first cut
-    // the first CTA's share: its second slot, unless its range begins with this unit
+    // the first range's share: the second slot of its CTA, unless it begins with this unit
     const int4 s1 = p.start[first];
-    const long long slot0 = 2 * first + (s1.x == st.x && s1.y == st.y ? 0 : 1);
-    const int g = st.y / p.row_groups, row0 = st.y % p.row_groups * p.rows_per_group;
-    const int nrows = min(p.rows_per_group, a.N * a.rep - row0), lane = threadIdx.x & 31;
-    for (int row = blockIdx.y * MERGE_WARPS + (threadIdx.x >> 5); row < nrows; row += gridDim.y * MERGE_WARPS) {
-        auto slot = [&](long long q) { return (size_t)(q == first ? slot0 : 2 * q) * p.rows_per_group + row; };
+    const int second = s1.x == st.x && s1.y == st.y ? 0 : 1;
+    const int g = st.y, row0 = blockIdx.y * ROWS, nrows = min(ROWS, a.N * a.rep - row0), lane = threadIdx.x & 31;
+    for (int row = blockIdx.z * JOIN_WARPS + (threadIdx.x >> 5); row < nrows; row += gridDim.z * JOIN_WARPS) {
+        auto slot = [&](long long q) {
+            return (size_t)(2 * (q * p.row_groups + blockIdx.y) + (q == first ? second : 0)) * ROWS + row;
+        };
         float M = -INFINITY, l = 0.0f;
         for (long long q = first; q <= last; ++q) M = fmaxf(M, p.part_ml[2 * slot(q)]);
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -1005,7 +962,7 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) cache_attn_join_kernel(const
 
 struct Plan {
     Wide w;
-    int ctas;
+    int ranges;
     size_t o_start, o_part, o_ml, bytes;
 };
 
@@ -1014,20 +971,16 @@ Plan plan(const CacheAttn &a, int requested) {
     Wide &w = pl.w;
     w = Wide();
     w.a = a;
-    const int rows = a.N * a.rep;
-    w.tiles2 = rows > 128;
-    w.rows_per_group = w.tiles2 ? 256 : 128;
-    w.row_groups = (rows + w.rows_per_group - 1) / w.rows_per_group;
-    w.heads = a.Hkv * w.row_groups;
+    w.row_groups = (a.N * a.rep + ROWS - 1) / ROWS;
     w.rep_magic = a.rep == 1 ? 0u : (uint32_t)(((1ull << 32) + a.rep - 1) / a.rep);
-    const int64_t units = (int64_t)a.B * w.heads;
-    const int64_t most = units * ((a.max_prefix + BK - 1) / BK + 1);
-    const int64_t sms = device_sm_count() > 0 ? device_sm_count() : 1;
-    int64_t ctas = requested > 0 ? units * requested : sms;
-    if (ctas > most) ctas = most;
-    if (ctas > 4 * 65535) ctas = 4 * 65535;
+    const int64_t units = (int64_t)a.B * a.Hkv, most = units * ((a.max_prefix + BK - 1) / BK + 1);
+    int64_t ranges = requested > 0 ? units * requested : device_sm_count() / w.row_groups;
+    if (ranges > most) ranges = most;
+    if (ranges * w.row_groups > 4 * 65535) ranges = 4 * 65535 / w.row_groups;
+    if (ranges < 1) ranges = 1;
     w.least = requested > 0 ? 1 : 2;
-    pl.ctas = (int)ctas;
+    pl.ranges = (int)ranges;
+    const size_t ctas = (size_t)ranges * w.row_groups;
     size_t at = 256;
     auto take = [&](size_t n) {
         const size_t o = at;
@@ -1035,9 +988,9 @@ Plan plan(const CacheAttn &a, int requested) {
         return o;
     };
     take(((size_t)a.B + 3) * sizeof(long long));
-    pl.o_start = take((size_t)ctas * sizeof(int4));
-    pl.o_part = take((size_t)ctas * 2 * w.rows_per_group * D * sizeof(float));
-    pl.o_ml = take((size_t)ctas * 2 * w.rows_per_group * 2 * sizeof(float));
+    pl.o_start = take((size_t)ranges * sizeof(int4));
+    pl.o_part = take(ctas * 2 * ROWS * D * sizeof(float));
+    pl.o_ml = take(ctas * 2 * ROWS * 2 * sizeof(float));
     pl.bytes = at;
     return pl;
 }
@@ -1066,10 +1019,10 @@ eagle3_status_t cache_attn_wide(const CacheAttn &a, int requested, const WaitRul
             return cudaFuncSetAttribute(cache_attn_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_DYN);
         }) != cudaSuccess)
         return EAGLE3_ERR_CUDA;
-    if (launch_pdl(cache_attn_wide_kernel, dim3((unsigned)pl.ctas), dim3(NT), SMEM_DYN, stream, tk, tv, pl.w) != cudaSuccess)
+    if (launch_pdl(cache_attn_wide_kernel, dim3((unsigned)(pl.ranges * pl.w.row_groups)), dim3(NT), SMEM_DYN, stream, tk, tv, pl.w) != cudaSuccess)
         return EAGLE3_ERR_CUDA;
-    if (pl.ctas > 1 && launch_pdl(cache_attn_join_kernel, dim3((unsigned)(pl.ctas - 1), 8), dim3(MERGE_WARPS * 32), 0, stream,
-                                  pl.w) != cudaSuccess)
+    if (pl.ranges > 1 && launch_pdl(cache_attn_join_kernel, dim3((unsigned)(pl.ranges - 1), (unsigned)pl.w.row_groups, 4),
+                                    dim3(JOIN_WARPS * 32), 0, stream, pl.w) != cudaSuccess)
         return EAGLE3_ERR_CUDA;
     return EAGLE3_OK;
 }
