@@ -179,7 +179,7 @@ E3_DEV bool row_maxima(const uint4 (&x)[N], uint32_t (&top)[N]) {
         all = max(all, top[j]);
     }
     const bool odd = __any_sync(0xffffffffu, all >= BF16_INF);
-    if (odd) {
+    if (__builtin_expect(odd, 0)) {
 #pragma unroll
         for (int j = 0; j < N; ++j) top[j] = amax_bits_finite(x[j]);
     }
@@ -245,6 +245,21 @@ E3_DEV float max3(float a, float b, float c) {
 
 E3_DEV float weight_of(float m, float l, float M) {
     return l == 0.0f ? 0.0f : m == -INFINITY ? 1.0f : fast_exp2(m - M);
+}
+
+// Rare paths are marked as such, so that the code of the loops is short: all roles' loops together have to stay in the
+// SM's instruction cache.
+#define RARELY(x) __builtin_expect(!!(x), 0)
+
+E3_DEV bool wait_warp(uint32_t bar, uint32_t parity, uint32_t abort, uint32_t limit) {
+    bool ok = true;
+    if (RARELY(!__all_sync(0xffffffffu, tc::mbar_try(bar, parity)))) ok = tc::mbar_wait_warp(bar, parity, abort, limit);
+    return ok;
+}
+E3_DEV bool wait_one(uint32_t bar, uint32_t parity, uint32_t abort, uint32_t limit) {
+    bool ok = true;
+    if (RARELY(!tc::mbar_try(bar, parity))) ok = tc::mbar_wait(bar, parity, abort, limit);
+    return ok;
 }
 
 __global__ void __launch_bounds__(NT, 1)
@@ -355,7 +370,7 @@ __global__ void __launch_bounds__(NT, 1)
             bool ok = true;
             for (bool more = w.begin(p, ss, range); more && ok; more = ok && w.next(p)) {
                 for (int i = w.i0; i < w.i1 && ok; ++i, ++t) {
-                    if (t % AHEAD == 0 && !tc::mbar_wait(bar(ss.ahead_full[t / AHEAD & 1]), t / (2 * AHEAD) & 1u, abort, limit)) {
+                    if (t % AHEAD == 0 && !wait_one(bar(ss.ahead_full[t / AHEAD & 1]), t / (2 * AHEAD) & 1u, abort, limit)) {
                         ok = false;
                         break;
                     }
@@ -363,7 +378,7 @@ __global__ void __launch_bounds__(NT, 1)
                     const int r0 = ss.row[t % (2 * AHEAD)][0], r1 = ss.row[t % (2 * AHEAD)][1];
                     if (t % AHEAD == AHEAD - 1) tc::mbar_arrive(bar(ss.ahead_empty[t / AHEAD & 1]));
                     if (w.is_tree(p, i)) continue;   // (warps 4..7 fill that stage)
-                    if (!tc::mbar_wait(bar(ss.k_empty[s]), ((t / KS) & 1u) ^ 1u, abort, limit)) {
+                    if (!wait_one(bar(ss.k_empty[s]), ((t / KS) & 1u) ^ 1u, abort, limit)) {
                         ok = false;
                         break;
                     }
@@ -371,7 +386,7 @@ __global__ void __launch_bounds__(NT, 1)
                     const uint32_t dst = sm + OFF_K + s * K_TILE, dv = sm + OFF_VR + sv * K_TILE;
                     tc::tma_load_2d(dst, &tm_k, 0, r0, bar(ss.k_full[s]));
                     tc::tma_load_2d(dst + K_TILE / 2, &tm_k, 0, r1, bar(ss.k_full[s]));
-                    if (!tc::mbar_wait(bar(ss.vr_empty[sv]), ((tv / VS) & 1u) ^ 1u, abort, limit)) {
+                    if (!wait_one(bar(ss.vr_empty[sv]), ((tv / VS) & 1u) ^ 1u, abort, limit)) {
                         ok = false;
                         ++t;
                         break;
@@ -397,23 +412,23 @@ __global__ void __launch_bounds__(NT, 1)
             uint32_t t = 0;
             bool ok = true;
             for (bool more = w.begin(p, ss, range); more && ok; more = ok && w.next(p)) {
-                ok = tc::mbar_wait(bar(ss.q_full), w.n & 1u, abort, limit);
+                ok = wait_one(bar(ss.q_full), w.n & 1u, abort, limit);
                 for (int i = w.i0; i < w.i1 && ok; ++i, ++t) {
                     const int s = (int)(t % KS);
-                    if (!tc::mbar_wait(bar(ss.k_full[s]), (t / KS) & 1u, abort, limit)) {
+                    if (!wait_one(bar(ss.k_full[s]), (t / KS) & 1u, abort, limit)) {
                         ok = false;
                         break;
                     }
                     const bool tree = w.is_tree(p, i);
                     const uint32_t kaddr = sm + OFF_K + s * K_TILE;
                     const int b = (int)(t & 1u);
-                    if (t >= 2 && !tc::mbar_wait(bar(ss.s_empty[b]), ((t - 2) >> 1) & 1u, abort, limit)) {
+                    if (t >= 2 && !wait_one(bar(ss.s_empty[b]), ((t - 2) >> 1) & 1u, abort, limit)) {
                         ok = false;
                         break;
                     }
                     tc::fence_after();
                     const uint32_t d = tmem + TM_S + (uint32_t)(b * BK), q = tmem + TM_Q;
-                    if (!tree) {
+                    if (!RARELY(tree)) {
 #pragma unroll
                         for (int k = 0; k < 8; ++k)   // hi, then lo
                             tc::mma_e4m3_ts(d, q + (uint32_t)(k * 8), tc::desc_sw128(kaddr + (k & 3) * 32), IDESC, k > 0 ? 1u : 0u);
@@ -443,23 +458,23 @@ __global__ void __launch_bounds__(NT, 1)
             for (bool more = w.begin(p, ss, range); more && ok; more = ok && w.next(p)) {
                 for (int i = w.i0; i < w.i1 && ok; ++i, ++t) {
                     const int s = (int)(t % VB);
-                    if (!tc::mbar_wait(bar(ss.v_full[s]), (t / VB) & 1u, abort, limit)) {
+                    if (!wait_one(bar(ss.v_full[s]), (t / VB) & 1u, abort, limit)) {
                         ok = false;
                         break;
                     }
-                    const int ksteps = (w.is_tree(p, i) ? BT : BK) / 16;
+                    const bool tree = w.is_tree(p, i);
                     const uint32_t vaddr = sm + OFF_V + s * V_TILE;
                     const bool fresh = i == w.i0;
                     // (a unit's first overwrites O: the one before it must have been read)
-                    if (!tc::mbar_wait(bar(ss.p_full), t & 1u, abort, limit) ||
-                        (fresh && w.n > 0 && !tc::mbar_wait(bar(ss.o_free), (w.n - 1) & 1u, abort, limit))) {
+                    if (!wait_one(bar(ss.p_full), t & 1u, abort, limit) ||
+                        (fresh && w.n > 0 && !wait_one(bar(ss.o_free), (w.n - 1) & 1u, abort, limit))) {
                         ok = false;
                         break;
                     }
                     tc::fence_after();
 #pragma unroll
                     for (int kk = 0; kk < BK / 16; ++kk)
-                        if (kk < ksteps)
+                        if (kk < BT / 16 || !tree)
                             tc::mma_bf16_ts(tmem + TM_O, tmem + TM_P + (uint32_t)(kk * 8),
                                             tc::desc_mn_sw128(vaddr + kk * 2048, V_TILE / 2, 1024), IDESC,
                                             !fresh || kk > 0 ? 1u : 0u);
@@ -482,7 +497,7 @@ __global__ void __launch_bounds__(NT, 1)
             for (int i = w.i0; i < w.i1;) {
                 const uint32_t batch = t / AHEAD;
                 if (t % AHEAD == 0 && batch >= 2 &&
-                    !tc::mbar_wait_warp(bar(ss.ahead_empty[batch & 1]), ((batch - 2) >> 1) & 1u, abort, limit)) {
+                    !wait_warp(bar(ss.ahead_empty[batch & 1]), ((batch - 2) >> 1) & 1u, abort, limit)) {
                     ok = false;
                     break;
                 }
@@ -522,12 +537,12 @@ __global__ void __launch_bounds__(NT, 1)
         auto together = [&] {
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(bar(ss.c_sync));
-            return tc::mbar_wait_warp(bar(ss.c_sync), syncs++ & 1u, abort, limit);
+            return wait_warp(bar(ss.c_sync), syncs++ & 1u, abort, limit);
         };
         for (bool more = w.begin(p, ss, range); more && ok; more = ok && w.next(p)) {
             const int u = w.n & 1, g = w.k;
-            if ((w.n >= 2 && !tc::mbar_wait_warp(bar(ss.u_empty[u]), ((w.n - 2) >> 1) & 1u, abort, limit)) ||
-                (w.n > 0 && !tc::mbar_wait_warp(bar(ss.q_empty), (w.n - 1) & 1u, abort, limit))) {
+            if ((w.n >= 2 && !wait_warp(bar(ss.u_empty[u]), ((w.n - 2) >> 1) & 1u, abort, limit)) ||
+                (w.n > 0 && !wait_warp(bar(ss.q_empty), (w.n - 1) & 1u, abort, limit))) {
                 ok = false;
                 break;
             }
@@ -553,7 +568,7 @@ __global__ void __launch_bounds__(NT, 1)
                 const uint32_t top2 = max_u16x2(max_u16x2(top4[0], top4[1]), max_u16x2(top4[2], top4[3]));
                 uint32_t top = max(top2 & 0xffffu, top2 >> 16);
                 const bool odd = top >= BF16_INF;   // something is not finite: the largest of the others, and NaN
-                if (odd) {
+                if (RARELY(odd)) {
                     top = 0;
 #pragma unroll
                     for (int j = 0; j < 64; ++j) {
@@ -570,7 +585,7 @@ __global__ void __launch_bounds__(NT, 1)
                     bf16x8(make_uint4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]), v);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) v[e] *= up;
-                    if (odd) {
+                    if (RARELY(odd)) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e) v[e] = fabsf(v[e]) <= FLT_MAX ? v[e] : __int_as_float(0x7fc00000);
                     }
@@ -615,7 +630,7 @@ __global__ void __launch_bounds__(NT, 1)
             for (int i = w.i0; i < w.i1; ++i, ++t) {
                 const int s = (int)(t % VB);
                 uint8_t *dst = smp + OFF_V + s * V_TILE;
-                if (w.is_tree(p, i)) {
+                if (RARELY(w.is_tree(p, i))) {
                     // ---- the tree: V in fp16, K in two parts into its stage, each by the power of two of its largest
                     const int c = lane & 15, r0 = cw * 2 + (lane >> 4);
                     uint4 x[BT / 8];
@@ -641,7 +656,7 @@ __global__ void __launch_bounds__(NT, 1)
                     int kb, vb;
                     if (cw == 0 && lane == 0) ss.odd_v[u] = 0;
                     if (!load(a.tree_v, ss.top_v, vb) ||
-                        !tc::mbar_wait_warp(bar(ss.v_empty[s]), ((t / VB) & 1u) ^ 1u, abort, limit)) {
+                        !wait_warp(bar(ss.v_empty[s]), ((t / VB) & 1u) ^ 1u, abort, limit)) {
                         ok = false;
                         break;
                     }
@@ -664,7 +679,7 @@ __global__ void __launch_bounds__(NT, 1)
                             make_uint4(h[0], h[1], h[2], h[3]);
                     }
                     if (!load(a.tree_k, ss.top_k, kb) ||
-                        !tc::mbar_wait_warp(bar(ss.k_empty[t % KS]), ((t / KS) & 1u) ^ 1u, abort, limit)) {
+                        !wait_warp(bar(ss.k_empty[t % KS]), ((t / KS) & 1u) ^ 1u, abort, limit)) {
                         ok = false;
                         break;
                     }
@@ -687,36 +702,34 @@ __global__ void __launch_bounds__(NT, 1)
                 }
                 // ---- V's codes of 32 keys a warp: 8 lanes a key
                 const int sv = (int)(tv % VS);
-                if (!tc::mbar_wait_warp(bar(ss.vr_full[sv]), (tv / VS) & 1u, abort, limit) ||
-                    !tc::mbar_wait_warp(bar(ss.v_empty[s]), ((t / VB) & 1u) ^ 1u, abort, limit)) {
+                if (!wait_warp(bar(ss.vr_full[sv]), (tv / VS) & 1u, abort, limit) ||
+                    !wait_warp(bar(ss.v_empty[s]), ((t / VB) & 1u) ^ 1u, abort, limit)) {
                     ok = false;
                     break;
                 }
-                const uint8_t *src = smp + OFF_VR + sv * K_TILE;
-                const int c = lane & 7;
+                // (lanes: 4 chunks of 16 dims, 2 keys, 2 blocks of 64 dims, 2 keys: 8 lanes' stores fill all banks)
+                const int c = (lane & 3) + (lane >> 3 & 1) * 4, k0 = cw * 32 + (lane >> 2 & 1) + (lane >> 4) * 2;
+                const uint8_t *src = smp + OFF_VR + sv * K_TILE + k0 * 128;
+                uint8_t *to = dst + (c >> 2) * (V_TILE / 2) + k0 * 128;
+                const bool cut = i * BK + BK > w.L;
 #pragma unroll
-                for (int it = 0; it < 8; it += 8) {
-                    uint4 x[8];
+                for (int it = 0; it < 8; it += 4) {
+                    uint4 x[4];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int key = cw * 32 + (it + j) * 4 + (lane >> 3);
-                        x[j] = *reinterpret_cast<const uint4 *>(src + key * 128 + (((uint32_t)c ^ ((uint32_t)key & 7u)) << 4));
-                        if (i * BK + key >= w.L) x[j] = make_uint4(0, 0, 0, 0);   // whatever lies behind the last key
+                    for (int j = 0; j < 4; ++j)   // key k0 + 4 (it + j): its low three bits are k0's, with bit 2 by j
+                        x[j] = *reinterpret_cast<const uint4 *>(src + (it + j) * 512 + ((c ^ ((k0 + 4 * j) & 7)) << 4));
+                    if (RARELY(cut)) {            // whatever lies behind the last key
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (i * BK + k0 + 4 * (it + j) >= w.L) x[j] = make_uint4(0, 0, 0, 0);
                     }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int key = cw * 32 + (it + j) * 4 + (lane >> 3);
-                        const uint4 lo = make_uint4(e4m3x2_f16(x[j].x), e4m3x2_f16(x[j].x >> 16), e4m3x2_f16(x[j].y),
-                                                    e4m3x2_f16(x[j].y >> 16));
-                        const uint4 hi = make_uint4(e4m3x2_f16(x[j].z), e4m3x2_f16(x[j].z >> 16), e4m3x2_f16(x[j].w),
-                                                    e4m3x2_f16(x[j].w >> 16));
-                        // 16 dims: two chunks of a block of 64; the upper block's lanes store theirs in the other order,
-                        // so that 8 lanes fill all banks
-                        uint8_t *blk = dst + (c >> 2) * (V_TILE / 2) + key * 128;
-                        const bool swap = c >= 4;
-                        const uint32_t c0 = (uint32_t)(2 * c) & 7u, key7 = (uint32_t)key & 7u;
-                        *reinterpret_cast<uint4 *>(blk + (((c0 + (swap ? 1u : 0u)) ^ key7) << 4)) = swap ? hi : lo;
-                        *reinterpret_cast<uint4 *>(blk + (((c0 + (swap ? 0u : 1u)) ^ key7) << 4)) = swap ? lo : hi;
+                    for (int j = 0; j < 4; ++j) {
+                        const int key7 = (k0 + 4 * j) & 7, c0 = 2 * c & 7;
+                        *reinterpret_cast<uint4 *>(to + (it + j) * 512 + ((c0 ^ key7) << 4)) =
+                            make_uint4(e4m3x2_f16(x[j].x), e4m3x2_f16(x[j].x >> 16), e4m3x2_f16(x[j].y), e4m3x2_f16(x[j].y >> 16));
+                        *reinterpret_cast<uint4 *>(to + (it + j) * 512 + (((c0 + 1) ^ key7) << 4)) =
+                            make_uint4(e4m3x2_f16(x[j].z), e4m3x2_f16(x[j].z >> 16), e4m3x2_f16(x[j].w), e4m3x2_f16(x[j].w >> 16));
                     }
                 }
                 tc::fence_proxy_async_smem();
@@ -739,7 +752,7 @@ __global__ void __launch_bounds__(NT, 1)
         auto pair_sync = [&] { asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory"); };
         uint32_t t = 0;
         bool ok = true;
-        auto wait = [&](uint64_t &b, uint32_t parity) { ok = ok && tc::mbar_wait_warp(bar(b), parity & 1u, abort, limit); };
+        auto wait = [&](uint64_t &b, uint32_t parity) { ok = ok && wait_warp(bar(b), parity & 1u, abort, limit); };
         for (bool more = w.begin(p, ss, range); more; more = w.next(p)) {
             const int u = w.n & 1, g = w.k;
             wait(ss.r_full[u], w.n >> 1);
@@ -756,7 +769,7 @@ __global__ void __launch_bounds__(NT, 1)
                     if (lane == 0) tc::mbar_arrive(bar(ss.ahead_empty[batch & 1]));
                 }
                 const bool tree = w.is_tree(p, i);
-                if (tree) {
+                if (RARELY(tree)) {
                     wait(ss.tree_full[u], w.n >> 1);
                     sb = make_uchar4(ss.tree_k[u], ss.tree_k[u], ss.tree_v[u], ss.tree_v[u]);
                     odd_v = ss.odd_v[u] != 0;
@@ -776,7 +789,7 @@ __global__ void __launch_bounds__(NT, 1)
                 tc::fence_before();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(bar(ss.s_empty[t & 1]));
-                if (tree || keys < 64) {
+                if (RARELY(tree || keys < 64)) {
                     uint64_t vis = keys > 0 ? (1ull << keys) - 1ull : 0ull;
                     if (tree) vis = half == 0 && r < nrows ? ss.anc[u][row_node(p, row0 + r)] : 0ull;
                     const uint32_t v0 = (uint32_t)vis, v1 = (uint32_t)(vis >> 32);
@@ -796,7 +809,7 @@ __global__ void __launch_bounds__(NT, 1)
                 const int ev = max(sb.z == 255 ? 0 : sb.z, sb.w == 255 ? 0 : sb.w);
                 const bool moved = __any_sync(0xffffffffu, need || ev > evref);
                 float corr = 1.0f;
-                if (moved) {
+                if (RARELY(moved)) {
                     const float m_new = need ? mx : m_run;
                     corr = need ? (m_run == -INFINITY ? 0.0f : fast_exp2(m_run - m_new)) : 1.0f;
                     l_run *= corr;
@@ -828,7 +841,7 @@ __global__ void __launch_bounds__(NT, 1)
                     tc::fence_after();
                 }
                 if (!tree || half == 0) tc::tmem_st32u_start(t_lane + TM_P + half * 32u, pk);
-                if (moved && i > w.i0) {
+                if (RARELY(moved && i > w.i0)) {
 #pragma unroll 1
                     for (int q = 0; q < 2; ++q) {
                         float o[32];
@@ -865,7 +878,7 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[e] = l != 0.0f ? o[e] * back : 0.0f;
                 // infinities and NaN of the tree's values, to the rows that see them
-                if (odd_v && mine) {
+                if (RARELY(odd_v && mine)) {
                     for (int j = 0; j < a.N; ++j) {
                         if (!(anc >> j & 1ull)) continue;
                         const __nv_bfloat16 *tv = a.tree_v + ((size_t)w.b * a.N + j) * a.kv_ns + (size_t)g * D + c0;

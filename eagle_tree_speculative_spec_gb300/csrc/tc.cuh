@@ -483,7 +483,7 @@ E3_DEV void tmem_st32u(uint32_t taddr, const uint32_t (&v)[32]) {
 }
 
 // The same without the wait, and the wait for all stores of the thread so far
-E3_DEV void tmem_st32u_start(uint32_t taddr, const uint32_t (&v)[32]) {
+E3_DEV void tmem_st32u_start(uint32_t taddr, const uint32_t *v) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
         "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),

@@ -500,6 +500,47 @@ def test_attn_splits(N, Hq, tree, splits):
     _check_attn([500, 31, 0, 170], N, Hq, 2, 64, tree, num_splits=splits)
 
 
+@pytest.mark.parametrize("lens,N,Hq", [([12000, 3], 5, 8), ([9000], 33, 4), ([5000, 7000, 0, 130], 60, 4)])
+def test_attn_many_tiles_in_a_row(lens, N, Hq):
+    """Hundreds of tiles for one CTA: every ring and barrier goes around many times."""
+    _check_attn(lens, N, Hq, 1, 128, True, num_splits=1)
+
+
+def test_attn_full_gpu_repeats():
+    """Every SM busy over many units: bit-identical every time, and equal to the oracle for two sequences."""
+    dev = require_gpu()
+    B, N, Hq, Hkv, L, size = 48, 60, 32, 8, 1500, 128
+    lens = [L - 17 * b for b in range(B)]
+    g = torch.Generator(device=dev).manual_seed(3)
+    need = [-(-n // size) for n in lens]
+    pages = sum(need)
+    ids = torch.randperm(pages, generator=g, device=dev).to(i32)
+    table = torch.full((B, max(need)), -1, dtype=i32, device=dev)
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = ids[at:at + n]
+        at += n
+    caches = [torch.randn(pages, Hkv, size, 128, generator=g, device=dev).mul_(60).to(f8) for _ in range(2)]
+    scales = [torch.randint(119, 122, (pages, Hkv, size // 64), generator=g, device=dev, dtype=i32).to(u8) for _ in range(2)]
+    q, tk, tv = (torch.randn(B, N, h, 128, generator=g, device=dev).to(bf) for h in (Hq, Hkv, Hkv))
+    par = _trees(B, N, 5)
+    st = torch.zeros(1, dtype=i32, device=dev)
+    outs = [torch.empty(B, N, Hq, 128, dtype=bf, device=dev) for _ in range(2)]
+    for i in range(60):
+        e3.eagle3_verify_attn_fp8(q, *caches, *scales, table, _ints(lens, dev), outs[min(i, 1)], max_prefix_len=L, tree_k=tk,
+                                  tree_v=tv, parents=torch.from_numpy(par).to(dev), dev_status=st)
+        assert i == 0 or torch.equal(outs[0], outs[1])
+    assert int(st) == 0
+    pool = Pool(dev, [64], Hkv, 128, size, 1)
+    pool.pages = pages
+    pool.codes = [c.view(u8).cpu() for c in caches]
+    pool.scale = [c.cpu() for c in scales]
+    for b in (0, B - 1):
+        pool.table = table[b:b + 1].cpu().numpy()
+        want, _, tol, _ = _expected(pool, lens[b:b + 1], q[b:b + 1].cpu(), tk[b:b + 1].cpu(), tv[b:b + 1].cpu(), par[b:b + 1])
+        assert (np.abs(_np(outs[0][b:b + 1]) - want) <= tol).all()
+
+
 @pytest.mark.parametrize("N,Hq", [(1, 8), (60, 8)])
 def test_attn_bound_above_the_lengths(N, Hq):
     _check_attn([200, 0, 1], N, Hq, 2, 64, N > 1, longest=3000)
