@@ -13,7 +13,7 @@
 // weight, would cost long sums) and V's codes, converted exactly; the scale of V's group is put on the weights, relative to
 // the largest so far, by adding to the exponent.
 //
-//   warp 0        TMA: K tiles into a ring of 4, V codes into a ring of 3
+//   warp 0        TMA: K tiles into a ring of 4, V codes into a ring of 2
 //   warp 1, 2     the MMAs of S, and of P V (one thread issues an MMA about every 110 cycles: two threads)
 //   warp 3        looks ahead: the places and scales of the next 32 tiles, a tile a lane (two dependent loads, which
 //                 whoever needs them would wait for tile by tile)
@@ -33,7 +33,7 @@ namespace {
 constexpr int D = 128;
 constexpr int BK = 128;                 // keys of a tile
 constexpr int BT = 64;                  // nodes of the tree's tile
-constexpr int KS = 4, VS = 3, VB = 3;   // stages: K codes, V codes, V in fp16
+constexpr int KS = 4, VS = 2, VB = 3;   // stages: K codes, V codes, V in fp16
 constexpr int AHEAD = 32;               // tiles that warp 3 looks up at once, two such batches
 constexpr int ROWS = 128;               // query rows of a CTA
 constexpr int NT = 512;
@@ -42,7 +42,9 @@ constexpr uint32_t K_TILE = BK * D, V_TILE = 2 * K_TILE;
 constexpr uint32_t OFF_K = 0;
 constexpr uint32_t OFF_VR = OFF_K + KS * K_TILE;
 constexpr uint32_t OFF_V = OFF_VR + VS * K_TILE;
-constexpr uint32_t SMEM_DYN = OFF_V + VB * V_TILE + 1024;   // + alignment slack
+constexpr uint32_t OUT_WARP = 32 * 64;   // a softmax warp's 32 rows of 32 outputs in bf16
+constexpr uint32_t OFF_OUT = OFF_V + VB * V_TILE;
+constexpr uint32_t SMEM_DYN = OFF_OUT + 8 * OUT_WARP + 1024;   // + alignment slack
 // tensor memory, columns: O; S of two tiles; P; Q's parts, 32 columns each
 constexpr uint32_t TM_O = 0, TM_S = 128, TM_P = 384, TM_Q = 448;
 constexpr int JOIN_WARPS = 8;
@@ -53,6 +55,7 @@ struct Smem {
     uint64_t q_full, q_empty;
     uint64_t ahead_full[2], ahead_empty[2];
     uint64_t r_full[2], u_empty[2], tree_full[2];   // by unit parity
+    uint64_t tree_rows;                          // the tree's K is in its stage
     uint64_t c_sync;                             // warps 4..7 among themselves (a wait that ends, unlike bar.sync)
     uint64_t mma_done[2];
     uint64_t anc[2][64];
@@ -62,7 +65,7 @@ struct Smem {
     int row[2 * AHEAD][2];                       // of the tile's two groups in the pool's map
     uchar4 scale[2 * AHEAD];                     // K, K, V, V
     int tree_k[2], tree_v[2], odd_v[2];          // the tree's scale bytes; whether a value is not finite
-    uint32_t top_k[4], top_v[4];
+    uint2 tree_top[2][4];                        // by warp: the largest of K and V as bits, whether V has odd ones
     long long start_off, range;
     int start_b, start_k;
     uint32_t tmem_base;
@@ -168,39 +171,6 @@ E3_DEV void store_parts(uint4 x, float up, bool odd, uint8_t *tile, uint32_t apa
     *reinterpret_cast<uint2 *>(at + apart) = lo;
 }
 
-// The largest finite magnitudes of N rows, 16 lanes a row (the other 16 of a warp N more), as bits; whether the warp has
-// anything that is not finite.  Two rows a word, and all words a step at a time: the exchanges overlap.
-template <int N>
-E3_DEV bool row_maxima(const uint4 (&x)[N], uint32_t (&top)[N]) {
-    uint32_t all = 0;
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-        top[j] = amax_bits(x[j]);
-        all = max(all, top[j]);
-    }
-    const bool odd = __any_sync(0xffffffffu, all >= BF16_INF);
-    if (__builtin_expect(odd, 0)) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) top[j] = amax_bits_finite(x[j]);
-    }
-    uint32_t two[N / 2], other[N / 2];
-#pragma unroll
-    for (int j = 0; j < N / 2; ++j) two[j] = top[2 * j] | top[2 * j + 1] << 16;
-#pragma unroll
-    for (int d = 8; d; d >>= 1) {
-#pragma unroll
-        for (int j = 0; j < N / 2; ++j) other[j] = __shfl_xor_sync(0xffffffffu, two[j], d);
-#pragma unroll
-        for (int j = 0; j < N / 2; ++j) two[j] = max_u16x2(two[j], other[j]);
-    }
-#pragma unroll
-    for (int j = 0; j < N / 2; ++j) {
-        top[2 * j] = two[j] & 0xffffu;
-        top[2 * j + 1] = two[j] >> 16;
-    }
-    return odd;
-}
-
 // The nodes that each node sees, by a warp: every node's set joined with that of the node it has got to, which moves
 // twice as far each time
 E3_DEV void tree_paths(const CacheAttn &a, int b, bool report, int lane, uint64_t *anc) {
@@ -251,15 +221,17 @@ E3_DEV float weight_of(float m, float l, float M) {
 // SM's instruction cache.
 #define RARELY(x) __builtin_expect(!!(x), 0)
 
-E3_DEV bool wait_warp(uint32_t bar, uint32_t parity, uint32_t abort, uint32_t limit) {
-    bool ok = true;
-    if (RARELY(!__all_sync(0xffffffffu, tc::mbar_try(bar, parity)))) ok = tc::mbar_wait_warp(bar, parity, abort, limit);
-    return ok;
+// A wait: one poll inline, the loop in one function for all roles (in line at every wait, the loops alone were some 6 KB of
+// code that took turns in the instruction cache).
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint32_t abort, uint32_t limit) {
+    return tc::mbar_wait(bar, parity, abort, limit);
 }
 E3_DEV bool wait_one(uint32_t bar, uint32_t parity, uint32_t abort, uint32_t limit) {
-    bool ok = true;
-    if (RARELY(!tc::mbar_try(bar, parity))) ok = tc::mbar_wait(bar, parity, abort, limit);
-    return ok;
+    return tc::mbar_try(bar, parity) || wait_slow(bar, parity, abort, limit);
+}
+E3_DEV bool wait_warp(uint32_t bar, uint32_t parity, uint32_t abort, uint32_t limit) {
+    const bool ok = wait_one(bar, parity, abort, limit);
+    return __all_sync(0xffffffffu, ok);
 }
 
 __global__ void __launch_bounds__(NT, 1)
@@ -305,6 +277,7 @@ __global__ void __launch_bounds__(NT, 1)
         tc::mbar_init(&ss.q_full, 4);
         tc::mbar_init(&ss.q_empty, 1);
         tc::mbar_init(&ss.c_sync, 4);
+        tc::mbar_init(&ss.tree_rows, 4);
         ss.abort_flag = 0;
         tc::fence_barrier_init();
         tc::prefetch_tmap(&tm_k);
@@ -409,7 +382,7 @@ __global__ void __launch_bounds__(NT, 1)
         // ------------------------------------------------------------------ S = Q K^T
         if (tc::elect_one()) {
             constexpr uint32_t IDESC = tc::idesc_e4m3(128, BK), IDESC_T = tc::idesc_e4m3(128, BT);
-            uint32_t t = 0;
+            uint32_t t = 0, trees = 0;
             bool ok = true;
             for (bool more = w.begin(p, ss, range); more && ok; more = ok && w.next(p)) {
                 ok = wait_one(bar(ss.q_full), w.n & 1u, abort, limit);
@@ -422,7 +395,8 @@ __global__ void __launch_bounds__(NT, 1)
                     const bool tree = w.is_tree(p, i);
                     const uint32_t kaddr = sm + OFF_K + s * K_TILE;
                     const int b = (int)(t & 1u);
-                    if (t >= 2 && !wait_one(bar(ss.s_empty[b]), ((t - 2) >> 1) & 1u, abort, limit)) {
+                    if ((tree && !wait_one(bar(ss.tree_rows), trees++ & 1u, abort, limit)) ||
+                        (t >= 2 && !wait_one(bar(ss.s_empty[b]), ((t - 2) >> 1) & 1u, abort, limit))) {
                         ok = false;
                         break;
                     }
@@ -633,41 +607,55 @@ __global__ void __launch_bounds__(NT, 1)
                 if (RARELY(w.is_tree(p, i))) {
                     // ---- the tree: V in fp16, K in two parts into its stage, each by the power of two of its largest
                     const int c = lane & 15, r0 = cw * 2 + (lane >> 4);
-                    uint4 x[BT / 8];
-                    bool odd = false;
-                    // the rows of this warp in x, and the scale byte of them all
-                    auto load = [&](const __nv_bfloat16 *src, uint32_t *tops, int &byte) {
-                        src += (size_t)w.b * a.N * a.kv_ns + (size_t)g * D + c * 8;
+                    const size_t base = (size_t)w.b * a.N * a.kv_ns + (size_t)g * D + c * 8;
+                    uint4 xk[BT / 8], xv[BT / 8];
 #pragma unroll
-                        for (int j = 0; j < BT / 8; ++j) {
-                            x[j] = make_uint4(0, 0, 0, 0);
-                            if (j * 8 + r0 < a.N) x[j] = *reinterpret_cast<const uint4 *>(src + (j * 8 + r0) * a.kv_ns);
-                        }
-                        uint32_t top[BT / 8], all = 0;
-                        odd = row_maxima<BT / 8>(x, top);
+                    for (int j = 0; j < BT / 8; ++j) {
+                        const size_t at = base + (size_t)min(j * 8 + r0, a.N - 1) * a.kv_ns;
+                        const bool there = j * 8 + r0 < a.N;
+                        xk[j] = *reinterpret_cast<const uint4 *>(a.tree_k + at);
+                        xv[j] = *reinterpret_cast<const uint4 *>(a.tree_v + at);
+                        if (!there) xk[j] = xv[j] = make_uint4(0, 0, 0, 0);
+                    }
+                    // the largest of all rows, K's and V's in one word
+                    uint32_t both = 0;
 #pragma unroll
-                        for (int j = 0; j < BT / 8; ++j) all = max(all, top[j]);
-                        all = max(all, __shfl_xor_sync(0xffffffffu, all, 16));
-                        if (lane == 0) tops[cw] = all;
-                        const bool got = together();
-                        byte = scale_byte_bits(max(max(tops[0], tops[1]), max(tops[2], tops[3])));
-                        return got;
-                    };
-                    int kb, vb;
-                    if (cw == 0 && lane == 0) ss.odd_v[u] = 0;
-                    if (!load(a.tree_v, ss.top_v, vb) ||
-                        !wait_warp(bar(ss.v_empty[s]), ((t / VB) & 1u) ^ 1u, abort, limit)) {
+                    for (int j = 0; j < BT / 8; ++j) both = max_u16x2(both, amax_bits(xk[j]) | amax_bits(xv[j]) << 16);
+                    const bool odd_k = __any_sync(0xffffffffu, (both & 0xffffu) >= BF16_INF);
+                    const bool odd_v = __any_sync(0xffffffffu, (both >> 16) >= BF16_INF);
+                    if (RARELY(odd_k || odd_v)) {
+                        both = 0;
+#pragma unroll
+                        for (int j = 0; j < BT / 8; ++j)
+                            both = max_u16x2(both, amax_bits_finite(xk[j]) | amax_bits_finite(xv[j]) << 16);
+                    }
+#pragma unroll
+                    for (int d = 16; d; d >>= 1) both = max_u16x2(both, __shfl_xor_sync(0xffffffffu, both, d));
+                    if (lane == 0) ss.tree_top[u][cw] = make_uint2(both, odd_v ? 1u : 0u);
+                    if (!together()) {
                         ok = false;
                         break;
                     }
-                    if (lane == 0 && odd) ss.odd_v[u] = 1;
-                    const float vup = inverse_scale(vb);
+                    uint2 all = ss.tree_top[u][0];
+#pragma unroll
+                    for (int j = 1; j < 4; ++j) {
+                        all.x = max_u16x2(all.x, ss.tree_top[u][j].x);
+                        all.y |= ss.tree_top[u][j].y;
+                    }
+                    const int kb = scale_byte_bits(all.x & 0xffffu), vb = scale_byte_bits(all.x >> 16);
+                    if (!wait_warp(bar(ss.v_empty[s]), ((t / VB) & 1u) ^ 1u, abort, limit) ||
+                        !wait_warp(bar(ss.k_empty[t % KS]), ((t / KS) & 1u) ^ 1u, abort, limit)) {
+                        ok = false;
+                        break;
+                    }
+                    const float kup = inverse_scale(kb), vup = inverse_scale(vb);
 #pragma unroll
                     for (int j = 0; j < BT / 8; ++j) {
                         const int row = j * 8 + r0;
+                        store_parts(xk[j], kup, odd_k, smp + OFF_K + (t % KS) * K_TILE, K_TILE / 2, row, c);
                         float v[8];
-                        bf16x8(x[j], v);
-                        if (odd) {
+                        bf16x8(xv[j], v);
+                        if (RARELY(odd_v)) {
 #pragma unroll
                             for (int e = 0; e < 8; ++e) v[e] = fabsf(v[e]) <= FLT_MAX ? v[e] : 0.0f;
                         }
@@ -678,26 +666,19 @@ __global__ void __launch_bounds__(NT, 1)
                                                    (((uint32_t)c & 7u) ^ ((uint32_t)row & 7u)) * 16) =
                             make_uint4(h[0], h[1], h[2], h[3]);
                     }
-                    if (!load(a.tree_k, ss.top_k, kb) ||
-                        !wait_warp(bar(ss.k_empty[t % KS]), ((t / KS) & 1u) ^ 1u, abort, limit)) {
-                        ok = false;
-                        break;
-                    }
-#pragma unroll
-                    for (int j = 0; j < BT / 8; ++j)
-                        store_parts(x[j], inverse_scale(kb), odd, smp + OFF_K + (t % KS) * K_TILE, K_TILE / 2, j * 8 + r0, c);
                     tc::fence_proxy_async_smem();
-                    if (!together()) {   // all of K is there: one arrival
-                        ok = false;
-                        break;
-                    }
+                    __syncwarp();
                     if (cw == 0 && lane == 0) {
                         ss.tree_k[u] = kb;
                         ss.tree_v[u] = vb;
+                        ss.odd_v[u] = (int)all.y;
                         tc::mbar_arrive(bar(ss.tree_full[u]));
-                        tc::mbar_arrive(bar(ss.k_full[t % KS]));
+                        tc::mbar_arrive(bar(ss.k_full[t % KS]));   // (the stage's phase; its rows are announced by tree_rows)
                     }
-                    if (lane == 0) tc::mbar_arrive(bar(ss.v_full[s]));
+                    if (lane == 0) {
+                        tc::mbar_arrive(bar(ss.tree_rows));
+                        tc::mbar_arrive(bar(ss.v_full[s]));
+                    }
                     continue;
                 }
                 // ---- V's codes of 32 keys a warp: 8 lanes a key
@@ -889,9 +870,10 @@ __global__ void __launch_bounds__(NT, 1)
                         }
                     }
                 }
-                if (!mine) continue;
                 if (whole) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(a.out + at * D + c0);
+                    // through shared memory: a store of the warp writes 64 bytes of 8 rows, not 16 bytes of 32
+                    uint8_t *buf = smp + OFF_OUT + (warp - 8) * OUT_WARP;
+                    __syncwarp();
 #pragma unroll
                     for (int c8 = 0; c8 < 4; ++c8) {
                         uint32_t x[4];
@@ -900,9 +882,21 @@ __global__ void __launch_bounds__(NT, 1)
                             const __nv_bfloat162 hv = __floats2bfloat162_rn(o[8 * c8 + 2 * e] * inv, o[8 * c8 + 2 * e + 1] * inv);
                             x[e] = *reinterpret_cast<const uint32_t *>(&hv);
                         }
-                        dst[c8] = make_uint4(x[0], x[1], x[2], x[3]);
+                        *reinterpret_cast<uint4 *>(buf + lane * 64 + ((c8 ^ (lane >> 1 & 3)) << 4)) =
+                            make_uint4(x[0], x[1], x[2], x[3]);
                     }
-                } else {
+                    __syncwarp();
+#pragma unroll
+                    for (int it = 0; it < 4; ++it) {
+                        const int rr = it * 8 + (lane >> 2), row = quarter * 32 + rr;
+                        const uint4 x = *reinterpret_cast<const uint4 *>(buf + rr * 64 + (((lane & 3) ^ (rr >> 1 & 3)) << 4));
+                        if (row < nrows) {
+                            const int nd = row_node(p, row0 + row);
+                            const size_t to = ((size_t)w.b * a.N + nd) * a.Hq + g * a.rep + row0 + row - nd * a.rep;
+                            *reinterpret_cast<uint4 *>(a.out + to * D + c0 + (lane & 3) * 8) = x;
+                        }
+                    }
+                } else if (mine) {
                     float4 *dst = reinterpret_cast<float4 *>(p.part_o + part * D + c0);
 #pragma unroll
                     for (int c4 = 0; c4 < 8; ++c4) dst[c4] = make_float4(o[4 * c4], o[4 * c4 + 1], o[4 * c4 + 2], o[4 * c4 + 3]);
