@@ -522,60 +522,46 @@ __global__ void __launch_bounds__(NT, 1)
             }
             const bool tree = a.tree_k && w.i1 == w.nt;
             tc::fence_after();
-            // ---- Q's parts: a row a thread, its 128 dims in registers
+            // ---- Q's parts: a row a thread, read twice (the second time from the first-level cache)
             {
                 const int r = cw * 32 + lane;
-                uint32_t x[64];
+                const uint4 *src = reinterpret_cast<const uint4 *>(a.q + row_at(p, w.b, g, row0 + min(r, nrows - 1)));
+                uint32_t top = 0;
 #pragma unroll
-                for (int j = 0; j < 64; ++j) x[j] = 0;
-                if (r < nrows) {
-                    const uint4 *src = reinterpret_cast<const uint4 *>(a.q + row_at(p, w.b, g, row0 + r));
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const uint4 v = src[j];
-                        x[4 * j] = v.x, x[4 * j + 1] = v.y, x[4 * j + 2] = v.z, x[4 * j + 3] = v.w;
-                    }
-                }
-                uint32_t top4[4] = {0, 0, 0, 0};
-#pragma unroll
-                for (int j = 0; j < 64; ++j) top4[j & 3] = max_u16x2(top4[j & 3], x[j] & 0x7fff7fffu);
-                const uint32_t top2 = max_u16x2(max_u16x2(top4[0], top4[1]), max_u16x2(top4[2], top4[3]));
-                uint32_t top = max(top2 & 0xffffu, top2 >> 16);
+                for (int j = 0; j < 16; ++j) top = max(top, amax_bits(__ldg(src + j)));
                 const bool odd = top >= BF16_INF;   // something is not finite: the largest of the others, and NaN
                 if (RARELY(odd)) {
                     top = 0;
-#pragma unroll
-                    for (int j = 0; j < 64; ++j) {
-                        const uint32_t lo = x[j] & 0x7fffu, hi = (x[j] >> 16) & 0x7fffu;
-                        top = max(top, max(lo < BF16_INF ? lo : 0u, hi < BF16_INF ? hi : 0u));
-                    }
+#pragma unroll 1
+                    for (int j = 0; j < 16; ++j) top = max(top, amax_bits_finite(__ldg(src + j)));
                 }
                 const int byte = scale_byte_bits(top);
-                const float up = inverse_scale(byte);
-                // words 4 j .. 4 j + 3 (8 dims) become two words of each part
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    float v[8];
-                    bf16x8(make_uint4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]), v);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] *= up;
-                    if (RARELY(odd)) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] = fabsf(v[e]) <= FLT_MAX ? v[e] : __int_as_float(0x7fc00000);
-                    }
-                    uint2 hi, lo;
-                    two_parts(v, hi, lo);
-                    x[4 * j] = hi.x, x[4 * j + 1] = hi.y, x[4 * j + 2] = lo.x, x[4 * j + 3] = lo.y;
-                }
+                const float up = r < nrows ? inverse_scale(byte) : 0.0f;   // (rows behind the last one: zeros)
                 const uint32_t tq = tmem + ((uint32_t)(cw * 32) << 16) + TM_Q;
-                uint32_t part[32];
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {   // 32 dims: 8 columns of each part
+                    uint4 x[4];
+                    uint32_t hi[8], lo[8];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) part[j] = x[4 * (j >> 1) + (j & 1)];
-                __syncwarp();
-                tc::tmem_st32u_start(tq, part);
+                    for (int j = 0; j < 4; ++j) x[j] = __ldg(src + 4 * q + j);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) part[j] = x[4 * (j >> 1) + 2 + (j & 1)];
-                tc::tmem_st32u_start(tq + 32u, part);
+                    for (int j = 0; j < 4; ++j) {
+                        float v[8];
+                        bf16x8(x[j], v);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] *= up;
+                        if (RARELY(odd)) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) v[e] = fabsf(v[e]) <= FLT_MAX ? v[e] : __int_as_float(0x7fc00000);
+                        }
+                        uint2 h2, l2;
+                        two_parts(v, h2, l2);
+                        hi[2 * j] = h2.x, hi[2 * j + 1] = h2.y, lo[2 * j] = l2.x, lo[2 * j + 1] = l2.y;
+                    }
+                    __syncwarp();
+                    tc::tmem_st8u_start(tq + 8u * q, hi);
+                    tc::tmem_st8u_start(tq + 32u + 8u * q, lo);
+                }
                 tc::tmem_st_wait();
                 ss.qf[u][r] = a.scale_log2 * scale_of(byte);
                 tc::fence_before();
@@ -608,26 +594,22 @@ __global__ void __launch_bounds__(NT, 1)
                     // ---- the tree: V in fp16, K in two parts into its stage, each by the power of two of its largest
                     const int c = lane & 15, r0 = cw * 2 + (lane >> 4);
                     const size_t base = (size_t)w.b * a.N * a.kv_ns + (size_t)g * D + c * 8;
-                    uint4 xk[BT / 8], xv[BT / 8];
-#pragma unroll
-                    for (int j = 0; j < BT / 8; ++j) {
-                        const size_t at = base + (size_t)min(j * 8 + r0, a.N - 1) * a.kv_ns;
-                        const bool there = j * 8 + r0 < a.N;
-                        xk[j] = *reinterpret_cast<const uint4 *>(a.tree_k + at);
-                        xv[j] = *reinterpret_cast<const uint4 *>(a.tree_v + at);
-                        if (!there) xk[j] = xv[j] = make_uint4(0, 0, 0, 0);
-                    }
-                    // the largest of all rows, K's and V's in one word
+                    // (both passes are short loops: straight-line code that runs once a unit costs its fetch)
+                    auto load = [&](const __nv_bfloat16 *src, int row) {
+                        return __ldg(reinterpret_cast<const uint4 *>(src + base + (size_t)min(row, a.N - 1) * a.kv_ns));
+                    };
+                    // the largest of all rows, K's and V's in one word (a row behind the last is the last again)
                     uint32_t both = 0;
-#pragma unroll
-                    for (int j = 0; j < BT / 8; ++j) both = max_u16x2(both, amax_bits(xk[j]) | amax_bits(xv[j]) << 16);
+#pragma unroll 4
+                    for (int row = r0; row < BT; row += 8)
+                        both = max_u16x2(both, amax_bits(load(a.tree_k, row)) | amax_bits(load(a.tree_v, row)) << 16);
                     const bool odd_k = __any_sync(0xffffffffu, (both & 0xffffu) >= BF16_INF);
                     const bool odd_v = __any_sync(0xffffffffu, (both >> 16) >= BF16_INF);
                     if (RARELY(odd_k || odd_v)) {
                         both = 0;
-#pragma unroll
-                        for (int j = 0; j < BT / 8; ++j)
-                            both = max_u16x2(both, amax_bits_finite(xk[j]) | amax_bits_finite(xv[j]) << 16);
+#pragma unroll 1
+                        for (int row = r0; row < BT; row += 8)
+                            both = max_u16x2(both, amax_bits_finite(load(a.tree_k, row)) | amax_bits_finite(load(a.tree_v, row)) << 16);
                     }
 #pragma unroll
                     for (int d = 16; d; d >>= 1) both = max_u16x2(both, __shfl_xor_sync(0xffffffffu, both, d));
@@ -649,12 +631,13 @@ __global__ void __launch_bounds__(NT, 1)
                         break;
                     }
                     const float kup = inverse_scale(kb), vup = inverse_scale(vb);
-#pragma unroll
-                    for (int j = 0; j < BT / 8; ++j) {
-                        const int row = j * 8 + r0;
-                        store_parts(xk[j], kup, odd_k, smp + OFF_K + (t % KS) * K_TILE, K_TILE / 2, row, c);
+#pragma unroll 2
+                    for (int row = r0; row < BT; row += 8) {
+                        uint4 xk = load(a.tree_k, row), xv = load(a.tree_v, row);
+                        if (row >= a.N) xk = xv = make_uint4(0, 0, 0, 0);
+                        store_parts(xk, kup, odd_k, smp + OFF_K + (t % KS) * K_TILE, K_TILE / 2, row, c);
                         float v[8];
-                        bf16x8(xv[j], v);
+                        bf16x8(xv, v);
                         if (RARELY(odd_v)) {
 #pragma unroll
                             for (int e = 0; e < 8; ++e) v[e] = fabsf(v[e]) <= FLT_MAX ? v[e] : 0.0f;
