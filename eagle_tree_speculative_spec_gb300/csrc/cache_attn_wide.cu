@@ -44,7 +44,9 @@ constexpr uint32_t OFF_VR = OFF_K + KS * K_TILE;
 constexpr uint32_t OFF_V = OFF_VR + VS * K_TILE;
 constexpr uint32_t OUT_WARP = 32 * 64;   // a softmax warp's 32 rows of 32 outputs in bf16
 constexpr uint32_t OFF_OUT = OFF_V + VB * V_TILE;
-constexpr uint32_t SMEM_DYN = OFF_OUT + 8 * OUT_WARP + 1024;   // + alignment slack
+constexpr uint32_t IN_WARP = 32 * 64;    // a converting warp's 32 rows of 32 query dims
+constexpr uint32_t OFF_IN = OFF_OUT + 8 * OUT_WARP;
+constexpr uint32_t SMEM_DYN = OFF_IN + 4 * IN_WARP + 1024;   // + alignment slack
 // tensor memory, columns: O; S of two tiles; P; Q's parts, 32 columns each
 constexpr uint32_t TM_O = 0, TM_S = 128, TM_P = 384, TM_Q = 448;
 constexpr int JOIN_WARPS = 8;
@@ -522,32 +524,57 @@ __global__ void __launch_bounds__(NT, 1)
             }
             const bool tree = a.tree_k && w.i1 == w.nt;
             tc::fence_after();
-            // ---- Q's parts: a row a thread, read twice (the second time from the first-level cache)
+            // ---- Q's parts, a row a thread.  Loaded by 4 lanes a row, 32 dims at a time, twice (the second time from the
+            // first-level cache): for the rows' maxima, then through shared memory to the rows' threads
             {
                 const int r = cw * 32 + lane;
-                const uint4 *src = reinterpret_cast<const uint4 *>(a.q + row_at(p, w.b, g, row0 + min(r, nrows - 1)));
-                uint32_t top = 0;
+                uint8_t *buf = smp + OFF_IN + cw * IN_WARP;
+                auto load = [&](int j, int c) {   // of row 8 j + lane / 4, dims [32 c + 8 (lane & 3), + 8)
+                    const int row = min(cw * 32 + 8 * j + (lane >> 2), nrows - 1);
+                    return __ldg(reinterpret_cast<const uint4 *>(a.q + row_at(p, w.b, g, row0 + row)) + 4 * c + (lane & 3));
+                };
+                uint32_t top[4] = {0, 0, 0, 0};
+#pragma unroll 2
+                for (int c = 0; c < 4; ++c)
 #pragma unroll
-                for (int j = 0; j < 16; ++j) top = max(top, amax_bits(__ldg(src + j)));
-                const bool odd = top >= BF16_INF;   // something is not finite: the largest of the others, and NaN
+                    for (int j = 0; j < 4; ++j) top[j] = max(top[j], amax_bits(load(j, c)));
+                // something is not finite: the largest of the others, and NaN
+                const bool odd = __any_sync(0xffffffffu, max(max(top[0], top[1]), max(top[2], top[3])) >= BF16_INF);
                 if (RARELY(odd)) {
-                    top = 0;
+                    top[0] = top[1] = top[2] = top[3] = 0;
 #pragma unroll 1
-                    for (int j = 0; j < 16; ++j) top = max(top, amax_bits_finite(__ldg(src + j)));
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) top[j] = max(top[j], amax_bits_finite(load(j, c)));
                 }
-                const int byte = scale_byte_bits(top);
+                uint32_t two[2] = {top[0] | top[1] << 16, top[2] | top[3] << 16};
+#pragma unroll
+                for (int d = 1; d < 4; d <<= 1)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) two[j] = max_u16x2(two[j], __shfl_xor_sync(0xffffffffu, two[j], d));
+                // row 8 j + k's from lane 4 k
+                const uint32_t t0 = __shfl_sync(0xffffffffu, two[0], (lane & 7) * 4), t1 = __shfl_sync(0xffffffffu, two[1], (lane & 7) * 4);
+                const uint32_t tj = lane & 16 ? t1 : t0;
+                const int byte = scale_byte_bits(lane & 8 ? tj >> 16 : tj & 0xffffu);
                 const float up = r < nrows ? inverse_scale(byte) : 0.0f;   // (rows behind the last one: zeros)
                 const uint32_t tq = tmem + ((uint32_t)(cw * 32) << 16) + TM_Q;
 #pragma unroll 1
-                for (int q = 0; q < 4; ++q) {   // 32 dims: 8 columns of each part
+                for (int c = 0; c < 4; ++c) {   // 32 dims: 8 columns of each part
                     uint4 x[4];
                     uint32_t hi[8], lo[8];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) x[j] = __ldg(src + 4 * q + j);
+                    for (int j = 0; j < 4; ++j) x[j] = load(j, c);
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int rr = 8 * j + (lane >> 2);
+                        *reinterpret_cast<uint4 *>(buf + rr * 64 + (((lane & 3) ^ (rr >> 1 & 3)) << 4)) = x[j];
+                    }
+                    __syncwarp();
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         float v[8];
-                        bf16x8(x[j], v);
+                        bf16x8(*reinterpret_cast<const uint4 *>(buf + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4)), v);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) v[e] *= up;
                         if (RARELY(odd)) {
@@ -558,9 +585,8 @@ __global__ void __launch_bounds__(NT, 1)
                         two_parts(v, h2, l2);
                         hi[2 * j] = h2.x, hi[2 * j + 1] = h2.y, lo[2 * j] = l2.x, lo[2 * j + 1] = l2.y;
                     }
-                    __syncwarp();
-                    tc::tmem_st8u_start(tq + 8u * q, hi);
-                    tc::tmem_st8u_start(tq + 32u + 8u * q, lo);
+                    tc::tmem_st8u_start(tq + 8u * c, hi);
+                    tc::tmem_st8u_start(tq + 32u + 8u * c, lo);
                 }
                 tc::tmem_st_wait();
                 ss.qf[u][r] = a.scale_log2 * scale_of(byte);
@@ -935,15 +961,30 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) cache_attn_join_kernel(const 
         auto slot = [&](long long q) {
             return (size_t)(2 * (q * p.row_groups + blockIdx.y) + (q == first ? second : 0)) * ROWS + row;
         };
+        // 32 ranges at a time: their statistics by lanes, their results as many loads in flight as there are
         float M = -INFINITY, l = 0.0f;
-        for (long long q = first; q <= last; ++q) M = fmaxf(M, p.part_ml[2 * slot(q)]);
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (long long q = first; q <= last; ++q) {
-            const float2 ml = *reinterpret_cast<const float2 *>(p.part_ml + 2 * slot(q));
+        for (long long q0 = first; q0 <= last; q0 += 32) {
+            const int n = (int)min(32ll, last - q0 + 1);
+            const float2 ml = lane < n ? *reinterpret_cast<const float2 *>(p.part_ml + 2 * slot(q0 + lane)) : make_float2(-INFINITY, 0.0f);
+            float top = ml.x;
+#pragma unroll
+            for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const float Mn = fmaxf(M, top), down = weight_of(M, l, Mn);
+            l *= down;
+            o = make_float4(o.x * down, o.y * down, o.z * down, o.w * down);
+            M = Mn;
             const float e = weight_of(ml.x, ml.y, M);
-            const float4 x = *reinterpret_cast<const float4 *>(p.part_o + slot(q) * D + 4 * lane);
-            l += e * ml.y;
-            if (e != 0.0f) o = make_float4(o.x + e * x.x, o.y + e * x.y, o.z + e * x.z, o.w + e * x.w);
+            float sum = e * ml.y;
+#pragma unroll
+            for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            l += sum;
+#pragma unroll 4
+            for (int q = 0; q < n; ++q) {
+                const float eq = __shfl_sync(0xffffffffu, e, q);
+                const float4 x = *reinterpret_cast<const float4 *>(p.part_o + slot(q0 + q) * D + 4 * lane);
+                if (eq != 0.0f) o = make_float4(o.x + eq * x.x, o.y + eq * x.y, o.z + eq * x.z, o.w + eq * x.w);
+            }
         }
         const int node = (row0 + row) / a.rep, head = g * a.rep + (row0 + row) % a.rep;
         store_row(a, ((size_t)st.x * a.N + node) * a.Hq + head, lane, M, l, o);
