@@ -17,7 +17,7 @@
 //   warp 1, 2     the MMAs of S, and of P V (one thread issues an MMA about every 110 cycles: two threads)
 //   warp 3        looks ahead: the places and scales of the next 32 tiles, a tile a lane (two dependent loads, which
 //                 whoever needs them would wait for tile by tile)
-//   warps 4..7    V codes to fp16; Q's parts, row scales and ancestor bits of the next unit; the tree's K and V
+//   warps 4..7    V codes to fp16; Q's parts, row scales and parents of the next unit; the tree's K and V
 //   warps 8..15   softmax, two warps for each quarter of the rows, a row a thread: each takes one of the tile's two groups
 //                 of 64 keys (so one scale), and they exchange the maxima; at the end of a unit its results
 // Tensor memory: O 128 columns, two tiles of S, one of P (fp16 pairs), Q's parts.  S is free for the tile after next once the
@@ -60,7 +60,7 @@ struct Smem {
     uint64_t tree_rows;                          // the tree's K is in its stage
     uint64_t c_sync;                             // warps 4..7 among themselves (a wait that ends, unlike bar.sync)
     uint64_t mma_done[2];
-    uint64_t anc[2][64];
+    int par[2][64];                              // a node's parent, -1 where its path ends [unit parity]
     float qf[2][ROWS];
     float mx[2][2][ROWS];                        // [tile parity][half][row]
     float l[2][ROWS];                            // [half][row]
@@ -130,7 +130,12 @@ struct Walk {
         i1 = (int)min((long long)nt, left);
         return true;
     }
-    E3_DEV bool is_tree(const Wide &p, int i) const { return p.a.tree_k && i == nt - 1; }
+    // the tree comes before the last three tiles of the prefix, which hide its conversion
+    E3_DEV int tree_at(const Wide &p) const { return p.a.tree_k ? max(0, nt - 4) : nt; }
+    E3_DEV bool is_tree(const Wide &p, int i) const { return i == tree_at(p); }
+    E3_DEV bool has_tree(const Wide &p) const { return i0 <= tree_at(p) && tree_at(p) < i1; }
+    // the first place of a tile that is not the tree
+    E3_DEV int place(const Wide &p, int i) const { return (i - (i > tree_at(p) ? 1 : 0)) * BK; }
 };
 
 // 8 fp32 as the two e4m3 parts, 8 bytes each
@@ -173,40 +178,11 @@ E3_DEV void store_parts(uint4 x, float up, bool odd, uint8_t *tile, uint32_t apa
     *reinterpret_cast<uint2 *>(at + apart) = lo;
 }
 
-// The nodes that each node sees, by a warp: every node's set joined with that of the node it has got to, which moves
-// twice as far each time
-E3_DEV void tree_paths(const CacheAttn &a, int b, bool report, int lane, uint64_t *anc) {
-    int to[2];
-    uint64_t bits[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int i = lane + 32 * h;
-        const int q = i < a.N ? __ldg(a.parents + (size_t)b * a.N + i) : -1;
-        const bool bad = i < a.N && (i == 0 ? q != -1 : q < 0 || q >= i);
-        if (bad && report) flag(a.dev_status, EAGLE3_DEV_BAD_TREE);
-        to[h] = i == 0 || bad ? -1 : q;
-        bits[h] = 1ull << i;
-    }
-    for (int step = 0; step < 6; ++step) {
-        uint64_t more[2];
-        int next[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int from = max(0, to[h]);
-            const uint64_t b0 = __shfl_sync(0xffffffffu, bits[0], from & 31), b1 = __shfl_sync(0xffffffffu, bits[1], from & 31);
-            const int n0 = __shfl_sync(0xffffffffu, to[0], from & 31), n1 = __shfl_sync(0xffffffffu, to[1], from & 31);
-            more[h] = to[h] < 0 ? 0ull : from < 32 ? b0 : b1;
-            next[h] = to[h] < 0 ? -1 : from < 32 ? n0 : n1;
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            bits[h] |= more[h];
-            to[h] = next[h];
-        }
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-        if (lane + 32 * h < a.N) anc[lane + 32 * h] = bits[h];
+// The nodes that a node sees: itself and its path
+E3_DEV uint64_t path_of(const int *par, int i) {
+    uint64_t bits = 0;
+    for (; i >= 0; i = par[i]) bits |= 1ull << i;
+    return bits;
 }
 
 E3_DEV float max3(float a, float b, float c) {
@@ -483,9 +459,9 @@ __global__ void __launch_bounds__(NT, 1)
                     int row[2] = {-64, -64}, ks[2] = {127, 127}, vs[2] = {1, 1};
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const long long pos = (long long)(i + lane) * BK + h * 64;
-                        if (pos >= w.L) continue;
-                        const int page = __ldg(bt + (int)pos / a.block_size), place = (int)pos % a.block_size;
+                        const int pos = w.place(p, i + lane) + h * 64;
+                        if (pos >= w.L) continue;   // (the tree's own tile is not loaded whatever stands here)
+                        const int page = __ldg(bt + pos / a.block_size), place = pos % a.block_size;
                         if (page < 0 || page >= a.n_pages) continue;
                         row[h] = (page * a.Hkv + g) * a.block_size + place;
                         const size_t at = ((size_t)page * a.Hkv + g) * sgroups + place / EAGLE3_KV_GROUP;
@@ -522,8 +498,16 @@ __global__ void __launch_bounds__(NT, 1)
                 ok = false;
                 break;
             }
-            const bool tree = a.tree_k && w.i1 == w.nt;
+            const bool tree = w.has_tree(p);
             tc::fence_after();
+            // the tree's parents, which the rows' paths are followed through; the loads return while Q is loaded
+            int par[2] = {-1, -1};
+            if (cw == 0 && tree) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (lane + 32 * h < a.N) par[h] = __ldg(a.parents + (size_t)w.b * a.N + lane + 32 * h);
+            }
+            const int L_given = __ldg(a.prefix_len + w.b);
             // ---- Q's parts, a row a thread.  Loaded by 4 lanes a row, 32 dims at a time, twice (the second time from the
             // first-level cache): for the rows' maxima, then through shared memory to the rows' threads
             {
@@ -534,7 +518,7 @@ __global__ void __launch_bounds__(NT, 1)
                     return __ldg(reinterpret_cast<const uint4 *>(a.q + row_at(p, w.b, g, row0 + row)) + 4 * c + (lane & 3));
                 };
                 uint32_t top[4] = {0, 0, 0, 0};
-#pragma unroll 2
+#pragma unroll
                 for (int c = 0; c < 4; ++c)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) top[j] = max(top[j], amax_bits(load(j, c)));
@@ -590,12 +574,19 @@ __global__ void __launch_bounds__(NT, 1)
                 }
                 tc::tmem_st_wait();
                 ss.qf[u][r] = a.scale_log2 * scale_of(byte);
+                if (cw == 0) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int i = lane + 32 * h;
+                        const bool none = i == 0 || par[h] < 0 || par[h] >= i;   // the root, or a parent that is none
+                        ss.par[u][i] = none ? -1 : par[h];
+                        if (RARELY(tree && i < a.N && none && !(i == 0 && par[h] == -1)) && w.k == 0)
+                            flag(a.dev_status, EAGLE3_DEV_BAD_TREE);
+                    }
+                    if (RARELY(L_given < 0 || L_given > a.max_prefix) && lane == 0 && w.k == 0 && w.i0 == 0)
+                        flag(a.dev_status, EAGLE3_DEV_CAPACITY);
+                }
                 tc::fence_before();
-            }
-            if (cw == 0) {
-                if (tree) tree_paths(a, w.b, w.k == 0, lane, ss.anc[u]);
-                const int L = __ldg(a.prefix_len + w.b);
-                if (lane == 0 && (L < 0 || L > a.max_prefix) && w.k == 0 && w.i0 == 0) flag(a.dev_status, EAGLE3_DEV_CAPACITY);
             }
             __syncwarp();
             if (lane == 0) {
@@ -626,7 +617,7 @@ __global__ void __launch_bounds__(NT, 1)
                     };
                     // the largest of all rows, K's and V's in one word (a row behind the last is the last again)
                     uint32_t both = 0;
-#pragma unroll 4
+#pragma unroll
                     for (int row = r0; row < BT; row += 8)
                         both = max_u16x2(both, amax_bits(load(a.tree_k, row)) | amax_bits(load(a.tree_v, row)) << 16);
                     const bool odd_k = __any_sync(0xffffffffu, (both & 0xffffu) >= BF16_INF);
@@ -701,7 +692,8 @@ __global__ void __launch_bounds__(NT, 1)
                 const int c = (lane & 3) + (lane >> 3 & 1) * 4, k0 = cw * 32 + (lane >> 2 & 1) + (lane >> 4) * 2;
                 const uint8_t *src = smp + OFF_VR + sv * K_TILE + k0 * 128;
                 uint8_t *to = dst + (c >> 2) * (V_TILE / 2) + k0 * 128;
-                const bool cut = i * BK + BK > w.L;
+                const int first = w.place(p, i);
+                const bool cut = first + BK > w.L;
 #pragma unroll
                 for (int it = 0; it < 8; it += 4) {
                     uint4 x[4];
@@ -711,7 +703,7 @@ __global__ void __launch_bounds__(NT, 1)
                     if (RARELY(cut)) {            // whatever lies behind the last key
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            if (i * BK + k0 + 4 * (it + j) >= w.L) x[j] = make_uint4(0, 0, 0, 0);
+                            if (first + k0 + 4 * (it + j) >= w.L) x[j] = make_uint4(0, 0, 0, 0);
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -773,7 +765,7 @@ __global__ void __launch_bounds__(NT, 1)
                 // (a factor that underflows would make NaN of the masked scores; a NaN stays)
                 float f = fr * scale_of(half ? sb.y : sb.x);
                 f = f < FLT_MIN ? FLT_MIN : f;
-                const int keys = tree ? -1 : w.L - i * BK - 64 * half;   // of this half, 64 or more: all
+                const int keys = tree ? -1 : w.L - w.place(p, i) - 64 * half;   // of this half, 64 or more: all
                 tc::tmem_ld32_wait(sc);
                 tc::tmem_ld32_wait(sc + 32);
                 tc::fence_before();
@@ -781,7 +773,7 @@ __global__ void __launch_bounds__(NT, 1)
                 if (lane == 0) tc::mbar_arrive(bar(ss.s_empty[t & 1]));
                 if (RARELY(tree || keys < 64)) {
                     uint64_t vis = keys > 0 ? (1ull << keys) - 1ull : 0ull;
-                    if (tree) vis = half == 0 && r < nrows ? ss.anc[u][row_node(p, row0 + r)] : 0ull;
+                    if (tree) vis = half == 0 && r < nrows ? path_of(ss.par[u], row_node(p, row0 + r)) : 0ull;
                     const uint32_t v0 = (uint32_t)vis, v1 = (uint32_t)(vis >> 32);
 #pragma unroll
                     for (int e = 0; e < 64; ++e) sc[e] = ((e < 32 ? v0 : v1) >> (e & 31)) & 1u ? sc[e] : -INFINITY;
@@ -857,7 +849,7 @@ __global__ void __launch_bounds__(NT, 1)
             const int node = row_node(p, row0 + r), head = g * a.rep + row0 + r - node * a.rep;
             const size_t at = ((size_t)w.b * a.N + (mine ? node : 0)) * a.Hq + (mine ? head : 0);
             const size_t part = (size_t)(2 * blockIdx.x + (w.n > 0 ? 1 : 0)) * ROWS + r;
-            const uint64_t anc = odd_v && mine ? ss.anc[u][node] : 0;
+            const uint64_t anc = odd_v && mine ? path_of(ss.par[u], node) : 0;
             // (a row without a key has summed up nothing)
             const float back = scale_of(evref), inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
 #pragma unroll 1
