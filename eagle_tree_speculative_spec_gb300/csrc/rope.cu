@@ -11,6 +11,7 @@
 #include "rope.cuh"
 
 #include <cmath>
+#include <type_traits>
 
 namespace e3 {
 namespace {
@@ -37,25 +38,27 @@ struct Params {
     void *out;
 };
 
-// V consecutive elements as fp32
-template <int V, typename T>
-E3_DEV void load(const T *p, float (&v)[V]) {
-    if constexpr (V == 1) {
-        v[0] = (float)*p;
-    } else if constexpr (sizeof(T) == 2) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(p);
-        const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&u);
+// V consecutive elements as they lie in memory
+template <typename T, int V>
+struct Run {
+    using Word = std::conditional_t<V == 1, T, uint4>;
+    static constexpr int WORDS = V * sizeof(T) / sizeof(Word);
+    Word w[WORDS];
+
+    E3_DEV void load(const T *p) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = __bfloat1622float2(h[i]);
-            v[2 * i] = f.x;
-            v[2 * i + 1] = f.y;
-        }
-    } else {
-        *reinterpret_cast<float4 *>(&v[0]) = *reinterpret_cast<const float4 *>(p);
-        *reinterpret_cast<float4 *>(&v[4]) = *reinterpret_cast<const float4 *>(p + 4);
+        for (int i = 0; i < WORDS; ++i) w[i] = reinterpret_cast<const Word *>(p)[i];
     }
-}
+    E3_DEV void unpack(float (&v)[V]) const {
+        if constexpr (V == 1) {
+            v[0] = (float)w[0];
+        } else {
+            const T *e = reinterpret_cast<const T *>(w);
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = (float)e[i];
+        }
+    }
+};
 
 template <int V, typename T>
 E3_DEV void store(T *p, const float (&v)[V]) {
@@ -75,7 +78,8 @@ E3_DEV void store(T *p, const float (&v)[V]) {
 
 // V = 8 pairs a unit where rotary_dim is a multiple of 16 (16- and 32-byte accesses), else one
 template <typename T, int V, bool INTERLEAVED>
-__global__ void __launch_bounds__(NT) rope_kernel(const Params p) {
+__global__ void __launch_bounds__(NT, 3) rope_kernel(const Params p) {
+    constexpr int AHEAD = V * sizeof(T) > 16 ? 2 : 4;   // heads that a thread loads before it turns the first
     __shared__ float2 cs[NT];   // [row][pair]
     pdl_wait();
     pdl_trigger();
@@ -89,35 +93,49 @@ __global__ void __launch_bounds__(NT) rope_kernel(const Params p) {
     }
     __syncthreads();
     const int units = half / V + (p.D - p.R) / V;   // runs of pairs, then runs that are copied; at most NT
-    const int per_pass = NT / units, hh = threadIdx.x / units, unit = threadIdx.x % units;
-    if (hh >= per_pass) return;
+    const int slots = NT / units, slot = threadIdx.x / units, unit = threadIdx.x % units;
+    const int at_once = min(p.rows_per_cta, slots), step = slots / at_once;   // rows at a time, heads of each
+    if (slot >= at_once * step) return;
     const bool copy = unit >= half / V;
     if (copy && p.x == p.out) return;
     const int j = unit * V;
     const int da = copy ? p.R + (unit - half / V) * V : INTERLEAVED ? 2 * j : j;
     const int db = INTERLEAVED ? 2 * j + V : half + j;
-    for (int r = 0; r < rn; ++r) {
+    for (int r = slot / step; r < rn; r += at_once) {
         const T *x = (const T *)p.x + (r0 + r) * p.x_rs;
         T *out = (T *)p.out + (r0 + r) * p.o_rs;
-        for (int h = h0 + hh; h < h1; h += per_pass) {
-            const size_t at = (size_t)h * p.D;
-            float a[V], b[V];
-            load<V>(x + at + da, a);
-            if (!copy) {
-                load<V>(x + at + db, b);
+        float2 w[V];
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float2 w = cs[r * half + j + i];
-                    // the pair's two elements: at the same place of both runs, or next to each other
-                    float &u = INTERLEAVED && V > 1 ? (2 * i < V ? a[(2 * i) % V] : b[(2 * i) % V]) : a[i];
-                    float &v = INTERLEAVED && V > 1 ? (2 * i < V ? a[(2 * i + 1) % V] : b[(2 * i + 1) % V]) : b[i];
-                    const float c = u * w.x - v * w.y, s = v * w.x + u * w.y;
-                    u = c;
-                    v = s;
-                }
-                store<V>(out + at + db, b);
+        for (int i = 0; i < V; ++i) w[i] = copy ? make_float2(1.0f, 0.0f) : cs[r * half + j + i];
+        for (int h = h0 + slot % step; h < h1; h += AHEAD * step) {
+            Run<T, V> ra[AHEAD], rb[AHEAD];
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                if (h + k * step >= h1) break;
+                ra[k].load(x + (size_t)(h + k * step) * p.D + da);
+                if (!copy) rb[k].load(x + (size_t)(h + k * step) * p.D + db);
             }
-            store<V>(out + at + da, a);
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                if (h + k * step >= h1) break;
+                T *o = out + (size_t)(h + k * step) * p.D;
+                float a[V], b[V];
+                ra[k].unpack(a);
+                if (!copy) {
+                    rb[k].unpack(b);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        // the pair's two elements: at the same place of both runs, or next to each other
+                        float &u = INTERLEAVED && V > 1 ? (2 * i < V ? a[(2 * i) % V] : b[(2 * i) % V]) : a[i];
+                        float &v = INTERLEAVED && V > 1 ? (2 * i < V ? a[(2 * i + 1) % V] : b[(2 * i + 1) % V]) : b[i];
+                        const float c = u * w[i].x - v * w[i].y, s = v * w[i].x + u * w[i].y;
+                        u = c;
+                        v = s;
+                    }
+                    store<V>(o + db, b);
+                }
+                store<V>(o + da, a);
+            }
         }
     }
 }
