@@ -26,7 +26,7 @@ struct Params {
     int B, Hkv, D, n_rows, max_new, rows_per_seq, max_blocks, block_size, n_pages, R, half;
     int groups_per_seq;      // groups that max_new tokens can touch
     int jobs_per_cta;        // of the 2 * Hkv (head, K or V) jobs of a group
-    int interleaved, wide;   // wide: the partner of 8 dims is 8 dims that start on 16 bytes
+    int interleaved, paired;   // paired: dims lie in whole runs of 8 pairs
     float amplitude;
     int64_t rs;
     const __nv_bfloat16 *k, *v;
@@ -85,61 +85,76 @@ E3_DEV int source_row(const Params &p, int b, int j) {
     return r < 0 || r >= p.n_rows ? -1 : (int)r;
 }
 
-E3_DEV void unpack8(uint4 u, float (&v)[8]) {
-    const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&u);
+// Cosines and sines of a row are kept as pairs of pairs, in fours: within a four they are swapped about by the four's
+// number, so that the lanes of eight consecutive fours meet all banks (a plain order: 4 of them at a time in 2 banks).
+E3_DEV int two_at(int two) { return (two & ~3) | ((two ^ two >> 3) & 3); }
+E3_DEV int pair_at(int j) { return two_at(j >> 1) * 2 + (j & 1); }
+E3_DEV int cs_pitch(int half) { return (half + 7) & ~7; }
+
+E3_DEV void unpack8(uint4 u, float *v) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 f = __bfloat1622float2(h[i]);
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
 }
 
-// 8 dims of a key row from d0 on, turned; cs: the row's cosines and sines
-E3_DEV void turn8(const Params &p, const __nv_bfloat16 *row, int d0, const float2 *cs, float (&v)[8]) {
-    if (d0 >= p.R) return;
-    if (p.interleaved) {
-        if (d0 + 8 <= p.R) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 w = cs[d0 / 2 + i];
-                const float a = v[2 * i], b = v[2 * i + 1];
-                v[2 * i] = a * w.x - b * w.y;
-                v[2 * i + 1] = b * w.x + a * w.y;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (d0 + 2 * i >= p.R) break;
-                const float2 w = cs[d0 / 2 + i];
-                const float a = v[2 * i], b = v[2 * i + 1];
-                v[2 * i] = a * w.x - b * w.y;
-                v[2 * i + 1] = b * w.x + a * w.y;
-            }
-        }
-        return;
-    }
-    if (p.wide) {
-        const bool upper = d0 >= p.half;
-        const int j = upper ? d0 - p.half : d0;
-        float o[8];
-        unpack8(*reinterpret_cast<const uint4 *>(row + (upper ? j : d0 + p.half)), o);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float2 w = cs[j + i];
-            v[i] = upper ? v[i] * w.x + o[i] * w.y : v[i] * w.x - o[i] * w.y;
-        }
-        return;
-    }
+E3_DEV void turn(float &a, float &b, float cos, float sin) {
+    const float x = a * cos - b * sin;
+    b = b * cos + a * sin;
+    a = x;
+}
+
+// A thread's unit, 16 dims of a row: the runs of 8 dims from da and from db on, which hold 8 whole pairs where
+// p.paired; db < 0: the row ends after the first.
+struct Unit {
+    int da, db, pair;   // pair: the first of its pairs, -1 where it is not turned as a whole
+};
+E3_DEV Unit unit_of(const Params &p, int u) {
+    if (p.paired && !p.interleaved && u < p.R / 16) return {8 * u, p.half + 8 * u, 8 * u};
+    return {16 * u, 16 * u + 8 < p.D ? 16 * u + 8 : -1, p.paired && u < p.R / 16 ? 8 * u : -1};
+}
+
+// 8 dims from d0 on of a key row whose pairs do not lie in whole runs; cs: the row's cosines and sines
+E3_DEV void turn_run(const Params &p, const __nv_bfloat16 *row, int d0, const float2 *cs, float *v) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int d = d0 + i;
         if (d >= p.R) break;
-        const bool upper = d >= p.half;
-        const int j = upper ? d - p.half : d;
-        const float2 w = cs[j];
-        const float o = (float)row[upper ? j : d + p.half];
-        v[i] = upper ? v[i] * w.x + o * w.y : v[i] * w.x - o * w.y;
+        if (p.interleaved) {
+            if (i % 2 == 0) {
+                const float2 w = cs[pair_at(d / 2)];
+                turn(v[i], v[i + 1], w.x, w.y);
+            }
+        } else {
+            const bool upper = d >= p.half;
+            const int j = upper ? d - p.half : d;
+            const float2 w = cs[pair_at(j)];
+            const float o = (float)row[upper ? j : d + p.half];
+            v[i] = upper ? v[i] * w.x + o * w.y : v[i] * w.x - o * w.y;
+        }
+    }
+}
+
+template <bool PAIRED>
+E3_DEV void turn_unit(const Params &p, const Unit &un, const __nv_bfloat16 *row, const float2 *cs, float *v) {
+    if constexpr (!PAIRED) {
+        turn_run(p, row, un.da, cs, v);
+        if (un.db >= 0) turn_run(p, row, un.db, cs, v + 8);
+        return;
+    }
+    if (un.pair < 0) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 w = reinterpret_cast<const float4 *>(cs)[two_at(un.pair / 2 + i)];
+        if (p.interleaved) {
+            turn(v[4 * i], v[4 * i + 1], w.x, w.y);
+            turn(v[4 * i + 2], v[4 * i + 3], w.z, w.w);
+        } else {
+            turn(v[2 * i], v[8 + 2 * i], w.x, w.y);
+            turn(v[2 * i + 1], v[9 + 2 * i], w.z, w.w);
+        }
     }
 }
 
@@ -154,137 +169,183 @@ E3_DEV uint2 scaled_down(uint2 c, float factor) {
     return make_uint2(w[0], w[1]);
 }
 
-// One job (a head's keys or values of a group) by THREADS threads, ITEMS runs of 8 dims each.  cs: cosines and sines by
-// [place - lo][pair], or null; scratch: a word a warp for the CTA's maximum.
-template <int THREADS, int ITEMS, bool E4M3>
-E3_DEV void append_job(const Params &p, const Span &s, int page, int job, int t, const float2 *cs, float *scratch) {
-    const bool is_v = job >= p.Hkv;
-    const int h = is_v ? job - p.Hkv : job;
-    const int cpr = p.D / 8, n = (s.hi - s.lo) * cpr;
-    const __nv_bfloat16 *src = (is_v ? p.v : p.k) + (size_t)h * p.D;
-    uint8_t *dst = is_v ? p.vc : p.kc;
-    float val[ITEMS][8];
-    bool have[ITEMS];
-    float top = 0.0f;
+E3_DEV uint2 codes8(const float *v, float inv) {
+    uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-        const int it = t + i * THREADS;
-        const int row = it / cpr, d0 = it % cpr * 8;
-        have[i] = it < n;
-        int r = -1;
-        if (have[i]) {
-            r = source_row(p, s.b, s.j0 + row);
-            if (r < 0 && job == 0 && d0 == 0) flag(p.dev_status, EAGLE3_DEV_BAD_TOKEN);
-            have[i] = r >= 0;
-        }
-        if (have[i]) unpack8(*reinterpret_cast<const uint4 *>(src + r * p.rs + d0), val[i]);
-        if (have[i] && cs && !is_v) turn8(p, src + r * p.rs, d0, cs + row * p.half, val[i]);
-        if (E4M3 && have[i]) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float a = fabsf(val[i][e]);
-                if (a <= FLT_MAX)
-                    top = fmaxf(top, a);
-                else
-                    val[i][e] = __int_as_float(0x7fc00000);
-            }
-        }
-    }
-    if constexpr (!E4M3) {
-#pragma unroll
-        for (int i = 0; i < ITEMS; ++i) {
-            if (!have[i]) continue;
-            const int it = t + i * THREADS;
-            const int place = s.lo + it / cpr, d0 = it % cpr * 8;
-            // a page may end inside the group
-            const long long pos = (long long)s.page * p.block_size + s.place + place;
-            const int id = __ldg(p.block_table + (size_t)s.b * p.max_blocks + (int)(pos / p.block_size));
-            if (id < 0 || id >= p.n_pages) {
-                if (job == 0 && d0 == 0) flag(p.dev_status, EAGLE3_DEV_CAPACITY);
-                continue;
-            }
-            const long long slot = (long long)id * p.block_size + pos % p.block_size;
-            uint4 u;
-            __nv_bfloat162 *b2 = reinterpret_cast<__nv_bfloat162 *>(&u);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) b2[e] = __floats2bfloat162_rn(val[i][2 * e], val[i][2 * e + 1]);
-            *reinterpret_cast<uint4 *>(dst + ((size_t)slot * p.Hkv + h) * p.D * 2 + d0 * 2) = u;
-        }
-        return;
-    } else {
-#pragma unroll
-        for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-        uint8_t *scales = (is_v ? p.vs : p.ks) + ((size_t)page * p.Hkv + h) * (p.block_size / GROUP) + s.place / GROUP;
-        int old = s.lo > 0 ? *scales : 0;
-        if constexpr (THREADS > 32) {
-            if ((t & 31) == 0) scratch[t >> 5] = top;
-            __syncthreads();   // the scale has been read by everyone too
-#pragma unroll
-            for (int w = 0; w < THREADS / 32; ++w) top = fmaxf(top, scratch[w]);
-            __syncthreads();
-        } else {
-            __syncwarp();
-        }
-        const int byte = max(old, scale_byte(top));
-        if (t == 0) *scales = (uint8_t)byte;
-        const float inv = inverse_scale(byte);
-        uint8_t *codes = dst + (((size_t)page * p.Hkv + h) * p.block_size + s.place) * p.D;
-        if (s.lo > 0 && byte > old) {
-            // steps far below the new one leave nothing but the sign
-            const float factor = byte - old > 40 ? 0.0f : __int_as_float((127 - (byte - old)) << 23);
-            for (int it = t; it < s.lo * cpr; it += THREADS) {
-                uint2 *c = reinterpret_cast<uint2 *>(codes + (size_t)it * 8);
-                *c = scaled_down(*c, factor);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < ITEMS; ++i) {
-            if (!have[i]) continue;
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = to_e4m3x2(val[i][2 * e] * inv, val[i][2 * e + 1] * inv);
-            *reinterpret_cast<uint2 *>(codes + (size_t)s.lo * p.D + (size_t)(t + i * THREADS) * 8) =
-                make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
-        }
-    }
+    for (int e = 0; e < 4; ++e) w[e] = to_e4m3x2(v[2 * e] * inv, v[2 * e + 1] * inv);
+    return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
 }
 
-// grid: (group of a sequence, share of its jobs, sequence)
-template <int ITEMS, bool E4M3, bool BY_WARP>
-__global__ void __launch_bounds__(NT) append_kernel(const Params p) {
-    extern __shared__ float2 cs[];   // [new rows of the group][pair]
-    __shared__ float scratch[NT / 32];
+E3_DEV uint4 bf16x8(const float *v) {
+    uint4 u;
+    __nv_bfloat162 *b2 = reinterpret_cast<__nv_bfloat162 *>(&u);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) b2[e] = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+    return u;
+}
+
+// A job is a head's keys (even) or values (odd) of a group, by a warp or by the CTA.  grid: (group of a sequence, share
+// of its jobs, sequence).  A thread keeps its unit and its rows, ITEMS of them, for all of its jobs, and loads the
+// next job's before it converts this one's.
+template <int ITEMS, bool E4M3, bool BY_WARP, bool PAIRED>
+__global__ void __launch_bounds__(NT, ITEMS == 2 && PAIRED ? 3 : 1) append_kernel(const Params p) {
+    constexpr int THREADS = BY_WARP ? 32 : NT;
+    extern __shared__ float4 cs4[];   // [new rows of the group][pair]
+    __shared__ float scratch[2][NT / 32];
+    float2 *const cs = reinterpret_cast<float2 *>(cs4);
     pdl_wait();
     pdl_trigger();
     Span s;
     if (!find_span(p, blockIdx.z, blockIdx.x, threadIdx.x == 0 && blockIdx.y == 0, s)) return;
+    const int32_t *bt = p.block_table + (size_t)s.b * p.max_blocks;
     int page = -1;
     if (E4M3) {
-        page = __ldg(p.block_table + (size_t)s.b * p.max_blocks + s.page);
+        page = __ldg(bt + s.page);
         if (page < 0 || page >= p.n_pages) {
             if (threadIdx.x == 0 && blockIdx.y == 0) flag(p.dev_status, EAGLE3_DEV_CAPACITY);
             return;
         }
     }
-    const int j0 = blockIdx.y * p.jobs_per_cta, j1 = min(2 * p.Hkv, j0 + p.jobs_per_cta);
-    if (p.table && j0 < p.Hkv) {   // some of the CTA's jobs are keys
-        for (int i = threadIdx.x; i < (s.hi - s.lo) * p.half; i += NT)
-            cs[i] = turned(s.len + s.j0 + i / p.half, __ldg(p.table + i % p.half), p.amplitude);
+    const int warp = threadIdx.x >> 5, t = BY_WARP ? threadIdx.x & 31 : threadIdx.x;
+    const int units = (p.D + 15) / 16, step = THREADS / units;   // rows at a time
+    const int row0 = t / units, u = t - row0 * units;
+    const bool reports = blockIdx.y == 0 && u == 0 && (!BY_WARP || warp == 0);
+    const Unit un = unit_of(p, u);
+    int src[ITEMS], slot[ITEMS];   // the rows they come from and, bf16, the places they go to; src < 0: none
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+        const int row = row0 + i * step;
+        src[i] = -1;
+        if (row0 < step && row < s.hi - s.lo) {
+            src[i] = source_row(p, s.b, s.j0 + row);
+            if (src[i] < 0 && reports) flag(p.dev_status, EAGLE3_DEV_BAD_TOKEN);
+        }
+        if (!E4M3 && src[i] >= 0) {   // a page may end inside the group
+            const int pos = s.len + s.j0 + row, block = pos / p.block_size;
+            const int id = __ldg(bt + block);
+            slot[i] = id * p.block_size + (pos - block * p.block_size);
+            if (id < 0 || id >= p.n_pages) {
+                if (reports) flag(p.dev_status, EAGLE3_DEV_CAPACITY);
+                src[i] = -1;
+            }
+        }
     }
+    uint4 next[ITEMS][2];
+    auto fetch = [&](int job) {
+        const __nv_bfloat16 *from = (job & 1 ? p.v : p.k) + (size_t)(job >> 1) * p.D;
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            next[i][0] = next[i][1] = make_uint4(0, 0, 0, 0);
+            if (src[i] < 0) continue;
+            next[i][0] = *reinterpret_cast<const uint4 *>(from + src[i] * p.rs + un.da);
+            if (un.db >= 0) next[i][1] = *reinterpret_cast<const uint4 *>(from + src[i] * p.rs + un.db);
+        }
+    };
+    const int j0 = blockIdx.y * p.jobs_per_cta, j1 = min(2 * p.Hkv, j0 + p.jobs_per_cta);
+    const int first = BY_WARP ? j0 + warp : j0, jump = BY_WARP ? NT / 32 : 1;
+    if (first < j1) fetch(first);
+    const int pitch = cs_pitch(p.half);
+    if (p.table)
+        for (int i = threadIdx.x; i < (s.hi - s.lo) * p.half; i += NT) {
+            const int row = i / p.half, j = i - row * p.half;
+            cs[row * pitch + pair_at(j)] = turned(s.len + s.j0 + row, __ldg(p.table + j), p.amplitude);
+        }
     __syncthreads();
-    const float2 *angles = p.table ? cs : nullptr;
-    if constexpr (BY_WARP) {
-        for (int job = j0 + (threadIdx.x >> 5); job < j1; job += NT / 32)
-            append_job<32, ITEMS, E4M3>(p, s, page, job, threadIdx.x & 31, angles, nullptr);
-    } else {
-        for (int job = j0; job < j1; ++job) append_job<NT, ITEMS, E4M3>(p, s, page, job, threadIdx.x, angles, scratch);
+    int parity = 0;
+    for (int job = first; job < j1; job += jump) {
+        const bool is_v = job & 1;
+        const int h = job >> 1;
+        const size_t head_page = (size_t)page * p.Hkv + h;
+        uint8_t *scales = nullptr;
+        int old = 0;
+        if (E4M3) {
+            scales = (is_v ? p.vs : p.ks) + head_page * (p.block_size / GROUP) + s.place / GROUP;
+            if (s.lo > 0) old = *scales;
+        }
+        float val[ITEMS][16];
+        float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {
+            unpack8(next[i][0], val[i]);
+            unpack8(next[i][1], val[i] + 8);
+        }
+        if (job + jump < j1) fetch(job + jump);
+        if (p.table && !is_v) {
+#pragma unroll
+            for (int i = 0; i < ITEMS; ++i)
+                if (src[i] >= 0)
+                    turn_unit<PAIRED>(p, un, p.k + (size_t)h * p.D + src[i] * p.rs, cs + (row0 + i * step) * pitch, val[i]);
+        }
+        uint8_t *dst = is_v ? p.vc : p.kc;
+        if constexpr (!E4M3) {
+#pragma unroll
+            for (int i = 0; i < ITEMS; ++i) {
+                if (src[i] < 0) continue;
+                uint8_t *to = dst + ((size_t)slot[i] * p.Hkv + h) * p.D * 2;
+                *reinterpret_cast<uint4 *>(to + un.da * 2) = bf16x8(val[i]);
+                if (un.db >= 0) *reinterpret_cast<uint4 *>(to + un.db * 2) = bf16x8(val[i] + 8);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < ITEMS; ++i)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(val[i][e]));   // (passes over NaN)
+            if (top > FLT_MAX) {   // infinities become NaN, and no scale follows them
+                top = 0.0f;
+#pragma unroll
+                for (int i = 0; i < ITEMS; ++i)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float a = fabsf(val[i][e]);
+                        if (a <= FLT_MAX)
+                            top = fmaxf(top, a);
+                        else
+                            val[i][e] = __int_as_float(0x7fc00000);
+                    }
+            }
+            // magnitudes are in the order of their bits
+            top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+            if constexpr (!BY_WARP) {
+                if ((t & 31) == 0) scratch[parity][warp] = top;
+                __syncthreads();   // the scale has been read by everyone too
+#pragma unroll
+                for (int w = 0; w < NT / 32; ++w) top = fmaxf(top, scratch[parity][w]);
+                parity ^= 1;
+            }
+            const int byte = max(old, scale_byte(top));
+            if (t == 0) *scales = (uint8_t)byte;
+            uint8_t *codes = dst + (head_page * p.block_size + s.place) * p.D;
+            const float inv = inverse_scale(byte);
+#pragma unroll
+            for (int i = 0; i < ITEMS; ++i) {
+                if (src[i] < 0) continue;
+                uint8_t *to = codes + (size_t)(s.lo + row0 + i * step) * p.D;
+                *reinterpret_cast<uint2 *>(to + un.da) = codes8(val[i], inv);
+                if (un.db >= 0) *reinterpret_cast<uint2 *>(to + un.db) = codes8(val[i] + 8, inv);
+            }
+            if (s.lo > 0 && byte > old) {
+                // steps far below the new one leave nothing but the sign
+                const float factor = byte - old > 40 ? 0.0f : __int_as_float((127 - (byte - old)) << 23);
+                uint2 *c = reinterpret_cast<uint2 *>(codes);
+                const int n = s.lo * (p.D / 8);
+                constexpr int K = 8;   // loads in flight
+                for (int it = t; it < n; it += K * THREADS) {
+                    uint2 w[K];
+#pragma unroll
+                    for (int k = 0; k < K; ++k) w[k] = it + k * THREADS < n ? c[it + k * THREADS] : make_uint2(0, 0);
+#pragma unroll
+                    for (int k = 0; k < K; ++k)
+                        if (it + k * THREADS < n) c[it + k * THREADS] = scaled_down(w[k], factor);
+                }
+            }
+        }
     }
 }
 
-template <int ITEMS, bool E4M3, bool BY_WARP>
+template <int ITEMS, bool E4M3, bool BY_WARP, bool PAIRED>
 cudaError_t launch(const Params &p, dim3 grid, size_t smem, cudaStream_t stream) {
     static PerDevice<cudaError_t> attr;
-    auto *kernel = append_kernel<ITEMS, E4M3, BY_WARP>;
+    auto *kernel = append_kernel<ITEMS, E4M3, BY_WARP, PAIRED>;
     const cudaError_t e = attr.get([=] {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     GROUP * EAGLE3_ROPE_MAX_DIM / 2 * (int)sizeof(float2));
@@ -292,10 +353,10 @@ cudaError_t launch(const Params &p, dim3 grid, size_t smem, cudaStream_t stream)
     return e != cudaSuccess ? e : launch_pdl(kernel, grid, dim3(NT), smem, stream, p);
 }
 
-template <int ITEMS>
+template <int ITEMS, bool PAIRED>
 cudaError_t launch_by(const Params &p, bool e4m3, bool few, dim3 grid, size_t smem, cudaStream_t stream) {
-    if (e4m3) return few ? launch<ITEMS, true, true>(p, grid, smem, stream) : launch<ITEMS, true, false>(p, grid, smem, stream);
-    return few ? launch<ITEMS, false, true>(p, grid, smem, stream) : launch<ITEMS, false, false>(p, grid, smem, stream);
+    if (e4m3) return few ? launch<ITEMS, true, true, PAIRED>(p, grid, smem, stream) : launch<ITEMS, true, false, PAIRED>(p, grid, smem, stream);
+    return few ? launch<ITEMS, false, true, PAIRED>(p, grid, smem, stream) : launch<ITEMS, false, false, PAIRED>(p, grid, smem, stream);
 }
 
 }  // namespace
@@ -343,7 +404,7 @@ extern "C" eagle3_status_t eagle3_append_kv(const eagle3_append_kv_args_t *a, ea
     p.R = a->rope_table ? a->rotary_dim : 0;
     p.half = p.R / 2;
     p.interleaved = a->rope_layout == EAGLE3_ROPE_INTERLEAVED;
-    p.wide = p.R % 16 == 0;
+    p.paired = p.R % 16 == 0 && p.D % 16 == 0;
     p.amplitude = a->rope_amplitude;
     p.rs = rs;
     p.k = (const __nv_bfloat16 *)a->k_new;
@@ -364,15 +425,19 @@ extern "C" eagle3_status_t eagle3_append_kv(const eagle3_append_kv_args_t *a, ea
     const int reach = p.max_new < p.max_blocks * p.block_size ? p.max_new : p.max_blocks * p.block_size;
     p.groups_per_seq = (reach - 1 + GROUP - 1) / GROUP + 1;
     const int jobs = 2 * p.Hkv;
-    // enough CTAs for every SM to have four; a share of jobs no smaller than its warps when a warp takes a job
+    // enough CTAs for every SM to have three; a share of jobs no smaller than its warps when a warp takes a job
     const int64_t ctas = (int64_t)p.groups_per_seq * p.B;
     int cuts = 1;
-    while (cuts < jobs && ctas * cuts < 4 * device_sm_count()) cuts *= 2;
+    while (cuts < jobs && ctas * cuts < 3 * device_sm_count()) cuts *= 2;
     p.jobs_per_cta = (jobs + cuts - 1) / cuts;
     if (few && p.jobs_per_cta < NT / 32) p.jobs_per_cta = jobs < NT / 32 ? jobs : NT / 32;
     const dim3 grid((unsigned)p.groups_per_seq, (unsigned)((jobs + p.jobs_per_cta - 1) / p.jobs_per_cta), (unsigned)p.B);
-    const size_t smem = (size_t)(few ? FEW : GROUP) * p.half * sizeof(float2);
+    const size_t smem = (size_t)(few ? FEW : GROUP) * ((p.half + 7) / 8 * 8) * sizeof(float2);
     const cudaStream_t st = (cudaStream_t)stream;
-    const cudaError_t e = p.D <= 128 ? launch_by<4>(p, e4m3, few, grid, smem, st) : launch_by<8>(p, e4m3, few, grid, smem, st);
+    cudaError_t e;
+    if (p.paired)
+        e = p.D <= 128 ? launch_by<2, true>(p, e4m3, few, grid, smem, st) : launch_by<4, true>(p, e4m3, few, grid, smem, st);
+    else
+        e = p.D <= 128 ? launch_by<2, false>(p, e4m3, few, grid, smem, st) : launch_by<4, false>(p, e4m3, few, grid, smem, st);
     return e == cudaSuccess ? EAGLE3_OK : EAGLE3_ERR_CUDA;
 }
