@@ -5,16 +5,19 @@
 // node sees the whole prefix plus itself and its ancestors); "EAGLE-3: Engineering Implementation of LLM Inference
 // Acceleration", appendix C (GQA, 1/sqrt(D) scaling).
 //
-// Rows kernel: 16 query rows (row = node * rep + head of the KV group) by the warps of a CTA, each with 32 keys of
-// its own at a time and running maxima and sums of its own, merged at the end in warp order.  Nothing is staged: a
-// lane reads 16 codes of a key row at once, and which dims of K (keys of V) a lane holds is laid out so that they are
-// the B fragments of mma.m16n8k16 after conversion to fp16, which is exact.  The dims of Q and the columns of O are
-// permuted to match.
-//   scores   lane (g, c) of a warp, g = lane / 4, c = lane % 4, reads key g of each 8, dims [16c, 16c + 16) and
-//            [64 + 16c, 64 + 16c + 16): word w of the first run is the fragment of k-step w, the k indices
+// Rows kernel: up to 8 or 16 query rows (row = node * rep + head of the KV group) by the warps of a CTA, each with 32
+// keys of its own at a time and running maxima and sums of its own, merged at the end in warp order.  Nothing is
+// staged: a lane reads 16 codes of a key row at once, and which dims of K (keys of V) a lane holds is laid out so that
+// they are fragments of mma.m16n8k16 after conversion to fp16, which is exact.  The dims are permuted to match.
+//   scores   S = Q K^T: lane (g, c) of a warp, g = lane / 4, c = lane % 4, reads key g of each 8, dims [16c, 16c + 16)
+//            and [64 + 16c, 64 + 16c + 16): word w of the first run is the B fragment of k-step w, the k indices
 //            {2c, 2c + 1, 2c + 8, 2c + 9} being the dims 16c + 4w + {0, 1, 2, 3}
-//   values   keys {2c, 2c + 1, 2c + 8, 2c + 9} of each 16, dims [16g, 16g + 16): byte permutes pair up two keys' codes
-//            of a dim; column tile t of O holds the dims 16n + t, n = 0 .. 7
+//   values   O^T = V^T P^T, so that 8 rows of queries need 8 columns and not a tile of 16: S's registers are P^T's B
+//            fragments as they are.  Keys {2c, 2c + 1, 2c + 8, 2c + 9} of each 16, dims [16g, 16g + 16): byte permutes
+//            pair up two keys' codes of a dim; tile t of O^T holds the dims 16g + 2t (row g) and 16g + 2t + 1
+//            (row g + 8), its columns 2c, 2c + 1 are rows of Q
+// A warp's next K is loaded once the products with this one have been issued, its next V after the weights' products,
+// and the pages two steps ahead: each load has about half a step to arrive, in no registers of its own.
 // Q is scaled by a power of two for each row so that fp16 holds it (bf16's 8 bits fit, elements 2^-36 below the row's
 // largest vanish); the factor comes back with the scale of K's group in fp32.  Weights are held 2^7 up, so that fp16's
 // 11 bits reach down to 2^-21 of the largest, and V's group scale is put on them relative to the largest so far.
@@ -29,14 +32,22 @@ constexpr int D = 128;
 constexpr int CHUNK = 32;           // keys of a warp's step: within one group of 64, so one scale and one page
 constexpr int NW = 4;               // warps
 constexpr int NT = NW * 32;
-constexpr int ROWS = 16;
+constexpr int MAX_ROWS = 16;
 constexpr int O_PITCH = D + 4;
+constexpr int MAX_SPLITS = 512;
 
 E3_DEV void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};\n"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 16 codes that this grid reads once
+E3_DEV uint4 ld_once(const uint8_t *p) {
+    uint4 u;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
+    return u;
 }
 
 // 16 consecutive bf16 as fp16 pairs, times a power of two
@@ -53,95 +64,148 @@ E3_DEV void bf16x16_f16(const __nv_bfloat16 *src, float factor, uint32_t (&out)[
     }
 }
 
-// The running state of a warp: rows g and g + 8 of its 16
+// The running state of a warp, rows g + 8 r
+template <int NR>
 struct RowState {
-    float m[2], l[2];
+    float m[NR], l[NR];   // the maximum and this lane's share of the sum of row g + 8 r
     int ev;               // V's scale byte that o is relative to
-    float o[16][4];
+    float o[8][NR][4];    // dims 16g + 2t + {0, 0, 1, 1} of rows 8r + 2c + {0, 1, 0, 1}
 };
 
-// The weights of a step of 32 keys, as A fragments, from its raw scores s (four tiles of 8 keys) by the rows' factors f;
+// The weights of a step of 32 keys, as B fragments, from its raw scores s (four tiles of 8 keys) by the rows' factors f;
 // seen: bit 2 n + i of a row for this lane's key 2c + i of tile n; ev: V's scale byte.
-E3_DEV void softmax_step(RowState &st, float (&s)[4][4], const float (&f)[2], const uint32_t (&seen)[2], int ev,
-                         uint32_t (&pf)[2][4]) {
-    float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-    for (int n = 0; n < 4; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int r = e >> 1;
-            s[n][e] = (seen[r] >> (2 * n + (e & 1))) & 1u ? s[n][e] * f[r] : -INFINITY;
-            mx[r] = fmaxf(mx[r], s[n][e]);
-        }
+template <int NR>
+E3_DEV void softmax_step(RowState<NR> &st, float (&s)[4][4], const float (&f)[NR], const uint32_t (&seen)[NR], int ev,
+                         uint32_t (&pf)[2][NR][2]) {
+    float mx[NR];
     bool grown = ev > st.ev && ev != 255;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+    for (int r = 0; r < NR; ++r) {
+        mx[r] = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float &x = s[n][2 * r + i];
+                x = (seen[r] >> (2 * n + i)) & 1u ? x * f[r] : -INFINITY;
+                mx[r] = fmaxf(mx[r], x);
+            }
         grown = grown || mx[r] > st.m[r] + RESCALE_LOG2;
     }
     if (__any_sync(0xffffffffu, grown)) {
         const float down = ev > st.ev && ev != 255 ? exp2_int(st.ev - ev) : 1.0f;
         if (ev != 255) st.ev = max(st.ev, ev);
-        float c[2];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
+        for (int r = 0; r < NR; ++r) {
+            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
             const float m = fmaxf(st.m[r], mx[r]);
-            c[r] = st.m[r] == -INFINITY ? 0.0f : fast_exp2(st.m[r] - m);
+            const float e = st.m[r] == -INFINITY ? 0.0f : fast_exp2(st.m[r] - m);
             st.m[r] = m;
-            st.l[r] *= c[r];
-            c[r] *= down;
-        }
+            st.l[r] *= e;
+            const int c = threadIdx.x & 3;
+            const float c0 = __shfl_sync(0xffffffffu, e, 8 * c) * down, c1 = __shfl_sync(0xffffffffu, e, 8 * c + 4) * down;
 #pragma unroll
-        for (int t = 0; t < 16; ++t) {
-            st.o[t][0] *= c[0];
-            st.o[t][1] *= c[0];
-            st.o[t][2] *= c[1];
-            st.o[t][3] *= c[1];
+            for (int t = 0; t < 8; ++t) {
+                st.o[t][r][0] *= c0;
+                st.o[t][r][1] *= c1;
+                st.o[t][r][2] *= c0;
+                st.o[t][r][3] *= c1;
+            }
         }
     }
     const float vs = ev == 255 ? __int_as_float(0x7fc00000) : exp2_int(ev - st.ev);
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < NR; ++r) {
         const float nm = st.m[r] == -INFINITY ? 0.0f : WEIGHT_LOG2 - st.m[r];
         float sum = 0.0f;
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             const float p0 = fast_exp2(s[n][2 * r] + nm), p1 = fast_exp2(s[n][2 * r + 1] + nm);
             sum += p0 + p1;
-            pf[n >> 1][(n & 1) * 2 + r] = pack_f16(p0 * vs, p1 * vs);
+            pf[n >> 1][r][n & 1] = pack_f16(p0 * vs, p1 * vs);
         }
         st.l[r] += sum;
     }
 }
 
-// grid: (split, KV head and row group, sequence)
-__global__ void __launch_bounds__(NT, 2) cache_attn_rows_kernel(const CacheAttn p) {
+// Where a step of 32 keys lies; ek, ev: its scale bytes
+struct Place {
+    const uint8_t *k, *v;
+    int left, ek, ev;   // left: its keys that are there, 0 or less: none
+};
+
+// grid: (split, KV head, sequence); NR: 8 NR rows at most
+template <int NR>
+__global__ void __launch_bounds__(NT, NR == 1 ? 3 : 2) cache_attn_rows_kernel(const CacheAttn p) {
+    constexpr int ROWS = 8 * NR;
     __shared__ float so[NW][ROWS][O_PITCH];
     __shared__ float sm[NW][ROWS], sl[NW][ROWS];
     __shared__ int sev[NW];
     pdl_wait();
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const int split = blockIdx.x, groups = p.row_groups, h = blockIdx.y / groups, b = blockIdx.z;
-    const int row0 = blockIdx.y % groups * ROWS, nrows = min(ROWS, p.N * p.rep - row0);
-    const bool reports = split == 0 && blockIdx.y == 0 && threadIdx.x == 0;
+    const int split = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+    const int nrows = p.N * p.rep;
+    const int32_t *bt = p.block_table + (size_t)b * p.max_blocks;
     int L = __ldg(p.prefix_len + b);
     if (L < 0 || L > p.max_prefix) {
-        if (reports) flag(p.dev_status, EAGLE3_DEV_CAPACITY);
+        if (split == 0 && h == 0 && threadIdx.x == 0) flag(p.dev_status, EAGLE3_DEV_CAPACITY);
         L = max(0, min(L, p.max_prefix));
     }
 
-    // ---- Q: fragments of the two rows of this lane, each row scaled to [2^12, 2^13)
-    uint32_t qf[8][4];
-    float f[2];
+    // ---- the prefix: chunks [c0, c1) of this split, one after the other by the warps
+    const int chunks = (L + CHUNK - 1) / CHUNK;
+    const int c0 = (int)((long long)chunks * split / p.splits), c1 = (int)((long long)chunks * (split + 1) / p.splits);
+    const int sgroups = p.block_size / EAGLE3_KV_GROUP;
+    auto page_of = [&](int ch) { return ch < c1 ? __ldg(bt + ch * CHUNK / p.block_size) : -1; };
+    auto place_of = [&](int ch, int page) {
+        const int place = ch * CHUNK % p.block_size;
+        const bool there = page >= 0 && page < p.n_pages;
+        const size_t head_page = (size_t)(there ? page : 0) * p.Hkv + h;
+        const size_t sg = head_page * sgroups + place / EAGLE3_KV_GROUP;
+        Place w;
+        w.k = p.kc + (head_page * p.block_size + place) * D + g * D + 16 * c;
+        w.v = p.vc + (head_page * p.block_size + place) * D + 2 * c * D + 16 * g;
+        w.left = there ? L - ch * CHUNK : 0;
+        w.ek = there ? __ldg(p.ks + sg) : 1;   // (a page that is not there reads as zeros)
+        w.ev = there ? __ldg(p.vs + sg) : 1;
+        return w;
+    };
+    uint4 kw[4][2], vw[2][4];
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    auto load_k = [&](const Place &w) {
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                kw[n][i] = 8 * n + g < w.left ? ld_once(w.k + 8 * n * D + 64 * i) : zero;
+    };
+    auto load_v = [&](const Place &w) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int key = 16 * k + (e & 1) + (e >> 1) * 8;
+                vw[k][e] = key + 2 * c < w.left ? ld_once(w.v + key * D) : zero;
+            }
+    };
+    int ch = c0 + warp;
+    int page_next = page_of(ch + NW);
+    Place at = place_of(ch, page_of(ch));
+    load_k(at);
+    load_v(at);
+
+    // ---- Q: fragments of the rows of this lane, each row scaled to [2^12, 2^13)
+    uint32_t qf[8][2 * NR];   // [k-step][row g + 8 r, then its second half]
+    float f[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
         const int row = g + 8 * r;
         float top = 0.0f;
         const __nv_bfloat16 *src = p.q;
         if (row < nrows) {
-            const int node = (row0 + row) / p.rep, head = h * p.rep + (row0 + row) % p.rep;
+            const int node = row / p.rep, head = h * p.rep + row % p.rep;
             src = p.q + ((size_t)b * p.N + node) * p.q_ns + (size_t)head * D + 16 * c;
             bool odd = false;
 #pragma unroll
@@ -159,50 +223,29 @@ __global__ void __launch_bounds__(NT, 2) cache_attn_rows_kernel(const CacheAttn 
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 qf[4 * i + k][r] = w[2 * k];
-                qf[4 * i + k][2 + r] = w[2 * k + 1];
+                qf[4 * i + k][NR + r] = w[2 * k + 1];
             }
         }
     }
+    auto score = [&](float (&s)[4], int k, uint32_t b0, uint32_t b1) {   // (rows that there are not: zeros)
+        mma_f16(s, qf[k][0], NR == 2 ? qf[k][NR - 1] : 0u, qf[k][NR], NR == 2 ? qf[k][2 * NR - 1] : 0u, b0, b1);
+    };
 
-    RowState st;
-    st.m[0] = st.m[1] = -INFINITY;
-    st.l[0] = st.l[1] = 0.0f;
+    RowState<NR> st;
     st.ev = 0;
 #pragma unroll
-    for (int t = 0; t < 16; ++t)
+    for (int r = 0; r < NR; ++r) {
+        st.m[r] = -INFINITY;
+        st.l[r] = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) st.o[t][e] = 0.0f;
+        for (int t = 0; t < 8; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) st.o[t][r][e] = 0.0f;
+    }
 
-    // ---- the prefix: chunks [c0, c1) of this split, one after the other by the warps
-    const int chunks = (L + CHUNK - 1) / CHUNK;
-    const int c0 = (int)((long long)chunks * split / p.splits), c1 = (int)((long long)chunks * (split + 1) / p.splits);
-    const int32_t *bt = p.block_table + (size_t)b * p.max_blocks;
-    const int sgroups = p.block_size / EAGLE3_KV_GROUP;
-    for (int ch = c0 + warp; ch < c1; ch += NW) {
-        const int key0 = ch * CHUNK;
-        const int page = __ldg(bt + key0 / p.block_size), place = key0 % p.block_size;
-        const bool there = page >= 0 && page < p.n_pages;
-        const size_t head_page = (size_t)(there ? page : 0) * p.Hkv + h;
-        const uint8_t *kp = p.kc + (head_page * p.block_size + place) * D;
-        const uint8_t *vp = p.vc + (head_page * p.block_size + place) * D;
-        const int left = L - key0;   // keys of this chunk that are there
-        const size_t sg = head_page * sgroups + place / EAGLE3_KV_GROUP;
-        const int ek = there ? __ldg(p.ks + sg) : 1, ev = there ? __ldg(p.vs + sg) : 1;
-        uint4 kw[4][2], vw[2][4];
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                kw[n][i] = there && 8 * n + g < left
-                               ? *reinterpret_cast<const uint4 *>(kp + (8 * n + g) * D + 64 * i + 16 * c) : zero;
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int key = 16 * k + 2 * c + (e & 1) + (e >> 1) * 8;
-                vw[k][e] = there && key < left ? *reinterpret_cast<const uint4 *>(vp + key * D + 16 * g) : zero;
-            }
+    for (; ch < c1; ch += NW) {
+        const Place next = place_of(ch + NW, page_next);
+        page_next = page_of(ch + 2 * NW);
         float s[4][4];
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
@@ -211,22 +254,28 @@ __global__ void __launch_bounds__(NT, 2) cache_attn_rows_kernel(const CacheAttn 
             for (int k = 0; k < 8; ++k) {
                 const uint4 u = kw[n][k >> 2];
                 const uint32_t w = (k & 3) == 0 ? u.x : (k & 3) == 1 ? u.y : (k & 3) == 2 ? u.z : u.w;
-                mma_f16(s[n], qf[k][0], qf[k][1], qf[k][2], qf[k][3], e4m3x2_f16(w), e4m3x2_f16(w >> 16));
+                score(s[n], k, e4m3x2_f16(w), e4m3x2_f16(w >> 16));
             }
         }
-        uint32_t seen[2] = {0xffu, 0xffu};
+        load_k(next);
+        const int left = L - ch * CHUNK;
+        uint32_t seen[NR];
+        seen[0] = 0xffu;
         if (left < CHUNK) {
             seen[0] = 0;
 #pragma unroll
             for (int n = 0; n < 4; ++n)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) seen[0] |= (8 * n + 2 * c + i < left ? 1u : 0u) << (2 * n + i);
-            seen[1] = seen[0];
         }
-        const float ks = scale_of(ek);
-        const float fs[2] = {f[0] * ks, f[1] * ks};
-        uint32_t pf[2][4];
-        softmax_step(st, s, fs, seen, ev, pf);
+        float fs[NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            seen[r] = seen[0];
+            fs[r] = f[r] * scale_of(at.ek);
+        }
+        uint32_t pf[2][NR][2];
+        softmax_step<NR>(st, s, fs, seen, at.ev, pf);
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -235,108 +284,109 @@ __global__ void __launch_bounds__(NT, 2) cache_attn_rows_kernel(const CacheAttn 
                 const uint32_t r0 = word(vw[k][0]), r1 = word(vw[k][1]), r2 = word(vw[k][2]), r3 = word(vw[k][3]);
                 const uint32_t lo0 = __byte_perm(r0, r1, 0x5140), hi0 = __byte_perm(r0, r1, 0x7362);
                 const uint32_t lo1 = __byte_perm(r2, r3, 0x5140), hi1 = __byte_perm(r2, r3, 0x7362);
-                mma_f16(st.o[4 * w], pf[k][0], pf[k][1], pf[k][2], pf[k][3], e4m3x2_f16(lo0), e4m3x2_f16(lo1));
-                mma_f16(st.o[4 * w + 1], pf[k][0], pf[k][1], pf[k][2], pf[k][3], e4m3x2_f16(lo0 >> 16), e4m3x2_f16(lo1 >> 16));
-                mma_f16(st.o[4 * w + 2], pf[k][0], pf[k][1], pf[k][2], pf[k][3], e4m3x2_f16(hi0), e4m3x2_f16(hi1));
-                mma_f16(st.o[4 * w + 3], pf[k][0], pf[k][1], pf[k][2], pf[k][3], e4m3x2_f16(hi0 >> 16), e4m3x2_f16(hi1 >> 16));
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    mma_f16(st.o[2 * w][r], e4m3x2_f16(lo0), e4m3x2_f16(lo0 >> 16), e4m3x2_f16(lo1),
+                            e4m3x2_f16(lo1 >> 16), pf[k][r][0], pf[k][r][1]);
+                    mma_f16(st.o[2 * w + 1][r], e4m3x2_f16(hi0), e4m3x2_f16(hi0 >> 16), e4m3x2_f16(hi1),
+                            e4m3x2_f16(hi1 >> 16), pf[k][r][0], pf[k][r][1]);
+                }
             }
+        load_v(next);
+        at = next;
     }
 
-    // ---- the tree: its nodes as one or two more chunks of the last split
-    if (p.tree_k && split == p.splits - 1) {
+    // ---- the tree: its nodes, 16 at most, as one more chunk of the last split
+    if (p.tree_k && split == p.splits - 1 && warp == 0) {
         const int32_t *par = p.parents + (size_t)b * p.N;
-        for (int ch = warp; ch * CHUNK < p.N; ch += NW) {
-            const int key0 = ch * CHUNK;
-            // bf16 rows as fp16, K and V each by a power of two of the chunk's largest
-            const __nv_bfloat16 *tk = p.tree_k + (size_t)b * p.N * p.kv_ns + (size_t)h * D;
-            const __nv_bfloat16 *tv = p.tree_v + (size_t)b * p.N * p.kv_ns + (size_t)h * D;
-            float km = 0.0f, vm = 0.0f;
-            bool odd_k = false, odd_v = false;   // V is not finite somewhere: see below
-            for (int i = lane; i < CHUNK * (D / 8); i += 32) {
-                const int key = key0 + i / (D / 8), d0 = i % (D / 8) * 8;
-                if (key >= p.N) break;
-                km = fmaxf(km, amax8(*reinterpret_cast<const uint4 *>(tk + key * p.kv_ns + d0), odd_k));
-                vm = fmaxf(vm, amax8(*reinterpret_cast<const uint4 *>(tv + key * p.kv_ns + d0), odd_v));
+        // bf16 rows as fp16, K and V each by a power of two of their largest
+        const __nv_bfloat16 *tk = p.tree_k + (size_t)b * p.N * p.kv_ns + (size_t)h * D;
+        const __nv_bfloat16 *tv = p.tree_v + (size_t)b * p.N * p.kv_ns + (size_t)h * D;
+        float km = 0.0f, vm = 0.0f;
+        bool odd_k = false, odd_v = false;   // V is not finite somewhere: see below
+        for (int i = lane; i < p.N * (D / 8); i += 32) {
+            const int key = i / (D / 8), d0 = i % (D / 8) * 8;
+            km = fmaxf(km, amax8(*reinterpret_cast<const uint4 *>(tk + key * p.kv_ns + d0), odd_k));
+            vm = fmaxf(vm, amax8(*reinterpret_cast<const uint4 *>(tv + key * p.kv_ns + d0), odd_v));
+        }
+        km = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(km)));
+        vm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vm)));
+        const int kup = row_shift(km, 8), vup = row_shift(vm, 8);   // to [2^8, 2^9), as the codes
+        float s[4][4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+            if (n >= 2) continue;
+            const int key = 8 * n + g;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                if (key < p.N) bf16x16_f16(tk + key * p.kv_ns + 64 * i + 16 * c, exp2_int(kup), w);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) score(s[n], 4 * i + k, w[2 * k], w[2 * k + 1]);
+            }
+        }
+        uint32_t seen[NR], anc[NR];
+        float fs[NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            const int row = g + 8 * r;
+            bool bad = false;
+            anc[r] = row < nrows ? (uint32_t)path_bits(par, row / p.rep, bad) : 0u;
+            if (bad && h == 0) flag(p.dev_status, EAGLE3_DEV_BAD_TREE);
+            seen[r] = 0;
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) seen[r] |= (anc[r] >> (8 * n + 2 * c + i) & 1u) << (2 * n + i);
+            fs[r] = f[r] * exp2_int(-kup);
+        }
+        uint32_t pf[2][NR][2];
+        softmax_step<NR>(st, s, fs, seen, max(0, min(254, 127 - vup)), pf);
+        const float vf = exp2_int(vup);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            uint32_t v[4][4];   // [key][8 dims as bf16 pairs]
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int key = 2 * c + (e & 1) + (e >> 1) * 8;
+                const uint4 u = key < p.N ? *reinterpret_cast<const uint4 *>(tv + key * p.kv_ns + 16 * g + 8 * half) : zero;
+                v[e][0] = u.x, v[e][1] = u.y, v[e][2] = u.z, v[e][3] = u.w;
             }
 #pragma unroll
-            for (int x = 16; x; x >>= 1) {
-                km = fmaxf(km, __shfl_xor_sync(0xffffffffu, km, x));
-                vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, x));
-            }
-            const int kup = row_shift(km, 8), vup = row_shift(vm, 8);   // to [2^8, 2^9), as the codes
-            float s[4][4];
+            for (int d = 0; d < 4; ++d) {
+                auto at = [&](int e, bool upper) {
+                    const float x = __uint_as_float(upper ? v[e][d] & 0xffff0000u : v[e][d] << 16);
+                    return fabsf(x) <= FLT_MAX ? x * vf : 0.0f;
+                };
+                const uint32_t a0 = pack_f16(at(0, false), at(1, false)), a1 = pack_f16(at(0, true), at(1, true));
+                const uint32_t a2 = pack_f16(at(2, false), at(3, false)), a3 = pack_f16(at(2, true), at(3, true));
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
-                const int key = key0 + 8 * n + g;
+                for (int r = 0; r < NR; ++r) mma_f16(st.o[4 * half + d][r], a0, a1, a2, a3, pf[0][r][0], pf[0][r][1]);
+            }
+        }
+        // infinities and NaN of V, which a weight of 0 would have spread over every row: to the rows that see them
+        if (__any_sync(0xffffffffu, odd_v)) {
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                    if (key < p.N) bf16x16_f16(tk + key * p.kv_ns + 64 * i + 16 * c, exp2_int(kup), w);
+                    const uint32_t sees = __shfl_sync(0xffffffffu, anc[r], 8 * c + 4 * i);   // of row 8r + 2c + i
+                    for (int key = 0; key < p.N; ++key)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_f16(s[n], qf[4 * i + k][0], qf[4 * i + k][1], qf[4 * i + k][2], qf[4 * i + k][3], w[2 * k],
-                                w[2 * k + 1]);
+                        for (int t = 0; t < 8; ++t)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const float x = (float)tv[key * p.kv_ns + 16 * g + 2 * t + e];
+                                if (!(fabsf(x) <= FLT_MAX) && (sees >> key & 1u)) st.o[t][r][2 * e + i] += x;
+                            }
                 }
-            }
-            uint32_t seen[2] = {0, 0};
-            uint64_t anc[2];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int row = g + 8 * r;
-                bool bad = false;
-                anc[r] = row < nrows ? path_bits(par, (row0 + row) / p.rep, bad) : 0ull;
-                if (bad && h == 0) flag(p.dev_status, EAGLE3_DEV_BAD_TREE);
-#pragma unroll
-                for (int n = 0; n < 4; ++n)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        seen[r] |= (uint32_t)((anc[r] >> (key0 + 8 * n + 2 * c + i)) & 1ull) << (2 * n + i);
-            }
-            const float fs[2] = {f[0] * exp2_int(-kup), f[1] * exp2_int(-kup)};
-            uint32_t pf[2][4];
-            softmax_step(st, s, fs, seen, max(0, min(254, 127 - vup)), pf);
-            const float vf = exp2_int(vup);
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t v[4][4];   // [key][8 dims as bf16 pairs]
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int key = key0 + 16 * k + 2 * c + (e & 1) + (e >> 1) * 8;
-                        const uint4 u = key < p.N ? *reinterpret_cast<const uint4 *>(tv + key * p.kv_ns + 16 * g + 8 * half)
-                                                  : make_uint4(0, 0, 0, 0);
-                        v[e][0] = u.x, v[e][1] = u.y, v[e][2] = u.z, v[e][3] = u.w;
-                    }
-#pragma unroll
-                    for (int d = 0; d < 8; ++d) {
-                        auto at = [&](int e) {
-                            const uint32_t w = v[e][d >> 1];
-                            const float x = __uint_as_float(d & 1 ? w & 0xffff0000u : w << 16);
-                            return fabsf(x) <= FLT_MAX ? x * vf : 0.0f;
-                        };
-                        mma_f16(st.o[8 * half + d], pf[k][0], pf[k][1], pf[k][2], pf[k][3], pack_f16(at(0), at(1)),
-                                pack_f16(at(2), at(3)));
-                    }
-                }
-            // infinities and NaN of V, which a weight of 0 would have spread over every row: to the rows that see them
-            if (__any_sync(0xffffffffu, odd_v)) {
-                for (int key = key0; key < min(p.N, key0 + CHUNK); ++key)
-#pragma unroll
-                    for (int t = 0; t < 16; ++t)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float x = (float)tv[key * p.kv_ns + 32 * c + 16 * (e & 1) + t];
-                            if (!(fabsf(x) <= FLT_MAX) && (anc[e >> 1] >> key & 1ull)) st.o[t][e] += x;
-                        }
-            }
         }
     }
 
     // ---- the warps' results, in warp order
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < NR; ++r) {
         float l = st.l[r];
         l += __shfl_xor_sync(0xffffffffu, l, 1);
         l += __shfl_xor_sync(0xffffffffu, l, 2);
@@ -347,9 +397,9 @@ __global__ void __launch_bounds__(NT, 2) cache_attn_rows_kernel(const CacheAttn 
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int t = 0; t < 16; t += 4)
-                *reinterpret_cast<float4 *>(&so[warp][g + 8 * r][32 * c + 16 * i + t]) =
-                    make_float4(st.o[t][2 * r + i], st.o[t + 1][2 * r + i], st.o[t + 2][2 * r + i], st.o[t + 3][2 * r + i]);
+            for (int t = 0; t < 8; t += 2)
+                *reinterpret_cast<float4 *>(&so[warp][8 * r + 2 * c + i][16 * g + 2 * t]) =
+                    make_float4(st.o[t][r][i], st.o[t][r][2 + i], st.o[t + 1][r][i], st.o[t + 1][r][2 + i]);
     }
     if (lane == 0) sev[warp] = st.ev;
     __syncthreads();
@@ -368,49 +418,92 @@ __global__ void __launch_bounds__(NT, 2) cache_attn_rows_kernel(const CacheAttn 
             const float4 x = *reinterpret_cast<const float4 *>(&so[w][row][4 * lane]);
             if (e != 0.0f) o = make_float4(o.x + vs * x.x, o.y + vs * x.y, o.z + vs * x.z, o.w + vs * x.w);
         }
-        const int node = (row0 + row) / p.rep, head = h * p.rep + (row0 + row) % p.rep;
-        const size_t at = ((size_t)b * p.N + node) * p.Hq + head;
+        const int node = row / p.rep, head = h * p.rep + row % p.rep;
+        const size_t at_row = ((size_t)b * p.N + node) * p.Hq + head;
         if (p.splits == 1) {
-            store_row(p, at, lane, M, l, o);
+            store_row(p, at_row, lane, M, l, o);
         } else {
-            const size_t part = (size_t)split * p.B * p.N * p.Hq + at;
+            const size_t part = (size_t)split * p.B * p.N * p.Hq + at_row;
             if (l != 0.0f) *reinterpret_cast<float4 *>(p.part_o + part * D + 4 * lane) = o;   // (NaN too)
             if (lane == 0) *reinterpret_cast<float2 *>(p.part_ml + 2 * part) = make_float2(M, l);
         }
     }
 }
 
-// The splits' results in split order: one warp a row.
-__global__ void __launch_bounds__(128) cache_attn_merge_kernel(const CacheAttn p) {
+// The splits' results: a CTA a row, a quarter of the splits to each of its warps, joined in warp order.
+__global__ void __launch_bounds__(NT) cache_attn_merge_kernel(const CacheAttn p) {
+    __shared__ float4 so[NW][32];
+    __shared__ float sl[NW];
+    __shared__ float sw[MAX_SPLITS];   // a split's factor
+    __shared__ float sm[NW];
     pdl_wait();
     pdl_trigger();
-    const long long rows = (long long)p.B * p.N * p.Hq;
-    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (row >= rows) return;
+    const long long rows = (long long)p.B * p.N * p.Hq, row = blockIdx.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float2 ml[MAX_SPLITS / NT];
     float M = -INFINITY, l = 0.0f;
-    for (int s = 0; s < p.splits; ++s) M = fmaxf(M, p.part_ml[2 * (s * rows + row)]);
+#pragma unroll
+    for (int i = 0; i < MAX_SPLITS / NT; ++i) {
+        const int s = threadIdx.x + i * NT;
+        ml[i] = s < p.splits ? *reinterpret_cast<const float2 *>(p.part_ml + 2 * (s * rows + row)) : make_float2(-INFINITY, 0.0f);
+        M = fmaxf(M, ml[i].x);
+    }
+#pragma unroll
+    for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+    if (lane == 0) sm[warp] = M;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < NW; ++w) M = fmaxf(M, sm[w]);
+#pragma unroll
+    for (int i = 0; i < MAX_SPLITS / NT; ++i) {
+        const int s = threadIdx.x + i * NT;
+        const float e = ml[i].y == 0.0f ? 0.0f : ml[i].x == -INFINITY ? 1.0f : fast_exp2(ml[i].x - M);
+        if (s < p.splits) sw[s] = e;
+        l += e * ml[i].y;
+    }
+#pragma unroll
+    for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+    if (lane == 0) sl[warp] = l;
+    __syncthreads();
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int s = 0; s < p.splits; ++s) {
-        const float2 ml = *reinterpret_cast<const float2 *>(p.part_ml + 2 * (s * rows + row));
-        if (ml.y == 0.0f) continue;
-        const float e = ml.x == -INFINITY ? 1.0f : fast_exp2(ml.x - M);
-        const float4 x = *reinterpret_cast<const float4 *>(p.part_o + (s * rows + row) * D + 4 * lane);
-        l += e * ml.y;
-        o = make_float4(o.x + e * x.x, o.y + e * x.y, o.z + e * x.z, o.w + e * x.w);
+    const int s0 = p.splits * warp / NW, s1 = p.splits * (warp + 1) / NW;
+    constexpr int K = 8;   // loads in flight
+    for (int s = s0; s < s1; s += K) {
+        float4 x[K];
+        float e[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            e[k] = s + k < s1 ? sw[s + k] : 0.0f;   // (a split with nothing to see has left nothing there)
+            if (e[k] != 0.0f) x[k] = *reinterpret_cast<const float4 *>(p.part_o + ((s + k) * rows + row) * D + 4 * lane);
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (e[k] != 0.0f) o = make_float4(o.x + e[k] * x[k].x, o.y + e[k] * x[k].y, o.z + e[k] * x[k].z, o.w + e[k] * x[k].w);
+    }
+    so[warp][lane] = o;
+    __syncthreads();
+    if (warp != 0) return;
+    l = 0.0f;
+    o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        const float4 x = so[w][lane];
+        l += sl[w];
+        o = make_float4(o.x + x.x, o.y + x.y, o.z + x.z, o.w + x.w);
     }
     store_row(p, (size_t)row, lane, M, l, o);
 }
 
-// parts of the prefix: enough CTAs for the GPU, none with fewer than 8 chunks a warp
+// Parts of the prefix.  Few sequences: one wave of CTAs (their lengths are likely one length), with no fewer than two
+// steps a warp; many: four waves, so that unequal lengths even out.
 int plan_splits(const CacheAttn &p, int requested) {
     const int chunks = (p.max_prefix + CHUNK - 1) / CHUNK;
-    if (requested > 0) return requested < chunks ? requested : chunks > 0 ? chunks : 1;
-    const int64_t units = (int64_t)p.B * p.Hkv * p.row_groups;
-    const int64_t want = (8 * (int64_t)device_sm_count() + units - 1) / units;
-    const int64_t most = chunks / (8 * NW);
+    if (requested > 0) return requested < chunks ? requested < MAX_SPLITS ? requested : MAX_SPLITS : chunks > 0 ? min(chunks, MAX_SPLITS) : 1;
+    const int64_t units = (int64_t)p.B * p.Hkv, resident = (int64_t)device_sm_count() * (p.N * p.rep <= 8 ? 3 : 2);
+    const int64_t want = 4 * units <= resident ? resident / units : (4 * resident + units - 1) / units;
+    const int64_t most = chunks / (2 * NW);
     const int64_t s = want < most ? want : most;
-    return s < 1 ? 1 : s > 512 ? 512 : (int)s;
+    return s < 1 ? 1 : s > MAX_SPLITS ? MAX_SPLITS : (int)s;
 }
 
 bool valid(const eagle3_verify_attn_fp8_args_t *a, eagle3_status_t *why) {
@@ -472,12 +565,11 @@ CacheAttn plan(const eagle3_verify_attn_fp8_args_t *a) {
     p.out = (__nv_bfloat16 *)a->out;
     p.lse = a->lse;
     p.dev_status = a->dev_status;
-    p.row_groups = (p.N * p.rep + ROWS - 1) / ROWS;
     p.splits = plan_splits(p, a->num_splits);
     return p;
 }
 
-bool is_wide(const CacheAttn &p) { return p.N * p.rep > ROWS; }
+bool is_wide(const CacheAttn &p) { return p.N * p.rep > MAX_ROWS; }
 
 size_t workspace_of(const CacheAttn &p) {
     return p.splits > 1 ? (size_t)p.splits * p.B * p.N * p.Hq * (D + 2) * sizeof(float) + 256 : 0;
@@ -507,11 +599,12 @@ extern "C" eagle3_status_t eagle3_verify_attn_fp8(const eagle3_verify_attn_fp8_a
         p.part_ml = p.part_o + (size_t)p.splits * p.B * p.N * p.Hq * D;
     }
     const cudaStream_t st = (cudaStream_t)stream;
-    const dim3 grid((unsigned)p.splits, (unsigned)(p.Hkv * p.row_groups), (unsigned)p.B);
-    if (launch_pdl(cache_attn_rows_kernel, grid, dim3(NT), 0, st, p) != cudaSuccess) return EAGLE3_ERR_CUDA;
+    const dim3 grid((unsigned)p.splits, (unsigned)p.Hkv, (unsigned)p.B);
+    auto *kernel = p.N * p.rep <= 8 ? cache_attn_rows_kernel<1> : cache_attn_rows_kernel<2>;
+    if (launch_pdl(kernel, grid, dim3(NT), 0, st, p) != cudaSuccess) return EAGLE3_ERR_CUDA;
     if (p.splits > 1) {
         const long long rows = (long long)p.B * p.N * p.Hq;
-        if (launch_pdl(cache_attn_merge_kernel, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, p) != cudaSuccess)
+        if (launch_pdl(cache_attn_merge_kernel, dim3((unsigned)rows), dim3(NT), 0, st, p) != cudaSuccess)
             return EAGLE3_ERR_CUDA;
     }
     return EAGLE3_OK;
