@@ -274,6 +274,10 @@ def _declare(L):
     L.eagle3_verify_attn_fp8_workspace_size.argtypes = [P(VerifyAttnFp8Args)]
     L.eagle3_verify_attn_fp8.restype = ctypes.c_int
     L.eagle3_verify_attn_fp8.argtypes = [P(VerifyAttnFp8Args), _p, ctypes.c_size_t, _p]
+    L.eagle3_test_verify_attn_fp8_workspace_size.restype = ctypes.c_size_t
+    L.eagle3_test_verify_attn_fp8_workspace_size.argtypes = [P(VerifyAttnFp8Args), _i32]
+    L.eagle3_test_verify_attn_fp8.restype = ctypes.c_int
+    L.eagle3_test_verify_attn_fp8.argtypes = [P(VerifyAttnFp8Args), _p, ctypes.c_size_t, _i32, _i32, _i64, _p]
     L.eagle3_test_grouped_linear_timeout.restype = ctypes.c_int
     L.eagle3_test_grouped_linear_timeout.argtypes = [P(GroupedLinearArgs), _i32, _i32, _i64, _p]
     L.eagle3_test_linear_fp8_timeout.restype = ctypes.c_int
@@ -1106,6 +1110,23 @@ def eagle3_verify_attn_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, p
         _check(L.eagle3_verify_attn_fp8(ref, own, need, st), "eagle3_verify_attn_fp8")
     finally:
         torch._C._cuda_cudaCachingAllocator_raw_delete(own)
+
+
+def eagle3_test_verify_attn_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, prefix_len, out, *, kernel,
+                                stall_block=-1, wait_limit_cycles=0, stream=None, **kw):
+    """Test hook (include/eagle3_testing.h): eagle3_verify_attn_fp8 by a kernel of the caller's choice, 1 or 2; with
+    stall_block a tile that never arrives and every bounded wait limited to wait_limit_cycles."""
+    a = verify_attn_fp8_args(q, k_cache, v_cache, k_scale, v_scale, block_table, prefix_len, out, **kw)
+    st = _on(q.get_device(), stream)
+    L, ref = lib(), ctypes.byref(a)
+    need = L.eagle3_test_verify_attn_fp8_workspace_size(ref, int(kernel))
+    own = torch._C._cuda_cudaCachingAllocator_raw_alloc(need, st) if need else None
+    try:
+        _check(L.eagle3_test_verify_attn_fp8(ref, own, need, int(kernel), int(stall_block), int(wait_limit_cycles), st),
+               "eagle3_test_verify_attn_fp8")
+    finally:
+        if own:
+            torch._C._cuda_cudaCachingAllocator_raw_delete(own)
 
 
 # ----------------------------------------------------------------------------- fp32 small-model blocks

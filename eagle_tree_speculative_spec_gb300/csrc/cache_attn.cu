@@ -22,6 +22,7 @@
 // largest vanish); the factor comes back with the scale of K's group in fp32.  Weights are held 2^7 up, so that fp16's
 // 11 bits reach down to 2^-21 of the largest, and V's group scale is put on them relative to the largest so far.
 #include "cache_attn.cuh"
+#include "eagle3_testing.h"
 
 #include <cfloat>
 
@@ -50,12 +51,11 @@ E3_DEV uint4 ld_once(const uint8_t *p) {
     return u;
 }
 
-// 16 consecutive bf16 as fp16 pairs, times a power of two
-E3_DEV void bf16x16_f16(const __nv_bfloat16 *src, float factor, uint32_t (&out)[8]) {
+// 16 bf16 as fp16 pairs, times a power of two
+E3_DEV void bf16x16_f16(const uint4 (&in)[2], float factor, uint32_t (&out)[8]) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(src + 8 * i);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        const uint32_t w[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[e]));
@@ -135,7 +135,7 @@ struct Place {
     int left, ek, ev;   // left: its keys that are there, 0 or less: none
 };
 
-// grid: (split, KV head, sequence); NR: 8 NR rows at most
+// grid: (split, KV head and group of rows, sequence); NR: 8 NR rows a group
 template <int NR>
 __global__ void __launch_bounds__(NT, NR == 1 ? 3 : 2) cache_attn_rows_kernel(const CacheAttn p) {
     constexpr int ROWS = 8 * NR;
@@ -145,18 +145,19 @@ __global__ void __launch_bounds__(NT, NR == 1 ? 3 : 2) cache_attn_rows_kernel(co
     pdl_wait();
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const int split = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
-    const int nrows = p.N * p.rep;
+    const int split = blockIdx.x, h = blockIdx.y / p.row_groups, b = blockIdx.z;
+    const int row0 = blockIdx.y % p.row_groups * ROWS, nrows = min(ROWS, p.N * p.rep - row0);
+    const bool reports = split == 0 && blockIdx.y == 0 && threadIdx.x == 0;
     const int32_t *bt = p.block_table + (size_t)b * p.max_blocks;
     int L = __ldg(p.prefix_len + b);
     if (L < 0 || L > p.max_prefix) {
-        if (split == 0 && h == 0 && threadIdx.x == 0) flag(p.dev_status, EAGLE3_DEV_CAPACITY);
+        if (reports) flag(p.dev_status, EAGLE3_DEV_CAPACITY);
         L = max(0, min(L, p.max_prefix));
     }
 
     // ---- the prefix: chunks [c0, c1) of this split, one after the other by the warps
     const int chunks = (L + CHUNK - 1) / CHUNK;
-    const int c0 = (int)((long long)chunks * split / p.splits), c1 = (int)((long long)chunks * (split + 1) / p.splits);
+    const int c0 = min(chunks, split * p.split_chunks), c1 = min(chunks, c0 + p.split_chunks);
     const int sgroups = p.block_size / EAGLE3_KV_GROUP;
     auto page_of = [&](int ch) { return ch < c1 ? __ldg(bt + ch * CHUNK / p.block_size) : -1; };
     auto place_of = [&](int ch, int page) {
@@ -203,14 +204,16 @@ __global__ void __launch_bounds__(NT, NR == 1 ? 3 : 2) cache_attn_rows_kernel(co
     for (int r = 0; r < NR; ++r) {
         const int row = g + 8 * r;
         float top = 0.0f;
-        const __nv_bfloat16 *src = p.q;
+        uint4 raw[2][2] = {{zero, zero}, {zero, zero}};
         if (row < nrows) {
-            const int node = row / p.rep, head = h * p.rep + row % p.rep;
-            src = p.q + ((size_t)b * p.N + node) * p.q_ns + (size_t)head * D + 16 * c;
+            const int node = (row0 + row) / p.rep, head = h * p.rep + (row0 + row) % p.rep;
+            const __nv_bfloat16 *src = p.q + ((size_t)b * p.N + node) * p.q_ns + (size_t)head * D + 16 * c;
             bool odd = false;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                top = fmaxf(top, amax8(*reinterpret_cast<const uint4 *>(src + 64 * (i >> 1) + 8 * (i & 1)), odd));
+            for (int i = 0; i < 4; ++i) {
+                raw[i >> 1][i & 1] = *reinterpret_cast<const uint4 *>(src + 64 * (i >> 1) + 8 * (i & 1));
+                top = fmaxf(top, amax8(raw[i >> 1][i & 1], odd));
+            }
         }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -218,8 +221,8 @@ __global__ void __launch_bounds__(NT, NR == 1 ? 3 : 2) cache_attn_rows_kernel(co
         f[r] = p.scale_log2 * exp2_int(-up);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (row < nrows) bf16x16_f16(src + 64 * i, exp2_int(up), w);
+            uint32_t w[8];
+            bf16x16_f16(raw[i], exp2_int(up), w);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 qf[4 * i + k][r] = w[2 * k];
@@ -296,47 +299,69 @@ __global__ void __launch_bounds__(NT, NR == 1 ? 3 : 2) cache_attn_rows_kernel(co
         at = next;
     }
 
-    // ---- the tree: its nodes, 16 at most, as one more chunk of the last split
-    if (p.tree_k && split == p.splits - 1 && warp == 0) {
+    // ---- the tree: its nodes as one or two more steps of the last split
+    if (p.tree_k && split == p.splits - 1 && warp * CHUNK < p.N) {
+        const int key0 = warp * CHUNK, keys = min(CHUNK, p.N - key0);
         const int32_t *par = p.parents + (size_t)b * p.N;
         // bf16 rows as fp16, K and V each by a power of two of their largest
-        const __nv_bfloat16 *tk = p.tree_k + (size_t)b * p.N * p.kv_ns + (size_t)h * D;
-        const __nv_bfloat16 *tv = p.tree_v + (size_t)b * p.N * p.kv_ns + (size_t)h * D;
-        float km = 0.0f, vm = 0.0f;
-        bool odd_k = false, odd_v = false;   // V is not finite somewhere: see below
-        for (int i = lane; i < p.N * (D / 8); i += 32) {
-            const int key = i / (D / 8), d0 = i % (D / 8) * 8;
-            km = fmaxf(km, amax8(*reinterpret_cast<const uint4 *>(tk + key * p.kv_ns + d0), odd_k));
-            vm = fmaxf(vm, amax8(*reinterpret_cast<const uint4 *>(tv + key * p.kv_ns + d0), odd_v));
-        }
-        km = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(km)));
-        vm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vm)));
-        const int kup = row_shift(km, 8), vup = row_shift(vm, 8);   // to [2^8, 2^9), as the codes
-        float s[4][4];
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
-            if (n >= 2) continue;
-            const int key = 8 * n + g;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                if (key < p.N) bf16x16_f16(tk + key * p.kv_ns + 64 * i + 16 * c, exp2_int(kup), w);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) score(s[n], 4 * i + k, w[2 * k], w[2 * k + 1]);
-            }
-        }
-        uint32_t seen[NR], anc[NR];
-        float fs[NR];
+        const __nv_bfloat16 *tk = p.tree_k + ((size_t)b * p.N + key0) * p.kv_ns + (size_t)h * D;
+        const __nv_bfloat16 *tv = p.tree_v + ((size_t)b * p.N + key0) * p.kv_ns + (size_t)h * D;
+        uint32_t anc[NR];   // which of these nodes a row sees
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
             const int row = g + 8 * r;
             bool bad = false;
-            anc[r] = row < nrows ? (uint32_t)path_bits(par, row / p.rep, bad) : 0u;
+            anc[r] = row < nrows ? (uint32_t)(path_bits(par, (row0 + row) / p.rep, bad) >> key0) : 0u;
             if (bad && h == 0) flag(p.dev_status, EAGLE3_DEV_BAD_TREE);
+        }
+        float top = 0.0f;
+        bool odd_k = false, odd_v = false;   // V is not finite somewhere: see below
+        uint4 raw[8][2];                     // K's dims [64i + 16c, + 16) of key 8n + g, then V's
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const int key = 8 * (x >> 1) + g;
+                raw[x][y] = key < keys ? *reinterpret_cast<const uint4 *>(tk + key * p.kv_ns + 64 * (x & 1) + 16 * c + 8 * y) : zero;
+            }
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) top = fmaxf(top, amax8(raw[x][y], odd_k));
+        const int kup = row_shift(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top))), 8);   // to [2^8, 2^9), as the codes
+        float s[4][4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                uint32_t w[8];
+                bf16x16_f16(raw[2 * n + i], exp2_int(kup), w);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) score(s[n], 4 * i + k, w[2 * k], w[2 * k + 1]);
+            }
+        }
+        // V's dims [16g, 16g + 16) of keys 16k + {2c, 2c + 1, 2c + 8, 2c + 9}
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const int key = 16 * (x >> 2) + 2 * c + (x & 1) + (x >> 1 & 1) * 8;
+                raw[x][y] = key < keys ? *reinterpret_cast<const uint4 *>(tv + key * p.kv_ns + 16 * g + 8 * y) : zero;
+            }
+        top = 0.0f;
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) top = fmaxf(top, amax8(raw[x][y], odd_v));
+        const int vup = row_shift(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top))), 8);
+        uint32_t seen[NR];
+        float fs[NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
             seen[r] = 0;
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < 4; ++n)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) seen[r] |= (anc[r] >> (8 * n + 2 * c + i) & 1u) << (2 * n + i);
             fs[r] = f[r] * exp2_int(-kup);
@@ -345,26 +370,26 @@ __global__ void __launch_bounds__(NT, NR == 1 ? 3 : 2) cache_attn_rows_kernel(co
         softmax_step<NR>(st, s, fs, seen, max(0, min(254, 127 - vup)), pf);
         const float vf = exp2_int(vup);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            uint32_t v[4][4];   // [key][8 dims as bf16 pairs]
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int key = 2 * c + (e & 1) + (e >> 1) * 8;
-                const uint4 u = key < p.N ? *reinterpret_cast<const uint4 *>(tv + key * p.kv_ns + 16 * g + 8 * half) : zero;
-                v[e][0] = u.x, v[e][1] = u.y, v[e][2] = u.z, v[e][3] = u.w;
-            }
-#pragma unroll
-            for (int d = 0; d < 4; ++d) {
-                auto at = [&](int e, bool upper) {
-                    const float x = __uint_as_float(upper ? v[e][d] & 0xffff0000u : v[e][d] << 16);
-                    return fabsf(x) <= FLT_MAX ? x * vf : 0.0f;
+            for (int half = 0; half < 2; ++half) {
+                auto word = [&](int e, int d) {
+                    const uint4 u = raw[4 * k + e][half];
+                    return d == 0 ? u.x : d == 1 ? u.y : d == 2 ? u.z : u.w;
                 };
-                const uint32_t a0 = pack_f16(at(0, false), at(1, false)), a1 = pack_f16(at(0, true), at(1, true));
-                const uint32_t a2 = pack_f16(at(2, false), at(3, false)), a3 = pack_f16(at(2, true), at(3, true));
 #pragma unroll
-                for (int r = 0; r < NR; ++r) mma_f16(st.o[4 * half + d][r], a0, a1, a2, a3, pf[0][r][0], pf[0][r][1]);
+                for (int d = 0; d < 4; ++d) {
+                    auto at = [&](int e, bool upper) {
+                        const float x = __uint_as_float(upper ? word(e, d) & 0xffff0000u : word(e, d) << 16);
+                        return fabsf(x) <= FLT_MAX ? x * vf : 0.0f;
+                    };
+                    const uint32_t a0 = pack_f16(at(0, false), at(1, false)), a1 = pack_f16(at(0, true), at(1, true));
+                    const uint32_t a2 = pack_f16(at(2, false), at(3, false)), a3 = pack_f16(at(2, true), at(3, true));
+#pragma unroll
+                    for (int r = 0; r < NR; ++r)
+                        mma_f16(st.o[4 * half + d][r], a0, a1, a2, a3, pf[k][r][0], pf[k][r][1]);
+                }
             }
-        }
         // infinities and NaN of V, which a weight of 0 would have spread over every row: to the rows that see them
         if (__any_sync(0xffffffffu, odd_v)) {
 #pragma unroll
@@ -372,7 +397,7 @@ __global__ void __launch_bounds__(NT, NR == 1 ? 3 : 2) cache_attn_rows_kernel(co
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const uint32_t sees = __shfl_sync(0xffffffffu, anc[r], 8 * c + 4 * i);   // of row 8r + 2c + i
-                    for (int key = 0; key < p.N; ++key)
+                    for (int key = 0; key < keys; ++key)
 #pragma unroll
                         for (int t = 0; t < 8; ++t)
 #pragma unroll
@@ -418,7 +443,7 @@ __global__ void __launch_bounds__(NT, NR == 1 ? 3 : 2) cache_attn_rows_kernel(co
             const float4 x = *reinterpret_cast<const float4 *>(&so[w][row][4 * lane]);
             if (e != 0.0f) o = make_float4(o.x + vs * x.x, o.y + vs * x.y, o.z + vs * x.z, o.w + vs * x.w);
         }
-        const int node = row / p.rep, head = h * p.rep + row % p.rep;
+        const int node = (row0 + row) / p.rep, head = h * p.rep + (row0 + row) % p.rep;
         const size_t at_row = ((size_t)b * p.N + node) * p.Hq + head;
         if (p.splits == 1) {
             store_row(p, at_row, lane, M, l, o);
@@ -430,12 +455,59 @@ __global__ void __launch_bounds__(NT, NR == 1 ? 3 : 2) cache_attn_rows_kernel(co
     }
 }
 
-// The splits' results: a CTA a row, a quarter of the splits to each of its warps, joined in warp order.
+// The splits' results.  Few splits: a warp a row.  Many: a CTA a row, a quarter of the splits to each of its warps.
+constexpr int FEW_SPLITS = 16;   // 16384 rows of 2 splits and 128 threads a row took 14 us; 32 rows of 57 and a warp a row 9 us
+
+// splits [s0, s1) of a row by their factors, with eight loads in flight; factor(s): of split s, the same in all lanes
+template <typename F>
+E3_DEV float4 weighted_sum(const CacheAttn &p, long long rows, long long row, int s0, int s1, int lane, F factor) {
+    constexpr int K = 8;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int s = s0; s < s1; s += K) {
+        float4 x[K];
+        float e[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            e[k] = factor(min(s + k, s1 - 1));   // (a split with nothing to see has left nothing there)
+            if (s + k >= s1) e[k] = 0.0f;
+            if (e[k] != 0.0f) x[k] = *reinterpret_cast<const float4 *>(p.part_o + ((s + k) * rows + row) * D + 4 * lane);
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (e[k] != 0.0f) o = make_float4(o.x + e[k] * x[k].x, o.y + e[k] * x[k].y, o.z + e[k] * x[k].z, o.w + e[k] * x[k].w);
+    }
+    return o;
+}
+E3_DEV float2 split_ml(const CacheAttn &p, long long rows, long long row, int s) {
+    return s < p.splits ? *reinterpret_cast<const float2 *>(p.part_ml + 2 * (s * rows + row)) : make_float2(-INFINITY, 0.0f);
+}
+E3_DEV float split_factor(float2 ml, float M) { return ml.y == 0.0f ? 0.0f : ml.x == -INFINITY ? 1.0f : fast_exp2(ml.x - M); }
+E3_DEV float warp_max(float x) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+    return x;
+}
+E3_DEV float warp_sum(float x) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    return x;
+}
+
+__global__ void __launch_bounds__(NT) cache_attn_merge_few_kernel(const CacheAttn p) {
+    pdl_wait();
+    pdl_trigger();
+    const long long rows = (long long)p.B * p.N * p.Hq, row = (long long)blockIdx.x * NW + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (row >= rows) return;
+    const float2 ml = split_ml(p, rows, row, lane);
+    const float M = warp_max(ml.x), e = split_factor(ml, M), l = warp_sum(e * ml.y);
+    store_row(p, (size_t)row, lane, M, l, weighted_sum(p, rows, row, 0, p.splits, lane, [&](int s) { return __shfl_sync(0xffffffffu, e, s); }));
+}
+
 __global__ void __launch_bounds__(NT) cache_attn_merge_kernel(const CacheAttn p) {
     __shared__ float4 so[NW][32];
-    __shared__ float sl[NW];
+    __shared__ float sl[NW], sm[NW];
     __shared__ float sw[MAX_SPLITS];   // a split's factor
-    __shared__ float sm[NW];
     pdl_wait();
     pdl_trigger();
     const long long rows = (long long)p.B * p.N * p.Hq, row = blockIdx.x;
@@ -444,47 +516,28 @@ __global__ void __launch_bounds__(NT) cache_attn_merge_kernel(const CacheAttn p)
     float M = -INFINITY, l = 0.0f;
 #pragma unroll
     for (int i = 0; i < MAX_SPLITS / NT; ++i) {
-        const int s = threadIdx.x + i * NT;
-        ml[i] = s < p.splits ? *reinterpret_cast<const float2 *>(p.part_ml + 2 * (s * rows + row)) : make_float2(-INFINITY, 0.0f);
+        ml[i] = split_ml(p, rows, row, threadIdx.x + i * NT);
         M = fmaxf(M, ml[i].x);
     }
-#pragma unroll
-    for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+    M = warp_max(M);
     if (lane == 0) sm[warp] = M;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < NW; ++w) M = fmaxf(M, sm[w]);
 #pragma unroll
     for (int i = 0; i < MAX_SPLITS / NT; ++i) {
-        const int s = threadIdx.x + i * NT;
-        const float e = ml[i].y == 0.0f ? 0.0f : ml[i].x == -INFINITY ? 1.0f : fast_exp2(ml[i].x - M);
-        if (s < p.splits) sw[s] = e;
+        const float e = split_factor(ml[i], M);
+        sw[threadIdx.x + i * NT] = e;
         l += e * ml[i].y;
     }
-#pragma unroll
-    for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+    l = warp_sum(l);
     if (lane == 0) sl[warp] = l;
     __syncthreads();
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const int s0 = p.splits * warp / NW, s1 = p.splits * (warp + 1) / NW;
-    constexpr int K = 8;   // loads in flight
-    for (int s = s0; s < s1; s += K) {
-        float4 x[K];
-        float e[K];
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            e[k] = s + k < s1 ? sw[s + k] : 0.0f;   // (a split with nothing to see has left nothing there)
-            if (e[k] != 0.0f) x[k] = *reinterpret_cast<const float4 *>(p.part_o + ((s + k) * rows + row) * D + 4 * lane);
-        }
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (e[k] != 0.0f) o = make_float4(o.x + e[k] * x[k].x, o.y + e[k] * x[k].y, o.z + e[k] * x[k].z, o.w + e[k] * x[k].w);
-    }
-    so[warp][lane] = o;
+    so[warp][lane] = weighted_sum(p, rows, row, p.splits * warp / NW, p.splits * (warp + 1) / NW, lane, [&](int s) { return sw[s]; });
     __syncthreads();
     if (warp != 0) return;
     l = 0.0f;
-    o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
         const float4 x = so[w][lane];
@@ -494,16 +547,29 @@ __global__ void __launch_bounds__(NT) cache_attn_merge_kernel(const CacheAttn p)
     store_row(p, (size_t)row, lane, M, l, o);
 }
 
-// Parts of the prefix.  Few sequences: one wave of CTAs (their lengths are likely one length), with no fewer than two
-// steps a warp; many: four waves, so that unequal lengths even out.
-int plan_splits(const CacheAttn &p, int requested) {
+// Parts of the prefix, of as many steps for a short sequence as for a long one, so that all CTAs take about the same
+// time: the number that gives the least waves * (steps of a warp + what a CTA costs besides, in steps), about in us.
+// Lengths are unknown here, so half a wave more stands for the uneven end of all but a single wave.
+float plan_splits(CacheAttn &p, int requested) {
     const int chunks = (p.max_prefix + CHUNK - 1) / CHUNK;
-    if (requested > 0) return requested < chunks ? requested < MAX_SPLITS ? requested : MAX_SPLITS : chunks > 0 ? min(chunks, MAX_SPLITS) : 1;
-    const int64_t units = (int64_t)p.B * p.Hkv, resident = (int64_t)device_sm_count() * (p.N * p.rep <= 8 ? 3 : 2);
-    const int64_t want = 4 * units <= resident ? resident / units : (4 * resident + units - 1) / units;
-    const int64_t most = chunks / (2 * NW);
-    const int64_t s = want < most ? want : most;
-    return s < 1 ? 1 : s > MAX_SPLITS ? MAX_SPLITS : (int)s;
+    const bool one = p.N * p.rep <= 8;
+    const float units = (float)p.B * p.Hkv * p.row_groups, resident = (float)device_sm_count() * (one ? 3 : 2);
+    const float besides = one ? 3.0f : 8.0f;
+    int best = 1;
+    float least = 0.0f;
+    for (int s = 1; s <= MAX_SPLITS && (s == 1 || s * NW <= chunks); ++s) {
+        const float waves = units * s / resident;
+        const float cost = (waves <= 1.0f ? 1.0f : waves + 0.5f) * ((chunks + s * NW - 1) / (s * NW) + besides) +
+                           (s > 1 ? 2.0f + s / 16 : 0.0f);   // the join
+        if (s == 1 || cost < least) least = cost, best = s;
+        if (waves > 8.0f) break;
+    }
+    if (requested > 0) best = requested < chunks ? requested : chunks;
+    if (best > MAX_SPLITS) best = MAX_SPLITS;
+    if (best < 1) best = 1;
+    p.split_chunks = (chunks + best - 1) / best;
+    p.splits = chunks == 0 ? 1 : (chunks + p.split_chunks - 1) / p.split_chunks;
+    return least;
 }
 
 bool valid(const eagle3_verify_attn_fp8_args_t *a, eagle3_status_t *why) {
@@ -538,7 +604,7 @@ bool valid(const eagle3_verify_attn_fp8_args_t *a, eagle3_status_t *why) {
     return true;
 }
 
-CacheAttn plan(const eagle3_verify_attn_fp8_args_t *a) {
+CacheAttn plan(const eagle3_verify_attn_fp8_args_t *a, bool &wide) {
     CacheAttn p = {};
     p.B = a->batch;
     p.N = a->n_nodes;
@@ -565,11 +631,16 @@ CacheAttn plan(const eagle3_verify_attn_fp8_args_t *a) {
     p.out = (__nv_bfloat16 *)a->out;
     p.lse = a->lse;
     p.dev_status = a->dev_status;
-    p.splits = plan_splits(p, a->num_splits);
+    p.row_groups = (p.N * p.rep + MAX_ROWS - 1) / MAX_ROWS;
+    // 16 rows at a time by warps, or 128 by tensor memory: the latter reads a prefix once for up to 128 rows, but takes
+    // 30 us to get going and to join.  Both fits in us, over measurements of 1 to 64 sequences: 8 nodes of 4 heads over
+    // 2048 positions 31 to 47 us (16 rows at a time first) of 8 sequences and 99 to 144 us of 64; 60 nodes 24 to 33 us
+    // of one sequence, 157 to 98 us of 16.
+    const float tiles = (p.max_prefix + 127) / 128 + (p.tree_k ? 8.0f : 2.0f);
+    const float wide_us = 30.0f + (float)p.B * p.Hkv * ((p.N * p.rep + 127) / 128) * tiles / 138.0f;
+    wide = plan_splits(p, a->num_splits) + 6.0f > wide_us && p.N * p.rep > MAX_ROWS;
     return p;
 }
-
-bool is_wide(const CacheAttn &p) { return p.N * p.rep > MAX_ROWS; }
 
 size_t workspace_of(const CacheAttn &p) {
     return p.splits > 1 ? (size_t)p.splits * p.B * p.N * p.Hq * (D + 2) * sizeof(float) + 256 : 0;
@@ -580,32 +651,72 @@ size_t workspace_of(const CacheAttn &p) {
 
 using namespace e3;
 
-extern "C" size_t eagle3_verify_attn_fp8_workspace_size(const eagle3_verify_attn_fp8_args_t *a) {
-    eagle3_status_t why;
-    if (!valid(a, &why) || a->batch == 0) return 0;
-    const CacheAttn p = plan(a);
-    return is_wide(p) ? cache_attn_wide_workspace(p, a->num_splits) : workspace_of(p);
+namespace {
+
+// choice: KERNEL_AUTO, or a kernel by name (test hooks); false: that kernel does not take the call
+enum { KERNEL_AUTO = 0, KERNEL_ROWS = 1, KERNEL_WIDE = 2 };
+bool choose(const CacheAttn &p, int choice, bool &wide) {
+    if (choice == KERNEL_AUTO) return true;
+    wide = choice == KERNEL_WIDE;
+    return !wide || p.N * p.rep > MAX_ROWS;
 }
 
-extern "C" eagle3_status_t eagle3_verify_attn_fp8(const eagle3_verify_attn_fp8_args_t *a, void *workspace,
-                                                  size_t workspace_bytes, eagle3_stream_t stream) {
+size_t workspace_size(const eagle3_verify_attn_fp8_args_t *a, int choice) {
+    eagle3_status_t why;
+    if (!valid(a, &why) || a->batch == 0) return 0;
+    bool wide;
+    const CacheAttn p = plan(a, wide);
+    if (!choose(p, choice, wide)) return 0;
+    return wide ? cache_attn_wide_workspace(p, a->num_splits) : workspace_of(p);
+}
+
+eagle3_status_t verify_attn(const eagle3_verify_attn_fp8_args_t *a, int choice, const WaitRule &wait, void *workspace,
+                            size_t workspace_bytes, cudaStream_t st) {
     eagle3_status_t why;
     if (!valid(a, &why) || a->batch == 0) return why;
-    CacheAttn p = plan(a);
-    if (is_wide(p)) return cache_attn_wide(p, a->num_splits, WaitRule(), workspace, workspace_bytes, (cudaStream_t)stream);
+    bool wide;
+    CacheAttn p = plan(a, wide);
+    if (!choose(p, choice, wide)) return EAGLE3_ERR_INVALID_ARGUMENT;
+    if (wide) return cache_attn_wide(p, a->num_splits, wait, workspace, workspace_bytes, st);
     if (p.splits > 1) {
         if (!workspace || workspace_bytes < workspace_of(p)) return EAGLE3_ERR_WORKSPACE;
         p.part_o = (float *)(((uintptr_t)workspace + 255) & ~(uintptr_t)255);
         p.part_ml = p.part_o + (size_t)p.splits * p.B * p.N * p.Hq * D;
     }
-    const cudaStream_t st = (cudaStream_t)stream;
-    const dim3 grid((unsigned)p.splits, (unsigned)p.Hkv, (unsigned)p.B);
+    const dim3 grid((unsigned)p.splits, (unsigned)(p.Hkv * p.row_groups), (unsigned)p.B);
     auto *kernel = p.N * p.rep <= 8 ? cache_attn_rows_kernel<1> : cache_attn_rows_kernel<2>;
     if (launch_pdl(kernel, grid, dim3(NT), 0, st, p) != cudaSuccess) return EAGLE3_ERR_CUDA;
     if (p.splits > 1) {
         const long long rows = (long long)p.B * p.N * p.Hq;
-        if (launch_pdl(cache_attn_merge_kernel, dim3((unsigned)rows), dim3(NT), 0, st, p) != cudaSuccess)
-            return EAGLE3_ERR_CUDA;
+        const cudaError_t e = p.splits <= FEW_SPLITS
+                                  ? launch_pdl(cache_attn_merge_few_kernel, dim3((unsigned)((rows + NW - 1) / NW)), dim3(NT), 0, st, p)
+                                  : launch_pdl(cache_attn_merge_kernel, dim3((unsigned)rows), dim3(NT), 0, st, p);
+        if (e != cudaSuccess) return EAGLE3_ERR_CUDA;
     }
     return EAGLE3_OK;
+}
+
+}  // namespace
+
+extern "C" size_t eagle3_verify_attn_fp8_workspace_size(const eagle3_verify_attn_fp8_args_t *a) {
+    return workspace_size(a, KERNEL_AUTO);
+}
+
+extern "C" eagle3_status_t eagle3_verify_attn_fp8(const eagle3_verify_attn_fp8_args_t *a, void *workspace,
+                                                  size_t workspace_bytes, eagle3_stream_t stream) {
+    return verify_attn(a, KERNEL_AUTO, WaitRule(), workspace, workspace_bytes, (cudaStream_t)stream);
+}
+
+extern "C" size_t eagle3_test_verify_attn_fp8_workspace_size(const eagle3_verify_attn_fp8_args_t *a, int32_t kernel) {
+    return kernel < KERNEL_ROWS || kernel > KERNEL_WIDE ? 0 : workspace_size(a, kernel);
+}
+
+extern "C" eagle3_status_t eagle3_test_verify_attn_fp8(const eagle3_verify_attn_fp8_args_t *a, void *workspace,
+                                                       size_t workspace_bytes, int32_t kernel, int32_t stall_block,
+                                                       int64_t wait_limit_cycles, eagle3_stream_t stream) {
+    WaitRule wait;
+    if (kernel < KERNEL_ROWS || kernel > KERNEL_WIDE || (stall_block >= 0 && kernel != KERNEL_WIDE) ||
+        (stall_block != -1 && !stall_rule(&wait, stall_block, -1, wait_limit_cycles)))
+        return EAGLE3_ERR_INVALID_ARGUMENT;
+    return verify_attn(a, kernel, wait, workspace, workspace_bytes, (cudaStream_t)stream);
 }

@@ -728,7 +728,7 @@ __global__ void __launch_bounds__(NT, 1)
     } else {
         // ------------------------------------------------------------------ softmax and results
         // (no way out of the loops: the two warps of a quarter meet at a barrier for every tile; after a wait that ran
-        // out they go on without waiting)
+        // out they go on without waiting, and follow no parents, which may not be there)
         const int quarter = warp & 3, half = (warp - 8) >> 2, r = quarter * 32 + lane;
         const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
         auto pair_sync = [&] { asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory"); };
@@ -773,7 +773,7 @@ __global__ void __launch_bounds__(NT, 1)
                 if (lane == 0) tc::mbar_arrive(bar(ss.s_empty[t & 1]));
                 if (RARELY(tree || keys < 64)) {
                     uint64_t vis = keys > 0 ? (1ull << keys) - 1ull : 0ull;
-                    if (tree) vis = half == 0 && r < nrows ? path_of(ss.par[u], row_node(p, row0 + r)) : 0ull;
+                    if (tree) vis = ok && half == 0 && r < nrows ? path_of(ss.par[u], row_node(p, row0 + r)) : 0ull;
                     const uint32_t v0 = (uint32_t)vis, v1 = (uint32_t)(vis >> 32);
 #pragma unroll
                     for (int e = 0; e < 64; ++e) sc[e] = ((e < 32 ? v0 : v1) >> (e & 31)) & 1u ? sc[e] : -INFINITY;
@@ -849,7 +849,7 @@ __global__ void __launch_bounds__(NT, 1)
             const int node = row_node(p, row0 + r), head = g * a.rep + row0 + r - node * a.rep;
             const size_t at = ((size_t)w.b * a.N + (mine ? node : 0)) * a.Hq + (mine ? head : 0);
             const size_t part = (size_t)(2 * blockIdx.x + (w.n > 0 ? 1 : 0)) * ROWS + r;
-            const uint64_t anc = odd_v && mine ? path_of(ss.par[u], node) : 0;
+            const uint64_t anc = ok && odd_v && mine ? path_of(ss.par[u], node) : 0;
             // (a row without a key has summed up nothing)
             const float back = scale_of(evref), inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
 #pragma unroll 1

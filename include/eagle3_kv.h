@@ -180,12 +180,12 @@ eagle3_status_t eagle3_append_kv(const eagle3_append_kv_args_t *args, eagle3_str
  * before L make the queries that see them NaN.  A page id outside the pool reads as keys and values of
  * zero.  prefix_len[b] outside [0, max_prefix_len] is cut and raises EAGLE3_DEV_CAPACITY; a tree that is
  * not one raises EAGLE3_DEV_BAD_TREE and its nodes end at the bad one.
- * Scores, softmax statistics and sums are fp32.  Up to 16 query rows a KV head (n_nodes * Hq / Hkv), q and
- * tree_k enter the tensor cores as fp16, scaled by a power of two of their own; beyond, as two e4m3 parts: 8
- * bits, but no finer than 2^-17 of the row's (of the tree's) largest element, and infinities as NaN.
- * Weights are rounded to fp16 (11 bits); V's codes are exact where their scale is above 2^-21 of the
- * sequence's largest, and at any scale no finer than 2^-31 of that.  Where work is cut depends on the lengths, the shape and the
- * number of SMs: results are reproducible for the same call on a given GPU model.
+ * Scores, softmax statistics and sums are fp32.  q and tree_k enter the tensor cores as fp16, scaled by a power
+ * of two of their own, or, with many query rows a KV head (more than 16 of n_nodes * Hq / Hkv; batch and
+ * max_prefix_len decide too), as two e4m3 parts: 8 bits, but no finer than 2^-17 of the row's (of the tree's)
+ * largest element, and infinities as NaN.  Weights are rounded to fp16 (11 bits); V's codes are exact where their scale is above
+ * 2^-21 of the sequence's largest, and at any scale no finer than 2^-31 of that.  Where work is cut depends
+ * on the lengths, the shape and the number of SMs: results are reproducible for the same call on a given GPU model.
  * ---------------------------------------------------------------------------------------------- */
 typedef struct {
     int32_t batch;               /* B >= 0                                                            */
@@ -194,7 +194,7 @@ typedef struct {
     int32_t n_kv_heads;          /* Hkv                                                               */
     int32_t head_dim;            /* D; 128 is supported                                               */
     int32_t max_prefix_len;      /* host bound on prefix_len[b], >= 0                                 */
-    int32_t num_splits;          /* parts of the prefix; 0 = choose automatically                     */
+    int32_t num_splits;          /* parts of the prefix, at most 512; 0 = choose automatically        */
     int32_t max_blocks;          /* columns of block_table; max_blocks * block_size >= max_prefix_len */
     int32_t block_size;          /* places of a page, a multiple of 64                                */
     int32_t n_pages;             /* pages of the pool                                                 */

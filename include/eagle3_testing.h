@@ -12,6 +12,7 @@
 
 #include "eagle3.h"
 #include "eagle3_fp8.h"
+#include "eagle3_kv.h"
 #include "eagle3_moe.h"
 
 #ifdef __cplusplus
@@ -43,6 +44,19 @@ eagle3_status_t eagle3_test_grouped_linear_timeout(const eagle3_grouped_linear_a
                                                    eagle3_stream_t stream);
 eagle3_status_t eagle3_test_linear_fp8_timeout(const eagle3_linear_fp8_args_t *args, int32_t stall_block,
                                                int32_t stall_rank, int64_t wait_limit_cycles, eagle3_stream_t stream);
+
+/* eagle3_test_verify_attn_fp8 - eagle3_verify_attn_fp8 by the kernel that takes 16 query rows at a time
+ * (kernel 1) or the one that takes 128 (kernel 2, more than 16 query rows a KV head only), whichever the call
+ * itself would choose, with a workspace of its own size.  stall_block >= 0, kernel 2 only: the barriers of the
+ * load stage that the prefix tile stall_block of each CTA goes through expect an arrival that never comes, and
+ * every bounded wait gives up after wait_limit_cycles SM clocks.  A CTA with more than stall_block prefix tiles
+ * gives up, sets EAGLE3_DEV_TIMEOUT and exits cleanly; the outputs are void.  stall_block -1: as ever.
+ * Returns EAGLE3_ERR_INVALID_ARGUMENT for another kernel, stall_block outside [-1, 3] or, with one,
+ * wait_limit_cycles outside [1000, 4e9], otherwise what eagle3_verify_attn_fp8 returns. */
+size_t eagle3_test_verify_attn_fp8_workspace_size(const eagle3_verify_attn_fp8_args_t *args, int32_t kernel);
+eagle3_status_t eagle3_test_verify_attn_fp8(const eagle3_verify_attn_fp8_args_t *args, void *workspace,
+                                            size_t workspace_bytes, int32_t kernel, int32_t stall_block,
+                                            int64_t wait_limit_cycles, eagle3_stream_t stream);
 
 #ifdef __cplusplus
 }

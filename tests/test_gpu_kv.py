@@ -22,6 +22,7 @@ import pytest
 import torch
 
 import eagle_tree_speculative_spec_gb300 as e3
+from eagle_tree_speculative_spec_gb300 import _lib
 from oracle import fp8, kv
 from tests._util import require_gpu
 
@@ -408,6 +409,25 @@ def test_append_offsets_past_32_bits():
 
 
 # ----------------------------------------------------------------------------- attention
+def pytest_generate_tests(metafunc):
+    """Each attention test by the kernel that the call chooses and, where it takes the call, by the one of 128 rows."""
+    if metafunc.function.__name__.startswith("test_attn"):
+        metafunc.parametrize("kernel", ["own choice", "128 rows"], indirect=True)
+
+
+@pytest.fixture(autouse=True)
+def kernel(request, monkeypatch):
+    if getattr(request, "param", None) != "128 rows":
+        return
+    public = e3.eagle3_verify_attn_fp8
+
+    def call(q, k_cache, *args, **kw):
+        if q.shape[1] * q.shape[2] // k_cache.shape[1] <= 16:
+            return public(q, k_cache, *args, **kw)
+        return _lib.eagle3_test_verify_attn_fp8(q, k_cache, *args, kernel=2, **kw)
+    monkeypatch.setattr(e3, "eagle3_verify_attn_fp8", call)
+
+
 def _trees(B, N, seed):
     r = np.random.default_rng(seed)
     par = np.full((B, N), -1, np.int32)
