@@ -25,7 +25,7 @@ constexpr int FEW = 8;   // new tokens a sequence for which a warp takes a job
 struct Params {
     int B, Hkv, D, n_rows, max_new, rows_per_seq, max_blocks, block_size, n_pages, R, half;
     int groups_per_seq;      // groups that max_new tokens can touch
-    int jobs_per_cta;        // of the 2 * Hkv (head, K or V) jobs of a group
+    int jobs, jobs_per_cta;  // the (sequence, group, head, K or V) jobs of all groups
     int interleaved, paired;   // paired: dims lie in whole runs of 8 pairs
     float amplitude;
     int64_t rs;
@@ -184,9 +184,9 @@ E3_DEV uint4 bf16x8(const float *v) {
     return u;
 }
 
-// A job is a head's keys (even) or values (odd) of a group, by a warp or by the CTA.  grid: (group of a sequence, share
-// of its jobs, sequence).  A thread keeps its unit and its rows, ITEMS of them, for all of its jobs, and loads the
-// next job's before it converts this one's.
+// A job is a head's keys (even) or values (odd) of a group, by a warp or by the CTA; a CTA takes a run of the jobs of all
+// groups.  A thread keeps its unit and its rows, ITEMS of them, for all jobs of a group, and loads the next job's before
+// it converts this one's.
 template <int ITEMS, bool E4M3, bool BY_WARP, bool PAIRED>
 __global__ void __launch_bounds__(NT, ITEMS == 2 && PAIRED ? 3 : 1) append_kernel(const Params p) {
     constexpr int THREADS = BY_WARP ? 32 : NT;
@@ -195,147 +195,156 @@ __global__ void __launch_bounds__(NT, ITEMS == 2 && PAIRED ? 3 : 1) append_kerne
     float2 *const cs = reinterpret_cast<float2 *>(cs4);
     pdl_wait();
     pdl_trigger();
-    Span s;
-    if (!find_span(p, blockIdx.z, blockIdx.x, threadIdx.x == 0 && blockIdx.y == 0, s)) return;
-    const int32_t *bt = p.block_table + (size_t)s.b * p.max_blocks;
-    int page = -1;
-    if (E4M3) {
-        page = __ldg(bt + s.page);
-        if (page < 0 || page >= p.n_pages) {
-            if (threadIdx.x == 0 && blockIdx.y == 0) flag(p.dev_status, EAGLE3_DEV_CAPACITY);
-            return;
-        }
-    }
     const int warp = threadIdx.x >> 5, t = BY_WARP ? threadIdx.x & 31 : threadIdx.x;
     const int units = (p.D + 15) / 16, step = THREADS / units;   // rows at a time
     const int row0 = t / units, u = t - row0 * units;
-    const bool reports = blockIdx.y == 0 && u == 0 && (!BY_WARP || warp == 0);
     const Unit un = unit_of(p, u);
-    int src[ITEMS], slot[ITEMS];   // the rows they come from and, bf16, the places they go to; src < 0: none
-#pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-        const int row = row0 + i * step;
-        src[i] = -1;
-        if (row0 < step && row < s.hi - s.lo) {
-            src[i] = source_row(p, s.b, s.j0 + row);
-            if (src[i] < 0 && reports) flag(p.dev_status, EAGLE3_DEV_BAD_TOKEN);
-        }
-        if (!E4M3 && src[i] >= 0) {   // a page may end inside the group
-            const int pos = s.len + s.j0 + row, block = pos / p.block_size;
-            const int id = __ldg(bt + block);
-            slot[i] = id * p.block_size + (pos - block * p.block_size);
-            if (id < 0 || id >= p.n_pages) {
-                if (reports) flag(p.dev_status, EAGLE3_DEV_CAPACITY);
-                src[i] = -1;
+    const int pitch = cs_pitch(p.half);
+    const int at0 = blockIdx.x * p.jobs_per_cta, end = min(p.jobs - at0, p.jobs_per_cta) + at0;
+    int parity = 0;
+    for (int at = at0; at < end;) {
+        const int group = at / (2 * p.Hkv), b = group / p.groups_per_seq;
+        const int j0 = at - group * (2 * p.Hkv), j1 = min(2 * p.Hkv, j0 + (end - at));
+        at += j1 - j0;
+        Span s;
+        if (!find_span(p, b, group - b * p.groups_per_seq, threadIdx.x == 0 && j0 == 0, s)) continue;
+        const int32_t *bt = p.block_table + (size_t)s.b * p.max_blocks;
+        int page = -1;
+        if (E4M3) {
+            page = __ldg(bt + s.page);
+            if (page < 0 || page >= p.n_pages) {
+                if (threadIdx.x == 0 && j0 == 0) flag(p.dev_status, EAGLE3_DEV_CAPACITY);
+                continue;
             }
         }
-    }
-    uint4 next[ITEMS][2];
-    auto fetch = [&](int job) {
-        const __nv_bfloat16 *from = (job & 1 ? p.v : p.k) + (size_t)(job >> 1) * p.D;
+        const bool reports = j0 == 0 && u == 0 && (!BY_WARP || warp == 0);
+        int src[ITEMS];
+        long long slot[ITEMS];   // the rows they come from and, bf16, the places they go to; src < 0: none
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
-            next[i][0] = next[i][1] = make_uint4(0, 0, 0, 0);
-            if (src[i] < 0) continue;
-            next[i][0] = *reinterpret_cast<const uint4 *>(from + src[i] * p.rs + un.da);
-            if (un.db >= 0) next[i][1] = *reinterpret_cast<const uint4 *>(from + src[i] * p.rs + un.db);
+            const int row = row0 + i * step;
+            src[i] = -1;
+            if (row0 < step && row < s.hi - s.lo) {
+                src[i] = source_row(p, s.b, s.j0 + row);
+                if (src[i] < 0 && reports) flag(p.dev_status, EAGLE3_DEV_BAD_TOKEN);
+            }
+            if (!E4M3 && src[i] >= 0) {   // a page may end inside the group
+                const int pos = s.len + s.j0 + row, block = pos / p.block_size;
+                const int id = __ldg(bt + block);
+                slot[i] = (long long)id * p.block_size + (pos - block * p.block_size);
+                if (id < 0 || id >= p.n_pages) {
+                    if (reports) flag(p.dev_status, EAGLE3_DEV_CAPACITY);
+                    src[i] = -1;
+                }
+            }
         }
-    };
-    const int j0 = blockIdx.y * p.jobs_per_cta, j1 = min(2 * p.Hkv, j0 + p.jobs_per_cta);
-    const int first = BY_WARP ? j0 + warp : j0, jump = BY_WARP ? NT / 32 : 1;
-    if (first < j1) fetch(first);
-    const int pitch = cs_pitch(p.half);
-    if (p.table)
-        for (int i = threadIdx.x; i < (s.hi - s.lo) * p.half; i += NT) {
-            const int row = i / p.half, j = i - row * p.half;
-            cs[row * pitch + pair_at(j)] = turned(s.len + s.j0 + row, __ldg(p.table + j), p.amplitude);
-        }
-    __syncthreads();
-    int parity = 0;
-    for (int job = first; job < j1; job += jump) {
-        const bool is_v = job & 1;
-        const int h = job >> 1;
-        const size_t head_page = (size_t)page * p.Hkv + h;
-        uint8_t *scales = nullptr;
-        int old = 0;
-        if (E4M3) {
-            scales = (is_v ? p.vs : p.ks) + head_page * (p.block_size / GROUP) + s.place / GROUP;
-            if (s.lo > 0) old = *scales;
-        }
-        float val[ITEMS][16];
-        float top = 0.0f;
-#pragma unroll
-        for (int i = 0; i < ITEMS; ++i) {
-            unpack8(next[i][0], val[i]);
-            unpack8(next[i][1], val[i] + 8);
-        }
-        if (job + jump < j1) fetch(job + jump);
-        if (p.table && !is_v) {
-#pragma unroll
-            for (int i = 0; i < ITEMS; ++i)
-                if (src[i] >= 0)
-                    turn_unit<PAIRED>(p, un, p.k + (size_t)h * p.D + src[i] * p.rs, cs + (row0 + i * step) * pitch, val[i]);
-        }
-        uint8_t *dst = is_v ? p.vc : p.kc;
-        if constexpr (!E4M3) {
+        uint4 next[ITEMS][2];
+        auto fetch = [&](int job) {
+            const __nv_bfloat16 *from = (job & 1 ? p.v : p.k) + (size_t)(job >> 1) * p.D;
 #pragma unroll
             for (int i = 0; i < ITEMS; ++i) {
+                next[i][0] = next[i][1] = make_uint4(0, 0, 0, 0);
                 if (src[i] < 0) continue;
-                uint8_t *to = dst + ((size_t)slot[i] * p.Hkv + h) * p.D * 2;
-                *reinterpret_cast<uint4 *>(to + un.da * 2) = bf16x8(val[i]);
-                if (un.db >= 0) *reinterpret_cast<uint4 *>(to + un.db * 2) = bf16x8(val[i] + 8);
+                next[i][0] = *reinterpret_cast<const uint4 *>(from + src[i] * p.rs + un.da);
+                if (un.db >= 0) next[i][1] = *reinterpret_cast<const uint4 *>(from + src[i] * p.rs + un.db);
             }
-        } else {
+        };
+        const int first = BY_WARP ? j0 + warp : j0, jump = BY_WARP ? NT / 32 : 1;
+        if (first < j1) fetch(first);
+        __syncthreads();   // (the group before has been turned)
+        if (p.table) {
+            const int j = threadIdx.x % p.half;
+            const uint64_t turns = __ldg(p.table + j);
+            if (threadIdx.x < NT / p.half * p.half)
+                for (int row = threadIdx.x / p.half; row < s.hi - s.lo; row += NT / p.half)
+                    cs[row * pitch + pair_at(j)] = turned(s.len + s.j0 + row, turns, p.amplitude);
+        }
+        __syncthreads();
+        for (int job = first; job < j1; job += jump) {
+            const bool is_v = job & 1;
+            const int h = job >> 1;
+            const size_t head_page = (size_t)page * p.Hkv + h;
+            uint8_t *scales = nullptr;
+            int old = 0;
+            if (E4M3) {
+                scales = (is_v ? p.vs : p.ks) + head_page * (p.block_size / GROUP) + s.place / GROUP;
+                if (s.lo > 0) old = *scales;
+            }
+            float val[ITEMS][16];
+            float top = 0.0f;
 #pragma unroll
-            for (int i = 0; i < ITEMS; ++i)
+            for (int i = 0; i < ITEMS; ++i) {
+                unpack8(next[i][0], val[i]);
+                unpack8(next[i][1], val[i] + 8);
+            }
+            if (job + jump < j1) fetch(job + jump);
+            if (p.table && !is_v) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(val[i][e]));   // (passes over NaN)
-            if (top > FLT_MAX) {   // infinities become NaN, and no scale follows them
-                top = 0.0f;
+                for (int i = 0; i < ITEMS; ++i)
+                    if (src[i] >= 0)
+                        turn_unit<PAIRED>(p, un, p.k + (size_t)h * p.D + src[i] * p.rs, cs + (row0 + i * step) * pitch, val[i]);
+            }
+            uint8_t *dst = is_v ? p.vc : p.kc;
+            if constexpr (!E4M3) {
+#pragma unroll
+                for (int i = 0; i < ITEMS; ++i) {
+                    if (src[i] < 0) continue;
+                    uint8_t *to = dst + ((size_t)slot[i] * p.Hkv + h) * p.D * 2;
+                    *reinterpret_cast<uint4 *>(to + un.da * 2) = bf16x8(val[i]);
+                    if (un.db >= 0) *reinterpret_cast<uint4 *>(to + un.db * 2) = bf16x8(val[i] + 8);
+                }
+            } else {
 #pragma unroll
                 for (int i = 0; i < ITEMS; ++i)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float a = fabsf(val[i][e]);
-                        if (a <= FLT_MAX)
-                            top = fmaxf(top, a);
-                        else
-                            val[i][e] = __int_as_float(0x7fc00000);
+                    for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(val[i][e]));   // (passes over NaN)
+                if (top > FLT_MAX) {   // infinities become NaN, and no scale follows them
+                    top = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < ITEMS; ++i)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float a = fabsf(val[i][e]);
+                            if (a <= FLT_MAX)
+                                top = fmaxf(top, a);
+                            else
+                                val[i][e] = __int_as_float(0x7fc00000);
+                        }
+                }
+                // magnitudes are in the order of their bits
+                top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+                if constexpr (!BY_WARP) {
+                    if ((t & 31) == 0) scratch[parity][warp] = top;
+                    __syncthreads();   // the scale has been read by everyone too
+#pragma unroll
+                    for (int w = 0; w < NT / 32; ++w) top = fmaxf(top, scratch[parity][w]);
+                    parity ^= 1;
+                }
+                const int byte = max(old, scale_byte(top));
+                if (t == 0) *scales = (uint8_t)byte;
+                uint8_t *codes = dst + (head_page * p.block_size + s.place) * p.D;
+                const float inv = inverse_scale(byte);
+#pragma unroll
+                for (int i = 0; i < ITEMS; ++i) {
+                    if (src[i] < 0) continue;
+                    uint8_t *to = codes + (size_t)(s.lo + row0 + i * step) * p.D;
+                    *reinterpret_cast<uint2 *>(to + un.da) = codes8(val[i], inv);
+                    if (un.db >= 0) *reinterpret_cast<uint2 *>(to + un.db) = codes8(val[i] + 8, inv);
+                }
+                if (s.lo > 0 && byte > old) {
+                    // steps far below the new one leave nothing but the sign
+                    const float factor = byte - old > 40 ? 0.0f : __int_as_float((127 - (byte - old)) << 23);
+                    uint2 *c = reinterpret_cast<uint2 *>(codes);
+                    const int n = s.lo * (p.D / 8);
+                    constexpr int K = 8;   // loads in flight
+                    for (int it = t; it < n; it += K * THREADS) {
+                        uint2 w[K];
+#pragma unroll
+                        for (int k = 0; k < K; ++k) w[k] = it + k * THREADS < n ? c[it + k * THREADS] : make_uint2(0, 0);
+#pragma unroll
+                        for (int k = 0; k < K; ++k)
+                            if (it + k * THREADS < n) c[it + k * THREADS] = scaled_down(w[k], factor);
                     }
-            }
-            // magnitudes are in the order of their bits
-            top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-            if constexpr (!BY_WARP) {
-                if ((t & 31) == 0) scratch[parity][warp] = top;
-                __syncthreads();   // the scale has been read by everyone too
-#pragma unroll
-                for (int w = 0; w < NT / 32; ++w) top = fmaxf(top, scratch[parity][w]);
-                parity ^= 1;
-            }
-            const int byte = max(old, scale_byte(top));
-            if (t == 0) *scales = (uint8_t)byte;
-            uint8_t *codes = dst + (head_page * p.block_size + s.place) * p.D;
-            const float inv = inverse_scale(byte);
-#pragma unroll
-            for (int i = 0; i < ITEMS; ++i) {
-                if (src[i] < 0) continue;
-                uint8_t *to = codes + (size_t)(s.lo + row0 + i * step) * p.D;
-                *reinterpret_cast<uint2 *>(to + un.da) = codes8(val[i], inv);
-                if (un.db >= 0) *reinterpret_cast<uint2 *>(to + un.db) = codes8(val[i] + 8, inv);
-            }
-            if (s.lo > 0 && byte > old) {
-                // steps far below the new one leave nothing but the sign
-                const float factor = byte - old > 40 ? 0.0f : __int_as_float((127 - (byte - old)) << 23);
-                uint2 *c = reinterpret_cast<uint2 *>(codes);
-                const int n = s.lo * (p.D / 8);
-                constexpr int K = 8;   // loads in flight
-                for (int it = t; it < n; it += K * THREADS) {
-                    uint2 w[K];
-#pragma unroll
-                    for (int k = 0; k < K; ++k) w[k] = it + k * THREADS < n ? c[it + k * THREADS] : make_uint2(0, 0);
-#pragma unroll
-                    for (int k = 0; k < K; ++k)
-                        if (it + k * THREADS < n) c[it + k * THREADS] = scaled_down(w[k], factor);
                 }
             }
         }
@@ -425,13 +434,16 @@ extern "C" eagle3_status_t eagle3_append_kv(const eagle3_append_kv_args_t *a, ea
     const int reach = p.max_new < p.max_blocks * p.block_size ? p.max_new : p.max_blocks * p.block_size;
     p.groups_per_seq = (reach - 1 + GROUP - 1) / GROUP + 1;
     const int jobs = 2 * p.Hkv;
-    // enough CTAs for every SM to have three; a share of jobs no smaller than its warps when a warp takes a job
-    const int64_t ctas = (int64_t)p.groups_per_seq * p.B;
-    int cuts = 1;
-    while (cuts < jobs && ctas * cuts < 3 * device_sm_count()) cuts *= 2;
-    p.jobs_per_cta = (jobs + cuts - 1) / cuts;
-    if (few && p.jobs_per_cta < NT / 32) p.jobs_per_cta = jobs < NT / 32 ? jobs : NT / 32;
-    const dim3 grid((unsigned)p.groups_per_seq, (unsigned)((jobs + p.jobs_per_cta - 1) / p.jobs_per_cta), (unsigned)p.B);
+    // one wave of CTAs, each with its run of jobs (16384 tokens of 8 heads: 9 jobs for each of 456; 8 for each of 512
+    // took 31.8 us); no fewer than its warps when a warp takes a job.  bf16 jobs are short beside what a CTA begins with,
+    // the table's angles: more CTAs, of fewer (7 x 999 tokens of 5 heads 7.4 us by two, 10.3 us by three jobs a CTA)
+    const int64_t most = (e4m3 ? 3 : 4) * (int64_t)device_sm_count(), all = (int64_t)p.groups_per_seq * p.B * jobs;
+    if (all > MAX_DIM) return EAGLE3_ERR_UNSUPPORTED;
+    p.jobs = (int)all;
+    p.jobs_per_cta = (int)((all + most - 1) / most);
+    const int least = few ? jobs < NT / 32 ? jobs : NT / 32 : 1;
+    if (p.jobs_per_cta < least) p.jobs_per_cta = least;
+    const dim3 grid((unsigned)((all + p.jobs_per_cta - 1) / p.jobs_per_cta));
     const size_t smem = (size_t)(few ? FEW : GROUP) * ((p.half + 7) / 8 * 8) * sizeof(float2);
     const cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e;
