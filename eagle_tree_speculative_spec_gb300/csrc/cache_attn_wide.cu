@@ -493,13 +493,7 @@ __global__ void __launch_bounds__(NT, 1)
         };
         for (bool more = w.begin(p, ss, range); more && ok; more = ok && w.next(p)) {
             const int u = w.n & 1, g = w.k;
-            if ((w.n >= 2 && !wait_warp(bar(ss.u_empty[u]), ((w.n - 2) >> 1) & 1u, abort, limit)) ||
-                (w.n > 0 && !wait_warp(bar(ss.q_empty), (w.n - 1) & 1u, abort, limit))) {
-                ok = false;
-                break;
-            }
             const bool tree = w.has_tree(p);
-            tc::fence_after();
             // the tree's parents, which the rows' paths are followed through; the loads return while Q is loaded
             int par[2] = {-1, -1};
             if (cw == 0 && tree) {
@@ -541,18 +535,26 @@ __global__ void __launch_bounds__(NT, 1)
                 const uint32_t tj = lane & 16 ? t1 : t0;
                 const int byte = scale_byte_bits(lane & 8 ? tj >> 16 : tj & 0xffffu);
                 const float up = r < nrows ? inverse_scale(byte) : 0.0f;   // (rows behind the last one: zeros)
+                // (until here beside the unit before's last tiles)
+                if ((w.n >= 2 && !wait_warp(bar(ss.u_empty[u]), ((w.n - 2) >> 1) & 1u, abort, limit)) ||
+                    (w.n > 0 && !wait_warp(bar(ss.q_empty), (w.n - 1) & 1u, abort, limit))) {
+                    ok = false;
+                    break;
+                }
+                tc::fence_after();
                 const uint32_t tq = tmem + ((uint32_t)(cw * 32) << 16) + TM_Q;
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {   // 32 dims: 8 columns of each part
-                    uint4 x[4];
-                    uint32_t hi[8], lo[8];
+                uint4 x[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) x[j] = load(j, c);
+                for (int j = 0; j < 4; ++j) x[j] = load(j, 0);
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {   // 32 dims: 8 columns of each part; the next 32 on their way
+                    uint32_t hi[8], lo[8];
                     __syncwarp();
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int rr = 8 * j + (lane >> 2);
                         *reinterpret_cast<uint4 *>(buf + rr * 64 + (((lane & 3) ^ (rr >> 1 & 3)) << 4)) = x[j];
+                        x[j] = load(j, min(c + 1, 3));
                     }
                     __syncwarp();
 #pragma unroll
