@@ -7,7 +7,10 @@
 //
 // A row's angles are shared by its heads: a CTA takes a few rows and first fills their cosines and sines into shared
 // memory, one sincospif a thread, then walks the heads.  A thread's unit is the two runs of V elements that hold V
-// pairs, so that it reads and writes both ends of each pair itself and the call can run in place.
+// pairs, so that it reads and writes both ends of each pair itself and the call can run in place; it stays with one row,
+// whose cosines it holds in registers, and has four heads' loads in flight.
+// Bound by memory: 3840 rows of 40 bf16 heads of 128 (78.6 MB) take 16.4 us, 4.8 TB/s (11.6 us at the copy's rate); with the
+// cosines read from shared memory for every head (lanes 64 bytes apart: four-way conflicts) and one head at a time, 26.9 us.
 #include "rope.cuh"
 
 #include <cmath>

@@ -127,7 +127,8 @@ eagle3_status_t eagle3_rope(const eagle3_rope_args_t *args, eagle3_stream_t stre
  * sequence is left out and EAGLE3_DEV_CAPACITY raised.  A page id outside the pool: the group is left
  * out and EAGLE3_DEV_CAPACITY raised.  A row outside [0, n_rows) (with row_ids: outside
  * [0, rows_per_seq) of its sequence): the token is left out and EAGLE3_DEV_BAD_TOKEN raised.
- * A page that is written must belong to one sequence.
+ * A page that is written must belong to one sequence.  batch * (groups of 64 that max_new tokens can touch) *
+ * 2 * n_kv_heads must be below 2^31 - 2^16.
  * ---------------------------------------------------------------------------------------------- */
 typedef enum {
     EAGLE3_KV_BF16 = 0,

@@ -90,6 +90,7 @@ def _append(**kw):
     (dict(block_size=96), 1),                # not whole groups
     (dict(n_pages=0), 1),
     (dict(max_blocks=2 ** 25, block_size=128), 2),
+    (dict(batch=65535, max_new=2 ** 20, max_blocks=2 ** 14), 2),   # more (group, head) jobs than 31 bits count
     (dict(rotary_dim=66), 1),
     (dict(rotary_dim=1), 1),
     (dict(rope_layout=-1), 1),
