@@ -10,7 +10,7 @@
 // once.  A thread's unit is 16 dims of a row, both ends of their pairs among them.  Prompts: a CTA of 256 threads takes a run
 // of jobs, one after the other, with their group's cosines and sines in shared memory, which the keys of all heads share.
 // Few tokens a sequence (at most 8): a warp takes a job.
-// Bound by issue slots: 16384 tokens of 8 heads of 128 (e4m3, 100.7 MB) take 27.2 us, 3.7 TB/s, of which some 15 us are
+// Bound by issue slots: 16384 tokens of 8 heads of 128 (e4m3, 100.7 MB) take 26.1 us, 3.9 TB/s, of which some 15 us are
 // instructions (300 a unit, the angles a quarter of them) and the rest waits for the maximum that the CTA's warps share; by
 // memory alone they would take 14.9 us.  Four CTAs an SM of 64 registers a thread and no load ahead took 29.3 us.
 #include "e4m3.cuh"
@@ -444,8 +444,10 @@ extern "C" eagle3_status_t eagle3_append_kv(const eagle3_append_kv_args_t *a, ea
     const int64_t all = (int64_t)p.groups_per_seq * p.B * jobs;
     if (all > MAX_DIM) return EAGLE3_ERR_UNSUPPORTED;
     const int64_t most = (e4m3 ? 3 : 4) * (int64_t)device_sm_count();
+    // (of the groups that a sequence touches at most, one is there because tokens may begin inside a group: shares are of the others)
+    const int64_t sure = (int64_t)((reach + GROUP - 1) / GROUP) * p.B * jobs;
     p.jobs = (int)all;
-    p.jobs_per_cta = (int)((all + most - 1) / most);
+    p.jobs_per_cta = (int)((sure + most - 1) / most);
     const int least = few ? jobs < NT / 32 ? jobs : NT / 32 : 1;
     if (p.jobs_per_cta < least) p.jobs_per_cta = least;
     const dim3 grid((unsigned)((all + p.jobs_per_cta - 1) / p.jobs_per_cta));
