@@ -21,12 +21,13 @@
 // Rows beyond 16 are groups of CTAs of their own, which read the keys again.
 // Bound by memory: 64 single tokens of 32 heads over up to 8192 positions (669 MB) take 116 us, 5.8 TB/s, one over 250000 (512 MB)
 // 84 us, 6.1 TB/s; the copy's rate is 6.8.  With Q's rows as the tile's 16 (64 MMAs a step where 8 rows need 48, 64 more
-// registers, loads only between steps) they took 174 and 216 us.  One token over 4096 positions: 7.5 us, latency.
+// registers, loads only between steps) they took 174 and 216 us.  One token over 4096 positions: 8.2 us, latency.
 // Q is scaled by a power of two for each row so that fp16 holds it (bf16's 8 bits fit, elements 2^-36 below the row's
 // largest vanish); the factor comes back with the scale of K's group in fp32.  Weights are held 2^7 up, so that fp16's
 // 11 bits reach down to 2^-21 of the largest, and V's group scale is put on them relative to the largest so far.
 #include "cache_attn.cuh"
 #include "eagle3_testing.h"
+#include "tc.cuh"
 
 #include <cfloat>
 
@@ -135,12 +136,25 @@ E3_DEV void softmax_step(RowState<NR> &st, float (&s)[4][4], const float (&f)[NR
 
 // Where a step of 32 keys lies; ek, ev: its scale bytes
 struct Place {
-    const uint8_t *k, *v;
+    size_t at;          // its first code
     int left, ek, ev;   // left: its keys that are there, 0 or less: none
 };
 
-// grid: (split, KV head and group of rows, sequence); NR: 8 NR rows a group
-template <int NR>
+E3_DEV float split_factor(float2 ml, float M) { return ml.y == 0.0f ? 0.0f : ml.x == -INFINITY ? 1.0f : fast_exp2(ml.x - M); }
+E3_DEV float warp_max(float x) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+    return x;
+}
+E3_DEV float warp_sum(float x) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    return x;
+}
+
+// grid: (split, KV head and group of rows, sequence); NR: 8 NR rows a group.  CLUSTERED: the splits are the CTAs of
+// a cluster and read each other's results from shared memory; otherwise they leave theirs to the merge kernels.
+template <int NR, bool CLUSTERED>
 __global__ void __launch_bounds__(NT, NR == 1 ? 3 : 2) cache_attn_rows_kernel(const CacheAttn p) {
     constexpr int ROWS = 8 * NR;
     __shared__ float so[NW][ROWS][O_PITCH];
@@ -170,8 +184,7 @@ __global__ void __launch_bounds__(NT, NR == 1 ? 3 : 2) cache_attn_rows_kernel(co
         const size_t head_page = (size_t)(there ? page : 0) * p.Hkv + h;
         const size_t sg = head_page * sgroups + place / EAGLE3_KV_GROUP;
         Place w;
-        w.k = p.kc + (head_page * p.block_size + place) * D + g * D + 16 * c;
-        w.v = p.vc + (head_page * p.block_size + place) * D + 2 * c * D + 16 * g;
+        w.at = (head_page * p.block_size + place) * D;
         w.left = there ? L - ch * CHUNK : 0;
         w.ek = there ? __ldg(p.ks + sg) : 1;   // (a page that is not there reads as zeros)
         w.ev = there ? __ldg(p.vs + sg) : 1;
@@ -180,19 +193,21 @@ __global__ void __launch_bounds__(NT, NR == 1 ? 3 : 2) cache_attn_rows_kernel(co
     uint4 kw[4][2], vw[2][4];
     const uint4 zero = make_uint4(0, 0, 0, 0);
     auto load_k = [&](const Place &w) {
+        const uint8_t *at = p.kc + w.at + (g * D + 16 * c);
 #pragma unroll
         for (int n = 0; n < 4; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                kw[n][i] = 8 * n + g < w.left ? ld_once(w.k + 8 * n * D + 64 * i) : zero;
+                kw[n][i] = 8 * n + g < w.left ? ld_once(at + 8 * n * D + 64 * i) : zero;
     };
     auto load_v = [&](const Place &w) {
+        const uint8_t *at = p.vc + w.at + (2 * c * D + 16 * g);
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int key = 16 * k + (e & 1) + (e >> 1) * 8;
-                vw[k][e] = key + 2 * c < w.left ? ld_once(w.v + key * D) : zero;
+                vw[k][e] = key + 2 * c < w.left ? ld_once(at + key * D) : zero;
             }
     };
     int ch = c0 + warp;
@@ -451,15 +466,43 @@ __global__ void __launch_bounds__(NT, NR == 1 ? 3 : 2) cache_attn_rows_kernel(co
         const size_t at_row = ((size_t)b * p.N + node) * p.Hq + head;
         if (p.splits == 1) {
             store_row(p, at_row, lane, M, l, o);
+        } else if constexpr (CLUSTERED) {
+            __syncwarp();   // (this row's statistics have been read)
+            *reinterpret_cast<float4 *>(&so[0][row][4 * lane]) = o;
+            if (lane == 0) sm[0][row] = M, sl[0][row] = l;
         } else {
             const size_t part = (size_t)split * p.B * p.N * p.Hq + at_row;
             if (l != 0.0f) *reinterpret_cast<float4 *>(p.part_o + part * D + 4 * lane) = o;   // (NaN too)
             if (lane == 0) *reinterpret_cast<float2 *>(p.part_ml + 2 * part) = make_float2(M, l);
         }
     }
+    if constexpr (!CLUSTERED) return;
+    // ---- the splits' results in their order, rows by turns of the cluster's warps
+    tc::cluster_sync();
+    for (int row = split * NW + warp; row < nrows; row += p.splits * NW) {
+        float2 ml = make_float2(-INFINITY, 0.0f);
+        if (lane < p.splits)
+            ml = make_float2(tc::cluster_ld(tc::cluster_addr(smem_u32(&sm[0][row]), lane)),
+                             tc::cluster_ld(tc::cluster_addr(smem_u32(&sl[0][row]), lane)));
+        const float M = warp_max(ml.x), e = split_factor(ml, M), l = warp_sum(e * ml.y);
+        const uint32_t at = smem_u32(&so[0][row][4 * lane]);
+        float4 x[MAX_CLUSTER], o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int s = 0; s < MAX_CLUSTER; ++s)
+            if (s < p.splits) x[s] = tc::cluster_ld4(tc::cluster_addr(at, s));
+#pragma unroll
+        for (int s = 0; s < MAX_CLUSTER; ++s) {
+            const float es = __shfl_sync(0xffffffffu, e, s);
+            if (s < p.splits && es != 0.0f) o = make_float4(o.x + es * x[s].x, o.y + es * x[s].y, o.z + es * x[s].z, o.w + es * x[s].w);
+        }
+        const int node = (row0 + row) / p.rep, head = h * p.rep + (row0 + row) % p.rep;
+        store_row(p, ((size_t)b * p.N + node) * p.Hq + head, lane, M, l, o);
+    }
+    tc::cluster_sync();   // no CTA leaves while another reads its results
 }
 
-// The splits' results.  Few splits: a warp a row.  Many: a CTA a row, a quarter of the splits to each of its warps.
+// The splits' results where they are not a cluster.  Few splits: a warp a row.  Many: a CTA a row, a quarter of the splits to
+// each of its warps.
 constexpr int FEW_SPLITS = 16;   // 16384 rows of 2 splits and 128 threads a row took 14 us; 32 rows of 57 and a warp a row 9 us
 
 // splits [s0, s1) of a row by their factors, with eight loads in flight; factor(s): of split s, the same in all lanes
@@ -484,17 +527,6 @@ E3_DEV float4 weighted_sum(const CacheAttn &p, long long rows, long long row, in
 }
 E3_DEV float2 split_ml(const CacheAttn &p, long long rows, long long row, int s) {
     return s < p.splits ? *reinterpret_cast<const float2 *>(p.part_ml + 2 * (s * rows + row)) : make_float2(-INFINITY, 0.0f);
-}
-E3_DEV float split_factor(float2 ml, float M) { return ml.y == 0.0f ? 0.0f : ml.x == -INFINITY ? 1.0f : fast_exp2(ml.x - M); }
-E3_DEV float warp_max(float x) {
-#pragma unroll
-    for (int d = 16; d; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-    return x;
-}
-E3_DEV float warp_sum(float x) {
-#pragma unroll
-    for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-    return x;
 }
 
 __global__ void __launch_bounds__(NT) cache_attn_merge_few_kernel(const CacheAttn p) {
@@ -559,12 +591,18 @@ float plan_splits(CacheAttn &p, int requested) {
     const bool one = p.N * p.rep <= 8;
     const float units = (float)p.B * p.Hkv * p.row_groups, resident = (float)device_sm_count() * (one ? 3 : 2);
     const float besides = one ? 3.0f : 8.0f;
+    // One launch, joined within a cluster, where all clusters fit at once: a CTA then keeps its SM until the slowest of its
+    // cluster is done, and clusters of many CTAs leave SMs out (64 sequences of up to 8192 positions, 4 parts: 154 us
+    // as clusters, 116 us with a second kernel; 8 sequences of 4096, 7 parts: 25 and 17 us; one of 4096: 11 and 15 us a call)
+    auto as_cluster = [&](int s) {
+        return s > 1 && s <= MAX_CLUSTER && units * s <= (s <= 4 && !one ? resident : (float)device_sm_count());
+    };
     int best = 1;
     float least = 0.0f;
     for (int s = 1; s <= MAX_SPLITS && (s == 1 || s * NW <= chunks); ++s) {
         const float waves = units * s / resident;
         const float cost = (waves <= 1.0f ? 1.0f : waves + 0.5f) * ((chunks + s * NW - 1) / (s * NW) + besides) +
-                           (s > 1 ? 2.0f + s / 16 : 0.0f);   // the join
+                           (s == 1 ? 0.0f : as_cluster(s) ? 0.5f : 4.0f + s / 24.0f);   // the join
         if (s == 1 || cost < least) least = cost, best = s;
         if (waves > 8.0f) break;
     }
@@ -573,6 +611,7 @@ float plan_splits(CacheAttn &p, int requested) {
     if (best < 1) best = 1;
     p.split_chunks = (chunks + best - 1) / best;
     p.splits = chunks == 0 ? 1 : (chunks + p.split_chunks - 1) / p.split_chunks;
+    p.clustered = as_cluster(p.splits);
     return least;
 }
 
@@ -637,17 +676,35 @@ CacheAttn plan(const eagle3_verify_attn_fp8_args_t *a, bool &wide) {
     p.dev_status = a->dev_status;
     p.row_groups = (p.N * p.rep + MAX_ROWS - 1) / MAX_ROWS;
     // 16 rows at a time by warps, or 128 by tensor memory: the latter reads a prefix once for up to 128 rows, but takes
-    // 30 us to get going and to join.  Both fits in us, over measurements of 1 to 64 sequences: 8 nodes of 4 heads over
-    // 2048 positions 31 to 47 us (16 rows at a time first) of 8 sequences and 99 to 144 us of 64; 60 nodes 24 to 33 us
-    // of one sequence, 157 to 98 us of 16.
+    // 30 us to get going and to join.  Both are fits in us; measured, 4 heads a KV head over up to 2048 positions, 16 rows
+    // at a time against 128: 16 nodes of 8 sequences 31 and 47 us, 8 nodes of 64 sequences 99 and 144, 60 nodes of one
+    // sequence 22 and 33, of 16 sequences 157 and 74.
     const float tiles = (p.max_prefix + 127) / 128 + (p.tree_k ? 8.0f : 2.0f);
     const float wide_us = 30.0f + (float)p.B * p.Hkv * ((p.N * p.rep + 127) / 128) * tiles / 138.0f;
     wide = plan_splits(p, a->num_splits) + 6.0f > wide_us && p.N * p.rep > MAX_ROWS;
     return p;
 }
 
+// launch_pdl by clusters of `ranks` CTAs along x
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl_clusters(void (*kernel)(KArgs...), dim3 grid, dim3 block, int ranks, cudaStream_t stream, Args &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)ranks;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = ranks > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args &&>(args)...);
+}
+
 size_t workspace_of(const CacheAttn &p) {
-    return p.splits > 1 ? (size_t)p.splits * p.B * p.N * p.Hq * (D + 2) * sizeof(float) + 256 : 0;
+    return p.splits > 1 && !p.clustered ? (size_t)p.splits * p.B * p.N * p.Hq * (D + 2) * sizeof(float) + 256 : 0;
 }
 
 }  // namespace
@@ -682,15 +739,17 @@ eagle3_status_t verify_attn(const eagle3_verify_attn_fp8_args_t *a, int choice, 
     CacheAttn p = plan(a, wide);
     if (!choose(p, choice, wide)) return EAGLE3_ERR_INVALID_ARGUMENT;
     if (wide) return cache_attn_wide(p, a->num_splits, wait, workspace, workspace_bytes, st);
-    if (p.splits > 1) {
+    if (p.splits > 1 && !p.clustered) {
         if (!workspace || workspace_bytes < workspace_of(p)) return EAGLE3_ERR_WORKSPACE;
         p.part_o = (float *)(((uintptr_t)workspace + 255) & ~(uintptr_t)255);
         p.part_ml = p.part_o + (size_t)p.splits * p.B * p.N * p.Hq * D;
     }
     const dim3 grid((unsigned)p.splits, (unsigned)(p.Hkv * p.row_groups), (unsigned)p.B);
-    auto *kernel = p.N * p.rep <= 8 ? cache_attn_rows_kernel<1> : cache_attn_rows_kernel<2>;
-    if (launch_pdl(kernel, grid, dim3(NT), 0, st, p) != cudaSuccess) return EAGLE3_ERR_CUDA;
-    if (p.splits > 1) {
+    auto *kernel = p.N * p.rep <= 8 ? (p.clustered ? cache_attn_rows_kernel<1, true> : cache_attn_rows_kernel<1, false>)
+                                    : (p.clustered ? cache_attn_rows_kernel<2, true> : cache_attn_rows_kernel<2, false>);
+    if (launch_pdl_clusters(kernel, grid, dim3(NT), p.clustered ? p.splits : 1, st, p) != cudaSuccess)
+        return EAGLE3_ERR_CUDA;
+    if (p.splits > 1 && !p.clustered) {
         const long long rows = (long long)p.B * p.N * p.Hq;
         const cudaError_t e = p.splits <= FEW_SPLITS
                                   ? launch_pdl(cache_attn_merge_few_kernel, dim3((unsigned)((rows + NW - 1) / NW)), dim3(NT), 0, st, p)

@@ -9,7 +9,7 @@
 namespace e3 {
 
 struct CacheAttn {
-    int B, N, Hq, Hkv, rep, max_prefix, splits, split_chunks, row_groups;
+    int B, N, Hq, Hkv, rep, max_prefix, splits, split_chunks, row_groups, clustered;
     int max_blocks, block_size, n_pages;
     float scale_log2;               // sm_scale * log2(e)
     int64_t q_ns, kv_ns;
