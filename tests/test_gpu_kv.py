@@ -1,8 +1,9 @@
 """GPU numerics of the 8-bit paged cache's operators against the fp64 oracle.
 
 Tolerances, from the arithmetic (u = 2^-24, half an fp32 step relative to a value):
-Rotations.  The angle is exact to 2^-33 turns and rounded to fp32 as a fraction of half a turn: off by at most
-2^-25 pi + 2^-32 pi; sine and cosine are within 2 steps (2^-23 at most), times the amplitude one rounding: together
+Rotations.  The angle is exact to 2^-33 turns; from the nearest quarter turn (at most pi / 4) it is rounded twice in
+fp32, off by at most (1/2 + 1) pi / 4 u + 2^-32 pi; the series leave out less than 2^-25 and round once at the end, to half a
+step: sine and cosine within 1.2 + 0.1 + 0.5 + 0.5 u, times the amplitude one rounding: together
 below ANGLE = 7 u for each of the two terms, and 3 roundings of the products and the sum: an element is off by at most
 amplitude (|a| + |b|) 10 u, and half a step of the type it is stored in (2^-8 of a bf16 value, 2^-4 of an e4m3 one or 2^-10 of its
 scale's unit).  Positions beyond 2^20 add the table's own 2^-53 of a turn each.
@@ -518,6 +519,30 @@ def test_attn_trees(lens, N, Hq, Hkv, size):
 @pytest.mark.parametrize("N,Hq,tree", [(1, 8, False), (5, 8, True), (60, 8, True)])
 def test_attn_splits(N, Hq, tree, splits):
     _check_attn([500, 31, 0, 170], N, Hq, 2, 64, tree, num_splits=splits)
+
+
+@pytest.mark.parametrize("lens,N,Hq,splits", [([3000, 40], 1, 8, 47), ([3000, 0], 3, 16, 33), ([1500, 600], 5, 8, 12), ([20000], 1, 8, 2000),
+                                              ([2500] * 40, 1, 8, 3), ([2500, 9] * 20, 3, 16, 8), ([1000], 1, 8, 5)])
+def test_attn_many_parts(lens, N, Hq, splits):
+    """Parts of few steps, joined by a warp or a CTA a row or within a cluster; more parts asked for than there are."""
+    _check_attn(lens, N, Hq, 2, 64, N > 1, num_splits=splits)
+
+
+@pytest.mark.parametrize("B,splits", [(1, 3), (1, 8), (2, 20), (40, 4)])
+def test_attn_nan_in_one_part(B, splits):
+    """A NaN key or value in one of many parts reaches its sequence's rows of that KV head, and no others."""
+    dev = require_gpu()
+    lens = [1500] * B
+    pool, q, tk, tv, par = _attn_inputs(dev, lens, 1, 8, 2, 64, 13, False)
+    pool.codes[0].numpy()[pool.table[0, 11], 0, 9, 3] = 0x7F
+    pool.codes[1].numpy()[pool.table[B - 1, 20], 1, 9, 5] = 0xFF
+    out, _, st = _call(pool, lens, q, tk, tv, par, dev, num_splits=splits)
+    nan = torch.isnan(out).cpu().numpy()
+    want = np.zeros(nan.shape, bool)
+    want[0, :, :4] = True
+    want[B - 1, :, 4:, 5] = True
+    assert st == 0
+    np.testing.assert_array_equal(nan, want)
 
 
 @pytest.mark.parametrize("lens,N,Hq", [([12000, 3], 5, 8), ([9000], 33, 4), ([5000, 7000, 0, 130], 60, 4)])
