@@ -173,10 +173,19 @@ E3_DEV uint2 scaled_down(uint2 c, float factor) {
     return make_uint2(w[0], w[1]);
 }
 
+E3_DEV float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 E3_DEV uint2 codes8(const float *v, float inv) {
     uint32_t w[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) w[e] = to_e4m3x2(v[2 * e] * inv, v[2 * e + 1] * inv);
+    for (int e = 0; e < 4; ++e) {
+        const float2 x = __fmul2_rn(make_float2(v[2 * e], v[2 * e + 1]), make_float2(inv, inv));
+        w[e] = to_e4m3x2(x.x, x.y);
+    }
     return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
 }
 
@@ -301,7 +310,8 @@ __global__ void __launch_bounds__(NT, ITEMS == 2 && PAIRED ? 3 : 1) append_kerne
 #pragma unroll
                 for (int i = 0; i < ITEMS; ++i)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(val[i][e]));   // (passes over NaN)
+                    for (int e = 0; e < 16; e += 2)   // (passes over NaN)
+                        top = max3(top, fabsf(val[i][e]), fabsf(val[i][e + 1]));
                 if (top > FLT_MAX) {   // infinities become NaN, and no scale follows them
                     top = 0.0f;
 #pragma unroll
