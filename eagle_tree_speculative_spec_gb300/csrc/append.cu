@@ -10,9 +10,10 @@
 // once.  A thread's unit is 16 dims of a row, both ends of their pairs among them.  Prompts: a CTA of 256 threads takes a run
 // of jobs, one after the other, with their group's cosines and sines in shared memory, which the keys of all heads share.
 // Few tokens a sequence (at most 8): a warp takes a job.
-// Bound by issue slots: 16384 tokens of 8 heads of 128 (e4m3, 100.7 MB) take 26.1 us, 3.9 TB/s, of which some 15 us are
-// instructions (300 a unit, the angles a quarter of them) and the rest waits for the maximum that the CTA's warps share; by
-// memory alone they would take 14.9 us.  Four CTAs an SM of 64 registers a thread and no load ahead took 29.3 us.
+// Bound by issue slots and the meeting of a CTA's warps: 16384 tokens of 8 heads of 128 (e4m3, 100.7 MB) take 25.7 us,
+// 3.9 TB/s (14.9 us at the copy's rate); 17.7 million warp instructions are 14 us of every scheduler, and the warps wait for
+// the maximum that they share and for their own chains.  Four CTAs an SM of 64 registers a thread and no load ahead took
+// 29.3 us; addresses kept in registers, which spill, 27.0 us.
 #include "e4m3.cuh"
 #include "rope.cuh"
 
@@ -204,7 +205,7 @@ template <int ITEMS, bool E4M3, bool BY_WARP, bool PAIRED>
 __global__ void __launch_bounds__(NT, ITEMS == 2 && PAIRED ? 3 : 1) append_kernel(const Params p) {
     constexpr int THREADS = BY_WARP ? 32 : NT;
     extern __shared__ float4 cs4[];   // [new rows of the group][pair]
-    __shared__ float scratch[2][NT / 32];
+    __shared__ float4 scratch[2][NT / 128];
     float2 *const cs = reinterpret_cast<float2 *>(cs4);
     pdl_wait();
     pdl_trigger();
@@ -328,11 +329,16 @@ __global__ void __launch_bounds__(NT, ITEMS == 2 && PAIRED ? 3 : 1) append_kerne
                 // magnitudes are in the order of their bits
                 top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
                 if constexpr (!BY_WARP) {
-                    if ((t & 31) == 0) scratch[parity][warp] = top;
+                    if ((t & 31) == 0) reinterpret_cast<float *>(scratch[parity])[warp] = top;
                     __syncthreads();   // the scale has been read by everyone too
 #pragma unroll
-                    for (int w = 0; w < NT / 32; ++w) top = fmaxf(top, scratch[parity][w]);
+                    for (int w = 0; w < NT / 128; ++w) {
+                        const float4 m = scratch[parity][w];
+                        top = max3(max3(top, m.x, m.y), m.z, m.w);
+                    }
                     parity ^= 1;
+                } else {
+                    __syncwarp();   // the scale has been read by all lanes
                 }
                 const int byte = max(old, scale_byte(top));
                 if (t == 0) *scales = (uint8_t)byte;
