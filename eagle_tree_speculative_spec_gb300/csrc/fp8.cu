@@ -348,6 +348,17 @@ E3_DEV uint32_t split_offset(int ranks, int src, int part, int j, int row) {
     return (uint32_t)((((src * 2 + part) * each + j % each) * 2 * BM + row) * 16);
 }
 
+template <int N>
+E3_DEV void registers_give() {
+    __syncwarp();
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N>
+E3_DEV void registers_take() {
+    __syncwarp();
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+
 // SPLIT: a cluster of p.ranks CTAs works on one tile (of 256 columns or 128), each on a range of the k-blocks.
 // Pieces of 4 columns of both runs belong to the ranks in shares: each rank sends the others their pieces of its sums
 // by remote stores (reading them took three times as long), and adds up and finishes its own.  The stores are bound
@@ -403,7 +414,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
     const int kb1 = SPLIT ? (int)((long long)p.kb_total * (rank + 1) / ranks) : p.kb_total;
 
     if (warp < WIDE_EPI0) {
-        tc::registers_give<40>();
+        registers_give<40>();
         if (warp == 0) {
             // ------------------------------------------------------------------ TMA producer
             if (tc::elect_one()) {
@@ -480,7 +491,7 @@ __global__ void __launch_bounds__(WIDE_THREADS, 1)
             tc::cluster_sync();
         }
     } else {
-        tc::registers_take<232>();
+        registers_take<232>();
         // ------------------------------------------------------------------ epilogue (warps 4..11)
         const int quarter = warp & 3, part = (warp - WIDE_EPI0) >> 2;
         uint8_t *box = boxes + (warp - WIDE_EPI0) * WIDE_BOX, *res_box = box + WIDE_EPI_WARPS * WIDE_BOX;

@@ -266,18 +266,6 @@ E3_DEV uint32_t thread_index() {
     return t;
 }
 
-// A warp's share of the registers that its block was launched with (every warp of the warpgroup)
-template <int N>
-E3_DEV void registers_give() {
-    __syncwarp();
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
-}
-template <int N>
-E3_DEV void registers_take() {
-    __syncwarp();
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
-}
-
 // ---- tcgen05 ---------------------------------------------------------------------------------------
 // Shared-memory matrix descriptor for a K-major tile written by TMA with 128-byte swizzle: rows of
 // 64 bf16 (128 B), 8-row groups 1024 B apart (stride byte offset), version 1, layout SWIZZLE_128B.
