@@ -8,8 +8,8 @@
 // A row's angles are shared by its heads: a CTA takes a few rows and first fills their cosines and sines into shared
 // memory, one sincospif a thread, then walks the heads.  A thread's unit is the two runs of V elements that hold V
 // pairs, so that it reads and writes both ends of each pair itself and the call can run in place; it stays with one row,
-// whose cosines it holds in registers, and has four heads' loads in flight.
-// Bound by memory: 3840 rows of 40 bf16 heads of 128 (78.6 MB) take 16.4 us, 4.8 TB/s (11.6 us at the copy's rate); with the
+// whose cosines it holds in registers, and has four heads' loads in flight, the first four while the angles are made.
+// Bound by memory: 3840 rows of 40 bf16 heads of 128 (78.6 MB) take 15.9 us, 5.0 TB/s (11.6 us at the copy's rate); with the
 // cosines read from shared memory for every head (lanes 64 bytes apart: four-way conflicts) and one head at a time, 26.9 us.
 #include "rope.cuh"
 
@@ -89,35 +89,38 @@ __global__ void __launch_bounds__(NT, 3) rope_kernel(const Params p) {
     const int half = p.R / 2;
     const int r0 = blockIdx.x * p.rows_per_cta, rn = min(p.rows_per_cta, p.rows - r0);
     const int h0 = blockIdx.y * p.heads_per_cta, h1 = min(p.heads, h0 + p.heads_per_cta);
+    const int units = half / V + (p.D - p.R) / V;   // runs of pairs, then runs that are copied; at most NT
+    const int slots = NT / units, slot = threadIdx.x / units, unit = threadIdx.x % units;
+    const int at_once = min(p.rows_per_cta, slots), step = slots / at_once;   // rows at a time, heads of each
+    const bool copy = unit >= half / V;
+    const int first_r = slot < at_once * step && !(copy && p.x == p.out) ? slot / step : rn, first_h = h0 + slot % step;
+    const int j = unit * V;
+    const int da = copy ? p.R + (unit - half / V) * V : INTERLEAVED ? 2 * j : j;
+    const int db = INTERLEAVED ? 2 * j + V : half + j;
+    Run<T, V> ra[AHEAD], rb[AHEAD];
+    auto load = [&](int r, int h) {
+        const T *x = (const T *)p.x + (r0 + r) * p.x_rs;
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            if (h + k * step >= h1) break;
+            ra[k].load(x + (size_t)(h + k * step) * p.D + da);
+            if (!copy) rb[k].load(x + (size_t)(h + k * step) * p.D + db);
+        }
+    };
+    if (first_r < rn) load(first_r, first_h);   // (these arrive while the angles are made)
     for (int i = threadIdx.x; i < rn * half; i += NT) {
         float2 w = turned(p.positions[r0 + i / half], p.table[i % half], p.amplitude);
         if (p.inverse) w.y = -w.y;
         cs[i] = w;
     }
     __syncthreads();
-    const int units = half / V + (p.D - p.R) / V;   // runs of pairs, then runs that are copied; at most NT
-    const int slots = NT / units, slot = threadIdx.x / units, unit = threadIdx.x % units;
-    const int at_once = min(p.rows_per_cta, slots), step = slots / at_once;   // rows at a time, heads of each
-    if (slot >= at_once * step) return;
-    const bool copy = unit >= half / V;
-    if (copy && p.x == p.out) return;
-    const int j = unit * V;
-    const int da = copy ? p.R + (unit - half / V) * V : INTERLEAVED ? 2 * j : j;
-    const int db = INTERLEAVED ? 2 * j + V : half + j;
-    for (int r = slot / step; r < rn; r += at_once) {
-        const T *x = (const T *)p.x + (r0 + r) * p.x_rs;
+    for (int r = first_r; r < rn; r += at_once) {
         T *out = (T *)p.out + (r0 + r) * p.o_rs;
         float2 w[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) w[i] = copy ? make_float2(1.0f, 0.0f) : cs[r * half + j + i];
-        for (int h = h0 + slot % step; h < h1; h += AHEAD * step) {
-            Run<T, V> ra[AHEAD], rb[AHEAD];
-#pragma unroll
-            for (int k = 0; k < AHEAD; ++k) {
-                if (h + k * step >= h1) break;
-                ra[k].load(x + (size_t)(h + k * step) * p.D + da);
-                if (!copy) rb[k].load(x + (size_t)(h + k * step) * p.D + db);
-            }
+        for (int h = first_h; h < h1; h += AHEAD * step) {
+            if (r != first_r || h != first_h) load(r, h);
 #pragma unroll
             for (int k = 0; k < AHEAD; ++k) {
                 if (h + k * step >= h1) break;
