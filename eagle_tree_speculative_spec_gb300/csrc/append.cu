@@ -17,6 +17,7 @@
 #include "e4m3.cuh"
 #include "rope.cuh"
 
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
 
@@ -459,7 +460,7 @@ extern "C" eagle3_status_t eagle3_append_kv(const eagle3_append_kv_args_t *a, ea
     // the table's angles: more CTAs, of fewer (7 x 999 tokens of 5 heads 7.4 us by two, 10.3 us by three jobs a CTA)
     const int64_t all = (int64_t)p.groups_per_seq * p.B * jobs;
     if (all > MAX_DIM) return EAGLE3_ERR_UNSUPPORTED;
-    const int64_t most = (e4m3 ? 3 : 4) * (int64_t)device_sm_count();
+    const int64_t most = (e4m3 ? 3 : 4) * (int64_t)std::max(1, device_sm_count());   // (0: no device, which the launch will say)
     // (of the groups that a sequence touches at most, one is there because tokens may begin inside a group: shares are of the others)
     const int64_t sure = (int64_t)((reach + GROUP - 1) / GROUP) * p.B * jobs;
     p.jobs = (int)all;

@@ -13,6 +13,7 @@
 // cosines read from shared memory for every head (lanes 64 bytes apart: four-way conflicts) and one head at a time, 26.9 us.
 #include "rope.cuh"
 
+#include <algorithm>
 #include <cmath>
 #include <type_traits>
 
@@ -233,7 +234,8 @@ extern "C" eagle3_status_t eagle3_rope(const eagle3_rope_args_t *a, eagle3_strea
     // rows a CTA, as many at most as there are threads for angles: those with which the waves of CTAs, each of a thread's
     // heads and what a CTA costs besides, take the least time (3840 rows of 40 heads: 3 rows, 2.8 waves; 4 rows are 2.1,
     // and took 17.6 us).  Few rows: the heads are cut over CTAs too, so that every SM gets four
-    const int want = 4 * device_sm_count(), resident = 3 * device_sm_count();
+    const int sms = std::max(1, device_sm_count());   // (0: no device, which the launch will say)
+    const int want = 4 * sms, resident = 3 * sms;
     int64_t least = 0;
     for (int n = 1; n <= NT / (p.R / 2) && (n == 1 || n <= pass); ++n) {
         const int64_t waves = ((p.rows + n - 1) / n + resident - 1) / resident, step = pass / n;
