@@ -412,9 +412,11 @@ extern "C" eagle3_status_t eagle3_append_kv(const eagle3_append_kv_args_t *a, ea
     const int64_t rs = a->row_stride ? a->row_stride : dense;
     if (rs < dense || rs % 8) return EAGLE3_ERR_INVALID_ARGUMENT;
     if (a->batch == 0 || a->max_new == 0) return EAGLE3_OK;
+    if (a->n_rows > 0 && (!a->k_new || !a->v_new)) return EAGLE3_ERR_INVALID_ARGUMENT;   // (no rows: nothing reads there)
+    if (!a->k_cache || !a->v_cache) return EAGLE3_ERR_INVALID_ARGUMENT;
     const void *wide[] = {a->k_new, a->v_new, a->k_cache, a->v_cache};
     for (const void *ptr : wide)
-        if (!ptr || ((uintptr_t)ptr & 15)) return EAGLE3_ERR_INVALID_ARGUMENT;
+        if ((uintptr_t)ptr & 15) return EAGLE3_ERR_INVALID_ARGUMENT;
     const void *words[] = {a->cache_len, a->block_table};
     for (const void *ptr : words)
         if (!ptr || ((uintptr_t)ptr & 3)) return EAGLE3_ERR_INVALID_ARGUMENT;

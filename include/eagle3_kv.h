@@ -140,7 +140,7 @@ typedef struct {
     int32_t n_kv_heads;          /* Hkv >= 1                                                          */
     int32_t head_dim;            /* D: a multiple of 8, <= 256                                        */
     int32_t format;              /* eagle3_kv_format_t                                                */
-    int32_t n_rows;              /* rows of k_new / v_new                                             */
+    int32_t n_rows;              /* rows of k_new / v_new, >= 0 (0: they may be NULL)                 */
     int32_t max_new;             /* host bound on every sequence's new tokens, >= 0                   */
     int32_t rows_per_seq;        /* row_ids only: rows of a sequence                                  */
     int32_t max_blocks;          /* columns of block_table                                            */

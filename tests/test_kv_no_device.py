@@ -39,3 +39,16 @@ def _status(call):
     "L.eagle3_verify_attn_fp8(ctypes.byref(abi._attn(num_splits=1)), None, 0, None)"])
 def test_no_device_is_an_error(call):
     assert _status(call) == ERR_CUDA
+
+
+@pytest.mark.parametrize("kw", [
+    "dict(n_rows=0, k_new=None, v_new=None)", "dict(n_rows=0, k_new=None, v_new=None, row_start=16)",
+    "dict(n_rows=0, k_new=None, v_new=None, row_ids=16, rows_per_seq=5, n_new=None)", "dict(n_rows=0)"])
+def test_an_append_of_no_rows_is_taken(kw):
+    """An empty tensor has no address; whether a sequence has new tokens is known on the device only."""
+    assert _status(f"L.eagle3_append_kv(ctypes.byref(abi._append(**{kw})), None)") == ERR_CUDA
+
+
+@pytest.mark.parametrize("kw", ["dict(k_new=None)", "dict(n_rows=0, k_new=24)", "dict(n_rows=0, k_new=None, v_cache=None)"])
+def test_an_append_without_its_tensors_is_refused(kw):
+    assert _status(f"L.eagle3_append_kv(ctypes.byref(abi._append(**{kw})), None)") == 1
