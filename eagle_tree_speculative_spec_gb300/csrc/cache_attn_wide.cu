@@ -810,9 +810,8 @@ __global__ void __launch_bounds__(NT, 1)
                     }
                 }
                 // the weights by V's scale: 2^down of them; their sum without it
-                const int vb = half ? sb.w : sb.z, down = max(LEAST_SHIFT, vb - evref);
-                const float nm = vb == 255 ? __int_as_float(0x7fc00000)
-                                           : (m_run == -INFINITY ? 0.0f : WEIGHT_LOG2 - m_run) + (float)down;
+                const int vb = half ? sb.w : sb.z, down = vb == 255 ? 0 : max(LEAST_SHIFT, vb - evref);
+                const float nm = (m_run == -INFINITY ? 0.0f : WEIGHT_LOG2 - m_run) + (float)down;
                 const float2 f2 = make_float2(f, f), nm2 = make_float2(nm, nm);
                 float2 sum[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
                 uint32_t pk[32];
@@ -823,6 +822,9 @@ __global__ void __launch_bounds__(NT, 1)
                     sum[e & 1] = __fadd2_rn(sum[e & 1], y);
                     pk[e] = pack_f16(y.x, y.y);
                 }
+                // (a NaN scale: the weight of the group's first key, which every query sees, so that all dims are NaN; the
+                // sum of the weights has no values in it)
+                if (RARELY(vb == 255)) pk[0] |= 0x7fffu;
                 const float2 s2 = __fadd2_rn(sum[0], sum[1]);
                 l_run += (s2.x + s2.y) * exp2_int(-down);
                 // P, and O: once the tile before has been multiplied

@@ -177,8 +177,9 @@ eagle3_status_t eagle3_append_kv(const eagle3_append_kv_args_t *args, eagle3_str
  * cache alone, all of it: a single token whose own key has been appended, or n_nodes queries over a shared
  * prefix.  A query that sees no key gets zeros and lse = -inf.  lse (optional) is the natural logarithm of
  * the sum of exp of the scaled scores.
- * Codes and scales of positions >= L are not looked at and may be anything; NaN codes or scales
- * before L make the queries that see them NaN.  A page id outside the pool reads as keys and values of
+ * Codes and scales of positions >= L are not looked at and may be anything.  Before L a NaN code or scale of K
+ * makes out and lse of the queries that see it NaN; one of V makes out NaN (a code: its dim), and lse, which has no
+ * values in it, stays what the keys make it.  A page id outside the pool reads as keys and values of
  * zero.  prefix_len[b] outside [0, max_prefix_len] is cut and raises EAGLE3_DEV_CAPACITY; a tree that is
  * not one raises EAGLE3_DEV_BAD_TREE and its nodes end at the bad one.
  * Scores, softmax statistics and sums are fp32.  q and tree_k enter the tensor cores as fp16, scaled by a power
