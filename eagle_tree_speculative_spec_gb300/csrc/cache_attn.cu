@@ -140,7 +140,6 @@ struct Place {
     int left, ek, ev;   // left: its keys that are there, 0 or less: none
 };
 
-E3_DEV float split_factor(float2 ml, float M) { return ml.y == 0.0f ? 0.0f : ml.x == -INFINITY ? 1.0f : fast_exp2(ml.x - M); }
 E3_DEV float warp_max(float x) {
 #pragma unroll
     for (int d = 16; d; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
@@ -454,13 +453,10 @@ __global__ void __launch_bounds__(NT, NR == 1 ? 3 : 2) cache_attn_rows_kernel(co
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
-            const float m = sm[w][row];
             // (a warp whose scores are all NaN has no maximum but a sum)
-            const float e = m == -INFINITY ? (sl[w][row] == 0.0f ? 0.0f : 1.0f) : fast_exp2(m - M);
+            const float e = part_factor(sm[w][row], sl[w][row], M);
             l += e * sl[w][row];
-            const float vs = e * scale_of(sev[w]);
-            const float4 x = *reinterpret_cast<const float4 *>(&so[w][row][4 * lane]);
-            if (e != 0.0f) o = make_float4(o.x + vs * x.x, o.y + vs * x.y, o.z + vs * x.z, o.w + vs * x.w);
+            if (counts(e)) add_part(o, e * scale_of(sev[w]), *reinterpret_cast<const float4 *>(&so[w][row][4 * lane]));
         }
         const int node = (row0 + row) / p.rep, head = h * p.rep + (row0 + row) % p.rep;
         const size_t at_row = ((size_t)b * p.N + node) * p.Hq + head;
@@ -484,7 +480,7 @@ __global__ void __launch_bounds__(NT, NR == 1 ? 3 : 2) cache_attn_rows_kernel(co
         if (lane < p.splits)
             ml = make_float2(tc::cluster_ld(tc::cluster_addr(smem_u32(&sm[0][row]), lane)),
                              tc::cluster_ld(tc::cluster_addr(smem_u32(&sl[0][row]), lane)));
-        const float M = warp_max(ml.x), e = split_factor(ml, M), l = warp_sum(e * ml.y);
+        const float M = warp_max(ml.x), e = part_factor(ml.x, ml.y, M), l = warp_sum(e * ml.y);
         const uint32_t at = smem_u32(&so[0][row][4 * lane]);
         float4 x[MAX_CLUSTER], o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
@@ -493,7 +489,7 @@ __global__ void __launch_bounds__(NT, NR == 1 ? 3 : 2) cache_attn_rows_kernel(co
 #pragma unroll
         for (int s = 0; s < MAX_CLUSTER; ++s) {
             const float es = __shfl_sync(0xffffffffu, e, s);
-            if (s < p.splits && es != 0.0f) o = make_float4(o.x + es * x[s].x, o.y + es * x[s].y, o.z + es * x[s].z, o.w + es * x[s].w);
+            if (s < p.splits && counts(es)) add_part(o, es, x[s]);
         }
         const int node = (row0 + row) / p.rep, head = h * p.rep + (row0 + row) % p.rep;
         store_row(p, ((size_t)b * p.N + node) * p.Hq + head, lane, M, l, o);
@@ -516,12 +512,12 @@ E3_DEV float4 weighted_sum(const CacheAttn &p, long long rows, long long row, in
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             e[k] = factor(min(s + k, s1 - 1));   // (a split with nothing to see has left nothing there)
-            if (s + k >= s1) e[k] = 0.0f;
-            if (e[k] != 0.0f) x[k] = *reinterpret_cast<const float4 *>(p.part_o + ((s + k) * rows + row) * D + 4 * lane);
+            if (s + k >= s1) e[k] = NOTHING;
+            if (counts(e[k])) x[k] = *reinterpret_cast<const float4 *>(p.part_o + ((s + k) * rows + row) * D + 4 * lane);
         }
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            if (e[k] != 0.0f) o = make_float4(o.x + e[k] * x[k].x, o.y + e[k] * x[k].y, o.z + e[k] * x[k].z, o.w + e[k] * x[k].w);
+            if (counts(e[k])) add_part(o, e[k], x[k]);
     }
     return o;
 }
@@ -536,7 +532,7 @@ __global__ void __launch_bounds__(NT) cache_attn_merge_few_kernel(const CacheAtt
     const int lane = threadIdx.x & 31;
     if (row >= rows) return;
     const float2 ml = split_ml(p, rows, row, lane);
-    const float M = warp_max(ml.x), e = split_factor(ml, M), l = warp_sum(e * ml.y);
+    const float M = warp_max(ml.x), e = part_factor(ml.x, ml.y, M), l = warp_sum(e * ml.y);
     store_row(p, (size_t)row, lane, M, l, weighted_sum(p, rows, row, 0, p.splits, lane, [&](int s) { return __shfl_sync(0xffffffffu, e, s); }));
 }
 
@@ -562,7 +558,7 @@ __global__ void __launch_bounds__(NT) cache_attn_merge_kernel(const CacheAttn p)
     for (int w = 0; w < NW; ++w) M = fmaxf(M, sm[w]);
 #pragma unroll
     for (int i = 0; i < MAX_SPLITS / NT; ++i) {
-        const float e = split_factor(ml[i], M);
+        const float e = part_factor(ml[i].x, ml[i].y, M);
         sw[threadIdx.x + i * NT] = e;
         l += e * ml[i].y;
     }

@@ -197,10 +197,6 @@ E3_DEV float max3(float a, float b, float c) {
     return r;
 }
 
-E3_DEV float weight_of(float m, float l, float M) {
-    return l == 0.0f ? 0.0f : m == -INFINITY ? 1.0f : fast_exp2(m - M);
-}
-
 // Rare paths are marked as such, so that the code of the loops is short: all roles' loops together have to stay in the
 // SM's instruction cache.
 #define RARELY(x) __builtin_expect(!!(x), 0)
@@ -972,11 +968,13 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) cache_attn_join_kernel(const 
             float top = ml.x;
 #pragma unroll
             for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            const float Mn = fmaxf(M, top), down = weight_of(M, l, Mn);
-            l *= down;
-            o = make_float4(o.x * down, o.y * down, o.z * down, o.w * down);
+            const float Mn = fmaxf(M, top), down = part_factor(M, l, Mn);
+            l *= down;   // (0 where that is NOTHING)
+            const float4 before = o;
+            o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (counts(down)) add_part(o, down, before);
             M = Mn;
-            const float e = weight_of(ml.x, ml.y, M);
+            const float e = part_factor(ml.x, ml.y, M);
             float sum = e * ml.y;
 #pragma unroll
             for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
@@ -985,7 +983,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) cache_attn_join_kernel(const 
             for (int q = 0; q < n; ++q) {
                 const float eq = __shfl_sync(0xffffffffu, e, q);
                 const float4 x = *reinterpret_cast<const float4 *>(p.part_o + slot(q0 + q) * D + 4 * lane);
-                if (eq != 0.0f) o = make_float4(o.x + eq * x.x, o.y + eq * x.y, o.z + eq * x.z, o.w + eq * x.w);
+                if (counts(eq)) add_part(o, eq, x);
             }
         }
         const int node = (row0 + row) / a.rep, head = g * a.rep + (row0 + row) % a.rep;

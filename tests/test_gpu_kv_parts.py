@@ -1,14 +1,17 @@
 """The parts that eagle3_verify_attn_fp8 cuts a prefix into, and their joins, on the GPU, each kernel by its name.
 
-The tolerances are those of tests/test_gpu_kv.py.
+Where a single key has all the weight, the other keys' scores lie some 181 below its own (e^-181 is 0 in fp32), so the output
+is that key's value, which bf16 holds: exact but for the 2^x unit and the roundings of a score, below bf16's half step of 2^-8.
+Elsewhere the tolerances are those of tests/test_gpu_kv.py.
 """
 import numpy as np
 import pytest
 import torch
 
 from eagle_tree_speculative_spec_gb300 import _lib
+from oracle import fp8, kv
 from tests._util import require_gpu
-from tests.test_gpu_kv import _attn_inputs, _expected, _ints, _np
+from tests.test_gpu_kv import BF16, U, _attn_inputs, _expected, _ints, _np
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +50,54 @@ def test_a_nan_scale_of_values_leaves_the_logarithms(kernel, N, splits, tree):
     nan[0, :, 4:] = nan[1, :, :4] = True
     np.testing.assert_array_equal(np.isnan(_np(out)), nan)
     assert (np.abs(_np(lse) - want) <= tol).all()
+
+
+# (kernel, sequences, nodes, parts): joins of a CTA's warps, within clusters, by a warp or a CTA a row; of ranges of CTAs
+JOINS = [(ROWS, 1, 1, 1), (ROWS, 1, 5, 1), (ROWS, 1, 1, 3), (ROWS, 1, 1, 8), (ROWS, 1, 5, 4), (ROWS, 40, 1, 4), (ROWS, 12, 40, 4),
+         (ROWS, 2, 1, 20), (ROWS, 2, 5, 20), (WIDE, 1, 60, 1), (WIDE, 1, 60, 3), (WIDE, 2, 60, 20), (WIDE, 1, 20, 5), (WIDE, 3, 60, 0)]
+JOIN_IDS = [f"{NAME[k]}, {b} x {n} nodes, {s} parts" for k, b, n, s in JOINS]
+
+
+@pytest.mark.parametrize("what", ["nothing", "code", "scale", "tree nan", "tree inf"])
+@pytest.mark.parametrize("kernel,B,N,splits", JOINS, ids=JOIN_IDS)
+def test_values_that_are_not_finite_far_below_the_maximum(kernel, B, N, splits, what):
+    """A NaN code, a NaN scale or a tree's value that is not finite makes the queries that see it so, in whatever part of
+    the prefix it lies and however little weight it has; no other query, and not the logarithm of the sum."""
+    dev = require_gpu()
+    Hq, Hkv, size, L, at = 8, 2, 64, 1500, 1400
+    lens = [L] * B
+    pool, q, tk, tv, par = _attn_inputs(dev, lens, N, Hq, Hkv, size, 31, True)
+    q.zero_()
+    q[..., 0] = 64
+    tk.zero_()
+    tk[..., 0] = -16
+    k = pool.codes[0].numpy()
+    k[:] = 0
+    k[..., 0] = fp8.encode(np.array(-16.0))
+    pool.scale[0].numpy()[:] = 127
+    for b in range(B):
+        k[pool.table[b, 0], :, 0, 0] = fp8.encode(np.array(16.0))
+    first = np.stack([kv.read(pool.codes[1].numpy(), pool.scale[1].numpy(), pool.table[b].tolist(), 1, pool.pages)[:, 0]
+                      for b in range(B)])                    # [B, Hkv, D]: the value of the key that has the weight
+    want = np.repeat(first, Hq // Hkv, 1)[:, None].repeat(N, 1)
+    node = N - 1 if N > 32 else N // 2
+    sees = np.array([node in kv.path(par[0], i) for i in range(N)])
+    if what == "code":
+        pool.codes[1].numpy()[pool.table[0, at // size], 1, at % size, 5] = 0xFF
+        want[0, :, 4:, 5] = np.nan
+    elif what == "scale":
+        pool.scale[1].numpy()[pool.table[0, at // size], 0, 0] = 255
+        want[0, :, :4] = np.nan
+    elif what != "nothing":
+        tv[0, node, 1, 7] = float(what.split()[1])
+        want[0, sees, 4:, 7] = float(what.split()[1])
+    out, lse = _run(kernel, pool, lens, q, tk, tv, par, dev, num_splits=splits)
+    got = _np(out)
+    np.testing.assert_array_equal(np.isnan(got), np.isnan(want))
+    inf = np.isinf(want)
+    np.testing.assert_array_equal(got[inf], want[inf])
+    ok = np.isfinite(want)
+    assert (np.abs(got[ok] - want[ok]) <= BF16 * np.abs(want[ok])).all()
+    score = 64 * 16 / 128 ** 0.5
+    # the sum of exp is 1; the score: 6 roundings and 2^x's unit, 128 products of which all but one are zeros
+    assert (np.abs(_np(lse) - score) <= (6 + 8) * U * score + 2.0 ** -21).all()
