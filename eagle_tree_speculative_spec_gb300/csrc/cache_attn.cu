@@ -40,7 +40,6 @@ constexpr int NW = 4;               // warps
 constexpr int NT = NW * 32;
 constexpr int MAX_ROWS = 16;
 constexpr int O_PITCH = D + 4;
-constexpr int MAX_SPLITS = 512;
 
 E3_DEV void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -582,7 +581,7 @@ __global__ void __launch_bounds__(NT) cache_attn_merge_kernel(const CacheAttn p)
 // Parts of the prefix, of as many steps for a short sequence as for a long one, so that all CTAs take about the same
 // time: the number that gives the least waves * (steps of a warp + what a CTA costs besides, in steps), about in us.
 // Lengths are unknown here, so half a wave more stands for the uneven end of all but a single wave.
-float plan_splits(CacheAttn &p, int requested) {
+float plan_splits(CacheAttn &p) {
     const int chunks = (p.max_prefix + CHUNK - 1) / CHUNK;
     const bool one = p.N * p.rep <= 8;
     const float units = (float)p.B * p.Hkv * p.row_groups, resident = (float)device_sm_count() * (one ? 3 : 2);
@@ -602,8 +601,7 @@ float plan_splits(CacheAttn &p, int requested) {
         if (s == 1 || cost < least) least = cost, best = s;
         if (waves > 8.0f) break;
     }
-    if (requested > 0) best = requested < chunks ? requested : chunks;
-    if (best > MAX_SPLITS) best = MAX_SPLITS;
+    if (p.requested > 0) best = p.requested < chunks ? p.requested : chunks;
     if (best < 1) best = 1;
     p.split_chunks = (chunks + best - 1) / best;
     p.splits = chunks == 0 ? 1 : (chunks + p.split_chunks - 1) / p.split_chunks;
@@ -671,13 +669,14 @@ CacheAttn plan(const eagle3_verify_attn_fp8_args_t *a, bool &wide) {
     p.lse = a->lse;
     p.dev_status = a->dev_status;
     p.row_groups = (p.N * p.rep + MAX_ROWS - 1) / MAX_ROWS;
+    p.requested = a->num_splits < MAX_SPLITS ? a->num_splits : MAX_SPLITS;
     // 16 rows at a time by warps, or 128 by tensor memory: the latter reads a prefix once for up to 128 rows, but takes
     // 30 us to get going and to join.  Both are fits in us; measured, 4 heads a KV head over up to 2048 positions, 16 rows
     // at a time against 128: 16 nodes of 8 sequences 31 and 47 us, 8 nodes of 64 sequences 99 and 144, 60 nodes of one
     // sequence 22 and 33, of 16 sequences 157 and 74.
     const float tiles = (p.max_prefix + 127) / 128 + (p.tree_k ? 8.0f : 2.0f);
     const float wide_us = 30.0f + (float)p.B * p.Hkv * ((p.N * p.rep + 127) / 128) * tiles / 138.0f;
-    wide = plan_splits(p, a->num_splits) + 6.0f > wide_us && p.N * p.rep > MAX_ROWS;
+    wide = plan_splits(p) + 6.0f > wide_us && p.N * p.rep > MAX_ROWS;
     return p;
 }
 
@@ -724,7 +723,7 @@ size_t workspace_size(const eagle3_verify_attn_fp8_args_t *a, int choice) {
     bool wide;
     const CacheAttn p = plan(a, wide);
     if (!choose(p, choice, wide)) return 0;
-    return wide ? cache_attn_wide_workspace(p, a->num_splits) : workspace_of(p);
+    return wide ? cache_attn_wide_workspace(p) : workspace_of(p);
 }
 
 eagle3_status_t verify_attn(const eagle3_verify_attn_fp8_args_t *a, int choice, const WaitRule &wait, void *workspace,
@@ -734,7 +733,7 @@ eagle3_status_t verify_attn(const eagle3_verify_attn_fp8_args_t *a, int choice, 
     bool wide;
     CacheAttn p = plan(a, wide);
     if (!choose(p, choice, wide)) return EAGLE3_ERR_INVALID_ARGUMENT;
-    if (wide) return cache_attn_wide(p, a->num_splits, wait, workspace, workspace_bytes, st);
+    if (wide) return cache_attn_wide(p, wait, workspace, workspace_bytes, st);
     if (p.splits > 1 && !p.clustered) {
         if (!workspace || workspace_bytes < workspace_of(p)) return EAGLE3_ERR_WORKSPACE;
         p.part_o = (float *)(((uintptr_t)workspace + 255) & ~(uintptr_t)255);

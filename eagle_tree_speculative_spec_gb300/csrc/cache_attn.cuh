@@ -10,6 +10,7 @@ namespace e3 {
 
 struct CacheAttn {
     int B, N, Hq, Hkv, rep, max_prefix, splits, split_chunks, row_groups, clustered;
+    int requested;                  // parts of the prefix that the caller asks for, at most MAX_SPLITS; 0: the kernels' choice
     int max_blocks, block_size, n_pages;
     float scale_log2;               // sm_scale * log2(e)
     int64_t q_ns, kv_ns;
@@ -24,6 +25,7 @@ struct CacheAttn {
     float *part_o, *part_ml;
 };
 
+constexpr int MAX_SPLITS = 512;
 constexpr float RESCALE_LOG2 = 8.0f;   // the running maximum moves once a score is this far above it
 constexpr float WEIGHT_LOG2 = 7.0f;    // weights are held times 2^7: at most 2^15 in fp16
 
@@ -123,9 +125,8 @@ E3_DEV void store_row(const CacheAttn &p, size_t row, int lane, float m, float l
     if (p.lse && lane == 0) p.lse[row] = lse_of(m, l);
 }
 
-// many rows (cache_attn_wide.cu); requested: parts of the prefix, 0 = its own choice
-size_t cache_attn_wide_workspace(const CacheAttn &a, int requested);
-eagle3_status_t cache_attn_wide(const CacheAttn &a, int requested, const WaitRule &wait, void *workspace, size_t bytes,
-                                cudaStream_t stream);
+// many rows (cache_attn_wide.cu)
+size_t cache_attn_wide_workspace(const CacheAttn &a);
+eagle3_status_t cache_attn_wide(const CacheAttn &a, const WaitRule &wait, void *workspace, size_t bytes, cudaStream_t stream);
 
 }  // namespace e3

@@ -33,6 +33,8 @@
 #include "tc.cuh"
 #include "tmap.cuh"
 
+#include <algorithm>
+
 namespace e3 {
 namespace {
 
@@ -56,6 +58,7 @@ constexpr uint32_t SMEM_DYN = OFF_IN + 4 * IN_WARP + 1024;   // + alignment slac
 // tensor memory, columns: O; S of two tiles; P; Q's parts, 32 columns each
 constexpr uint32_t TM_O = 0, TM_S = 128, TM_P = 384, TM_Q = 448;
 constexpr int JOIN_WARPS = 8;
+constexpr int MOST_WAVES = 8;            // of CTAs: each has partial results of 131 KB in the workspace and an SM to itself
 
 struct Smem {
     uint64_t k_full[KS], k_empty[KS], vr_full[VS], vr_empty[VS], v_full[VB], v_empty[VB];
@@ -997,7 +1000,7 @@ struct Plan {
     size_t o_start, o_part, o_ml, bytes;
 };
 
-Plan plan(const CacheAttn &a, int requested) {
+Plan plan(const CacheAttn &a) {
     Plan pl;
     Wide &w = pl.w;
     w = Wide();
@@ -1005,11 +1008,11 @@ Plan plan(const CacheAttn &a, int requested) {
     w.row_groups = (a.N * a.rep + ROWS - 1) / ROWS;
     w.rep_magic = a.rep == 1 ? 0u : (uint32_t)(((1ull << 32) + a.rep - 1) / a.rep);
     const int64_t units = (int64_t)a.B * a.Hkv, most = units * ((a.max_prefix + BK - 1) / BK + 1);
-    int64_t ranges = requested > 0 ? units * requested : device_sm_count() / w.row_groups;
+    const int sms = std::max(1, device_sm_count());
+    int64_t ranges = a.requested > 0 ? std::min(units * a.requested, (int64_t)MOST_WAVES * sms / w.row_groups) : sms / w.row_groups;
     if (ranges > most) ranges = most;
-    if (ranges * w.row_groups > 4 * 65535) ranges = 4 * 65535 / w.row_groups;
     if (ranges < 1) ranges = 1;
-    w.least = requested > 0 ? 1 : 2;
+    w.least = a.requested > 0 ? 1 : 2;
     pl.ranges = (int)ranges;
     const size_t ctas = (size_t)ranges * w.row_groups;
     size_t at = 256;
@@ -1028,11 +1031,10 @@ Plan plan(const CacheAttn &a, int requested) {
 
 }  // namespace
 
-size_t cache_attn_wide_workspace(const CacheAttn &a, int requested) { return plan(a, requested).bytes; }
+size_t cache_attn_wide_workspace(const CacheAttn &a) { return plan(a).bytes; }
 
-eagle3_status_t cache_attn_wide(const CacheAttn &a, int requested, const WaitRule &wait, void *workspace, size_t bytes,
-                                cudaStream_t stream) {
-    Plan pl = plan(a, requested);
+eagle3_status_t cache_attn_wide(const CacheAttn &a, const WaitRule &wait, void *workspace, size_t bytes, cudaStream_t stream) {
+    Plan pl = plan(a);
     if (!workspace || bytes < pl.bytes) return EAGLE3_ERR_WORKSPACE;
     uint8_t *ws = (uint8_t *)(((uintptr_t)workspace + 255) & ~(uintptr_t)255);
     pl.w.wait = wait;

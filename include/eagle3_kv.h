@@ -196,7 +196,7 @@ typedef struct {
     int32_t n_kv_heads;          /* Hkv                                                               */
     int32_t head_dim;            /* D; 128 is supported                                               */
     int32_t max_prefix_len;      /* host bound on prefix_len[b], >= 0                                 */
-    int32_t num_splits;          /* parts of the prefix, at most 512; 0 = choose automatically        */
+    int32_t num_splits;          /* parts of the prefix (more than 512 are 512); 0 = choose automatically */
     int32_t max_blocks;          /* columns of block_table; max_blocks * block_size >= max_prefix_len */
     int32_t block_size;          /* places of a page, a multiple of 64                                */
     int32_t n_pages;             /* pages of the pool                                                 */

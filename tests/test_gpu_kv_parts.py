@@ -101,3 +101,15 @@ def test_values_that_are_not_finite_far_below_the_maximum(kernel, B, N, splits, 
     score = 64 * 16 / 128 ** 0.5
     # the sum of exp is 1; the score: 6 roundings and 2^x's unit, 128 products of which all but one are zeros
     assert (np.abs(_np(lse) - score) <= (6 + 8) * U * score + 2.0 ** -21).all()
+
+
+@pytest.mark.parametrize("kernel", [ROWS, WIDE], ids=NAME.get)
+def test_more_than_512_parts_give_the_same_bits(kernel):
+    dev = require_gpu()
+    lens = [20000, 300]
+    pool, q, tk, tv, par = _attn_inputs(dev, lens, 20, 8, 1, 64, 37, True)
+    outs = [_run(kernel, pool, lens, q, tk, tv, par, dev, num_splits=s) for s in (512, 513, 2 ** 31 - 1)]
+    for out, lse in outs[1:]:
+        assert torch.equal(out, outs[0][0]) and torch.equal(lse, outs[0][1])
+    want, _, tol, _ = _expected(pool, lens, q, tk, tv, par)
+    assert (np.abs(_np(outs[0][0]) - want) <= tol).all()
