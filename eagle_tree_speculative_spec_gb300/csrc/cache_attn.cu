@@ -698,8 +698,12 @@ cudaError_t launch_pdl_clusters(void (*kernel)(KArgs...), dim3 grid, dim3 block,
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args &&>(args)...);
 }
 
+// Whether a call wants its parts' workspace.  Parts that the caller asks for do, although a cluster, where the device's SMs
+// allow one, has no use for it: such a call is taken or refused alike on every device, and on a machine without one.
+bool wants_workspace(const CacheAttn &p) { return p.splits > 1 && (!p.clustered || p.requested > 0); }
+
 size_t workspace_of(const CacheAttn &p) {
-    return p.splits > 1 && !p.clustered ? (size_t)p.splits * p.B * p.N * p.Hq * (D + 2) * sizeof(float) + 256 : 0;
+    return wants_workspace(p) ? (size_t)p.splits * p.B * p.N * p.Hq * (D + 2) * sizeof(float) + 256 : 0;
 }
 
 }  // namespace
@@ -734,7 +738,7 @@ eagle3_status_t verify_attn(const eagle3_verify_attn_fp8_args_t *a, int choice, 
     CacheAttn p = plan(a, wide);
     if (!choose(p, choice, wide)) return EAGLE3_ERR_INVALID_ARGUMENT;
     if (wide) return cache_attn_wide(p, wait, workspace, workspace_bytes, st);
-    if (p.splits > 1 && !p.clustered) {
+    if (wants_workspace(p)) {
         if (!workspace || workspace_bytes < workspace_of(p)) return EAGLE3_ERR_WORKSPACE;
         p.part_o = (float *)(((uintptr_t)workspace + 255) & ~(uintptr_t)255);
         p.part_ml = p.part_o + (size_t)p.splits * p.B * p.N * p.Hq * D;

@@ -4,6 +4,8 @@ Where a single key has all the weight, the other keys' scores lie some 181 below
 is that key's value, which bf16 holds: exact but for the 2^x unit and the roundings of a score, below bf16's half step of 2^-8.
 Elsewhere the tolerances are those of tests/test_gpu_kv.py.
 """
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -113,3 +115,25 @@ def test_more_than_512_parts_give_the_same_bits(kernel):
         assert torch.equal(out, outs[0][0]) and torch.equal(lse, outs[0][1])
     want, _, tol, _ = _expected(pool, lens, q, tk, tv, par)
     assert (np.abs(_np(outs[0][0]) - want) <= tol).all()
+
+
+@pytest.mark.parametrize("B,N,splits", [(1, 1, 2), (1, 1, 8), (2, 3, 2), (1, 5, 4), (40, 1, 3)])
+def test_parts_asked_for_need_their_workspace(B, N, splits):
+    """However they are joined: a size that depends on the sizes alone, and a refusal without it."""
+    dev = require_gpu()
+    pool, q, *_ = _attn_inputs(dev, [500] * B, N, 8, 2, 64, 36, False)
+    (kc, vc), (ks, vs), table = pool.device()
+    out, q = torch.full(q.shape, 7.0, dtype=bf, device=dev), q.to(dev)
+    a = _lib.verify_attn_fp8_args(q, kc, vc, ks, vs, table, _ints([500] * B, dev), out, max_prefix_len=500, num_splits=splits)
+    L = _lib.lib()
+    need = L.eagle3_verify_attn_fp8_workspace_size(ctypes.byref(a))
+    assert need >= splits * B * N * 8 * 130 * 4
+    stream = torch.cuda.current_stream().cuda_stream
+    assert L.eagle3_verify_attn_fp8(ctypes.byref(a), None, 0, stream) == 6
+    ws = torch.empty(need, dtype=u8, device=dev)
+    assert L.eagle3_verify_attn_fp8(ctypes.byref(a), ws.data_ptr(), need - 1, stream) == 6
+    torch.cuda.synchronize()
+    assert (out == 7).all()
+    assert L.eagle3_verify_attn_fp8(ctypes.byref(a), ws.data_ptr(), need, stream) == 0
+    torch.cuda.synchronize()
+    assert not (out == 7).all()
