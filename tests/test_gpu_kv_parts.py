@@ -137,3 +137,32 @@ def test_parts_asked_for_need_their_workspace(B, N, splits):
     assert L.eagle3_verify_attn_fp8(ctypes.byref(a), ws.data_ptr(), need, stream) == 0
     torch.cuda.synchronize()
     assert not (out == 7).all()
+
+
+@pytest.mark.parametrize("lens,N,Hq,splits", [([3000, 40], 20, 8, 47), ([3000, 0], 17, 16, 33), ([1500, 600], 33, 4, 12),
+                                              ([9000], 20, 2, 2000), ([1500, 9] * 4, 30, 4, 8), ([1000], 64, 8, 5)])
+@pytest.mark.parametrize("tree", [False, True])
+def test_many_parts_of_128_rows(lens, N, Hq, splits, tree):
+    dev = require_gpu()
+    pool, q, tk, tv, par = _attn_inputs(dev, lens, N, Hq, 2 if Hq > 2 else 1, 64, 35, tree)
+    out, lse = _run(WIDE, pool, lens, q, tk, tv, par, dev, num_splits=splits)
+    want, want_lse, tol, lse_tol = _expected(pool, lens, q, tk, tv, par)
+    assert (np.abs(_np(out) - want) <= tol).all()
+    got, empty = _np(lse), np.isinf(want_lse)
+    assert (got[empty] == -np.inf).all()
+    assert (np.abs(got[~empty] - want_lse[~empty]) <= lse_tol[~empty]).all()
+
+
+@pytest.mark.parametrize("B,splits", [(1, 3), (1, 8), (2, 20), (20, 4)])
+def test_nan_in_one_part_of_128_rows(B, splits):
+    """A NaN key or value in one of many parts reaches its sequence's rows of that KV head, and no others."""
+    dev = require_gpu()
+    N, lens = 20, [1500] * B
+    pool, q, tk, tv, par = _attn_inputs(dev, lens, N, 8, 2, 64, 13, False)
+    pool.codes[0].numpy()[pool.table[0, 11], 0, 9, 3] = 0x7F
+    pool.codes[1].numpy()[pool.table[B - 1, 20], 1, 9, 5] = 0xFF
+    out, _ = _run(WIDE, pool, lens, q, tk, tv, par, dev, num_splits=splits)
+    want = np.zeros(out.shape, bool)
+    want[0, :, :4] = True
+    want[B - 1, :, 4:, 5] = True
+    np.testing.assert_array_equal(torch.isnan(out).cpu().numpy(), want)
