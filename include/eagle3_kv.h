@@ -124,8 +124,9 @@ eagle3_status_t eagle3_rope(const eagle3_rope_args_t *args, eagle3_stream_t stre
  * codes and take no part in m.  Places that no token goes to keep their codes.
  *
  * n_new[b] outside [0, max_new], cache_len[b] < 0 or a last position past max_blocks * block_size: the
- * sequence is left out and EAGLE3_DEV_CAPACITY raised.  A page id outside the pool: the group is left
- * out and EAGLE3_DEV_CAPACITY raised.  A row outside [0, n_rows) (with row_ids: outside
+ * sequence is left out and EAGLE3_DEV_CAPACITY raised.  A page id outside the pool: what would go there is left
+ * out (E4M3: the group; BF16, whose pages may end inside a group: the tokens of that page) and
+ * EAGLE3_DEV_CAPACITY raised.  A row outside [0, n_rows) (with row_ids: outside
  * [0, rows_per_seq) of its sequence): the token is left out and EAGLE3_DEV_BAD_TOKEN raised.
  * A page that is written must belong to one sequence.  batch * (groups of 64 that max_new tokens can touch) *
  * 2 * n_kv_heads must be below 2^31 - 2^16.
