@@ -452,10 +452,11 @@ __global__ void __launch_bounds__(NT, NR == 1 ? 3 : 2) cache_attn_rows_kernel(co
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
-            // (a warp whose scores are all NaN has no maximum but a sum)
             const float e = part_factor(sm[w][row], sl[w][row], M);
             l += e * sl[w][row];
-            if (counts(e)) add_part(o, e * scale_of(sev[w]), *reinterpret_cast<const float4 *>(&so[w][row][4 * lane]));
+            const float vs = e * scale_of(sev[w]);
+            const float4 x = *reinterpret_cast<const float4 *>(&so[w][row][4 * lane]);
+            if (e != 0.0f) o = make_float4(o.x + vs * x.x, o.y + vs * x.y, o.z + vs * x.z, o.w + vs * x.w);
         }
         const int node = (row0 + row) / p.rep, head = h * p.rep + (row0 + row) % p.rep;
         const size_t at_row = ((size_t)b * p.N + node) * p.Hq + head;
@@ -488,7 +489,7 @@ __global__ void __launch_bounds__(NT, NR == 1 ? 3 : 2) cache_attn_rows_kernel(co
 #pragma unroll
         for (int s = 0; s < MAX_CLUSTER; ++s) {
             const float es = __shfl_sync(0xffffffffu, e, s);
-            if (s < p.splits && counts(es)) add_part(o, es, x[s]);
+            if (s < p.splits && es != 0.0f) o = make_float4(o.x + es * x[s].x, o.y + es * x[s].y, o.z + es * x[s].z, o.w + es * x[s].w);
         }
         const int node = (row0 + row) / p.rep, head = h * p.rep + (row0 + row) % p.rep;
         store_row(p, ((size_t)b * p.N + node) * p.Hq + head, lane, M, l, o);
@@ -511,12 +512,12 @@ E3_DEV float4 weighted_sum(const CacheAttn &p, long long rows, long long row, in
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             e[k] = factor(min(s + k, s1 - 1));   // (a split with nothing to see has left nothing there)
-            if (s + k >= s1) e[k] = NOTHING;
-            if (counts(e[k])) x[k] = *reinterpret_cast<const float4 *>(p.part_o + ((s + k) * rows + row) * D + 4 * lane);
+            if (s + k >= s1) e[k] = 0.0f;
+            if (e[k] != 0.0f) x[k] = *reinterpret_cast<const float4 *>(p.part_o + ((s + k) * rows + row) * D + 4 * lane);
         }
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            if (counts(e[k])) add_part(o, e[k], x[k]);
+            if (e[k] != 0.0f) o = make_float4(o.x + e[k] * x[k].x, o.y + e[k] * x[k].y, o.z + e[k] * x[k].z, o.w + e[k] * x[k].w);
     }
     return o;
 }

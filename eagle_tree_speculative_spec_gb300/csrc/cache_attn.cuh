@@ -102,15 +102,12 @@ E3_DEV uint64_t path_bits(const int32_t *par, int i, bool &bad) {
     }
 }
 
-// Joins.  A part of a prefix counts by 2^(m - M) of its row's maximum, NOTHING where it has summed up nothing and may have left
-// nothing.  That factor may well come to 0 of a part that has: what is not finite there (NaN codes and scales of V, a tree's
-// values) still reaches the row, as it does inside a part.
-constexpr float NOTHING = -1.0f;
-E3_DEV float part_factor(float m, float l, float M) { return l == 0.0f ? NOTHING : m == -INFINITY ? 1.0f : fast_exp2(m - M); }
-E3_DEV bool counts(float factor) { return !(factor < 0.0f); }   // (NaN does)
-E3_DEV float weighted(float factor, float x) { return fabsf(x) <= FLT_MAX ? factor * x : x; }
-E3_DEV void add_part(float4 &o, float factor, float4 x) {
-    o = make_float4(o.x + weighted(factor, x.x), o.y + weighted(factor, x.y), o.z + weighted(factor, x.z), o.w + weighted(factor, x.w));
+// What a part of a prefix counts by when parts are joined: 2^(m - M) of its row's maximum, 0 where it has summed up nothing (and
+// may have left nothing).  No less than 2^-126 otherwise, so that what is not finite there (NaN codes and scales of V, a
+// tree's values) reaches the row as it does inside a part; of finite values that is n 2^-118 of the largest at most, where
+// the weights' floor inside a part is 2^-31 of it.
+E3_DEV float part_factor(float m, float l, float M) {
+    return m == -INFINITY ? (l == 0.0f ? 0.0f : 1.0f) : fmaxf(fast_exp2(m - M), FLT_MIN);   // (all scores NaN: a sum, no maximum)
 }
 
 E3_DEV float lse_of(float m, float l) {   // (the weights are 2^WEIGHT_LOG2 up)

@@ -972,10 +972,8 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) cache_attn_join_kernel(const 
 #pragma unroll
             for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
             const float Mn = fmaxf(M, top), down = part_factor(M, l, Mn);
-            l *= down;   // (0 where that is NOTHING)
-            const float4 before = o;
-            o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (counts(down)) add_part(o, down, before);
+            l *= down;
+            o = make_float4(o.x * down, o.y * down, o.z * down, o.w * down);
             M = Mn;
             const float e = part_factor(ml.x, ml.y, M);
             float sum = e * ml.y;
@@ -986,7 +984,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) cache_attn_join_kernel(const 
             for (int q = 0; q < n; ++q) {
                 const float eq = __shfl_sync(0xffffffffu, e, q);
                 const float4 x = *reinterpret_cast<const float4 *>(p.part_o + slot(q0 + q) * D + 4 * lane);
-                if (counts(eq)) add_part(o, eq, x);
+                if (eq != 0.0f) o = make_float4(o.x + eq * x.x, o.y + eq * x.y, o.z + eq * x.z, o.w + eq * x.w);
             }
         }
         const int node = (row0 + row) / a.rep, head = g * a.rep + (row0 + row) % a.rep;
