@@ -10,9 +10,10 @@
 // once.  A thread's unit is 16 dims of a row, both ends of their pairs among them.  Prompts: a CTA of 256 threads takes a run
 // of jobs, one after the other, with their group's cosines and sines in shared memory, which the keys of all heads share.
 // Few tokens a sequence (at most 8): a warp takes a job.
-// Bound by issue slots and the meeting of a CTA's warps: 16384 tokens of 8 heads of 128 (e4m3, 100.7 MB) take 25.7 us,
-// 3.9 TB/s (14.9 us at the copy's rate); 17.7 million warp instructions are 14 us of every scheduler, and the warps wait for
-// the maximum that they share and for their own chains.  Four CTAs an SM of 64 registers a thread and no load ahead took
+// Bound by latency: 16384 tokens of 8 heads of 128 (e4m3, 100.7 MB) take 25.7 us, 3.9 TB/s (14.8 us at the copy's rate).  17.7
+// million warp instructions are 14 us of every scheduler; the rest is a job's chain from its loads over the maximum that a
+// CTA's warps share to its codes, with three CTAs an SM to hide it (of 8 cycles an issue 1.5 wait for memory, 1.5 for
+// another warp's turn, 0.7 at the barrier, 0.7 for a pipe).  Four CTAs an SM of 64 registers a thread and no load ahead took
 // 29.3 us; addresses kept in registers, which spill, 27.0 us.
 #include "e4m3.cuh"
 #include "rope.cuh"

@@ -19,9 +19,11 @@
 // A warp's next K is loaded once the products with this one have been issued, its next V after the weights' products,
 // and the pages two steps ahead: each load has about half a step to arrive, in no registers of its own.
 // Rows beyond 16 are groups of CTAs of their own, which read the keys again.
-// Bound by memory: 64 single tokens of 32 heads over up to 8192 positions (669 MB) take 116 us, 5.8 TB/s, one over 250000 (512 MB)
-// 84 us, 6.1 TB/s; the copy's rate is 6.8.  With Q's rows as the tile's 16 (64 MMAs a step where 8 rows need 48, 64 more
-// registers, loads only between steps) they took 174 and 216 us.  One token over 4096 positions: 8.2 us, latency.
+// Bound by memory at the largest calls: 64 single tokens of 32 heads over up to 8192 positions (669 MB) take 115 us,
+// 5.8 TB/s, one over 250000 (512 MB) 84 us, 6.1 TB/s; the copy's rate is 6.8.  With Q's rows as the tile's 16 (64 MMAs a
+// step where 8 rows need 48, 64 more registers, loads only between steps) they took 174 and 216 us.  By waves and latency
+// below that: 8 sequences of 4096 positions 17.5 us, 3.8 TB/s, 32 of them 54 to 56 us, 4.9 TB/s; 64 of 5 queries each, two
+// groups of rows that each read the keys, 150 us, 3.6 TB/s.  One token over 4096 positions: 8.1 to 9.0 us, latency.
 // Q is scaled by a power of two for each row so that fp16 holds it (bf16's 8 bits fit, elements 2^-36 below the row's
 // largest vanish); the factor comes back with the scale of K's group in fp32.  Weights are held 2^7 up, so that fp16's
 // 11 bits reach down to 2^-21 of the largest, and V's group scale is put on them relative to the largest so far.
@@ -581,7 +583,9 @@ __global__ void __launch_bounds__(NT) cache_attn_merge_kernel(const CacheAttn p)
 
 // Parts of the prefix, of as many steps for a short sequence as for a long one, so that all CTAs take about the same
 // time: the number that gives the least waves * (steps of a warp + what a CTA costs besides, in steps), about in us.
-// Lengths are unknown here, so half a wave more stands for the uneven end of all but a single wave.
+// Lengths are on the device, so half a wave more stands for the uneven end of all but a single wave, and the bound for the
+// lengths: one far above them costs parts without keys (one sequence of 4096 positions by a bound of 4096, 16384 and
+// 131072: 8.5, 12 and 26 us; 8: 18, 36 and 53; 32: 56, 66 and 82).
 float plan_splits(CacheAttn &p) {
     const int chunks = (p.max_prefix + CHUNK - 1) / CHUNK;
     const bool one = p.N * p.rep <= 8;
@@ -589,7 +593,11 @@ float plan_splits(CacheAttn &p) {
     const float besides = one ? 3.0f : 8.0f;
     // One launch, joined within a cluster, where all clusters fit at once: a CTA then keeps its SM until the slowest of its
     // cluster is done, and clusters of many CTAs leave SMs out (64 sequences of up to 8192 positions, 4 parts: 154 us
-    // as clusters, 116 us with a second kernel; 8 sequences of 4096, 7 parts: 25 and 17 us; one of 4096: 11 and 15 us a call)
+    // as clusters, 116 us with a second kernel; 8 sequences of 4096, 7 parts: 25 and 17 us; one of 4096: 11 and 15 us a call).
+    // More than 8 rows, up to 4 parts: also where an SM gets two CTAs, which such small clusters leave fewer SMs out for (7 x
+    // 17 nodes of 12 heads over 3001 positions, 3 parts: 24.4 us as clusters, 25.1 with a second kernel; 4 nodes of 9
+    // sequences over 4096, 4 parts: 26.5 and 27.9; 60 nodes of 2 sequences over 2048, 2 heads a KV head, 4 parts: 19.0 and
+    // 20.5; with 2 parts 29.2 and 28.1, 22.5 and 22.6, but 3 or 4 are then the choice)
     auto as_cluster = [&](int s) {
         return s > 1 && s <= MAX_CLUSTER && units * s <= (s <= 4 && !one ? resident : (float)device_sm_count());
     };

@@ -22,12 +22,12 @@
 //                 of 64 keys (so one scale), and they exchange the maxima; at the end of a unit its results
 // Tensor memory: O 128 columns, two tiles of S, one of P (fp16 pairs), Q's parts.  S is free for the tile after next once the
 // softmax has loaded it, so that QK runs two tiles ahead.
-// Limited by instruction fetch: the roles' loops together are more than the SM's instruction cache holds at once (no warp had
-// an instruction ready for more than a cycle of each issue), so every loop is kept short: what is rare is out of line, waits
-// share one function, a unit's work runs in loops, not unrolled.  That took 64 trees of 60 nodes of 4 heads over 2048
-// positions (67 us by tensor operations) from 307 to 225 us.  A tile takes some 2060 cycles (its two groups of MMAs 1024
-// each), a unit 11000 more: Q's parts, the tree and the results, in part beside the units before and after.  210 us now,
-// 0.62 PFLOP/s; over 16384 positions 1047 us, 0.99 PFLOP/s.
+// Bound by its roles' own work: 64 trees of 60 nodes of 4 heads over 2048 positions take 207 us, 0.63 PFLOP/s, where tensor
+// operations are 69; over 16384 positions 1049 us, 0.99 PFLOP/s.  A tile takes some 2060 cycles (its two groups of MMAs 1024
+// each), a unit 11000 more: Q's parts, the tree and the results, in part beside the units before and after.  The kernel of the
+// bf16 cache (verify_attn.cu), as many MMAs a tile, needs no conversions: 1800 cycles a tile, 134 and 882 us for the same
+// two.  The loops are short because the roles' code together is more than the SM's instruction cache holds: what is rare is
+// out of line, waits share one function, a unit's work runs in loops, not unrolled (307 to 225 us for the first).
 // All waits are bounded; one that runs out sets EAGLE3_DEV_TIMEOUT and the CTA drains and exits.
 #include "cache_attn.cuh"
 #include "tc.cuh"

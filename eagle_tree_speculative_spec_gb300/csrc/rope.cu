@@ -6,11 +6,13 @@
 // Llama 3.1 model card's configuration and of "YaRN: Efficient Context Window Extension" (Peng et al., 2023).
 //
 // A row's angles are shared by its heads: a CTA takes a few rows and first fills their cosines and sines into shared
-// memory, one sincospif a thread, then walks the heads.  A thread's unit is the two runs of V elements that hold V
-// pairs, so that it reads and writes both ends of each pair itself and the call can run in place; it stays with one row,
-// whose cosines it holds in registers, and has four heads' loads in flight, the first four while the angles are made.
-// Bound by memory: 3840 rows of 40 bf16 heads of 128 (78.6 MB) take 15.9 us, 5.0 TB/s (11.6 us at the copy's rate); with the
-// cosines read from shared memory for every head (lanes 64 bytes apart: four-way conflicts) and one head at a time, 26.9 us.
+// memory (series about the nearest quarter turn, turned() in rope.cuh; at most one angle a thread), then walks the heads.
+// A thread's unit is the two runs of V elements that hold V pairs, so that it reads and writes both ends of each pair
+// itself and the call can run in place; it stays with one row, whose cosines it holds in registers, and has four heads'
+// loads in flight, the first four while the angles are made.
+// Bound by memory and the latency of its waves: 3840 rows of 40 bf16 heads of 128 (78.6 MB) take 15.9 us, 5.0 TB/s (11.6 us
+// at the copy's rate), in three waves of CTAs, each with its first loads and angles; with the cosines read from shared
+// memory for every head (lanes 64 bytes apart: four-way conflicts) and one head at a time, 26.9 us.
 #include "rope.cuh"
 
 #include <algorithm>

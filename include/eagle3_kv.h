@@ -188,7 +188,8 @@ eagle3_status_t eagle3_append_kv(const eagle3_append_kv_args_t *args, eagle3_str
  * max_prefix_len decide too), as two e4m3 parts: 8 bits, but no finer than 2^-17 of the row's (of the tree's)
  * largest element, and infinities as NaN.  Weights are rounded to fp16 (11 bits); V's codes are exact where their scale is above
  * 2^-21 of the sequence's largest, and at any scale no finer than 2^-31 of that.  Where work is cut depends
- * on the lengths, the shape and the number of SMs: results are reproducible for the same call on a given GPU model.
+ * on the lengths, max_prefix_len, the shape and the number of SMs: results are reproducible for the same call on a given
+ * GPU model.  Where few query rows are read at a time, a max_prefix_len far above the lengths costs time.
  * ---------------------------------------------------------------------------------------------- */
 typedef struct {
     int32_t batch;               /* B >= 0                                                            */
