@@ -996,6 +996,8 @@ def append_kv_args(k_new, v_new, cache_len, n_new, block_table, k_cache, v_cache
     vp, vrs = _heads_arg(v_new, bf, (n_rows, Hkv, D), dev, "v_new")
     if rs != vrs:
         raise ValueError("k_new and v_new must share a row pitch")
+    if rope_table is not None and rope_table.dim() != 1:
+        raise ValueError("rope_table must be [rotary_dim / 2]")
     if e4m3:
         pages = k_cache.shape[0]
         shape, dt = (pages, Hkv, bs, D), torch.float8_e4m3fn
